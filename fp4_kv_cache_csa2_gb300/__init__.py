@@ -49,6 +49,30 @@ class DecodeArgs(ctypes.Structure):
                 ("swa_fp8", ctypes.c_int32), ("attn_split", ctypes.c_int32)]
 
 
+class QkArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("pos", ctypes.c_void_p), ("rope_cs", ctypes.c_void_p),
+                ("rope_P", ctypes.c_int64), ("eps", ctypes.c_float), ("rows_fp8", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("q_weight", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("k", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+                ("k_weight", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("n_rows", ctypes.c_int64),
+                ("k_slot", ctypes.c_void_p)]
+
+
+class WindowArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Q", ctypes.c_int), ("S", ctypes.c_int), ("W", ctypes.c_int),
+                ("n_sink", ctypes.c_int), ("scale", ctypes.c_float), ("q_pos", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("swa_base_pos", ctypes.c_void_p),
+                ("sinks", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("rows_fp8", ctypes.c_int32)]
+
+
+class DenseArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Q", ctypes.c_int), ("S", ctypes.c_int), ("scale", ctypes.c_float),
+                ("max_n", ctypes.c_int64), ("q_pos", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("swa", ctypes.c_void_p), ("swa_base_pos", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("swa_fp8", ctypes.c_int32)]
+
+
 _P, _I, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _SIGNATURES = {
     "csa2_layout_version": (ctypes.c_int, []),
@@ -76,6 +100,11 @@ _SIGNATURES = {
                               _P, _SZ, _P]),
     "csa2_decode_workspace_size": (_SZ, [_I, _I, _I, _I64, _I, _I]),
     "csa2_decode": (_I, [ctypes.POINTER(CacheStruct), ctypes.POINTER(DecodeArgs), _P, _SZ, _P]),
+    "csa2_qk_norm_rope": (_I, [ctypes.POINTER(QkArgs), _P, _SZ, _P]),
+    "csa2_window_attn_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "csa2_window_attn": (_I, [ctypes.POINTER(WindowArgs), _P, _SZ, _P]),
+    "csa2_dense_attn_workspace_size": (_SZ, [_I, _I, _I64]),
+    "csa2_dense_attn": (_I, [ctypes.POINTER(CacheStruct), ctypes.POINTER(DenseArgs), _P, _SZ, _P]),
     "csa2_test_withhold_arrival": (_I, [_I]),
 }
 
@@ -302,3 +331,104 @@ def decode(mode: int, cache: Cache, *, q_pos, q, swa, swa_base_pos, scale: float
     c = cache.struct()
     _check("csa2_decode", load().csa2_decode(ctypes.byref(c), ctypes.byref(a), ws.ptr, ws.nbytes,
                                              _stream(stream)))
+
+
+# The calls below also check what the C boundary cannot see: shapes, element
+# sizes, and that every tensor lies contiguous on the device of the workspace.
+def _tensor(name: str, t, shape, itemsizes, device, token_stride: bool = False):
+    """Address of `t`, which has `shape` (None: any size), elements of one of
+    `itemsizes` bytes, lies on `device` and is contiguous (with token_stride:
+    but for the stride of its first dimension)."""
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.element_size() not in itemsizes:
+        raise ValueError(f"{name}: {t.dtype}, expected elements of {itemsizes} bytes")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the workspace on {device}")
+    if not t.is_contiguous() and not (token_stride and t[0].is_contiguous()):
+        raise ValueError(f"{name}: strides {t.stride()} of shape {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _call(name: str, fn, device, stream, *args):
+    """fn(*args, stream) with `device` current; its error, if any, raised."""
+    import torch
+    with torch.cuda.device(device):
+        _check(name, fn(*args, _stream(stream)))
+
+
+def qk_norm_rope(pos, rope_cs, ws: Workspace, *, q=None, q_weight=None, q_out=None, k=None, k_weight=None, rows=None,
+                 k_slot=None, eps: float = 1e-6, stream=None):
+    """RMSNorm per head and rotation of the last 64 channels: queries q [T][64][512]
+    -> q_out, window keys k [T][512] -> row k_slot[t] (None: t) of rows [..][512]
+    (bf16, or uint8: E4M3).  Tokens with pos -1 write nothing.  q and k may be
+    views with a larger token stride; q_out may be q itself."""
+    dev, T = ws.buf.device, pos.numel()
+    a = QkArgs(T=T, pos=_tensor("pos", pos, (T,), (8,), dev),
+               rope_cs=_tensor("rope_cs", rope_cs, (None, D_ROPE // 2, 2), (4,), dev), rope_P=rope_cs.shape[0],
+               eps=float(eps))
+    if q is not None:
+        a.q = _tensor("q", q, (T, N_HEADS, D_LATENT), (2,), dev, True)
+        a.q_stride = q.stride(0) if T > 1 else N_HEADS * D_LATENT
+        a.q_out = _tensor("q_out", q_out, (T, N_HEADS, D_LATENT), (2,), dev)
+        if q_weight is not None:
+            a.q_weight = _tensor("q_weight", q_weight, (D_LATENT,), (4,), dev)
+    if k is not None:
+        a.k = _tensor("k", k, (T, D_LATENT), (2,), dev, True)
+        a.k_stride = k.stride(0) if T > 1 else D_LATENT
+        a.rows = _tensor("rows", rows, (*[None] * (rows.dim() - 1), D_LATENT), (1, 2), dev)
+        a.n_rows, a.rows_fp8 = rows.numel() // D_LATENT, int(rows.element_size() == 1)
+        if k_weight is not None:
+            a.k_weight = _tensor("k_weight", k_weight, (D_LATENT,), (4,), dev)
+        if k_slot is not None:
+            a.k_slot = _tensor("k_slot", k_slot, (T,), (8,), dev)
+    _call("csa2_qk_norm_rope", load().csa2_qk_norm_rope, dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
+
+
+def window_attn_workspace_size(B: int, Q: int, W: int, n_sink: int) -> int:
+    return load().csa2_window_attn_workspace_size(B, Q, W, n_sink)
+
+
+def window_attn(q, rows, swa_base_pos, q_pos, scale: float, out, ws: Workspace, *, W: int, sinks=None, lse=None,
+                stream=None):
+    """Queries [B][Q][64][512] over the window rows [B][S][512] of positions
+    t-W+1 .. t and the sinks [B][n][512] before them (both bf16, or both uint8:
+    E4M3).  lse: float32 [B][Q][64] or None."""
+    dev, (B, Q), S, n = ws.buf.device, q_pos.shape, rows.shape[1], 0 if sinks is None else sinks.shape[1]
+    size = rows.element_size()
+    a = WindowArgs(B=B, Q=Q, S=S, W=W, n_sink=n, scale=float(scale), rows_fp8=int(size == 1),
+                   q_pos=_tensor("q_pos", q_pos, (B, Q), (8,), dev),
+                   q=_tensor("q", q, (B, Q, N_HEADS, D_LATENT), (2,), dev),
+                   rows=_tensor("rows", rows, (B, S, D_LATENT), (1, 2), dev),
+                   swa_base_pos=_tensor("swa_base_pos", swa_base_pos, (B,), (8,), dev),
+                   out=_tensor("out", out, (B, Q, N_HEADS, D_LATENT), (2,), dev))
+    if sinks is not None:
+        a.sinks = _tensor("sinks", sinks, (B, n, D_LATENT), (size,), dev)
+    if lse is not None:
+        a.lse = _tensor("lse", lse, (B, Q, N_HEADS), (4,), dev)
+    _call("csa2_window_attn", load().csa2_window_attn, dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
+
+
+def dense_attn_workspace_size(B: int, Q: int, max_n: int) -> int:
+    return load().csa2_dense_attn_workspace_size(B, Q, max_n)
+
+
+def dense_attn(cache: Cache, q, swa, swa_base_pos, q_pos, scale: float, out, ws: Workspace, *, max_n: int, lse=None,
+               stream=None):
+    """Queries [B][Q][64][512] over every visible cache entry and the 128-token
+    window, rows swa [B][S][512] (bf16, or uint8: E4M3).  max_n: the most entries
+    a query sees (it sizes the work split, nothing else).  lse: float32
+    [B][Q][64] or None."""
+    dev, (B, Q), S = ws.buf.device, q_pos.shape, swa.shape[1]
+    if B != cache.B:
+        raise ValueError(f"q_pos: {B} sequences, the cache has {cache.B}")
+    a = DenseArgs(B=B, Q=Q, S=S, scale=float(scale), max_n=max_n, swa_fp8=int(swa.element_size() == 1),
+                  q_pos=_tensor("q_pos", q_pos, (B, Q), (8,), dev),
+                  q=_tensor("q", q, (B, Q, N_HEADS, D_LATENT), (2,), dev),
+                  swa=_tensor("swa", swa, (B, S, D_LATENT), (1, 2), dev),
+                  swa_base_pos=_tensor("swa_base_pos", swa_base_pos, (B,), (8,), dev),
+                  out=_tensor("out", out, (B, Q, N_HEADS, D_LATENT), (2,), dev))
+    if lse is not None:
+        a.lse = _tensor("lse", lse, (B, Q, N_HEADS), (4,), dev)
+    c = cache.struct()
+    _call("csa2_dense_attn", load().csa2_dense_attn, dev, stream, ctypes.byref(c), ctypes.byref(a), ws.ptr, ws.nbytes)

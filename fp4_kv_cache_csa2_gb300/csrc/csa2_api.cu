@@ -18,7 +18,13 @@ constexpr size_t HDR = CSA2_WS_HEADER_BYTES;
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned8(const void* p) { return ((uintptr_t)p & 7u) == 0; }
 
+// [a, a + an) and [b, b + bn) share a byte
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
 
 csa2_status check_cache(const csa2_cache* c) {
   if (!c || !c->main_kv || !c->idx_codes || !c->idx_scales || !c->n_entries) return CSA2_ERR_INVALID_ARG;
@@ -327,6 +333,147 @@ csa2_status csa2_block_summary(const csa2_cache* cache, const int64_t* first_blo
   p.sum_cap = sum_cap;
   p.hdr = header(ws);
   return from_cuda(launch_block_summary(p, (cudaStream_t)stream));
+}
+
+csa2_status csa2_qk_norm_rope(const csa2_qk_args* a, void* ws, size_t ws_bytes, void* stream) {
+  if (!a) return CSA2_ERR_INVALID_ARG;
+  if (a->T < 0 || a->rope_P < 0 || a->n_rows < 0) return CSA2_ERR_INVALID_ARG;
+  if (a->T > MAX_QUERIES || a->n_rows > ((int64_t)1 << 40)) return CSA2_ERR_UNSUPPORTED;
+  if (!std::isfinite(a->eps) || a->eps < 0.f) return CSA2_ERR_INVALID_ARG;
+  if (a->rows_fp8 != 0 && a->rows_fp8 != 1) return CSA2_ERR_INVALID_ARG;
+  csa2_status st = check_ws(ws, ws_bytes, HDR);
+  if (st != CSA2_OK) return st;
+  if (a->T == 0 || (!a->q && !a->k)) return CSA2_OK;
+  if (!a->pos || !aligned8(a->pos) || !a->rope_cs || !aligned16(a->rope_cs)) return CSA2_ERR_INVALID_ARG;
+  const int64_t max_stride = (int64_t)1 << 32;
+  int64_t q_bytes = 0, k_bytes = 0, out_bytes = 0, row_bytes = 0;
+  if (a->q) {
+    if (!a->q_out || !aligned16(a->q) || !aligned16(a->q_out)) return CSA2_ERR_INVALID_ARG;
+    if (a->q_weight && !aligned16(a->q_weight)) return CSA2_ERR_INVALID_ARG;
+    if (a->q_stride < H * D || a->q_stride > max_stride || a->q_stride % 8 != 0) return CSA2_ERR_INVALID_ARG;
+    q_bytes = ((a->T - 1) * a->q_stride + H * D) * 2;
+    out_bytes = a->T * H * D * 2;
+  }
+  if (a->k) {
+    if (!a->rows || !aligned16(a->k) || !aligned16(a->rows)) return CSA2_ERR_INVALID_ARG;
+    if (a->k_weight && !aligned16(a->k_weight)) return CSA2_ERR_INVALID_ARG;
+    if (a->k_slot && !aligned8(a->k_slot)) return CSA2_ERR_INVALID_ARG;
+    if (a->k_stride < D || a->k_stride > max_stride || a->k_stride % 8 != 0) return CSA2_ERR_INVALID_ARG;
+    k_bytes = ((a->T - 1) * a->k_stride + D) * 2;
+    row_bytes = a->n_rows * D * (a->rows_fp8 ? 1 : 2);
+  }
+  const bool in_place = a->q && a->q_out == a->q && a->q_stride == H * D;
+  if (!in_place && overlap(a->q, q_bytes, a->q_out, out_bytes)) return CSA2_ERR_INVALID_ARG;
+  if (overlap(a->k, k_bytes, a->rows, row_bytes) || overlap(a->k, k_bytes, a->q_out, out_bytes) ||
+      overlap(a->q, q_bytes, a->rows, row_bytes) || overlap(a->q_out, out_bytes, a->rows, row_bytes))
+    return CSA2_ERR_INVALID_ARG;
+  QkParams p{};
+  p.T = a->T;
+  p.pos = a->pos;
+  p.rope_cs = a->rope_cs;
+  p.rope_P = a->rope_P;
+  p.eps = a->eps;
+  p.q = a->q;
+  p.q_stride = a->q_stride;
+  p.q_weight = a->q_weight;
+  p.q_out = a->q_out;
+  p.k = a->k;
+  p.k_stride = a->k_stride;
+  p.k_weight = a->k_weight;
+  p.rows = static_cast<uint8_t*>(a->rows);
+  p.n_rows = a->n_rows;
+  p.k_slot = a->k_slot;
+  p.rows_fp8 = a->rows_fp8;
+  p.hdr = header(ws);
+  return from_cuda(launch_qk_norm_rope(p, (cudaStream_t)stream));
+}
+
+// The attentions over every visible key: their queries, rows and outputs.
+constexpr int64_t MAX_KEY_QUERIES = (int64_t)1 << 24;   // 64 rows each below 2^31 (tensor-map coordinates)
+
+static csa2_status check_keys_call(const KeysParams& p, int B, int Q, size_t need, void* ws, size_t ws_bytes) {
+  if (B < 0 || Q < 0 || p.S < 0 || p.n_sink < 0 || p.W < 1 || !std::isfinite(p.scale)) return CSA2_ERR_INVALID_ARG;
+  if (p.rows_fp8 != 0 && p.rows_fp8 != 1) return CSA2_ERR_INVALID_ARG;
+  const int64_t BQ = (int64_t)B * Q, nr = B * p.S, nk = (int64_t)B * p.n_sink, lim = (int64_t)1 << 31;
+  if (BQ > MAX_KEY_QUERIES || nr >= lim || nk >= lim) return CSA2_ERR_UNSUPPORTED;
+  csa2_status st = check_ws(ws, ws_bytes, need);
+  if (st != CSA2_OK || BQ == 0) return st;
+  if (!p.q || !p.q_pos || !p.base_pos || !p.out || (nr > 0 && !p.rows) || (nk > 0 && !p.sinks))
+    return CSA2_ERR_INVALID_ARG;
+  if (!aligned16(p.q) || !aligned16(p.rows) || !aligned16(p.sinks) || !aligned16(p.out) || !aligned8(p.q_pos) ||
+      !aligned8(p.base_pos) || ((uintptr_t)p.lse & 3u) != 0)
+    return CSA2_ERR_INVALID_ARG;
+  const int64_t row = D * (p.rows_fp8 ? 1 : 2), out_n = BQ * H * D * 2, lse_n = p.lse ? BQ * H * 4 : 0;
+  const struct { const void* a; int64_t n; } in[] = {{p.q, out_n}, {p.q_pos, BQ * 8}, {p.base_pos, (int64_t)B * 8},
+      {p.rows, nr * row}, {p.sinks, nk * row}, {ws, (int64_t)need},
+      {p.main_kv, p.main_kv ? B * p.cap * MAIN_BYTES : 0}, {p.n_entries, p.n_entries ? (int64_t)B * 4 : 0}};
+  for (const auto& x : in)
+    if (overlap(x.a, x.n, p.out, out_n) || overlap(x.a, x.n, p.lse, lse_n)) return CSA2_ERR_INVALID_ARG;
+  return overlap(p.out, out_n, p.lse, lse_n) ? CSA2_ERR_INVALID_ARG : CSA2_OK;
+}
+
+// runs of 128 keys that a query of a window call / a dense call sees at most
+static int64_t window_chunks(int64_t W, int64_t n_sink) { return ceil_div(W, 128) + ceil_div(n_sink, 128); }
+static int64_t dense_chunks(int64_t max_n) { return 1 + ceil_div(max_n, 128); }
+
+size_t csa2_window_attn_workspace_size(int B, int Q, int W, int n_sink) {
+  if (B < 0 || Q < 0 || W < 1 || n_sink < 0 || (int64_t)B * Q > MAX_KEY_QUERIES) return 0;
+  return HDR + align256(keys_part_bytes((int64_t)B * Q, window_chunks(W, n_sink)));
+}
+
+csa2_status csa2_window_attn(const csa2_window_args* a, void* ws, size_t ws_bytes, void* stream) {
+  if (!a) return CSA2_ERR_INVALID_ARG;
+  KeysParams p{};
+  p.q = a->q;
+  p.q_pos = a->q_pos;
+  p.Q = a->Q;
+  p.rows = static_cast<const uint8_t*>(a->rows);
+  p.base_pos = a->swa_base_pos;
+  p.S = a->S;
+  p.sinks = static_cast<const uint8_t*>(a->sinks);
+  p.n_sink = a->n_sink;
+  p.rows_fp8 = a->rows_fp8;
+  p.W = a->W;
+  p.scale = a->scale;
+  p.out = a->out;
+  p.lse = a->lse;
+  const csa2_status st = check_keys_call(p, a->B, a->Q, csa2_window_attn_workspace_size(a->B, a->Q, a->W, a->n_sink),
+                                         ws, ws_bytes);
+  if (st != CSA2_OK || a->B == 0 || a->Q == 0) return st;
+  p.hdr = header(ws);
+  return from_cuda(launch_keys_attention(p, a->B, window_chunks(a->W, a->n_sink), scratch(ws), (cudaStream_t)stream));
+}
+
+size_t csa2_dense_attn_workspace_size(int B, int Q, int64_t max_n) {
+  if (B < 0 || Q < 0 || max_n < 0 || (int64_t)B * Q > MAX_KEY_QUERIES) return 0;
+  return HDR + align256(keys_part_bytes((int64_t)B * Q, dense_chunks(max_n)));
+}
+
+csa2_status csa2_dense_attn(const csa2_cache* cache, const csa2_dense_args* a, void* ws, size_t ws_bytes,
+                            void* stream) {
+  csa2_status st = check_cache(cache);
+  if (st != CSA2_OK) return st;
+  if (!a || a->max_n < 0) return CSA2_ERR_INVALID_ARG;
+  KeysParams p{};
+  p.q = a->q;
+  p.q_pos = a->q_pos;
+  p.Q = a->Q;
+  p.rows = static_cast<const uint8_t*>(a->swa);
+  p.base_pos = a->swa_base_pos;
+  p.S = a->S;
+  p.rows_fp8 = a->swa_fp8;
+  p.W = WIN;
+  p.main_kv = cache->main_kv;
+  p.cap = cache->cap;
+  p.n_entries = cache->n_entries;
+  p.m = cache->m;
+  p.scale = a->scale;
+  p.out = a->out;
+  p.lse = a->lse;
+  st = check_keys_call(p, a->B, a->Q, csa2_dense_attn_workspace_size(a->B, a->Q, a->max_n), ws, ws_bytes);
+  if (st != CSA2_OK || a->B == 0 || a->Q == 0) return st;
+  p.hdr = header(ws);
+  return from_cuda(launch_keys_attention(p, a->B, dense_chunks(a->max_n), scratch(ws), (cudaStream_t)stream));
 }
 
 // HISA keeps up to 2048 of its summary rows: past 4096 blocks a row goes to

@@ -1,0 +1,184 @@
+// Queries and window keys: RMSNorm per head and the rotation of the last 64
+// channels in one pass.
+//
+//   y = x / sqrt(mean(x^2) + eps) * w        over the 512 channels of a head
+//   (y_a, y_b) -> (y_a cos - y_b sin, y_a sin + y_b cos)
+//                                            pairs a = 448 + 2i, b = a + 1,
+//                                            cos/sin from row pos of the table
+//
+// Everything between the bf16 load and the final rounding (bf16, or E4M3 for a
+// window stored in 8 bits) is binary32: the squares, their sum and the
+// reciprocal root lose nothing that the 8 significant bits of the result hold.
+//
+// Bound by HBM: a token reads and writes 64 KB of queries and 1 + 1 KB (or
+// 512 B) of window row against 0.2 Mflop.  One warp takes four rows at a time
+// (four heads of a token, or four tokens' key rows); lane l owns channels
+// 8l .. 8l + 7 and 256 + 8l .. 256 + 8l + 7, so every load and store of a warp
+// is 512 contiguous bytes and the eight 16-byte loads of a lane are in flight
+// together before the first is used.  The rotated tail lies in the second half
+// of lanes 24..31 (four pairs a lane).
+#include "host_once.cuh"
+#include "params.cuh"
+
+namespace csa2 {
+
+constexpr int QK_THREADS = 256;
+constexpr int QK_ROWS = 4;                          // rows per warp
+constexpr int QK_TASKS = H / QK_ROWS;               // warps per token's queries
+
+__device__ __forceinline__ uint32_t qk_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+// a in the low byte
+__device__ __forceinline__ uint32_t qk_e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ void qk_unpack(const uint4& v, float* f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// 1 / sqrt(mean square + eps) of a row, from this lane's 16 channels of it
+__device__ __forceinline__ float qk_inv_rms(const uint4& a, const uint4& b, float eps) {
+  float f[16];
+  qk_unpack(a, f);
+  qk_unpack(b, f + 8);
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; i++) s = fmaf(f[i], f[i], s);
+#pragma unroll
+  for (int k = 16; k >= 1; k >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, k);
+  return 1.0f / sqrtf(s * (1.0f / D) + eps);
+}
+
+// eight channels of the half `half` (0: 8l.., 1: 256 + 8l..) scaled, weighted and rotated
+__device__ __forceinline__ void qk_finish(const uint4& v, float r, const float4* w, int half, int lane,
+                                          const float4* cs, float* f) {
+  qk_unpack(v, f);
+#pragma unroll
+  for (int i = 0; i < 8; i++) f[i] *= r;
+  if (w) {
+    const float4 w0 = __ldg(w + 64 * half + 2 * lane), w1 = __ldg(w + 64 * half + 2 * lane + 1);
+    const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+    for (int i = 0; i < 8; i++) f[i] *= wv[i];
+  }
+  if (half == 1 && lane >= 24) {
+    const float4 c0 = __ldg(cs + 2 * (lane - 24)), c1 = __ldg(cs + 2 * (lane - 24) + 1);   // cos, sin, cos, sin
+    const float c[4] = {c0.x, c0.z, c1.x, c1.z}, s[4] = {c0.y, c0.w, c1.y, c1.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const float y0 = f[2 * i], y1 = f[2 * i + 1];
+      f[2 * i] = y0 * c[i] - y1 * s[i];
+      f[2 * i + 1] = y0 * s[i] + y1 * c[i];
+    }
+  }
+}
+
+__device__ __forceinline__ uint4 qk_pack_bf16(const float* f) {
+  return make_uint4(qk_bf16x2(f[0], f[1]), qk_bf16x2(f[2], f[3]), qk_bf16x2(f[4], f[5]), qk_bf16x2(f[6], f[7]));
+}
+
+// A token's row of the rotation table, or null when the token is padding (-1)
+// or its position lies outside the table (reported).
+__device__ __forceinline__ const float4* qk_table_row(const QkParams& p, int64_t pos, bool reports) {
+  if (pos >= 0 && pos < p.rope_P) return reinterpret_cast<const float4*>(p.rope_cs + pos * D_ROPE);
+  if (pos != -1 && reports) report(p.hdr, CSA2_ERR_BOUNDS, pos);
+  return nullptr;
+}
+
+__global__ void __launch_bounds__(QK_THREADS) qk_norm_rope_kernel(QkParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t g = (int64_t)blockIdx.x * (QK_THREADS / 32) + (threadIdx.x >> 5);
+  const int64_t nq = p.q ? p.T * QK_TASKS : 0;
+  uint4 x[QK_ROWS][2];
+  if (g < nq) {                                     // four heads of one token
+    const int64_t token = g / QK_TASKS;
+    const int head = (int)(g % QK_TASKS) * QK_ROWS;
+    const uint4* in = reinterpret_cast<const uint4*>(p.q + token * p.q_stride + head * D);
+#pragma unroll
+    for (int i = 0; i < QK_ROWS; i++) {
+      x[i][0] = __ldcs(in + 64 * i + lane);
+      x[i][1] = __ldcs(in + 64 * i + 32 + lane);
+    }
+    const float4* cs = qk_table_row(p, p.pos[token], head == 0 && lane == 0);
+    if (!cs) return;
+    uint4* out = reinterpret_cast<uint4*>(p.q_out + (token * H + head) * D);
+    const float4* w = reinterpret_cast<const float4*>(p.q_weight);
+    float r[QK_ROWS];
+#pragma unroll
+    for (int i = 0; i < QK_ROWS; i++) r[i] = qk_inv_rms(x[i][0], x[i][1], p.eps);
+#pragma unroll
+    for (int i = 0; i < QK_ROWS; i++)
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+        float f[8];
+        qk_finish(x[i][half], r[i], w, half, lane, cs, f);
+        __stcs(out + 64 * i + 32 * half + lane, qk_pack_bf16(f));
+      }
+    return;
+  }
+  const int64_t t0 = (g - nq) * QK_ROWS;            // four tokens' key rows
+  if (!p.k || t0 >= p.T) return;
+  const int n = (int)(p.T - t0 < QK_ROWS ? p.T - t0 : QK_ROWS);
+#pragma unroll
+  for (int i = 0; i < QK_ROWS; i++) {
+    const uint4* in = reinterpret_cast<const uint4*>(p.k + (t0 + (i < n ? i : 0)) * p.k_stride);
+    x[i][0] = __ldcs(in + lane);
+    x[i][1] = __ldcs(in + 32 + lane);
+  }
+  const float4* w = reinterpret_cast<const float4*>(p.k_weight);
+#pragma unroll
+  for (int i = 0; i < QK_ROWS; i++) {
+    if (i >= n) break;
+    // the queries' warps report a bad position when there are queries
+    const float4* cs = qk_table_row(p, p.pos[t0 + i], !p.q && lane == 0);
+    const int64_t slot = p.k_slot ? p.k_slot[t0 + i] : t0 + i;
+    if (!cs || slot == -1) continue;
+    if (slot < 0 || slot >= p.n_rows) {
+      if (lane == 0) report(p.hdr, CSA2_ERR_BOUNDS, slot);
+      continue;
+    }
+    const float r = qk_inv_rms(x[i][0], x[i][1], p.eps);
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+      float f[8];
+      qk_finish(x[i][half], r, w, half, lane, cs, f);
+      if (p.rows_fp8) {
+        uint2* out = reinterpret_cast<uint2*>(p.rows + slot * D) + 32 * half + lane;
+        *out = make_uint2(qk_e4m3x2(f[0], f[1]) | qk_e4m3x2(f[2], f[3]) << 16,
+                          qk_e4m3x2(f[4], f[5]) | qk_e4m3x2(f[6], f[7]) << 16);
+      } else {
+        reinterpret_cast<uint4*>(p.rows + slot * D * 2)[32 * half + lane] = qk_pack_bf16(f);
+      }
+    }
+  }
+}
+
+cudaError_t launch_qk_norm_rope(const QkParams& p, cudaStream_t stream) {
+  const int64_t tasks = (p.q ? p.T * QK_TASKS : 0) + (p.k ? ceil_div(p.T, QK_ROWS) : 0);
+  if (tasks == 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ceil_div(tasks, QK_THREADS / 32));
+  cfg.blockDim = dim3(QK_THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel, p);
+}
+
+}  // namespace csa2

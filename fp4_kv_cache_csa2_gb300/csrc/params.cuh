@@ -88,6 +88,49 @@ struct HvParams {             // HISA view of the summary store as an m = 1 cach
   int32_t* view_n;            // [B] out
 };
 
+struct QkParams {             // norm and rotation of queries and window keys
+  int64_t T;
+  const int64_t* pos;         // [T], -1: padding
+  const float* rope_cs;       // [rope_P][32][2]
+  int64_t rope_P;
+  float eps;
+  const uint16_t* q;          // token t at t * q_stride: [64][512], or null
+  int64_t q_stride;
+  const float* q_weight;      // [512] or null
+  uint16_t* q_out;            // [T][64][512]
+  const uint16_t* k;          // token t at t * k_stride: [512], or null
+  int64_t k_stride;
+  const float* k_weight;      // [512] or null
+  uint8_t* rows;              // [n_rows][512] bf16, or E4M3 bytes when rows_fp8
+  int64_t n_rows;
+  const int64_t* k_slot;      // [T] row of each token (-1: none), or null: row = token
+  int rows_fp8;
+  WsHeader* hdr;
+};
+
+struct KeysParams {           // attention over every visible key
+  const uint16_t* q;          // [BQ][64][512] bf16
+  const int64_t* q_pos;       // [BQ]
+  int Q;
+  const uint8_t* rows;        // [B][S][512] bf16, or E4M3 bytes when rows_fp8
+  const int64_t* base_pos;    // [B] position of row 0
+  int64_t S;
+  const uint8_t* sinks;       // [B][n_sink][512] rows of positions 0 .. n_sink - 1, or null
+  int n_sink;
+  int rows_fp8;
+  int64_t W;                  // window
+  const uint8_t* main_kv;     // [B][cap][288], or null: no cache entries
+  int64_t cap;
+  const int32_t* n_entries;   // [B]
+  int m;
+  float scale;
+  uint16_t* out;              // [BQ][64][512] bf16
+  float* lse;                 // [BQ][64] or null
+  int split;                  // CTAs per query (set by the launcher)
+  float* part;                // split > 1: partial states
+  WsHeader* hdr;
+};
+
 cudaError_t launch_cache_write(const CwParams& p, cudaStream_t stream, int num_sms);
 cudaError_t launch_swa_fp8(const uint16_t* x, int64_t n_rows, uint8_t* out, cudaStream_t stream);
 cudaError_t launch_index_score(IsParams p, cudaStream_t stream);
@@ -110,5 +153,10 @@ size_t attn_partials_bytes(int64_t BQ, int K);
 int attn_split_max_queries();
 cudaError_t launch_block_summary(const HsParams& p, cudaStream_t stream);
 cudaError_t launch_hisa_view(const HvParams& p, cudaStream_t stream);
+// `chunks`: runs of 128 keys of the longest query (for the split over CTAs);
+// `part`: keys_part_bytes(B * Q, chunks) of scratch
+cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* part, cudaStream_t stream);
+size_t keys_part_bytes(int64_t BQ, int64_t chunks);
+cudaError_t launch_qk_norm_rope(const QkParams& p, cudaStream_t stream);
 
 }  // namespace csa2

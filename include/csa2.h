@@ -381,6 +381,117 @@ csa2_status csa2_decode(const csa2_cache *cache, const csa2_decode_args *args, v
                         size_t ws_bytes, void *stream);
 
 /*
+ * Queries and window keys from their projections: RMSNorm over the 512
+ * channels of each head and the rotation of its last 64, in one pass.  The
+ * outputs are what the attention calls take (q, and rows of a window buffer).
+ * [zartbot §1.2 rope_head_dim, §2.4.4: norm, then RoPE, then the stored format]
+ *   y = x / sqrt(mean(x^2) + eps) * weight, then pairs (448+2i, 449+2i) rotate
+ *   with row pos of the table; binary32 until the one final rounding.
+ * Tokens with pos = -1 are padding: nothing of theirs is written.  Any other
+ * position outside [0, rope_P) is skipped and raises CSA2_ERR_BOUNDS, and so
+ * does a slot outside [0, n_rows) (-1 skips the row without an error).  The
+ * slots of a call must be distinct (a row that two tokens name holds channels
+ * of either).  q_out may be q itself (q_stride = 64 * 512); any other overlap
+ * of an output with an input or with the other output returns
+ * CSA2_ERR_INVALID_ARG.  Either q or k may be NULL (that part is left out).
+ * Device pointers are 16-byte aligned (pos and k_slot 8-byte); strides are
+ * multiples of 8 and at least a token's size.  T <= 2^26.  Needs only the
+ * workspace header.
+ */
+typedef struct {
+    int64_t T;                  /* tokens                                       */
+    const int64_t *pos;         /* [T] rotation position, -1: padding           */
+    const float *rope_cs;       /* [rope_P][32][2] from csa2_rope_table         */
+    int64_t rope_P;
+    float eps;                  /* finite, >= 0                                 */
+    int32_t rows_fp8;           /* 0: rows is bf16; 1: E4M3, saturating at 448  */
+    const uint16_t *q;          /* bf16, token t at q + t * q_stride: [64][512] */
+    int64_t q_stride;           /* elements                                     */
+    const float *q_weight;      /* [512], NULL: 1                               */
+    uint16_t *q_out;            /* bf16 [T][64][512]                            */
+    const uint16_t *k;          /* bf16, token t at k + t * k_stride: [512]     */
+    int64_t k_stride;           /* elements                                     */
+    const float *k_weight;      /* [512], NULL: 1                               */
+    void *rows;                 /* [n_rows][512] window rows                    */
+    int64_t n_rows;
+    const int64_t *k_slot;      /* [T] row of token t, -1: none; NULL: row t    */
+} csa2_qk_args;
+
+csa2_status csa2_qk_norm_rope(const csa2_qk_args *args, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of a window-only layer: 64 query heads over the window rows and a
+ * few first tokens that stay visible (sinks), key = value, one softmax.  The
+ * schedule of the pages begins with two such layers.  [dilfish §4.3]
+ *   A query at raw position t sees the positions max(0, t-W+1) .. t of `rows`
+ *   and the sinks at positions p < min(n_sink, max(0, t-W+1)); a query with
+ *   t < 0 (padding) sees nothing: its output is zeros, its lse -inf.
+ *   lse (optional) = log sum exp(scale * q_h . v_i), natural logarithm.
+ * A window position outside the supplied rows is skipped and raises
+ * CSA2_ERR_BOUNDS.  Rows and sinks that a query does not see may hold anything,
+ * infinities and NaN among it.
+ * Sizes: W >= 1, n_sink >= 0 (sinks may be NULL when 0), S >= 0; B * Q <= 2^24,
+ * B * S < 2^31 and B * n_sink < 2^31, else CSA2_ERR_UNSUPPORTED.  q, rows, sinks
+ * and out 16-byte, q_pos, swa_base_pos 8-byte and lse 4-byte aligned; out and
+ * lse must not overlap an input or each other.
+ * Precision: bf16 operands, binary32 accumulation and softmax state; E4M3 rows
+ * are exact.  Workspace: csa2_window_attn_workspace_size (partial states when
+ * a query's keys are divided over several CTAs).
+ */
+typedef struct {
+    int B, Q;                   /* sequences, queries per sequence              */
+    int S;                      /* window rows supplied per sequence            */
+    int W;                      /* window size                                  */
+    int n_sink;                 /* first tokens that stay visible               */
+    float scale;                /* softmax scale                                */
+    const int64_t *q_pos;       /* [B][Q] raw positions                         */
+    const uint16_t *q;          /* bf16 [B][Q][64][512], rotated                */
+    const void *rows;           /* [B][S][512]: row r is position swa_base_pos[b] + r */
+    const int64_t *swa_base_pos;/* [B]                                          */
+    const void *sinks;          /* [B][n_sink][512]: row p is position p        */
+    uint16_t *out;              /* bf16 [B][Q][64][512]                         */
+    float *lse;                 /* [B][Q][64] or NULL                           */
+    int32_t rows_fp8;           /* 0: rows and sinks are bf16; 1: E4M3          */
+} csa2_window_args;
+
+size_t csa2_window_attn_workspace_size(int B, int Q, int W, int n_sink);
+csa2_status csa2_window_attn(const csa2_window_args *args, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Attention over every visible entry of the 4-bit cache and the 128-token
+ * window: csa2_sparse_swa_attn with no selection, for contexts that are short
+ * enough not to need one and as what a selection is measured against.
+ *   A query at raw position t >= 0 sees the entries j < min(n_entries[b],
+ *   floor((t+1)/m)) and the window positions max(0, t-127) .. t; a query with
+ *   t < 0 (padding) sees nothing: its output is zeros, its lse -inf.
+ *   max_n        the most entries any query sees: it only sizes the split of a
+ *                query over CTAs, every visible entry is attended in any case.
+ * n_entries[b] > cap raises CSA2_ERR_BOUNDS (cap entries are attended), and so
+ * does a window position outside the supplied rows (skipped).  Entries and
+ * rows that a query does not see may hold anything.
+ * Sizes and alignment as in csa2_window_attn; operands as in
+ * csa2_sparse_swa_attn (f16, the dequantised entries exact).  Workspace:
+ * csa2_dense_attn_workspace_size with the call's B, Q and max_n.
+ */
+typedef struct {
+    int B, Q;                   /* sequences, queries per sequence              */
+    int S;                      /* window rows supplied per sequence            */
+    float scale;                /* softmax scale                                */
+    int64_t max_n;              /* >= 0                                         */
+    const int64_t *q_pos;       /* [B][Q] raw positions                         */
+    const uint16_t *q;          /* bf16 [B][Q][64][512], rotated                */
+    const void *swa;            /* [B][S][512]                                  */
+    const int64_t *swa_base_pos;/* [B]                                          */
+    uint16_t *out;              /* bf16 [B][Q][64][512]                         */
+    float *lse;                 /* [B][Q][64] or NULL                           */
+    int32_t swa_fp8;            /* 0: swa is bf16; 1: E4M3                      */
+} csa2_dense_args;
+
+size_t csa2_dense_attn_workspace_size(int B, int Q, int64_t max_n);
+csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_dense_args *args, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/*
  * Test hook for the device-side timeout path; off unless a caller turns it on,
  * and never needed in production.  The pages have no counterpart.
  * While enabled (enable = 1) on the calling host thread, every index-scan
