@@ -4,19 +4,22 @@
 //
 //   o_h = sum_i softmax_i(scale q_h . v_i) v_i,   lse_h = log sum_i exp(scale q_h . v_i)
 //
-// A query's keys are numbered in chunks of 128: the window rows (positions
-// max(0, t-W+1) .. t), then the sinks (those before the window), then the
-// cache entries.  A CTA walks a run of a query's chunks with one running
-// softmax state; a query's chunks are divided over `split` CTAs when the call
-// has too few queries to fill the GPU, and keys_combine_kernel joins their
-// states.
+// A query's keys are numbered in chunks of 64: the window rows (positions
+// max(0, t-W+1) .. t), then the sinks (those before the window), then the cache
+// entries.  A CTA walks a run of one query's chunks with one running softmax
+// state.  A call with too few queries to fill the GPU divides each query's chunks
+// over `split` CTAs, and keys_combine_kernel joins their states.
 //
-// Per chunk (one CTA, one query):
-//   * S^T = K Q^T    M = 128 keys, N = 64 heads, K = 512   (32 MMAs, one accumulator)
-//   * P^T = 2^(S^T scale log2 e - m)   16-bit, MN-major operand of the next product;
-//     the reference m of a head moves only when a chunk exceeds it by more than
-//     e^8 (then O^T and the sum are rescaled), so P stays inside f16
-//   * O^T += V^T P^T 4 tiles of M = 128 dims, N = 64, K = 128 (32 MMAs)
+// Per chunk, with the 64 heads as the rows of M = 64 tiles:
+//   * S = Q K^T   N = keys, K = 512 (32 MMAs)
+//   * softmax, one thread a head, straight from TMEM; P = 2^(S scale log2 e - m) goes
+//     to shared memory as the 16-bit A operand of the next product.  The reference m
+//     of a head moves only when a chunk exceeds it by more than e^8 (then the head's O
+//     and its sum are rescaled), so P stays inside f16
+//   * O += P V    N = 2 x 256 dims, K = keys: V is the K tile read MN-major
+// An M = 64 accumulator takes 16 lanes of each of TMEM's four lane quarters: the
+// dims 0..255 of O lie in lanes 0..15 of a quarter, the dims 256..511 in lanes
+// 16..31 of the same 256 columns, and S is double-buffered beside them.
 // Operands: F16 (calls with cache entries) keeps every dequantised FP4 value
 // exactly (at most 6 significant bits, 2^-10 .. 2688) and rounds q and bf16
 // window rows to f16, exact inside [2^-14, 65504], with P to 11 bits.  Without
@@ -24,54 +27,60 @@
 // exactly, P to 8 bits (its rounding errors are independent and average out;
 // the sum of the softmax is taken before that rounding, in binary32).
 //
-// Roles: warps 0..7 softmax and output, warps 8..15 bring a chunk into the key
-// buffer (entries dequantised from registers that were loaded one chunk ahead,
-// rows by TMA and then widened or rounded in place), one thread of warp 16
-// issues all MMAs.  Tile t of the key buffer (dims 128t ..) is refilled as soon
-// as the O^T tile t of the chunk before is done, and S^T's chain follows tile by
-// tile.  All waits are bounded; a timeout reports CSA2_ERR_TIMEOUT and every
-// thread still takes every barrier.
+// Shared memory: Q 64 KB, two K buffers of [64 keys][512 dims] (two halves of 32 KB,
+// four SW128 column chunks each), P 8 KB, and the next chunk's entries as stored,
+// 18 KB.  Roles: warps 0..3 softmax and output; warps 4..11 fill the K buffers
+// (entries: from the staged bytes to registers, then a half at a time; rows: widened
+// or rounded in place); warp 12 issues the MMAs, S of chunk c + 1 before O of chunk c,
+// so that the softmax of a chunk runs beside the products of its neighbours;
+// warp 13 issues the copies: entries to the staging area, rows to their K buffer.
+// A half of a K buffer is refilled as soon as its part of O is done.  All waits are
+// bounded; a timeout reports CSA2_ERR_TIMEOUT and every thread still takes every
+// barrier.
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "params.cuh"
 
 namespace csa2 {
 
-constexpr int KA_MATH_WARPS = 8;                          // softmax, output
-constexpr int KA_FILL_WARPS = 8;                          // key buffer
+constexpr int KA_SOFT_WARPS = 4;                          // softmax, output: lane (mod 16) = head
+constexpr int KA_FILL_WARPS = 8;                          // K buffers
 constexpr int KA_FILL = 32 * KA_FILL_WARPS;
-constexpr int KA_MMA_WARP = KA_MATH_WARPS + KA_FILL_WARPS;
-constexpr int KA_THREADS = 32 * (KA_MMA_WARP + 1);
-constexpr int KA_KEYS = 128;                              // keys per chunk
-constexpr int KA_KCOL = KA_KEYS * 128;                    // column chunk of 64 dims: [128 keys][128 B], SW128
-constexpr int KA_QCOL = H * 128;                          // [64 heads][128 B], SW128
-constexpr int KA_OFF_Q = 8 * KA_KCOL;
-constexpr int KA_OFF_P = KA_OFF_Q + 8 * KA_QCOL;          // P^T [128 keys][64 heads], SW128
-constexpr int KA_OFF_SMALL = KA_OFF_P + KA_KEYS * H * 2;
-constexpr int KA_TMEM_COLS = 512;                         // S^T 64 + O^T 256, a power of two
-constexpr int KA_S_COL = 0;
-constexpr int KA_O_COL = 256;
+constexpr int KA_MMA_WARP = KA_SOFT_WARPS + KA_FILL_WARPS;
+constexpr int KA_COPY_WARP = KA_MMA_WARP + 1;
+constexpr int KA_THREADS = 32 * (KA_COPY_WARP + 1);
+constexpr int KA_KEYS = KEYS_CHUNK;                       // keys per chunk
+constexpr int KA_COL = 64 * 128;                          // [64 rows][64 dims] 16-bit, SW128
+constexpr int KA_HALF = 4 * KA_COL;                       // half of a K buffer: 256 dims
+constexpr int KA_OFF_Q = 4 * KA_HALF;
+constexpr int KA_OFF_P = KA_OFF_Q + 8 * KA_COL;
+constexpr int KA_OFF_STAGE = KA_OFF_P + KA_COL;
+constexpr int KA_OFF_SMALL = KA_OFF_STAGE + KA_KEYS * MAIN_BYTES;
+constexpr int KA_TMEM_COLS = 512;
+constexpr int KA_O_COL = 0;                               // dims 256 h ..: lanes 16 h .. of each quarter
+constexpr int KA_S_COL = 256;                             // S of chunk c at 64 (c % 2)
 constexpr float KA_LOG2E = 1.4426950408889634f;
 constexpr float KA_LN2 = 0.6931471805599453f;
 constexpr float KA_TAU = 8.0f * KA_LOG2E;
 constexpr int KA_PART_FLOATS = 2 * H + H * D;             // one partial state: references, sums, O [head][dim]
 
 struct KaSmall {
-  float red[KA_MATH_WARPS][32];
-  alignas(16) float mv[KA_MATH_WARPS][32];
-  uint64_t q_full[4];                 // TMA: Q column chunks 2t, 2t + 1
-  uint64_t row_full[4];               // TMA: a row chunk's column chunks 2t, 2t + 1
-  uint64_t kready[4];                 // tile t of a chunk is in the key buffer (a fill warp each)
-  uint64_t s_full;                    // S^T of a chunk is done
-  uint64_t p_ready;                   // P^T is written, O^T rescaled if needed (a math warp each)
-  uint64_t pv_done[4];                // O^T tile t of a chunk is done
+  uint64_t q_full;                    // TMA: Q
+  uint64_t stage_full, stage_free;    // the staged entries have come / were read (a fill warp each)
+  uint64_t row_full[2][2];            // TMA: rows in half h of K buffer i
+  uint64_t full[2][2];                // half h of K buffer i is filled (a fill warp each)
+  uint64_t free_[2][2];               // ... its part of O is done
+  uint64_t s_full;                    // S of a chunk is done
+  uint64_t p_ready;                   // P is written, O rescaled if needed (a softmax warp each)
   uint32_t tmem_base;
   int err;
 };
 constexpr int KA_SMEM = KA_OFF_SMALL + (int)sizeof(KaSmall) + 1024;
 static_assert(KA_SMEM <= 227 * 1024, "shared memory per CTA");
 
-__device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t parity, KaSmall& sm, WsHeader* hdr, int where) {
-  if (tc::bar_wait(bar, parity)) return true;
+__device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t count, KaSmall& sm, WsHeader* hdr, int where) {
+  if (tc::bar_wait(bar, count & 1u)) return true;
   if (atomicExch(&sm.err, 1) == 0) report(hdr, CSA2_ERR_TIMEOUT, where);
   return false;
 }
@@ -79,52 +88,60 @@ __device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t parity, KaSmall&
 // One query's keys and how they lie in chunks.
 struct KaQuery {
   int64_t t, lo;                      // position, first window position
+  int64_t r0;                         // its first window row that was supplied
   int64_t wn, sn, en;                 // window rows, sinks, cache entries it sees
-  int64_t cw, cs, nc;                 // window chunks, sink chunks, all chunks
+  int64_t cw, cr, nc;                 // window chunks, chunks of rows (window and sinks), all chunks
 };
 
-__device__ __forceinline__ KaQuery ka_query(const KeysParams& p, int64_t bq, int b) {
+__device__ __forceinline__ KaQuery ka_query(const KeysParams& p, int64_t bq, int b, int64_t base) {
   KaQuery q;
   q.t = p.q_pos[bq];
   const bool live = q.t >= 0;
   q.lo = live && q.t >= p.W ? q.t - p.W + 1 : 0;
-  q.wn = live ? q.t - q.lo + 1 : 0;
+  // the window positions lo .. t that lie in rows 0 .. S - 1 (unsigned differences: any
+  // two positions have one), so that the work is bounded by what was supplied
+  q.r0 = q.wn = 0;
+  if (live && q.t >= base) {
+    const uint64_t s = (uint64_t)p.S, r0 = q.lo > base ? (uint64_t)q.lo - (uint64_t)base : 0;
+    const uint64_t end = (uint64_t)q.t - (uint64_t)base;     // row of position t
+    const uint64_t r1 = end < s ? end + 1 : s;
+    if (r0 < r1) {
+      q.r0 = (int64_t)r0;
+      q.wn = (int64_t)(r1 - r0);
+    }
+  }
   q.sn = live ? (q.lo < p.n_sink ? q.lo : (int64_t)p.n_sink) : 0;
   q.en = 0;
   if (live && p.main_kv) {
     q.en = visible_entries(q.t, p.m, p.n_entries[b]);
-    if (q.en > p.cap) q.en = p.cap;   // reported below
+    if (q.en > p.cap) q.en = p.cap;   // reported by the kernel
     if (q.en < 0) q.en = 0;
   }
   q.cw = ceil_div(q.wn, KA_KEYS);
-  q.cs = ceil_div(q.sn, KA_KEYS);
-  q.nc = q.cw + q.cs + ceil_div(q.en, KA_KEYS);
+  q.cr = q.cw + ceil_div(q.sn, KA_KEYS);
+  q.nc = q.cr + ceil_div(q.en, KA_KEYS);
   return q;
 }
 
-// A chunk's rows: where they start in their buffer (row 0 = the sequence's
-// first) and which of the 128 are visible and supplied, [ra, rb).
-struct KaRows {
-  int64_t first;
-  int ra, rb;
+struct KaChunk {
+  int64_t first;                      // buffer row or entry of key 0
+  int b;                              // its keys
+  int n;                              // the same rounded up to a multiple of 16
 };
 
-__device__ __forceinline__ KaRows ka_rows(const KeysParams& p, const KaQuery& q, int64_t c, int64_t base) {
-  KaRows r;
+__device__ __forceinline__ KaChunk ka_chunk(const KaQuery& q, int64_t c) {
+  KaChunk k;
+  int64_t left;
   if (c < q.cw) {
-    r.first = q.lo + KA_KEYS * c - base;
-    const int64_t n = q.wn - KA_KEYS * c;
-    r.rb = n < KA_KEYS ? (int)n : KA_KEYS;
-    if (r.first + r.rb > p.S) r.rb = r.first >= p.S ? 0 : (int)(p.S - r.first);
-    r.ra = r.first >= 0 ? 0 : (r.first <= -KA_KEYS ? KA_KEYS : (int)-r.first);
+    k.first = q.r0 + KA_KEYS * c;
+    left = q.wn - KA_KEYS * c;
   } else {
-    r.first = KA_KEYS * (c - q.cw);
-    const int64_t n = q.sn - r.first;
-    r.rb = n < KA_KEYS ? (int)n : KA_KEYS;
-    r.ra = 0;
+    k.first = KA_KEYS * (c - (c < q.cr ? q.cw : q.cr));
+    left = (c < q.cr ? q.sn : q.en) - k.first;
   }
-  if (r.ra >= r.rb) r.ra = r.rb = 0;
-  return r;
+  k.b = left < KA_KEYS ? (int)left : KA_KEYS;
+  k.n = (k.b + 15) & ~15;
+  return k;
 }
 
 // f16x2 -> bf16x2, for values that bf16 holds exactly
@@ -139,9 +156,9 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
                  const __grid_constant__ CUtensorMap map_sinks) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = tc::align_smem_1k(smem_raw);
-  unsigned char* kbuf = smem;
   unsigned char* qbuf = smem + KA_OFF_Q;
   unsigned char* pbuf = smem + KA_OFF_P;
+  unsigned char* stage = smem + KA_OFF_STAGE;
   KaSmall& sm = *reinterpret_cast<KaSmall*>(smem + KA_OFF_SMALL);
 
   const int split = SPLIT ? p.split : 1;
@@ -153,14 +170,17 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   // ---------------- set-up (reads no input: overlaps the previous kernel)
   if (warp == KA_MMA_WARP) tc::tmem_alloc(&sm.tmem_base, KA_TMEM_COLS);
   if (tid == 0) {
-    for (int t = 0; t < 4; t++) {
-      tc::bar_init(&sm.q_full[t], 1);
-      tc::bar_init(&sm.row_full[t], 1);
-      tc::bar_init(&sm.kready[t], KA_FILL_WARPS);
-      tc::bar_init(&sm.pv_done[t], 1);
-    }
+    tc::bar_init(&sm.q_full, 1);
+    tc::bar_init(&sm.stage_full, 1);
+    tc::bar_init(&sm.stage_free, KA_FILL_WARPS);
+    for (int i = 0; i < 2; i++)
+      for (int h = 0; h < 2; h++) {
+        tc::bar_init(&sm.row_full[i][h], 1);
+        tc::bar_init(&sm.full[i][h], KA_FILL_WARPS);
+        tc::bar_init(&sm.free_[i][h], 1);
+      }
     tc::bar_init(&sm.s_full, 1);
-    tc::bar_init(&sm.p_ready, KA_MATH_WARPS);
+    tc::bar_init(&sm.p_ready, KA_SOFT_WARPS);
     sm.err = 0;
     tc::bar_init_fence();
     tc::prefetch_tensormap(&map_q);
@@ -173,150 +193,161 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   const uint32_t tmem = sm.tmem_base;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  const KaQuery q = ka_query(p, bq, b);
   const int64_t base = p.base_pos[b];
-  const int64_t c_lo = q.nc * sp / split, c_hi = q.nc * (sp + 1) / split;
+  const KaQuery q = ka_query(p, bq, b, base);
+  const int64_t c_lo = q.nc * sp / split;
+  const int n_ch = (int)(q.nc * (sp + 1) / split - c_lo);
   if (sp == 0 && tid == 0 && q.t >= 0) {              // what the caller did not supply
     if (q.lo < base) report(p.hdr, CSA2_ERR_BOUNDS, q.lo);
-    else if (q.t - base >= p.S) report(p.hdr, CSA2_ERR_BOUNDS, q.t);
+    else if ((uint64_t)q.t - (uint64_t)base >= (uint64_t)p.S) report(p.hdr, CSA2_ERR_BOUNDS, q.t);
     if (p.main_kv && p.n_entries[b] > p.cap) report(p.hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
   }
 
+  // Chunk c (counted from c_lo) uses K buffer c % 2; it is that buffer's use c / 2.
   if (warp == KA_MMA_WARP) {
-    // ================= MMAs
-    if (lane == 0 && c_lo < c_hi) {
-      constexpr uint32_t idesc_s = F16 ? tc::idesc_f16(KA_KEYS, H, 0, 0) : tc::idesc_bf16(KA_KEYS, H, 0, 0);
-      constexpr uint32_t idesc_o = F16 ? tc::idesc_f16(128, H, 1, 1) : tc::idesc_bf16(128, H, 1, 1);
-      const uint64_t a_s = tc::smem_desc(tc::smem_u32(kbuf), 16, 1024, tc::SW_128B);
-      const uint64_t b_s = tc::smem_desc(tc::smem_u32(qbuf), 16, 1024, tc::SW_128B);
-      const uint64_t a_o = tc::smem_desc(tc::smem_u32(kbuf), KA_KCOL, 1024, tc::SW_128B);
-      const uint64_t b_o = tc::smem_desc(tc::smem_u32(pbuf), 8192, 1024, tc::SW_128B);
-      bool ok = true;
-      uint32_t ph = 0;
-      for (int64_t c = c_lo; c < c_hi; c++, ph ^= 1u) {
+    // ================= MMAs (the whole warp runs the loop, one elected lane issues)
+    constexpr uint32_t idesc_s = F16 ? tc::idesc_f16(H, 0, 0, 0) : tc::idesc_bf16(H, 0, 0, 0);       // + N
+    constexpr uint32_t idesc_o = F16 ? tc::idesc_f16(H, 256, 0, 1) : tc::idesc_bf16(H, 256, 0, 1);
+    const uint64_t q_d = tc::smem_desc(tc::smem_u32(qbuf), 16, 1024, tc::SW_128B);
+    const uint64_t p_d = tc::smem_desc(tc::smem_u32(pbuf), 16, 1024, tc::SW_128B);
+    const uint64_t k_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
+    const uint64_t v_d = tc::smem_desc(tc::smem_u32(smem), KA_COL, 1024, tc::SW_128B);
+    bool ok = true;
+    auto scores = [&](int c) {
+      const uint32_t idesc = idesc_s | (uint32_t)(ka_chunk(q, c_lo + c).n >> 3) << 17;
+      const uint32_t s = tmem + KA_S_COL + 64 * (c & 1);
 #pragma unroll
-        for (int t = 0; t < 4; t++) {
-          ok = ka_wait(&sm.kready[t], ph, sm, p.hdr, 41) && ok;
-          tc::fence_after_sync();
-          if (ok) {
+      for (int h = 0; h < 2; h++) {
+        ok = ka_wait(&sm.full[c & 1][h], c >> 1, sm, p.hdr, 41) && ok;
+        tc::fence_after_sync();
+        if (ok) {
+          const uint64_t qa = q_d + (uint32_t)(h * (KA_HALF >> 4)), ka = k_d + (uint32_t)((2 * (c & 1) + h) * (KA_HALF >> 4));
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-              const uint32_t ka = (uint32_t)((2 * t + (i >> 2)) * KA_KCOL + (i & 3) * 32) >> 4;
-              const uint32_t qa = (uint32_t)((2 * t + (i >> 2)) * KA_QCOL + (i & 3) * 32) >> 4;
-              tc::mma_f16(tmem + KA_S_COL, a_s + ka, b_s + qa, idesc_s, (t || i) ? 1u : 0u);
-            }
+          for (int i = 0; i < 16; i++) {
+            const uint32_t off = (uint32_t)((i >> 2) * KA_COL + (i & 3) * 32) >> 4;
+            tc::mma_f16_warp(s, qa + off, ka + off, idesc, (h || i) ? 1u : 0u);
           }
         }
-        tc::commit(&sm.s_full);
-        ok = ka_wait(&sm.p_ready, ph, sm, p.hdr, 42) && ok;
-        tc::fence_after_sync();
-        const uint32_t add = c > c_lo ? 1u : 0u;
+      }
+      tc::commit_warp(&sm.s_full);
+    };
+    if (n_ch > 0) scores(0);
+    for (int c = 0; c < n_ch; c++) {
+      if (c + 1 < n_ch) scores(c + 1);
+      const int steps = ka_chunk(q, c_lo + c).n / 16;
+      ok = ka_wait(&sm.p_ready, c, sm, p.hdr, 42) && ok;
+      tc::fence_after_sync();
 #pragma unroll
-        for (int t = 0; t < 4; t++) {
-          if (ok) {
+      for (int h = 0; h < 2; h++) {
+        if (ok) {
+          const uint64_t va = v_d + (uint32_t)((2 * (c & 1) + h) * (KA_HALF >> 4));
 #pragma unroll
-            for (int ks = 0; ks < KA_KEYS / 16; ks++)
-              tc::mma_f16(tmem + KA_O_COL + 64 * t, a_o + (uint32_t)((2 * t * KA_KCOL + ks * 2048) >> 4),
-                          b_o + (uint32_t)(ks * 2048 >> 4), idesc_o, ks ? 1u : add);
+          for (int ks = 0; ks < KA_KEYS / 16; ks++)
+            if (ks < steps)
+              tc::mma_f16_warp(tmem + KA_O_COL + ((uint32_t)(16 * h) << 16), p_d + (uint32_t)(2 * ks),
+                               va + (uint32_t)(ks * (2048 >> 4)), idesc_o, (c || ks) ? 1u : 0u);
+        }
+        tc::commit_warp(&sm.free_[c & 1][h]);
+      }
+    }
+  } else if (warp == KA_COPY_WARP) {
+    // ================= copies
+    if (lane == 0 && n_ch > 0) {
+      bool ok = true;
+      tc::bar_arrive_expect_tx(&sm.q_full, 8u * KA_COL);
+      for (int i = 0; i < 8; i++) tc::tma_load_2d(qbuf + i * KA_COL, &map_q, i * 64, (int32_t)(bq * H), &sm.q_full);
+      uint32_t staged = 0;
+      for (int c = 0; c < n_ch; c++) {
+        const KaChunk k = ka_chunk(q, c_lo + c);
+        if (c_lo + c >= q.cr) {                       // entries [first, first + b), contiguous
+          if (staged > 0) ok = ka_wait(&sm.stage_free, staged - 1, sm, p.hdr, 43) && ok;
+          staged++;
+          tc::bar_arrive_expect_tx(&sm.stage_full, (uint32_t)(k.b * MAIN_BYTES));
+          tc::bulk_load(stage, p.main_kv + ((int64_t)b * p.cap + k.first) * MAIN_BYTES, (uint32_t)(k.b * MAIN_BYTES),
+                        &sm.stage_full);
+        } else {
+          const bool window = c_lo + c < q.cw;
+          const CUtensorMap* map = window ? &map_rows : &map_sinks;
+          const int32_t y = (int32_t)((int64_t)b * (window ? p.S : (int64_t)p.n_sink) + k.first);
+          for (int h = 0; h < 2; h++) {
+            if (c >= 2) {
+              // the tensor cores have read the half (waited for here), after the fill warps wrote
+              // it and made that visible to the asynchronous proxy
+              ok = ka_wait(&sm.free_[c & 1][h], (c >> 1) - 1, sm, p.hdr, 44) && ok;
+            }
+            unsigned char* kt = smem + (2 * (c & 1) + h) * KA_HALF;
+            tc::bar_arrive_expect_tx(&sm.row_full[c & 1][h], p.rows_fp8 ? KA_HALF / 2u : (uint32_t)KA_HALF);
+            for (int i = 0; i < 4; i++)
+              tc::tma_load_2d(kt + i * KA_COL + (p.rows_fp8 ? KA_COL / 2 : 0), map, (4 * h + i) * 64, y,
+                              &sm.row_full[c & 1][h]);
           }
-          tc::commit(&sm.pv_done[t]);
         }
       }
     }
     __syncwarp();
-  } else if (warp >= KA_MATH_WARPS) {
-    // ================= the key buffer
-    const int ft = tid - 32 * KA_MATH_WARPS;
-    const int key = ft >> 1, kh = ft & 1;             // entries: key row, 64-dim half of each tile
-    const uint32_t xr = (uint32_t)key & 7u;
-    const bool lead = ft == 0;
+  } else if (warp >= KA_SOFT_WARPS) {
+    // ================= K buffers
+    const int ft = tid - 32 * KA_SOFT_WARPS;
     bool ok = true;
-    const int64_t c_rows = q.cw + q.cs;
-    if (lead && c_lo < c_hi) {                        // Q, 8 column chunks of 64 heads
-      for (int t = 0; t < 4; t++) {
-        tc::bar_arrive_expect_tx(&sm.q_full[t], 2u * KA_QCOL);
-        for (int c = 2 * t; c < 2 * t + 2; c++)
-          tc::tma_load_2d(qbuf + c * KA_QCOL, &map_q, c * 64, (int32_t)(bq * H), &sm.q_full[t]);
-      }
-    }
-    uint4 cd[8];                                      // FP4 codes of the next entry chunk: tile t in cd[2t], cd[2t+1]
-    uint4 scv[2];                                     // its 32 scale bytes
-    auto load_entries = [&](int64_t c) {
-      const int64_t e = KA_KEYS * (c - c_rows) + key;
+    // entries: thread = (key, 16 bytes of each 64: 32 of each 128 dims).  The lanes of an
+    // eight-lane phase hold keys k and k + 2: with 18 units of 16 bytes an entry, their reads
+    // lie in eight different bank groups
+    const int k8 = (ft >> 2) & 7, j = ft & 3;
+    const int key = ((ft >> 2) & ~7) + ((k8 & 4) | (k8 & 1) << 1 | (k8 >> 1 & 1));
+    uint4 cd[4] = {}, sc[2] = {};                               // codes of the four quarters, scales of the two halves
+    auto dequant = [&](int i, uint32_t* o) {          // quarter i: 32 dims
+      const uint4 c = cd[i], s = sc[i >> 1];
+      const uint32_t w = (i & 1) ? (j & 2 ? s.w : s.z) : (j & 2 ? s.y : s.x);   // scale bytes 2j, 2j + 1 of the quarter
+      const uint32_t w2 = w >> (16 * (j & 1));
+      const uint32_t sa = e4m3x2_to_f16x2(prmt(w2, 0u, 0x0000u)), sb = e4m3x2_to_f16x2(prmt(w2, 0u, 0x1111u));
+      const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-      for (int i = 0; i < 8; i++) cd[i] = make_uint4(0u, 0u, 0u, 0u);
-      scv[0] = scv[1] = make_uint4(0u, 0u, 0u, 0u);
-      if (e < q.en) {
-        const uint4* s4 = reinterpret_cast<const uint4*>(p.main_kv + ((int64_t)b * p.cap + e) * MAIN_BYTES);
+      for (int g = 0; g < 4; g++) {
+        e2m1x8_to_f16(cw[g], o + 4 * g);
 #pragma unroll
-        for (int t = 0; t < 4; t++) {
-          cd[2 * t] = __ldg(s4 + 4 * t + 2 * kh);
-          cd[2 * t + 1] = __ldg(s4 + 4 * t + 2 * kh + 1);
-        }
-        scv[0] = __ldg(s4 + 16);
-        scv[1] = __ldg(s4 + 17);
+        for (int x = 0; x < 4; x++) o[4 * g + x] = hmul2(o[4 * g + x], g < 2 ? sa : sb);
       }
     };
-    auto dequant_tile = [&](int t) {
-      const uint4 c0 = cd[2 * t], c1 = cd[2 * t + 1];
-      const uint32_t cwd[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-      const uint4& sv = scv[t >> 1];
-      const uint32_t sw = (t & 1) ? (kh ? sv.w : sv.z) : (kh ? sv.y : sv.x);
-      unsigned char* dst = kbuf + (2 * t + kh) * KA_KCOL + key * 128;
+    auto store = [&](unsigned char* kt, int i, const uint32_t* o) {
+      // column chunk 2 (i % 2) + j / 2, units 4 (j % 2) ..; lanes with j >= 2 walk them as g ^ 1,
+      // so that the eight lanes of a phase store to eight different bank groups
+      unsigned char* dst = kt + (2 * (i & 1) + (j >> 1)) * KA_COL + key * 128;
+      const bool odd = (j & 2) != 0;
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        // the odd half walks its 16-channel groups as i ^ 2: the two threads of a key
-        // then never store to the same 16-byte bank group in one instruction
-        const int g = kh ? (i ^ 2) : i;
-        const uint32_t wa = kh ? cwd[2 * (i ^ 2)] : cwd[2 * i];
-        const uint32_t wb = kh ? cwd[2 * (i ^ 2) + 1] : cwd[2 * i + 1];
-        const uint32_t sc2 = e4m3x2_to_f16x2(prmt(sw >> (8 * g), 0u, 0x0000u));
-        uint32_t o[8];
-        e2m1x8_to_f16(wa, o);
-        e2m1x8_to_f16(wb, o + 4);
-#pragma unroll
-        for (int k = 0; k < 8; k++) o[k] = hmul2(o[k], sc2);
-        *reinterpret_cast<uint4*>(dst + (((2u * g) ^ xr) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(dst + (((2u * g + 1u) ^ xr) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      for (int g = 0; g < 4; g++) {
+        const uint4 v = make_uint4(odd ? o[4 * (g ^ 1)] : o[4 * g], odd ? o[4 * (g ^ 1) + 1] : o[4 * g + 1],
+                                   odd ? o[4 * (g ^ 1) + 2] : o[4 * g + 2], odd ? o[4 * (g ^ 1) + 3] : o[4 * g + 3]);
+        const uint32_t unit = (uint32_t)(4 * (j & 1) + (odd ? g ^ 1 : g));
+        *reinterpret_cast<uint4*>(dst + ((unit ^ (uint32_t)(key & 7)) << 4)) = v;
       }
     };
-    // a tile of rows that the copy has brought: E4M3 widened, bf16 rounded to f16
-    // when the operands are f16, rows outside [ra, rb) set to zero (a masked row
+    // a half of rows that the copy has brought: E4M3 widened, bf16 rounded to f16 when
+    // the operands are f16, rows behind the chunk's last set to zero (what is not seen
     // may hold anything, infinities among it)
-    auto convert_rows = [&](int t, const KaRows& r) {
-      unsigned char* kt = kbuf + 2 * t * KA_KCOL;
+    auto convert_rows = [&](unsigned char* kt, int rb) {
       if (p.rows_fp8) {
-        const int row = ft >> 1, h = ft & 1;
-        uint4 raw[2][2];
+        const int row = ft >> 2;
+        unsigned char* col = kt + (ft & 3) * KA_COL;
+        uint4 raw[4];
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const uint4* src = reinterpret_cast<const uint4*>(kt + i * KA_KCOL + KA_KCOL / 2 + row * 64 + h * 32);
-          raw[i][0] = src[0];
-          raw[i][1] = src[1];
-        }
+        for (int i = 0; i < 4; i++) raw[i] = reinterpret_cast<const uint4*>(col + KA_COL / 2 + row * 64)[i];
         named_sync(1, KA_FILL);
-        const bool vis = row >= r.ra && row < r.rb;
+        const bool vis = row < rb;
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
+        for (int x = 0; x < 8; x++) {
+          const uint4& w = raw[x >> 1];
+          const uint32_t lo = (x & 1) ? w.z : w.x, hi = (x & 1) ? w.w : w.y;
+          uint32_t o[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(hi >> 16)};
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const uint4& w = raw[i][j >> 1];
-            const uint32_t lo = (j & 1) ? w.z : w.x, hi = (j & 1) ? w.w : w.y;
-            uint32_t o[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
-                             e4m3x2_to_f16x2(hi >> 16)};
-#pragma unroll
-            for (int k = 0; k < 4; k++) o[k] = !vis ? 0u : (F16 ? o[k] : f16x2_to_bf16x2(o[k]));
-            *reinterpret_cast<uint4*>(kt + i * KA_KCOL + sw128((uint32_t)row, (uint32_t)(64 * h + 16 * j))) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-          }
+          for (int y = 0; y < 4; y++) o[y] = !vis ? 0u : (F16 ? o[y] : f16x2_to_bf16x2(o[y]));
+          *reinterpret_cast<uint4*>(col + sw128((uint32_t)row, (uint32_t)(16 * x))) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-      } else if (F16 || r.ra > 0 || r.rb < KA_KEYS) {
+      } else if (F16 || rb < KA_KEYS) {
 #pragma unroll 4
-        for (int i = ft; i < 2 * KA_KCOL / 16; i += KA_FILL) {
+        for (int i = ft; i < KA_HALF / 16; i += KA_FILL) {
           uint4* u = reinterpret_cast<uint4*>(kt) + i;
           const int row = (i >> 3) & (KA_KEYS - 1);
-          const bool vis = row >= r.ra && row < r.rb;
-          if (!vis) *u = make_uint4(0u, 0u, 0u, 0u);
+          if (row >= rb) *u = make_uint4(0u, 0u, 0u, 0u);
           else if (F16) {
             const uint4 x = *u;
             *u = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
@@ -324,176 +355,189 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         }
       }
     };
-    if (F16 && c_lo < c_hi && c_lo >= c_rows) load_entries(c_lo);
-    uint32_t ph = 0, rph = 0;
-    for (int64_t c = c_lo; c < c_hi; c++, ph ^= 1u) {
-      const bool rows = c < c_rows;
-      KaRows r{0, 0, 0};
-      if (rows) r = ka_rows(p, q, c, base);
-      const bool fetch = rows && r.rb > r.ra;
+    if (n_ch > 0) {
+      ok = ka_wait(&sm.q_full, 0, sm, p.hdr, 45) && ok;
+      if (F16) {                                      // Q rounded to f16 in place
+        uint4* qv = reinterpret_cast<uint4*>(qbuf);
+#pragma unroll 4
+        for (int i = ft; i < 8 * KA_COL / 16; i += KA_FILL) {
+          const uint4 x = qv[i];
+          qv[i] = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
+        }
+      }
+    }
+    uint32_t staged = 0;                              // chunks of entries so far
+    for (int c = 0; c < n_ch; c++) {
+      const KaChunk k = ka_chunk(q, c_lo + c);
+      const bool entries = c_lo + c >= q.cr;
+      if (F16 && entries) {                           // the staged bytes to registers
+        ok = ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46) && ok;
 #pragma unroll
-      for (int t = 0; t < 4; t++) {
-        if (c > c_lo) {
-          ok = ka_wait(&sm.pv_done[t], ph ^ 1u, sm, p.hdr, 43) && ok;
+        for (int i = 0; i < 4; i++) cd[i] = make_uint4(0u, 0u, 0u, 0u);
+        sc[0] = sc[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (key < k.b) {
+          const uint4* e = reinterpret_cast<const uint4*>(stage + key * MAIN_BYTES);
+#pragma unroll
+          for (int i = 0; i < 4; i++) cd[i] = e[4 * i + j];
+          sc[0] = e[16];
+          sc[1] = e[17];
+        }
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sm.stage_free);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        unsigned char* kt = smem + (2 * (c & 1) + h) * KA_HALF;
+        uint32_t o[2][16];
+        if (F16 && entries) {                         // before the wait: only the stores come after it
+          dequant(2 * h, o[0]);
+          dequant(2 * h + 1, o[1]);
+        }
+        if (c >= 2) {
+          ok = ka_wait(&sm.free_[c & 1][h], (c >> 1) - 1, sm, p.hdr, 47) && ok;
           tc::fence_after_sync();
         }
-        if (fetch && lead) {
-          // the buffer was read by the tensor cores (their completion was waited for)
-          // and written by ordinary stores before; the copy comes after both
-          tc::fence_proxy_async_smem();
-          const CUtensorMap* map = c < q.cw ? &map_rows : &map_sinks;
-          const int64_t y = (int64_t)b * (c < q.cw ? (int64_t)p.S : (int64_t)p.n_sink) + r.first;
-          tc::bar_arrive_expect_tx(&sm.row_full[t], p.rows_fp8 ? (uint32_t)KA_KCOL : 2u * KA_KCOL);
-          for (int cc = 2 * t; cc < 2 * t + 2; cc++)
-            tc::tma_load_2d(kbuf + cc * KA_KCOL + (p.rows_fp8 ? KA_KCOL / 2 : 0), map, cc * 64, (int32_t)y,
-                            &sm.row_full[t]);
-        }
-        if (F16 && c == c_lo) {                       // Q's tile rounded to f16 in place
-          ok = ka_wait(&sm.q_full[t], 0, sm, p.hdr, 44) && ok;
-          uint4* qv = reinterpret_cast<uint4*>(qbuf + 2 * t * KA_QCOL);
-#pragma unroll
-          for (int i = ft; i < 2 * KA_QCOL / 16; i += KA_FILL) {
-            const uint4 x = qv[i];
-            qv[i] = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
+        if (entries) {
+          if (F16) {
+            store(kt, 0, o[0]);
+            store(kt, 1, o[1]);
           }
-        }
-        if (!F16 && c == c_lo) ok = ka_wait(&sm.q_full[t], 0, sm, p.hdr, 44) && ok;
-        if (!rows) {
-          if (F16) dequant_tile(t);
-        } else if (fetch) {
-          ok = ka_wait(&sm.row_full[t], rph, sm, p.hdr, 45) && ok;
-          convert_rows(t, r);
-        } else {                                      // no row of the chunk was supplied
-          for (int i = ft; i < 2 * KA_KCOL / 16; i += KA_FILL)
-            reinterpret_cast<uint4*>(kbuf + 2 * t * KA_KCOL)[i] = make_uint4(0u, 0u, 0u, 0u);
+        } else {                                      // rows come first: use c / 2 of this buffer's copies too
+          ok = ka_wait(&sm.row_full[c & 1][h], c >> 1, sm, p.hdr, 48) && ok;
+          convert_rows(kt, k.b);
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sm.kready[t]);
+        if (lane == 0) tc::bar_arrive(&sm.full[c & 1][h]);
       }
-      if (fetch) rph ^= 1u;
-      if (F16 && c + 1 < c_hi && c + 1 >= c_rows) load_entries(c + 1);
     }
   } else {
-    // ================= softmax and output
-    const int q4 = warp & 3, hh = warp >> 2;          // TMEM lane quarter; head half (heads 32 hh ..)
-    const int m = q4 * 32 + lane;                     // key row of a chunk / dim row of a tile
-    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    // ================= softmax: lanes 0..15 hold heads 16 warp ..; output: all lanes
+    const uint32_t quarter = (uint32_t)(warp * 32) << 16;
     const float sc2 = p.scale * KA_LOG2E;
-    float m_used = -INFINITY;                         // reference of head 32 hh + lane
-    float l_part = 0.f;                               // sum of P over this warp's keys, head 32 hh + lane
+    const int head = 16 * warp + (lane & 15);
+    float m_used = -INFINITY, l_sum = 0.f;            // the head's reference and sum (lanes 0..15)
     bool ok = true;
-    uint32_t ph = 0;
-    for (int64_t c = c_lo; c < c_hi; c++, ph ^= 1u) {
-      bool valid;
-      if (c < q.cw + q.cs) {
-        const KaRows r = ka_rows(p, q, c, base);
-        valid = m >= r.ra && m < r.rb;
-      } else {
-        valid = KA_KEYS * (c - q.cw - q.cs) + m < q.en;
-      }
-      ok = ka_wait(&sm.s_full, ph, sm, p.hdr, 46) && ok;
+    for (int c = 0; c < n_ch; c++) {
+      const KaChunk k = ka_chunk(q, c_lo + c);
+      ok = ka_wait(&sm.s_full, c, sm, p.hdr, 49) && ok;
       tc::fence_after_sync();
-      float v[32], r[32];
+      uint32_t s[64];
       {
-        uint32_t s[32];
-        tmem_ld32(tmem + lane_off + KA_S_COL + 32 * hh, s);
-#pragma unroll
-        for (int j = 0; j < 32; j++) r[j] = v[j] = valid ? __uint_as_float(s[j]) * sc2 : -INFINITY;
+        const uint32_t s_addr = tmem + quarter + KA_S_COL + 64 * (c & 1);
+        tc::tmem_ld_x32_nowait(s_addr, s);
+        tc::tmem_ld_x32_nowait(s_addr + 32, s + 32);
+        tc::tmem_wait_ld_regs(s);
+        tc::tmem_wait_ld_regs(s + 32);
       }
-      sm.red[warp][lane] = lane_columns<true>(r, lane);
-      named_sync(2 + hh, 128);                        // the four warps of this head half
-      const float cm = fmaxf(fmaxf(sm.red[4 * hh][lane], sm.red[4 * hh + 1][lane]),
-                             fmaxf(sm.red[4 * hh + 2][lane], sm.red[4 * hh + 3][lane]));
+      const bool whole = k.b == KA_KEYS;
+      float c4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (whole) {
+#pragma unroll
+        for (int x = 0; x < 64; x++) c4[x & 3] = fmaxf(c4[x & 3], __uint_as_float(s[x]) * sc2);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 64; x++)
+          c4[x & 3] = fmaxf(c4[x & 3], (x < k.b) ? __uint_as_float(s[x]) * sc2 : -INFINITY);
+      }
+      const float cm = lane < 16 ? fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3])) : -INFINITY;
       float alpha = 1.f;
       if (m_used == -INFINITY) {
-        m_used = cm;                                  // O^T holds nothing yet, or only zeros
+        m_used = cm;                                  // O holds nothing yet, or only zeros
       } else if (cm > m_used + KA_TAU) {
         alpha = ex2_ftz(m_used - cm);
         m_used = cm;
-        l_part *= alpha;
+        l_sum *= alpha;
+      }
+      // O of the chunk before is done: P's buffer is free, and O may be rescaled
+      if (c > 0) {
+        for (int h = 0; h < 2; h++) ok = ka_wait(&sm.free_[(c - 1) & 1][h], (c - 1) >> 1, sm, p.hdr, 50) && ok;
+        tc::fence_after_sync();
       }
       if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {
-        // the same decision in the four warps of the half; the chunk before is in
-        // O^T entirely (this chunk's S^T needed its buffer)
-        float al[32];
-#pragma unroll
-        for (int j = 0; j < 32; j++) al[j] = __shfl_sync(0xFFFFFFFFu, alpha, j);
+        const float al = __shfl_sync(0xFFFFFFFFu, alpha, lane & 15);
 #pragma unroll 1
-        for (int u = 0; u < 4; u++) {
+        for (int g = 0; g < D / 2; g += 32) {
           uint32_t o[32];
-          const uint32_t taddr = tmem + lane_off + KA_O_COL + 64 * u + 32 * hh;
-          tmem_ld32(taddr, o);
+          tmem_ld32(tmem + quarter + KA_O_COL + g, o);
 #pragma unroll
-          for (int j = 0; j < 32; j++) o[j] = __float_as_uint(__uint_as_float(o[j]) * al[j]);
-          tmem_st32(taddr, o);
+          for (int x = 0; x < 32; x++) o[x] = __float_as_uint(__uint_as_float(o[x]) * al);
+          tmem_st32(tmem + quarter + KA_O_COL + g, o);
         }
         tc::tmem_wait_st();
       }
-      sm.mv[warp][lane] = m_used;
-      __syncwarp();
-      uint32_t pk[16];
+      const float ref = m_used == -INFINITY ? 0.f : m_used;
+      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+      auto weights = [&](auto masked) {
 #pragma unroll
-      for (int j4 = 0; j4 < 8; j4++) {
-        const float4 m4 = *reinterpret_cast<const float4*>(&sm.mv[warp][4 * j4]);
-        const float mj[4] = {m4.x, m4.y, m4.z, m4.w};
+        for (int u = 0; u < 8; u++) {                 // 8 keys, 16 bytes of P
+          uint32_t pk[4];
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const int j = 4 * j4 + e;
-          r[j] = (v[j] == -INFINITY) ? 0.f : ex2_ftz(v[j] - mj[e]);
-          if (j & 1) pk[j >> 1] = F16 ? pack_f16x2(r[j - 1], r[j]) : pack_bf16x2(r[j - 1], r[j]);
+          for (int y = 0; y < 4; y++) {
+            const int x = 8 * u + 2 * y;
+            float e0 = ex2_ftz(fmaf(__uint_as_float(s[x]), sc2, -ref));
+            float e1 = ex2_ftz(fmaf(__uint_as_float(s[x + 1]), sc2, -ref));
+            if (decltype(masked)::value) {
+              e0 = (x < k.b) ? e0 : 0.f;
+              e1 = (x + 1 < k.b) ? e1 : 0.f;
+            }
+            l4[y] += e0 + e1;
+            pk[y] = F16 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+          }
+          if (lane < 16)
+            *reinterpret_cast<uint4*>(pbuf + sw128((uint32_t)head, (uint32_t)(16 * u))) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; u++)
-        *reinterpret_cast<uint4*>(pbuf + sw128((uint32_t)m, (uint32_t)(hh * 64 + u * 16))) =
-            make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+      };
+      if (whole) weights(std::false_type{});
+      else weights(std::true_type{});
+      l_sum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::bar_arrive(&sm.p_ready);
-      l_part += lane_columns<false>(r, lane);         // beside the product, not before it
     }
 
-    // ---------------- output
-    if (c_lo < c_hi) {
-      for (int t = 0; t < 4; t++) ok = ka_wait(&sm.pv_done[t], ph ^ 1u, sm, p.hdr, 47) && ok;
+    // ---------------- output: lane = (head, half of the dims)
+    if (n_ch > 0) {
+      for (int h = 0; h < 2; h++) ok = ka_wait(&sm.free_[(n_ch - 1) & 1][h], (n_ch - 1) >> 1, sm, p.hdr, 51) && ok;
       tc::fence_after_sync();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    sm.red[warp][lane] = l_part;
-    named_sync(2 + hh, 128);
-    const float l = sm.red[4 * hh][lane] + sm.red[4 * hh + 1][lane] + sm.red[4 * hh + 2][lane] + sm.red[4 * hh + 3][lane];
+    const float m = __shfl_sync(0xFFFFFFFFu, m_used, lane & 15), l = __shfl_sync(0xFFFFFFFFu, l_sum, lane & 15);
+    const int d0 = (D / 2) * (lane >> 4);
     if (!SPLIT) {
-      if (p.lse && q4 == 0)
-        p.lse[bq * H + 32 * hh + lane] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * KA_LN2;
-      const float inv = l == 0.f ? 0.f : 1.0f / l;    // no visible key: zeros
-      uint16_t* out = p.out + bq * H * D + (int64_t)(32 * hh) * D + m;
+      if (p.lse && lane < 16) p.lse[bq * H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * KA_LN2;
+      const float inv = 1.0f / l;
+      uint4* out = reinterpret_cast<uint4*>(p.out + (bq * H + head) * D + d0);
 #pragma unroll 1
-      for (int u = 0; u < 4; u++) {
+      for (int g = 0; g < D / 2; g += 32) {
         uint32_t o[32];
-        if (c_lo < c_hi) tmem_ld32(tmem + lane_off + KA_O_COL + 64 * u + 32 * hh, o);
+        if (n_ch > 0) tmem_ld32(tmem + quarter + KA_O_COL + g, o);
 #pragma unroll
-        for (int j = 0; j < 32; j++) {
-          const float i = __shfl_sync(0xFFFFFFFFu, inv, j);
-          const float x = c_lo < c_hi ? __uint_as_float(o[j]) * i : 0.f;
-          out[j * D + 128 * u] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xFFFFu);
+        for (int x = 0; x < 4; x++) {
+          float f[8];
+#pragma unroll
+          for (int y = 0; y < 8; y++) f[y] = l == 0.f ? 0.f : __uint_as_float(o[8 * x + y]) * inv;   // no key: zeros
+          out[g / 8 + x] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                      pack_bf16x2(f[6], f[7]));
         }
       }
     } else {
       float* part = p.part + (int64_t)blockIdx.x * KA_PART_FLOATS;
-      if (q4 == 0) {
-        part[32 * hh + lane] = m_used;
-        part[H + 32 * hh + lane] = l;
+      if (lane < 16) {
+        part[head] = m;
+        part[H + head] = l;
       }
-      float* op = part + 2 * H + (int64_t)(32 * hh) * D + m;
-      if (c_lo < c_hi) {
+      float4* out = reinterpret_cast<float4*>(part + 2 * H + head * D + d0);
+      if (n_ch > 0) {
 #pragma unroll 1
-        for (int u = 0; u < 4; u++) {
+        for (int g = 0; g < D / 2; g += 32) {
           uint32_t o[32];
-          tmem_ld32(tmem + lane_off + KA_O_COL + 64 * u + 32 * hh, o);
+          tmem_ld32(tmem + quarter + KA_O_COL + g, o);
 #pragma unroll
-          for (int j = 0; j < 32; j++) op[j * D + 128 * u] = __uint_as_float(o[j]);
+          for (int x = 0; x < 8; x++)
+            out[g / 4 + x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                         __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
         }
       }
     }
@@ -565,7 +609,7 @@ __global__ void __launch_bounds__(256) keys_combine_kernel(const float* __restri
 // call KA_JOIN more; CTAs run one to an SM.  The GPU's 152 SMs are a constant
 // here so that the workspace can be sized without a device.
 constexpr int KA_SMS = 152;
-constexpr int KA_FIXED = 3, KA_JOIN = 3;
+constexpr int KA_FIXED = 5, KA_JOIN = 4;
 
 int keys_split(int64_t BQ, int64_t chunks) {
   if (BQ <= 0 || BQ >= 4 * KA_SMS) return 1;

@@ -153,8 +153,9 @@ size_t attn_partials_bytes(int64_t BQ, int K);
 int attn_split_max_queries();
 cudaError_t launch_block_summary(const HsParams& p, cudaStream_t stream);
 cudaError_t launch_hisa_view(const HvParams& p, cudaStream_t stream);
-// `chunks`: runs of 128 keys of the longest query (for the split over CTAs);
+// `chunks`: runs of KEYS_CHUNK keys of the longest query (for the split over CTAs);
 // `part`: keys_part_bytes(B * Q, chunks) of scratch
+constexpr int KEYS_CHUNK = 64;
 cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* part, cudaStream_t stream);
 size_t keys_part_bytes(int64_t BQ, int64_t chunks);
 cudaError_t launch_qk_norm_rope(const QkParams& p, cudaStream_t stream);

@@ -102,6 +102,16 @@ def test_window_any_positions(fp8, W, n_sink):
     verify_window(2, 4, 10, W, n_sink, fp8, pos, np.zeros(4, np.int64), 512)
 
 
+@pytest.mark.parametrize("W,n_sink", [(1, 3), (50, 0), (128, 5)])
+def test_window_neighbours_apart(W, n_sink):
+    """Neighbouring queries whose windows touch, leave a small gap or lie in reverse order."""
+    rows = []
+    for t in (260, 130, 131):
+        for d in (1, W - 1, W, W + 1, W + 7, W + 40, -1, -W + 1, -W, -W - 1, -W - 9):
+            rows.append([t, max(0, t + d)])
+    verify_window(14, len(rows), 2, W, n_sink, False, np.array(rows), np.zeros(len(rows), np.int64), 440)
+
+
 def test_window_causal_neighbour_not_finite():
     """A row that the next query sees and this one does not may be infinite or NaN:
     this query's output stays finite, the next one's does not."""
@@ -169,7 +179,7 @@ def run_dense(cache, q, rows, base, pos, max_n, scale=SCALE, status=0, stream=No
 def make_cache(kv, ns, m):
     B, cap = kv.shape[:2]
     cache = csa2.Cache(B, cap, m)
-    cache.main_kv.copy_(up(kv))
+    cache.main_kv[:, :cap].copy_(up(kv))
     cache.n_entries.copy_(torch.tensor(ns, dtype=torch.int32))
     return cache
 
@@ -197,6 +207,26 @@ def test_dense(fp8, B, Q, m, ns, last):
         for i in range(Q):
             keys = ref.dense_keys(entries, ns[b], m, rv, int(base[b]), int(pos[b, i]))
             check(o[b, i], l[b, i], ref.bf16(q[b, i]), keys, SCALE, ref.U_F16, (b, i))
+
+
+def test_dense_newest_entry_not_finite():
+    """An entry whose stored scale is NaN, seen by the newer queries only (m = 2: by every second pair)."""
+    g = synth.rng(15)
+    for m, n in ((1, 300), (2, 200), (1, 5000)):
+        kv, rows, q = draw_entries(g, 1, n), draw_rows(g, False, 1, 140), synth.main_queries(g, 1, 6)
+        pos = n * m - 6 + np.arange(6)[None, :]
+        bad = n - 3
+        kv[0, bad, 270] = 0x7F
+        base = np.array([pos[0, 0] - 127])
+        o, l = run_dense(make_cache(kv, [n], m), q, rows, base, pos, n)
+        entries, rv = oracle.dequant_main(kv[0]), ref.row_values(rows[0])
+        for i in range(6):
+            t = int(pos[0, i])
+            if bad < min(n, (t + 1) // m):
+                assert np.all(np.isnan(o[0, i])) and np.all(np.isnan(l[0, i]))
+            else:
+                check(o[0, i], l[0, i], ref.bf16(q[0, i]), ref.dense_keys(entries, n, m, rv, int(base[0]), t), SCALE,
+                      ref.U_F16, (m, i))
 
 
 def test_dense_one_cta_a_query_equals_the_split():
