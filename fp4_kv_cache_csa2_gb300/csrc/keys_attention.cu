@@ -16,27 +16,30 @@
 //     to shared memory as the 16-bit A operand of the next product.  The reference m
 //     of a head moves only when a chunk exceeds it by more than e^8 (then the head's O
 //     and its sum are rescaled), so P stays inside f16
-//   * O += P V    N = 2 x 256 dims, K = keys: V is the K tile read MN-major
+//   * O += P V    N = 4 x 128 dims, K = keys: V is the K tile read MN-major
 // An M = 64 accumulator takes 16 lanes of each of TMEM's four lane quarters: the
 // dims 0..255 of O lie in lanes 0..15 of a quarter, the dims 256..511 in lanes
 // 16..31 of the same 256 columns, and S is double-buffered beside them.
-// Operands: F16 (calls with cache entries) keeps every dequantised FP4 value
-// exactly (at most 6 significant bits, 2^-10 .. 2688) and rounds q and bf16
-// window rows to f16, exact inside [2^-14, 65504], with P to 11 bits.  Without
-// cache entries the operands are bf16: q and bf16 rows as they are, E4M3 rows
-// exactly, P to 8 bits (its rounding errors are independent and average out;
-// the sum of the softmax is taken before that rounding, in binary32).
+// Operands: F16 (calls with cache entries or E4M3 rows) keeps every dequantised FP4
+// value (at most 6 significant bits, 2^-10 .. 2688) and every E4M3 value exactly and
+// rounds q and bf16 window rows to f16, exact inside [2^-14, 65504], with P to 11
+// bits.  With bf16 rows alone the operands are bf16: q and rows as they are, P to 8
+// bits (its rounding errors are independent and average out; the sum of the softmax
+// is taken before that rounding, in binary32).
 //
-// Shared memory: Q 64 KB, two K buffers of [64 keys][512 dims] (two halves of 32 KB,
-// four SW128 column chunks each), P 8 KB, and the next chunk's entries as stored,
-// 18 KB.  Roles: warps 0..3 softmax and output; warps 4..11 fill the K buffers
-// (entries: from the staged bytes to registers, then a half at a time; rows: widened
-// or rounded in place); warp 12 issues the MMAs, S of chunk c + 1 before O of chunk c,
-// so that the softmax of a chunk runs beside the products of its neighbours;
-// warp 13 issues the copies: entries to the staging area, rows to their K buffer.
-// A half of a K buffer is refilled as soon as its part of O is done.  All waits are
-// bounded; a timeout reports CSA2_ERR_TIMEOUT and every thread still takes every
-// barrier.
+// Shared memory: Q 64 KB, two K buffers of [64 keys][512 dims] (four quarters of 16 KB,
+// two SW128 column chunks each), two P of 8 KB, and a staging area of 18 KB for the
+// next chunk's entries, or half a chunk's E4M3 rows, as stored.  Roles: warps 0..3
+// softmax and output; warps 4..11 fill the K buffers (staged bytes are converted in
+// registers before the wait for the buffer, so that only stores come after it; bf16
+// rows are rounded in place if need be); warp 12 issues the MMAs, S of chunk c + 1
+// before O of chunk c, so that the softmax of a chunk runs beside the products of its
+// neighbours; warp 13 issues the copies.
+// A quarter of a K buffer is refilled as soon as its part of O is done, and its part of
+// S follows as soon as it is filled: the chain product, refill, product of one chunk
+// sets the pace, and its links are as short as the hand-offs (100 to 200 cycles each)
+// allow.  All waits are bounded; a timeout reports CSA2_ERR_TIMEOUT and every thread
+// still takes every barrier.
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -52,10 +55,10 @@ constexpr int KA_COPY_WARP = KA_MMA_WARP + 1;
 constexpr int KA_THREADS = 32 * (KA_COPY_WARP + 1);
 constexpr int KA_KEYS = KEYS_CHUNK;                       // keys per chunk
 constexpr int KA_COL = 64 * 128;                          // [64 rows][64 dims] 16-bit, SW128
-constexpr int KA_HALF = 4 * KA_COL;                       // half of a K buffer: 256 dims
-constexpr int KA_OFF_Q = 4 * KA_HALF;
+constexpr int KA_QUART = 2 * KA_COL;                      // a quarter of a K buffer: 128 dims
+constexpr int KA_OFF_Q = 8 * KA_QUART;
 constexpr int KA_OFF_P = KA_OFF_Q + 8 * KA_COL;
-constexpr int KA_OFF_STAGE = KA_OFF_P + KA_COL;
+constexpr int KA_OFF_STAGE = KA_OFF_P + 2 * KA_COL;       // P of chunk c at c % 2
 constexpr int KA_OFF_SMALL = KA_OFF_STAGE + KA_KEYS * MAIN_BYTES;
 constexpr int KA_TMEM_COLS = 512;
 constexpr int KA_O_COL = 0;                               // dims 256 h ..: lanes 16 h .. of each quarter
@@ -67,22 +70,25 @@ constexpr int KA_PART_FLOATS = 2 * H + H * D;             // one partial state: 
 
 struct KaSmall {
   uint64_t q_full;                    // TMA: Q
-  uint64_t stage_full, stage_free;    // the staged entries have come / were read (a fill warp each)
-  uint64_t row_full[2][2];            // TMA: rows in half h of K buffer i
-  uint64_t full[2][2];                // half h of K buffer i is filled (a fill warp each)
-  uint64_t free_[2][2];               // ... its part of O is done
+  uint64_t stage_full, stage_free;    // the staged bytes have come / were read (a fill warp each)
+  uint64_t row_full[2][4];            // TMA: bf16 rows in quarter u of K buffer i
+  uint64_t full[2][4];                // quarter u of K buffer i is filled (a fill warp each)
+  uint64_t free_[2][4];               // ... its part of O, and all before it, is done
   uint64_t s_full;                    // S of a chunk is done
   uint64_t p_ready;                   // P is written, O rescaled if needed (a softmax warp each)
   uint32_t tmem_base;
   int err;
 };
-constexpr int KA_SMEM = KA_OFF_SMALL + (int)sizeof(KaSmall) + 1024;
+constexpr int KA_SMEM = KA_OFF_SMALL + (int)sizeof(KaSmall);
 static_assert(KA_SMEM <= 227 * 1024, "shared memory per CTA");
 
-__device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t count, KaSmall& sm, WsHeader* hdr, int where) {
-  if (tc::bar_wait(bar, count & 1u)) return true;
-  if (atomicExch(&sm.err, 1) == 0) report(hdr, CSA2_ERR_TIMEOUT, where);
+__device__ __noinline__ bool ka_timeout(int* err, WsHeader* hdr, int where) {
+  if (atomicExch(err, 1) == 0) report(hdr, CSA2_ERR_TIMEOUT, where);
   return false;
+}
+
+__device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t count, KaSmall& sm, WsHeader* hdr, int where) {
+  return tc::bar_wait(bar, count & 1u) || ka_timeout(&sm.err, hdr, where);
 }
 
 // One query's keys and how they lie in chunks.
@@ -144,23 +150,19 @@ __device__ __forceinline__ KaChunk ka_chunk(const KaQuery& q, int64_t c) {
   return k;
 }
 
-// f16x2 -> bf16x2, for values that bf16 holds exactly
-__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return pack_bf16x2(f.x, f.y);
-}
-
 template <bool F16, bool SPLIT>
 __global__ void __launch_bounds__(KA_THREADS, 1)
 keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_rows,
                  const __grid_constant__ CUtensorMap map_sinks) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = tc::align_smem_1k(smem_raw);
+  extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* qbuf = smem + KA_OFF_Q;
-  unsigned char* pbuf = smem + KA_OFF_P;
   unsigned char* stage = smem + KA_OFF_STAGE;
   KaSmall& sm = *reinterpret_cast<KaSmall*>(smem + KA_OFF_SMALL);
 
+  if (tc::smem_u32(smem) & 1023u) {                   // the swizzled tiles need the declared alignment
+    if (threadIdx.x == 0) report(p.hdr, CSA2_ERR_CUDA, 1);
+    return;
+  }
   const int split = SPLIT ? p.split : 1;
   const int64_t bq = blockIdx.x / split;
   const int sp = blockIdx.x % split;
@@ -174,10 +176,10 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     tc::bar_init(&sm.stage_full, 1);
     tc::bar_init(&sm.stage_free, KA_FILL_WARPS);
     for (int i = 0; i < 2; i++)
-      for (int h = 0; h < 2; h++) {
-        tc::bar_init(&sm.row_full[i][h], 1);
-        tc::bar_init(&sm.full[i][h], KA_FILL_WARPS);
-        tc::bar_init(&sm.free_[i][h], 1);
+      for (int u = 0; u < 4; u++) {
+        tc::bar_init(&sm.row_full[i][u], 1);
+        tc::bar_init(&sm.full[i][u], KA_FILL_WARPS);
+        tc::bar_init(&sm.free_[i][u], 1);
       }
     tc::bar_init(&sm.s_full, 1);
     tc::bar_init(&sm.p_ready, KA_SOFT_WARPS);
@@ -207,29 +209,30 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   if (warp == KA_MMA_WARP) {
     // ================= MMAs (the whole warp runs the loop, one elected lane issues)
     constexpr uint32_t idesc_s = F16 ? tc::idesc_f16(H, 0, 0, 0) : tc::idesc_bf16(H, 0, 0, 0);       // + N
-    constexpr uint32_t idesc_o = F16 ? tc::idesc_f16(H, 256, 0, 1) : tc::idesc_bf16(H, 256, 0, 1);
+    constexpr uint32_t idesc_o = F16 ? tc::idesc_f16(H, 128, 0, 1) : tc::idesc_bf16(H, 128, 0, 1);
     const uint64_t q_d = tc::smem_desc(tc::smem_u32(qbuf), 16, 1024, tc::SW_128B);
-    const uint64_t p_d = tc::smem_desc(tc::smem_u32(pbuf), 16, 1024, tc::SW_128B);
+    const uint64_t p_d = tc::smem_desc(tc::smem_u32(smem + KA_OFF_P), 16, 1024, tc::SW_128B);
     const uint64_t k_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
     const uint64_t v_d = tc::smem_desc(tc::smem_u32(smem), KA_COL, 1024, tc::SW_128B);
+    const uint32_t leader = tc::elect_one();
     bool ok = true;
     auto scores = [&](int c) {
       const uint32_t idesc = idesc_s | (uint32_t)(ka_chunk(q, c_lo + c).n >> 3) << 17;
       const uint32_t s = tmem + KA_S_COL + 64 * (c & 1);
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        ok = ka_wait(&sm.full[c & 1][h], c >> 1, sm, p.hdr, 41) && ok;
+#pragma unroll 1
+      for (int u = 0; u < 4; u++) {
+        ok = ka_wait(&sm.full[c & 1][u], c >> 1, sm, p.hdr, 41) && ok;
         tc::fence_after_sync();
         if (ok) {
-          const uint64_t qa = q_d + (uint32_t)(h * (KA_HALF >> 4)), ka = k_d + (uint32_t)((2 * (c & 1) + h) * (KA_HALF >> 4));
+          const uint64_t qa = q_d + (uint32_t)(u * (KA_QUART >> 4)), ka = k_d + (uint32_t)((4 * (c & 1) + u) * (KA_QUART >> 4));
 #pragma unroll
-          for (int i = 0; i < 16; i++) {
+          for (int i = 0; i < 8; i++) {
             const uint32_t off = (uint32_t)((i >> 2) * KA_COL + (i & 3) * 32) >> 4;
-            tc::mma_f16_warp(s, qa + off, ka + off, idesc, (h || i) ? 1u : 0u);
+            tc::mma_f16_warp(leader, s, qa + off, ka + off, idesc, (u || i) ? 1u : 0u);
           }
         }
       }
-      tc::commit_warp(&sm.s_full);
+      tc::commit_warp(leader, &sm.s_full);
     };
     if (n_ch > 0) scores(0);
     for (int c = 0; c < n_ch; c++) {
@@ -237,17 +240,18 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       const int steps = ka_chunk(q, c_lo + c).n / 16;
       ok = ka_wait(&sm.p_ready, c, sm, p.hdr, 42) && ok;
       tc::fence_after_sync();
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
+#pragma unroll 1
+      for (int u = 0; u < 4; u++) {
         if (ok) {
-          const uint64_t va = v_d + (uint32_t)((2 * (c & 1) + h) * (KA_HALF >> 4));
+          const uint64_t va = v_d + (uint32_t)((4 * (c & 1) + u) * (KA_QUART >> 4));
+          const uint32_t o = tmem + KA_O_COL + 128 * (u & 1) + ((uint32_t)(16 * (u >> 1)) << 16);
 #pragma unroll
           for (int ks = 0; ks < KA_KEYS / 16; ks++)
             if (ks < steps)
-              tc::mma_f16_warp(tmem + KA_O_COL + ((uint32_t)(16 * h) << 16), p_d + (uint32_t)(2 * ks),
-                               va + (uint32_t)(ks * (2048 >> 4)), idesc_o, (c || ks) ? 1u : 0u);
+              tc::mma_f16_warp(leader, o, p_d + (uint32_t)((c & 1) * (KA_COL >> 4) + 2 * ks), va + (uint32_t)(ks * (2048 >> 4)),
+                               idesc_o, (c || ks) ? 1u : 0u);
         }
-        tc::commit_warp(&sm.free_[c & 1][h]);
+        tc::commit_warp(leader, &sm.free_[c & 1][u]);
       }
     }
   } else if (warp == KA_COPY_WARP) {
@@ -256,31 +260,36 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       bool ok = true;
       tc::bar_arrive_expect_tx(&sm.q_full, 8u * KA_COL);
       for (int i = 0; i < 8; i++) tc::tma_load_2d(qbuf + i * KA_COL, &map_q, i * 64, (int32_t)(bq * H), &sm.q_full);
-      uint32_t staged = 0;
+      uint32_t staged = 0;                            // uses of the staging area
+      auto next_stage = [&](uint32_t bytes) {
+        if (staged > 0) ok = ka_wait(&sm.stage_free, staged - 1, sm, p.hdr, 43) && ok;
+        staged++;
+        tc::bar_arrive_expect_tx(&sm.stage_full, bytes);
+      };
       for (int c = 0; c < n_ch; c++) {
         const KaChunk k = ka_chunk(q, c_lo + c);
         if (c_lo + c >= q.cr) {                       // entries [first, first + b), contiguous
-          if (staged > 0) ok = ka_wait(&sm.stage_free, staged - 1, sm, p.hdr, 43) && ok;
-          staged++;
-          tc::bar_arrive_expect_tx(&sm.stage_full, (uint32_t)(k.b * MAIN_BYTES));
-          tc::bulk_load(stage, p.main_kv + ((int64_t)b * p.cap + k.first) * MAIN_BYTES, (uint32_t)(k.b * MAIN_BYTES),
-                        &sm.stage_full);
-        } else {
-          const bool window = c_lo + c < q.cw;
-          const CUtensorMap* map = window ? &map_rows : &map_sinks;
-          const int32_t y = (int32_t)((int64_t)b * (window ? p.S : (int64_t)p.n_sink) + k.first);
+          const uint32_t bytes = (uint32_t)(k.b * MAIN_BYTES);
+          next_stage(bytes);
+          tc::bulk_load(stage, p.main_kv + ((int64_t)b * p.cap + k.first) * MAIN_BYTES, bytes, &sm.stage_full);
+          continue;
+        }
+        const bool window = c_lo + c < q.cw;
+        const CUtensorMap* map = window ? &map_rows : &map_sinks;
+        const int32_t y = (int32_t)((int64_t)b * (window ? p.S : (int64_t)p.n_sink) + k.first);
+        if (p.rows_fp8) {
           for (int h = 0; h < 2; h++) {
-            if (c >= 2) {
-              // the tensor cores have read the half (waited for here), after the fill warps wrote
-              // it and made that visible to the asynchronous proxy
-              ok = ka_wait(&sm.free_[c & 1][h], (c >> 1) - 1, sm, p.hdr, 44) && ok;
-            }
-            unsigned char* kt = smem + (2 * (c & 1) + h) * KA_HALF;
-            tc::bar_arrive_expect_tx(&sm.row_full[c & 1][h], p.rows_fp8 ? KA_HALF / 2u : (uint32_t)KA_HALF);
-            for (int i = 0; i < 4; i++)
-              tc::tma_load_2d(kt + i * KA_COL + (p.rows_fp8 ? KA_COL / 2 : 0), map, (4 * h + i) * 64, y,
-                              &sm.row_full[c & 1][h]);
+            next_stage(KA_QUART);
+            for (int i = 0; i < 4; i++) tc::tma_load_2d(stage + i * (KA_COL / 2), map, (4 * h + i) * 64, y, &sm.stage_full);
           }
+          continue;
+        }
+        for (int u = 0; u < 4; u++) {
+          // the quarter was read by the tensor cores, whose completion is waited for here
+          if (c >= 2) ok = ka_wait(&sm.free_[c & 1][u], (c >> 1) - 1, sm, p.hdr, 44) && ok;
+          unsigned char* kt = smem + (4 * (c & 1) + u) * KA_QUART;
+          tc::bar_arrive_expect_tx(&sm.row_full[c & 1][u], KA_QUART);
+          for (int i = 0; i < 2; i++) tc::tma_load_2d(kt + i * KA_COL, map, (2 * u + i) * 64, y, &sm.row_full[c & 1][u]);
         }
       }
     }
@@ -294,11 +303,8 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     // lie in eight different bank groups
     const int k8 = (ft >> 2) & 7, j = ft & 3;
     const int key = ((ft >> 2) & ~7) + ((k8 & 4) | (k8 & 1) << 1 | (k8 >> 1 & 1));
-    uint4 cd[4] = {}, sc[2] = {};                               // codes of the four quarters, scales of the two halves
-    auto dequant = [&](int i, uint32_t* o) {          // quarter i: 32 dims
-      const uint4 c = cd[i], s = sc[i >> 1];
-      const uint32_t w = (i & 1) ? (j & 2 ? s.w : s.z) : (j & 2 ? s.y : s.x);   // scale bytes 2j, 2j + 1 of the quarter
-      const uint32_t w2 = w >> (16 * (j & 1));
+    // 16 bytes of codes (32 dims) times their two scales, the bytes of `w2`
+    auto dequant = [&](const uint4& c, uint32_t w2, uint32_t* o) {
       const uint32_t sa = e4m3x2_to_f16x2(prmt(w2, 0u, 0x0000u)), sb = e4m3x2_to_f16x2(prmt(w2, 0u, 0x1111u));
       const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
@@ -308,10 +314,11 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         for (int x = 0; x < 4; x++) o[4 * g + x] = hmul2(o[4 * g + x], g < 2 ? sa : sb);
       }
     };
-    auto store = [&](unsigned char* kt, int i, const uint32_t* o) {
-      // column chunk 2 (i % 2) + j / 2, units 4 (j % 2) ..; lanes with j >= 2 walk them as g ^ 1,
-      // so that the eight lanes of a phase store to eight different bank groups
-      unsigned char* dst = kt + (2 * (i & 1) + (j >> 1)) * KA_COL + key * 128;
+    // 32 dims of key `key` into a quarter
+    auto store = [&](unsigned char* kt, const uint32_t* o) {
+      // column chunk j / 2, units 4 (j % 2) ..; lanes with j >= 2 walk them as g ^ 1, so that the
+      // eight lanes of a phase store to eight different bank groups
+      unsigned char* dst = kt + (j >> 1) * KA_COL + key * 128;
       const bool odd = (j & 2) != 0;
 #pragma unroll
       for (int g = 0; g < 4; g++) {
@@ -321,37 +328,36 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         *reinterpret_cast<uint4*>(dst + ((unit ^ (uint32_t)(key & 7)) << 4)) = v;
       }
     };
-    // a half of rows that the copy has brought: E4M3 widened, bf16 rounded to f16 when
-    // the operands are f16, rows behind the chunk's last set to zero (what is not seen
-    // may hold anything, infinities among it)
-    auto convert_rows = [&](unsigned char* kt, int rb) {
-      if (p.rows_fp8) {
-        const int row = ft >> 2;
-        unsigned char* col = kt + (ft & 3) * KA_COL;
-        uint4 raw[4];
+    // 32 E4M3 dims of row `key` from quarter u % 2 of the staged half; rows behind the chunk's
+    // last: zeros.  Lanes with j >= 2 take their two pieces in the other order (bank groups)
+    auto widen = [&](int u, uint32_t* o, int n) {
+      const uint4* src = reinterpret_cast<const uint4*>(stage + (2 * (u & 1) + (j >> 1)) * (KA_COL / 2) + key * 64 + 32 * (j & 1));
+      const bool odd = (j & 2) != 0;
+      uint4 a = make_uint4(0u, 0u, 0u, 0u), e = a;
+      if (key < n) {
+        a = src[odd ? 1 : 0];
+        e = src[odd ? 0 : 1];
+      }
+      const uint32_t v[8] = {odd ? e.x : a.x, odd ? e.y : a.y, odd ? e.z : a.z, odd ? e.w : a.w,
+                             odd ? a.x : e.x, odd ? a.y : e.y, odd ? a.z : e.z, odd ? a.w : e.w};
 #pragma unroll
-        for (int i = 0; i < 4; i++) raw[i] = reinterpret_cast<const uint4*>(col + KA_COL / 2 + row * 64)[i];
-        named_sync(1, KA_FILL);
-        const bool vis = row < rb;
-#pragma unroll
-        for (int x = 0; x < 8; x++) {
-          const uint4& w = raw[x >> 1];
-          const uint32_t lo = (x & 1) ? w.z : w.x, hi = (x & 1) ? w.w : w.y;
-          uint32_t o[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(hi >> 16)};
-#pragma unroll
-          for (int y = 0; y < 4; y++) o[y] = !vis ? 0u : (F16 ? o[y] : f16x2_to_bf16x2(o[y]));
-          *reinterpret_cast<uint4*>(col + sw128((uint32_t)row, (uint32_t)(16 * x))) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      } else if (F16 || rb < KA_KEYS) {
+      for (int x = 0; x < 8; x++) {
+        o[2 * x] = e4m3x2_to_f16x2(v[x]);
+        o[2 * x + 1] = e4m3x2_to_f16x2(v[x] >> 16);
+      }
+    };
+    // a quarter of bf16 rows, where the copy has put it: rounded to f16 when the operands
+    // are f16, rows behind the chunk's last set to zero (what is not seen may hold anything,
+    // infinities among it)
+    auto convert_rows = [&](unsigned char* kt, int n) {
+      if (!F16 && n == KA_KEYS) return;
 #pragma unroll 4
-        for (int i = ft; i < KA_HALF / 16; i += KA_FILL) {
-          uint4* u = reinterpret_cast<uint4*>(kt) + i;
-          const int row = (i >> 3) & (KA_KEYS - 1);
-          if (row >= rb) *u = make_uint4(0u, 0u, 0u, 0u);
-          else if (F16) {
-            const uint4 x = *u;
-            *u = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
-          }
+      for (int i = ft; i < KA_QUART / 16; i += KA_FILL) {
+        uint4* u = reinterpret_cast<uint4*>(kt) + i;
+        if (((i >> 3) & (KA_KEYS - 1)) >= n) *u = make_uint4(0u, 0u, 0u, 0u);
+        else if (F16) {
+          const uint4 x = *u;
+          *u = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
         }
       }
     };
@@ -366,15 +372,28 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         }
       }
     }
-    uint32_t staged = 0;                              // chunks of entries so far
+    uint32_t staged = 0;                              // uses of the staging area
+    auto wait_stage = [&]() { ok = ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46) && ok; };
+    auto stage_read = [&]() {
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sm.stage_free);
+    };
+    auto wait_free = [&](int c, int u) {
+      if (c < 2) return;
+      ok = ka_wait(&sm.free_[c & 1][u], (c >> 1) - 1, sm, p.hdr, 47) && ok;
+      tc::fence_after_sync();
+    };
+    auto filled = [&](int c, int u) {
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sm.full[c & 1][u]);
+    };
     for (int c = 0; c < n_ch; c++) {
       const KaChunk k = ka_chunk(q, c_lo + c);
-      const bool entries = c_lo + c >= q.cr;
-      if (F16 && entries) {                           // the staged bytes to registers
-        ok = ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46) && ok;
-#pragma unroll
-        for (int i = 0; i < 4; i++) cd[i] = make_uint4(0u, 0u, 0u, 0u);
-        sc[0] = sc[1] = make_uint4(0u, 0u, 0u, 0u);
+      unsigned char* kt = smem + 4 * (c & 1) * KA_QUART;
+      if (F16 && c_lo + c >= q.cr) {                  // entries
+        wait_stage();
+        uint4 cd[4] = {}, sc[2] = {};                 // codes of the four quarters, scales of the two halves
         if (key < k.b) {
           const uint4* e = reinterpret_cast<const uint4*>(stage + key * MAIN_BYTES);
 #pragma unroll
@@ -382,33 +401,42 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           sc[0] = e[16];
           sc[1] = e[17];
         }
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sm.stage_free);
-      }
+        stage_read();
+        uint32_t o[4][16];
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        unsigned char* kt = smem + (2 * (c & 1) + h) * KA_HALF;
-        uint32_t o[2][16];
-        if (F16 && entries) {                         // before the wait: only the stores come after it
-          dequant(2 * h, o[0]);
-          dequant(2 * h + 1, o[1]);
+        for (int i = 0; i < 4; i++) {
+          const uint4 s4 = sc[i >> 1];                // scale bytes 2j, 2j + 1 of the quarter
+          const uint32_t w = (i & 1) ? (j & 2 ? s4.w : s4.z) : (j & 2 ? s4.y : s4.x);
+          dequant(cd[i], w >> (16 * (j & 1)), o[i]);
+#pragma unroll
+          for (int x = 0; x < 16; x++) asm volatile("" : "+r"(o[i][x]));   // here, not after the wait below
         }
-        if (c >= 2) {
-          ok = ka_wait(&sm.free_[c & 1][h], (c >> 1) - 1, sm, p.hdr, 47) && ok;
-          tc::fence_after_sync();
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          wait_free(c, u);
+          store(kt + u * KA_QUART, o[u]);
+          filled(c, u);
         }
-        if (entries) {
-          if (F16) {
-            store(kt, 0, o[0]);
-            store(kt, 1, o[1]);
+      } else if (F16 && p.rows_fp8) {
+        for (int h = 0; h < 2; h++) {
+          uint32_t o[2][16];
+          wait_stage();
+          widen(0, o[0], k.b);
+          widen(1, o[1], k.b);
+          stage_read();
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+            wait_free(c, 2 * h + i);
+            store(kt + (2 * h + i) * KA_QUART, o[i]);
+            filled(c, 2 * h + i);
           }
-        } else {                                      // rows come first: use c / 2 of this buffer's copies too
-          ok = ka_wait(&sm.row_full[c & 1][h], c >> 1, sm, p.hdr, 48) && ok;
-          convert_rows(kt, k.b);
         }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sm.full[c & 1][h]);
+      } else {
+        for (int u = 0; u < 4; u++) {                 // rows come first: use c / 2 of the buffer's copies too
+          ok = ka_wait(&sm.row_full[c & 1][u], c >> 1, sm, p.hdr, 48) && ok;
+          convert_rows(kt + u * KA_QUART, k.b);
+          filled(c, u);
+        }
       }
     }
   } else {
@@ -449,12 +477,9 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         m_used = cm;
         l_sum *= alpha;
       }
-      // O of the chunk before is done: P's buffer is free, and O may be rescaled
-      if (c > 0) {
-        for (int h = 0; h < 2; h++) ok = ka_wait(&sm.free_[(c - 1) & 1][h], (c - 1) >> 1, sm, p.hdr, 50) && ok;
+      if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {    // after the chunk before is in O
+        ok = ka_wait(&sm.free_[(c - 1) & 1][3], (c - 1) >> 1, sm, p.hdr, 50) && ok;
         tc::fence_after_sync();
-      }
-      if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {
         const float al = __shfl_sync(0xFFFFFFFFu, alpha, lane & 15);
 #pragma unroll 1
         for (int g = 0; g < D / 2; g += 32) {
@@ -466,6 +491,9 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         }
         tc::tmem_wait_st();
       }
+      // P's buffer is free once chunk c - 2 is in O
+      if (c >= 2) ok = ka_wait(&sm.free_[c & 1][3], (c >> 1) - 1, sm, p.hdr, 52) && ok;
+      unsigned char* pbuf = smem + KA_OFF_P + (c & 1) * KA_COL;
       const float ref = m_used == -INFINITY ? 0.f : m_used;
       float l4[4] = {0.f, 0.f, 0.f, 0.f};
       auto weights = [&](auto masked) {
@@ -499,7 +527,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 
     // ---------------- output: lane = (head, half of the dims)
     if (n_ch > 0) {
-      for (int h = 0; h < 2; h++) ok = ka_wait(&sm.free_[(n_ch - 1) & 1][h], (n_ch - 1) >> 1, sm, p.hdr, 51) && ok;
+      ok = ka_wait(&sm.free_[(n_ch - 1) & 1][3], (n_ch - 1) >> 1, sm, p.hdr, 51) && ok;
       tc::fence_after_sync();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -679,7 +707,7 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
   if (nr == 0) mr = mq;
   if (nk > 0 && !rows(&ms, p.sinks, nk)) return cudaErrorInvalidValue;
   if (nk == 0) ms = mr;
-  return p.main_kv ? keys_launch<true>(p, BQ, mq, mr, ms, stream) : keys_launch<false>(p, BQ, mq, mr, ms, stream);
+  return p.main_kv || p.rows_fp8 ? keys_launch<true>(p, BQ, mq, mr, ms, stream) : keys_launch<false>(p, BQ, mq, mr, ms, stream);
 }
 
 }  // namespace csa2

@@ -128,29 +128,27 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_
   mma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);
 }
 
-// The same two for a warp that runs its loop as a whole: one elected lane (the
-// same one every time) issues.  Addresses and descriptors then stay in uniform
-// registers; issued under `if (lane == 0)` every instruction moves them there
-// first, which costs more time than a small MMA takes.
-__device__ __forceinline__ void mma_f16_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile("{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xFFFFFFFF;\n"
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(r));
+  return r;
+}
+
+// The same two for a warp that runs its loop as a whole; the lane with `leader` set
+// issues.  Addresses and descriptors then stay in uniform registers; issued under
+// `if (lane == 0)` every instruction moves them there first.
+__device__ __forceinline__ void mma_f16_warp(uint32_t leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
                " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-               :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+               :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
 }
 
-// The same with A (M rows, two 16-bit elements of K per 32-bit column) in TMEM.
-__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                                uint32_t accumulate) {
-  asm volatile("{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xFFFFFFFF;\n"
-               " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-               :: "r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
-}
-
-__device__ __forceinline__ void commit_warp(uint64_t* bar) {
-  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n"
+__device__ __forceinline__ void commit_warp(uint32_t leader, uint64_t* bar) {
+  asm volatile("{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
                " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"
-               :: "r"(smem_u32(bar)) : "memory");
+               :: "r"(smem_u32(bar)), "r"(leader) : "memory");
 }
 
 // Instruction descriptor: kind::mxf4 (E2M1 x E2M1, UE8M0 scales), K-major A and B.

@@ -434,9 +434,11 @@ csa2_status csa2_qk_norm_rope(const csa2_qk_args *args, void *ws, size_t ws_byte
  * B * S < 2^31 and B * n_sink < 2^31, else CSA2_ERR_UNSUPPORTED.  q, rows, sinks
  * and out 16-byte, q_pos, swa_base_pos 8-byte and lse 4-byte aligned; out and
  * lse must not overlap an input or each other.
- * Precision: bf16 operands, binary32 accumulation and softmax state; E4M3 rows
- * are exact.  Workspace: csa2_window_attn_workspace_size (partial states when
- * a query's keys are divided over several CTAs).
+ * Precision: binary32 accumulation and softmax state.  With bf16 rows the
+ * operands are bf16; with E4M3 rows they are f16, which holds the rows exactly
+ * and rounds q as csa2_sparse_swa_attn does.  Workspace:
+ * csa2_window_attn_workspace_size (partial states when a query's keys are
+ * divided over several CTAs).
  */
 typedef struct {
     int B, Q;                   /* sequences, queries per sequence              */
