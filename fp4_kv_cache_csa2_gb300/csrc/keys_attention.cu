@@ -150,7 +150,7 @@ __device__ __forceinline__ KaChunk ka_chunk(const KaQuery& q, int64_t c) {
   return k;
 }
 
-template <bool F16, bool SPLIT>
+template <bool F16>
 __global__ void __launch_bounds__(KA_THREADS, 1)
 keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_rows,
                  const __grid_constant__ CUtensorMap map_sinks) {
@@ -163,7 +163,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     if (threadIdx.x == 0) report(p.hdr, CSA2_ERR_CUDA, 1);
     return;
   }
-  const int split = SPLIT ? p.split : 1;
+  const int split = p.split;
   const int64_t bq = blockIdx.x / split;
   const int sp = blockIdx.x % split;
   const int b = (int)(bq / p.Q);
@@ -533,7 +533,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const float m = __shfl_sync(0xFFFFFFFFu, m_used, lane & 15), l = __shfl_sync(0xFFFFFFFFu, l_sum, lane & 15);
     const int d0 = (D / 2) * (lane >> 4);
-    if (!SPLIT) {
+    if (split == 1) {
       if (p.lse && lane < 16) p.lse[bq * H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * KA_LN2;
       const float inv = 1.0f / l;
       uint4* out = reinterpret_cast<uint4*>(p.out + (bq * H + head) * D + d0);
@@ -663,9 +663,7 @@ static cudaError_t keys_launch(const KeysParams& p, int64_t BQ, const CUtensorMa
                                const CUtensorMap& ms, cudaStream_t stream) {
   static PerDeviceOnce attrs;
   cudaError_t e = attrs.ensure([](int) {
-    cudaError_t r = cudaFuncSetAttribute(keys_attn_kernel<F16, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, KA_SMEM);
-    if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(keys_attn_kernel<F16, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, KA_SMEM);
+    return cudaFuncSetAttribute(keys_attn_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, KA_SMEM);
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -678,8 +676,7 @@ static cudaError_t keys_launch(const KeysParams& p, int64_t BQ, const CUtensorMa
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = p.split > 1 ? cudaLaunchKernelEx(&cfg, keys_attn_kernel<F16, true>, p, mq, mr, ms)
-                  : cudaLaunchKernelEx(&cfg, keys_attn_kernel<F16, false>, p, mq, mr, ms);
+  e = cudaLaunchKernelEx(&cfg, keys_attn_kernel<F16>, p, mq, mr, ms);
   if (e != cudaSuccess || p.split == 1) return e;
   cudaLaunchConfig_t cc = {};
   cc.gridDim = dim3((unsigned)(BQ * 16));
