@@ -11,15 +11,18 @@
 // over `split` CTAs, and keys_combine_kernel joins their states.
 //
 // Per chunk, with the 64 heads as the rows of M = 64 tiles:
-//   * S = Q K^T   N = keys, K = 512 (32 MMAs)
-//   * softmax, one thread a head, straight from TMEM; P = 2^(S scale log2 e - m) goes
-//     to shared memory as the 16-bit A operand of the next product.  The reference m
-//     of a head moves only when a chunk exceeds it by more than e^8 (then the head's O
-//     and its sum are rescaled), so P stays inside f16
-//   * O += P V    N = 4 x 128 dims, K = keys: V is the K tile read MN-major
-// An M = 64 accumulator takes 16 lanes of each of TMEM's four lane quarters: the
-// dims 0..255 of O lie in lanes 0..15 of a quarter, the dims 256..511 in lanes
-// 16..31 of the same 256 columns, and S is double-buffered beside them.
+//   * S = Q K^T   N = keys, K = 512 in two halves of 256 dims (16 MMAs each)
+//   * softmax, two lanes a head, straight from TMEM; P = 2^(S scale log2 e - m) goes back
+//     to TMEM over S as the 16-bit A operand of the next product.  The reference m of a
+//     head moves only when a chunk exceeds it by more than e^8 (then the head's O and its
+//     sum are rescaled), so P stays inside f16
+//   * O += P V    N = 2 x 256 dims, K = keys: V is the K tile read MN-major
+// An M = 64 tile takes 16 lanes of each of TMEM's four lane quarters, so two of them
+// share columns: half h of the dims has its Q, its part of S and its O in lanes
+// 16h .. 16h + 15 (256 columns of O, 128 of Q, twice 64 of S), P lies in both.  With Q and P
+// in TMEM a product reads only the K tile from shared memory, 16 of its 32 cycles at
+// N = 64 (with Q there too it takes all 32, and the fill's stores come on top: 3100
+// cycles a chunk instead of RESULT).
 // Operands: F16 (calls with cache entries or E4M3 rows) keeps every dequantised FP4
 // value (at most 6 significant bits, 2^-10 .. 2688) and every E4M3 value exactly and
 // rounds q and bf16 window rows to f16, exact inside [2^-14, 65504], with P to 11
@@ -27,27 +30,20 @@
 // bits (its rounding errors are independent and average out; the sum of the softmax
 // is taken before that rounding, in binary32).
 //
-// Shared memory: Q 64 KB, two K buffers of [64 keys][512 dims] (four quarters of 16 KB,
-// two SW128 column chunks each), two P of 8 KB, and a staging area of 18 KB for the
-// next chunk's entries, or half a chunk's E4M3 rows, as stored.  Roles: warps 0..3
-// softmax and output; warps 4..11 fill the K buffers (staged bytes are converted in
-// registers before the wait for the buffer, so that only stores come after it; bf16
-// rows are rounded in place if need be); warp 12 issues the MMAs, S of chunk c + 1
-// before O of chunk c, so that the softmax of a chunk runs beside the products of its
-// neighbours; warp 13 issues the copies.
-// A quarter of a K buffer is refilled as soon as its part of O is done, and its part of
-// S follows as soon as it is filled: the chain product, refill, product of one chunk
-// sets the pace, and its links are as short as the hand-offs (100 to 200 cycles each)
-// allow.  All waits are bounded; a timeout reports CSA2_ERR_TIMEOUT and every thread
-// still takes every barrier.
-#include <type_traits>
-
+// Shared memory: three K buffers of [64 keys][512 dims] (two halves of 32 KB, four SW128
+// column chunks each; the third takes Q on its way to TMEM first) and a staging area of
+// 18 KB for the next chunk's entries, or half a chunk's E4M3 rows, as stored.  Roles:
+// warps 0..3 move Q, then softmax and output; warps 4..11 fill the K buffers (from the
+// staged bytes through registers; bf16 rows are rounded in place if need be); warp 12
+// issues the MMAs, S of chunk c + 1 before O of chunk c, so that the softmax of a chunk
+// runs beside the products of its neighbours; warp 13 issues the copies.  All waits are
+// bounded; a timeout reports CSA2_ERR_TIMEOUT and every thread still takes every barrier.
 #include "attn_common.cuh"
 #include "params.cuh"
 
 namespace csa2 {
 
-constexpr int KA_SOFT_WARPS = 4;                          // softmax, output: lane (mod 16) = head
+constexpr int KA_SOFT_WARPS = 4;                          // softmax, output: lane = (half of the dims or keys, head)
 constexpr int KA_FILL_WARPS = 8;                          // K buffers
 constexpr int KA_FILL = 32 * KA_FILL_WARPS;
 constexpr int KA_MMA_WARP = KA_SOFT_WARPS + KA_FILL_WARPS;
@@ -55,25 +51,26 @@ constexpr int KA_COPY_WARP = KA_MMA_WARP + 1;
 constexpr int KA_THREADS = 32 * (KA_COPY_WARP + 1);
 constexpr int KA_KEYS = KEYS_CHUNK;                       // keys per chunk
 constexpr int KA_COL = 64 * 128;                          // [64 rows][64 dims] 16-bit, SW128
-constexpr int KA_QUART = 2 * KA_COL;                      // a quarter of a K buffer: 128 dims
-constexpr int KA_OFF_Q = 8 * KA_QUART;
-constexpr int KA_OFF_P = KA_OFF_Q + 8 * KA_COL;
-constexpr int KA_OFF_STAGE = KA_OFF_P + 2 * KA_COL;       // P of chunk c at c % 2
+constexpr int KA_HALF = 4 * KA_COL;                       // half of a K buffer: 256 dims
+constexpr int KA_BUFS = 3;                                // K buffers: chunk c in c % 3
+constexpr int KA_OFF_STAGE = KA_BUFS * 2 * KA_HALF;
 constexpr int KA_OFF_SMALL = KA_OFF_STAGE + KA_KEYS * MAIN_BYTES;
 constexpr int KA_TMEM_COLS = 512;
-constexpr int KA_O_COL = 0;                               // dims 256 h ..: lanes 16 h .. of each quarter
-constexpr int KA_S_COL = 256;                             // S of chunk c at 64 (c % 2)
+constexpr int KA_O_COL = 0;                               // half h of the dims: lanes 16h .. of each quarter
+constexpr int KA_Q_COL = 256;
+constexpr int KA_S_COL = 384;                             // S, then P, of chunk c at 64 (c % 2)
+constexpr uint32_t KA_HALF_LANES = 16u << 16;
 constexpr float KA_LOG2E = 1.4426950408889634f;
 constexpr float KA_LN2 = 0.6931471805599453f;
 constexpr float KA_TAU = 8.0f * KA_LOG2E;
 constexpr int KA_PART_FLOATS = 2 * H + H * D;             // one partial state: references, sums, O [head][dim]
 
 struct KaSmall {
-  uint64_t q_full;                    // TMA: Q
+  uint64_t q_full, q_moved;           // TMA: Q; Q is in TMEM (a softmax warp each)
   uint64_t stage_full, stage_free;    // the staged bytes have come / were read (a fill warp each)
-  uint64_t row_full[2][4];            // TMA: bf16 rows in quarter u of K buffer i
-  uint64_t full[2][4];                // quarter u of K buffer i is filled (a fill warp each)
-  uint64_t free_[2][4];               // ... its part of O, and all before it, is done
+  uint64_t row_full[KA_BUFS][2];      // TMA: bf16 rows in half h of K buffer i
+  uint64_t full[KA_BUFS][2];          // half h of K buffer i is filled (a fill warp each)
+  uint64_t free_[KA_BUFS];            // O of the chunk in K buffer i is done
   uint64_t s_full;                    // S of a chunk is done
   uint64_t p_ready;                   // P is written, O rescaled if needed (a softmax warp each)
   uint32_t tmem_base;
@@ -155,7 +152,6 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
 keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_rows,
                  const __grid_constant__ CUtensorMap map_sinks) {
   extern __shared__ __align__(1024) unsigned char smem[];
-  unsigned char* qbuf = smem + KA_OFF_Q;
   unsigned char* stage = smem + KA_OFF_STAGE;
   KaSmall& sm = *reinterpret_cast<KaSmall*>(smem + KA_OFF_SMALL);
 
@@ -173,14 +169,16 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   if (warp == KA_MMA_WARP) tc::tmem_alloc(&sm.tmem_base, KA_TMEM_COLS);
   if (tid == 0) {
     tc::bar_init(&sm.q_full, 1);
+    tc::bar_init(&sm.q_moved, KA_SOFT_WARPS);
     tc::bar_init(&sm.stage_full, 1);
     tc::bar_init(&sm.stage_free, KA_FILL_WARPS);
-    for (int i = 0; i < 2; i++)
-      for (int u = 0; u < 4; u++) {
-        tc::bar_init(&sm.row_full[i][u], 1);
-        tc::bar_init(&sm.full[i][u], KA_FILL_WARPS);
-        tc::bar_init(&sm.free_[i][u], 1);
+    for (int i = 0; i < KA_BUFS; i++) {
+      for (int h = 0; h < 2; h++) {
+        tc::bar_init(&sm.row_full[i][h], 1);
+        tc::bar_init(&sm.full[i][h], KA_FILL_WARPS);
       }
+      tc::bar_init(&sm.free_[i], 1);
+    }
     tc::bar_init(&sm.s_full, 1);
     tc::bar_init(&sm.p_ready, KA_SOFT_WARPS);
     sm.err = 0;
@@ -205,34 +203,34 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     if (p.main_kv && p.n_entries[b] > p.cap) report(p.hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
   }
 
-  // Chunk c (counted from c_lo) uses K buffer c % 2; it is that buffer's use c / 2.
+  // Chunk c (counted from c_lo) uses K buffer c % 3; it is that buffer's use c / 3.
   if (warp == KA_MMA_WARP) {
-    // ================= MMAs (the whole warp runs the loop, one elected lane issues)
+    // ================= MMAs (the whole warp runs the loop, one lane issues)
     constexpr uint32_t idesc_s = F16 ? tc::idesc_f16(H, 0, 0, 0) : tc::idesc_bf16(H, 0, 0, 0);       // + N
-    constexpr uint32_t idesc_o = F16 ? tc::idesc_f16(H, 128, 0, 1) : tc::idesc_bf16(H, 128, 0, 1);
-    const uint64_t q_d = tc::smem_desc(tc::smem_u32(qbuf), 16, 1024, tc::SW_128B);
-    const uint64_t p_d = tc::smem_desc(tc::smem_u32(smem + KA_OFF_P), 16, 1024, tc::SW_128B);
+    constexpr uint32_t idesc_o = F16 ? tc::idesc_f16(H, 256, 0, 1) : tc::idesc_bf16(H, 256, 0, 1);
     const uint64_t k_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
     const uint64_t v_d = tc::smem_desc(tc::smem_u32(smem), KA_COL, 1024, tc::SW_128B);
     const uint32_t leader = tc::elect_one();
-    bool ok = true;
+    bool ok = n_ch > 0 ? ka_wait(&sm.q_moved, 0, sm, p.hdr, 40) : true;
+    int sb = 0, su = 0, ob = 0;                       // K buffer and use of the next S, K buffer of the next O
     auto scores = [&](int c) {
       const uint32_t idesc = idesc_s | (uint32_t)(ka_chunk(q, c_lo + c).n >> 3) << 17;
       const uint32_t s = tmem + KA_S_COL + 64 * (c & 1);
 #pragma unroll 1
-      for (int u = 0; u < 4; u++) {
-        ok = ka_wait(&sm.full[c & 1][u], c >> 1, sm, p.hdr, 41) && ok;
+      for (int h = 0; h < 2; h++) {
+        ok = ka_wait(&sm.full[sb][h], su, sm, p.hdr, 41) && ok;
         tc::fence_after_sync();
         if (ok) {
-          const uint64_t qa = q_d + (uint32_t)(u * (KA_QUART >> 4)), ka = k_d + (uint32_t)((4 * (c & 1) + u) * (KA_QUART >> 4));
+          const uint64_t ka = k_d + (uint32_t)((2 * sb + h) * (KA_HALF >> 4));
+          const uint32_t lanes = h * KA_HALF_LANES;
 #pragma unroll
-          for (int i = 0; i < 8; i++) {
-            const uint32_t off = (uint32_t)((i >> 2) * KA_COL + (i & 3) * 32) >> 4;
-            tc::mma_f16_warp(leader, s, qa + off, ka + off, idesc, (u || i) ? 1u : 0u);
-          }
+          for (int i = 0; i < 16; i++)
+            tc::mma_f16_ts_warp(leader, s + lanes, tmem + KA_Q_COL + lanes + 8 * i,
+                                ka + ((uint32_t)((i >> 2) * KA_COL + (i & 3) * 32) >> 4), idesc, i ? 1u : 0u);
         }
       }
       tc::commit_warp(leader, &sm.s_full);
+      if (++sb == KA_BUFS) sb = 0, su++;
     };
     if (n_ch > 0) scores(0);
     for (int c = 0; c < n_ch; c++) {
@@ -240,32 +238,35 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       const int steps = ka_chunk(q, c_lo + c).n / 16;
       ok = ka_wait(&sm.p_ready, c, sm, p.hdr, 42) && ok;
       tc::fence_after_sync();
+      if (ok) {
 #pragma unroll 1
-      for (int u = 0; u < 4; u++) {
-        if (ok) {
-          const uint64_t va = v_d + (uint32_t)((4 * (c & 1) + u) * (KA_QUART >> 4));
-          const uint32_t o = tmem + KA_O_COL + 128 * (u & 1) + ((uint32_t)(16 * (u >> 1)) << 16);
+        for (int h = 0; h < 2; h++) {
+          const uint64_t va = v_d + (uint32_t)((2 * ob + h) * (KA_HALF >> 4));
+          const uint32_t lanes = h * KA_HALF_LANES;
 #pragma unroll
           for (int ks = 0; ks < KA_KEYS / 16; ks++)
             if (ks < steps)
-              tc::mma_f16_warp(leader, o, p_d + (uint32_t)((c & 1) * (KA_COL >> 4) + 2 * ks), va + (uint32_t)(ks * (2048 >> 4)),
-                               idesc_o, (c || ks) ? 1u : 0u);
+              tc::mma_f16_ts_warp(leader, tmem + KA_O_COL + lanes, tmem + KA_S_COL + 64 * (c & 1) + lanes + 8 * ks,
+                                  va + (uint32_t)(ks * (2048 >> 4)), idesc_o, (c || ks) ? 1u : 0u);
         }
-        tc::commit_warp(leader, &sm.free_[c & 1][u]);
       }
+      tc::commit_warp(leader, &sm.free_[ob]);
+      if (++ob == KA_BUFS) ob = 0;
     }
   } else if (warp == KA_COPY_WARP) {
     // ================= copies
     if (lane == 0 && n_ch > 0) {
       bool ok = true;
-      tc::bar_arrive_expect_tx(&sm.q_full, 8u * KA_COL);
-      for (int i = 0; i < 8; i++) tc::tma_load_2d(qbuf + i * KA_COL, &map_q, i * 64, (int32_t)(bq * H), &sm.q_full);
+      tc::bar_arrive_expect_tx(&sm.q_full, 8u * KA_COL);   // Q into the last K buffer
+      for (int i = 0; i < 8; i++)
+        tc::tma_load_2d(smem + (KA_BUFS - 1) * 2 * KA_HALF + i * KA_COL, &map_q, i * 64, (int32_t)(bq * H), &sm.q_full);
       uint32_t staged = 0;                            // uses of the staging area
       auto next_stage = [&](uint32_t bytes) {
         if (staged > 0) ok = ka_wait(&sm.stage_free, staged - 1, sm, p.hdr, 43) && ok;
         staged++;
         tc::bar_arrive_expect_tx(&sm.stage_full, bytes);
       };
+      int kb = 0, use = 0;
       for (int c = 0; c < n_ch; c++) {
         const KaChunk k = ka_chunk(q, c_lo + c);
         if (c_lo + c >= q.cr) {                       // entries [first, first + b), contiguous
@@ -277,20 +278,21 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         const bool window = c_lo + c < q.cw;
         const CUtensorMap* map = window ? &map_rows : &map_sinks;
         const int32_t y = (int32_t)((int64_t)b * (window ? p.S : (int64_t)p.n_sink) + k.first);
-        if (p.rows_fp8) {
-          for (int h = 0; h < 2; h++) {
-            next_stage(KA_QUART);
-            for (int i = 0; i < 4; i++) tc::tma_load_2d(stage + i * (KA_COL / 2), map, (4 * h + i) * 64, y, &sm.stage_full);
+        if (!p.rows_fp8) {
+          // the tensor cores (the softmax warps, of Q) have read the buffer, which is waited for here
+          if (use > 0) ok = ka_wait(&sm.free_[kb], use - 1, sm, p.hdr, 44) && ok;
+          else if (kb == KA_BUFS - 1) ok = ka_wait(&sm.q_moved, 0, sm, p.hdr, 44) && ok;
+        }
+        for (int h = 0; h < 2; h++) {
+          unsigned char* kt = smem + (2 * kb + h) * KA_HALF;
+          if (p.rows_fp8) next_stage(KA_HALF / 2);
+          else tc::bar_arrive_expect_tx(&sm.row_full[kb][h], KA_HALF);
+          for (int i = 0; i < 4; i++) {
+            if (p.rows_fp8) tc::tma_load_2d(stage + i * (KA_COL / 2), map, (4 * h + i) * 64, y, &sm.stage_full);
+            else tc::tma_load_2d(kt + i * KA_COL, map, (4 * h + i) * 64, y, &sm.row_full[kb][h]);
           }
-          continue;
         }
-        for (int u = 0; u < 4; u++) {
-          // the quarter was read by the tensor cores, whose completion is waited for here
-          if (c >= 2) ok = ka_wait(&sm.free_[c & 1][u], (c >> 1) - 1, sm, p.hdr, 44) && ok;
-          unsigned char* kt = smem + (4 * (c & 1) + u) * KA_QUART;
-          tc::bar_arrive_expect_tx(&sm.row_full[c & 1][u], KA_QUART);
-          for (int i = 0; i < 2; i++) tc::tma_load_2d(kt + i * KA_COL, map, (2 * u + i) * 64, y, &sm.row_full[c & 1][u]);
-        }
+        if (++kb == KA_BUFS) kb = 0, use++;
       }
     }
     __syncwarp();
@@ -298,11 +300,12 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     // ================= K buffers
     const int ft = tid - 32 * KA_SOFT_WARPS;
     bool ok = true;
-    // entries: thread = (key, 16 bytes of each 64: 32 of each 128 dims).  The lanes of an
-    // eight-lane phase hold keys k and k + 2: with 18 units of 16 bytes an entry, their reads
-    // lie in eight different bank groups
+    // thread = (key, part j: 32 of each 128 dims).  The lanes of an eight-lane phase hold keys
+    // k and k + 2: with 18 units of 16 bytes an entry, their reads lie in eight different bank
+    // groups
     const int k8 = (ft >> 2) & 7, j = ft & 3;
     const int key = ((ft >> 2) & ~7) + ((k8 & 4) | (k8 & 1) << 1 | (k8 >> 1 & 1));
+    const bool odd = (j & 2) != 0;
     // 16 bytes of codes (32 dims) times their two scales, the bytes of `w2`
     auto dequant = [&](const uint4& c, uint32_t w2, uint32_t* o) {
       const uint32_t sa = e4m3x2_to_f16x2(prmt(w2, 0u, 0x0000u)), sb = e4m3x2_to_f16x2(prmt(w2, 0u, 0x1111u));
@@ -314,12 +317,11 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         for (int x = 0; x < 4; x++) o[4 * g + x] = hmul2(o[4 * g + x], g < 2 ? sa : sb);
       }
     };
-    // 32 dims of key `key` into a quarter
+    // 32 dims of key `key` into a quarter (two column chunks): column chunk j / 2, units
+    // 4 (j % 2) ..; lanes with j >= 2 walk them as g ^ 1, so that the eight lanes of a phase store
+    // to eight different bank groups
     auto store = [&](unsigned char* kt, const uint32_t* o) {
-      // column chunk j / 2, units 4 (j % 2) ..; lanes with j >= 2 walk them as g ^ 1, so that the
-      // eight lanes of a phase store to eight different bank groups
       unsigned char* dst = kt + (j >> 1) * KA_COL + key * 128;
-      const bool odd = (j & 2) != 0;
 #pragma unroll
       for (int g = 0; g < 4; g++) {
         const uint4 v = make_uint4(odd ? o[4 * (g ^ 1)] : o[4 * g], odd ? o[4 * (g ^ 1) + 1] : o[4 * g + 1],
@@ -328,11 +330,10 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         *reinterpret_cast<uint4*>(dst + ((unit ^ (uint32_t)(key & 7)) << 4)) = v;
       }
     };
-    // 32 E4M3 dims of row `key` from quarter u % 2 of the staged half; rows behind the chunk's
-    // last: zeros.  Lanes with j >= 2 take their two pieces in the other order (bank groups)
+    // 32 E4M3 dims of row `key` from quarter u of the staged half; rows behind the chunk's last:
+    // zeros.  Lanes with j >= 2 take their two pieces in the other order (bank groups)
     auto widen = [&](int u, uint32_t* o, int n) {
-      const uint4* src = reinterpret_cast<const uint4*>(stage + (2 * (u & 1) + (j >> 1)) * (KA_COL / 2) + key * 64 + 32 * (j & 1));
-      const bool odd = (j & 2) != 0;
+      const uint4* src = reinterpret_cast<const uint4*>(stage + (2 * u + (j >> 1)) * (KA_COL / 2) + key * 64 + 32 * (j & 1));
       uint4 a = make_uint4(0u, 0u, 0u, 0u), e = a;
       if (key < n) {
         a = src[odd ? 1 : 0];
@@ -346,129 +347,130 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         o[2 * x + 1] = e4m3x2_to_f16x2(v[x] >> 16);
       }
     };
-    // a quarter of bf16 rows, where the copy has put it: rounded to f16 when the operands
-    // are f16, rows behind the chunk's last set to zero (what is not seen may hold anything,
-    // infinities among it)
-    auto convert_rows = [&](unsigned char* kt, int n) {
-      if (!F16 && n == KA_KEYS) return;
-#pragma unroll 4
-      for (int i = ft; i < KA_QUART / 16; i += KA_FILL) {
-        uint4* u = reinterpret_cast<uint4*>(kt) + i;
-        if (((i >> 3) & (KA_KEYS - 1)) >= n) *u = make_uint4(0u, 0u, 0u, 0u);
-        else if (F16) {
-          const uint4 x = *u;
-          *u = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
-        }
-      }
-    };
-    if (n_ch > 0) {
-      ok = ka_wait(&sm.q_full, 0, sm, p.hdr, 45) && ok;
-      if (F16) {                                      // Q rounded to f16 in place
-        uint4* qv = reinterpret_cast<uint4*>(qbuf);
-#pragma unroll 4
-        for (int i = ft; i < 8 * KA_COL / 16; i += KA_FILL) {
-          const uint4 x = qv[i];
-          qv[i] = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
-        }
-      }
-    }
     uint32_t staged = 0;                              // uses of the staging area
-    auto wait_stage = [&]() { ok = ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46) && ok; };
     auto stage_read = [&]() {
       __syncwarp();
       if (lane == 0) tc::bar_arrive(&sm.stage_free);
     };
-    auto wait_free = [&](int c, int u) {
-      if (c < 2) return;
-      ok = ka_wait(&sm.free_[c & 1][u], (c >> 1) - 1, sm, p.hdr, 47) && ok;
-      tc::fence_after_sync();
-    };
-    auto filled = [&](int c, int u) {
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sm.full[c & 1][u]);
-    };
+    int kb = 0, use = 0;
     for (int c = 0; c < n_ch; c++) {
       const KaChunk k = ka_chunk(q, c_lo + c);
-      unsigned char* kt = smem + 4 * (c & 1) * KA_QUART;
-      if (F16 && c_lo + c >= q.cr) {                  // entries
-        wait_stage();
-        uint4 cd[4] = {}, sc[2] = {};                 // codes of the four quarters, scales of the two halves
-        if (key < k.b) {
-          const uint4* e = reinterpret_cast<const uint4*>(stage + key * MAIN_BYTES);
-#pragma unroll
-          for (int i = 0; i < 4; i++) cd[i] = e[4 * i + j];
-          sc[0] = e[16];
-          sc[1] = e[17];
-        }
-        stage_read();
-        uint32_t o[4][16];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const uint4 s4 = sc[i >> 1];                // scale bytes 2j, 2j + 1 of the quarter
-          const uint32_t w = (i & 1) ? (j & 2 ? s4.w : s4.z) : (j & 2 ? s4.y : s4.x);
-          dequant(cd[i], w >> (16 * (j & 1)), o[i]);
-#pragma unroll
-          for (int x = 0; x < 16; x++) asm volatile("" : "+r"(o[i][x]));   // here, not after the wait below
-        }
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-          wait_free(c, u);
-          store(kt + u * KA_QUART, o[u]);
-          filled(c, u);
-        }
-      } else if (F16 && p.rows_fp8) {
-        for (int h = 0; h < 2; h++) {
+      const bool entries = c_lo + c >= q.cr;
+      if (use > 0) {
+        ok = ka_wait(&sm.free_[kb], use - 1, sm, p.hdr, 47) && ok;
+        tc::fence_after_sync();
+      } else if (kb == KA_BUFS - 1) {
+        ok = ka_wait(&sm.q_moved, 0, sm, p.hdr, 47) && ok;
+      }
+      if (F16 && entries) ok = ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46) && ok;
+#pragma unroll 1
+      for (int h = 0; h < 2; h++) {
+        unsigned char* kt = smem + (2 * kb + h) * KA_HALF;
+        if (F16 && (entries || p.rows_fp8)) {
           uint32_t o[2][16];
-          wait_stage();
-          widen(0, o[0], k.b);
-          widen(1, o[1], k.b);
-          stage_read();
-#pragma unroll
-          for (int i = 0; i < 2; i++) {
-            wait_free(c, 2 * h + i);
-            store(kt + (2 * h + i) * KA_QUART, o[i]);
-            filled(c, 2 * h + i);
+          if (entries) {
+            uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0, s4 = c0;     // keys behind the last: zeros
+            if (key < k.b) {
+              const uint4* e = reinterpret_cast<const uint4*>(stage + key * MAIN_BYTES);
+              c0 = e[8 * h + j];
+              c1 = e[8 * h + 4 + j];
+              s4 = e[16 + h];
+            }
+            if (h == 1) stage_read();
+            // scale bytes 2j, 2j + 1 of each quarter
+            dequant(c0, (odd ? s4.y : s4.x) >> (16 * (j & 1)), o[0]);
+            dequant(c1, (odd ? s4.w : s4.z) >> (16 * (j & 1)), o[1]);
+          } else {
+            ok = ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46) && ok;
+            widen(0, o[0], k.b);
+            widen(1, o[1], k.b);
+            stage_read();
+          }
+          store(kt, o[0]);
+          store(kt + 2 * KA_COL, o[1]);
+        } else {
+          // bf16 rows, where the copy has put them (rows come first: copy `use` of the buffer too):
+          // rounded to f16 when the operands are f16, rows behind the chunk's last set to zero
+          // (what is not seen may hold anything, infinities among it)
+          ok = ka_wait(&sm.row_full[kb][h], use, sm, p.hdr, 48) && ok;
+          if (F16 || k.b < KA_KEYS) {
+#pragma unroll 4
+            for (int i = ft; i < KA_HALF / 16; i += KA_FILL) {
+              uint4* u = reinterpret_cast<uint4*>(kt) + i;
+              if (((i >> 3) & (KA_KEYS - 1)) >= k.b) *u = make_uint4(0u, 0u, 0u, 0u);
+              else if (F16) {
+                const uint4 x = *u;
+                *u = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
+              }
+            }
           }
         }
-      } else {
-        for (int u = 0; u < 4; u++) {                 // rows come first: use c / 2 of the buffer's copies too
-          ok = ka_wait(&sm.row_full[c & 1][u], c >> 1, sm, p.hdr, 48) && ok;
-          convert_rows(kt + u * KA_QUART, k.b);
-          filled(c, u);
-        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sm.full[kb][h]);
       }
+      if (++kb == KA_BUFS) kb = 0, use++;
     }
   } else {
-    // ================= softmax: lanes 0..15 hold heads 16 warp ..; output: all lanes
+    // ================= softmax and output: lane = (half, head 16 warp + lane % 16)
     const uint32_t quarter = (uint32_t)(warp * 32) << 16;
     const float sc2 = p.scale * KA_LOG2E;
-    const int head = 16 * warp + (lane & 15);
-    float m_used = -INFINITY, l_sum = 0.f;            // the head's reference and sum (lanes 0..15)
+    const int head = 16 * warp + (lane & 15), half = lane >> 4;
+    float m_used = -INFINITY, l_sum = 0.f;            // the head's reference; its sum over this lane's keys
     bool ok = true;
+    if (n_ch > 0) {                                   // Q: this lane's 256 dims of its head to TMEM
+      ok = ka_wait(&sm.q_full, 0, sm, p.hdr, 45) && ok;
+      const unsigned char* qh = smem + ((KA_BUFS - 1) * 2 + half) * KA_HALF;
+#pragma unroll 1
+      for (int g = 0; g < 4; g++) {                   // column chunk g of the half: 32 columns of TMEM
+        uint32_t w[32];
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+          const uint4 x = *reinterpret_cast<const uint4*>(qh + g * KA_COL + sw128((uint32_t)head, 16u * u));
+          w[4 * u] = F16 ? bf16x2_to_f16x2(x.x) : x.x;
+          w[4 * u + 1] = F16 ? bf16x2_to_f16x2(x.y) : x.y;
+          w[4 * u + 2] = F16 ? bf16x2_to_f16x2(x.z) : x.z;
+          w[4 * u + 3] = F16 ? bf16x2_to_f16x2(x.w) : x.w;
+        }
+        tmem_st32(tmem + quarter + KA_Q_COL + 32 * g, w);
+      }
+      tc::tmem_wait_st();
+      tc::fence_proxy_async_smem();                   // the buffer goes to copies and stores of others
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sm.q_moved);
+    }
+    int ob = 0, ou = 0;                               // K buffer and use of the chunk before
     for (int c = 0; c < n_ch; c++) {
-      const KaChunk k = ka_chunk(q, c_lo + c);
+      const int n = ka_chunk(q, c_lo + c).b - 32 * half;   // this lane takes keys 32 half ..: n of them are there
+      const uint32_t s_addr = tmem + quarter + KA_S_COL + 64 * (c & 1);
       ok = ka_wait(&sm.s_full, c, sm, p.hdr, 49) && ok;
       tc::fence_after_sync();
-      uint32_t s[64];
+      float v[32];
       {
-        const uint32_t s_addr = tmem + quarter + KA_S_COL + 64 * (c & 1);
-        tc::tmem_ld_x32_nowait(s_addr, s);
-        tc::tmem_ld_x32_nowait(s_addr + 32, s + 32);
-        tc::tmem_wait_ld_regs(s);
-        tc::tmem_wait_ld_regs(s + 32);
+        // every lane holds its half of the dims' part of 64 keys: the two lanes of a head
+        // swap 32 of them, so that each has the whole of its 32 keys
+        uint32_t s0[32], s1[32];
+        tc::tmem_ld_x32_nowait(s_addr, s0);
+        tc::tmem_ld_x32_nowait(s_addr + 32, s1);
+        tc::tmem_wait_ld_regs(s0);
+        tc::tmem_wait_ld_regs(s1);
+#pragma unroll
+        for (int x = 0; x < 32; x++) {
+          const float got = __uint_as_float(__shfl_xor_sync(0xFFFFFFFFu, half ? s0[x] : s1[x], 16));
+          v[x] = (__uint_as_float(half ? s1[x] : s0[x]) + got) * sc2;
+        }
       }
-      const bool whole = k.b == KA_KEYS;
+      const bool whole = __all_sync(0xFFFFFFFFu, n >= 32);
+      if (!whole) {
+#pragma unroll
+        for (int x = 0; x < 32; x++) v[x] = x < n ? v[x] : -INFINITY;
+      }
       float c4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (whole) {
 #pragma unroll
-        for (int x = 0; x < 64; x++) c4[x & 3] = fmaxf(c4[x & 3], __uint_as_float(s[x]) * sc2);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 64; x++)
-          c4[x & 3] = fmaxf(c4[x & 3], (x < k.b) ? __uint_as_float(s[x]) * sc2 : -INFINITY);
-      }
-      const float cm = lane < 16 ? fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3])) : -INFINITY;
+      for (int x = 0; x < 32; x++) c4[x & 3] = fmaxf(c4[x & 3], v[x]);
+      float cm = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
+      cm = fmaxf(cm, __shfl_xor_sync(0xFFFFFFFFu, cm, 16));
       float alpha = 1.f;
       if (m_used == -INFINITY) {
         m_used = cm;                                  // O holds nothing yet, or only zeros
@@ -478,48 +480,37 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         l_sum *= alpha;
       }
       if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {    // after the chunk before is in O
-        ok = ka_wait(&sm.free_[(c - 1) & 1][3], (c - 1) >> 1, sm, p.hdr, 50) && ok;
+        ok = ka_wait(&sm.free_[ob], ou, sm, p.hdr, 50) && ok;
         tc::fence_after_sync();
-        const float al = __shfl_sync(0xFFFFFFFFu, alpha, lane & 15);
 #pragma unroll 1
         for (int g = 0; g < D / 2; g += 32) {
           uint32_t o[32];
           tmem_ld32(tmem + quarter + KA_O_COL + g, o);
 #pragma unroll
-          for (int x = 0; x < 32; x++) o[x] = __float_as_uint(__uint_as_float(o[x]) * al);
+          for (int x = 0; x < 32; x++) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
           tmem_st32(tmem + quarter + KA_O_COL + g, o);
         }
-        tc::tmem_wait_st();
       }
-      // P's buffer is free once chunk c - 2 is in O
-      if (c >= 2) ok = ka_wait(&sm.free_[c & 1][3], (c >> 1) - 1, sm, p.hdr, 52) && ok;
-      unsigned char* pbuf = smem + KA_OFF_P + (c & 1) * KA_COL;
+      if (c > 0 && ++ob == KA_BUFS) ob = 0, ou++;
       const float ref = m_used == -INFINITY ? 0.f : m_used;
       float l4[4] = {0.f, 0.f, 0.f, 0.f};
-      auto weights = [&](auto masked) {
+      uint32_t pk[16];
 #pragma unroll
-        for (int u = 0; u < 8; u++) {                 // 8 keys, 16 bytes of P
-          uint32_t pk[4];
-#pragma unroll
-          for (int y = 0; y < 4; y++) {
-            const int x = 8 * u + 2 * y;
-            float e0 = ex2_ftz(fmaf(__uint_as_float(s[x]), sc2, -ref));
-            float e1 = ex2_ftz(fmaf(__uint_as_float(s[x + 1]), sc2, -ref));
-            if (decltype(masked)::value) {
-              e0 = (x < k.b) ? e0 : 0.f;
-              e1 = (x + 1 < k.b) ? e1 : 0.f;
-            }
-            l4[y] += e0 + e1;
-            pk[y] = F16 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
-          }
-          if (lane < 16)
-            *reinterpret_cast<uint4*>(pbuf + sw128((uint32_t)head, (uint32_t)(16 * u))) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        }
-      };
-      if (whole) weights(std::false_type{});
-      else weights(std::true_type{});
+      for (int x = 0; x < 16; x++) {
+        float e0 = ex2_ftz(v[2 * x] - ref), e1 = ex2_ftz(v[2 * x + 1] - ref);
+        l4[x & 3] += e0 + e1;
+        pk[x] = F16 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+      }
       l_sum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-      tc::fence_proxy_async_smem();
+      uint32_t pw[32];                                // P of all 64 keys for this lane's half of the dims, over S
+#pragma unroll
+      for (int x = 0; x < 16; x++) {
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, pk[x], 16);
+        pw[x] = half ? got : pk[x];
+        pw[16 + x] = half ? pk[x] : got;
+      }
+      tmem_st32(s_addr, pw);
+      tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::bar_arrive(&sm.p_ready);
@@ -527,12 +518,12 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 
     // ---------------- output: lane = (head, half of the dims)
     if (n_ch > 0) {
-      ok = ka_wait(&sm.free_[(n_ch - 1) & 1][3], (n_ch - 1) >> 1, sm, p.hdr, 51) && ok;
+      ok = ka_wait(&sm.free_[(n_ch - 1) % KA_BUFS], (n_ch - 1) / KA_BUFS, sm, p.hdr, 51) && ok;
       tc::fence_after_sync();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const float m = __shfl_sync(0xFFFFFFFFu, m_used, lane & 15), l = __shfl_sync(0xFFFFFFFFu, l_sum, lane & 15);
-    const int d0 = (D / 2) * (lane >> 4);
+    const float m = m_used, l = l_sum + __shfl_xor_sync(0xFFFFFFFFu, l_sum, 16);
+    const int d0 = (D / 2) * half;
     if (split == 1) {
       if (p.lse && lane < 16) p.lse[bq * H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * KA_LN2;
       const float inv = 1.0f / l;

@@ -135,14 +135,15 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 
-// The same two for a warp that runs its loop as a whole; the lane with `leader` set
-// issues.  Addresses and descriptors then stay in uniform registers; issued under
-// `if (lane == 0)` every instruction moves them there first.
-__device__ __forceinline__ void mma_f16_warp(uint32_t leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit operands, fp32 accumulate (K = 16: two
+// elements per 32-bit column of A), for a warp that runs its loop as a whole; the lane
+// with `leader` set issues.  Addresses and descriptors then stay in uniform registers;
+// issued under `if (lane == 0)` every instruction moves them there first.
+__device__ __forceinline__ void mma_f16_ts_warp(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
   asm volatile("{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
-               " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-               :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
+               " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+               :: "r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
 }
 
 __device__ __forceinline__ void commit_warp(uint32_t leader, uint64_t* bar) {
