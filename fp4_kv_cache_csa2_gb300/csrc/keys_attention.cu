@@ -60,6 +60,7 @@ constexpr int KA_O_COL = 0;                               // half h of the dims:
 constexpr int KA_Q_COL = 256;
 constexpr int KA_S_COL = 384;                             // S, then P, of chunk c at 64 (c % 2)
 constexpr uint32_t KA_HALF_LANES = 16u << 16;
+constexpr int KA_AHEAD = 5;                               // chunks of entries that are on their way to L2
 constexpr float KA_LOG2E = 1.4426950408889634f;
 constexpr float KA_LN2 = 0.6931471805599453f;
 constexpr float KA_TAU = 8.0f * KA_LOG2E;
@@ -88,63 +89,58 @@ __device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t count, KaSmall& 
   return tc::bar_wait(bar, count & 1u) || ka_timeout(&sm.err, hdr, where);
 }
 
-// One query's keys and how they lie in chunks.
-struct KaQuery {
+// One query's keys, and a CTA's run of their chunks [c_lo, c_lo + n): window rows, then
+// sinks, then cache entries.
+struct KaRun {
   int64_t t, lo;                      // position, first window position
-  int64_t r0;                         // its first window row that was supplied
-  int64_t wn, sn, en;                 // window rows, sinks, cache entries it sees
-  int64_t cw, cr, nc;                 // window chunks, chunks of rows (window and sinks), all chunks
+  int64_t r0;                         // buffer row of the run's first window key, were it chunk 0
+  int64_t s0, e0;                     // the same for sinks and entries (negative: they start later)
+  int n, cw, cr;                      // chunks; those before cw are of the window, before cr of rows
+  uint32_t wl, sl, el;                // keys of each kind from chunk 0 on (chunk c has them less 64 c)
 };
 
-__device__ __forceinline__ KaQuery ka_query(const KeysParams& p, int64_t bq, int b, int64_t base) {
-  KaQuery q;
+__device__ __forceinline__ KaRun ka_run(const KeysParams& p, int64_t bq, int b, int64_t base, int sp, int split) {
+  KaRun q;
   q.t = p.q_pos[bq];
   const bool live = q.t >= 0;
   q.lo = live && q.t >= p.W ? q.t - p.W + 1 : 0;
   // the window positions lo .. t that lie in rows 0 .. S - 1 (unsigned differences: any
   // two positions have one), so that the work is bounded by what was supplied
-  q.r0 = q.wn = 0;
+  int64_t row = 0, wn = 0, en = 0;
   if (live && q.t >= base) {
     const uint64_t s = (uint64_t)p.S, r0 = q.lo > base ? (uint64_t)q.lo - (uint64_t)base : 0;
     const uint64_t end = (uint64_t)q.t - (uint64_t)base;     // row of position t
     const uint64_t r1 = end < s ? end + 1 : s;
     if (r0 < r1) {
-      q.r0 = (int64_t)r0;
-      q.wn = (int64_t)(r1 - r0);
+      row = (int64_t)r0;
+      wn = (int64_t)(r1 - r0);
     }
   }
-  q.sn = live ? (q.lo < p.n_sink ? q.lo : (int64_t)p.n_sink) : 0;
-  q.en = 0;
+  const int64_t sn = live ? (q.lo < p.n_sink ? q.lo : (int64_t)p.n_sink) : 0;
   if (live && p.main_kv) {
-    q.en = visible_entries(q.t, p.m, p.n_entries[b]);
-    if (q.en > p.cap) q.en = p.cap;   // reported by the kernel
-    if (q.en < 0) q.en = 0;
+    en = visible_entries(q.t, p.m, p.n_entries[b]);
+    if (en > p.cap) en = p.cap;       // reported by the kernel
+    if (en < 0) en = 0;
   }
-  q.cw = ceil_div(q.wn, KA_KEYS);
-  q.cr = q.cw + ceil_div(q.sn, KA_KEYS);
-  q.nc = q.cr + ceil_div(q.en, KA_KEYS);
+  const int64_t cw = ceil_div(wn, KA_KEYS), cr = cw + ceil_div(sn, KA_KEYS), nc = cr + ceil_div(en, KA_KEYS);
+  const int64_t c_lo = nc * sp / split;
+  q.n = (int)(nc * (sp + 1) / split - c_lo);
+  q.cw = (int)max(cw - c_lo, (int64_t)0);
+  q.cr = (int)max(cr - c_lo, (int64_t)0);
+  q.r0 = row + KA_KEYS * c_lo;
+  q.s0 = KA_KEYS * (c_lo - cw);
+  q.e0 = KA_KEYS * (c_lo - cr);
+  // every count is below 2^31 and so is 64 c: no wrap where a chunk has keys of the kind
+  q.wl = (uint32_t)(wn - KA_KEYS * c_lo);
+  q.sl = (uint32_t)(sn - q.s0);
+  q.el = (uint32_t)(en - q.e0);
   return q;
 }
 
-struct KaChunk {
-  int64_t first;                      // buffer row or entry of key 0
-  int b;                              // its keys
-  int n;                              // the same rounded up to a multiple of 16
-};
-
-__device__ __forceinline__ KaChunk ka_chunk(const KaQuery& q, int64_t c) {
-  KaChunk k;
-  int64_t left;
-  if (c < q.cw) {
-    k.first = q.r0 + KA_KEYS * c;
-    left = q.wn - KA_KEYS * c;
-  } else {
-    k.first = KA_KEYS * (c - (c < q.cr ? q.cw : q.cr));
-    left = (c < q.cr ? q.sn : q.en) - k.first;
-  }
-  k.b = left < KA_KEYS ? (int)left : KA_KEYS;
-  k.n = (k.b + 15) & ~15;
-  return k;
+// Keys of chunk c (1 .. 64).
+__device__ __forceinline__ int ka_keys(const KaRun& q, int c) {
+  const uint32_t left = (c < q.cw ? q.wl : c < q.cr ? q.sl : q.el) - (uint32_t)(KA_KEYS * c);
+  return left < (uint32_t)KA_KEYS ? (int)left : KA_KEYS;
 }
 
 template <bool F16>
@@ -194,9 +190,8 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const int64_t base = p.base_pos[b];
-  const KaQuery q = ka_query(p, bq, b, base);
-  const int64_t c_lo = q.nc * sp / split;
-  const int n_ch = (int)(q.nc * (sp + 1) / split - c_lo);
+  const KaRun q = ka_run(p, bq, b, base, sp, split);
+  const int n_ch = q.n;
   if (sp == 0 && tid == 0 && q.t >= 0) {              // what the caller did not supply
     if (q.lo < base) report(p.hdr, CSA2_ERR_BOUNDS, q.lo);
     else if ((uint64_t)q.t - (uint64_t)base >= (uint64_t)p.S) report(p.hdr, CSA2_ERR_BOUNDS, q.t);
@@ -214,7 +209,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     bool ok = n_ch > 0 ? ka_wait(&sm.q_moved, 0, sm, p.hdr, 40) : true;
     int sb = 0, su = 0, ob = 0;                       // K buffer and use of the next S, K buffer of the next O
     auto scores = [&](int c) {
-      const uint32_t idesc = idesc_s | (uint32_t)(ka_chunk(q, c_lo + c).n >> 3) << 17;
+      const uint32_t idesc = idesc_s | (uint32_t)((ka_keys(q, c) + 15) >> 4 << 1) << 17;
       const uint32_t s = tmem + KA_S_COL + 64 * (c & 1);
 #pragma unroll 1
       for (int h = 0; h < 2; h++) {
@@ -235,7 +230,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     if (n_ch > 0) scores(0);
     for (int c = 0; c < n_ch; c++) {
       if (c + 1 < n_ch) scores(c + 1);
-      const int steps = ka_chunk(q, c_lo + c).n / 16;
+      const int steps = (ka_keys(q, c) + 15) >> 4;
       ok = ka_wait(&sm.p_ready, c, sm, p.hdr, 42) && ok;
       tc::fence_after_sync();
       if (ok) {
@@ -267,17 +262,26 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         tc::bar_arrive_expect_tx(&sm.stage_full, bytes);
       };
       int kb = 0, use = 0;
+      // entries ahead of the staging area into L2: a copy from there takes a third of the
+      // time of one from memory, and there is room for one chunk only
+      const uint8_t* kv = p.main_kv + ((int64_t)b * p.cap + q.e0) * MAIN_BYTES;   // entry 0 of chunk 0
+      auto ahead = [&](int c) {
+        if (c >= q.cr && c < n_ch) tc::prefetch_l2(kv + (int64_t)c * (KA_KEYS * MAIN_BYTES), ka_keys(q, c) * MAIN_BYTES);
+      };
+      if (p.main_kv)
+        for (int c = 1; c < KA_AHEAD; c++) ahead(c);
       for (int c = 0; c < n_ch; c++) {
-        const KaChunk k = ka_chunk(q, c_lo + c);
-        if (c_lo + c >= q.cr) {                       // entries [first, first + b), contiguous
-          const uint32_t bytes = (uint32_t)(k.b * MAIN_BYTES);
+        if (c >= q.cr) {                              // entries, contiguous
+          const uint32_t bytes = (uint32_t)(ka_keys(q, c) * MAIN_BYTES);
           next_stage(bytes);
-          tc::bulk_load(stage, p.main_kv + ((int64_t)b * p.cap + k.first) * MAIN_BYTES, bytes, &sm.stage_full);
+          tc::bulk_load(stage, kv + (int64_t)c * (KA_KEYS * MAIN_BYTES), bytes, &sm.stage_full);
+          ahead(c + KA_AHEAD);
           continue;
         }
-        const bool window = c_lo + c < q.cw;
+        if (p.main_kv) ahead(c + KA_AHEAD);
+        const bool window = c < q.cw;
         const CUtensorMap* map = window ? &map_rows : &map_sinks;
-        const int32_t y = (int32_t)((int64_t)b * (window ? p.S : (int64_t)p.n_sink) + k.first);
+        const int32_t y = (int32_t)(window ? (int64_t)b * p.S + q.r0 + KA_KEYS * c : (int64_t)b * p.n_sink + q.s0 + KA_KEYS * c);
         if (!p.rows_fp8) {
           // the tensor cores (the softmax warps, of Q) have read the buffer, which is waited for here
           if (use > 0) ok = ka_wait(&sm.free_[kb], use - 1, sm, p.hdr, 44) && ok;
@@ -354,8 +358,8 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     };
     int kb = 0, use = 0;
     for (int c = 0; c < n_ch; c++) {
-      const KaChunk k = ka_chunk(q, c_lo + c);
-      const bool entries = c_lo + c >= q.cr;
+      const int keys = ka_keys(q, c);
+      const bool entries = c >= q.cr;
       if (use > 0) {
         ok = ka_wait(&sm.free_[kb], use - 1, sm, p.hdr, 47) && ok;
         tc::fence_after_sync();
@@ -370,7 +374,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           uint32_t o[2][16];
           if (entries) {
             uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0, s4 = c0;     // keys behind the last: zeros
-            if (key < k.b) {
+            if (key < keys) {
               const uint4* e = reinterpret_cast<const uint4*>(stage + key * MAIN_BYTES);
               c0 = e[8 * h + j];
               c1 = e[8 * h + 4 + j];
@@ -382,8 +386,8 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
             dequant(c1, (odd ? s4.w : s4.z) >> (16 * (j & 1)), o[1]);
           } else {
             ok = ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46) && ok;
-            widen(0, o[0], k.b);
-            widen(1, o[1], k.b);
+            widen(0, o[0], keys);
+            widen(1, o[1], keys);
             stage_read();
           }
           store(kt, o[0]);
@@ -393,11 +397,11 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           // rounded to f16 when the operands are f16, rows behind the chunk's last set to zero
           // (what is not seen may hold anything, infinities among it)
           ok = ka_wait(&sm.row_full[kb][h], use, sm, p.hdr, 48) && ok;
-          if (F16 || k.b < KA_KEYS) {
+          if (F16 || keys < KA_KEYS) {
 #pragma unroll 4
             for (int i = ft; i < KA_HALF / 16; i += KA_FILL) {
               uint4* u = reinterpret_cast<uint4*>(kt) + i;
-              if (((i >> 3) & (KA_KEYS - 1)) >= k.b) *u = make_uint4(0u, 0u, 0u, 0u);
+              if (((i >> 3) & (KA_KEYS - 1)) >= keys) *u = make_uint4(0u, 0u, 0u, 0u);
               else if (F16) {
                 const uint4 x = *u;
                 *u = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
@@ -442,7 +446,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     }
     int ob = 0, ou = 0;                               // K buffer and use of the chunk before
     for (int c = 0; c < n_ch; c++) {
-      const int n = ka_chunk(q, c_lo + c).b - 32 * half;   // this lane takes keys 32 half ..: n of them are there
+      const int n = ka_keys(q, c) - 32 * half;   // this lane takes keys 32 half ..: n of them are there
       const uint32_t s_addr = tmem + quarter + KA_S_COL + 64 * (c & 1);
       ok = ka_wait(&sm.s_full, c, sm, p.hdr, 49) && ok;
       tc::fence_after_sync();
