@@ -335,26 +335,59 @@ def decode(mode: int, cache: Cache, *, q_pos, q, swa, swa_base_pos, scale: float
 
 # The calls below also check what the C boundary cannot see: shapes, element
 # sizes, and that every tensor lies contiguous on the device of the workspace.
-def _tensor(name: str, t, shape, itemsizes, device, token_stride: bool = False):
-    """Address of `t`, which has `shape` (None: any size), elements of one of
-    `itemsizes` bytes, lies on `device` and is contiguous (with token_stride:
-    but for the stride of its first dimension)."""
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.element_size() not in itemsizes:
-        raise ValueError(f"{name}: {t.dtype}, expected elements of {itemsizes} bytes")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the workspace on {device}")
-    if not t.is_contiguous() and not (token_stride and t[0].is_contiguous()):
-        raise ValueError(f"{name}: strides {t.stride()} of shape {tuple(t.shape)}")
+# A decode step makes these calls one after another, each of a few microseconds on
+# the GPU, so the checks are plain comparisons and the message is put together
+# only for a call that is refused.
+def _refuse(name: str, t, shape, what: str, device):
+    raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}; expected {what} "
+                     f"{tuple(shape)}, contiguous, on {device}")
+
+
+def _bits16(name: str, t, shape, device):
+    """Address of a contiguous 16-bit tensor of this shape on this device."""
+    if t.shape != shape or t.element_size() != 2 or t.device != device or not t.is_contiguous():
+        _refuse(name, t, shape, "16-bit elements", device)
     return t.data_ptr()
 
 
-def _call(name: str, fn, device, stream, *args):
-    """fn(*args, stream) with `device` current; its error, if any, raised."""
+def _rows(name: str, t, shape, device):
+    """Address of window rows: 16-bit elements (bf16) or bytes (E4M3)."""
+    if t.shape != shape or t.element_size() > 2 or t.device != device or not t.is_contiguous():
+        _refuse(name, t, shape, "16-bit or 8-bit elements", device)
+    return t.data_ptr()
+
+
+def _int64(name: str, t, shape, device):
+    if t.shape != shape or t.element_size() != 8 or t.device != device or not t.is_contiguous():
+        _refuse(name, t, shape, "64-bit integers", device)
+    return t.data_ptr()
+
+
+def _float32(name: str, t, shape, device):
+    if t.shape != shape or t.element_size() != 4 or t.device != device or not t.is_contiguous():
+        _refuse(name, t, shape, "float32", device)
+    return t.data_ptr()
+
+
+def _tokens(name: str, t, shape, inner, device):
+    """Address of 16-bit tokens whose strides but the first are `inner`."""
+    if t.shape != shape or t.stride()[1:] != inner or t.element_size() != 2 or t.device != device:
+        _refuse(name, t, shape, f"16-bit elements with inner strides {inner}, not", device)
+    return t.data_ptr()
+
+
+def _call(name: str, device, stream, *args):
+    """The library's `name` on `stream` (None: the device's current one), with `device` current."""
     import torch
-    with torch.cuda.device(device):
-        _check(name, fn(*args, _stream(stream)))
+    fn = getattr(_lib or load(), name)
+    handle = (stream or torch.cuda.current_stream(device)).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status != 0:
+        raise Csa2Error(name, status)
 
 
 def qk_norm_rope(pos, rope_cs, ws: Workspace, *, q=None, q_weight=None, q_out=None, k=None, k_weight=None, rows=None,
@@ -364,25 +397,24 @@ def qk_norm_rope(pos, rope_cs, ws: Workspace, *, q=None, q_weight=None, q_out=No
     (bf16, or uint8: E4M3).  Tokens with pos -1 write nothing.  q and k may be
     views with a larger token stride; q_out may be q itself."""
     dev, T = ws.buf.device, pos.numel()
-    a = QkArgs(T=T, pos=_tensor("pos", pos, (T,), (8,), dev),
-               rope_cs=_tensor("rope_cs", rope_cs, (None, D_ROPE // 2, 2), (4,), dev), rope_P=rope_cs.shape[0],
-               eps=float(eps))
+    table = rope_cs.shape[0]
+    qa = qs = qw = qo = ka = ks = kw = ro = sl = None
+    n_rows = fp8 = 0
     if q is not None:
-        a.q = _tensor("q", q, (T, N_HEADS, D_LATENT), (2,), dev, True)
-        a.q_stride = q.stride(0) if T > 1 else N_HEADS * D_LATENT
-        a.q_out = _tensor("q_out", q_out, (T, N_HEADS, D_LATENT), (2,), dev)
-        if q_weight is not None:
-            a.q_weight = _tensor("q_weight", q_weight, (D_LATENT,), (4,), dev)
+        qa = _tokens("q", q, (T, N_HEADS, D_LATENT), (D_LATENT, 1), dev)
+        qs = q.stride(0) if T > 1 else N_HEADS * D_LATENT
+        qw = None if q_weight is None else _float32("q_weight", q_weight, (D_LATENT,), dev)
+        qo = _bits16("q_out", q_out, (T, N_HEADS, D_LATENT), dev)
     if k is not None:
-        a.k = _tensor("k", k, (T, D_LATENT), (2,), dev, True)
-        a.k_stride = k.stride(0) if T > 1 else D_LATENT
-        a.rows = _tensor("rows", rows, (*[None] * (rows.dim() - 1), D_LATENT), (1, 2), dev)
-        a.n_rows, a.rows_fp8 = rows.numel() // D_LATENT, int(rows.element_size() == 1)
-        if k_weight is not None:
-            a.k_weight = _tensor("k_weight", k_weight, (D_LATENT,), (4,), dev)
-        if k_slot is not None:
-            a.k_slot = _tensor("k_slot", k_slot, (T,), (8,), dev)
-    _call("csa2_qk_norm_rope", load().csa2_qk_norm_rope, dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
+        ka = _tokens("k", k, (T, D_LATENT), (1,), dev)
+        ks = k.stride(0) if T > 1 else D_LATENT
+        kw = None if k_weight is None else _float32("k_weight", k_weight, (D_LATENT,), dev)
+        ro = _rows("rows", rows, (*rows.shape[:-1], D_LATENT), dev)
+        n_rows, fp8 = rows.numel() // D_LATENT, 1 if rows.element_size() == 1 else 0
+        sl = None if k_slot is None else _int64("k_slot", k_slot, (T,), dev)
+    a = QkArgs(T, _int64("pos", pos, (T,), dev), _float32("rope_cs", rope_cs, (table, D_ROPE // 2, 2), dev), table,
+               float(eps), fp8, qa, qs or 0, qw, qo, ka, ks or 0, kw, ro, n_rows, sl)
+    _call("csa2_qk_norm_rope", dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
 
 
 def window_attn_workspace_size(B: int, Q: int, W: int, n_sink: int) -> int:
@@ -395,18 +427,15 @@ def window_attn(q, rows, swa_base_pos, q_pos, scale: float, out, ws: Workspace, 
     t-W+1 .. t and the sinks [B][n][512] before them (both bf16, or both uint8:
     E4M3).  lse: float32 [B][Q][64] or None."""
     dev, (B, Q), S, n = ws.buf.device, q_pos.shape, rows.shape[1], 0 if sinks is None else sinks.shape[1]
-    size = rows.element_size()
-    a = WindowArgs(B=B, Q=Q, S=S, W=W, n_sink=n, scale=float(scale), rows_fp8=int(size == 1),
-                   q_pos=_tensor("q_pos", q_pos, (B, Q), (8,), dev),
-                   q=_tensor("q", q, (B, Q, N_HEADS, D_LATENT), (2,), dev),
-                   rows=_tensor("rows", rows, (B, S, D_LATENT), (1, 2), dev),
-                   swa_base_pos=_tensor("swa_base_pos", swa_base_pos, (B,), (8,), dev),
-                   out=_tensor("out", out, (B, Q, N_HEADS, D_LATENT), (2,), dev))
-    if sinks is not None:
-        a.sinks = _tensor("sinks", sinks, (B, n, D_LATENT), (size,), dev)
-    if lse is not None:
-        a.lse = _tensor("lse", lse, (B, Q, N_HEADS), (4,), dev)
-    _call("csa2_window_attn", load().csa2_window_attn, dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
+    shape = (B, Q, N_HEADS, D_LATENT)
+    if n and sinks.element_size() != rows.element_size():
+        _refuse("sinks", sinks, (B, n, D_LATENT), "elements of the rows' size", dev)
+    a = WindowArgs(B, Q, S, W, n, float(scale), _int64("q_pos", q_pos, (B, Q), dev), _bits16("q", q, shape, dev),
+                   _rows("rows", rows, (B, S, D_LATENT), dev), _int64("swa_base_pos", swa_base_pos, (B,), dev),
+                   _rows("sinks", sinks, (B, n, D_LATENT), dev) if n else None, _bits16("out", out, shape, dev),
+                   None if lse is None else _float32("lse", lse, (B, Q, N_HEADS), dev),
+                   1 if rows.element_size() == 1 else 0)
+    _call("csa2_window_attn", dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
 
 
 def dense_attn_workspace_size(B: int, Q: int, max_n: int) -> int:
@@ -422,13 +451,9 @@ def dense_attn(cache: Cache, q, swa, swa_base_pos, q_pos, scale: float, out, ws:
     dev, (B, Q), S = ws.buf.device, q_pos.shape, swa.shape[1]
     if B != cache.B:
         raise ValueError(f"q_pos: {B} sequences, the cache has {cache.B}")
-    a = DenseArgs(B=B, Q=Q, S=S, scale=float(scale), max_n=max_n, swa_fp8=int(swa.element_size() == 1),
-                  q_pos=_tensor("q_pos", q_pos, (B, Q), (8,), dev),
-                  q=_tensor("q", q, (B, Q, N_HEADS, D_LATENT), (2,), dev),
-                  swa=_tensor("swa", swa, (B, S, D_LATENT), (1, 2), dev),
-                  swa_base_pos=_tensor("swa_base_pos", swa_base_pos, (B,), (8,), dev),
-                  out=_tensor("out", out, (B, Q, N_HEADS, D_LATENT), (2,), dev))
-    if lse is not None:
-        a.lse = _tensor("lse", lse, (B, Q, N_HEADS), (4,), dev)
-    c = cache.struct()
-    _call("csa2_dense_attn", load().csa2_dense_attn, dev, stream, ctypes.byref(c), ctypes.byref(a), ws.ptr, ws.nbytes)
+    shape = (B, Q, N_HEADS, D_LATENT)
+    a = DenseArgs(B, Q, S, float(scale), max_n, _int64("q_pos", q_pos, (B, Q), dev), _bits16("q", q, shape, dev),
+                  _rows("swa", swa, (B, S, D_LATENT), dev), _int64("swa_base_pos", swa_base_pos, (B,), dev),
+                  _bits16("out", out, shape, dev), None if lse is None else _float32("lse", lse, (B, Q, N_HEADS), dev),
+                  1 if swa.element_size() == 1 else 0)
+    _call("csa2_dense_attn", dev, stream, ctypes.byref(cache.struct()), ctypes.byref(a), ws.ptr, ws.nbytes)
