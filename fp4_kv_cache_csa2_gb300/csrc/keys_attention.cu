@@ -54,6 +54,7 @@ constexpr int KA_COL = 64 * 128;                          // [64 rows][64 dims] 
 constexpr int KA_HALF = 4 * KA_COL;                       // half of a K buffer: 256 dims
 constexpr int KA_BUFS = 3;                                // K buffers: chunk c in c % 3
 constexpr int KA_OFF_STAGE = KA_BUFS * 2 * KA_HALF;
+constexpr int KA_OFF_OUT = 0;                             // outputs: [32 rows][128 dims] bf16 a softmax warp, over the K buffers
 constexpr int KA_OFF_SMALL = KA_OFF_STAGE + KA_KEYS * MAIN_BYTES;
 constexpr int KA_TMEM_COLS = 512;
 constexpr int KA_O_COL = 0;                               // half h of the dims: lanes 16h .. of each quarter
@@ -64,16 +65,19 @@ constexpr int KA_AHEAD = 5;                               // chunks of entries t
 constexpr float KA_LOG2E = 1.4426950408889634f;
 constexpr float KA_LN2 = 0.6931471805599453f;
 constexpr float KA_TAU = 8.0f * KA_LOG2E;
-constexpr int KA_PART_FLOATS = 2 * H + H * D;             // one partial state: references, sums, O [head][dim]
+constexpr int KA_PART_FLOATS = 2 * H + H * D;             // one partial state: references, sums, O [dims / 4][head][4]
 
+// A wait for a phase by its parity needs that the barrier cannot have passed the phase
+// after it: whatever completes that one must itself wait for the waiter.  Where two
+// phases in a row do not depend on the waiter, there are two barriers in turn.
 struct KaSmall {
   uint64_t q_full, q_moved;           // TMA: Q; Q is in TMEM (a softmax warp each)
   uint64_t stage_full, stage_free;    // the staged bytes have come / were read (a fill warp each)
   uint64_t row_full[KA_BUFS][2];      // TMA: bf16 rows in half h of K buffer i
   uint64_t full[KA_BUFS][2];          // half h of K buffer i is filled (a fill warp each)
   uint64_t free_[KA_BUFS];            // O of the chunk in K buffer i is done
-  uint64_t s_full;                    // S of a chunk is done
-  uint64_t p_ready;                   // P is written, O rescaled if needed (a softmax warp each)
+  uint64_t s_full[2];                 // S of every second chunk is done
+  uint64_t p_ready[2];                // its P is written, O rescaled if needed (a softmax warp each)
   uint32_t tmem_base;
   int err;
 };
@@ -85,6 +89,7 @@ __device__ __noinline__ bool ka_timeout(int* err, WsHeader* hdr, int where) {
   return false;
 }
 
+// `ok = ok && ka_wait(..)`: a thread that has given up once waits no more.
 __device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t count, KaSmall& sm, WsHeader* hdr, int where) {
   return tc::bar_wait(bar, count & 1u) || ka_timeout(&sm.err, hdr, where);
 }
@@ -175,8 +180,10 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       }
       tc::bar_init(&sm.free_[i], 1);
     }
-    tc::bar_init(&sm.s_full, 1);
-    tc::bar_init(&sm.p_ready, KA_SOFT_WARPS);
+    for (int i = 0; i < 2; i++) {
+      tc::bar_init(&sm.s_full[i], 1);
+      tc::bar_init(&sm.p_ready[i], KA_SOFT_WARPS);
+    }
     sm.err = 0;
     tc::bar_init_fence();
     tc::prefetch_tensormap(&map_q);
@@ -213,7 +220,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       const uint32_t s = tmem + KA_S_COL + 64 * (c & 1);
 #pragma unroll 1
       for (int h = 0; h < 2; h++) {
-        ok = ka_wait(&sm.full[sb][h], su, sm, p.hdr, 41) && ok;
+        ok = ok && ka_wait(&sm.full[sb][h], su, sm, p.hdr, 41);
         tc::fence_after_sync();
         if (ok) {
           const uint64_t ka = k_d + (uint32_t)((2 * sb + h) * (KA_HALF >> 4));
@@ -224,14 +231,14 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
                                 ka + ((uint32_t)((i >> 2) * KA_COL + (i & 3) * 32) >> 4), idesc, i ? 1u : 0u);
         }
       }
-      tc::commit_warp(leader, &sm.s_full);
+      tc::commit_warp(leader, &sm.s_full[c & 1]);
       if (++sb == KA_BUFS) sb = 0, su++;
     };
     if (n_ch > 0) scores(0);
     for (int c = 0; c < n_ch; c++) {
       if (c + 1 < n_ch) scores(c + 1);
       const int steps = (ka_keys(q, c) + 15) >> 4;
-      ok = ka_wait(&sm.p_ready, c, sm, p.hdr, 42) && ok;
+      ok = ok && ka_wait(&sm.p_ready[c & 1], c >> 1, sm, p.hdr, 42);
       tc::fence_after_sync();
       if (ok) {
 #pragma unroll 1
@@ -257,7 +264,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         tc::tma_load_2d(smem + (KA_BUFS - 1) * 2 * KA_HALF + i * KA_COL, &map_q, i * 64, (int32_t)(bq * H), &sm.q_full);
       uint32_t staged = 0;                            // uses of the staging area
       auto next_stage = [&](uint32_t bytes) {
-        if (staged > 0) ok = ka_wait(&sm.stage_free, staged - 1, sm, p.hdr, 43) && ok;
+        if (staged > 0) ok = ok && ka_wait(&sm.stage_free, staged - 1, sm, p.hdr, 43);
         staged++;
         tc::bar_arrive_expect_tx(&sm.stage_full, bytes);
       };
@@ -284,8 +291,8 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         const int32_t y = (int32_t)(window ? (int64_t)b * p.S + q.r0 + KA_KEYS * c : (int64_t)b * p.n_sink + q.s0 + KA_KEYS * c);
         if (!p.rows_fp8) {
           // the tensor cores (the softmax warps, of Q) have read the buffer, which is waited for here
-          if (use > 0) ok = ka_wait(&sm.free_[kb], use - 1, sm, p.hdr, 44) && ok;
-          else if (kb == KA_BUFS - 1) ok = ka_wait(&sm.q_moved, 0, sm, p.hdr, 44) && ok;
+          if (use > 0) ok = ok && ka_wait(&sm.free_[kb], use - 1, sm, p.hdr, 44);
+          else if (kb == KA_BUFS - 1) ok = ok && ka_wait(&sm.q_moved, 0, sm, p.hdr, 44);
         }
         for (int h = 0; h < 2; h++) {
           unsigned char* kt = smem + (2 * kb + h) * KA_HALF;
@@ -361,12 +368,12 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       const int keys = ka_keys(q, c);
       const bool entries = c >= q.cr;
       if (use > 0) {
-        ok = ka_wait(&sm.free_[kb], use - 1, sm, p.hdr, 47) && ok;
+        ok = ok && ka_wait(&sm.free_[kb], use - 1, sm, p.hdr, 47);
         tc::fence_after_sync();
       } else if (kb == KA_BUFS - 1) {
-        ok = ka_wait(&sm.q_moved, 0, sm, p.hdr, 47) && ok;
+        ok = ok && ka_wait(&sm.q_moved, 0, sm, p.hdr, 47);
       }
-      if (F16 && entries) ok = ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46) && ok;
+      if (F16 && entries) ok = ok && ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46);
 #pragma unroll 1
       for (int h = 0; h < 2; h++) {
         unsigned char* kt = smem + (2 * kb + h) * KA_HALF;
@@ -385,7 +392,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
             dequant(c0, (odd ? s4.y : s4.x) >> (16 * (j & 1)), o[0]);
             dequant(c1, (odd ? s4.w : s4.z) >> (16 * (j & 1)), o[1]);
           } else {
-            ok = ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46) && ok;
+            ok = ok && ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46);
             widen(0, o[0], keys);
             widen(1, o[1], keys);
             stage_read();
@@ -396,7 +403,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           // bf16 rows, where the copy has put them (rows come first: copy `use` of the buffer too):
           // rounded to f16 when the operands are f16, rows behind the chunk's last set to zero
           // (what is not seen may hold anything, infinities among it)
-          ok = ka_wait(&sm.row_full[kb][h], use, sm, p.hdr, 48) && ok;
+          ok = ok && ka_wait(&sm.row_full[kb][h], use, sm, p.hdr, 48);
           if (F16 || keys < KA_KEYS) {
 #pragma unroll 4
             for (int i = ft; i < KA_HALF / 16; i += KA_FILL) {
@@ -423,7 +430,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     float m_used = -INFINITY, l_sum = 0.f;            // the head's reference; its sum over this lane's keys
     bool ok = true;
     if (n_ch > 0) {                                   // Q: this lane's 256 dims of its head to TMEM
-      ok = ka_wait(&sm.q_full, 0, sm, p.hdr, 45) && ok;
+      ok = ok && ka_wait(&sm.q_full, 0, sm, p.hdr, 45);
       const unsigned char* qh = smem + ((KA_BUFS - 1) * 2 + half) * KA_HALF;
 #pragma unroll 1
       for (int g = 0; g < 4; g++) {                   // column chunk g of the half: 32 columns of TMEM
@@ -448,7 +455,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     for (int c = 0; c < n_ch; c++) {
       const int n = ka_keys(q, c) - 32 * half;   // this lane takes keys 32 half ..: n of them are there
       const uint32_t s_addr = tmem + quarter + KA_S_COL + 64 * (c & 1);
-      ok = ka_wait(&sm.s_full, c, sm, p.hdr, 49) && ok;
+      ok = ok && ka_wait(&sm.s_full[c & 1], c >> 1, sm, p.hdr, 49);
       tc::fence_after_sync();
       float v[32];
       {
@@ -484,7 +491,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         l_sum *= alpha;
       }
       if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {    // after the chunk before is in O
-        ok = ka_wait(&sm.free_[ob], ou, sm, p.hdr, 50) && ok;
+        ok = ok && ka_wait(&sm.free_[ob], ou, sm, p.hdr, 50);
         tc::fence_after_sync();
 #pragma unroll 1
         for (int g = 0; g < D / 2; g += 32) {
@@ -517,41 +524,57 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sm.p_ready);
+      if (lane == 0) tc::bar_arrive(&sm.p_ready[c & 1]);
     }
 
     // ---------------- output: lane = (head, half of the dims)
     if (n_ch > 0) {
-      ok = ka_wait(&sm.free_[(n_ch - 1) % KA_BUFS], (n_ch - 1) / KA_BUFS, sm, p.hdr, 51) && ok;
+      ok = ok && ka_wait(&sm.free_[(n_ch - 1) % KA_BUFS], (n_ch - 1) / KA_BUFS, sm, p.hdr, 51);
       tc::fence_after_sync();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const float m = m_used, l = l_sum + __shfl_xor_sync(0xFFFFFFFFu, l_sum, 16);
-    const int d0 = (D / 2) * half;
+    const bool none = l == 0.f;                       // no visible key: zeros
     if (split == 1) {
-      if (p.lse && lane < 16) p.lse[bq * H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * KA_LN2;
+      if (p.lse && half == 0) p.lse[bq * H + head] = none ? -INFINITY : (m + log2f(l)) * KA_LN2;
       const float inv = 1.0f / l;
-      uint4* out = reinterpret_cast<uint4*>(p.out + (bq * H + head) * D + d0);
+      // A lane holds 32 dims of its row at a time.  Stored from there, an instruction would touch
+      // 32 rows of 1 KB with 16 bytes each (7000 cycles an output); through shared memory (the K
+      // buffers, whose last reader is done) it covers 256 bytes of two rows.
+      unsigned char* mine = smem + KA_OFF_OUT + warp * 8192;
+      uint4* out = reinterpret_cast<uint4*>(p.out + (bq * H + 16 * warp) * D);
 #pragma unroll 1
-      for (int g = 0; g < D / 2; g += 32) {
-        uint32_t o[32];
-        if (n_ch > 0) tmem_ld32(tmem + quarter + KA_O_COL + g, o);
+      for (int g = 0; g < D / 2; g += 128) {
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t o[32];
+          if (n_ch > 0) tmem_ld32(tmem + quarter + KA_O_COL + g + c, o);
 #pragma unroll
-        for (int x = 0; x < 4; x++) {
-          float f[8];
+          for (int x = 0; x < 4; x++) {
+            float f[8];
 #pragma unroll
-          for (int y = 0; y < 8; y++) f[y] = l == 0.f ? 0.f : __uint_as_float(o[8 * x + y]) * inv;   // no key: zeros
-          out[g / 8 + x] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                      pack_bf16x2(f[6], f[7]));
+            for (int y = 0; y < 8; y++) f[y] = none ? 0.f : __uint_as_float(o[8 * x + y]) * inv;
+            *reinterpret_cast<uint4*>(mine + lane * 256 + ((((c >> 3) + x) ^ (lane & 7)) << 4)) =
+                make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+          }
         }
+        __syncwarp();
+#pragma unroll 4
+        for (int x = 0; x < 16; x++) {                // lane `row` of the warp: head 16 warp + row % 16, half row / 16
+          const int row = 2 * x + half, u = lane & 15;
+          out[(row & 15) * (D / 8) + (D / 16) * (row >> 4) + g / 8 + u] =
+              *reinterpret_cast<const uint4*>(mine + row * 256 + ((u ^ (row & 7)) << 4));
+        }
+        __syncwarp();
       }
     } else {
+      // a partial state: O as [dims / 4][head][4], so that the lanes of a half write 256 bytes
       float* part = p.part + (int64_t)blockIdx.x * KA_PART_FLOATS;
-      if (lane < 16) {
+      if (half == 0) {
         part[head] = m;
         part[H + head] = l;
       }
-      float4* out = reinterpret_cast<float4*>(part + 2 * H + head * D + d0);
+      float4* out = reinterpret_cast<float4*>(part + 2 * H) + (D / 8) * half * H + head;
       if (n_ch > 0) {
 #pragma unroll 1
         for (int g = 0; g < D / 2; g += 32) {
@@ -559,14 +582,17 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           tmem_ld32(tmem + quarter + KA_O_COL + g, o);
 #pragma unroll
           for (int x = 0; x < 8; x++)
-            out[g / 4 + x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                                         __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+            out[(g / 4 + x) * H] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                               __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
         }
       }
     }
   }
   tc::fence_before_sync();
   __syncthreads();
+  // after a timeout copies may be in flight that nobody waited for: time for them to land
+  if (*(volatile int*)&sm.err != 0)
+    for (int i = 0; i < 1000; i++) __nanosleep(1000);
   if (warp == KA_MMA_WARP) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, KA_TMEM_COLS);
@@ -574,38 +600,40 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 }
 
 // One query's output from its CTAs' partial states: with m = max_s m_s and
-// w_s = 2^(m_s - m), O = sum_s w_s O_s / sum_s w_s l_s.  One warp per (head,
-// half of the dims); the weights of 32 states at a time lie in the lanes.
+// w_s = 2^(m_s - m), O = sum_s w_s O_s / sum_s w_s l_s.  A CTA takes four heads: thread =
+// (head, 4 dims of each half), so that a warp reads 64-byte pieces of [dims / 4][head][4].
+// Every warp works out the weights of its four heads, 8 states at a time in its lanes.
 __global__ void __launch_bounds__(256) keys_combine_kernel(const float* __restrict__ part, int split,
                                                            uint16_t* __restrict__ out, float* __restrict__ lse) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, hl = lane & 3;
   const int64_t bq = blockIdx.x >> 4;
-  const int h = (blockIdx.x & 15) * 4 + (threadIdx.x >> 6), d0 = ((threadIdx.x >> 5) & 1) * (D / 2) + 4 * lane;
+  const int h = (blockIdx.x & 15) * 4 + hl, dg = threadIdx.x >> 2;   // dims 4 dg .. and 256 + 4 dg ..
   const float* pb = part + bq * split * KA_PART_FLOATS;
-  float mx = -INFINITY;
-  for (int s = lane; s < split; s += 32) mx = fmaxf(mx, pb[(int64_t)s * KA_PART_FLOATS + h]);
+  float mx = -INFINITY;                               // lane = (state of eight, head)
+  for (int s = lane >> 2; s < split; s += 8) mx = fmaxf(mx, pb[(int64_t)s * KA_PART_FLOATS + h]);
 #pragma unroll
-  for (int k = 16; k >= 1; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
+  for (int k = 16; k >= 4; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
   float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   float L = 0.f;
-  for (int s0 = 0; s0 < split; s0 += 32) {
+  for (int s0 = 0; s0 < split; s0 += 8) {
     float w = 0.f;
-    if (s0 + lane < split) {
-      const float* ps = pb + (int64_t)(s0 + lane) * KA_PART_FLOATS;
+    const int s = s0 + (lane >> 2);
+    if (s < split) {
+      const float* ps = pb + (int64_t)s * KA_PART_FLOATS;
       const float l = ps[H + h];
       if (l != 0.f) {                                 // a state that saw a key
         w = exp2f(ps[h] - mx);
         L += w * l;
       }
     }
-    const int n = min(32, split - s0);
-#pragma unroll 4
-    for (int i = 0; i < n; i++) {
-      const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
-      const float* o = pb + (int64_t)(s0 + i) * KA_PART_FLOATS + 2 * H + h * D + d0;
-      if (wi != 0.f) {                                // a state without keys holds no O
-        const float4 x = *reinterpret_cast<const float4*>(o), y = *reinterpret_cast<const float4*>(o + 128);
+    const int n = min(8, split - s0);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const float wi = __shfl_sync(0xFFFFFFFFu, w, 4 * i + hl);
+      if (i < n && wi != 0.f) {                       // a state without keys holds no O
+        const float4* o = reinterpret_cast<const float4*>(pb + (int64_t)(s0 + i) * KA_PART_FLOATS + 2 * H) + dg * H + h;
+        const float4 x = o[0], y = o[(D / 8) * H];
         a[0] += wi * x.x;
         a[1] += wi * x.y;
         a[2] += wi * x.z;
@@ -618,12 +646,12 @@ __global__ void __launch_bounds__(256) keys_combine_kernel(const float* __restri
     }
   }
 #pragma unroll
-  for (int k = 16; k >= 1; k >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, k);
+  for (int k = 16; k >= 4; k >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, k);
   const float inv = L == 0.f ? 0.f : 1.0f / L;        // no visible key: zeros
-  if (lse && (threadIdx.x & 63) == 0) lse[bq * H + h] = L == 0.f ? -INFINITY : (mx + log2f(L)) * KA_LN2;
-  uint16_t* o = out + (bq * H + h) * D + d0;
+  if (lse && threadIdx.x < 4) lse[bq * H + h] = L == 0.f ? -INFINITY : (mx + log2f(L)) * KA_LN2;
+  uint16_t* o = out + (bq * H + h) * D + 4 * dg;
   *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv));
-  *reinterpret_cast<uint2*>(o + 128) = make_uint2(pack_bf16x2(a[4] * inv, a[5] * inv), pack_bf16x2(a[6] * inv, a[7] * inv));
+  *reinterpret_cast<uint2*>(o + D / 2) = make_uint2(pack_bf16x2(a[4] * inv, a[5] * inv), pack_bf16x2(a[6] * inv, a[7] * inv));
 }
 
 // ------------------------------------------------------------------ host side
