@@ -142,6 +142,9 @@ __device__ __forceinline__ KaRun ka_run(const KeysParams& p, int64_t bq, int b, 
   return q;
 }
 
+// x, the same in every lane, in a uniform register.
+__device__ __forceinline__ uint32_t ka_uniform(uint32_t x) { return __reduce_or_sync(0xFFFFFFFFu, x); }
+
 // Keys of chunk c (1 .. 64).
 __device__ __forceinline__ int ka_keys(const KaRun& q, int c) {
   const uint32_t left = (c < q.cw ? q.wl : c < q.cr ? q.sl : q.el) - (uint32_t)(KA_KEYS * c);
@@ -193,7 +196,8 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = sm.tmem_base;
+  // all 512 columns: an allocation of them begins at column 0
+  if (sm.tmem_base != 0 && tid == 0) report(p.hdr, CSA2_ERR_CUDA, 2);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const int64_t base = p.base_pos[b];
@@ -208,49 +212,56 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   // Chunk c (counted from c_lo) uses K buffer c % 3; it is that buffer's use c / 3.
   if (warp == KA_MMA_WARP) {
     // ================= MMAs (the whole warp runs the loop, one lane issues)
+    // An MMA takes its addresses and descriptors from uniform registers.  They stay there when
+    // the compiler sees that every lane has the same: TMEM addresses are constants (the CTA has
+    // all of TMEM, from column 0), and what the chunks follow from is read from memory, so it
+    // goes through a reduction over the warp, whose result is uniform.
     constexpr uint32_t idesc_s = F16 ? tc::idesc_f16(H, 0, 0, 0) : tc::idesc_bf16(H, 0, 0, 0);       // + N
     constexpr uint32_t idesc_o = F16 ? tc::idesc_f16(H, 256, 0, 1) : tc::idesc_bf16(H, 256, 0, 1);
     const uint64_t k_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
     const uint64_t v_d = tc::smem_desc(tc::smem_u32(smem), KA_COL, 1024, tc::SW_128B);
     const uint32_t leader = tc::elect_one();
-    bool ok = n_ch > 0 ? ka_wait(&sm.q_moved, 0, sm, p.hdr, 40) : true;
+    KaRun run;                                        // q, uniform
+    run.cw = (int)ka_uniform((uint32_t)q.cw);
+    run.cr = (int)ka_uniform((uint32_t)q.cr);
+    run.wl = ka_uniform(q.wl);
+    run.sl = ka_uniform(q.sl);
+    run.el = ka_uniform(q.el);
+    const int n = (int)ka_uniform((uint32_t)n_ch);
+    bool ok = n > 0 ? ka_wait(&sm.q_moved, 0, sm, p.hdr, 40) : true;
     int sb = 0, su = 0, ob = 0;                       // K buffer and use of the next S, K buffer of the next O
     auto scores = [&](int c) {
-      const uint32_t idesc = idesc_s | (uint32_t)((ka_keys(q, c) + 15) >> 4 << 1) << 17;
-      const uint32_t s = tmem + KA_S_COL + 64 * (c & 1);
+      const uint32_t idesc = idesc_s | (uint32_t)((ka_keys(run, c) + 15) >> 4 << 1) << 17;
+      const uint32_t s = KA_S_COL + 64 * (c & 1);
 #pragma unroll 1
       for (int h = 0; h < 2; h++) {
         ok = ok && ka_wait(&sm.full[sb][h], su, sm, p.hdr, 41);
         tc::fence_after_sync();
-        if (ok) {
-          const uint64_t ka = k_d + (uint32_t)((2 * sb + h) * (KA_HALF >> 4));
-          const uint32_t lanes = h * KA_HALF_LANES;
+        const uint64_t ka = k_d + (uint32_t)((2 * sb + h) * (KA_HALF >> 4));
+        const uint32_t lanes = h * KA_HALF_LANES;
 #pragma unroll
-          for (int i = 0; i < 16; i++)
-            tc::mma_f16_ts_warp(leader, s + lanes, tmem + KA_Q_COL + lanes + 8 * i,
-                                ka + ((uint32_t)((i >> 2) * KA_COL + (i & 3) * 32) >> 4), idesc, i ? 1u : 0u);
-        }
+        for (int i = 0; i < 16; i++)
+          tc::mma_f16_ts_warp(leader, s + lanes, KA_Q_COL + lanes + 8 * i,
+                              ka + ((uint32_t)((i >> 2) * KA_COL + (i & 3) * 32) >> 4), idesc, i ? 1u : 0u);
       }
       tc::commit_warp(leader, &sm.s_full[c & 1]);
       if (++sb == KA_BUFS) sb = 0, su++;
     };
-    if (n_ch > 0) scores(0);
-    for (int c = 0; c < n_ch; c++) {
-      if (c + 1 < n_ch) scores(c + 1);
-      const int steps = (ka_keys(q, c) + 15) >> 4;
+    if (n > 0) scores(0);
+    for (int c = 0; c < n; c++) {
+      if (c + 1 < n) scores(c + 1);
+      const int steps = (ka_keys(run, c) + 15) >> 4;
       ok = ok && ka_wait(&sm.p_ready[c & 1], c >> 1, sm, p.hdr, 42);
       tc::fence_after_sync();
-      if (ok) {
 #pragma unroll 1
-        for (int h = 0; h < 2; h++) {
-          const uint64_t va = v_d + (uint32_t)((2 * ob + h) * (KA_HALF >> 4));
-          const uint32_t lanes = h * KA_HALF_LANES;
+      for (int h = 0; h < 2; h++) {
+        const uint64_t va = v_d + (uint32_t)((2 * ob + h) * (KA_HALF >> 4));
+        const uint32_t lanes = h * KA_HALF_LANES;
 #pragma unroll
-          for (int ks = 0; ks < KA_KEYS / 16; ks++)
-            if (ks < steps)
-              tc::mma_f16_ts_warp(leader, tmem + KA_O_COL + lanes, tmem + KA_S_COL + 64 * (c & 1) + lanes + 8 * ks,
-                                  va + (uint32_t)(ks * (2048 >> 4)), idesc_o, (c || ks) ? 1u : 0u);
-        }
+        for (int ks = 0; ks < KA_KEYS / 16; ks++)
+          if (ks < steps)
+            tc::mma_f16_ts_warp(leader, KA_O_COL + lanes, KA_S_COL + 64 * (c & 1) + lanes + 8 * ks,
+                                va + (uint32_t)(ks * (2048 >> 4)), idesc_o, (c || ks) ? 1u : 0u);
       }
       tc::commit_warp(leader, &sm.free_[ob]);
       if (++ob == KA_BUFS) ob = 0;
@@ -443,7 +454,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           w[4 * u + 2] = F16 ? bf16x2_to_f16x2(x.z) : x.z;
           w[4 * u + 3] = F16 ? bf16x2_to_f16x2(x.w) : x.w;
         }
-        tmem_st32(tmem + quarter + KA_Q_COL + 32 * g, w);
+        tmem_st32(quarter + KA_Q_COL + 32 * g, w);
       }
       tc::tmem_wait_st();
       tc::fence_proxy_async_smem();                   // the buffer goes to copies and stores of others
@@ -454,7 +465,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     int ob = 0, ou = 0;                               // K buffer and use of the chunk before
     for (int c = 0; c < n_ch; c++) {
       const int n = ka_keys(q, c) - 32 * half;   // this lane takes keys 32 half ..: n of them are there
-      const uint32_t s_addr = tmem + quarter + KA_S_COL + 64 * (c & 1);
+      const uint32_t s_addr = quarter + KA_S_COL + 64 * (c & 1);
       ok = ok && ka_wait(&sm.s_full[c & 1], c >> 1, sm, p.hdr, 49);
       tc::fence_after_sync();
       float v[32];
@@ -496,10 +507,10 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 #pragma unroll 1
         for (int g = 0; g < D / 2; g += 32) {
           uint32_t o[32];
-          tmem_ld32(tmem + quarter + KA_O_COL + g, o);
+          tmem_ld32(quarter + KA_O_COL + g, o);
 #pragma unroll
           for (int x = 0; x < 32; x++) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-          tmem_st32(tmem + quarter + KA_O_COL + g, o);
+          tmem_st32(quarter + KA_O_COL + g, o);
         }
       }
       if (c > 0 && ++ob == KA_BUFS) ob = 0, ou++;
@@ -548,7 +559,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
           uint32_t o[32];
-          if (n_ch > 0) tmem_ld32(tmem + quarter + KA_O_COL + g + c, o);
+          if (n_ch > 0) tmem_ld32(quarter + KA_O_COL + g + c, o);
 #pragma unroll
           for (int x = 0; x < 4; x++) {
             float f[8];
@@ -579,7 +590,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 #pragma unroll 1
         for (int g = 0; g < D / 2; g += 32) {
           uint32_t o[32];
-          tmem_ld32(tmem + quarter + KA_O_COL + g, o);
+          tmem_ld32(quarter + KA_O_COL + g, o);
 #pragma unroll
           for (int x = 0; x < 8; x++)
             out[(g / 4 + x) * H] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
@@ -595,7 +606,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     for (int i = 0; i < 1000; i++) __nanosleep(1000);
   if (warp == KA_MMA_WARP) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, KA_TMEM_COLS);
+    tc::tmem_dealloc(0u, KA_TMEM_COLS);
   }
 }
 
