@@ -376,18 +376,18 @@ def _tokens(name: str, t, shape, inner, device):
     return t.data_ptr()
 
 
-def _call(name: str, device, stream, *args):
-    """The library's `name` on `stream` (None: the device's current one), with `device` current."""
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) with `device` current; stream None: the device's current one, whose
+    handle is asked for directly (a stream object costs as much as the launch)."""
     import torch
-    fn = getattr(_lib or load(), name)
-    handle = (stream or torch.cuda.current_stream(device)).cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == device.index:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(device):
             status = fn(*args, handle)
     if status != 0:
-        raise Csa2Error(name, status)
+        raise Csa2Error(fn.__name__, status)
 
 
 def qk_norm_rope(pos, rope_cs, ws: Workspace, *, q=None, q_weight=None, q_out=None, k=None, k_weight=None, rows=None,
@@ -414,7 +414,7 @@ def qk_norm_rope(pos, rope_cs, ws: Workspace, *, q=None, q_weight=None, q_out=No
         sl = None if k_slot is None else _int64("k_slot", k_slot, (T,), dev)
     a = QkArgs(T, _int64("pos", pos, (T,), dev), _float32("rope_cs", rope_cs, (table, D_ROPE // 2, 2), dev), table,
                float(eps), fp8, qa, qs or 0, qw, qo, ka, ks or 0, kw, ro, n_rows, sl)
-    _call("csa2_qk_norm_rope", dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
+    _call((_lib or load()).csa2_qk_norm_rope, dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
 
 
 def window_attn_workspace_size(B: int, Q: int, W: int, n_sink: int) -> int:
@@ -435,7 +435,7 @@ def window_attn(q, rows, swa_base_pos, q_pos, scale: float, out, ws: Workspace, 
                    _rows("sinks", sinks, (B, n, D_LATENT), dev) if n else None, _bits16("out", out, shape, dev),
                    None if lse is None else _float32("lse", lse, (B, Q, N_HEADS), dev),
                    1 if rows.element_size() == 1 else 0)
-    _call("csa2_window_attn", dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
+    _call((_lib or load()).csa2_window_attn, dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
 
 
 def dense_attn_workspace_size(B: int, Q: int, max_n: int) -> int:
@@ -456,4 +456,4 @@ def dense_attn(cache: Cache, q, swa, swa_base_pos, q_pos, scale: float, out, ws:
                   _rows("swa", swa, (B, S, D_LATENT), dev), _int64("swa_base_pos", swa_base_pos, (B,), dev),
                   _bits16("out", out, shape, dev), None if lse is None else _float32("lse", lse, (B, Q, N_HEADS), dev),
                   1 if swa.element_size() == 1 else 0)
-    _call("csa2_dense_attn", dev, stream, ctypes.byref(cache.struct()), ctypes.byref(a), ws.ptr, ws.nbytes)
+    _call((_lib or load()).csa2_dense_attn, dev, stream, ctypes.byref(cache.struct()), ctypes.byref(a), ws.ptr, ws.nbytes)
