@@ -19,7 +19,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libcsa2.so")
 
 SOURCES = ["csa2_api.cu", "cache_write.cu", "index_score.cu", "reindex.cu", "topk.cu", "attention.cu", "hisa.cu",
-           "norm_rope.cu", "keys_attention.cu"]
+           "norm_rope.cu", "keys_attention.cu", "window_attention.cu"]
 # cache_write.cu and hisa.cu keep the binary32 order written in the source: no
 # implicit multiply-add contraction anywhere in those units.
 EXTRA = {"cache_write.cu": ["-fmad=false"], "hisa.cu": ["-fmad=false"]}

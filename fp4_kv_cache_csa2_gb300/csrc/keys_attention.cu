@@ -721,9 +721,15 @@ static cudaError_t keys_launch(const KeysParams& p, int64_t BQ, const CUtensorMa
   return cudaLaunchKernelEx(&cc, keys_combine_kernel, (const float*)p.part, p.split, p.out, p.lse);
 }
 
+// Short windows of many neighbouring queries: RULE
+static bool keys_in_ring(const KeysParams& p, int64_t BQ) {
+  return !p.main_kv && window_ring_fits(p.W, p.n_sink) && p.Q >= 16 && BQ >= 4 * KA_SMS;
+}
+
 cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* part, cudaStream_t stream) {
   const int64_t BQ = (int64_t)B * p.Q;
   if (BQ == 0) return cudaSuccess;
+  if (keys_in_ring(p, BQ)) return launch_window_ring(p, B, stream);
   p.split = keys_split(BQ, chunks);
   p.part = reinterpret_cast<float*>(part);
   CUtensorMap mq, mr, ms;

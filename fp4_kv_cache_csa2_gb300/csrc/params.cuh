@@ -157,6 +157,10 @@ cudaError_t launch_hisa_view(const HvParams& p, cudaStream_t stream);
 // `part`: keys_part_bytes(B * Q, chunks) of scratch
 constexpr int KEYS_CHUNK = 64;
 cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* part, cudaStream_t stream);
+// The same for a call without cache entries whose windows are short enough (window_ring_fits):
+// many queries in a row over a ring of rows in shared memory
+cudaError_t launch_window_ring(const KeysParams& p, int B, cudaStream_t stream);
+bool window_ring_fits(int64_t W, int n_sink);
 size_t keys_part_bytes(int64_t BQ, int64_t chunks);
 cudaError_t launch_qk_norm_rope(const QkParams& p, cudaStream_t stream);
 

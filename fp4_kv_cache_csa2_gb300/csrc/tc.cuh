@@ -146,6 +146,14 @@ __device__ __forceinline__ void mma_f16_ts_warp(uint32_t leader, uint32_t d_tmem
                :: "r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
 }
 
+// The same with A in shared memory.
+__device__ __forceinline__ void mma_f16_ss_warp(uint32_t leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+               " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+               :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
+}
+
 __device__ __forceinline__ void commit_warp(uint32_t leader, uint64_t* bar) {
   asm volatile("{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
                " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"

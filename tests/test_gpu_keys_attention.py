@@ -166,6 +166,71 @@ def test_window_split_over_ctas_and_many_queries():
     verify_window(7, 1, 640, 260, 5, False, pos, np.array([0]), 640)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,Q,W,n_sink,start", [
+    (1, 700, 128, 4, 0), (1, 609, 1, 0, 5), (1, 640, 1, 3, 1), (2, 333, 31, 0, 0), (3, 205, 100, 59, 40),
+    (1, 611, 159, 0, 1000), (1, 650, 157, 2, 100), (20, 31, 64, 5, 3), (1, 620, 127, 1, 1 << 33)])
+def test_window_many_queries(fp8, B, Q, W, n_sink, start):
+    """Short windows of many neighbouring queries, with padding behind the shorter sequences."""
+    pos = start + np.arange(Q)[None, :] + 7 * np.arange(B)[:, None]
+    base = np.maximum(0, pos[:, 0] - W + 1)
+    for b in range(1, B):
+        pos[b, Q - 3 * b:] = -1
+    verify_window(16, B, Q, W, n_sink, fp8, pos, base, Q + W - 1 + 3)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("W,n_sink", [(40, 4), (128, 16), (159, 0)])
+def test_window_many_queries_in_any_order(fp8, W, n_sink):
+    """The same with jumps, repeated and descending positions, padding and rows that are missing."""
+    g = synth.rng(17)
+    pos = g.integers(0, 800, (2, 320))
+    pos[0, 40:200] = 300 + np.arange(160)
+    pos[0, 200:260] = 500 - np.arange(60)
+    pos[1, 10:50] = np.repeat(np.arange(600, 620), 2)
+    pos[1, 60:90] = 100 + 3 * np.arange(30)
+    pos[1, 100:140] = np.where(np.arange(40) % 2, 200 + np.arange(40), 600 + np.arange(40))
+    pos[g.random((2, 320)) < 0.1] = -1
+    verify_window(18, 2, 320, W, n_sink, fp8, pos, np.array([0, 0]), 800)
+    verify_window(19, 2, 320, W, n_sink, fp8, pos, np.array([250, -100]), 500, status=6)
+
+
+def test_window_many_queries_not_finite():
+    """Rows and sinks that are not finite among many queries: only who sees them is touched."""
+    g = synth.rng(20)
+    for fp8, bads in ((False, (NAN_BF16, INF_BF16, 0xFF80)), (True, (NAN_E4M3, 0xFF))):
+        for W, n_sink in ((32, 4), (128, 4)):
+            Q = 620
+            pos = np.arange(Q)[None, :]
+            rows, sinks, q = draw_rows(g, fp8, 1, Q), draw_rows(g, fp8, 1, n_sink), synth.main_queries(g, 1, Q)
+            where = [(0, 3), (200, 7), (201, 500), (333, 0), (430, 511), (619, 5)]
+            for n, (r, c) in enumerate(where):
+                rows[0, r, c] = bads[n % len(bads)]
+            sinks[0, 2, 9] = bads[0]                          # seen from position W + 2 on
+            o, l = run_window(q, rows, np.zeros(1, np.int64), pos, W, sinks)
+            rv = ref.row_values(rows[0])
+            for t in list(range(W + 2)) + [r + d for r, _ in where for d in (-2, -1)]:
+                if not 0 <= t < Q or t >= W + 2:
+                    continue
+                keys = ref.window_keys(rv, 0, t, W, ref.row_values(sinks[0]))
+                if np.all(np.isfinite(keys)):
+                    check(o[0, t], l[0, t], ref.bf16(q[0, t]), keys, SCALE, ref.U_BF16, t)
+                else:
+                    assert np.any(np.isnan(o[0, t]))
+            assert np.all(np.any(np.isnan(o[0, W + 2:]), axis=(1, 2)))
+            # without the sink: the windows between the bad rows
+            o, l = run_window(q, rows, np.zeros(1, np.int64), pos, W, None)
+            seen = 0
+            for t in range(Q):
+                keys = ref.window_keys(rv, 0, t, W)
+                if np.all(np.isfinite(keys)):
+                    seen += 1
+                    check(o[0, t], l[0, t], ref.bf16(q[0, t]), keys, SCALE, ref.U_BF16, t)
+                else:
+                    assert np.any(np.isnan(o[0, t]))
+            assert seen > 60
+
+
 def run_dense(cache, q, rows, base, pos, max_n, scale=SCALE, status=0, stream=None):
     B, Q = pos.shape
     out = torch.full((B, Q, 64, 512), 0x4242, dtype=torch.int16, device="cuda")
