@@ -59,6 +59,8 @@ struct WaJob {
 struct WaSmall {
   WaJob job[WA_JOBS];
   float2 state[2][WA_ROWS];           // 1 / sum and lse of each row, of every second job
+  uint32_t next_bq[WA_JOBS];          // first query of a job to come, ~0: none, for the copies of Q
+  uint64_t told[WA_JOBS];             // it is written
   uint64_t job_ready[WA_JOBS];        // the job is written and its slots are filled (a ring warp each)
   uint64_t job_free[WA_JOBS];         // every reader is done with it
   uint64_t q_full[WA_STAGES], q_free[WA_STAGES];
@@ -68,7 +70,7 @@ struct WaSmall {
   int err, dirty;
 };
 constexpr int WA_SMEM = WA_OFF_SMALL + (int)sizeof(WaSmall);
-constexpr int WA_READERS = 1 + 1 + 1 + 4 + 4;             // copy, S, O, softmax, output warps
+constexpr int WA_READERS = 1 + 1 + 1 + 4 + 4;             // of a job: copy, S, O, softmax, output warps
 static_assert(WA_SMEM <= 227 * 1024, "shared memory per CTA");
 static_assert(WA_O_COL + 64 * WA_O_BUFS <= 512, "TMEM columns");
 
@@ -147,6 +149,7 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
   if (warp == WA_S_WARP) tc::tmem_alloc(&sm.tmem_base, 512);
   if (tid == 0) {
     for (int i = 0; i < WA_JOBS; i++) {
+      tc::bar_init(&sm.told[i], 1);
       tc::bar_init(&sm.job_ready[i], WA_RING / 32);
       tc::bar_init(&sm.job_free[i], WA_READERS);
     }
@@ -250,13 +253,16 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
     int stage = 0;
     uint32_t use = 0;
     for (uint32_t j = 0;; j++) {
-      const WaJob job = next_job(j);
-      if (job.write < 0) break;
+      // told before the job's slots are filled: Q is on its way while the ring's rows come
+      ok = ok && wa_wait(&sm.told[j % WA_JOBS], j / WA_JOBS, sm, p.hdr, 59);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      const uint32_t bq = sm.next_bq[j % WA_JOBS];
+      if (bq == ~0u || !ok) break;
       for (int c = 0; c < 8; c++) {
         if (use > 0) ok = ok && wa_wait(&sm.q_free[stage], use - 1, sm, p.hdr, 65);
         if (lane == 0) {
           tc::bar_arrive_expect_tx(&sm.q_full[stage], WA_QCOL);
-          tc::tma_load_2d(smem + WA_OFF_Q + stage * WA_QCOL, &map_q, c * 64, (int32_t)(job.bq * H), &sm.q_full[stage]);
+          tc::tma_load_2d(smem + WA_OFF_Q + stage * WA_QCOL, &map_q, c * 64, (int32_t)(bq * H), &sm.q_full[stage]);
         }
         if (++stage == WA_STAGES) stage = 0, use++;
       }
@@ -267,70 +273,31 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
     const int rt = tid - 32 * WA_RING_WARP, rw = rt >> 5;
     const int R = slots - p.n_sink;                   // window slots
     const size_t row_bytes = p.rows_fp8 ? D : 2 * D;
-    uint32_t j = 0;                                   // jobs so far
-    // rows [first, first + n) of a buffer to slots: row first + i to slot0 + i, around `around`
-    // slots from `begin` on.  A row that is not finite is left out (and told) unless `any`
-    auto load = [&](const uint8_t* src, int n, int begin, int slot0, int around, bool any) {
-#pragma unroll 1
-      for (int i0 = 4 * rw; i0 < n; i0 += 4 * (WA_RING / 32)) {
-        uint4 v[4][2];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          if (i0 + i >= n) continue;
-          const uint4* s = reinterpret_cast<const uint4*>(src + (size_t)(i0 + i) * row_bytes);
-          if (p.rows_fp8) {                           // 16 dims a lane
-            const uint4 w = __ldg(s + lane);
-            const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-            uint32_t o[8];
-#pragma unroll
-            for (int x = 0; x < 4; x++) {
-              o[2 * x] = wa_f16x2_to_bf16x2(e4m3x2_to_f16x2(e[x]));
-              o[2 * x + 1] = wa_f16x2_to_bf16x2(e4m3x2_to_f16x2(e[x] >> 16));
-            }
-            v[i][0] = make_uint4(o[0], o[1], o[2], o[3]);
-            v[i][1] = make_uint4(o[4], o[5], o[6], o[7]);
-          } else {                                    // 8 dims of each half
-            v[i][0] = __ldg(s + lane);
-            v[i][1] = __ldg(s + 32 + lane);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          if (i0 + i >= n) continue;
-          const bool bad = __any_sync(0xFFFFFFFFu, wa_not_finite(v[i][0]) || wa_not_finite(v[i][1]));
-          if (bad && !any) {
-            if (lane == 0) sm.dirty = 1;
-            continue;
-          }
-          int slot = slot0 + i0 + i;
-          if (slot >= begin + around) slot -= around;
-          const int u0 = p.rows_fp8 ? 2 * lane : lane, u1 = p.rows_fp8 ? 2 * lane + 1 : 32 + lane;   // 16-byte units
-          unsigned char* dst = smem + slot * 128;
-          *reinterpret_cast<uint4*>(dst + (u0 >> 3) * WA_KCOL + (((u0 ^ slot) & 7) << 4)) = v[i][0];
-          *reinterpret_cast<uint4*>(dst + (u1 >> 3) * WA_KCOL + (((u1 ^ slot) & 7) << 4)) = v[i][1];
-        }
-      }
-    };
+    uint32_t j = 0;                                   // jobs published, and (told ones) announced
+    uint32_t announced = 0;
     auto pv_wait = [&](uint32_t job) { ok = ok && wa_wait(&sm.pv_done[job & 1], job >> 1, sm, p.hdr, 66); };
-    // all tiles at work are done with the ring
-    auto settle = [&]() {
-      if (j >= 2) pv_wait(j - 2);
-      if (j >= 1) pv_wait(j - 1);
-    };
-    auto publish = [&](uint32_t bq, int write, const WaQuery* q, int mask) {
-      tc::fence_proxy_async_smem();
-      if (j >= WA_JOBS) ok = ok && wa_wait(&sm.job_free[j % WA_JOBS], j / WA_JOBS - 1, sm, p.hdr, 67);
+    // the first query of the next job, as soon as it is known
+    auto announce = [&](uint32_t bq) {
+      if (announced >= WA_JOBS)
+        ok = ok && wa_wait(&sm.job_free[announced % WA_JOBS], announced / WA_JOBS - 1, sm, p.hdr, 67);
       if (rt == 0) {
+        sm.next_bq[announced % WA_JOBS] = bq;
+        tc::bar_arrive(&sm.told[announced % WA_JOBS]);
+      }
+      announced++;
+    };
+    auto publish = [&](uint32_t bq, int write, int sn0, int r0, int n0, int sn1, int r1, int n1) {
+      tc::fence_proxy_async_smem();
+      if (rt == 0) {                                  // the slot is free: announce waited for it
         WaJob& job = sm.job[j % WA_JOBS];
         job.bq = bq;
         job.write = write;
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const bool on = write >= 0 && (mask >> i & 1) != 0;
-          job.sn[i] = on ? q[i].sn : 0;
-          job.s0[i] = on ? p.n_sink + q[i].r0 % R : 0;
-          job.cnt[i] = on ? q[i].wn : 0;
-        }
+        job.sn[0] = sn0;
+        job.s0[0] = p.n_sink + r0 % R;
+        job.cnt[0] = n0;
+        job.sn[1] = sn1;
+        job.s0[1] = p.n_sink + r1 % R;
+        job.cnt[1] = n1;
       }
       __syncwarp();
       if (lane == 0) tc::bar_arrive(&sm.job_ready[j % WA_JOBS]);
@@ -340,89 +307,138 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
     int held_b = -1, rl = 0, rh = 0, ns = 0;          // the ring: rows [rl, rh) and sinks [0, ns) of sequence held_b
     bool stale = false;                               // it may hold rows that are not finite
     int before = 0;                                   // first row that the job before sees
-    auto fetch = [&](int64_t k, int64_t* t, int64_t* base) {
-      if (k >= k_hi) return;
-      const int b = (int)(k / pairs), i = 2 * (int)(k % pairs);
-      t[0] = p.q_pos[(int64_t)b * p.Q + i];
-      t[1] = i + 1 < p.Q ? p.q_pos[(int64_t)b * p.Q + i + 1] : -1;
-      *base = p.base_pos[b];
+    int b = (int)(k_lo / pairs), i0 = 2 * (int)(k_lo - (int64_t)b * pairs);
+    // positions of the next tile, loaded one tile ahead
+    int64_t nt0 = -1, nt1 = -1, nbase = 0;
+    auto fetch = [&](int fb, int fi) {
+      const int64_t at = (int64_t)fb * p.Q + fi;
+      nt0 = p.q_pos[at];
+      nt1 = fi + 1 < p.Q ? p.q_pos[at + 1] : -1;
+      nbase = p.base_pos[fb];
     };
-    int64_t nt[2] = {-1, -1}, nbase = 0;
-    fetch(k_lo, nt, &nbase);
+    if (k_lo < k_hi) fetch(b, i0);
     for (int64_t k = k_lo; k < k_hi; k++) {
-      const int b = (int)(k / pairs), i0 = 2 * (int)(k % pairs);
       const uint32_t bq = (uint32_t)b * (uint32_t)p.Q + (uint32_t)i0;
       const int have = i0 + 1 < p.Q ? 3 : 1;
-      WaQuery q[2];
-#pragma unroll
-      for (int i = 0; i < 2; i++) q[i] = wa_query(p, nt[i], nbase, rt == 0);
-      fetch(k + 1, nt, &nbase);
+      announce(bq);
+      const WaQuery q0 = wa_query(p, nt0, nbase, rt == 0), q1 = wa_query(p, nt1, nbase, rt == 0);
       const uint8_t* rows = p.rows + (size_t)b * (size_t)p.S * row_bytes;
       const uint8_t* sinks = p.sinks + (size_t)b * (size_t)p.n_sink * row_bytes;
+      const int tile_b = b;
+      i0 += 2;
+      if (i0 >= p.Q) i0 = 0, b++;
+      if (k + 1 < k_hi) fetch(b, i0);
       // both queries at once when their rows together fit the ring, else one after the other
-      const int lo = q[0].wn == 0 ? q[1].r0 : (q[1].wn == 0 ? q[0].r0 : min(q[0].r0, q[1].r0));
-      const int hi = max(q[0].wn ? q[0].r0 + q[0].wn : 0, q[1].wn ? q[1].r0 + q[1].wn : 0);
-      const bool joint = q[0].wn == 0 || q[1].wn == 0 || hi - lo <= R;
-      int todo = joint ? 1 : 2;
-      for (int part = 0; part < todo; part++) {
-        const int mask = joint ? 3 : 1 << part;
-        const int L = joint ? lo : (part ? q[1].r0 : q[0].r0);
-        const int E = joint ? hi : L + (part ? q[1].wn : q[0].wn);      // rows [L, E)
-        const int NS = joint ? max(q[0].sn, q[1].sn) : (part ? q[1].sn : q[0].sn);
-        if (j >= 2) pv_wait(j - 2);
-        if (stale) {                                  // what was left out of an earlier job's view may lie there
-          settle();
-          for (int i = rt; i < 8 * WA_KCOL / 16; i += WA_RING) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
-          named_sync(1, WA_RING);
-          stale = false;
-          held_b = -1;
-        }
-        if (b != held_b) {
-          settle();
-          held_b = b;
+      const int lo = q0.wn == 0 ? q1.r0 : (q1.wn == 0 ? q0.r0 : min(q0.r0, q1.r0));
+      const int hi = max(q0.wn ? q0.r0 + q0.wn : 0, q1.wn ? q1.r0 + q1.wn : 0);
+      const bool joint = q0.wn == 0 || q1.wn == 0 || hi - lo <= R;
+      int todo = joint ? 3 : 1 | 2 << 2;              // two bits a job: the queries it takes
+      bool exact = false, first = true;               // exact: on zeros and what its query sees
+      while (todo != 0) {
+        const int mask = todo & 3;
+        todo >>= 2;
+        if (!first) announce(bq);
+        first = false;
+        const int L = mask == 3 ? lo : (mask == 2 ? q1.r0 : q0.r0);
+        const int E = mask == 3 ? hi : L + (mask == 2 ? q1.wn : q0.wn);      // rows [L, E)
+        const int NS = mask == 3 ? max(q0.sn, q1.sn) : (mask == 2 ? q1.sn : q0.sn);
+        // what may be written when: after every tile at work, or after the last but one, or (a
+        // new row takes a slot that the job before sees) after the one before
+        bool all = false, last = false;
+        if (exact || stale || tile_b != held_b) {
+          all = true;
+          held_b = exact ? -1 : tile_b;
           rl = rh = L;
           ns = 0;
         } else if (E > L && (L < rl || L > rh)) {
-          settle();
+          all = true;
           rl = rh = L;
-        } else if (E > rh && E - R > before) {         // a new row takes a slot that the job before sees
-          if (j >= 1) pv_wait(j - 1);
+        } else {
+          last = E > rh && E - R > before;
         }
-        if (E > rh) {
-          const int from = max(rh, E - R);
-          load(rows + (size_t)from * row_bytes, E - from, p.n_sink, p.n_sink + from % R, R, false);
-          rh = E;
-          rl = max(rl, E - R);
-        }
-        if (NS > ns) {
-          load(sinks + (size_t)ns * row_bytes, NS - ns, 0, ns, WA_SLOTS, false);
-          ns = NS;
-        }
-        named_sync(1, WA_RING);
-        const bool dirty = *(volatile int*)&sm.dirty != 0;
-        if (!dirty) {
-          publish(bq, mask & have, q, mask);
-          before = L;
-          continue;
-        }
-        // each query of this part alone, with what it sees as it is
-        for (int i = 0; i < 2; i++) {
-          if ((mask & have) >> i & 1) {
-            const WaQuery one = i ? q[1] : q[0];
-            settle();
+        const bool zero = exact || stale;
+        stale = exact;
+        bool open = false;                            // whether that wait is over
+        auto gate = [&]() {
+          if (open) return;
+          open = true;
+          if (j >= 2) pv_wait(j - 2);
+          if (j >= 1 && (all || last)) pv_wait(j - 1);
+          if (zero) {
             for (int x = rt; x < 8 * WA_KCOL / 16; x += WA_RING) reinterpret_cast<uint4*>(smem)[x] = make_uint4(0u, 0u, 0u, 0u);
             named_sync(1, WA_RING);
-            load(rows + (size_t)one.r0 * row_bytes, one.wn, p.n_sink, p.n_sink + one.r0 % R, R, true);
-            load(sinks, one.sn, 0, 0, WA_SLOTS, true);
             if (rt == 0) sm.dirty = 0;
             named_sync(1, WA_RING);
-            publish(bq, 1 << i, q, 1 << i);
+          }
+        };
+        // new rows [rh, E) to their window slots, new sinks [ns, NS) to theirs.  A row that is not
+        // finite is left out (and told) unless the job is exact
+        const int n_row = max(E - rh, 0), n_all = n_row + max(NS - ns, 0);
+        const int slot_r = p.n_sink + rh % R;
+#pragma unroll 1
+        for (int x0 = 0; x0 < n_all; x0 += 4 * (WA_RING / 32)) {
+          uint4 v[4][2];
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int x = x0 + 4 * i + rw;            // neighbouring rows in different warps
+            v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (x < n_all) {
+              const uint4* src = reinterpret_cast<const uint4*>(x < n_row ? rows + (size_t)(rh + x) * row_bytes
+                                                                          : sinks + (size_t)(ns + x - n_row) * row_bytes);
+              v[i][0] = __ldg(src + lane);            // E4M3: 16 dims a lane; bf16: 8 dims of each half
+              if (!p.rows_fp8) v[i][1] = __ldg(src + 32 + lane);
+            }
+          }
+          gate();
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int x = x0 + 4 * i + rw;
+            if (x >= n_all) continue;
+            uint4 lo4 = v[i][0], hi4 = v[i][1];
+            if (p.rows_fp8) {
+              const uint32_t e[4] = {lo4.x, lo4.y, lo4.z, lo4.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int y = 0; y < 4; y++) {
+                o[2 * y] = wa_f16x2_to_bf16x2(e4m3x2_to_f16x2(e[y]));
+                o[2 * y + 1] = wa_f16x2_to_bf16x2(e4m3x2_to_f16x2(e[y] >> 16));
+              }
+              lo4 = make_uint4(o[0], o[1], o[2], o[3]);
+              hi4 = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            if (!exact && __any_sync(0xFFFFFFFFu, wa_not_finite(lo4) || wa_not_finite(hi4))) {
+              if (lane == 0) sm.dirty = 1;
+              continue;
+            }
+            int slot = slot_r + x;
+            if (slot >= slots) slot -= R;             // around the ring
+            if (x >= n_row) slot = ns + x - n_row;
+            const int u0 = p.rows_fp8 ? 2 * lane : lane, u1 = p.rows_fp8 ? 2 * lane + 1 : 32 + lane;   // 16-byte units
+            unsigned char* dst = smem + slot * 128;
+            *reinterpret_cast<uint4*>(dst + (u0 >> 3) * WA_KCOL + (((u0 ^ slot) & 7) << 4)) = lo4;
+            *reinterpret_cast<uint4*>(dst + (u1 >> 3) * WA_KCOL + (((u1 ^ slot) & 7) << 4)) = hi4;
           }
         }
-        stale = true;
+        gate();
+        rh = max(rh, E);
+        rl = max(rl, E - R);
+        ns = max(ns, NS);
+        named_sync(1, WA_RING);
+        const bool dirty = *(volatile int*)&sm.dirty != 0;
+        if (dirty && !exact) {                        // each query of this job alone, with what it sees as it is
+          const int singles = (mask & have) == 3 ? 1 | 2 << 2 : mask & have;
+          todo = singles | todo << (singles > 3 ? 4 : 2);
+          exact = true;
+          first = true;                               // the announced job is the first of them
+          continue;
+        }
+        before = L;
+        const bool on0 = (mask & 1) != 0, on1 = (mask & 2) != 0;
+        publish(bq, mask & have, on0 ? q0.sn : 0, q0.r0, on0 ? q0.wn : 0, on1 ? q1.sn : 0, q1.r0, on1 ? q1.wn : 0);
       }
     }
-    publish(0, -1, nullptr, 0);
+    announce(~0u);
+    publish(0, -1, 0, 0, 0, 0, 0, 0);
   } else if (warp >= WA_OUT_WARP) {
     // ================= output: thread = row
     const int ow = warp - WA_OUT_WARP, i = ow >> 1;   // query
