@@ -22,7 +22,7 @@
 // 16h .. 16h + 15 (256 columns of O, 128 of Q, twice 64 of S), P lies in both.  With Q and P
 // in TMEM a product reads only the K tile from shared memory, 16 of its 32 cycles at
 // N = 64 (with Q there too it takes all 32, and the fill's stores come on top: 3100
-// cycles a chunk instead of RESULT).
+// cycles a chunk instead of 2300).
 // Operands: F16 (calls with cache entries or E4M3 rows) keeps every dequantised FP4
 // value (at most 6 significant bits, 2^-10 .. 2688) and every E4M3 value exactly and
 // rounds q and bf16 window rows to f16, exact inside [2^-14, 65504], with P to 11
@@ -370,7 +370,10 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       }
     };
     uint32_t staged = 0;                              // uses of the staging area
+    // the reads of the staged bytes are done, before a copy (the asynchronous proxy) writes there
+    // again: without the fence the arrival may overtake reads whose values are not used yet
     auto stage_read = [&]() {
+      tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::bar_arrive(&sm.stage_free);
     };
@@ -721,9 +724,13 @@ static cudaError_t keys_launch(const KeysParams& p, int64_t BQ, const CUtensorMa
   return cudaLaunchKernelEx(&cc, keys_combine_kernel, (const float*)p.part, p.split, p.out, p.lse);
 }
 
-// Short windows of many neighbouring queries: RULE
+// Calls that window_attention.cu takes: short windows of at least four queries a sequence, and
+// enough of them that a CTA has several tiles (its first one waits for a whole window of rows).
+// Window 128, 4 sinks, bf16, us (this file's kernel / the ring's): 1 x 64 queries 8.5 / 19.1, 64 x 8
+// 33.7 / 35.9, 152 x 4 40.3 / 26.1, 1 x 608 36.2 / 23.7, 1 x 2432 148 / 68; with one or two queries
+// a sequence a tile brings a window for every query: 608 x 1 46.8 / 86.9, 300 x 2 42.7 / 46.3.
 static bool keys_in_ring(const KeysParams& p, int64_t BQ) {
-  return !p.main_kv && window_ring_fits(p.W, p.n_sink) && p.Q >= 16 && BQ >= 4 * KA_SMS;
+  return !p.main_kv && window_ring_fits(p.W, p.n_sink) && p.Q >= 4 && BQ >= 3 * KA_SMS;
 }
 
 cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* part, cudaStream_t stream) {

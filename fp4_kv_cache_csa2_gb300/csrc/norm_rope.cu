@@ -11,20 +11,21 @@
 // reciprocal root lose nothing that the 8 significant bits of the result hold.
 //
 // Bound by HBM: a token reads and writes 64 KB of queries and 1 + 1 KB (or
-// 512 B) of window row against 0.2 Mflop.  One warp takes four rows at a time
-// (four heads of a token, or four tokens' key rows); lane l owns channels
-// 8l .. 8l + 7 and 256 + 8l .. 256 + 8l + 7, so every load and store of a warp
-// is 512 contiguous bytes and the eight 16-byte loads of a lane are in flight
-// together before the first is used.  The rotated tail lies in the second half
-// of lanes 24..31 (four pairs a lane).
+// 512 B) of window row against 0.2 Mflop.  One warp takes one row (a head of a
+// token, or a token's key row); lane l owns channels 8l .. 8l + 7 and 256 + 8l ..
+// 256 + 8l + 7, so every load and store of a warp is 512 contiguous bytes.  The
+// rotated tail lies in the second half of lanes 24..31 (four pairs a lane).
+// Rows a warp and threads a CTA, us for 16 / 300 / 777 / 8192 tokens: 1 and 128
+// 2.1 / 7.9 / 17.1 / 160, 2 and 128 2.8 / 8.4 / 17.8 / 156, 4 and 256 4.0 / 10.9 /
+// 22.1 / 175: many small CTAs keep as many loads in flight as several rows a warp
+// do, and fill the last wave better.
 #include "host_once.cuh"
 #include "params.cuh"
 
 namespace csa2 {
 
-constexpr int QK_THREADS = 256;
-constexpr int QK_ROWS = 4;                          // rows per warp
-constexpr int QK_TASKS = H / QK_ROWS;               // warps per token's queries
+constexpr int QK_THREADS = 128;
+constexpr int QK_CTAS = 12;                         // an SM, for 48 warps of at most 40 registers
 
 __device__ __forceinline__ uint32_t qk_bf16x2(float lo, float hi) {
   uint32_t r;
@@ -97,77 +98,44 @@ __device__ __forceinline__ const float4* qk_table_row(const QkParams& p, int64_t
   return nullptr;
 }
 
-__global__ void __launch_bounds__(QK_THREADS) qk_norm_rope_kernel(QkParams p) {
+__global__ void __launch_bounds__(QK_THREADS, QK_CTAS) qk_norm_rope_kernel(QkParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t g = (int64_t)blockIdx.x * (QK_THREADS / 32) + (threadIdx.x >> 5);
-  const int64_t nq = p.q ? p.T * QK_TASKS : 0;
-  uint4 x[QK_ROWS][2];
-  if (g < nq) {                                     // four heads of one token
-    const int64_t token = g / QK_TASKS;
-    const int head = (int)(g % QK_TASKS) * QK_ROWS;
-    const uint4* in = reinterpret_cast<const uint4*>(p.q + token * p.q_stride + head * D);
-#pragma unroll
-    for (int i = 0; i < QK_ROWS; i++) {
-      x[i][0] = __ldcs(in + 64 * i + lane);
-      x[i][1] = __ldcs(in + 64 * i + 32 + lane);
-    }
-    const float4* cs = qk_table_row(p, p.pos[token], head == 0 && lane == 0);
-    if (!cs) return;
-    uint4* out = reinterpret_cast<uint4*>(p.q_out + (token * H + head) * D);
-    const float4* w = reinterpret_cast<const float4*>(p.q_weight);
-    float r[QK_ROWS];
-#pragma unroll
-    for (int i = 0; i < QK_ROWS; i++) r[i] = qk_inv_rms(x[i][0], x[i][1], p.eps);
-#pragma unroll
-    for (int i = 0; i < QK_ROWS; i++)
-#pragma unroll
-      for (int half = 0; half < 2; half++) {
-        float f[8];
-        qk_finish(x[i][half], r[i], w, half, lane, cs, f);
-        __stcs(out + 64 * i + 32 * half + lane, qk_pack_bf16(f));
-      }
+  const int64_t nq = p.q ? p.T * H : 0;
+  const bool is_q = g < nq;
+  const int64_t token = is_q ? g / H : g - nq;
+  if (!is_q && (!p.k || token >= p.T)) return;
+  const int head = is_q ? (int)(g % H) : 0;
+  const uint4* in = reinterpret_cast<const uint4*>(is_q ? p.q + token * p.q_stride + head * D : p.k + token * p.k_stride);
+  const uint4 a = __ldcs(in + lane), b = __ldcs(in + 32 + lane);
+  // the queries' warps report a bad position when there are queries
+  const float4* cs = qk_table_row(p, p.pos[token], lane == 0 && (is_q ? head == 0 : !p.q));
+  int64_t slot = is_q ? 0 : (p.k_slot ? p.k_slot[token] : token);
+  if (!cs || slot == -1) return;
+  if (!is_q && (slot < 0 || slot >= p.n_rows)) {
+    if (lane == 0) report(p.hdr, CSA2_ERR_BOUNDS, slot);
     return;
   }
-  const int64_t t0 = (g - nq) * QK_ROWS;            // four tokens' key rows
-  if (!p.k || t0 >= p.T) return;
-  const int n = (int)(p.T - t0 < QK_ROWS ? p.T - t0 : QK_ROWS);
+  const float4* w = reinterpret_cast<const float4*>(is_q ? p.q_weight : p.k_weight);
+  const float r = qk_inv_rms(a, b, p.eps);
 #pragma unroll
-  for (int i = 0; i < QK_ROWS; i++) {
-    const uint4* in = reinterpret_cast<const uint4*>(p.k + (t0 + (i < n ? i : 0)) * p.k_stride);
-    x[i][0] = __ldcs(in + lane);
-    x[i][1] = __ldcs(in + 32 + lane);
-  }
-  const float4* w = reinterpret_cast<const float4*>(p.k_weight);
-#pragma unroll
-  for (int i = 0; i < QK_ROWS; i++) {
-    if (i >= n) break;
-    // the queries' warps report a bad position when there are queries
-    const float4* cs = qk_table_row(p, p.pos[t0 + i], !p.q && lane == 0);
-    const int64_t slot = p.k_slot ? p.k_slot[t0 + i] : t0 + i;
-    if (!cs || slot == -1) continue;
-    if (slot < 0 || slot >= p.n_rows) {
-      if (lane == 0) report(p.hdr, CSA2_ERR_BOUNDS, slot);
-      continue;
-    }
-    const float r = qk_inv_rms(x[i][0], x[i][1], p.eps);
-#pragma unroll
-    for (int half = 0; half < 2; half++) {
-      float f[8];
-      qk_finish(x[i][half], r, w, half, lane, cs, f);
-      if (p.rows_fp8) {
-        uint2* out = reinterpret_cast<uint2*>(p.rows + slot * D) + 32 * half + lane;
-        *out = make_uint2(qk_e4m3x2(f[0], f[1]) | qk_e4m3x2(f[2], f[3]) << 16,
-                          qk_e4m3x2(f[4], f[5]) | qk_e4m3x2(f[6], f[7]) << 16);
-      } else {
-        reinterpret_cast<uint4*>(p.rows + slot * D * 2)[32 * half + lane] = qk_pack_bf16(f);
-      }
+  for (int half = 0; half < 2; half++) {
+    float f[8];
+    qk_finish(half ? b : a, r, w, half, lane, cs, f);
+    if (is_q) {
+      __stcs(reinterpret_cast<uint4*>(p.q_out + (token * H + head) * D) + 32 * half + lane, qk_pack_bf16(f));
+    } else if (p.rows_fp8) {
+      reinterpret_cast<uint2*>(p.rows + slot * D)[32 * half + lane] =
+          make_uint2(qk_e4m3x2(f[0], f[1]) | qk_e4m3x2(f[2], f[3]) << 16, qk_e4m3x2(f[4], f[5]) | qk_e4m3x2(f[6], f[7]) << 16);
+    } else {
+      reinterpret_cast<uint4*>(p.rows + slot * D * 2)[32 * half + lane] = qk_pack_bf16(f);
     }
   }
 }
 
 cudaError_t launch_qk_norm_rope(const QkParams& p, cudaStream_t stream) {
-  const int64_t tasks = (p.q ? p.T * QK_TASKS : 0) + (p.k ? ceil_div(p.T, QK_ROWS) : 0);
+  const int64_t tasks = (p.q ? p.T * H : 0) + (p.k ? p.T : 0);
   if (tasks == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ceil_div(tasks, QK_THREADS / 32));

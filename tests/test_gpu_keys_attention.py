@@ -166,6 +166,41 @@ def test_window_split_over_ctas_and_many_queries():
     verify_window(7, 1, 640, 260, 5, False, pos, np.array([0]), 640)
 
 
+@pytest.mark.parametrize("kind", ["window", "window fp8", "ring", "ring fp8", "dense"])
+def test_repeated_runs_are_identical(kind):
+    """Many long runs of chunks on a warm cache, where copies arrive as early as they can:
+    every repetition gives the same bits, and a sample of them is right."""
+    g = synth.rng(21)
+    fp8, Q, W = "fp8" in kind, 602, 120 if "ring" in kind else 1000
+    rows, q = draw_rows(g, fp8, 1, Q + W - 1), synth.main_queries(g, 1, Q)
+    pos = W + np.arange(Q)[None, :]
+    base = np.ones(1, np.int64)
+    dq, drows, dpos, dbase = up(q), up(rows), up(pos), up(base)
+    out, lse = torch.empty(1, Q, 64, 512, dtype=torch.int16, device="cuda"), torch.empty(1, Q, 64, device="cuda")
+    if kind == "dense":
+        kv = draw_entries(g, 1, 1504)
+        cache = make_cache(kv, [1500], 1)
+        ws = csa2.Workspace(csa2.dense_attn_workspace_size(1, Q, 1504))
+    else:
+        ws = csa2.Workspace(csa2.window_attn_workspace_size(1, Q, W, 0))
+    first = None
+    for _ in range(20):
+        if kind == "dense":
+            csa2.dense_attn(cache, dq, drows, dbase, dpos, SCALE, out, ws, max_n=1504, lse=lse)
+        else:
+            csa2.window_attn(dq, drows, dbase, dpos, SCALE, out, ws, W=W, lse=lse)
+        if first is None:
+            first = out.clone(), lse.clone()
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert ws.sync_status()[0] == 0
+    rv, o, l = ref.row_values(rows[0]), out_values(out), lse.cpu().double().numpy()
+    for i in range(0, Q, 43):
+        t = int(pos[0, i])
+        keys = (ref.dense_keys(oracle.dequant_main(kv[0]), 1500, 1, rv, 1, t) if kind == "dense"
+                else ref.window_keys(rv, 1, t, W))
+        check(o[0, i], l[0, i], ref.bf16(q[0, i]), keys, SCALE, ref.U_F16 if kind == "dense" else ref.U_BF16, i)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("B,Q,W,n_sink,start", [
     (1, 700, 128, 4, 0), (1, 609, 1, 0, 5), (1, 640, 1, 3, 1), (2, 333, 31, 0, 0), (3, 205, 100, 59, 40),
