@@ -32,7 +32,7 @@
 //
 // Shared memory: three K buffers of [64 keys][512 dims] (two halves of 32 KB, four SW128
 // column chunks each; the third takes Q on its way to TMEM first) and a staging area of
-// 18 KB for the next chunk's entries, or half a chunk's E4M3 rows, as stored.  Roles:
+// 18 KB for the next chunk's entries as stored.  Roles:
 // warps 0..3 move Q, then softmax and output; warps 4..11 fill the K buffers (from the
 // staged bytes through registers; bf16 rows are rounded in place if need be); warp 12
 // issues the MMAs, S of chunk c + 1 before O of chunk c, so that the softmax of a chunk
@@ -73,7 +73,7 @@ constexpr int KA_PART_FLOATS = 2 * H + H * D;             // one partial state: 
 struct KaSmall {
   uint64_t q_full, q_moved;           // TMA: Q; Q is in TMEM (a softmax warp each)
   uint64_t stage_full, stage_free;    // the staged bytes have come / were read (a fill warp each)
-  uint64_t row_full[KA_BUFS][2];      // TMA: bf16 rows in half h of K buffer i
+  uint64_t row_full[KA_BUFS][2];      // TMA: rows in half h of K buffer i
   uint64_t full[KA_BUFS][2];          // half h of K buffer i is filled (a fill warp each)
   uint64_t free_[KA_BUFS];            // O of the chunk in K buffer i is done
   uint64_t s_full[2];                 // S of every second chunk is done
@@ -300,19 +300,13 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         const bool window = c < q.cw;
         const CUtensorMap* map = window ? &map_rows : &map_sinks;
         const int32_t y = (int32_t)(window ? (int64_t)b * p.S + q.r0 + KA_KEYS * c : (int64_t)b * p.n_sink + q.s0 + KA_KEYS * c);
-        if (!p.rows_fp8) {
-          // the tensor cores (the softmax warps, of Q) have read the buffer, which is waited for here
-          if (use > 0) ok = ok && ka_wait(&sm.free_[kb], use - 1, sm, p.hdr, 44);
-          else if (kb == KA_BUFS - 1) ok = ok && ka_wait(&sm.q_moved, 0, sm, p.hdr, 44);
-        }
+        // the tensor cores (the softmax warps, of Q) have read the buffer, which is waited for here
+        if (use > 0) ok = ok && ka_wait(&sm.free_[kb], use - 1, sm, p.hdr, 44);
+        else if (kb == KA_BUFS - 1) ok = ok && ka_wait(&sm.q_moved, 0, sm, p.hdr, 44);
         for (int h = 0; h < 2; h++) {
-          unsigned char* kt = smem + (2 * kb + h) * KA_HALF;
-          if (p.rows_fp8) next_stage(KA_HALF / 2);
-          else tc::bar_arrive_expect_tx(&sm.row_full[kb][h], KA_HALF);
-          for (int i = 0; i < 4; i++) {
-            if (p.rows_fp8) tc::tma_load_2d(stage + i * (KA_COL / 2), map, (4 * h + i) * 64, y, &sm.stage_full);
-            else tc::tma_load_2d(kt + i * KA_COL, map, (4 * h + i) * 64, y, &sm.row_full[kb][h]);
-          }
+          unsigned char* kt = smem + (2 * kb + h) * KA_HALF + (p.rows_fp8 ? KA_COL / 2 : 0);
+          tc::bar_arrive_expect_tx(&sm.row_full[kb][h], p.rows_fp8 ? KA_HALF / 2 : KA_HALF);
+          for (int i = 0; i < 4; i++) tc::tma_load_2d(kt + i * KA_COL, map, (4 * h + i) * 64, y, &sm.row_full[kb][h]);
         }
         if (++kb == KA_BUFS) kb = 0, use++;
       }
@@ -352,10 +346,10 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         *reinterpret_cast<uint4*>(dst + ((unit ^ (uint32_t)(key & 7)) << 4)) = v;
       }
     };
-    // 32 E4M3 dims of row `key` from quarter u of the staged half; rows behind the chunk's last:
-    // zeros.  Lanes with j >= 2 take their two pieces in the other order (bank groups)
-    auto widen = [&](int u, uint32_t* o, int n) {
-      const uint4* src = reinterpret_cast<const uint4*>(stage + (2 * u + (j >> 1)) * (KA_COL / 2) + key * 64 + 32 * (j & 1));
+    // 32 E4M3 dims of row `key` from a quarter; rows behind the chunk's last: zeros.  Lanes with
+    // j >= 2 take their two pieces in the other order (bank groups)
+    auto widen = [&](const unsigned char* kt, uint32_t* o, int n) {
+      const uint4* src = reinterpret_cast<const uint4*>(kt + (j >> 1) * KA_COL + KA_COL / 2 + key * 64 + 32 * (j & 1));
       uint4 a = make_uint4(0u, 0u, 0u, 0u), e = a;
       if (key < n) {
         a = src[odd ? 1 : 0];
@@ -387,29 +381,35 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       } else if (kb == KA_BUFS - 1) {
         ok = ok && ka_wait(&sm.q_moved, 0, sm, p.hdr, 47);
       }
-      if (F16 && entries) ok = ok && ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46);
-#pragma unroll 1
+      uint4 cd[4] = {}, sc[2] = {};                   // entries: codes of the four quarters, scales of the two halves
+      if (F16 && entries) {
+        // all at once (263 us for 16 queries over 131,072 entries; a half at a time, which holds
+        // the staging area longer, 310)
+        ok = ok && ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46);
+        if (key < keys) {                             // keys behind the last: zeros
+          const uint4* e = reinterpret_cast<const uint4*>(stage + key * MAIN_BYTES);
+#pragma unroll
+          for (int i = 0; i < 4; i++) cd[i] = e[4 * i + j];
+          sc[0] = e[16];
+          sc[1] = e[17];
+        }
+        stage_read();
+      }
+#pragma unroll
       for (int h = 0; h < 2; h++) {
         unsigned char* kt = smem + (2 * kb + h) * KA_HALF;
         if (F16 && (entries || p.rows_fp8)) {
           uint32_t o[2][16];
           if (entries) {
-            uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0, s4 = c0;     // keys behind the last: zeros
-            if (key < keys) {
-              const uint4* e = reinterpret_cast<const uint4*>(stage + key * MAIN_BYTES);
-              c0 = e[8 * h + j];
-              c1 = e[8 * h + 4 + j];
-              s4 = e[16 + h];
-            }
-            if (h == 1) stage_read();
             // scale bytes 2j, 2j + 1 of each quarter
-            dequant(c0, (odd ? s4.y : s4.x) >> (16 * (j & 1)), o[0]);
-            dequant(c1, (odd ? s4.w : s4.z) >> (16 * (j & 1)), o[1]);
+            dequant(cd[2 * h], (odd ? sc[h].y : sc[h].x) >> (16 * (j & 1)), o[0]);
+            dequant(cd[2 * h + 1], (odd ? sc[h].w : sc[h].z) >> (16 * (j & 1)), o[1]);
           } else {
-            ok = ok && ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46);
-            widen(0, o[0], keys);
-            widen(1, o[1], keys);
-            stage_read();
+            // E4M3 rows, in the upper halves of the column chunks: all are read before any is written
+            ok = ok && ka_wait(&sm.row_full[kb][h], use, sm, p.hdr, 48);
+            widen(kt, o[0], keys);
+            widen(kt + 2 * KA_COL, o[1], keys);
+            named_sync(1, KA_FILL);
           }
           store(kt, o[0]);
           store(kt + 2 * KA_COL, o[1]);
