@@ -451,6 +451,8 @@ def dense_attn(cache: Cache, q, swa, swa_base_pos, q_pos, scale: float, out, ws:
     dev, (B, Q), S = ws.buf.device, q_pos.shape, swa.shape[1]
     if B != cache.B:
         raise ValueError(f"q_pos: {B} sequences, the cache has {cache.B}")
+    if cache.main_kv.device != dev:
+        raise ValueError(f"the cache is on {cache.main_kv.device}, the workspace on {dev}")
     shape = (B, Q, N_HEADS, D_LATENT)
     a = DenseArgs(B, Q, S, float(scale), max_n, _int64("q_pos", q_pos, (B, Q), dev), _bits16("q", q, shape, dev),
                   _rows("swa", swa, (B, S, D_LATENT), dev), _int64("swa_base_pos", swa_base_pos, (B,), dev),

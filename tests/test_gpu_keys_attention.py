@@ -479,3 +479,84 @@ def test_the_layer_from_projections_to_outputs(fp8):
     keys = np.concatenate([entries[:64], rv[:64]])
     bound = ref.attend(qv[0], keys, SCALE, ref.U_F16)[2]
     assert np.all(np.abs(va - vb) <= 2 * bound)
+
+
+def test_offsets_past_32_bits_in_the_cache():
+    """The second sequence of a cache of 4.3 GB a sequence, and the end of the first: entries
+    far behind 2^32 bytes.  All entries but the last thousand are zeros (logits 0)."""
+    g = synth.rng(22)
+    cap, m = 15_000_008, 1
+    cache = csa2.Cache(2, cap, m)
+    assert cap * 288 > 1 << 32
+    tail = draw_entries(g, 2, 1000)
+    ns = [cap - 3, 1000]
+    cache.main_kv[0, ns[0] - 1000:ns[0]].copy_(up(tail[0]))
+    cache.main_kv[1, :1000].copy_(up(tail[1]))
+    cache.n_entries.copy_(torch.tensor(ns, dtype=torch.int32))
+    rows, q = draw_rows(g, False, 2, 128), synth.main_queries(g, 2, 1)
+    pos = np.array([[ns[0] - 1], [999]])
+    base = pos[:, 0] - 127
+    o, l = run_dense(cache, q, rows, base, pos, cap)
+    for b in range(2):
+        far = oracle.dequant_main(tail[b])
+        qv = ref.bf16(q[b, 0])
+        keys = np.concatenate([far, ref.row_values(rows[b])])
+        zeros = ns[b] - 1000                                  # each adds exp(0) to the sum
+        logit = SCALE * (qv @ keys.T)
+        e = np.exp(logit)
+        total = e.sum(-1, keepdims=True) + zeros
+        want = (e / total) @ keys
+        # many terms of the sum: 2^-24 each at most, 64 at a time in one register
+        tol = ref.U_BF16 * np.abs(want) + (2.0 ** -10 + zeros / 64 / 152 * 2.0 ** -24) * ((e / total) @ np.abs(keys)) + \
+            1128 * 2.0 ** -25 * np.abs(keys).max() / total
+        assert np.all(np.abs(o[b, 0] - want) <= tol)
+        assert np.all(np.abs(l[b, 0] - np.log(total[:, 0])) <= 1e-3)
+
+
+@pytest.mark.parametrize("Q", [3, 460])
+def test_offsets_past_32_bits_in_the_rows(Q):
+    """Window rows behind 2^32 bytes, for few queries and for many."""
+    g = synth.rng(23)
+    S, W = 4_300_000, 100
+    assert (S - Q - W) * 1024 > 1 << 32
+    rows = torch.zeros(1, S, 512, dtype=torch.int16, device="cuda")
+    last = draw_rows(g, False, 1, Q + W)
+    rows[0, S - Q - W:] = up(last)[0]
+    q = synth.main_queries(g, 1, Q)
+    pos, base = 7 + np.arange(S - Q, S)[None, :], np.array([7])
+    out = torch.empty(1, Q, 64, 512, dtype=torch.int16, device="cuda")
+    lse = torch.empty(1, Q, 64, device="cuda")
+    ws = csa2.Workspace(csa2.window_attn_workspace_size(1, Q, W, 0))
+    csa2.window_attn(up(q), rows, up(base), up(pos), SCALE, out, ws, W=W, lse=lse)
+    assert ws.sync_status()[0] == 0
+    o, l, rv = out_values(out), lse.cpu().double().numpy(), ref.row_values(last[0])
+    for i in range(0, Q, 1 if Q < 10 else 51):
+        check(o[0, i], l[0, i], ref.bf16(q[0, i]), ref.window_keys(rv, 7 + S - Q - W, int(pos[0, i]), W), SCALE, ref.U_BF16, i)
+
+
+def test_offsets_past_32_bits_in_queries_and_outputs():
+    """65,600 queries in one call: q and the output pass 2^32 bytes."""
+    Q, W = 65_600, 20
+    assert Q * 64 * 512 * 2 > 1 << 32
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.empty(1, Q, 64, 512, dtype=torch.bfloat16, device="cuda")
+    q.normal_(generator=gen)
+    rows = torch.randn(1, Q, 512, device="cuda", generator=gen).to(torch.float8_e4m3fn).view(torch.uint8)
+    pos, base = torch.arange(Q, device="cuda")[None], torch.zeros(1, dtype=torch.int64, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(1, Q, 64, device="cuda")
+    ws = csa2.Workspace(csa2.window_attn_workspace_size(1, Q, W, 0))
+    csa2.window_attn(q, rows, base, pos, SCALE, out, ws, W=W, lse=lse)
+    assert ws.sync_status()[0] == 0
+    rv = ref.row_values(rows[0].cpu().numpy())
+    for t in (0, 1, 30000, 32767, 32768, 65535, 65536, 65599):
+        check(out[0, t].double().cpu().numpy(), lse[0, t].double().cpu().numpy(), q[0, t].double().cpu().numpy(),
+              ref.window_keys(rv, 0, t, W), SCALE, ref.U_BF16, t)
+    # one wide window over the same queries' buffer, two of them
+    two = q[:, -2:].contiguous()
+    o2, l2 = torch.empty_like(two), torch.empty(1, 2, 64, device="cuda")
+    ws = csa2.Workspace(csa2.window_attn_workspace_size(1, 2, 900, 0))
+    csa2.window_attn(two, rows, base, pos[:, -2:].contiguous(), SCALE, o2, ws, W=900, lse=l2)
+    assert ws.sync_status()[0] == 0
+    for i in range(2):
+        check(o2[0, i].double().cpu().numpy(), l2[0, i].double().cpu().numpy(), two[0, i].double().cpu().numpy(),
+              ref.window_keys(rv, 0, Q - 2 + i, 900), SCALE, ref.U_BF16, i)

@@ -139,3 +139,22 @@ def test_another_stream_and_a_replayed_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, out2) and torch.equal(rows, rows2)
+
+
+def test_offsets_past_32_bits():
+    """66,000 tokens in place: the queries pass 2^32 bytes."""
+    T = 66_000
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.empty(T, 64, 512, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    at = [0, 1, 32767, 32768, 65535, 65536, 65999]
+    x = q[at].double().cpu().numpy()
+    k = q[:, 5].clone()
+    xk = k[at].double().cpu().numpy()
+    cs, ws = csa2.rope_table(P), csa2.Workspace(256)
+    pos = torch.arange(T, device="cuda") % P
+    rows = torch.empty(T, 512, dtype=torch.uint8, device="cuda")
+    csa2.qk_norm_rope(pos, cs.cuda(), ws, q=q, q_out=q, k=k, rows=rows)
+    assert ws.sync_status()[0] == 0
+    for n, t in enumerate(at):
+        check(q[t].double().cpu().numpy(), x[n], None, cs[t % P].numpy(), 1e-6, ref.U_BF16)
+        check(ref.row_values(rows[t].cpu().numpy()), xk[n], None, cs[t % P].numpy(), 1e-6, ref.U_E4M3)

@@ -124,9 +124,10 @@ def test_workspace_sizes(lib):
     # a long cache and one query: a state per SM at most
     one = csa2.dense_attn_workspace_size(1, 1, 1 << 20) - 256
     assert one % PART == 0 and 64 * PART <= one <= 152 * PART
-    for b in (1, 3, 16, 100, 300):
-        n = csa2.dense_attn_workspace_size(b, 1, 131072) - 256
-        assert n <= -(-16 * 152 * PART // 256) * 256
+    # however long the window or the cache, at most four states an SM
+    for b in (1, 3, 16, 100, 300, 600):
+        for n in (csa2.dense_attn_workspace_size(b, 1, 1 << 31), csa2.window_attn_workspace_size(b, 1, (1 << 31) - 1, 0)):
+            assert n - 256 <= 4 * 152 * PART
 
 
 def test_binding_structs_match_the_c_layout(tmp_path):
