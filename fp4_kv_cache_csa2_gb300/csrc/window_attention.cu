@@ -11,7 +11,7 @@
 // slots a query sees is a circular interval.  A CTA takes a run of neighbouring tiles, so that
 // a tile loads the two rows that its queries see newly, and streams q in and the output out:
 //   warps 0..3    softmax, one thread a row, from TMEM; P goes back over S as 16-bit A operand
-//   warps 4..7    output: O by quarters of a half (64 dims) to bf16 rows
+//   warps 4..7    output: O by 64 dims to bf16 rows
 //   warps 8..11   the ring: rows that the next tile's queries see newly
 //   warp 12       S = Q K^T (M = 128, N = slots, K = 512), Q in 64-dim pieces through 3 stages
 //   warp 13       O = P V by 64 dims (M = 128, N = 64, K = slots), V the ring read MN-major
@@ -67,7 +67,7 @@ struct WaSmall {
   uint64_t s_full[2], p_ready[2], state_ready[2], pv_done[2];   // of every second job
   uint64_t o_full[WA_O_BUFS], o_free[WA_O_BUFS];
   uint32_t tmem_base;
-  int err, dirty;
+  int err;
 };
 constexpr int WA_SMEM = WA_OFF_SMALL + (int)sizeof(WaSmall);
 constexpr int WA_READERS = 1 + 1 + 1 + 4 + 4;             // of a job: copy, S, O, softmax, output warps
@@ -121,6 +121,16 @@ __device__ __forceinline__ bool wa_not_finite(const uint4& v) {
          (v.z >> 16 & E) == E || (v.w & E) == E || (v.w >> 16 & E) == E;
 }
 
+// Barrier of the ring warps that tells each of them whether any thread came with x set.  A flag
+// in shared memory, read behind a plain barrier, could already be the next tile's: a warp that
+// reads it late would part from the others.
+__device__ __forceinline__ bool wa_ring_any(bool x) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, 1, %2, a;\n"
+               " selp.u32 %0, 1, 0, b;\n}\n" : "=r"(r) : "r"((uint32_t)x), "n"(WA_RING) : "memory");
+  return r != 0;
+}
+
 // bits [a, b) of the 32 from g on
 __device__ __forceinline__ uint32_t wa_bits(int a, int b, int g) {
   a = max(a - g, 0);
@@ -168,7 +178,6 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
       tc::bar_init(&sm.o_free[i], 4);
     }
     sm.err = 0;
-    sm.dirty = 0;
     tc::bar_init_fence();
     tc::prefetch_tensormap(&map_q);
   }
@@ -367,12 +376,11 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
           if (zero) {
             for (int x = rt; x < 8 * WA_KCOL / 16; x += WA_RING) reinterpret_cast<uint4*>(smem)[x] = make_uint4(0u, 0u, 0u, 0u);
             named_sync(1, WA_RING);
-            if (rt == 0) sm.dirty = 0;
-            named_sync(1, WA_RING);
           }
         };
         // new rows [rh, E) to their window slots, new sinks [ns, NS) to theirs.  A row that is not
         // finite is left out (and told) unless the job is exact
+        bool dirty = false;
         const int n_row = max(E - rh, 0), n_all = n_row + max(NS - ns, 0);
         const int slot_r = p.n_sink + rh % R;
 #pragma unroll 1
@@ -407,7 +415,7 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
               hi4 = make_uint4(o[4], o[5], o[6], o[7]);
             }
             if (!exact && __any_sync(0xFFFFFFFFu, wa_not_finite(lo4) || wa_not_finite(hi4))) {
-              if (lane == 0) sm.dirty = 1;
+              dirty = true;
               continue;
             }
             int slot = slot_r + x;
@@ -423,9 +431,7 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
         rh = max(rh, E);
         rl = max(rl, E - R);
         ns = max(ns, NS);
-        named_sync(1, WA_RING);
-        const bool dirty = *(volatile int*)&sm.dirty != 0;
-        if (dirty && !exact) {                        // each query of this job alone, with what it sees as it is
+        if (wa_ring_any(dirty)) {                      // each query of this job alone, with what it sees as it is
           const int singles = (mask & have) == 3 ? 1 | 2 << 2 : mask & have;
           todo = singles | todo << (singles > 3 ? 4 : 2);
           exact = true;

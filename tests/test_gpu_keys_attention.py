@@ -266,6 +266,31 @@ def test_window_many_queries_not_finite():
             assert seen > 60
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_window_bad_rows_everywhere_repeated(fp8):
+    """Tiles with and without a bad row take turns (every ring warp has to agree which is which):
+    each run ends, and gives the same bits."""
+    g = synth.rng(41)
+    B, Q, W = 3, 640, 60
+    rows, q = draw_rows(g, fp8, B, Q), synth.main_queries(g, B, Q)
+    for b, step in enumerate((61, 97, 3)):                    # some, few and no windows without one
+        for n, r in enumerate(range(5, Q, step)):
+            rows[b, r, (37 * n) % 512] = NAN_E4M3 if fp8 else NAN_BF16
+    bad = np.isnan(ref.row_values(rows)).any(axis=-1)
+    want = np.array([[bad[b, max(0, t - W + 1):t + 1].any() for t in range(Q)] for b in range(B)])
+    q, rows, base = up(q), up(rows), up(np.zeros(B, np.int64))
+    pos = up(np.broadcast_to(np.arange(Q), (B, Q)))
+    ws = csa2.Workspace(csa2.window_attn_workspace_size(B, Q, W, 0))
+    runs = [(torch.zeros(B, Q, 64, 512, dtype=torch.int16, device="cuda"), torch.zeros(B, Q, 64, device="cuda"))
+            for _ in range(20)]
+    for o, l in runs:
+        csa2.window_attn(q, rows, base, pos, SCALE, o, ws, W=W, lse=l)
+    assert ws.sync_status()[0] == 0
+    np.testing.assert_array_equal(runs[0][1].isnan().any(dim=-1).cpu().numpy(), want)
+    for o, l in runs[1:]:
+        assert torch.equal(o, runs[0][0]) and torch.equal(l.view(torch.int32), runs[0][1].view(torch.int32))
+
+
 def run_dense(cache, q, rows, base, pos, max_n, scale=SCALE, status=0, stream=None):
     B, Q = pos.shape
     out = torch.full((B, Q, 64, 512), 0x4242, dtype=torch.int16, device="cuda")
