@@ -414,7 +414,10 @@ static csa2_status check_keys_call(const KeysParams& p, int B, int Q, size_t nee
 
 // runs of keys that a query of a window call / a dense call sees at most
 static int64_t window_chunks(int64_t W, int64_t n_sink) { return ceil_div(W, KEYS_CHUNK) + ceil_div(n_sink, KEYS_CHUNK); }
-static int64_t dense_chunks(int64_t max_n) { return WIN / KEYS_CHUNK + ceil_div(max_n, KEYS_CHUNK); }
+static int64_t dense_chunks(int64_t max_n) {
+  const int64_t most = INT32_MAX;                     // n_entries is 32 bits: no query sees more
+  return WIN / KEYS_CHUNK + ceil_div(max_n < most ? max_n : most, KEYS_CHUNK);
+}
 
 size_t csa2_window_attn_workspace_size(int B, int Q, int W, int n_sink) {
   if (B < 0 || Q < 0 || W < 1 || n_sink < 0 || (int64_t)B * Q > MAX_KEY_QUERIES) return 0;

@@ -130,6 +130,15 @@ def test_workspace_sizes(lib):
             assert n - 256 <= 4 * 152 * PART
 
 
+@pytest.mark.parametrize("B,Q", [(1, 1), (3, 7), (152, 1), (600, 1), (4096, 4096)])
+def test_the_largest_max_n(lib, B, Q):
+    """However many entries a call names, its workspace is that of the most a cache can hold."""
+    most = csa2.dense_attn_workspace_size(B, Q, (1 << 31) - 1)
+    assert 256 <= most <= 256 + 4 * 152 * PART
+    for n in (1 << 31, 1 << 40, 1 << 62, (1 << 63) - 1):
+        assert csa2.dense_attn_workspace_size(B, Q, n) == most
+
+
 def test_binding_structs_match_the_c_layout(tmp_path):
     from tests.test_library_abi import _c_layout
     for cls, struct in ((csa2.QkArgs, "csa2_qk_args"), (csa2.WindowArgs, "csa2_window_args"),
