@@ -367,6 +367,12 @@ csa2_status csa2_qk_norm_rope(const csa2_qk_args* a, void* ws, size_t ws_bytes, 
   if (overlap(a->k, k_bytes, a->rows, row_bytes) || overlap(a->k, k_bytes, a->q_out, out_bytes) ||
       overlap(a->q, q_bytes, a->rows, row_bytes) || overlap(a->q_out, out_bytes, a->rows, row_bytes))
     return CSA2_ERR_INVALID_ARG;
+  const int64_t weight = D * 4, table = a->rope_P < ((int64_t)1 << 48) ? a->rope_P * D_ROPE * 4 : INT64_MAX / 2;
+  const struct { const void* a; int64_t n; } in[] = {{a->pos, a->T * 8}, {a->rope_cs, table}, {ws, (int64_t)HDR},
+      {a->q_weight, a->q && a->q_weight ? weight : 0}, {a->k_weight, a->k && a->k_weight ? weight : 0},
+      {a->k_slot, a->k && a->k_slot ? a->T * 8 : 0}};
+  for (const auto& x : in)
+    if (overlap(x.a, x.n, a->q_out, out_bytes) || overlap(x.a, x.n, a->rows, row_bytes)) return CSA2_ERR_INVALID_ARG;
   QkParams p{};
   p.T = a->T;
   p.pos = a->pos;

@@ -44,6 +44,18 @@ def test_norm_rope_refuses(lib, change, want):
     assert lib.csa2_qk_norm_rope(ctypes.byref(qk_args(**change)), WS, 256, None) == want
 
 
+@pytest.mark.parametrize("out", ["q_out", "rows"])
+@pytest.mark.parametrize("name,last", [("pos", 4 * 8), ("rope_cs", 64 * 256), ("q_weight", 2048), ("k_weight", 2048),
+                                       ("k_slot", 4 * 8), ("ws", 256)])
+def test_norm_rope_refuses_outputs_over_its_small_inputs(lib, out, name, last):
+    at = (8 << 32) + 4096
+    ws = at if name == "ws" else WS
+    kw = {} if name == "ws" else {name: at}
+    size = 4 * 65536 if out == "q_out" else 8 * 1024
+    for addr in (at, at + last - 16, at - size + 16):
+        assert lib.csa2_qk_norm_rope(ctypes.byref(qk_args(**kw, **{out: addr})), ws, 256, None) == 1, addr - at
+
+
 def test_norm_rope_nothing_to_do_and_workspace(lib):
     assert lib.csa2_qk_norm_rope(None, WS, 256, None) == 1
     assert lib.csa2_qk_norm_rope(ctypes.byref(qk_args()), None, 0, None) == 3
