@@ -8,6 +8,7 @@ does not build anything; ``load()`` raises if the library has not been built
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -333,8 +334,9 @@ def decode(mode: int, cache: Cache, *, q_pos, q, swa, swa_base_pos, scale: float
                                              _stream(stream)))
 
 
-# The calls below also check what the C boundary cannot see: shapes, element
-# sizes, and that every tensor lies contiguous on the device of the workspace.
+# The calls below also check what the C boundary cannot see: shapes, types, and
+# that every tensor lies contiguous on the device of the workspace.  bf16 and
+# E4M3 may come as their bits (16-bit and 8-bit integers).
 # A decode step makes these calls one after another, each of a few microseconds on
 # the GPU, so the checks are plain comparisons and the message is put together
 # only for a call that is refused.
@@ -343,36 +345,44 @@ def _refuse(name: str, t, shape, what: str, device):
                      f"{tuple(shape)}, contiguous, on {device}")
 
 
+@functools.cache
+def _types():
+    """Types that hold bf16, window rows, 64-bit integers and float32."""
+    import torch
+    bf16 = (torch.bfloat16, torch.int16, torch.uint16)
+    return bf16, (*bf16, torch.uint8, torch.int8, torch.float8_e4m3fn), torch.int64, torch.float32
+
+
 def _bits16(name: str, t, shape, device):
-    """Address of a contiguous 16-bit tensor of this shape on this device."""
-    if t.shape != shape or t.element_size() != 2 or t.device != device or not t.is_contiguous():
-        _refuse(name, t, shape, "16-bit elements", device)
+    """Address of a contiguous bf16 tensor of this shape on this device."""
+    if t.shape != shape or t.dtype not in _types()[0] or t.device != device or not t.is_contiguous():
+        _refuse(name, t, shape, "bf16", device)
     return t.data_ptr()
 
 
 def _rows(name: str, t, shape, device):
-    """Address of window rows: 16-bit elements (bf16) or bytes (E4M3)."""
-    if t.shape != shape or t.element_size() > 2 or t.device != device or not t.is_contiguous():
-        _refuse(name, t, shape, "16-bit or 8-bit elements", device)
+    """Address of window rows, bf16 or E4M3."""
+    if t.shape != shape or t.dtype not in _types()[1] or t.device != device or not t.is_contiguous():
+        _refuse(name, t, shape, "bf16 or E4M3", device)
     return t.data_ptr()
 
 
 def _int64(name: str, t, shape, device):
-    if t.shape != shape or t.element_size() != 8 or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not _types()[2] or t.device != device or not t.is_contiguous():
         _refuse(name, t, shape, "64-bit integers", device)
     return t.data_ptr()
 
 
 def _float32(name: str, t, shape, device):
-    if t.shape != shape or t.element_size() != 4 or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not _types()[3] or t.device != device or not t.is_contiguous():
         _refuse(name, t, shape, "float32", device)
     return t.data_ptr()
 
 
 def _tokens(name: str, t, shape, inner, device):
-    """Address of 16-bit tokens whose strides but the first are `inner`."""
-    if t.shape != shape or t.stride()[1:] != inner or t.element_size() != 2 or t.device != device:
-        _refuse(name, t, shape, f"16-bit elements with inner strides {inner}, not", device)
+    """Address of bf16 tokens whose strides but the first are `inner`."""
+    if t.shape != shape or t.stride()[1:] != inner or t.dtype not in _types()[0] or t.device != device:
+        _refuse(name, t, shape, f"bf16 with inner strides {inner}, not", device)
     return t.data_ptr()
 
 

@@ -189,3 +189,28 @@ def test_binding_refuses_shapes_types_and_strides():
         csa2.window_attn(q1, rows, base, p1, 0.1, torch.empty_like(q1), _FakeWs, W=8, lse=torch.zeros(1, 2, 32))
     with pytest.raises(ValueError, match="sequences"):
         csa2.dense_attn(csa2.Cache(2, 8, 1, device="cpu"), q1, rows, base, p1, 0.1, torch.empty_like(q1), _FakeWs, max_n=8)
+
+
+def test_binding_refuses_types_of_the_right_size():
+    """A type of the same width would be read as another number."""
+    q = torch.zeros(2, 64, 512, dtype=torch.bfloat16)
+    pos, cs = torch.zeros(2, dtype=torch.int64), torch.zeros(4, 32, 2)
+    with pytest.raises(ValueError, match="q:"):
+        csa2.qk_norm_rope(pos, cs, _FakeWs, q=q.half(), q_out=q)
+    with pytest.raises(ValueError, match="q_out"):
+        csa2.qk_norm_rope(pos, cs, _FakeWs, q=q, q_out=q.half())
+    with pytest.raises(ValueError, match="pos"):
+        csa2.qk_norm_rope(pos.double(), cs, _FakeWs, q=q, q_out=q)
+    with pytest.raises(ValueError, match="rope_cs"):
+        csa2.qk_norm_rope(pos, cs.int(), _FakeWs, q=q, q_out=q)
+    k, rows = torch.zeros(2, 512, dtype=torch.bfloat16), torch.zeros(2, 512)
+    for wrong in (torch.float8_e5m2, torch.bool, torch.float16):
+        with pytest.raises(ValueError, match="rows"):
+            csa2.qk_norm_rope(pos, cs, _FakeWs, k=k, rows=rows.to(wrong))
+    base, p1, q1 = torch.zeros(1, dtype=torch.int64), torch.zeros(1, 2, dtype=torch.int64), q[None]
+    r1 = torch.zeros(1, 130, 512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="lse"):
+        csa2.window_attn(q1, r1, base, p1, 0.1, torch.empty_like(q1), _FakeWs, W=8,
+                         lse=torch.zeros(1, 2, 64, dtype=torch.int32))
+    with pytest.raises(ValueError, match="out"):
+        csa2.dense_attn(csa2.Cache(1, 8, 1, device="cpu"), q1, r1, base, p1, 0.1, q1.half(), _FakeWs, max_n=8)
