@@ -21,8 +21,8 @@
 // share columns: half h of the dims has its Q, its part of S and its O in lanes
 // 16h .. 16h + 15 (256 columns of O, 128 of Q, twice 64 of S), P lies in both.  With Q and P
 // in TMEM a product reads only the K tile from shared memory, 16 of its 32 cycles at
-// N = 64 (with Q there too it takes all 32, and the fill's stores come on top: 3100
-// cycles a chunk instead of 2300).
+// N = 64 (with Q there too it takes all 32, and the fill's stores come on top: 3100 to 3300
+// cycles a chunk, and 2300 to 2500 with Q and P in TMEM and the third buffer).
 // Operands: F16 (calls with cache entries or E4M3 rows) keeps every dequantised FP4
 // value (at most 6 significant bits, 2^-10 .. 2688) and every E4M3 value exactly and
 // rounds q and bf16 window rows to f16, exact inside [2^-14, 65504], with P to 11
@@ -123,7 +123,7 @@ __device__ __forceinline__ KaRun ka_run(const KeysParams& p, int64_t bq, int b, 
   }
   const int64_t sn = live ? (q.lo < p.n_sink ? q.lo : (int64_t)p.n_sink) : 0;
   if (live && p.main_kv) {
-    en = visible_entries(q.t, p.m, p.n_entries[b]);
+    en = visible_entries(min(q.t, INT64_MAX - 1), p.m, p.n_entries[b]);   // t + 1 has to exist
     if (en > p.cap) en = p.cap;       // reported by the kernel
     if (en < 0) en = 0;
   }

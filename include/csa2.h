@@ -386,7 +386,8 @@ csa2_status csa2_decode(const csa2_cache *cache, const csa2_decode_args *args, v
  * outputs are what the attention calls take (q, and rows of a window buffer).
  * [zartbot §1.2 rope_head_dim, §2.4.4: norm, then RoPE, then the stored format]
  *   y = x / sqrt(mean(x^2) + eps) * weight, then pairs (448+2i, 449+2i) rotate
- *   with row pos of the table; binary32 until the one final rounding.
+ *   with row pos of the table; binary32 until the one final rounding (a sum of
+ *   squares past its range gives zeros; a row of zeros with eps = 0 is NaN).
  * Tokens with pos = -1 are padding: nothing of theirs is written.  Any other
  * position outside [0, rope_P) is skipped and raises CSA2_ERR_BOUNDS, and so
  * does a slot outside [0, n_rows) (-1 skips the row without an error).  The
@@ -435,8 +436,9 @@ csa2_status csa2_qk_norm_rope(const csa2_qk_args *args, void *ws, size_t ws_byte
  * and out 16-byte, q_pos, swa_base_pos 8-byte and lse 4-byte aligned; out and
  * lse must not overlap an input or each other.
  * Precision: binary32 accumulation and softmax state.  With bf16 rows the
- * operands are bf16; with E4M3 rows they are f16, which holds the rows exactly
- * and rounds q as csa2_sparse_swa_attn does.  Workspace:
+ * operands are bf16.  With E4M3 rows, which both types hold exactly, they are
+ * bf16 (calls of many neighbouring queries with short windows) or f16, and q
+ * is then rounded as csa2_sparse_swa_attn does.  Workspace:
  * csa2_window_attn_workspace_size (partial states when a query's keys are
  * divided over several CTAs).
  */

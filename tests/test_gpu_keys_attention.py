@@ -413,6 +413,35 @@ def test_dense_growing_maxima():
             check(o[0, i], l[0, i], ref.bf16(q[0, i]), keys, scale, ref.U_F16, (scale, i))
 
 
+def test_the_largest_positions_and_the_farthest_buffers():
+    """Positions up to 2^63 - 1, and buffers that begin far before or behind every query."""
+    g = synth.rng(42)
+    top = (1 << 63) - 1
+    for Q in (2, 460):                                        # one CTA a query, and the ring
+        S = Q + 40
+        for fp8 in (False, True):
+            rows, q = draw_rows(g, fp8, 1, S), synth.main_queries(g, 1, Q)
+            pos, base = top - Q + 1 + np.arange(Q)[None, :], np.array([top - S + 1])
+            o, l = run_window(q, rows, base, pos, 41, None)
+            rv = ref.row_values(rows[0])
+            for i in range(0, Q, 51):
+                first = int(pos[0, i]) - int(base[0])
+                check(o[0, i], l[0, i], ref.bf16(q[0, i]), rv[max(0, first - 40):first + 1], SCALE,
+                      ref.U_F16 if fp8 and Q == 2 else ref.U_BF16, i)
+            for far, at in ((-top - 1, 50), (top, 50)):       # nothing of the window was supplied
+                o, l = run_window(q, rows, np.array([far]), at + np.arange(Q)[None, :], 41, None, status=6)
+                assert np.all(o == 0) and np.all(l == -math.inf)
+    kv, ns = draw_entries(g, 1, 200), [200]
+    rows, q = draw_rows(g, False, 1, 130), synth.main_queries(g, 1, 2)
+    rv = ref.row_values(rows[0])
+    for m in (1, 2):
+        pos = np.array([[top - 1, top]])
+        o, l = run_dense(make_cache(kv, ns, m), q, rows, np.array([top - 129]), pos, 200)
+        for i in range(2):
+            keys = np.concatenate([rv[1 + i:129 + i], oracle.dequant_main(kv[0])])
+            check(o[0, i], l[0, i], ref.bf16(q[0, i]), keys, SCALE, ref.U_F16, (m, i))
+
+
 def test_two_calls_at_once_another_stream_and_graphs():
     """Calls on two streams with a workspace each, and two graphs that share one and are replayed in turn."""
     g = synth.rng(12)
