@@ -65,6 +65,7 @@ constexpr int KA_AHEAD = 5;                               // chunks of entries t
 constexpr float KA_LOG2E = 1.4426950408889634f;
 constexpr float KA_LN2 = 0.6931471805599453f;
 constexpr float KA_TAU = 8.0f * KA_LOG2E;
+constexpr int KA_SMS = 152;                               // GB300; CTAs a query is divided over at most
 constexpr int KA_PART_FLOATS = 2 * H + H * D;             // one partial state: references, sums, O [dims / 4][head][4]
 
 // A wait for a phase by its parity needs that the barrier cannot have passed the phase
@@ -614,75 +615,118 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 }
 
 // One query's output from its CTAs' partial states: with m = max_s m_s and
-// w_s = 2^(m_s - m), O = sum_s w_s O_s / sum_s w_s l_s.  A CTA takes four heads: thread =
-// (head, 4 dims of each half), so that a warp reads 64-byte pieces of [dims / 4][head][4].
-// Every warp works out the weights of its four heads, 8 states at a time in its lanes.
-__global__ void __launch_bounds__(256) keys_combine_kernel(const float* __restrict__ part, int split,
-                                                           uint16_t* __restrict__ out, float* __restrict__ lse) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, hl = lane & 3;
-  const int64_t bq = blockIdx.x >> 4;
-  const int h = (blockIdx.x & 15) * 4 + hl, dg = threadIdx.x >> 2;   // dims 4 dg .. and 256 + 4 dg ..
+// w_s = 2^(m_s - m), O = sum_s w_s O_s / sum_s w_s l_s.  A CTA takes 16 GROUPS dims of all
+// heads: thread = (slice of the states, head, 4 dims of each group), so that a warp reads pieces of
+// 128 bytes of [dims / 4][head][4] and writes 32 bytes a head.  Bound by the latency of its reads (a
+// state is 130 KB, in L2): a thread has BATCH states on their way while the CTA works out
+// the weights.
+template <int SLICES, int GROUPS, int BATCH, int MOST>
+__global__ void __launch_bounds__(SLICES * H * 4)
+keys_combine_kernel(const float* __restrict__ part, int split, uint16_t* __restrict__ out, float* __restrict__ lse) {
+  constexpr int ROWS = SLICES * 4;                    // states whose references are read at once
+  constexpr int CTAS = D / (16 * GROUPS);             // of a query
+  __shared__ __align__(16) float weight[MOST][H];     // then the slices' sums
+  __shared__ float red[ROWS][H], sum[H];
+  static_assert(MOST >= (SLICES - 1) * 16 && (SLICES == 1 || GROUPS == 1), "the slices' sums lie over the weights");
+  const int tid = threadIdx.x;
+  const int64_t bq = blockIdx.x / CTAS;
+  const int dims = (blockIdx.x % CTAS) * 16 * GROUPS;
+  const int g = tid % 4, h = tid / 4 % H, z = tid / (4 * H);
   const float* pb = part + bq * split * KA_PART_FLOATS;
-  float mx = -INFINITY;                               // lane = (state of eight, head)
-  for (int s = lane >> 2; s < split; s += 8) mx = fmaxf(mx, pb[(int64_t)s * KA_PART_FLOATS + h]);
+  const float4* o = reinterpret_cast<const float4*>(pb + 2 * H) + (dims / 4 + g) * H + h;
+  float4 x[BATCH][GROUPS];                         // O of states s, s + SLICES ..
+  auto load = [&](int s) {
 #pragma unroll
-  for (int k = 16; k >= 4; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
-  float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  float L = 0.f;
-  for (int s0 = 0; s0 < split; s0 += 8) {
-    float w = 0.f;
-    const int s = s0 + (lane >> 2);
-    if (s < split) {
-      const float* ps = pb + (int64_t)s * KA_PART_FLOATS;
-      const float l = ps[H + h];
-      if (l != 0.f) {                                 // a state that saw a key
-        w = exp2f(ps[h] - mx);
-        L += w * l;
-      }
+    for (int i = 0; i < BATCH; i++)
+      if (s + i * SLICES < split)
+#pragma unroll
+        for (int k = 0; k < GROUPS; k++) x[i][k] = __ldcg(o + (int64_t)(s + i * SLICES) * (KA_PART_FLOATS / 4) + k * 4 * H);
+  };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  load(z);
+  {
+    const int hw = tid % H, r = tid / H;
+    float mx = -INFINITY, L = 0.f;
+#pragma unroll 4
+    for (int s = r; s < split; s += ROWS) mx = fmaxf(mx, pb[(int64_t)s * KA_PART_FLOATS + hw]);
+    red[r][hw] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ROWS; i++) mx = fmaxf(mx, red[i][hw]);
+    __syncthreads();
+#pragma unroll 4
+    for (int s = r; s < split; s += ROWS) {
+      const float* ps = pb + (int64_t)s * KA_PART_FLOATS + hw;
+      const float l = ps[H], w = l != 0.f ? exp2f(ps[0] - mx) : 0.f;   // l = 0: a state without keys
+      weight[s][hw] = w;
+      L += w * l;
     }
-    const int n = min(8, split - s0);
+    red[r][hw] = L;
+    __syncthreads();
+    if (r == 0) {
+      L = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const float wi = __shfl_sync(0xFFFFFFFFu, w, 4 * i + hl);
-      if (i < n && wi != 0.f) {                       // a state without keys holds no O
-        const float4* o = reinterpret_cast<const float4*>(pb + (int64_t)(s0 + i) * KA_PART_FLOATS + 2 * H) + dg * H + h;
-        const float4 x = o[0], y = o[(D / 8) * H];
-        a[0] += wi * x.x;
-        a[1] += wi * x.y;
-        a[2] += wi * x.z;
-        a[3] += wi * x.w;
-        a[4] += wi * y.x;
-        a[5] += wi * y.y;
-        a[6] += wi * y.z;
-        a[7] += wi * y.w;
+      for (int i = 0; i < ROWS; i++) L += red[i][hw];
+      sum[hw] = L;
+      if (lse && dims == 0) lse[bq * H + hw] = L == 0.f ? -INFINITY : (mx + log2f(L)) * KA_LN2;
+    }
+    __syncthreads();
+  }
+  float4 a[GROUPS] = {};
+  for (int s = z; s < split; s += BATCH * SLICES) {
+    if (s > z) load(s);
+#pragma unroll
+    for (int i = 0; i < BATCH; i++) {
+      const float w = s + i * SLICES < split ? weight[s + i * SLICES][h] : 0.f;
+      if (w != 0.f) {                                 // a state without keys holds no O
+#pragma unroll
+        for (int k = 0; k < GROUPS; k++) {
+          a[k].x += w * x[i][k].x;
+          a[k].y += w * x[i][k].y;
+          a[k].z += w * x[i][k].z;
+          a[k].w += w * x[i][k].w;
+        }
       }
     }
   }
+  if (SLICES > 1) {
+    float4* slice = reinterpret_cast<float4*>(weight);
+    __syncthreads();
+    if (z > 0) slice[tid - 4 * H] = a[0];
+    __syncthreads();
+    if (z > 0) return;
 #pragma unroll
-  for (int k = 16; k >= 4; k >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, k);
-  const float inv = L == 0.f ? 0.f : 1.0f / L;        // no visible key: zeros
-  if (lse && threadIdx.x < 4) lse[bq * H + h] = L == 0.f ? -INFINITY : (mx + log2f(L)) * KA_LN2;
-  uint16_t* o = out + (bq * H + h) * D + 4 * dg;
-  *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv));
-  *reinterpret_cast<uint2*>(o + D / 2) = make_uint2(pack_bf16x2(a[4] * inv, a[5] * inv), pack_bf16x2(a[6] * inv, a[7] * inv));
+    for (int i = 0; i < SLICES - 1; i++) {
+      const float4 y = slice[tid + i * 4 * H];
+      a[0].x += y.x;
+      a[0].y += y.y;
+      a[0].z += y.z;
+      a[0].w += y.w;
+    }
+  }
+  const float inv = sum[h] == 0.f ? 0.f : 1.0f / sum[h];   // no visible key: zeros
+#pragma unroll
+  for (int k = 0; k < GROUPS; k++)
+    *reinterpret_cast<uint2*>(out + (bq * H + h) * D + dims + 16 * k + 4 * g) =
+        make_uint2(pack_bf16x2(a[k].x * inv, a[k].y * inv), pack_bf16x2(a[k].z * inv, a[k].w * inv));
 }
 
 // ------------------------------------------------------------------ host side
-// CTAs per query: the number whose time, in chunks (1.2 us each), is least.  A CTA costs its
-// chunks and about KA_FIXED more (set-up, the first keys, the output), a split call KA_JOIN
-// more; CTAs run one to an SM.  At most KA_WAVES CTAs an SM, which bounds the partial states to
-// 80 MB.  The GPU's 152 SMs are a constant here so that the workspace can be sized without a
-// device.  One query over 600 entries: 14 us over 12 CTAs, 21 in one.
-constexpr int KA_SMS = 152;
-constexpr int KA_FIXED = 5, KA_JOIN = 4, KA_WAVES = 4;
+// CTAs per query: the number whose time is least.  In chunks (1.2 us each) a CTA costs those it
+// has and about KA_FIXED more (set-up, the first keys, the output), one to an SM; the join costs
+// 2.5, 1/16 for each state of a query and 1/48 for each of the call.  At most KA_WAVES CTAs an SM, which
+// bounds the partial states to 80 MB.  The GPU's 152 SMs are a constant here so that the workspace can be
+// sized without a device.  One query, us (undivided / as chosen): 600 entries 21.3 / 12.4, 2000
+// 47.1 / 14.9, 8000 157 / 17.3.
+constexpr int KA_FIXED = 6, KA_WAVES = 4;
+constexpr int KC_LATENT = 4;                          // queries whose join takes CTAs of many threads
 
 int keys_split(int64_t BQ, int64_t chunks) {
   if (BQ <= 0) return 1;
   int best = 1;
-  int64_t best_cost = ceil_div(BQ, KA_SMS) * (KA_FIXED + chunks);
+  int64_t best_cost = 48 * ceil_div(BQ, KA_SMS) * (KA_FIXED + chunks);   // in 48ths
   for (int s = 2; s <= KA_SMS && s <= chunks && BQ * s <= KA_WAVES * KA_SMS; s++) {
-    const int64_t cost = ceil_div(BQ * s, KA_SMS) * (KA_FIXED + ceil_div(chunks, s)) + KA_JOIN;
+    const int64_t cost = 48 * ceil_div(BQ * s, KA_SMS) * (KA_FIXED + ceil_div(chunks, s)) + 120 + 3 * s + BQ * s;
     if (cost < best_cost) {
       best = s;
       best_cost = cost;
@@ -717,12 +761,17 @@ static cudaError_t keys_launch(const KeysParams& p, int64_t BQ, const CUtensorMa
   e = cudaLaunchKernelEx(&cfg, keys_attn_kernel<F16>, p, mq, mr, ms);
   if (e != cudaSuccess || p.split == 1) return e;
   cudaLaunchConfig_t cc = {};
-  cc.gridDim = dim3((unsigned)(BQ * 16));
-  cc.blockDim = dim3(256);
+  // Few queries: CTAs of many threads, one to an SM.  Else one slice; up to four states then
+  // want the registers of half as many CTAs (4 states of 111 queries 132 us in all, 136 otherwise).
+  const bool latent = BQ <= KC_LATENT, few = !latent && p.split <= 4;
+  cc.gridDim = dim3((unsigned)(BQ * (few ? D / 32 : D / 16)));
+  cc.blockDim = dim3((latent ? 4 : 1) * H * 4);
   cc.stream = stream;
   cc.attrs = attr;
   cc.numAttrs = 1;
-  return cudaLaunchKernelEx(&cc, keys_combine_kernel, (const float*)p.part, p.split, p.out, p.lse);
+  auto* kernel = latent ? keys_combine_kernel<4, 1, 8, KA_SMS>
+                 : few ? keys_combine_kernel<1, 2, 4, 4> : keys_combine_kernel<1, 1, 8, KA_WAVES * KA_SMS / (KC_LATENT + 1)>;
+  return cudaLaunchKernelEx(&cc, kernel, (const float*)p.part, p.split, p.out, p.lse);
 }
 
 // Calls that window_attention.cu takes: short windows of at least four queries a sequence, and

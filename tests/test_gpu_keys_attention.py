@@ -371,6 +371,23 @@ def test_dense_one_cta_a_query_equals_the_split():
         check(o1[0, 0], l1[0, 0], ref.bf16(q[0, i]), keys, SCALE, ref.U_F16, i)
 
 
+@pytest.mark.parametrize("B,n,max_n", [(1, 9000, 9000), (4, 2500, 2500), (5, 2500, 2500), (12, 1200, 1200),
+                                       (60, 900, 900), (1, 70, 9000), (1, 0, 9000), (6, 150, 40000), (50, 3, 30000)])
+def test_dense_joins(B, n, max_n):
+    """Few queries of many states, more queries of fewer, states without keys."""
+    g = synth.rng(43)
+    kv = draw_entries(g, B, max(8, -(-n // 8) * 8))
+    q, rows = synth.main_queries(g, B, 1), draw_rows(g, False, B, 140)
+    pos = np.full((B, 1), max(n, 139)) + np.arange(B)[:, None]
+    base = pos[:, 0] - 139
+    ns = [max(0, n - 3 * b) for b in range(B)]
+    assert csa2.dense_attn_workspace_size(B, 1, max_n) > 256
+    o, l = run_dense(make_cache(kv, ns, 1), q, rows, base, pos, max_n)
+    for b in sorted({0, 1, B // 2, B - 1} & set(range(B))):
+        keys = ref.dense_keys(oracle.dequant_main(kv[b]), ns[b], 1, ref.row_values(rows[b]), int(base[b]), int(pos[b, 0]))
+        check(o[b, 0], l[b, 0], ref.bf16(q[b, 0]), keys, SCALE, ref.U_F16, b)
+
+
 def test_dense_padding_positions_and_bounds():
     g = synth.rng(10)
     kv, rows, q = draw_entries(g, 2, 64), draw_rows(g, False, 2, 200), synth.main_queries(g, 2, 3)
