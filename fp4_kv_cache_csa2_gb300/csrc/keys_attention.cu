@@ -420,15 +420,16 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           // (what is not seen may hold anything, infinities among it)
           ok = ok && ka_wait(&sm.row_full[kb][h], use, sm, p.hdr, 48);
           if (F16 || keys < KA_KEYS) {
-#pragma unroll 4
-            for (int i = ft; i < KA_HALF / 16; i += KA_FILL) {
-              uint4* u = reinterpret_cast<uint4*>(kt) + i;
-              if (((i >> 3) & (KA_KEYS - 1)) >= keys) *u = make_uint4(0u, 0u, 0u, 0u);
-              else if (F16) {
-                const uint4 x = *u;
-                *u = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
-              }
-            }
+            uint4* u = reinterpret_cast<uint4*>(kt) + ft;
+            uint4 x[KA_HALF / 16 / KA_FILL] = {};
+#pragma unroll
+            for (int i = 0; i < KA_HALF / 16 / KA_FILL; i++)
+              if (F16 && (((ft + i * KA_FILL) >> 3) & (KA_KEYS - 1)) < keys) x[i] = u[i * KA_FILL];
+#pragma unroll
+            for (int i = 0; i < KA_HALF / 16 / KA_FILL; i++)
+              if (F16 || (((ft + i * KA_FILL) >> 3) & (KA_KEYS - 1)) >= keys)
+                u[i * KA_FILL] = make_uint4(bf16x2_to_f16x2(x[i].x), bf16x2_to_f16x2(x[i].y), bf16x2_to_f16x2(x[i].z),
+                                            bf16x2_to_f16x2(x[i].w));
           }
         }
         tc::fence_proxy_async_smem();
@@ -716,8 +717,8 @@ keys_combine_kernel(const float* __restrict__ part, int split, uint16_t* __restr
 // has and about KA_FIXED more (set-up, the first keys, the output), one to an SM; the join costs
 // 2.5, 1/16 for each state of a query and 1/48 for each of the call.  At most KA_WAVES CTAs an SM, which
 // bounds the partial states to 80 MB.  The GPU's 152 SMs are a constant here so that the workspace can be
-// sized without a device.  One query, us (undivided / as chosen): 600 entries 21.3 / 12.4, 2000
-// 47.1 / 14.9, 8000 157 / 17.3.
+// sized without a device.  One query, us (undivided / as chosen): 600 entries 20.5 / 11.7, 2000
+// 46.4 / 13.8, 8000 157 / 17.3.
 constexpr int KA_FIXED = 6, KA_WAVES = 4;
 constexpr int KC_LATENT = 4;                          // queries whose join takes CTAs of many threads
 
