@@ -33,8 +33,9 @@
 // Shared memory: three K buffers of [64 keys][512 dims] (two halves of 32 KB, four SW128
 // column chunks each; the third takes Q on its way to TMEM first) and a staging area of
 // 18 KB for the next chunk's entries as stored.  Roles:
-// warps 0..3 move Q, then softmax and output; warps 4..11 fill the K buffers (from the
-// staged bytes through registers; bf16 rows are rounded in place if need be); warp 12
+// warps 0..3 move Q, then softmax; warps 4..11 fill the K buffers (from the
+// staged bytes through registers; bf16 rows are rounded in place if need be); warps 0..7
+// write the output; warp 12
 // issues the MMAs, S of chunk c + 1 before O of chunk c, so that the softmax of a chunk
 // runs beside the products of its neighbours; warp 13 issues the copies.  All waits are
 // bounded; a timeout reports CSA2_ERR_TIMEOUT and every thread still takes every barrier.
@@ -43,7 +44,8 @@
 
 namespace csa2 {
 
-constexpr int KA_SOFT_WARPS = 4;                          // softmax, output: lane = (half of the dims or keys, head)
+constexpr int KA_SOFT_WARPS = 4;                          // softmax: lane = (half of the dims or keys, head)
+constexpr int KA_OUT_WARPS = 2 * KA_SOFT_WARPS;             // output: these and the first fill warps
 constexpr int KA_FILL_WARPS = 8;                          // K buffers
 constexpr int KA_FILL = 32 * KA_FILL_WARPS;
 constexpr int KA_MMA_WARP = KA_SOFT_WARPS + KA_FILL_WARPS;
@@ -54,7 +56,7 @@ constexpr int KA_COL = 64 * 128;                          // [64 rows][64 dims] 
 constexpr int KA_HALF = 4 * KA_COL;                       // half of a K buffer: 256 dims
 constexpr int KA_BUFS = 3;                                // K buffers: chunk c in c % 3
 constexpr int KA_OFF_STAGE = KA_BUFS * 2 * KA_HALF;
-constexpr int KA_OFF_OUT = 0;                             // outputs: [32 rows][128 dims] bf16 a softmax warp, over the K buffers
+constexpr int KA_OFF_OUT = 0;                             // outputs: [32 rows][128 dims] bf16 an output warp, over the K buffers
 constexpr int KA_OFF_SMALL = KA_OFF_STAGE + KA_KEYS * MAIN_BYTES;
 constexpr int KA_TMEM_COLS = 512;
 constexpr int KA_O_COL = 0;                               // half h of the dims: lanes 16h .. of each quarter
@@ -79,6 +81,7 @@ struct KaSmall {
   uint64_t free_[KA_BUFS];            // O of the chunk in K buffer i is done
   uint64_t s_full[2];                 // S of every second chunk is done
   uint64_t p_ready[2];                // its P is written, O rescaled if needed (a softmax warp each)
+  float sum[H];                       // of the softmax
   uint32_t tmem_base;
   int err;
 };
@@ -129,8 +132,9 @@ __device__ __forceinline__ KaRun ka_run(const KeysParams& p, int64_t bq, int b, 
     if (en < 0) en = 0;
   }
   const int64_t cw = ceil_div(wn, KA_KEYS), cr = cw + ceil_div(sn, KA_KEYS), nc = cr + ceil_div(en, KA_KEYS);
-  const int64_t c_lo = nc * sp / split;
-  q.n = (int)(nc * (sp + 1) / split - c_lo);
+  const uint32_t each = (uint32_t)nc / (uint32_t)split, more = (uint32_t)nc - each * (uint32_t)split;   // nc < 2^27
+  const int64_t c_lo = (int64_t)sp * each + min((uint32_t)sp, more);
+  q.n = (int)(each + ((uint32_t)sp < more ? 1u : 0u));
   q.cw = (int)max(cw - c_lo, (int64_t)0);
   q.cr = (int)max(cr - c_lo, (int64_t)0);
   q.r0 = row + KA_KEYS * c_lo;
@@ -165,10 +169,11 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     return;
   }
   const int split = p.split;
-  const int64_t bq = blockIdx.x / split;
-  const int sp = blockIdx.x % split;
-  const int b = (int)(bq / p.Q);
+  const int64_t bq = blockIdx.x / (uint32_t)split;
+  const int sp = (int)(blockIdx.x % (uint32_t)split);
+  const int b = (int)((uint32_t)bq / (uint32_t)p.Q);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  float* part = p.part + (int64_t)blockIdx.x * KA_PART_FLOATS;   // with split > 1
 
   // ---------------- set-up (reads no input: overlaps the previous kernel)
   if (warp == KA_MMA_WARP) tc::tmem_alloc(&sm.tmem_base, KA_TMEM_COLS);
@@ -543,64 +548,69 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       if (lane == 0) tc::bar_arrive(&sm.p_ready[c & 1]);
     }
 
-    // ---------------- output: lane = (head, half of the dims)
+    const float l = l_sum + __shfl_xor_sync(0xFFFFFFFFu, l_sum, 16);
+    if (half == 0) {
+      sm.sum[head] = l;
+      if (split > 1) {
+        part[head] = m_used;
+        part[H + head] = l;
+      } else if (p.lse) {                             // l = 0: no visible key
+        p.lse[bq * H + head] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * KA_LN2;
+      }
+    }
+  }
+
+  if (warp < KA_OUT_WARPS) {
+    // ================= output: lane = (half of the dims, head), 128 of the half's dims a warp
+    // (four warps alone take 3900 cycles, half of what the CTA needs beside its chunks)
     if (n_ch > 0) {
-      ok = ok && ka_wait(&sm.free_[(n_ch - 1) % KA_BUFS], (n_ch - 1) / KA_BUFS, sm, p.hdr, 51);
+      const int last = n_ch - 1;
+      if (*(volatile int*)&sm.err == 0) ka_wait(&sm.free_[last % KA_BUFS], last / KA_BUFS, sm, p.hdr, 51);
       tc::fence_after_sync();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const float m = m_used, l = l_sum + __shfl_xor_sync(0xFFFFFFFFu, l_sum, 16);
-    const bool none = l == 0.f;                       // no visible key: zeros
+    named_sync(2, 32 * KA_OUT_WARPS);                 // the sums
+    const int qt = warp & 3, half = lane >> 4, head = 16 * qt + (lane & 15), g0 = 128 * (warp >> 2);
+    const uint32_t o_addr = ((uint32_t)(qt * 32) << 16) + KA_O_COL + g0;
     if (split == 1) {
-      if (p.lse && half == 0) p.lse[bq * H + head] = none ? -INFINITY : (m + log2f(l)) * KA_LN2;
-      const float inv = 1.0f / l;
+      const float l = sm.sum[head], inv = 1.0f / l;
+      const bool none = l == 0.f;                     // no visible key: zeros
       // A lane holds 32 dims of its row at a time.  Stored from there, an instruction would touch
-      // 32 rows of 1 KB with 16 bytes each (7000 cycles an output); through shared memory (the K
+      // 32 rows of 1 KB with 16 bytes each (7000 cycles for 256 dims a lane); through shared memory (the K
       // buffers, whose last reader is done) it covers 256 bytes of two rows.
       unsigned char* mine = smem + KA_OFF_OUT + warp * 8192;
-      uint4* out = reinterpret_cast<uint4*>(p.out + (bq * H + 16 * warp) * D);
 #pragma unroll 1
-      for (int g = 0; g < D / 2; g += 128) {
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t o[32];
-          if (n_ch > 0) tmem_ld32(quarter + KA_O_COL + g + c, o);
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        if (n_ch > 0) tmem_ld32(o_addr + c, o);
 #pragma unroll
-          for (int x = 0; x < 4; x++) {
-            float f[8];
+        for (int x = 0; x < 4; x++) {
+          float f[8];
 #pragma unroll
-            for (int y = 0; y < 8; y++) f[y] = none ? 0.f : __uint_as_float(o[8 * x + y]) * inv;
-            *reinterpret_cast<uint4*>(mine + lane * 256 + ((((c >> 3) + x) ^ (lane & 7)) << 4)) =
-                make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-          }
+          for (int y = 0; y < 8; y++) f[y] = none ? 0.f : __uint_as_float(o[8 * x + y]) * inv;
+          *reinterpret_cast<uint4*>(mine + lane * 256 + ((((c >> 3) + x) ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
         }
-        __syncwarp();
+      }
+      __syncwarp();
+      uint4* out = reinterpret_cast<uint4*>(p.out + (bq * H + 16 * qt) * D);
 #pragma unroll 4
-        for (int x = 0; x < 16; x++) {                // lane `row` of the warp: head 16 warp + row % 16, half row / 16
-          const int row = 2 * x + half, u = lane & 15;
-          out[(row & 15) * (D / 8) + (D / 16) * (row >> 4) + g / 8 + u] =
-              *reinterpret_cast<const uint4*>(mine + row * 256 + ((u ^ (row & 7)) << 4));
-        }
-        __syncwarp();
+      for (int x = 0; x < 16; x++) {                  // lane `row` of the warp: head 16 qt + row % 16, half row / 16
+        const int row = 2 * x + half, u = lane & 15;
+        out[(row & 15) * (D / 8) + (D / 16) * (row >> 4) + g0 / 8 + u] =
+            *reinterpret_cast<const uint4*>(mine + row * 256 + ((u ^ (row & 7)) << 4));
       }
-    } else {
+    } else if (n_ch > 0) {
       // a partial state: O as [dims / 4][head][4], so that the lanes of a half write 256 bytes
-      float* part = p.part + (int64_t)blockIdx.x * KA_PART_FLOATS;
-      if (half == 0) {
-        part[head] = m;
-        part[H + head] = l;
-      }
-      float4* out = reinterpret_cast<float4*>(part + 2 * H) + (D / 8) * half * H + head;
-      if (n_ch > 0) {
+      float4* out = reinterpret_cast<float4*>(part + 2 * H) + ((D / 8) * half + g0 / 4) * H + head;
 #pragma unroll 1
-        for (int g = 0; g < D / 2; g += 32) {
-          uint32_t o[32];
-          tmem_ld32(quarter + KA_O_COL + g, o);
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_addr + c, o);
 #pragma unroll
-          for (int x = 0; x < 8; x++)
-            out[(g / 4 + x) * H] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                                               __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
-        }
+        for (int x = 0; x < 8; x++)
+          out[(c / 4 + x) * H] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                             __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
       }
     }
   }
