@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libcsa2.so")
@@ -101,11 +102,11 @@ _SIGNATURES = {
                               _P, _SZ, _P]),
     "csa2_decode_workspace_size": (_SZ, [_I, _I, _I, _I64, _I, _I]),
     "csa2_decode": (_I, [ctypes.POINTER(CacheStruct), ctypes.POINTER(DecodeArgs), _P, _SZ, _P]),
-    "csa2_qk_norm_rope": (_I, [ctypes.POINTER(QkArgs), _P, _SZ, _P]),
+    "csa2_qk_norm_rope": (_I, [_P, _P, _SZ, _P]),
     "csa2_window_attn_workspace_size": (_SZ, [_I, _I, _I, _I]),
-    "csa2_window_attn": (_I, [ctypes.POINTER(WindowArgs), _P, _SZ, _P]),
+    "csa2_window_attn": (_I, [_P, _P, _SZ, _P]),
     "csa2_dense_attn_workspace_size": (_SZ, [_I, _I, _I64]),
-    "csa2_dense_attn": (_I, [ctypes.POINTER(CacheStruct), ctypes.POINTER(DenseArgs), _P, _SZ, _P]),
+    "csa2_dense_attn": (_I, [ctypes.POINTER(CacheStruct), _P, _P, _SZ, _P]),
     "csa2_test_withhold_arrival": (_I, [_I]),
 }
 
@@ -338,63 +339,56 @@ def decode(mode: int, cache: Cache, *, q_pos, q, swa, swa_base_pos, scale: float
 # that every tensor lies contiguous on the device of the workspace.  bf16 and
 # E4M3 may come as their bits (16-bit and 8-bit integers).
 # A decode step makes these calls one after another, each of a few microseconds on
-# the GPU, so the checks are plain comparisons and the message is put together
-# only for a call that is refused.
-def _refuse(name: str, t, shape, what: str, device):
-    raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}; expected {what} "
-                     f"{tuple(shape)}, contiguous, on {device}")
-
-
+# the GPU, so the checks are plain comparisons, the arguments are packed in one go,
+# and the message is put together only for a call that is refused.
 @functools.cache
 def _types():
     """Types that hold bf16, window rows, 64-bit integers and float32."""
     import torch
     bf16 = (torch.bfloat16, torch.int16, torch.uint16)
-    return bf16, (*bf16, torch.uint8, torch.int8, torch.float8_e4m3fn), torch.int64, torch.float32
+    return bf16, (*bf16, torch.uint8, torch.int8, torch.float8_e4m3fn), (torch.int64,), (torch.float32,)
 
 
-def _bits16(name: str, t, shape, device):
-    """Address of a contiguous bf16 tensor of this shape on this device."""
-    if t.shape != shape or t.dtype not in _types()[0] or t.device != device or not t.is_contiguous():
-        _refuse(name, t, shape, "bf16", device)
+def _packer(cls):
+    """The layout of a struct of C arguments; bytes packed by it stand for the struct."""
+    codes = {ctypes.c_int: "i", ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "Q"}
+    s = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_) + "0q")
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_qk, _pack_window, _pack_dense = _packer(QkArgs), _packer(WindowArgs), _packer(DenseArgs)
+
+
+def _refuse(name: str, t, shape, what, index):
+    raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}; expected "
+                     f"{tuple(shape)} of {what}, on device {index}")
+
+
+def _at(name: str, t, shape, types, index):
+    """Address of a contiguous tensor of this shape and one of these types on CUDA device `index`."""
+    if t.shape != shape or t.dtype not in types or t.get_device() != index or not t.is_contiguous():
+        _refuse(name, t, shape, f"{types}, contiguous", index)
     return t.data_ptr()
 
 
-def _rows(name: str, t, shape, device):
-    """Address of window rows, bf16 or E4M3."""
-    if t.shape != shape or t.dtype not in _types()[1] or t.device != device or not t.is_contiguous():
-        _refuse(name, t, shape, "bf16 or E4M3", device)
-    return t.data_ptr()
+def _tokens(name: str, t, shape, inner, types, index):
+    """Address of tokens whose strides but the first are `inner`, and that stride."""
+    first, *rest = t.stride()
+    if t.shape != shape or rest != inner or t.dtype not in types or t.get_device() != index:
+        _refuse(name, t, shape, f"{types}, inner strides {inner}", index)
+    return t.data_ptr(), first
 
 
-def _int64(name: str, t, shape, device):
-    if t.shape != shape or t.dtype is not _types()[2] or t.device != device or not t.is_contiguous():
-        _refuse(name, t, shape, "64-bit integers", device)
-    return t.data_ptr()
-
-
-def _float32(name: str, t, shape, device):
-    if t.shape != shape or t.dtype is not _types()[3] or t.device != device or not t.is_contiguous():
-        _refuse(name, t, shape, "float32", device)
-    return t.data_ptr()
-
-
-def _tokens(name: str, t, shape, inner, device):
-    """Address of bf16 tokens whose strides but the first are `inner`."""
-    if t.shape != shape or t.stride()[1:] != inner or t.dtype not in _types()[0] or t.device != device:
-        _refuse(name, t, shape, f"bf16 with inner strides {inner}, not", device)
-    return t.data_ptr()
-
-
-def _call(fn, device, stream, *args):
-    """fn(*args, stream) with `device` current; stream None: the device's current one, whose
+def _call(fn, index, stream, *args):
+    """fn(*args, stream) with device `index` current; stream None: the device's current one, whose
     handle is asked for directly (a stream object costs as much as the launch)."""
     import torch
-    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
         status = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = fn(*args, handle)
     if status != 0:
         raise Csa2Error(fn.__name__, status)
@@ -404,27 +398,33 @@ def qk_norm_rope(pos, rope_cs, ws: Workspace, *, q=None, q_weight=None, q_out=No
                  k_slot=None, eps: float = 1e-6, stream=None):
     """RMSNorm per head and rotation of the last 64 channels: queries q [T][64][512]
     -> q_out, window keys k [T][512] -> row k_slot[t] (None: t) of rows [..][512]
-    (bf16, or uint8: E4M3).  Tokens with pos -1 write nothing.  q and k may be
+    (bf16, or E4M3).  Tokens with pos -1 write nothing.  q and k may be
     views with a larger token stride; q_out may be q itself."""
-    dev, T = ws.buf.device, pos.numel()
-    table = rope_cs.shape[0]
-    qa = qs = qw = qo = ka = ks = kw = ro = sl = None
-    n_rows = fp8 = 0
+    buf, T, table = ws.buf, pos.numel(), rope_cs.shape[0]
+    dev = buf.get_device()
+    bf16, row_types, i64, f32 = _types()
+    qa = qs = qw = qo = ka = ks = kw = ro = sl = n_rows = fp8 = 0
     if q is not None:
-        qa = _tokens("q", q, (T, N_HEADS, D_LATENT), (D_LATENT, 1), dev)
-        qs = q.stride(0) if T > 1 else N_HEADS * D_LATENT
-        qw = None if q_weight is None else _float32("q_weight", q_weight, (D_LATENT,), dev)
-        qo = _bits16("q_out", q_out, (T, N_HEADS, D_LATENT), dev)
+        shape = (T, N_HEADS, D_LATENT)
+        qa, qs = _tokens("q", q, shape, [D_LATENT, 1], bf16, dev)
+        if T <= 1:
+            qs = N_HEADS * D_LATENT
+        if q_weight is not None:
+            qw = _at("q_weight", q_weight, (D_LATENT,), f32, dev)
+        qo = _at("q_out", q_out, shape, bf16, dev)
     if k is not None:
-        ka = _tokens("k", k, (T, D_LATENT), (1,), dev)
-        ks = k.stride(0) if T > 1 else D_LATENT
-        kw = None if k_weight is None else _float32("k_weight", k_weight, (D_LATENT,), dev)
-        ro = _rows("rows", rows, (*rows.shape[:-1], D_LATENT), dev)
+        ka, ks = _tokens("k", k, (T, D_LATENT), [1], bf16, dev)
+        if T <= 1:
+            ks = D_LATENT
+        if k_weight is not None:
+            kw = _at("k_weight", k_weight, (D_LATENT,), f32, dev)
+        ro = _at("rows", rows, (*rows.shape[:-1], D_LATENT), row_types, dev)
         n_rows, fp8 = rows.numel() // D_LATENT, 1 if rows.element_size() == 1 else 0
-        sl = None if k_slot is None else _int64("k_slot", k_slot, (T,), dev)
-    a = QkArgs(T, _int64("pos", pos, (T,), dev), _float32("rope_cs", rope_cs, (table, D_ROPE // 2, 2), dev), table,
-               float(eps), fp8, qa, qs or 0, qw, qo, ka, ks or 0, kw, ro, n_rows, sl)
-    _call((_lib or load()).csa2_qk_norm_rope, dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
+        if k_slot is not None:
+            sl = _at("k_slot", k_slot, (T,), i64, dev)
+    a = _pack_qk(T, _at("pos", pos, (T,), i64, dev), _at("rope_cs", rope_cs, (table, D_ROPE // 2, 2), f32, dev), table,
+                 eps, fp8, qa, qs, qw, qo, ka, ks, kw, ro, n_rows, sl)
+    _call((_lib or load()).csa2_qk_norm_rope, dev, stream, a, buf.data_ptr(), ws.nbytes)
 
 
 def window_attn_workspace_size(B: int, Q: int, W: int, n_sink: int) -> int:
@@ -434,18 +434,21 @@ def window_attn_workspace_size(B: int, Q: int, W: int, n_sink: int) -> int:
 def window_attn(q, rows, swa_base_pos, q_pos, scale: float, out, ws: Workspace, *, W: int, sinks=None, lse=None,
                 stream=None):
     """Queries [B][Q][64][512] over the window rows [B][S][512] of positions
-    t-W+1 .. t and the sinks [B][n][512] before them (both bf16, or both uint8:
+    t-W+1 .. t and the sinks [B][n][512] before them (both bf16, or both
     E4M3).  lse: float32 [B][Q][64] or None."""
-    dev, (B, Q), S, n = ws.buf.device, q_pos.shape, rows.shape[1], 0 if sinks is None else sinks.shape[1]
+    buf, (B, Q), S, n = ws.buf, q_pos.shape, rows.shape[1], 0 if sinks is None else sinks.shape[1]
+    dev = buf.get_device()
+    bf16, row_types, i64, f32 = _types()
     shape = (B, Q, N_HEADS, D_LATENT)
     if n and sinks.element_size() != rows.element_size():
         _refuse("sinks", sinks, (B, n, D_LATENT), "elements of the rows' size", dev)
-    a = WindowArgs(B, Q, S, W, n, float(scale), _int64("q_pos", q_pos, (B, Q), dev), _bits16("q", q, shape, dev),
-                   _rows("rows", rows, (B, S, D_LATENT), dev), _int64("swa_base_pos", swa_base_pos, (B,), dev),
-                   _rows("sinks", sinks, (B, n, D_LATENT), dev) if n else None, _bits16("out", out, shape, dev),
-                   None if lse is None else _float32("lse", lse, (B, Q, N_HEADS), dev),
-                   1 if rows.element_size() == 1 else 0)
-    _call((_lib or load()).csa2_window_attn, dev, stream, ctypes.byref(a), ws.ptr, ws.nbytes)
+    a = _pack_window(B, Q, S, W, n, scale, _at("q_pos", q_pos, (B, Q), i64, dev), _at("q", q, shape, bf16, dev),
+                     _at("rows", rows, (B, S, D_LATENT), row_types, dev),
+                     _at("swa_base_pos", swa_base_pos, (B,), i64, dev),
+                     _at("sinks", sinks, (B, n, D_LATENT), row_types, dev) if n else 0, _at("out", out, shape, bf16, dev),
+                     0 if lse is None else _at("lse", lse, (B, Q, N_HEADS), f32, dev),
+                     1 if rows.element_size() == 1 else 0)
+    _call((_lib or load()).csa2_window_attn, dev, stream, a, buf.data_ptr(), ws.nbytes)
 
 
 def dense_attn_workspace_size(B: int, Q: int, max_n: int) -> int:
@@ -455,17 +458,20 @@ def dense_attn_workspace_size(B: int, Q: int, max_n: int) -> int:
 def dense_attn(cache: Cache, q, swa, swa_base_pos, q_pos, scale: float, out, ws: Workspace, *, max_n: int, lse=None,
                stream=None):
     """Queries [B][Q][64][512] over every visible cache entry and the 128-token
-    window, rows swa [B][S][512] (bf16, or uint8: E4M3).  max_n: the most entries
+    window, rows swa [B][S][512] (bf16, or E4M3).  max_n: the most entries
     a query sees (it sizes the work split, nothing else).  lse: float32
     [B][Q][64] or None."""
-    dev, (B, Q), S = ws.buf.device, q_pos.shape, swa.shape[1]
+    buf, (B, Q), S = ws.buf, q_pos.shape, swa.shape[1]
+    dev = buf.get_device()
     if B != cache.B:
         raise ValueError(f"q_pos: {B} sequences, the cache has {cache.B}")
-    if cache.main_kv.device != dev:
-        raise ValueError(f"the cache is on {cache.main_kv.device}, the workspace on {dev}")
+    if cache.main_kv.get_device() != dev:
+        raise ValueError(f"the cache is on {cache.main_kv.device}, the workspace on {buf.device}")
+    bf16, row_types, i64, f32 = _types()
     shape = (B, Q, N_HEADS, D_LATENT)
-    a = DenseArgs(B, Q, S, float(scale), max_n, _int64("q_pos", q_pos, (B, Q), dev), _bits16("q", q, shape, dev),
-                  _rows("swa", swa, (B, S, D_LATENT), dev), _int64("swa_base_pos", swa_base_pos, (B,), dev),
-                  _bits16("out", out, shape, dev), None if lse is None else _float32("lse", lse, (B, Q, N_HEADS), dev),
-                  1 if swa.element_size() == 1 else 0)
-    _call((_lib or load()).csa2_dense_attn, dev, stream, ctypes.byref(cache.struct()), ctypes.byref(a), ws.ptr, ws.nbytes)
+    a = _pack_dense(B, Q, S, scale, max_n, _at("q_pos", q_pos, (B, Q), i64, dev), _at("q", q, shape, bf16, dev),
+                    _at("swa", swa, (B, S, D_LATENT), row_types, dev),
+                    _at("swa_base_pos", swa_base_pos, (B,), i64, dev), _at("out", out, shape, bf16, dev),
+                    0 if lse is None else _at("lse", lse, (B, Q, N_HEADS), f32, dev),
+                    1 if swa.element_size() == 1 else 0)
+    _call((_lib or load()).csa2_dense_attn, dev, stream, ctypes.byref(cache.struct()), a, buf.data_ptr(), ws.nbytes)
