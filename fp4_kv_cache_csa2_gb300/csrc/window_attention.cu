@@ -121,14 +121,58 @@ __device__ __forceinline__ bool wa_not_finite(const uint4& v) {
          (v.z >> 16 & E) == E || (v.w & E) == E || (v.w >> 16 & E) == E;
 }
 
-// Barrier of the ring warps that tells each of them whether any thread came with x set.  A flag
-// in shared memory, read behind a plain barrier, could already be the next tile's: a warp that
-// reads it late would part from the others.
-__device__ __forceinline__ bool wa_ring_any(bool x) {
+// Barrier ID of N threads that tells each of them whether any came with x set.  A flag in shared
+// memory, read behind a plain barrier, could already be the next tile's: a warp that reads it late
+// would part from the others.
+template <int ID, int N>
+__device__ __forceinline__ bool wa_any(bool x) {
   uint32_t r;
-  asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, 1, %2, a;\n"
-               " selp.u32 %0, 1, 0, b;\n}\n" : "=r"(r) : "r"((uint32_t)x), "n"(WA_RING) : "memory");
+  asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, %2, %3, a;\n"
+               " selp.u32 %0, 1, 0, b;\n}\n" : "=r"(r) : "r"((uint32_t)x), "n"(ID), "n"(N) : "memory");
   return r != 0;
+}
+
+// A row of the window buffer, 16 bytes of each half a lane (E4M3: 16 dims in the first)
+__device__ __forceinline__ void wa_load_row(uint4* v, const uint8_t* row, int fp8, int lane) {
+  const uint4* src = reinterpret_cast<const uint4*>(row);
+  v[0] = __ldg(src + lane);
+  if (!fp8) v[1] = __ldg(src + 32 + lane);
+}
+
+// to its slot, as bf16.  False: it is not finite, and stays out unless `any` row may go in
+__device__ __forceinline__ bool wa_put_row(unsigned char* ring, int slot, const uint4* v, int fp8, bool any, int lane) {
+  uint4 lo = v[0], hi = v[1];
+  if (fp8) {
+    const uint32_t e[4] = {lo.x, lo.y, lo.z, lo.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int y = 0; y < 4; y++) {
+      o[2 * y] = wa_f16x2_to_bf16x2(e4m3x2_to_f16x2(e[y]));
+      o[2 * y + 1] = wa_f16x2_to_bf16x2(e4m3x2_to_f16x2(e[y] >> 16));
+    }
+    lo = make_uint4(o[0], o[1], o[2], o[3]);
+    hi = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  if (!any && __any_sync(0xFFFFFFFFu, wa_not_finite(lo) || wa_not_finite(hi))) return false;
+  const int u0 = fp8 ? 2 * lane : lane, u1 = fp8 ? 2 * lane + 1 : 32 + lane;   // 16-byte units
+  unsigned char* dst = ring + slot * 128;
+  *reinterpret_cast<uint4*>(dst + (u0 >> 3) * WA_KCOL + (((u0 ^ slot) & 7) << 4)) = lo;
+  *reinterpret_cast<uint4*>(dst + (u1 >> 3) * WA_KCOL + (((u1 ^ slot) & 7) << 4)) = hi;
+  return true;
+}
+
+// The rows that a tile's queries see: both queries at once when they together fit the ring.
+struct WaTile {
+  int lo, hi;                         // rows [lo, hi), if joint
+  bool joint;
+};
+
+__device__ __forceinline__ WaTile wa_tile(const WaQuery& q0, const WaQuery& q1, int R) {
+  WaTile t;
+  t.lo = q0.wn == 0 ? q1.r0 : (q1.wn == 0 ? q0.r0 : min(q0.r0, q1.r0));
+  t.hi = max(q0.wn ? q0.r0 + q0.wn : 0, q1.wn ? q1.r0 + q1.wn : 0);
+  t.joint = q0.wn == 0 || q1.wn == 0 || t.hi - t.lo <= R;
+  return t;
 }
 
 // bits [a, b) of the 32 from g on
@@ -194,6 +238,56 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
   const int pairs = (p.Q + 1) >> 1;
   const int64_t tiles = (int64_t)B * pairs;
   bool ok = true;
+  const int64_t k_lo = tiles * blockIdx.x / gridDim.x, k_hi = tiles * (blockIdx.x + 1) / gridDim.x;
+  const int R = slots - p.n_sink;                     // window slots
+  const size_t row_bytes = p.rows_fp8 ? D : 2 * D;
+  int held_b = -1, rl = 0, rh = 0, ns = 0;            // the ring: rows [rl, rh) and sinks [0, ns) of sequence held_b
+  if (warp != WA_COPY_WARP) {
+    // the first tile's window is loaded by every other warp (a call of one tile a CTA: 15 us, 19 with the
+    // ring warps alone), its queries by that one meanwhile.  If a row is not finite, the ring
+    // warps begin anew
+    const int b = (int)(k_lo / pairs), i = 2 * (int)(k_lo - (int64_t)b * pairs);
+    const int64_t at = (int64_t)b * p.Q + i;
+    if (tid == 0) {
+      sm.next_bq[0] = (uint32_t)at;
+      tc::bar_arrive(&sm.told[0]);
+    }
+    const int64_t base = p.base_pos[b];
+    const WaQuery q0 = wa_query(p, p.q_pos[at], base, false);
+    const WaQuery q1 = wa_query(p, i + 1 < p.Q ? p.q_pos[at + 1] : -1, base, false);
+    const WaTile t = wa_tile(q0, q1, R);
+    const int n_row = t.joint ? max(t.hi - t.lo, 0) : 0, n_sink = t.joint ? max(q0.sn, q1.sn) : 0;
+    const uint8_t* rows = p.rows + ((size_t)b * (size_t)p.S + (size_t)t.lo) * row_bytes;
+    const uint8_t* sinks = p.sinks + (size_t)b * (size_t)p.n_sink * row_bytes;
+    bool bad = !t.joint;
+#pragma unroll 1
+    for (int x0 = warp; x0 < n_row + n_sink; x0 += 4 * WA_COPY_WARP) {
+      uint4 v[4][2];
+#pragma unroll
+      for (int y = 0; y < 4; y++) {
+        const int x = x0 + y * WA_COPY_WARP;
+        v[y][0] = v[y][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (x < n_row + n_sink)
+          wa_load_row(v[y], x < n_row ? rows + (size_t)x * row_bytes : sinks + (size_t)(x - n_row) * row_bytes, p.rows_fp8, lane);
+      }
+#pragma unroll
+      for (int y = 0; y < 4; y++) {
+        const int x = x0 + y * WA_COPY_WARP;
+        if (x >= n_row + n_sink) continue;
+        int slot = p.n_sink + t.lo % R + x;
+        if (slot >= slots) slot -= R;
+        if (x >= n_row) slot = x - n_row;
+        if (!wa_put_row(smem, slot, v[y], p.rows_fp8, false, lane)) bad = true;
+      }
+    }
+    tc::fence_proxy_async_smem();
+    if (!wa_any<2, 32 * WA_COPY_WARP>(bad)) {
+      held_b = b;
+      rl = t.lo;
+      rh = t.lo + n_row;
+      ns = n_sink;
+    }
+  }
   // the readers' view of the jobs
   auto next_job = [&](uint32_t j) -> WaJob {
     ok = ok && wa_wait(&sm.job_ready[j % WA_JOBS], j / WA_JOBS, sm, p.hdr, 60);
@@ -280,10 +374,8 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
   } else if (warp >= WA_RING_WARP) {
     // ================= the ring
     const int rt = tid - 32 * WA_RING_WARP, rw = rt >> 5;
-    const int R = slots - p.n_sink;                   // window slots
-    const size_t row_bytes = p.rows_fp8 ? D : 2 * D;
     uint32_t j = 0;                                   // jobs published, and (told ones) announced
-    uint32_t announced = 0;
+    uint32_t announced = 1;
     auto pv_wait = [&](uint32_t job) { ok = ok && wa_wait(&sm.pv_done[job & 1], job >> 1, sm, p.hdr, 66); };
     // the first query of the next job, as soon as it is known
     auto announce = [&](uint32_t bq) {
@@ -312,8 +404,6 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
       if (lane == 0) tc::bar_arrive(&sm.job_ready[j % WA_JOBS]);
       j++;
     };
-    const int64_t k_lo = tiles * blockIdx.x / gridDim.x, k_hi = tiles * (blockIdx.x + 1) / gridDim.x;
-    int held_b = -1, rl = 0, rh = 0, ns = 0;          // the ring: rows [rl, rh) and sinks [0, ns) of sequence held_b
     bool stale = false;                               // it may hold rows that are not finite
     int before = 0;                                   // first row that the job before sees
     int b = (int)(k_lo / pairs), i0 = 2 * (int)(k_lo - (int64_t)b * pairs);
@@ -329,7 +419,7 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
     for (int64_t k = k_lo; k < k_hi; k++) {
       const uint32_t bq = (uint32_t)b * (uint32_t)p.Q + (uint32_t)i0;
       const int have = i0 + 1 < p.Q ? 3 : 1;
-      announce(bq);
+      if (k > k_lo) announce(bq);
       const WaQuery q0 = wa_query(p, nt0, nbase, rt == 0), q1 = wa_query(p, nt1, nbase, rt == 0);
       const uint8_t* rows = p.rows + (size_t)b * (size_t)p.S * row_bytes;
       const uint8_t* sinks = p.sinks + (size_t)b * (size_t)p.n_sink * row_bytes;
@@ -337,11 +427,9 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
       i0 += 2;
       if (i0 >= p.Q) i0 = 0, b++;
       if (k + 1 < k_hi) fetch(b, i0);
-      // both queries at once when their rows together fit the ring, else one after the other
-      const int lo = q0.wn == 0 ? q1.r0 : (q1.wn == 0 ? q0.r0 : min(q0.r0, q1.r0));
-      const int hi = max(q0.wn ? q0.r0 + q0.wn : 0, q1.wn ? q1.r0 + q1.wn : 0);
-      const bool joint = q0.wn == 0 || q1.wn == 0 || hi - lo <= R;
-      int todo = joint ? 3 : 1 | 2 << 2;              // two bits a job: the queries it takes
+      const WaTile tile = wa_tile(q0, q1, R);
+      const int lo = tile.lo, hi = tile.hi;
+      int todo = tile.joint ? 3 : 1 | 2 << 2;         // two bits a job: the queries it takes
       bool exact = false, first = true;               // exact: on zeros and what its query sees
       while (todo != 0) {
         const int mask = todo & 3;
@@ -390,48 +478,26 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
           for (int i = 0; i < 4; i++) {
             const int x = x0 + 4 * i + rw;            // neighbouring rows in different warps
             v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (x < n_all) {
-              const uint4* src = reinterpret_cast<const uint4*>(x < n_row ? rows + (size_t)(rh + x) * row_bytes
-                                                                          : sinks + (size_t)(ns + x - n_row) * row_bytes);
-              v[i][0] = __ldg(src + lane);            // E4M3: 16 dims a lane; bf16: 8 dims of each half
-              if (!p.rows_fp8) v[i][1] = __ldg(src + 32 + lane);
-            }
+            if (x < n_all)
+              wa_load_row(v[i], x < n_row ? rows + (size_t)(rh + x) * row_bytes : sinks + (size_t)(ns + x - n_row) * row_bytes,
+                          p.rows_fp8, lane);
           }
           gate();
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             const int x = x0 + 4 * i + rw;
             if (x >= n_all) continue;
-            uint4 lo4 = v[i][0], hi4 = v[i][1];
-            if (p.rows_fp8) {
-              const uint32_t e[4] = {lo4.x, lo4.y, lo4.z, lo4.w};
-              uint32_t o[8];
-#pragma unroll
-              for (int y = 0; y < 4; y++) {
-                o[2 * y] = wa_f16x2_to_bf16x2(e4m3x2_to_f16x2(e[y]));
-                o[2 * y + 1] = wa_f16x2_to_bf16x2(e4m3x2_to_f16x2(e[y] >> 16));
-              }
-              lo4 = make_uint4(o[0], o[1], o[2], o[3]);
-              hi4 = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-            if (!exact && __any_sync(0xFFFFFFFFu, wa_not_finite(lo4) || wa_not_finite(hi4))) {
-              dirty = true;
-              continue;
-            }
             int slot = slot_r + x;
             if (slot >= slots) slot -= R;             // around the ring
             if (x >= n_row) slot = ns + x - n_row;
-            const int u0 = p.rows_fp8 ? 2 * lane : lane, u1 = p.rows_fp8 ? 2 * lane + 1 : 32 + lane;   // 16-byte units
-            unsigned char* dst = smem + slot * 128;
-            *reinterpret_cast<uint4*>(dst + (u0 >> 3) * WA_KCOL + (((u0 ^ slot) & 7) << 4)) = lo4;
-            *reinterpret_cast<uint4*>(dst + (u1 >> 3) * WA_KCOL + (((u1 ^ slot) & 7) << 4)) = hi4;
+            if (!wa_put_row(smem, slot, v[i], p.rows_fp8, exact, lane)) dirty = true;
           }
         }
         gate();
         rh = max(rh, E);
         rl = max(rl, E - R);
         ns = max(ns, NS);
-        if (wa_ring_any(dirty)) {                      // each query of this job alone, with what it sees as it is
+        if (wa_any<1, WA_RING>(dirty)) {              // each query of this job alone, with what it sees as it is
           const int singles = (mask & have) == 3 ? 1 | 2 << 2 : mask & have;
           todo = singles | todo << (singles > 3 ? 4 : 2);
           exact = true;
