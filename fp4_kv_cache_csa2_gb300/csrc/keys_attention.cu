@@ -785,19 +785,28 @@ static cudaError_t keys_launch(const KeysParams& p, int64_t BQ, const CUtensorMa
   return cudaLaunchKernelEx(&cc, kernel, (const float*)p.part, p.split, p.out, p.lse);
 }
 
-// Calls that window_attention.cu takes: short windows of at least four queries a sequence, and
-// enough of them that a CTA has several tiles (its first one waits for a whole window of rows).
-// Window 128, 4 sinks, bf16, us (this file's kernel / the ring's): 1 x 64 queries 8.5 / 19.1, 64 x 8
-// 33.7 / 35.9, 152 x 4 40.3 / 26.1, 1 x 608 36.2 / 23.7, 1 x 2432 148 / 68; with one or two queries
-// a sequence a tile brings a window for every query: 608 x 1 46.8 / 86.9, 300 x 2 42.7 / 46.3.
-static bool keys_in_ring(const KeysParams& p, int64_t BQ) {
-  return !p.main_kv && window_ring_fits(p.W, p.n_sink) && p.Q >= 4 && BQ >= 3 * KA_SMS;
+// Calls that window_attention.cu takes: short windows, where its time is less.  In tenths of a us: this
+// file's kernel takes 70 and 1/10 a key for each wave of queries; the ring's 60, 3/10 a key for a CTA's
+// first window, and for its longest CTA 45 a tile (two queries) and 9/10 a key for each further sequence in
+// its run (of 410 calls measured both ways none loses more than 3 % by it).  Window 128, 4 sinks,
+// bf16, us (here / the ring's): 1 x 152 queries 8.7 / 15.4, 1 x 304 16.6 / 16.5, 1 x 608 34.2 / 19.6, 1 x 2432
+// 140 / 62, 100 x 4 23.9 / 31.9, 152 x 4 38.0 / 21.1, 60 x 5 16.5 / 31.5, 80 x 8 42.8 / 35.6, 608 x 1 44.3 / 80.0;
+// window 32: 1 x 153 13.4 / 11.4, 100 x 4 21.6 / 19.9.
+static bool keys_in_ring(const KeysParams& p, int B, int64_t BQ) {
+  if (p.main_kv || !window_ring_fits(p.W, p.n_sink) || BQ <= KA_SMS) return false;
+  const int64_t keys = p.W + p.n_sink, pairs = (p.Q + 1) / 2, tiles = B * pairs, ctas = min(tiles, (int64_t)KA_SMS);
+  int64_t longest = 0;
+  for (int64_t i = 0; i < ctas; i++) {
+    const int64_t lo = tiles * i / ctas, hi = tiles * (i + 1) / ctas;
+    longest = max(longest, 45 * (hi - lo) + ((hi - 1) / pairs - lo / pairs) * keys * 9 / 10);
+  }
+  return 60 + keys * 3 / 10 + longest < ceil_div(BQ, KA_SMS) * (70 + keys / 10);
 }
 
 cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* part, cudaStream_t stream) {
   const int64_t BQ = (int64_t)B * p.Q;
   if (BQ == 0) return cudaSuccess;
-  if (keys_in_ring(p, BQ)) return launch_window_ring(p, B, stream);
+  if (keys_in_ring(p, B, BQ)) return launch_window_ring(p, B, stream);
   p.split = keys_split(BQ, chunks);
   p.part = reinterpret_cast<float*>(part);
   CUtensorMap mq, mr, ms;

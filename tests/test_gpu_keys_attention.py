@@ -215,6 +215,18 @@ def test_window_many_queries(fp8, B, Q, W, n_sink, start):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,Q,W,n_sink,start", [
+    (1, 160, 32, 4, 0), (40, 8, 20, 3, 5), (152, 2, 9, 0, 100), (3, 100, 155, 0, 7), (160, 1, 3, 2, 0), (305, 1, 1, 0, 9),
+    (7, 23, 128, 4, 60), (2, 77, 5, 154, 90)])
+def test_window_one_or_two_tiles_a_cta(fp8, B, Q, W, n_sink, start):
+    """Sizes about the one where the ring takes a call over; a CTA's run ends inside a sequence."""
+    pos = start + np.arange(Q)[None, :] + 3 * (np.arange(B) % 5)[:, None]
+    base = np.maximum(0, pos[:, 0] - W + 1)
+    pos[1::3, Q // 2:] = -1
+    verify_window(44, B, Q, W, n_sink, fp8, pos, base, Q + W - 1 + 2)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("W,n_sink", [(40, 4), (128, 16), (159, 0)])
 def test_window_many_queries_in_any_order(fp8, W, n_sink):
     """The same with jumps, repeated and descending positions, padding and rows that are missing."""
