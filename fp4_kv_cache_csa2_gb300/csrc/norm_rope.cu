@@ -18,7 +18,7 @@
 // Rows a warp and threads a CTA, us for 16 / 300 / 777 / 8192 tokens: 1 and 128
 // 2.1 / 7.9 / 17.1 / 160, 2 and 128 2.8 / 8.4 / 17.8 / 156, 4 and 256 4.0 / 10.9 /
 // 22.1 / 175: many small CTAs keep as many loads in flight as several rows a warp
-// do, and fill the last wave better.
+// do, and fill the last wave better.  8192 tokens: 6.6 TB/s.
 #include "host_once.cuh"
 #include "params.cuh"
 
