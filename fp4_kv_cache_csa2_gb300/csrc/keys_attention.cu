@@ -33,12 +33,12 @@
 // Shared memory: three K buffers of [64 keys][512 dims] (two halves of 32 KB, four SW128
 // column chunks each; the third takes Q on its way to TMEM first) and a staging area of
 // 18 KB for the next chunk's entries as stored.  Roles:
-// warps 0..3 move Q, then softmax; warps 4..11 fill the K buffers (from the
-// staged bytes through registers; bf16 rows are rounded in place if need be); warps 0..7
-// write the output; warp 12
-// issues the MMAs, S of chunk c + 1 before O of chunk c, so that the softmax of a chunk
-// runs beside the products of its neighbours; warp 13 issues the copies.  All waits are
-// bounded; a timeout reports CSA2_ERR_TIMEOUT and every thread still takes every barrier.
+// warps 0..3 move Q, then softmax; warps 4..11 fill the K buffers (from the staged bytes
+// through registers; bf16 rows are rounded in place if need be); warps 0..7 write the
+// output; warp 12 issues the MMAs, S of chunk c + 1 before O of chunk c, so that the
+// softmax of a chunk runs beside the products of its neighbours; warp 13 issues the copies.
+// All waits are bounded; a timeout reports CSA2_ERR_TIMEOUT and every thread still takes
+// every barrier.
 //
 // Bound by the tensor cores, on which an M = 64 tile takes as long as one of M = 128 (two queries a
 // tile would need all of TMEM for O): 2048 cycles a chunk.  2048 queries over 8192 entries 1.91 ms,
