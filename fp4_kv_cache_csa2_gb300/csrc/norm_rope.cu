@@ -12,20 +12,22 @@
 //
 // Bound by HBM: a token reads and writes 64 KB of queries and 1 + 1 KB (or
 // 512 B) of window row against 0.2 Mflop.  One warp takes one row (a head of a
-// token, or a token's key row); lane l owns channels 8l .. 8l + 7 and 256 + 8l ..
-// 256 + 8l + 7, so every load and store of a warp is 512 contiguous bytes.  The
-// rotated tail lies in the second half of lanes 24..31 (four pairs a lane).
-// Rows a warp and threads a CTA, us for 16 / 300 / 777 / 8192 tokens: 1 and 128
-// 2.1 / 7.9 / 17.1 / 160, 2 and 128 2.8 / 8.4 / 17.8 / 156, 4 and 256 4.0 / 10.9 /
-// 22.1 / 175: many small CTAs keep as many loads in flight as several rows a warp
-// do, and fill the last wave better.  8192 tokens: 6.6 TB/s.
+// token, or a token's key row) or, in long calls, two heads of a token; lane l owns
+// channels 8l .. 8l + 7 and 256 + 8l .. 256 + 8l + 7 of a row, so every load and store of
+// a warp is 512 contiguous bytes.  The rotated tail lies in the second half of lanes
+// 24..31 (four pairs a lane).
+// Rows a warp and CTAs an SM, us for 16 / 300 / 777 / 1500 / 3000 / 8192 tokens: 1 and 12
+// 2.0 / 7.6 / 18.0 / 32.1 / 61.5 / 164.7, 2 and 10 2.3 / 8.0 / 17.6 / 30.6 / 58.2 / 155.2 (7.0
+// TB/s), 2 and 12 (with spills) 157.8 at 8192, 4 rows 158.7.  Two rows keep more loads in
+// flight; one fills a short call's only waves better.
 #include "host_once.cuh"
 #include "params.cuh"
 
 namespace csa2 {
 
 constexpr int QK_THREADS = 128;
-constexpr int QK_CTAS = 12;                         // an SM, for 48 warps of at most 40 registers
+constexpr int qk_ctas(int rows) { return rows == 1 ? 12 : 10; }   // an SM: at most 40 and 48 registers
+constexpr int64_t QK_LONG = 600;                    // tokens from which a warp takes two heads
 
 __device__ __forceinline__ uint32_t qk_bf16x2(float lo, float hi) {
   uint32_t r;
@@ -98,17 +100,25 @@ __device__ __forceinline__ const float4* qk_table_row(const QkParams& p, int64_t
   return nullptr;
 }
 
-__global__ void __launch_bounds__(QK_THREADS, QK_CTAS) qk_norm_rope_kernel(QkParams p) {
+// QROWS: neighbouring heads of a token that a warp takes.
+template <int QROWS>
+__global__ void __launch_bounds__(QK_THREADS, qk_ctas(QROWS)) qk_norm_rope_kernel(QkParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t g = (int64_t)blockIdx.x * (QK_THREADS / 32) + (threadIdx.x >> 5);
-  const int64_t nq = p.q ? p.T * H : 0;
+  const int64_t nq = p.q ? p.T * (H / QROWS) : 0;
   const bool is_q = g < nq;
-  const int64_t token = is_q ? g / H : g - nq;
+  const int64_t token = is_q ? g / (H / QROWS) : g - nq;
   if (!is_q && (!p.k || token >= p.T)) return;
-  const int head = is_q ? (int)(g % H) : 0;
+  const int head = is_q ? (int)(g % (H / QROWS)) * QROWS : 0, rows = is_q ? QROWS : 1;
   const uint4* in = reinterpret_cast<const uint4*>(is_q ? p.q + token * p.q_stride + head * D : p.k + token * p.k_stride);
-  const uint4 a = __ldcs(in + lane), b = __ldcs(in + 32 + lane);
+  uint4 v[QROWS][2] = {};
+#pragma unroll
+  for (int i = 0; i < QROWS; i++)
+    if (i < rows) {
+      v[i][0] = __ldcs(in + i * (D / 8) + lane);
+      v[i][1] = __ldcs(in + i * (D / 8) + 32 + lane);
+    }
   // the queries' warps report a bad position when there are queries
   const float4* cs = qk_table_row(p, p.pos[token], lane == 0 && (is_q ? head == 0 : !p.q));
   int64_t slot = is_q ? 0 : (p.k_slot ? p.k_slot[token] : token);
@@ -118,24 +128,30 @@ __global__ void __launch_bounds__(QK_THREADS, QK_CTAS) qk_norm_rope_kernel(QkPar
     return;
   }
   const float4* w = reinterpret_cast<const float4*>(is_q ? p.q_weight : p.k_weight);
-  const float r = qk_inv_rms(a, b, p.eps);
 #pragma unroll
-  for (int half = 0; half < 2; half++) {
-    float f[8];
-    qk_finish(half ? b : a, r, w, half, lane, cs, f);
-    if (is_q) {
-      __stcs(reinterpret_cast<uint4*>(p.q_out + (token * H + head) * D) + 32 * half + lane, qk_pack_bf16(f));
-    } else if (p.rows_fp8) {
-      reinterpret_cast<uint2*>(p.rows + slot * D)[32 * half + lane] =
-          make_uint2(qk_e4m3x2(f[0], f[1]) | qk_e4m3x2(f[2], f[3]) << 16, qk_e4m3x2(f[4], f[5]) | qk_e4m3x2(f[6], f[7]) << 16);
-    } else {
-      reinterpret_cast<uint4*>(p.rows + slot * D * 2)[32 * half + lane] = qk_pack_bf16(f);
+  for (int i = 0; i < QROWS; i++) {
+    if (i >= rows) break;
+    const float r = qk_inv_rms(v[i][0], v[i][1], p.eps);
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+      float f[8];
+      qk_finish(v[i][half], r, w, half, lane, cs, f);
+      if (is_q) {
+        __stcs(reinterpret_cast<uint4*>(p.q_out + (token * H + head + i) * D) + 32 * half + lane, qk_pack_bf16(f));
+      } else if (p.rows_fp8) {
+        reinterpret_cast<uint2*>(p.rows + slot * D)[32 * half + lane] =
+            make_uint2(qk_e4m3x2(f[0], f[1]) | qk_e4m3x2(f[2], f[3]) << 16,
+                       qk_e4m3x2(f[4], f[5]) | qk_e4m3x2(f[6], f[7]) << 16);
+      } else {
+        reinterpret_cast<uint4*>(p.rows + slot * D * 2)[32 * half + lane] = qk_pack_bf16(f);
+      }
     }
   }
 }
 
 cudaError_t launch_qk_norm_rope(const QkParams& p, cudaStream_t stream) {
-  const int64_t tasks = (p.q ? p.T * H : 0) + (p.k ? p.T : 0);
+  const int qrows = p.T >= QK_LONG ? 2 : 1;
+  const int64_t tasks = (p.q ? p.T * (H / qrows) : 0) + (p.k ? p.T : 0);
   if (tasks == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ceil_div(tasks, QK_THREADS / 32));
@@ -146,7 +162,7 @@ cudaError_t launch_qk_norm_rope(const QkParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel, p);
+  return cudaLaunchKernelEx(&cfg, qrows == 2 ? qk_norm_rope_kernel<2> : qk_norm_rope_kernel<1>, p);
 }
 
 }  // namespace csa2

@@ -158,3 +158,39 @@ def test_offsets_past_32_bits():
     for n, t in enumerate(at):
         check(q[t].double().cpu().numpy(), x[n], None, cs[t % P].numpy(), 1e-6, ref.U_BF16)
         check(ref.row_values(rows[t].cpu().numpy()), xk[n], None, cs[t % P].numpy(), 1e-6, ref.U_E4M3)
+
+
+@pytest.mark.parametrize("T,q_gap,k_gap,weights,fp8,eps", [
+    (600, 0, 0, True, False, 1e-6), (601, 8, 8, False, True, 1e-6), (777, 640, 24, True, True, 1e-5)])
+def test_long_calls_against_the_formula(T, q_gap, k_gap, weights, fp8, eps):
+    """From 600 tokens on a warp takes two heads."""
+    test_against_the_formula(T, q_gap, k_gap, weights, fp8, eps)
+
+
+@pytest.mark.parametrize("parts", ["both", "q", "k", "in place"])
+def test_a_long_call_is_its_tokens_calls(parts):
+    """A long call gives the bits of short ones, padding, bad positions and bad slots among its tokens."""
+    T = 1203
+    q, k, qw, kw = make(9, T, 64, 8)
+    cs, ws = csa2.rope_table(P).cuda(), csa2.Workspace(256)
+    rng = np.random.default_rng(9)
+    pos, slot = rng.integers(0, P, T), rng.permutation(T + 40)[:T]
+    pos[rng.integers(0, T, 60)] = -1
+    pos[[7, 650]], pos[[8, 900]] = P, -2
+    slot[rng.integers(0, T, 30)] = -1
+    slot[[11, 700]] = T + 40
+    pos, slot = torch.from_numpy(pos).cuda(), torch.from_numpy(slot).cuda()
+    got = []
+    for step in (T, 401):
+        src = q.contiguous() if parts == "in place" else q
+        out = src if parts == "in place" else torch.full((T, 64, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        rows = torch.full((T + 40, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        for a in range(0, T, step):
+            s = slice(a, a + step)
+            kw_q = {} if parts == "k" else dict(q=src[s], q_weight=qw, q_out=out[s])
+            kw_k = {} if parts == "q" else dict(k=k[s], k_weight=kw, rows=rows, k_slot=slot[s])
+            csa2.qk_norm_rope(pos[s], cs, ws, **kw_q, **kw_k)
+        assert ws.sync_status()[0] == 6
+        got.append((out, rows))
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
