@@ -18,6 +18,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
+// what the rounding of (lo, hi) to the two bf16 of `w` left of them, as two bf16: together they
+// hold 16 bits of each
+__device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t w) {
+  return pack_bf16x2(lo - __uint_as_float(w << 16), hi - __uint_as_float(w & 0xFFFF0000u));
+}
+
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));

@@ -16,7 +16,7 @@
 //     to TMEM over S as the 16-bit A operand of the next product.  The reference m of a
 //     head moves only when a chunk exceeds it by more than e^8 (then the head's O and its
 //     sum are rescaled), so P stays inside f16
-//   * O += P V    N = 2 x 256 dims, K = keys: V is the K tile read MN-major
+//   * O += P V    N = 2 x 256 dims, K = keys: V is the K tile read MN-major (twice with two-part P)
 // An M = 64 tile takes 16 lanes of each of TMEM's four lane quarters, so two of them
 // share columns: half h of the dims has its Q, its part of S and its O in lanes
 // 16h .. 16h + 15 (256 columns of O, 128 of Q, twice 64 of S), P lies in both.  With Q and P
@@ -26,9 +26,11 @@
 // Operands: F16 (calls with cache entries or E4M3 rows) keeps every dequantised FP4
 // value (at most 6 significant bits, 2^-10 .. 2688) and every E4M3 value exactly and
 // rounds q and bf16 window rows to f16, exact inside [2^-14, 65504], with P to 11
-// bits.  With bf16 rows alone the operands are bf16: q and rows as they are, P to 8
-// bits (its rounding errors are independent and average out; the sum of the softmax
-// is taken before that rounding, in binary32).
+// bits.  With bf16 rows alone the operands are bf16: q and rows as they are, P as two bf16
+// of 8 bits, its rounding and what that left (a second product with the same V): with the
+// first alone the errors of the outputs are 1.3 times those of their own rounding, with both
+// 1.00; 16 queries of 132 rows take 9.0 us instead of 7.7.  The sum of the softmax is taken
+// before any rounding, in binary32.
 //
 // Shared memory: three K buffers of [64 keys][512 dims] (two halves of 32 KB, four SW128
 // column chunks each; the third takes Q on its way to TMEM first) and a staging area of
@@ -44,7 +46,7 @@
 // tile would need all of TMEM for O): 2048 cycles a chunk.  2048 queries over 8192 entries 1.91 ms,
 // 1.03 PFLOP/s, their pipe active in 86 % of the cycles; 16 queries over 131,072 entries 260 us, 1.0
 // PFLOP/s; 602 queries of 1000 E4M3 rows 114 us.  A CTA costs about 7 us beside its chunks: 16
-// queries of 132 rows take 7.6 us.
+// queries of 132 bf16 rows take 9.0 us.
 #include "attn_common.cuh"
 #include "params.cuh"
 
@@ -272,8 +274,10 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 #pragma unroll
         for (int ks = 0; ks < KA_KEYS / 16; ks++)
           if (ks < steps)
-            tc::mma_f16_ts_warp(leader, KA_O_COL + lanes, KA_S_COL + 64 * (c & 1) + lanes + 8 * ks,
-                                va + (uint32_t)(ks * (2048 >> 4)), idesc_o, (c || ks) ? 1u : 0u);
+#pragma unroll
+            for (int part = 0; part < (F16 ? 1 : 2); part++)     // P, what its rounding left of it
+              tc::mma_f16_ts_warp(leader, KA_O_COL + lanes, KA_S_COL + 64 * (c & 1) + lanes + 32 * part + 8 * ks,
+                                  va + (uint32_t)(ks * (2048 >> 4)), idesc_o, (c || ks || part) ? 1u : 0u);
       }
       tc::commit_warp(leader, &sm.free_[ob]);
       if (++ob == KA_BUFS) ob = 0;
@@ -532,22 +536,28 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       if (c > 0 && ++ob == KA_BUFS) ob = 0, ou++;
       const float ref = m_used == -INFINITY ? 0.f : m_used;
       float l4[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t pk[16];
+      uint32_t pk[16], rest[16];
 #pragma unroll
       for (int x = 0; x < 16; x++) {
         float e0 = ex2_ftz(v[2 * x] - ref), e1 = ex2_ftz(v[2 * x + 1] - ref);
         l4[x & 3] += e0 + e1;
         pk[x] = F16 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+        if (!F16) rest[x] = bf16x2_rest(e0, e1, pk[x]);
       }
       l_sum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-      uint32_t pw[32];                                // P of all 64 keys for this lane's half of the dims, over S
+      // P of all 64 keys for this lane's half of the dims, over S
+      auto put = [&](uint32_t taddr, const uint32_t* k) {
+        uint32_t pw[32];
 #pragma unroll
-      for (int x = 0; x < 16; x++) {
-        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, pk[x], 16);
-        pw[x] = half ? got : pk[x];
-        pw[16 + x] = half ? pk[x] : got;
-      }
-      tmem_st32(s_addr, pw);
+        for (int x = 0; x < 16; x++) {
+          const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, k[x], 16);
+          pw[x] = half ? got : k[x];
+          pw[16 + x] = half ? k[x] : got;
+        }
+        tmem_st32(taddr, pw);
+      };
+      put(s_addr, pk);
+      if (!F16) put(s_addr + 32, rest);
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();

@@ -11,16 +11,19 @@
 // slots a query sees is a circular interval.  A CTA takes a run of neighbouring tiles, so that
 // a tile loads the two rows that its queries see newly (the first one its window, by all warps but
 // the copies'), and streams q in and the output out:
-//   warps 0..3    softmax, one thread a row, from TMEM; P goes back over S as 16-bit A operand
+//   warps 0..3    softmax, one thread a row, from TMEM; P goes back over S as 16-bit A operands
 //   warps 4..7    output: O by 64 dims to bf16 rows
 //   warps 8..11   the ring: rows that the next tile's queries see newly
 //   warp 12       S = Q K^T (M = 128, N = slots, K = 512), Q in 64-dim pieces through 3 stages
-//   warp 13       O = P V by 64 dims (M = 128, N = 64, K = slots), V the ring read MN-major
+//   warp 13       O = P V by 64 dims (M = 128, N = 64, K = slots, P in two parts), V the ring read MN-major
 //   warp 14       copies of Q
 // S has two buffers of 160 columns of TMEM and O three of 64, so a tile's products run beside
 // the softmax and the output of its neighbours.  Operands are bf16 (q and bf16 rows as they
-// are, E4M3 rows exactly, P to 8 bits with the softmax's sum taken before that rounding).
-// 8192 queries of 128 rows and 4 sinks: 183 us, 5.9 TB/s of q, rows and output.
+// are, E4M3 rows exactly, P as two bf16 of 8 bits, its rounding and what that left, with the
+// softmax's sum taken before either; the first alone makes the outputs' errors 1.3 times those
+// of their own rounding).  8192 queries of 128 rows and 4 sinks: 202 us, 5.4 TB/s of q, rows and
+// output (one part 183, the second product 15 of the difference: a tile's S waits for the P V
+// of the tile before the last).
 //
 // A slot that a query does not see has weight zero for it, and zero times an infinity or a NaN
 // is a NaN.  A row goes to the ring while tiles are at work only if all of it is finite; when
@@ -344,9 +347,12 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
         tc::fence_after_sync();
         const uint64_t va = v_d + (uint32_t)(u * (WA_KCOL >> 4));
 #pragma unroll 2
-        for (int k = 0; k < steps; k++)
-          tc::mma_f16_ts_warp(leader, WA_O_COL + 64 * buf, WA_S_COL + WA_SLOTS * (j & 1) + 8 * k, va + (uint32_t)(k * (2048 >> 4)),
-                              idesc, k ? 1u : 0u);
+        for (int k = 0; k < steps; k++) {             // P of 16 keys, then what its rounding left of it
+          const uint32_t pa = WA_S_COL + WA_SLOTS * (j & 1) + 32 * (k >> 1) + 8 * (k & 1);
+          const uint64_t vk = va + (uint32_t)(k * (2048 >> 4));
+          tc::mma_f16_ts_warp(leader, WA_O_COL + 64 * buf, pa, vk, idesc, k ? 1u : 0u);
+          tc::mma_f16_ts_warp(leader, WA_O_COL + 64 * buf, pa + 16, vk, idesc, 1u);
+        }
         tc::commit_warp(leader, &sm.o_full[buf]);
         if (++buf == WA_O_BUFS) buf = 0, use++;
       }
@@ -599,7 +605,7 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
       float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
       for (int g = 0; g < slots; g += 32) {
-        uint32_t s[32], pk[16];
+        uint32_t s[32], pk[16], rest[16];
         tmem_ld32(s_addr + g, s);
         const uint32_t m = seen(g);
 #pragma unroll
@@ -608,8 +614,10 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
           const float e1 = (m >> (2 * x + 1) & 1) ? ex2_ftz(fmaf(__uint_as_float(s[2 * x + 1]), sc2, -ref)) : 0.f;
           l4[x & 3] += e0 + e1;
           pk[x] = pack_bf16x2(e0, e1);
+          rest[x] = bf16x2_rest(e0, e1, pk[x]);
         }
-        wa_tmem_st16(s_addr + (g >> 1), pk);          // over columns of S that are read already
+        wa_tmem_st16(s_addr + g, pk);                 // over these 32 columns of S: 16 bits a weight in two halves
+        wa_tmem_st16(s_addr + g + 16, rest);
       }
       const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
       tc::tmem_wait_st();

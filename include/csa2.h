@@ -438,7 +438,8 @@ csa2_status csa2_qk_norm_rope(const csa2_qk_args *args, void *ws, size_t ws_byte
  * Precision: binary32 accumulation and softmax state.  With bf16 rows the
  * operands are bf16.  With E4M3 rows, which both types hold exactly, they are
  * bf16 (calls of many neighbouring queries with short windows) or f16, and q
- * is then rounded as csa2_sparse_swa_attn does.  Workspace:
+ * is then rounded as csa2_sparse_swa_attn does.  The probabilities are held to
+ * 16 bits with bf16 operands (two of 8) and to 11 with f16.  Workspace:
  * csa2_window_attn_workspace_size (partial states when a query's keys are
  * divided over several CTAs).
  */

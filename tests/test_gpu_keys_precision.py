@@ -1,0 +1,108 @@
+"""Precision and range of the window attention and of the dense attention: what a key of any
+weight adds to the output, and queries and scores far from the ordinary."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import fp4_kv_cache_csa2_gb300 as csa2
+import oracle
+import synth
+from tests import keys_ref as ref
+
+pytestmark = pytest.mark.gpu
+SCALE = 1 / math.sqrt(512)
+
+
+def up(a):
+    return torch.from_numpy(np.ascontiguousarray(a.view(np.int16) if a.dtype == np.uint16 else a)).cuda()
+
+
+def bf16_bits(x):
+    return synth.f32_to_bf16_bits(np.asarray(x, np.float32))
+
+
+def draw_rows(g, fp8, *shape):
+    r = synth.swa_rows(g, *shape)
+    return oracle.swa_fp8_quantize(r) if fp8 else r
+
+
+def as_rows(x, fp8):
+    return oracle.swa_fp8_quantize(bf16_bits(x)) if fp8 else bf16_bits(x)
+
+
+def run_window(q, rows, base, pos, W, sinks=None, scale=SCALE):
+    B, Q = pos.shape
+    out = torch.full((B, Q, 64, 512), 0x4242, dtype=torch.int16, device="cuda")
+    lse = torch.full((B, Q, 64), 42.0, device="cuda")
+    ws = csa2.Workspace(csa2.window_attn_workspace_size(B, Q, W, 0 if sinks is None else sinks.shape[1]))
+    csa2.window_attn(up(q), up(rows), up(base), up(pos), scale, out, ws, W=W,
+                     sinks=None if sinks is None else up(sinks), lse=lse)
+    assert ws.sync_status()[0] == 0
+    return ref.bf16(out.cpu().numpy().view(np.uint16)), lse.cpu().double().numpy()
+
+
+def exact(q, keys, scale):
+    """Output and lse of one query's heads [64][512] over keys [n][512], in 64 bits."""
+    logit = scale * (q @ keys.T)
+    top = logit.max(-1, keepdims=True)
+    e = np.exp(logit - top)
+    total = e.sum(-1, keepdims=True)
+    return (e / total) @ keys, (top + np.log(total))[:, 0]
+
+
+def check_rms(got, want):
+    """Errors of many outputs are those of their rounding to bf16.
+
+    The weights' roundings are independent of it and of one another.  At 11 bits (f16) a weight is
+    off by an eighth of what the output's own rounding is off (2^-11 and 2^-8 at most, both spread
+    alike), and more keys than one average out: the root of the mean squares grows by
+    sqrt(1 + 1/64) = 1.008 at most.  At 8 bits it would grow by about sqrt(2), and a key left out of 1000
+    alike adds 1/32 of an output.  The logits' errors (2^-20) and those of the sums are far below.
+    The mean over the 32,768 or more outputs is itself known to about 0.5 %: 1.05 in all."""
+    rounded = ref.bf16(bf16_bits(want.astype(np.float32)))
+    own = np.sqrt(np.mean((rounded - want) ** 2))
+    err = np.sqrt(np.mean((got - want) ** 2))
+    assert err <= 1.05 * own, (err / own, own)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,Q,W,n_sink,start", [
+    (16, 1, 128, 4, 4095), (40, 3, 99, 0, 700), (1, 640, 128, 4, 1000), (160, 4, 30, 2, 50), (1, 2, 1000, 17, 3000),
+    (1, 1, 4000, 5, 9000), (1, 320, 400, 3, 900)])
+def test_window_errors_are_those_of_the_output(fp8, B, Q, W, n_sink, start):
+    """One CTA a query, many queries over a ring, keys divided over CTAs."""
+    g = synth.rng(61)
+    pos = start + np.arange(Q)[None, :] + np.zeros((B, 1), np.int64)
+    base = pos[:, 0] - W + 1
+    q, rows = synth.main_queries(g, B, Q), draw_rows(g, fp8, B, Q + W - 1)
+    sinks = draw_rows(g, fp8, B, n_sink) if n_sink else None
+    o, _ = run_window(q, rows, base, pos, W, sinks)
+    got, want = [], []
+    for b in range(0, B, max(1, B // 8)):
+        rv = ref.row_values(rows[b])
+        for i in range(0, Q, max(1, Q // 8)):
+            keys = ref.window_keys(rv, int(base[b]), int(pos[b, i]), W, ref.row_values(sinks[b]) if n_sink else None)
+            got.append(o[b, i])
+            want.append(exact(ref.bf16(q[b, i]), keys, SCALE)[0])
+    check_rms(np.array(got), np.array(want))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Q", [3, 640])
+def test_window_of_two_opposite_rows(fp8, Q):
+    """Rows v, -v, v ..: an output is v times the difference of two weights near 1, which a weight
+    of 8 bits (half a step below 1: 2^-9, of a sum of 2) gives up to 2^-10 off."""
+    g = synth.rng(62)
+    v = ref.row_values(draw_rows(g, True, 1))[0]
+    rows = as_rows(np.where(np.arange(Q + 1)[:, None] % 2, -v, v), fp8)[None]
+    q, scale = synth.main_queries(g, 1, Q), 0.03 * SCALE
+    pos = 1 + np.arange(Q)[None, :]
+    o, l = run_window(q, rows, np.zeros(1, np.int64), pos, 2, scale=scale)
+    rv = ref.row_values(rows[0])
+    for i in range(0, Q, max(1, Q // 20)):
+        want, lse, tol, tol_l = ref.attend(ref.bf16(q[0, i]), rv[i:i + 2], scale, ref.U_F16 if fp8 else 2.0 ** -16)
+        assert np.abs(want).max() < 0.5 * np.abs(v).max()
+        assert np.all(np.abs(o[0, i] - want) <= tol), (i, np.max(np.abs(o[0, i] - want) / tol))
+        assert np.all(np.abs(l[0, i] - lse) <= tol_l)
