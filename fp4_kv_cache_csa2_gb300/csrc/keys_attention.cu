@@ -516,7 +516,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       float alpha = 1.f;
       if (m_used == -INFINITY) {
         m_used = cm;                                  // O holds nothing yet, or only zeros
-      } else if (cm > m_used + KA_TAU) {
+      } else if (cm - m_used > KA_TAU) {              // (a sum m_used + KA_TAU could round up to the next score)
         alpha = ex2_ftz(m_used - cm);
         m_used = cm;
         l_sum *= alpha;

@@ -43,6 +43,20 @@ def run_window(q, rows, base, pos, W, sinks=None, scale=SCALE):
     return ref.bf16(out.cpu().numpy().view(np.uint16)), lse.cpu().double().numpy()
 
 
+def run_dense(kv, n, q, rows, base, pos, max_n, scale=SCALE):
+    """kv [cap][288] on the GPU: a cache of one sequence."""
+    Q = pos.shape[1]
+    cache = csa2.Cache(1, kv.shape[0], 1)
+    cache.main_kv[0, :kv.shape[0]].copy_(kv)
+    cache.n_entries.fill_(n)
+    out = torch.full((1, Q, 64, 512), 0x4242, dtype=torch.int16, device="cuda")
+    lse = torch.full((1, Q, 64), 42.0, device="cuda")
+    ws = csa2.Workspace(csa2.dense_attn_workspace_size(1, Q, max_n))
+    csa2.dense_attn(cache, up(q), up(rows), up(base), up(pos), scale, out, ws, max_n=max_n, lse=lse)
+    assert ws.sync_status()[0] == 0
+    return ref.bf16(out.cpu().numpy().view(np.uint16)), lse.cpu().double().numpy()
+
+
 def exact(q, keys, scale):
     """Output and lse of one query's heads [64][512] over keys [n][512], in 64 bits."""
     logit = scale * (q @ keys.T)
@@ -106,3 +120,29 @@ def test_window_of_two_opposite_rows(fp8, Q):
         assert np.abs(want).max() < 0.5 * np.abs(v).max()
         assert np.all(np.abs(o[0, i] - want) <= tol), (i, np.max(np.abs(o[0, i] - want) / tol))
         assert np.all(np.abs(l[0, i] - lse) <= tol_l)
+
+
+@pytest.mark.parametrize("kind", ["window", "dense"])
+def test_scores_that_grow_by_the_last_bit(kind):
+    """Scores (in powers of two) about 1.25 * 2^27, where neighbouring floats are 16 apart, growing by
+    one step from one run of 64 keys to the next: a weight of 2^16 would be infinite in f16.  All keys
+    are alike but for dim 256, which holds 0 .. 3."""
+    row = np.zeros((256, 512))
+    row[:, :256] = 1.0
+    row[:, 256] = np.arange(256) // 64
+    q = np.zeros((1, 1, 64, 512))
+    q[..., :256], q[..., 256] = 40960.0, 1.0                 # 1.25 * 2^23 + 0 .. 3
+    scale = 16 * math.log(2)
+    pos = np.array([[255]])
+    if kind == "window":                                      # enough queries for one CTA each
+        q, pos = np.repeat(q, 305, 1), np.repeat(pos, 305, 1)
+        o, l = run_window(bf16_bits(q), as_rows(row, True)[None], np.zeros(1, np.int64), pos, 256, scale=scale)
+    else:
+        kv = np.zeros((256, 288), np.uint8)
+        kv[:, 256:], kv[:, :128] = 0x38, 0x22
+        kv[:, 128] = np.array([0, 2, 4, 5])[np.arange(256) // 64]      # 0, 1, 2, 3
+        near = np.zeros((1, 128, 512))                       # the window: scores of 0
+        o, l = run_dense(torch.from_numpy(kv).cuda(), 256, bf16_bits(q), bf16_bits(near), np.array([128]), pos, 0, scale)
+    assert np.all(np.isfinite(o)) and np.all(np.isfinite(l))
+    assert np.all(np.abs(o[..., :256] - 1) <= 2.0 ** -8)
+    assert np.all((o[..., 256] >= 0) & (o[..., 256] <= 3)) and np.all(o[..., 257:] == 0)
