@@ -13,9 +13,9 @@
 // Per chunk, with the 64 heads as the rows of M = 64 tiles:
 //   * S = Q K^T   N = keys, K = 512 in two halves of 256 dims (16 MMAs each)
 //   * softmax, two lanes a head, straight from TMEM; P = 2^(S scale log2 e - m) goes back
-//     to TMEM over S as the 16-bit A operand of the next product.  The reference m of a
-//     head moves only when a chunk exceeds it by more than e^8 (then the head's O and its
-//     sum are rescaled), so P stays inside f16
+//     to TMEM over S as the 16-bit A operand of the next product.  The reference m of a head,
+//     2^-8 of the largest score when it is set (f16), moves only when a chunk exceeds it by more
+//     than 2^15.9 (then the head's O and its sum are rescaled): P uses the whole of f16's range
 //   * O += P V    N = 2 x 256 dims, K = keys: V is the K tile read MN-major (twice with two-part P)
 // An M = 64 tile takes 16 lanes of each of TMEM's four lane quarters, so two of them
 // share columns: half h of the dims has its Q, its part of S and its O in lanes
@@ -26,7 +26,7 @@
 // Operands: F16 (calls with cache entries or E4M3 rows) keeps every dequantised FP4
 // value (at most 6 significant bits, 2^-10 .. 2688) and every E4M3 value exactly and
 // rounds q and bf16 window rows to f16, exact inside [2^-14, 65504], with P to 11
-// bits.  With bf16 rows alone the operands are bf16: q and rows as they are, P as two bf16
+// bits (fewer below 2^-22 of the largest weight, see KA_TOP).  With bf16 rows alone the operands are bf16: q and rows as they are, P as two bf16
 // of 8 bits, its rounding and what that left (a second product with the same V): with the
 // first alone the errors of the outputs are 1.3 times those of their own rounding, with both
 // 1.00; 16 queries of 132 rows take 9.0 us instead of 7.7.  The sum of the softmax is taken
@@ -74,7 +74,15 @@ constexpr uint32_t KA_HALF_LANES = 16u << 16;
 constexpr int KA_AHEAD = 5;                               // chunks of entries that are on their way to L2
 constexpr float KA_LOG2E = 1.4426950408889634f;
 constexpr float KA_LN2 = 0.6931471805599453f;
+// The reference of a head moves when a score (in powers of two) lies this far above it.  bf16: P
+// has binary32's range.  F16: P of the largest score is 2^KA_TOP when the reference is set, and at
+// most 2^KA_MOST, f16's range less a little, before it moves.  Weights down to 2^-22 of the largest
+// keep f16's 11 bits, and what lies below loses 2^-33 of it at most: with a reference at the largest
+// score itself one key 17.3 above 131,072 others alike lost all of their 0.4 %.  The room between
+// the two (5.5 in logits) keeps rescalings rare: 2048 queries over 8192 entries take 1911 us, with
+// 2^0 at the top 1910, with 2^10 1933, with 2^11 1971.
 constexpr float KA_TAU = 8.0f * KA_LOG2E;
+constexpr float KA_TOP = 8.0f, KA_MOST = 15.9f;
 constexpr int KA_SMS = 152;                               // GB300; CTAs a query is divided over at most
 constexpr int KA_PART_FLOATS = 2 * H + H * D;             // one partial state: references, sums, O [dims / 4][head][4]
 
@@ -514,11 +522,13 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       float cm = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
       cm = fmaxf(cm, __shfl_xor_sync(0xFFFFFFFFu, cm, 16));
       float alpha = 1.f;
+      // where neighbouring scores lie 8 and more apart, a rounded cm - KA_TOP could lie too low
+      const float to = F16 && fabsf(cm) < 0x1p26f ? cm - KA_TOP : cm;
       if (m_used == -INFINITY) {
-        m_used = cm;                                  // O holds nothing yet, or only zeros
-      } else if (cm - m_used > KA_TAU) {              // (a sum m_used + KA_TAU could round up to the next score)
-        alpha = ex2_ftz(m_used - cm);
-        m_used = cm;
+        m_used = to;                                  // O holds nothing yet, or only zeros
+      } else if (cm - m_used > (F16 ? KA_MOST : KA_TAU)) {   // (a sum m_used + .. could round up to the next score)
+        alpha = ex2_ftz(m_used - to);
+        m_used = to;
         l_sum *= alpha;
       }
       if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {    // after the chunk before is in O

@@ -122,6 +122,37 @@ def test_window_of_two_opposite_rows(fp8, Q):
         assert np.all(np.abs(l[0, i] - lse) <= tol_l)
 
 
+@pytest.mark.parametrize("n,max_n", [(1 << 17, 0), (1 << 17, 1 << 17), (1 << 20, 0), (70_001, 0)])
+def test_dense_one_key_far_above_a_long_tail(n, max_n):
+    """Entry 0 lies 12 to 23.8 (a head each) above all the others, which are alike: the others' share,
+    alone in its dims, is N e^-gap / (1 + N e^-gap).  max_n = 0: one CTA walks the whole cache.
+
+    Weights in f16 are exact to 2^-11 down to 2^-14, below to 2^-25, of a largest one of 2^8 or more
+    (2^-33 each, N of them).  The tensor cores' sums of 16 products may lose 2^-23 of what is there
+    each time, the softmax's sum 2^-24 for each run of 64 keys and lane; 2^-12 for the exponentials; the
+    output's own rounding 2^-8."""
+    kv = torch.zeros(n, 288, dtype=torch.uint8, device="cuda")
+    kv[:, 256:] = 0x38                                        # scales 1
+    kv[0, :128], kv[1:, 128:256] = 0x22, 0x22                 # 1 in dims 0 .. 255, in dims 256 .. 511
+    row = np.zeros(512)
+    row[256:] = 1.0
+    rows = np.broadcast_to(bf16_bits(row), (1, 128, 512))
+    q = np.zeros((1, 1, 64, 512))
+    q[0, 0, :, :256] = (1 + np.arange(64) / 64)[:, None]
+    o, l = run_dense(kv, n, bf16_bits(q), rows, np.array([n - 128]), np.array([[n - 1]]), max_n, 12 / 256)
+    gap = 12 * (1 + np.arange(64) / 64)
+    N = n - 1 + 128
+    share = N * np.exp(-gap)
+    total = 1 + share
+    sums = N / 16 * 2.0 ** -23 + N / 64 * 2.0 ** -24
+    tail = share / total
+    tol = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12 + sums) * tail + N * 2.0 ** -33
+    assert np.all(np.abs(o[0, 0, :, 256:] - tail[:, None]) <= tol[:, None]), \
+        np.max(np.abs(o[0, 0, :, 256:] - tail[:, None]) / tol[:, None])
+    assert np.all(np.abs(o[0, 0, :, :256] - (1 / total)[:, None]) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12 + sums) / total[:, None])
+    assert np.all(np.abs(l[0, 0] - (gap + np.log(total))) <= sums + 2.0 ** -12 * tail + 2.0 ** -18)
+
+
 @pytest.mark.parametrize("kind", ["window", "dense"])
 def test_scores_that_grow_by_the_last_bit(kind):
     """Scores (in powers of two) about 1.25 * 2^27, where neighbouring floats are 16 apart, growing by
