@@ -508,7 +508,8 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 #pragma unroll
         for (int x = 0; x < 32; x++) {
           const float got = __uint_as_float(__shfl_xor_sync(0xFFFFFFFFu, half ? s0[x] : s1[x], 16));
-          v[x] = (__uint_as_float(half ? s1[x] : s0[x]) + got) * sc2;
+          // (not to be fused with the reference's subtraction: the largest score minus itself is 0)
+          v[x] = __fmul_rn(__uint_as_float(half ? s1[x] : s0[x]) + got, sc2);
         }
       }
       const bool whole = __all_sync(0xFFFFFFFFu, n >= 32);

@@ -575,6 +575,9 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
     const int i = warp >> 1;                          // query
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const float sc2 = p.scale * WA_LOG2E;
+    // rounded before the largest is subtracted: a fused multiply-add of the two would leave the largest
+    // itself its rounding, 2^128 and more from scores of 2^32 on
+    auto score = [&](uint32_t s) { return __fmul_rn(__uint_as_float(s), sc2); };
     for (uint32_t j = 0;; j++) {
       const WaJob job = next_job(j);
       if (job.write < 0) break;
@@ -594,10 +597,10 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
         const uint32_t m = seen(g);
         if (m == ~0u) {
 #pragma unroll
-          for (int x = 0; x < 32; x++) c4[x & 3] = fmaxf(c4[x & 3], __uint_as_float(s[x]) * sc2);
+          for (int x = 0; x < 32; x++) c4[x & 3] = fmaxf(c4[x & 3], score(s[x]));
         } else {
 #pragma unroll
-          for (int x = 0; x < 32; x++) c4[x & 3] = fmaxf(c4[x & 3], (m >> x & 1) ? __uint_as_float(s[x]) * sc2 : -INFINITY);
+          for (int x = 0; x < 32; x++) c4[x & 3] = fmaxf(c4[x & 3], (m >> x & 1) ? score(s[x]) : -INFINITY);
         }
       }
       const float mx = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
@@ -610,8 +613,8 @@ window_attn_kernel(KeysParams p, int B, int slots, const __grid_constant__ CUten
         const uint32_t m = seen(g);
 #pragma unroll
         for (int x = 0; x < 16; x++) {
-          const float e0 = (m >> (2 * x) & 1) ? ex2_ftz(fmaf(__uint_as_float(s[2 * x]), sc2, -ref)) : 0.f;
-          const float e1 = (m >> (2 * x + 1) & 1) ? ex2_ftz(fmaf(__uint_as_float(s[2 * x + 1]), sc2, -ref)) : 0.f;
+          const float e0 = (m >> (2 * x) & 1) ? ex2_ftz(score(s[2 * x]) - ref) : 0.f;
+          const float e1 = (m >> (2 * x + 1) & 1) ? ex2_ftz(score(s[2 * x + 1]) - ref) : 0.f;
           l4[x & 3] += e0 + e1;
           pk[x] = pack_bf16x2(e0, e1);
           rest[x] = bf16x2_rest(e0, e1, pk[x]);

@@ -153,6 +153,34 @@ def test_dense_one_key_far_above_a_long_tail(n, max_n):
     assert np.all(np.abs(l[0, 0] - (gap + np.log(total))) <= sums + 2.0 ** -12 * tail + 2.0 ** -18)
 
 
+def check_one_hot(o, q, keys, scale, what):
+    """Logits of thousands and more: the output is the row of the largest one, wherever the next lies
+    far below it (the logits' own error is 2^-19 of the sum of their products' sizes: 512 terms in binary32)."""
+    logit, size = scale * (q @ keys.T), scale * (np.abs(q) @ np.abs(keys).T)
+    order = np.sort(logit, -1)
+    clear = order[:, -1] - order[:, -2] > 30 + 2.0 ** -18 * size.max(-1)
+    assert clear.mean() > 0.5, what
+    assert np.all(np.isfinite(o)), what
+    top = keys[np.argmax(logit, -1)]
+    assert np.all(np.abs(o - top)[clear] <= 2.0 ** -8 * np.abs(top)[clear] + 2.0 ** -30 * np.abs(keys).max()), what
+
+
+@pytest.mark.parametrize("fp8", [False])
+@pytest.mark.parametrize("Q,W", [(2, 64), (640, 64), (2, 700)])
+@pytest.mark.parametrize("size", [1e4, 1e9, 1e12, 1e30])
+def test_window_of_huge_queries(fp8, Q, W, size):
+    """Queries far above f16's range, whichever kernel takes them."""
+    g = synth.rng(63)
+    rows = draw_rows(g, fp8, 1, Q + W - 1)
+    q = bf16_bits(ref.bf16(synth.main_queries(g, 1, Q)) * size)
+    pos = W - 1 + np.arange(Q)[None, :]
+    o, l = run_window(q, rows, np.zeros(1, np.int64), pos, W)
+    rv = ref.row_values(rows[0])
+    assert np.all(np.isfinite(l))
+    for i in range(0, Q, max(1, Q // 20)):
+        check_one_hot(o[0, i], ref.bf16(q[0, i]), rv[i:i + W], SCALE, (i, size))
+
+
 @pytest.mark.parametrize("kind", ["window", "dense"])
 def test_scores_that_grow_by_the_last_bit(kind):
     """Scores (in powers of two) about 1.25 * 2^27, where neighbouring floats are 16 apart, growing by
