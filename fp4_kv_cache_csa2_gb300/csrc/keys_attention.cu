@@ -26,7 +26,8 @@
 // Operands: F16 (calls with cache entries or E4M3 rows) keeps every dequantised FP4
 // value (at most 6 significant bits, 2^-10 .. 2688) and every E4M3 value exactly and
 // rounds q and bf16 window rows to f16, exact inside [2^-14, 65504], with P to 11
-// bits (fewer below 2^-22 of the largest weight, see KA_TOP).  With bf16 rows alone the operands are bf16: q and rows as they are, P as two bf16
+// bits (fewer below 2^-22 of the largest weight, see KA_TOP); a head of q that reaches 2^16 is
+// scaled into f16's range by a power of two, so that q may be of any size, as with bf16 operands.  With bf16 rows alone the operands are bf16: q and rows as they are, P as two bf16
 // of 8 bits, its rounding and what that left (a second product with the same V): with the
 // first alone the errors of the outputs are 1.3 times those of their own rounding, with both
 // 1.00; 16 queries of 132 rows take 9.0 us instead of 7.7.  The sum of the softmax is taken
@@ -47,6 +48,8 @@
 // 1.03 PFLOP/s, their pipe active in 86 % of the cycles; 16 queries over 131,072 entries 260 us, 1.0
 // PFLOP/s; 602 queries of 1000 E4M3 rows 114 us.  A CTA costs about 7 us beside its chunks: 16
 // queries of 132 bf16 rows take 9.0 us.
+#include <cfloat>
+
 #include "attn_common.cuh"
 #include "params.cuh"
 
@@ -464,25 +467,63 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   } else {
     // ================= softmax and output: lane = (half, head 16 warp + lane % 16)
     const uint32_t quarter = (uint32_t)(warp * 32) << 16;
-    const float sc2 = p.scale * KA_LOG2E;
+    float sc2 = p.scale * KA_LOG2E;                   // products to scores in powers of two
     const int head = 16 * warp + (lane & 15), half = lane >> 4;
     float m_used = -INFINITY, l_sum = 0.f;            // the head's reference; its sum over this lane's keys
     bool ok = true;
     if (n_ch > 0) {                                   // Q: this lane's 256 dims of its head to TMEM
       ok = ok && ka_wait(&sm.q_full, 0, sm, p.hdr, 45);
       const unsigned char* qh = smem + ((KA_BUFS - 1) * 2 + half) * KA_HALF;
+      __half2 most = __half2half2(__ushort_as_half(0));   // F16: largest |q| of the lane's even and odd dims
 #pragma unroll 1
       for (int g = 0; g < 4; g++) {                   // column chunk g of the half: 32 columns of TMEM
         uint32_t w[32];
 #pragma unroll
         for (int u = 0; u < 8; u++) {
           const uint4 x = *reinterpret_cast<const uint4*>(qh + g * KA_COL + sw128((uint32_t)head, 16u * u));
-          w[4 * u] = F16 ? bf16x2_to_f16x2(x.x) : x.x;
-          w[4 * u + 1] = F16 ? bf16x2_to_f16x2(x.y) : x.y;
-          w[4 * u + 2] = F16 ? bf16x2_to_f16x2(x.z) : x.z;
-          w[4 * u + 3] = F16 ? bf16x2_to_f16x2(x.w) : x.w;
+          w[4 * u] = x.x;
+          w[4 * u + 1] = x.y;
+          w[4 * u + 2] = x.z;
+          w[4 * u + 3] = x.w;
+        }
+        if (F16) {
+#pragma unroll
+          for (int x = 0; x < 32; x++) {
+            w[x] = bf16x2_to_f16x2(w[x]);
+            most = __hmax2(most, __habs2(*reinterpret_cast<const __half2*>(&w[x])));
+          }
         }
         tmem_st32(quarter + KA_Q_COL + 32 * g, w);
+      }
+      if (F16) {
+        if (__any_sync(0xFFFFFFFFu, __hisinf(__hmax(__low2half(most), __high2half(most))) != 0)) {
+          // heads with a |q| of 2^16 or more, out of f16's range: once more, times a power of two that
+          // puts the largest into [2^15, 2^16), and their scale times its inverse.  (An infinity
+          // stays one.)
+          uint32_t size = 0u;                         // largest |q|, bf16 bits (2^16: 143 << 7)
+#pragma unroll 1
+          for (uint32_t x = 0; x < 128; x++) {
+            const uint32_t b =
+                *reinterpret_cast<const uint32_t*>(qh + (x >> 5) * KA_COL + sw128((uint32_t)head, 4u * (x & 31u)));
+            size = max(size, max(b & 0x7FFFu, b >> 16 & 0x7FFFu));
+          }
+          size = max(size, __shfl_xor_sync(0xFFFFFFFFu, size, 16));
+          const int e = max(min((int)(size >> 7), 254) - 142, 0);
+          const float down = __int_as_float((127 - e) << 23);
+          sc2 = fmaxf(fminf(sc2 * __int_as_float((127 + e) << 23), FLT_MAX), -FLT_MAX);   // finite: a product may be 0
+          tc::tmem_wait_st();
+#pragma unroll 1
+          for (int g = 0; g < 4; g++) {
+            uint32_t w[32];
+#pragma unroll
+            for (int x = 0; x < 32; x++) {
+              const uint32_t b =
+                  *reinterpret_cast<const uint32_t*>(qh + g * KA_COL + sw128((uint32_t)head, 4u * x));
+              w[x] = pack_f16x2(__uint_as_float(b << 16) * down, __uint_as_float(b & 0xFFFF0000u) * down);
+            }
+            tmem_st32(quarter + KA_Q_COL + 32 * g, w);
+          }
+        }
       }
       tc::tmem_wait_st();
       tc::fence_proxy_async_smem();                   // the buffer goes to copies and stores of others

@@ -438,7 +438,9 @@ csa2_status csa2_qk_norm_rope(const csa2_qk_args *args, void *ws, size_t ws_byte
  * Precision: binary32 accumulation and softmax state.  With bf16 rows the
  * operands are bf16.  With E4M3 rows, which both types hold exactly, they are
  * bf16 (calls of many neighbouring queries with short windows) or f16, and q
- * is then rounded as csa2_sparse_swa_attn does.  The probabilities are held to
+ * is then rounded to f16: exact from 2^-14 on, and a head with a value of 2^16
+ * or more is scaled by a power of two first, so that q may be of any size in
+ * every call.  The probabilities are held to
  * 16 bits with bf16 operands (two of 8) and to 11 with f16 (as in
  * csa2_dense_attn).  Workspace:
  * csa2_window_attn_workspace_size (partial states when a query's keys are
@@ -476,7 +478,8 @@ csa2_status csa2_window_attn(const csa2_window_args *args, void *ws, size_t ws_b
  * does a window position outside the supplied rows (skipped).  Entries and
  * rows that a query does not see may hold anything.
  * Sizes and alignment as in csa2_window_attn; operands as in
- * csa2_sparse_swa_attn (f16, the dequantised entries exact).  The probabilities
+ * csa2_sparse_swa_attn (f16, the dequantised entries exact; a head of q beyond
+ * f16's range is scaled into it as in csa2_window_attn).  The probabilities
  * are held to 11 bits; one below 2^-22 of a head's largest is off by at most
  * 2^-33 of that, while the softmax's sum has it in binary32.  Workspace:
  * csa2_dense_attn_workspace_size with the call's B, Q and max_n.

@@ -181,6 +181,75 @@ def test_window_of_huge_queries(fp8, Q, W, size):
         check_one_hot(o[0, i], ref.bf16(q[0, i]), rv[i:i + W], SCALE, (i, size))
 
 
+@pytest.mark.parametrize("Q", [2, 640])
+@pytest.mark.parametrize("size", [4e4, 1e6, 1e20, 1e35])
+def test_window_range_of_q_over_e4m3_rows(Q, size):
+    """A head's q of any size with a scale to match gives what the head of ordinary size gives."""
+    g = synth.rng(64)
+    W = 64
+    rows = draw_rows(g, True, 1, Q + W - 1)
+    small = ref.bf16(synth.main_queries(g, 1, Q))
+    big = ref.bf16(bf16_bits(small * np.where(np.arange(64) % 3 == 1, size, 1.0)[:, None]))   # every third head
+    pos = W - 1 + np.arange(Q)[None, :]
+    rv = ref.row_values(rows[0])
+    for scale, heads in ((SCALE, np.arange(64) % 3 != 1), (SCALE / size, np.arange(64) % 3 == 1)):
+        o, l = run_window(bf16_bits(big), rows, np.zeros(1, np.int64), pos, W, scale=scale)
+        assert np.all(np.isfinite(l[0][:, heads]))
+        for i in range(0, Q, max(1, Q // 20)):
+            want, lse, tol, tol_l = ref.attend(big[0, i], rv[i:i + W], scale, ref.U_F16)
+            assert np.all(np.abs(o[0, i] - want)[heads] <= tol[heads]), (i, scale)
+            assert np.all(np.abs(l[0, i] - lse)[heads] <= tol_l[heads])
+
+
+@pytest.mark.parametrize("Q,W", [(2, 64), (640, 64), (2, 700)])
+@pytest.mark.parametrize("size", [1e4, 1e9, 1e12, 1e30])
+def test_huge_queries_over_e4m3_rows(Q, W, size):
+    test_window_of_huge_queries(size=size, Q=Q, W=W, fp8=True)
+
+
+@pytest.mark.parametrize("size", [1e5, 1e9, 1e30])
+def test_huge_queries_over_the_cache(size):
+    g = synth.rng(67)
+    n = 700
+    kv = g.integers(0, 256, (n, 288), dtype=np.uint8)
+    kv[:, 256:] = g.integers(0x28, 0x30, (n, 32), dtype=np.uint8)
+    rows, pos, base = draw_rows(g, False, 1, 130), np.array([[n - 3, n - 1, n - 2]]), np.array([n - 130])
+    q = ref.bf16(synth.main_queries(g, 1, 3)) * np.where(np.arange(64) % 2, size, 1.0)[:, None]
+    q[0, 1, :, 100:] /= size                                  # large and small dims in a head
+    q = bf16_bits(q)
+    o, l = run_dense(torch.from_numpy(kv).cuda(), n, q, rows, base, pos, n)
+    entries, rv, odd = oracle.dequant_main(kv), ref.row_values(rows[0]), np.arange(64) % 2 == 1
+    for i in range(3):
+        keys, qv = ref.dense_keys(entries, n, 1, rv, int(base[0]), int(pos[0, i])), ref.bf16(q[0, i])
+        check_one_hot(o[0, i][odd], qv[odd], keys, SCALE, (i, size))
+        want, lse, tol, tol_l = ref.attend(qv, keys, SCALE, ref.U_F16)
+        # heads of ordinary size beside them (f16 below 2^-14: 2^-25 of each product's q)
+        tol += 2 * SCALE * 2.0 ** -25 * np.abs(keys).sum(-1).max() * np.abs(keys).max()
+        assert np.all(np.abs(o[0, i] - want)[~odd] <= tol[~odd]), i
+
+
+@pytest.mark.parametrize("Q", [2, 640])
+def test_queries_that_are_not_finite_over_e4m3_rows(Q):
+    """A head's infinity or NaN stays in that head, whatever the sizes of the others."""
+    g = synth.rng(68)
+    W = 40
+    rows = draw_rows(g, True, 1, Q + W - 1)
+    q = ref.bf16(synth.main_queries(g, 1, Q))
+    q[0, :, 1::4] *= 1e20
+    q[0, :, 5, 17], q[0, :, 6, 300] = np.inf, np.nan
+    q[0, :, 9, 511] = -np.inf
+    q = bf16_bits(q)
+    pos = W - 1 + np.arange(Q)[None, :]
+    o, l = run_window(q, rows, np.zeros(1, np.int64), pos, W)
+    rv, plain = ref.row_values(rows[0]), np.arange(64) % 4 != 1
+    assert np.all(np.isnan(o[0, :, [5, 6, 9]]))
+    plain[6] = False
+    for i in range(0, Q, max(1, Q // 20)):
+        want, lse, tol, tol_l = ref.attend(np.where(plain[:, None], ref.bf16(q[0, i]), 0.0), rv[i:i + W], SCALE, ref.U_F16)
+        assert np.all(np.abs(o[0, i] - want)[plain] <= tol[plain])
+        assert np.all(np.abs(l[0, i] - lse)[plain] <= tol_l[plain])
+
+
 @pytest.mark.parametrize("kind", ["window", "dense"])
 def test_scores_that_grow_by_the_last_bit(kind):
     """Scores (in powers of two) about 1.25 * 2^27, where neighbouring floats are 16 apart, growing by
