@@ -698,10 +698,11 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 // heads: thread = (slice of the states, head, 4 dims of each group), so that a warp reads pieces of
 // 128 bytes of [dims / 4][head][4] and writes 32 bytes a head.  Bound by the latency of its reads (a
 // state is 130 KB, in L2): a thread has BATCH states on their way while the CTA works out
-// the weights.
+// the weights.  It may start while the CTAs of the query still write their states, so these are not
+// read-only for its life: no __restrict__, and every read of them is a load from L2 behind the wait.
 template <int SLICES, int GROUPS, int BATCH, int MOST>
 __global__ void __launch_bounds__(SLICES * H * 4)
-keys_combine_kernel(const float* __restrict__ part, int split, uint16_t* __restrict__ out, float* __restrict__ lse) {
+keys_combine_kernel(const float* part, int split, uint16_t* out, float* lse) {
   constexpr int ROWS = SLICES * 4;                    // states whose references are read at once
   constexpr int CTAS = D / (16 * GROUPS);             // of a query
   __shared__ __align__(16) float weight[MOST][H];     // then the slices' sums
@@ -727,7 +728,7 @@ keys_combine_kernel(const float* __restrict__ part, int split, uint16_t* __restr
     const int hw = tid % H, r = tid / H;
     float mx = -INFINITY, L = 0.f;
 #pragma unroll 4
-    for (int s = r; s < split; s += ROWS) mx = fmaxf(mx, pb[(int64_t)s * KA_PART_FLOATS + hw]);
+    for (int s = r; s < split; s += ROWS) mx = fmaxf(mx, __ldcg(pb + (int64_t)s * KA_PART_FLOATS + hw));
     red[r][hw] = mx;
     __syncthreads();
 #pragma unroll
@@ -736,7 +737,7 @@ keys_combine_kernel(const float* __restrict__ part, int split, uint16_t* __restr
 #pragma unroll 4
     for (int s = r; s < split; s += ROWS) {
       const float* ps = pb + (int64_t)s * KA_PART_FLOATS + hw;
-      const float l = ps[H], w = l != 0.f ? exp2f(ps[0] - mx) : 0.f;   // l = 0: a state without keys
+      const float l = __ldcg(ps + H), w = l != 0.f ? exp2f(__ldcg(ps) - mx) : 0.f;   // l = 0: a state without keys
       weight[s][hw] = w;
       L += w * l;
     }

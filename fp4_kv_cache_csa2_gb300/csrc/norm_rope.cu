@@ -71,13 +71,13 @@ __device__ __forceinline__ void qk_finish(const uint4& v, float r, const float4*
 #pragma unroll
   for (int i = 0; i < 8; i++) f[i] *= r;
   if (w) {
-    const float4 w0 = __ldg(w + 64 * half + 2 * lane), w1 = __ldg(w + 64 * half + 2 * lane + 1);
+    const float4 w0 = __ldca(w + 64 * half + 2 * lane), w1 = __ldca(w + 64 * half + 2 * lane + 1);
     const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
     for (int i = 0; i < 8; i++) f[i] *= wv[i];
   }
   if (half == 1 && lane >= 24) {
-    const float4 c0 = __ldg(cs + 2 * (lane - 24)), c1 = __ldg(cs + 2 * (lane - 24) + 1);   // cos, sin, cos, sin
+    const float4 c0 = __ldca(cs + 2 * (lane - 24)), c1 = __ldca(cs + 2 * (lane - 24) + 1);   // cos, sin, cos, sin
     const float c[4] = {c0.x, c0.z, c1.x, c1.z}, s[4] = {c0.y, c0.w, c1.y, c1.w};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -103,6 +103,8 @@ __device__ __forceinline__ const float4* qk_table_row(const QkParams& p, int64_t
 // QROWS: neighbouring heads of a token that a warp takes.
 template <int QROWS>
 __global__ void __launch_bounds__(QK_THREADS, qk_ctas(QROWS)) qk_norm_rope_kernel(QkParams p) {
+  // (what the kernel before writes is not read-only for this one's life: no __ldg, and every load behind
+  // the wait)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t g = (int64_t)blockIdx.x * (QK_THREADS / 32) + (threadIdx.x >> 5);

@@ -137,11 +137,12 @@ __device__ __forceinline__ bool wa_any(bool x) {
   return r != 0;
 }
 
-// A row of the window buffer, 16 bytes of each half a lane (E4M3: 16 dims in the first)
+// A row of the window buffer, 16 bytes of each half a lane (E4M3: 16 dims in the first).  From L2: the
+// kernel before, beside whose end this one starts, may have written it.
 __device__ __forceinline__ void wa_load_row(uint4* v, const uint8_t* row, int fp8, int lane) {
   const uint4* src = reinterpret_cast<const uint4*>(row);
-  v[0] = __ldg(src + lane);
-  if (!fp8) v[1] = __ldg(src + 32 + lane);
+  v[0] = __ldcg(src + lane);
+  if (!fp8) v[1] = __ldcg(src + 32 + lane);
 }
 
 // to its slot, as bf16.  False: it is not finite, and stays out unless `any` row may go in

@@ -274,3 +274,33 @@ def test_scores_that_grow_by_the_last_bit(kind):
     assert np.all(np.isfinite(o)) and np.all(np.isfinite(l))
     assert np.all(np.abs(o[..., :256] - 1) <= 2.0 ** -8)
     assert np.all((o[..., 256] >= 0) & (o[..., 256] <= 3)) and np.all(o[..., 257:] == 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Q,W", [(640, 60), (3, 2000), (16, 128)])
+def test_calls_in_a_row_read_what_the_one_before_wrote(fp8, Q, W):
+    """Rows and queries made by one call and read by the next, again and again over the same buffers
+    (each call may start beside the end of the one before): the bits of calls that are waited for."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    S, n = Q + W - 1, 12
+    k = torch.randn(n, S, 512, device="cuda", generator=gen).bfloat16()
+    q = torch.randn(n, Q, 64, 512, device="cuda", generator=gen).bfloat16()
+    cs, pos, base = csa2.rope_table(S).cuda(), torch.arange(S, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    rows = torch.zeros(1, S, 512, dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+    mine = torch.zeros(1, Q, 64, 512, dtype=torch.bfloat16, device="cuda")
+    ws = csa2.Workspace(csa2.window_attn_workspace_size(1, Q, W, 0))
+    got = []
+    for wait in (False, True):
+        out, lse = torch.zeros(n, 1, Q, 64, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, 1, Q, 64, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(n):
+            for call in (lambda: csa2.qk_norm_rope(pos, cs, ws, k=k[i], rows=rows),
+                         lambda: csa2.qk_norm_rope(pos[W - 1:], cs, ws, q=q[i], q_out=mine[0]),
+                         lambda: csa2.window_attn(mine, rows, base, pos[None, W - 1:], SCALE, out[i], ws, W=W, lse=lse[i])):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        got.append((out, lse))
+    assert ws.sync_status()[0] == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert not torch.equal(got[0][0][0], got[0][0][1])
