@@ -361,23 +361,32 @@ _pack_qk, _pack_window, _pack_dense = _packer(QkArgs), _packer(WindowArgs), _pac
 
 
 def _refuse(name: str, t, shape, what, index):
+    if t is None:
+        raise ValueError(f"{name}: missing; expected {tuple(shape)} of {what}, on device {index}")
     raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}; expected "
                      f"{tuple(shape)} of {what}, on device {index}")
 
 
 def _at(name: str, t, shape, types, index):
     """Address of a contiguous tensor of this shape and one of these types on CUDA device `index`."""
-    if t.shape != shape or t.dtype not in types or t.get_device() != index or not t.is_contiguous():
+    if t is None or t.shape != shape or t.dtype not in types or t.get_device() != index or not t.is_contiguous():
         _refuse(name, t, shape, f"{types}, contiguous", index)
     return t.data_ptr()
 
 
 def _tokens(name: str, t, shape, inner, types, index):
     """Address of tokens whose strides but the first are `inner`, and that stride."""
-    first, *rest = t.stride()
+    first, *rest = t.stride() or (0,)                  # (none at all: refused by its shape)
     if t.shape != shape or rest != inner or t.dtype not in types or t.get_device() != index:
         _refuse(name, t, shape, f"{types}, inner strides {inner}", index)
     return t.data_ptr(), first
+
+
+def _rank(name: str, t, shape):
+    """The sizes of a tensor with as many axes as `shape` names."""
+    if t is None or t.dim() != len(shape):
+        raise ValueError(f"{name}: {'missing' if t is None else tuple(t.shape)}; expected [{']['.join(shape)}]")
+    return t.shape
 
 
 def _call(fn, index, stream, *args):
@@ -400,7 +409,7 @@ def qk_norm_rope(pos, rope_cs, ws: Workspace, *, q=None, q_weight=None, q_out=No
     -> q_out, window keys k [T][512] -> row k_slot[t] (None: t) of rows [..][512]
     (bf16, or E4M3).  Tokens with pos -1 write nothing.  q and k may be
     views with a larger token stride; q_out may be q itself."""
-    buf, T, table = ws.buf, pos.numel(), rope_cs.shape[0]
+    buf, (T,), table = ws.buf, _rank("pos", pos, ("T",)), _rank("rope_cs", rope_cs, ("P", "32", "2"))[0]
     dev = buf.get_device()
     bf16, row_types, i64, f32 = _types()
     qa = qs = qw = qo = ka = ks = kw = ro = sl = n_rows = fp8 = 0
@@ -418,7 +427,7 @@ def qk_norm_rope(pos, rope_cs, ws: Workspace, *, q=None, q_weight=None, q_out=No
             ks = D_LATENT
         if k_weight is not None:
             kw = _at("k_weight", k_weight, (D_LATENT,), f32, dev)
-        ro = _at("rows", rows, (*rows.shape[:-1], D_LATENT), row_types, dev)
+        ro = _at("rows", rows, (D_LATENT,) if rows is None else (*rows.shape[:-1], D_LATENT), row_types, dev)
         n_rows, fp8 = rows.numel() // D_LATENT, 1 if rows.element_size() == 1 else 0
         if k_slot is not None:
             sl = _at("k_slot", k_slot, (T,), i64, dev)
@@ -436,7 +445,8 @@ def window_attn(q, rows, swa_base_pos, q_pos, scale: float, out, ws: Workspace, 
     """Queries [B][Q][64][512] over the window rows [B][S][512] of positions
     t-W+1 .. t and the sinks [B][n][512] before them (both bf16, or both
     E4M3).  lse: float32 [B][Q][64] or None."""
-    buf, (B, Q), S, n = ws.buf, q_pos.shape, rows.shape[1], 0 if sinks is None else sinks.shape[1]
+    buf, (B, Q), S = ws.buf, _rank("q_pos", q_pos, ("B", "Q")), _rank("rows", rows, ("B", "S", "512"))[1]
+    n = 0 if sinks is None else _rank("sinks", sinks, ("B", "n_sink", "512"))[1]
     dev = buf.get_device()
     bf16, row_types, i64, f32 = _types()
     shape = (B, Q, N_HEADS, D_LATENT)
@@ -461,7 +471,7 @@ def dense_attn(cache: Cache, q, swa, swa_base_pos, q_pos, scale: float, out, ws:
     window, rows swa [B][S][512] (bf16, or E4M3).  max_n: the most entries
     a query sees (it sizes the work split, nothing else).  lse: float32
     [B][Q][64] or None."""
-    buf, (B, Q), S = ws.buf, q_pos.shape, swa.shape[1]
+    buf, (B, Q), S = ws.buf, _rank("q_pos", q_pos, ("B", "Q")), _rank("swa", swa, ("B", "S", "512"))[1]
     dev = buf.get_device()
     if B != cache.B:
         raise ValueError(f"q_pos: {B} sequences, the cache has {cache.B}")

@@ -1,0 +1,64 @@
+"""Refusals of the binding's norm and rotation, window attention and dense attention: arguments that
+are missing or have another number of axes.  Nothing here reaches the library."""
+import pytest
+import torch
+
+import fp4_kv_cache_csa2_gb300 as csa2
+
+
+class _FakeWs:
+    """Stands for a workspace: the binding's own checks come before the call."""
+    buf, ptr, nbytes = torch.zeros(1, dtype=torch.uint8), 1 << 36, 256
+
+
+BF16, I64 = torch.bfloat16, torch.int64
+
+
+def norm_args(**kw):
+    a = dict(pos=torch.zeros(2, dtype=I64), rope_cs=torch.zeros(4, 32, 2), ws=_FakeWs, q=torch.zeros(2, 64, 512, dtype=BF16),
+             q_out=torch.zeros(2, 64, 512, dtype=BF16), k=torch.zeros(2, 512, dtype=BF16), rows=torch.zeros(5, 512, dtype=BF16))
+    a.update(kw)
+    return a
+
+
+def attn_args(name, **kw):
+    a = dict(q=torch.zeros(1, 2, 64, 512, dtype=BF16), swa_base_pos=torch.zeros(1, dtype=I64),
+             q_pos=torch.zeros(1, 2, dtype=I64), scale=0.1, out=torch.zeros(1, 2, 64, 512, dtype=BF16), ws=_FakeWs)
+    if name == "window":
+        a.update(rows=torch.zeros(1, 9, 512, dtype=BF16), W=8, sinks=torch.zeros(1, 3, 512, dtype=BF16))
+    else:
+        a.update(cache=csa2.Cache(1, 8, 1, device="cpu"), swa=torch.zeros(1, 9, 512, dtype=BF16), max_n=8)
+    a.update(kw)
+    return a
+
+
+@pytest.mark.parametrize("name", ["pos", "rope_cs", "q_out", "rows"])
+def test_norm_refuses_what_is_missing(name):
+    with pytest.raises(ValueError, match=f"{name}: missing"):
+        csa2.qk_norm_rope(**norm_args(**{name: None}))
+
+
+@pytest.mark.parametrize("name,shape", [("pos", (1, 2)), ("pos", ()), ("rope_cs", (4, 64)), ("q", (64, 512)), ("q", ()),
+                                        ("k", (1, 2, 512)), ("rows", ()), ("rows", (5, 511)), ("q_out", (2, 64 * 512))])
+def test_norm_refuses_other_axes(name, shape):
+    old = norm_args()[name]
+    with pytest.raises(ValueError, match=f"{name}:"):
+        csa2.qk_norm_rope(**norm_args(**{name: torch.zeros(shape, dtype=old.dtype)}))
+
+
+@pytest.mark.parametrize("call,names", [("window", ["q", "rows", "swa_base_pos", "q_pos", "out"]),
+                                        ("dense", ["q", "swa", "swa_base_pos", "q_pos", "out"])])
+def test_attentions_refuse_what_is_missing_or_has_other_axes(call, names):
+    fn = csa2.window_attn if call == "window" else csa2.dense_attn
+    for name in names:
+        with pytest.raises(ValueError, match=f"{name}: missing"):
+            fn(**attn_args(call, **{name: None}))
+        old = attn_args(call)[name]
+        for other in (old.flatten()[0], old.flatten(), old[None]):
+            if other.shape == old.shape:
+                continue
+            with pytest.raises(ValueError, match=f"{name}:"):
+                fn(**attn_args(call, **{name: other}))
+    if call == "window":
+        with pytest.raises(ValueError, match="sinks:"):
+            fn(**attn_args(call, sinks=torch.zeros(3, dtype=BF16)))
