@@ -393,6 +393,8 @@ def _call(fn, index, stream, *args):
     """fn(*args, stream) with device `index` current; stream None: the device's current one, whose
     handle is asked for directly (a stream object costs as much as the launch)."""
     import torch
+    if index < 0:
+        raise ValueError("ws: the workspace is not on a CUDA device")
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == index:
         status = fn(*args, handle)

@@ -62,3 +62,11 @@ def test_attentions_refuse_what_is_missing_or_has_other_axes(call, names):
     if call == "window":
         with pytest.raises(ValueError, match="sinks:"):
             fn(**attn_args(call, sinks=torch.zeros(3, dtype=BF16)))
+
+
+def test_a_workspace_on_the_host_is_refused():
+    """Everything in host memory agrees with itself: no call may take it to the GPU."""
+    for call in (lambda: csa2.qk_norm_rope(**norm_args()), lambda: csa2.window_attn(**attn_args("window")),
+                 lambda: csa2.dense_attn(**attn_args("dense"))):
+        with pytest.raises(ValueError, match="ws: the workspace is not on a CUDA device"):
+            call()
