@@ -389,13 +389,20 @@ def _rank(name: str, t, shape):
     return t.shape
 
 
+def _current_stream(index):
+    """Handle of the current stream of CUDA device `index`: asked for directly where torch offers that (a
+    stream object costs as much as the launch), else through the public call."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(index).cuda_stream if raw is None else raw(index)
+
+
 def _call(fn, index, stream, *args):
-    """fn(*args, stream) with device `index` current; stream None: the device's current one, whose
-    handle is asked for directly (a stream object costs as much as the launch)."""
+    """fn(*args, stream) with device `index` current; stream None: the device's current one."""
     import torch
     if index < 0:
         raise ValueError("ws: the workspace is not on a CUDA device")
-    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    handle = _current_stream(index) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == index:
         status = fn(*args, handle)
     else:

@@ -70,3 +70,13 @@ def test_a_workspace_on_the_host_is_refused():
                  lambda: csa2.dense_attn(**attn_args("dense"))):
         with pytest.raises(ValueError, match="ws: the workspace is not on a CUDA device"):
             call()
+
+
+def test_the_current_stream_without_torchs_own_shortcut(monkeypatch):
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: Stream if index == 3 else None)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 40 + index, raising=False)
+    assert csa2._current_stream(3) == 43
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert csa2._current_stream(3) == 77
