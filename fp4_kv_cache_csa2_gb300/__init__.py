@@ -349,6 +349,13 @@ def _types():
     return bf16, (*bf16, torch.uint8, torch.int8, torch.float8_e4m3fn), (torch.int64,), (torch.float32,)
 
 
+@functools.cache
+def _cache_types():
+    """Types that hold cache entries and their number."""
+    import torch
+    return (torch.uint8, torch.int8), (torch.int32,)
+
+
 def _packer(cls):
     """The layout of a struct of C arguments; bytes packed by it stand for the struct."""
     codes = {ctypes.c_int: "i", ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "Q"}
@@ -484,9 +491,10 @@ def dense_attn(cache: Cache, q, swa, swa_base_pos, q_pos, scale: float, out, ws:
     dev = buf.get_device()
     if B != cache.B:
         raise ValueError(f"q_pos: {B} sequences, the cache has {cache.B}")
-    if cache.main_kv.get_device() != dev:
-        raise ValueError(f"the cache is on {cache.main_kv.device}, the workspace on {buf.device}")
     bf16, row_types, i64, f32 = _types()
+    u8, i32 = _cache_types()
+    _at("cache.main_kv", cache.main_kv, (B, cache.cap, MAIN_ENTRY_BYTES), u8, dev)
+    _at("cache.n_entries", cache.n_entries, (B,), i32, dev)
     shape = (B, Q, N_HEADS, D_LATENT)
     a = _pack_dense(B, Q, S, scale, max_n, _at("q_pos", q_pos, (B, Q), i64, dev), _at("q", q, shape, bf16, dev),
                     _at("swa", swa, (B, S, D_LATENT), row_types, dev),

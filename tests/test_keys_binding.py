@@ -80,3 +80,23 @@ def test_the_current_stream_without_torchs_own_shortcut(monkeypatch):
     assert csa2._current_stream(3) == 43
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     assert csa2._current_stream(3) == 77
+
+
+def test_dense_refuses_a_cache_that_is_not_as_it_says():
+    """The tensors of a cache are the caller's to replace: entries of another size or type, fewer than `cap`,
+    strided ones, and numbers of entries in 64 bits or of another batch."""
+    def call(**kw):
+        cache = csa2.Cache(1, 8, 1, device="cpu")
+        for name, value in kw.items():
+            setattr(cache, name, value)
+        return csa2.dense_attn(**attn_args("dense", cache=cache))
+    u8 = torch.uint8
+    for bad in (torch.zeros(1, 8, 280, dtype=u8), torch.zeros(1, 7, 288, dtype=u8), torch.zeros(2, 8, 288, dtype=u8),
+                torch.zeros(1, 8, 288), torch.zeros(1, 16, 288, dtype=u8)[:, ::2], torch.zeros(8, 288, dtype=u8), None):
+        with pytest.raises(ValueError, match="cache.main_kv"):
+            call(main_kv=bad)
+    with pytest.raises(ValueError, match="cache.main_kv"):
+        call(cap=16)
+    for bad in (torch.zeros(1, dtype=I64), torch.zeros(2, dtype=torch.int32), torch.zeros(1), None):
+        with pytest.raises(ValueError, match="cache.n_entries"):
+            call(n_entries=bad)
