@@ -150,20 +150,23 @@ def _stream(stream) -> int | None:
 
 # ------------------------------------------------------------------ objects
 class Cache:
-    """One source layer's global cache in device memory (caller-owned tensors)."""
+    """One source layer's global cache in device memory (caller-owned tensors).
+    index=False: without index keys, for dense_attn alone (the other calls refuse it)."""
 
-    def __init__(self, B: int, cap: int, m: int, device="cuda"):
+    def __init__(self, B: int, cap: int, m: int, device="cuda", index: bool = True):
         import torch
         cap = -(-int(cap) // BLOCK) * BLOCK        # the library needs cap % 8 == 0
         self.B, self.cap, self.m = B, cap, m
         self.main_kv = torch.zeros((B, cap, MAIN_ENTRY_BYTES), dtype=torch.uint8, device=device)
-        self.idx_codes = torch.zeros((B, cap, INDEX_CODE_BYTES), dtype=torch.uint8, device=device)
-        self.idx_scales = torch.zeros((B, cap, INDEX_SCALE_BYTES), dtype=torch.uint8, device=device)
+        self.idx_codes = self.idx_scales = None
+        if index:
+            self.idx_codes = torch.zeros((B, cap, INDEX_CODE_BYTES), dtype=torch.uint8, device=device)
+            self.idx_scales = torch.zeros((B, cap, INDEX_SCALE_BYTES), dtype=torch.uint8, device=device)
         self.n_entries = torch.zeros((B,), dtype=torch.int32, device=device)
 
     def struct(self) -> CacheStruct:
-        return CacheStruct(self.main_kv.data_ptr(), self.idx_codes.data_ptr(),
-                           self.idx_scales.data_ptr(), self.cap, self.n_entries.data_ptr(), self.m)
+        return CacheStruct(self.main_kv.data_ptr(), _ptr(self.idx_codes), _ptr(self.idx_scales), self.cap,
+                           self.n_entries.data_ptr(), self.m)
 
     def sequence(self, b: int) -> "Cache":
         """Sequence b as a batch-1 cache sharing this cache's memory (for writing
@@ -171,8 +174,8 @@ class Cache:
         v = Cache.__new__(Cache)
         v.B, v.cap, v.m = 1, self.cap, self.m
         v.main_kv = self.main_kv[b:b + 1]
-        v.idx_codes = self.idx_codes[b:b + 1]
-        v.idx_scales = self.idx_scales[b:b + 1]
+        v.idx_codes = None if self.idx_codes is None else self.idx_codes[b:b + 1]
+        v.idx_scales = None if self.idx_scales is None else self.idx_scales[b:b + 1]
         v.n_entries = self.n_entries[b:b + 1]
         return v
 
@@ -404,11 +407,12 @@ def _current_stream(index):
     return torch.cuda.current_stream(index).cuda_stream if raw is None else raw(index)
 
 
-def _call(fn, index, stream, *args):
-    """fn(*args, stream) with device `index` current; stream None: the device's current one."""
+def _call(name: str, index, stream, *args):
+    """The library's call `name`(*args, stream) with device `index` current; stream None: the device's current one."""
     import torch
     if index < 0:
         raise ValueError("ws: the workspace is not on a CUDA device")
+    fn = getattr(_lib or load(), name)
     handle = _current_stream(index) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == index:
         status = fn(*args, handle)
@@ -416,7 +420,7 @@ def _call(fn, index, stream, *args):
         with torch.cuda.device(index):
             status = fn(*args, handle)
     if status != 0:
-        raise Csa2Error(fn.__name__, status)
+        raise Csa2Error(name, status)
 
 
 def qk_norm_rope(pos, rope_cs, ws: Workspace, *, q=None, q_weight=None, q_out=None, k=None, k_weight=None, rows=None,
@@ -449,7 +453,7 @@ def qk_norm_rope(pos, rope_cs, ws: Workspace, *, q=None, q_weight=None, q_out=No
             sl = _at("k_slot", k_slot, (T,), i64, dev)
     a = _pack_qk(T, _at("pos", pos, (T,), i64, dev), _at("rope_cs", rope_cs, (table, D_ROPE // 2, 2), f32, dev), table,
                  eps, fp8, qa, qs, qw, qo, ka, ks, kw, ro, n_rows, sl)
-    _call((_lib or load()).csa2_qk_norm_rope, dev, stream, a, buf.data_ptr(), ws.nbytes)
+    _call("csa2_qk_norm_rope", dev, stream, a, buf.data_ptr(), ws.nbytes)
 
 
 def window_attn_workspace_size(B: int, Q: int, W: int, n_sink: int) -> int:
@@ -474,7 +478,7 @@ def window_attn(q, rows, swa_base_pos, q_pos, scale: float, out, ws: Workspace, 
                      _at("sinks", sinks, (B, n, D_LATENT), row_types, dev) if n else 0, _at("out", out, shape, bf16, dev),
                      0 if lse is None else _at("lse", lse, (B, Q, N_HEADS), f32, dev),
                      1 if rows.element_size() == 1 else 0)
-    _call((_lib or load()).csa2_window_attn, dev, stream, a, buf.data_ptr(), ws.nbytes)
+    _call("csa2_window_attn", dev, stream, a, buf.data_ptr(), ws.nbytes)
 
 
 def dense_attn_workspace_size(B: int, Q: int, max_n: int) -> int:
@@ -501,4 +505,4 @@ def dense_attn(cache: Cache, q, swa, swa_base_pos, q_pos, scale: float, out, ws:
                     _at("swa_base_pos", swa_base_pos, (B,), i64, dev), _at("out", out, shape, bf16, dev),
                     0 if lse is None else _at("lse", lse, (B, Q, N_HEADS), f32, dev),
                     1 if swa.element_size() == 1 else 0)
-    _call((_lib or load()).csa2_dense_attn, dev, stream, ctypes.byref(cache.struct()), a, buf.data_ptr(), ws.nbytes)
+    _call("csa2_dense_attn", dev, stream, ctypes.byref(cache.struct()), a, buf.data_ptr(), ws.nbytes)

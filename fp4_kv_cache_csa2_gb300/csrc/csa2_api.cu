@@ -26,12 +26,19 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
   return an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
 }
 
-csa2_status check_cache(const csa2_cache* c) {
-  if (!c || !c->main_kv || !c->idx_codes || !c->idx_scales || !c->n_entries) return CSA2_ERR_INVALID_ARG;
+// what a call that reads no index key needs of a cache
+csa2_status check_cache_entries(const csa2_cache* c) {
+  if (!c || !c->main_kv || !c->n_entries) return CSA2_ERR_INVALID_ARG;
   if (c->cap < 0 || (c->cap % BLK) != 0) return CSA2_ERR_INVALID_ARG;
   if (c->m != 1 && c->m != 2) return CSA2_ERR_UNSUPPORTED;
-  if (!aligned16(c->main_kv) || !aligned16(c->idx_codes) || !aligned16(c->idx_scales)) return CSA2_ERR_INVALID_ARG;
-  return CSA2_OK;
+  return aligned16(c->main_kv) ? CSA2_OK : CSA2_ERR_INVALID_ARG;
+}
+
+csa2_status check_cache(const csa2_cache* c) {
+  if (!c || !c->idx_codes || !c->idx_scales) return CSA2_ERR_INVALID_ARG;
+  const csa2_status st = check_cache_entries(c);
+  if (st != CSA2_OK) return st;
+  return aligned16(c->idx_codes) && aligned16(c->idx_scales) ? CSA2_OK : CSA2_ERR_INVALID_ARG;
 }
 
 csa2_status check_ws(void* ws, size_t ws_bytes, size_t need) {
@@ -460,9 +467,9 @@ size_t csa2_dense_attn_workspace_size(int B, int Q, int64_t max_n) {
 
 csa2_status csa2_dense_attn(const csa2_cache* cache, const csa2_dense_args* a, void* ws, size_t ws_bytes,
                             void* stream) {
-  csa2_status st = check_cache(cache);
+  csa2_status st = check_cache_entries(cache);
   if (st != CSA2_OK) return st;
-  if (!a || a->max_n < 0) return CSA2_ERR_INVALID_ARG;
+  if (!a || a->max_n < 0 || ((uintptr_t)cache->n_entries & 3u) != 0) return CSA2_ERR_INVALID_ARG;
   KeysParams p{};
   p.q = a->q;
   p.q_pos = a->q_pos;

@@ -472,6 +472,8 @@ csa2_status csa2_window_attn(const csa2_window_args *args, void *ws, size_t ws_b
  *   A query at raw position t >= 0 sees the entries j < min(n_entries[b],
  *   floor((t+1)/m)) and the window positions max(0, t-127) .. t; a query with
  *   t < 0 (padding) sees nothing: its output is zeros, its lse -inf.
+ *   cache        main_kv, cap, n_entries (4-byte aligned) and m; idx_codes and
+ *                idx_scales are not read and may be NULL.
  *   max_n        the most entries any query sees: it only sizes the split of a
  *                query over CTAs, every visible entry is attended in any case.
  * n_entries[b] > cap raises CSA2_ERR_BOUNDS (cap entries are attended), and so
