@@ -13,6 +13,7 @@ from tests import keys_ref as ref
 
 pytestmark = pytest.mark.gpu
 SCALE = 1 / math.sqrt(512)
+NAN_BF16, NAN_E4M3, INF_BF16 = 0x7FC0, 0x7F, 0x7F80
 
 
 def up(a):
@@ -274,6 +275,47 @@ def test_scores_that_grow_by_the_last_bit(kind):
     assert np.all(np.isfinite(o)) and np.all(np.isfinite(l))
     assert np.all(np.abs(o[..., :256] - 1) <= 2.0 ** -8)
     assert np.all((o[..., 256] >= 0) & (o[..., 256] <= 3)) and np.all(o[..., 257:] == 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_window_bad_rows_beside_finite_sinks(fp8):
+    """Rows that are not finite among many queries with sinks: each query takes what it sees, and no more."""
+    g = synth.rng(65)
+    bads = (NAN_E4M3, 0xFF) if fp8 else (NAN_BF16, INF_BF16, 0xFF80)
+    for W, n_sink in ((32, 4), (128, 16)):
+        Q = 620
+        pos = np.arange(Q)[None, :]
+        rows, sinks, q = draw_rows(g, fp8, 1, Q), draw_rows(g, fp8, 1, n_sink), synth.main_queries(g, 1, Q)
+        for n, (r, c) in enumerate([(0, 3), (200, 7), (201, 500), (333, 0), (430, 511), (619, 5)]):
+            rows[0, r, c] = bads[n % len(bads)]
+        o, l = run_window(q, rows, np.zeros(1, np.int64), pos, W, sinks)
+        rv, sv = ref.row_values(rows[0]), ref.row_values(sinks[0])
+        finite = 0
+        for t in range(Q):
+            keys = ref.window_keys(rv, 0, t, W, sv)
+            if np.all(np.isfinite(keys)):
+                finite += 1
+                want, lse, tol, tol_l = ref.attend(ref.bf16(q[0, t]), keys, SCALE, 2.0 ** -11)
+                assert np.all(np.abs(o[0, t] - want) <= tol), t
+                assert np.all(np.abs(l[0, t] - lse) <= tol_l), t
+            else:
+                assert np.any(np.isnan(o[0, t])), t
+        assert finite > 60
+
+
+@pytest.mark.parametrize("n,Q,max_n", [(1500, 320, 1500), (1500, 2, 1500), (9000, 2, 0)])
+def test_dense_errors_are_those_of_the_output(n, Q, max_n):
+    g = synth.rng(66)
+    kv = g.integers(0, 256, (n, 288), dtype=np.uint8)
+    kv[:, 256:] = g.integers(0x28, 0x30, (n, 32), dtype=np.uint8)
+    rows, q = draw_rows(g, False, 1, Q + 127), synth.main_queries(g, 1, Q)
+    pos = n - Q + np.arange(Q)[None, :]
+    base = pos[:, 0] - 127
+    o, _ = run_dense(torch.from_numpy(kv).cuda(), n, q, rows, base, pos, max_n)
+    entries, rv = oracle.dequant_main(kv), ref.row_values(rows[0])
+    some = list(range(0, Q, max(1, Q // 8)))
+    want = [exact(ref.bf16(q[0, i]), ref.dense_keys(entries, n, 1, rv, int(base[0]), int(pos[0, i])), SCALE)[0] for i in some]
+    check_rms(o[0, some], np.array(want))
 
 
 @pytest.mark.parametrize("fp8", [False, True])
