@@ -799,7 +799,12 @@ keys_combine_kernel(const float* part, int split, uint16_t* out, float* lse) {
 // sized without a device.  One query, us (undivided / as chosen): 600 entries 19.7 / 11.6, 2000
 // 44.2 / 13.8, 8000 149 / 17.3.
 constexpr int KA_FIXED = 6, KA_WAVES = 4;
-constexpr int KC_LATENT = 4;                          // queries whose join takes CTAs of many threads
+// Queries whose join takes CTAs of four slices: one slice / four, us a call over 600, 2000 and 8000 entries:
+// 1 query 13.2 / 12.1, 15.0 / 14.3, 21.5 / 18.0; 4 queries 13.8 / 12.1, 16.5 / 14.4, 25.9 / 18.0; 5 queries
+// 13.0 / 15.1, 17.5 / 17.3, 26.0 / 22.6; 8 queries 13.5 / 15.4, 17.7 / 17.5, 25.8 / 25.1; 12 queries
+// 14.0 / 18.0, 18.4 / 20.8, 27.7 / 30.3.  (Five to eight long caches would gain too; the weights of one
+// slice's CTA lie in shared memory for 608 / (KC_LATENT + 1) states.)
+constexpr int KC_LATENT = 4;
 
 int keys_split(int64_t BQ, int64_t chunks) {
   if (BQ <= 0) return 1;
@@ -857,10 +862,11 @@ static cudaError_t keys_launch(const KeysParams& p, int64_t BQ, const CUtensorMa
 // Calls that window_attention.cu takes: short windows, where its time is less.  In tenths of a us: this
 // file's kernel takes 70 and 1/10 a key for each wave of queries; the ring's 60, 3/10 a key for a CTA's
 // first window, and for its longest CTA 45 a tile (two queries) and 9/10 a key for each further sequence in
-// its run (of 410 calls measured both ways none loses more than 3 % by it).  Window 128, 4 sinks,
-// bf16, us (here / the ring's): 1 x 152 queries 8.7 / 15.4, 1 x 304 16.6 / 16.5, 1 x 608 34.2 / 19.6, 1 x 2432
-// 140 / 62, 100 x 4 23.9 / 31.9, 152 x 4 38.0 / 21.1, 60 x 5 16.5 / 31.5, 80 x 8 42.8 / 35.6, 608 x 1 44.3 / 80.0;
-// window 32: 1 x 153 13.4 / 11.4, 100 x 4 21.6 / 19.9.
+// its run (of 410 calls measured both ways none loses more than 2 % by it).  The SMs are KA_SMS here, for
+// the kernel's launch the device's: with another number the rule would still be right, but not the best.
+// Window 128, 4 sinks, bf16, us (here / the ring's): 1 x 153 queries 17.9 / 16.3, 1 x 304 19.4 / 17.3, 1 x 608
+// 39.8 / 21.6, 1 x 2432 164 / 66, 100 x 4 28.1 / 34.2, 152 x 4 43.3 / 21.7, 60 x 5 19.4 / 34.1, 80 x 8 49.1 / 38.6,
+// 608 x 1 48.8 / 85.8; window 32: 1 x 153 14.2 / 11.8, 100 x 4 22.7 / 20.6.
 static bool keys_in_ring(const KeysParams& p, int B, int64_t BQ) {
   if (p.main_kv || !window_ring_fits(p.W, p.n_sink) || BQ <= KA_SMS) return false;
   const int64_t keys = p.W + p.n_sink, pairs = (p.Q + 1) / 2, tiles = B * pairs, ctas = min(tiles, (int64_t)KA_SMS);

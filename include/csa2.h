@@ -389,7 +389,8 @@ csa2_status csa2_decode(const csa2_cache *cache, const csa2_decode_args *args, v
  *   with row pos of the table; binary32 until the one final rounding (a sum of
  *   squares past its range gives zeros; a row of zeros with eps = 0 is NaN).
  * Tokens with pos = -1 are padding: nothing of theirs is written.  Any other
- * position outside [0, rope_P) is skipped and raises CSA2_ERR_BOUNDS, and so
+ * position outside [0, rope_P) is skipped and raises CSA2_ERR_BOUNDS (the
+ * attention calls take every negative position as padding), and so
  * does a slot outside [0, n_rows) (-1 skips the row without an error).  The
  * slots of a call must be distinct (a row that two tokens name holds channels
  * of either).  q_out may be q itself (q_stride = 64 * 512); any other overlap
@@ -426,7 +427,8 @@ csa2_status csa2_qk_norm_rope(const csa2_qk_args *args, void *ws, size_t ws_byte
  * schedule of the pages begins with two such layers.  [dilfish §4.3]
  *   A query at raw position t sees the positions max(0, t-W+1) .. t of `rows`
  *   and the sinks at positions p < min(n_sink, max(0, t-W+1)); a query with
- *   t < 0 (padding) sees nothing: its output is zeros, its lse -inf.
+ *   t < 0 (padding, whichever negative number: nothing is reported) sees
+ *   nothing: its output is zeros, its lse -inf.
  *   lse (optional) = log sum exp(scale * q_h . v_i), natural logarithm.
  * A window position outside the supplied rows is skipped and raises
  * CSA2_ERR_BOUNDS.  Rows and sinks that a query does not see may hold anything,
@@ -471,7 +473,8 @@ csa2_status csa2_window_attn(const csa2_window_args *args, void *ws, size_t ws_b
  * enough not to need one and as what a selection is measured against.
  *   A query at raw position t >= 0 sees the entries j < min(n_entries[b],
  *   floor((t+1)/m)) and the window positions max(0, t-127) .. t; a query with
- *   t < 0 (padding) sees nothing: its output is zeros, its lse -inf.
+ *   t < 0 (padding, as in csa2_window_attn) sees nothing: its output is zeros,
+ *   its lse -inf.
  *   cache        main_kv, cap, n_entries (4-byte aligned) and m; idx_codes and
  *                idx_scales are not read and may be NULL.
  *   max_n        the most entries any query sees: it only sizes the split of a
