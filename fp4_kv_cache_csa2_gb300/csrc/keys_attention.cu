@@ -44,9 +44,9 @@
 // every barrier.
 //
 // Bound by the tensor cores, on which an M = 64 tile takes as long as one of M = 128 (two queries a
-// tile would need all of TMEM for O): 2048 cycles a chunk.  2048 queries over 8192 entries 1.91 ms,
-// 1.03 PFLOP/s, their pipe active in 86 % of the cycles; 16 queries over 131,072 entries 260 us, 1.0
-// PFLOP/s; 602 queries of 1000 E4M3 rows 114 us.  A CTA costs about 7 us beside its chunks: 16
+// tile would need all of TMEM for O): 2048 cycles a chunk, 3072 with two-part P.  2048 queries over 8192
+// entries 1.93 ms, 1.02 PFLOP/s, their pipe active in 86 % of the cycles; 16 queries over 131,072 entries
+// 262 us, 0.99 PFLOP/s; 602 queries of 1000 E4M3 rows 114 us.  A CTA costs about 7 us beside its chunks: 16
 // queries of 132 bf16 rows take 9.0 us.
 #include <cfloat>
 
@@ -82,8 +82,8 @@ constexpr float KA_LN2 = 0.6931471805599453f;
 // most 2^KA_MOST, f16's range less a little, before it moves.  Weights down to 2^-22 of the largest
 // keep f16's 11 bits, and what lies below loses 2^-33 of it at most: with a reference at the largest
 // score itself one key 17.3 above 131,072 others alike lost all of their 0.4 %.  The room between
-// the two (5.5 in logits) keeps rescalings rare: 2048 queries over 8192 entries take 1911 us, with
-// 2^0 at the top 1910, with 2^10 1933, with 2^11 1971.
+// the two (5.5 in logits) keeps rescalings rare: 2048 queries over 8192 entries took 1911 us, with
+// 2^0 at the top 1910, with 2^10 1933, with 2^11 1971 (and 15 more each with the check of q's range).
 constexpr float KA_TAU = 8.0f * KA_LOG2E;
 constexpr float KA_TOP = 8.0f, KA_MOST = 15.9f;
 constexpr int KA_SMS = 152;                               // GB300; CTAs a query is divided over at most

@@ -21,8 +21,8 @@
 // the softmax and the output of its neighbours.  Operands are bf16 (q and bf16 rows as they
 // are, E4M3 rows exactly, P as two bf16 of 8 bits, its rounding and what that left, with the
 // softmax's sum taken before either; the first alone makes the outputs' errors 1.3 times those
-// of their own rounding).  8192 queries of 128 rows and 4 sinks: 202 us, 5.4 TB/s of q, rows and
-// output (one part 183, the second product 15 of the difference: a tile's S waits for the P V
+// of their own rounding).  8192 queries of 128 rows and 4 sinks: 205 us, 5.3 TB/s of q, rows and
+// output (one part 183; the second product is most of the difference: a tile's S waits for the P V
 // of the tile before the last).
 //
 // A slot that a query does not see has weight zero for it, and zero times an infinity or a NaN
