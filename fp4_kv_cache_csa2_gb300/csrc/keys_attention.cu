@@ -13,9 +13,9 @@
 // Per chunk, with the 64 heads as the rows of M = 64 tiles:
 //   * S = Q K^T   N = keys, K = 512 in two halves of 256 dims (16 MMAs each)
 //   * softmax, two lanes a head, straight from TMEM; P = 2^(S scale log2 e - m) goes back
-//     to TMEM over S as the 16-bit A operand of the next product.  The reference m of a head,
-//     2^-8 of the largest score when it is set (f16), moves only when a chunk exceeds it by more
-//     than 2^15.9 (then the head's O and its sum are rescaled): P uses the whole of f16's range
+//     to TMEM over S as the 16-bit A operand of the next product.  The reference m of a head
+//     moves only when a chunk's scores exceed it by far (KA_TOP, KA_MOST, KA_TAU; then the head's
+//     O and its sum are rescaled), and P stays inside f16
 //   * O += P V    N = 2 x 256 dims, K = keys: V is the K tile read MN-major (twice with two-part P)
 // An M = 64 tile takes 16 lanes of each of TMEM's four lane quarters, so two of them
 // share columns: half h of the dims has its Q, its part of S and its O in lanes
@@ -27,7 +27,8 @@
 // value (at most 6 significant bits, 2^-10 .. 2688) and every E4M3 value exactly and
 // rounds q and bf16 window rows to f16, exact inside [2^-14, 65504], with P to 11
 // bits (fewer below 2^-22 of the largest weight, see KA_TOP); a head of q that reaches 2^16 is
-// scaled into f16's range by a power of two, so that q may be of any size, as with bf16 operands.  With bf16 rows alone the operands are bf16: q and rows as they are, P as two bf16
+// scaled into f16's range by a power of two, so that q may be of any size, as with bf16
+// operands.  With bf16 rows alone the operands are bf16: q and rows as they are, P as two bf16
 // of 8 bits, its rounding and what that left (a second product with the same V): with the
 // first alone the errors of the outputs are 1.3 times those of their own rounding, with both
 // 1.00; 16 queries of 132 rows take 9.0 us instead of 7.7.  The sum of the softmax is taken
@@ -77,8 +78,8 @@ constexpr uint32_t KA_HALF_LANES = 16u << 16;
 constexpr int KA_AHEAD = 5;                               // chunks of entries that are on their way to L2
 constexpr float KA_LOG2E = 1.4426950408889634f;
 constexpr float KA_LN2 = 0.6931471805599453f;
-// The reference of a head moves when a score (in powers of two) lies this far above it.  bf16: P
-// has binary32's range.  F16: P of the largest score is 2^KA_TOP when the reference is set, and at
+// The reference of a head moves when a score (in powers of two) lies KA_TAU (bf16, where P has
+// binary32's range) or KA_MOST (F16) above it.  F16: P of the largest score is 2^KA_TOP when the reference is set, and at
 // most 2^KA_MOST, f16's range less a little, before it moves.  Weights down to 2^-22 of the largest
 // keep f16's 11 bits, and what lies below loses 2^-33 of it at most: with a reference at the largest
 // score itself one key 17.3 above 131,072 others alike lost all of their 0.4 %.  The room between

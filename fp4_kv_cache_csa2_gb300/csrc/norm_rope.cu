@@ -18,8 +18,8 @@
 // 24..31 (four pairs a lane).
 // Rows a warp and CTAs an SM, us for 16 / 300 / 777 / 1500 / 3000 / 8192 tokens: 1 and 12
 // 2.0 / 7.6 / 18.0 / 32.1 / 61.5 / 164.7, 2 and 10 (48 registers, one of them spilled) 2.3 / 8.0 / 17.6 /
-// 30.6 / 58.2 / 155.2 (7.0 TB/s), 2 and 12 (40 registers, more spills) 157.8 at 8192, 4 rows 158.7.  Two rows keep more loads in
-// flight; one fills a short call's only waves better.
+// 30.6 / 58.2 / 155.2 (7.0 TB/s), 2 and 12 (40 registers, more spills) 157.8 at 8192, 4 rows 158.7.
+// Two rows keep more loads in flight; one fills a short call's only waves better.
 #include "host_once.cuh"
 #include "params.cuh"
 
