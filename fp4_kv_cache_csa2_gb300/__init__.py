@@ -75,6 +75,23 @@ class DenseArgs(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("swa_fp8", ctypes.c_int32)]
 
 
+class Cache8Struct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("cap", ctypes.c_int64),
+                ("n_entries", ctypes.c_void_p), ("m", ctypes.c_int32)]
+
+
+class Cache8WriteArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("entry_start", ctypes.c_void_p), ("n_new", ctypes.c_void_p)]
+
+
+class Cache8AttnArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Q", ctypes.c_int), ("S", ctypes.c_int), ("W", ctypes.c_int),
+                ("scale", ctypes.c_float), ("max_n", ctypes.c_int64), ("q_pos", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("swa", ctypes.c_void_p), ("swa_base_pos", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("swa_fp8", ctypes.c_int32)]
+
+
 _P, _I, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _SIGNATURES = {
     "csa2_layout_version": (ctypes.c_int, []),
@@ -107,6 +124,9 @@ _SIGNATURES = {
     "csa2_window_attn": (_I, [_P, _P, _SZ, _P]),
     "csa2_dense_attn_workspace_size": (_SZ, [_I, _I, _I64]),
     "csa2_dense_attn": (_I, [ctypes.POINTER(CacheStruct), _P, _P, _SZ, _P]),
+    "csa2_cache8_write": (_I, [_P, _P, _P, _SZ, _P]),
+    "csa2_cache8_attn_workspace_size": (_SZ, [_I, _I, _I64, _I]),
+    "csa2_cache8_attn": (_I, [_P, _P, _P, _SZ, _P]),
     "csa2_test_withhold_arrival": (_I, [_I]),
 }
 
@@ -177,6 +197,26 @@ class Cache:
         v.idx_codes = None if self.idx_codes is None else self.idx_codes[b:b + 1]
         v.idx_scales = None if self.idx_scales is None else self.idx_scales[b:b + 1]
         v.n_entries = self.n_entries[b:b + 1]
+        return v
+
+
+class Cache8:
+    """One source layer's cache in 8 bits (caller-owned tensors): int8 codes [B][cap][512] and one
+    float32 scale for each block of 8 entries, [B][cap / 8]."""
+
+    def __init__(self, B: int, cap: int, m: int, device="cuda"):
+        import torch
+        cap = -(-int(cap) // BLOCK) * BLOCK        # the library needs cap % 8 == 0
+        self.B, self.cap, self.m = B, cap, m
+        self.codes = torch.zeros((B, cap, D_LATENT), dtype=torch.int8, device=device)
+        self.scales = torch.zeros((B, cap // BLOCK), dtype=torch.float32, device=device)
+        self.n_entries = torch.zeros((B,), dtype=torch.int32, device=device)
+
+    def sequence(self, b: int) -> "Cache8":
+        """Sequence b as a batch-1 cache sharing this cache's memory."""
+        v = Cache8.__new__(Cache8)
+        v.B, v.cap, v.m = 1, self.cap, self.m
+        v.codes, v.scales, v.n_entries = self.codes[b:b + 1], self.scales[b:b + 1], self.n_entries[b:b + 1]
         return v
 
 
@@ -368,6 +408,7 @@ def _packer(cls):
 
 
 _pack_qk, _pack_window, _pack_dense = _packer(QkArgs), _packer(WindowArgs), _packer(DenseArgs)
+_pack_cache8, _pack_write8, _pack_attn8 = _packer(Cache8Struct), _packer(Cache8WriteArgs), _packer(Cache8AttnArgs)
 
 
 def _refuse(name: str, t, shape, what, index):
@@ -506,3 +547,62 @@ def dense_attn(cache: Cache, q, swa, swa_base_pos, q_pos, scale: float, out, ws:
                     0 if lse is None else _at("lse", lse, (B, Q, N_HEADS), f32, dev),
                     1 if swa.element_size() == 1 else 0)
     _call("csa2_dense_attn", dev, stream, ctypes.byref(cache.struct()), a, buf.data_ptr(), ws.nbytes)
+
+
+def _cache8(cache: Cache8, dev):
+    """The cache's tensors, checked, as the bytes of a csa2_cache8."""
+    B, cap = cache.B, cache.cap
+    if cap % BLOCK:
+        raise ValueError(f"cache.cap: {cap}; expected a multiple of {BLOCK}")
+    _, _, _, f32 = _types()
+    i8, i32 = _cache_types()
+    return _pack_cache8(_at("cache.codes", cache.codes, (B, cap, D_LATENT), i8, dev),
+                        _at("cache.scales", cache.scales, (B, cap // BLOCK), f32, dev), cap,
+                        _at("cache.n_entries", cache.n_entries, (B,), i32, dev), cache.m)
+
+
+def cache8_write(cache: Cache8, x, entry_start, ws: Workspace, *, n_new=None, stream=None):
+    """Finished latents x [B][T][512] (bf16; tokens may lie apart by one stride, as columns of a wider
+    matrix do) into entries entry_start[b] .. + n_new[b] - 1 (int32 [B], None: T).  n_entries stays."""
+    buf, (B, T, _) = ws.buf, _rank("x", x, ("B", "T", "512"))
+    dev = buf.get_device()
+    if B != cache.B:
+        raise ValueError(f"x: {B} sequences, the cache has {cache.B}")
+    bf16, _, i64, _ = _types()
+    stride = x.stride(1) if T > 1 else x.stride(0) if B > 1 else D_LATENT
+    if (x.shape[2] != D_LATENT or x.dtype not in bf16 or x.get_device() != dev or x.stride(2) != 1
+            or (B > 1 and x.stride(0) != T * stride)):
+        _refuse("x", x, (B, T, D_LATENT), f"{bf16}, one stride between tokens", dev)
+    c = _cache8(cache, dev)
+    a = _pack_write8(B, T, x.data_ptr(), stride, _at("entry_start", entry_start, (B,), i64, dev),
+                     0 if n_new is None else _at("n_new", n_new, (B,), _cache_types()[1], dev))
+    _call("csa2_cache8_write", dev, stream, c, a, buf.data_ptr(), ws.nbytes)
+
+
+def cache8_attn_workspace_size(B: int, Q: int, max_n: int, W: int = 0) -> int:
+    return load().csa2_cache8_attn_workspace_size(B, Q, max_n, W)
+
+
+def cache8_attn(cache: Cache8, q, q_pos, scale: float, out, ws: Workspace, *, max_n: int, W: int = 0, swa=None,
+                swa_base_pos=None, lse=None, stream=None):
+    """Queries [B][Q][64][512] over every visible entry of the 8-bit cache and, with W > 0, the window
+    rows swa [B][S][512] (bf16, or E4M3) of positions t-W+1 .. t.  max_n: the most entries a
+    query sees (it sizes the work split, nothing else).  lse: float32 [B][Q][64] or None."""
+    buf, (B, Q) = ws.buf, _rank("q_pos", q_pos, ("B", "Q"))
+    dev = buf.get_device()
+    if B != cache.B:
+        raise ValueError(f"q_pos: {B} sequences, the cache has {cache.B}")
+    bf16, row_types, i64, f32 = _types()
+    S = rows = base = fp8 = 0
+    if W:
+        S = _rank("swa", swa, ("B", "S", "512"))[1]
+        rows, fp8 = _at("swa", swa, (B, S, D_LATENT), row_types, dev), 1 if swa.element_size() == 1 else 0
+        base = _at("swa_base_pos", swa_base_pos, (B,), i64, dev)
+    elif swa is not None:
+        raise ValueError("swa: window rows, but W is 0")
+    shape = (B, Q, N_HEADS, D_LATENT)
+    c = _cache8(cache, dev)
+    a = _pack_attn8(B, Q, S, W, scale, max_n, _at("q_pos", q_pos, (B, Q), i64, dev), _at("q", q, shape, bf16, dev), rows,
+                    base, _at("out", out, shape, bf16, dev),
+                    0 if lse is None else _at("lse", lse, (B, Q, N_HEADS), f32, dev), fp8)
+    _call("csa2_cache8_attn", dev, stream, c, a, buf.data_ptr(), ws.nbytes)

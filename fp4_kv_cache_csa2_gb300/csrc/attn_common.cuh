@@ -58,6 +58,18 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   return d;
 }
 
+// Sixteen int8 -> eight f16x2 words (element 2i in the low half of word i), exactly: the byte
+// b + 128 in the low bits of f16 1024 is 1152 + b.
+__device__ __forceinline__ void i8x16_to_f16(const uint4& c, uint32_t* o) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const uint32_t u = w[i] ^ 0x80808080u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * i]) : "r"(prmt(u, 0x64646464u, 0x4140u)), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * i + 1]) : "r"(prmt(u, 0x64646464u, 0x4342u)), "r"(0x64806480u));
+  }
+}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));

@@ -19,6 +19,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned8(const void* p) { return ((uintptr_t)p & 7u) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 // [a, a + an) and [b, b + bn) share a byte
 bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
@@ -405,21 +406,24 @@ csa2_status csa2_qk_norm_rope(const csa2_qk_args* a, void* ws, size_t ws_bytes, 
 constexpr int64_t MAX_KEY_QUERIES = (int64_t)1 << 24;   // 64 rows each below 2^31 (tensor-map coordinates)
 
 static csa2_status check_keys_call(const KeysParams& p, int B, int Q, size_t need, void* ws, size_t ws_bytes) {
-  if (B < 0 || Q < 0 || p.S < 0 || p.n_sink < 0 || p.W < 1 || !std::isfinite(p.scale)) return CSA2_ERR_INVALID_ARG;
+  const bool rows = p.W > 0;                          // (an 8-bit cache may be attended without a window)
+  if (B < 0 || Q < 0 || p.S < 0 || p.n_sink < 0 || p.W < (p.scales8 ? 0 : 1) || !std::isfinite(p.scale))
+    return CSA2_ERR_INVALID_ARG;
   if (p.rows_fp8 != 0 && p.rows_fp8 != 1) return CSA2_ERR_INVALID_ARG;
   const int64_t BQ = (int64_t)B * Q, nr = B * p.S, nk = (int64_t)B * p.n_sink, lim = (int64_t)1 << 31;
   if (BQ > MAX_KEY_QUERIES || nr >= lim || nk >= lim) return CSA2_ERR_UNSUPPORTED;
   csa2_status st = check_ws(ws, ws_bytes, need);
   if (st != CSA2_OK || BQ == 0) return st;
-  if (!p.q || !p.q_pos || !p.base_pos || !p.out || (nr > 0 && !p.rows) || (nk > 0 && !p.sinks))
+  if (!p.q || !p.q_pos || (rows && !p.base_pos) || !p.out || (nr > 0 && !p.rows) || (nk > 0 && !p.sinks))
     return CSA2_ERR_INVALID_ARG;
   if (!aligned16(p.q) || !aligned16(p.rows) || !aligned16(p.sinks) || !aligned16(p.out) || !aligned8(p.q_pos) ||
       !aligned8(p.base_pos) || ((uintptr_t)p.lse & 3u) != 0)
     return CSA2_ERR_INVALID_ARG;
   const int64_t row = D * (p.rows_fp8 ? 1 : 2), out_n = BQ * H * D * 2, lse_n = p.lse ? BQ * H * 4 : 0;
-  const struct { const void* a; int64_t n; } in[] = {{p.q, out_n}, {p.q_pos, BQ * 8}, {p.base_pos, (int64_t)B * 8},
+  const struct { const void* a; int64_t n; } in[] = {{p.q, out_n}, {p.q_pos, BQ * 8}, {p.base_pos, rows ? (int64_t)B * 8 : 0},
       {p.rows, nr * row}, {p.sinks, nk * row}, {ws, (int64_t)need},
-      {p.main_kv, p.main_kv ? B * p.cap * MAIN_BYTES : 0}, {p.n_entries, p.n_entries ? (int64_t)B * 4 : 0}};
+      {p.main_kv, p.main_kv ? B * p.cap * (p.scales8 ? D : MAIN_BYTES) : 0},
+      {p.scales8, p.scales8 ? B * (p.cap / BLK) * 4 : 0}, {p.n_entries, p.n_entries ? (int64_t)B * 4 : 0}};
   for (const auto& x : in)
     if (overlap(x.a, x.n, p.out, out_n) || overlap(x.a, x.n, p.lse, lse_n)) return CSA2_ERR_INVALID_ARG;
   return overlap(p.out, out_n, p.lse, lse_n) ? CSA2_ERR_INVALID_ARG : CSA2_OK;
@@ -490,6 +494,87 @@ csa2_status csa2_dense_attn(const csa2_cache* cache, const csa2_dense_args* a, v
   if (st != CSA2_OK || a->B == 0 || a->Q == 0) return st;
   p.hdr = header(ws);
   return from_cuda(launch_keys_attention(p, a->B, dense_chunks(a->max_n), scratch(ws), (cudaStream_t)stream));
+}
+
+// ---------------------------------------------------------------- the 8-bit cache
+static csa2_status check_cache8(const csa2_cache8* c, int B) {
+  if (!c || !c->codes || !c->scales || !c->n_entries || B < 0) return CSA2_ERR_INVALID_ARG;
+  if (c->cap < 0 || c->cap % BLK != 0) return CSA2_ERR_INVALID_ARG;
+  if (!aligned16(c->codes) || !aligned4(c->scales) || !aligned4(c->n_entries)) return CSA2_ERR_INVALID_ARG;
+  if (c->m != 1 && c->m != 2) return CSA2_ERR_UNSUPPORTED;
+  const int64_t lim = (int64_t)1 << 31;
+  return c->cap < lim && B * c->cap < lim ? CSA2_OK : CSA2_ERR_UNSUPPORTED;
+}
+
+csa2_status csa2_cache8_write(const csa2_cache8* cache, const csa2_cache8_write_args* a, void* ws, size_t ws_bytes,
+                              void* stream) {
+  if (!a) return CSA2_ERR_INVALID_ARG;
+  csa2_status st = check_cache8(cache, a->B);
+  if (st != CSA2_OK) return st;
+  if ((st = check_q(a->B, a->T)) != CSA2_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, HDR)) != CSA2_OK || a->B == 0 || a->T == 0) return st;
+  if (!a->x || !aligned16(a->x) || !a->entry_start || !aligned8(a->entry_start) || !aligned4(a->n_new))
+    return CSA2_ERR_INVALID_ARG;
+  if (a->x_stride < D || a->x_stride > ((int64_t)1 << 32) || a->x_stride % 8 != 0) return CSA2_ERR_INVALID_ARG;
+  const int64_t n = (int64_t)a->B * cache->cap, scale_n = n / BLK * 4;
+  const struct { const void* a; int64_t n; } in[] = {
+      {a->x, (((int64_t)a->B * a->T - 1) * a->x_stride + D) * 2}, {a->entry_start, (int64_t)a->B * 8},
+      {a->n_new, a->n_new ? (int64_t)a->B * 4 : 0}, {cache->n_entries, (int64_t)a->B * 4}, {ws, (int64_t)HDR}};
+  for (const auto& x : in)
+    if (overlap(x.a, x.n, cache->codes, n * D) || overlap(x.a, x.n, cache->scales, scale_n)) return CSA2_ERR_INVALID_ARG;
+  if (overlap(cache->codes, n * D, cache->scales, scale_n)) return CSA2_ERR_INVALID_ARG;
+  C8WriteParams p{};
+  p.codes = reinterpret_cast<uint8_t*>(cache->codes);
+  p.scales = cache->scales;
+  p.cap = cache->cap;
+  p.n_entries = cache->n_entries;
+  p.x = a->x;
+  p.x_stride = a->x_stride;
+  p.B = a->B;
+  p.T = a->T;
+  p.start = a->entry_start;
+  p.n_new = a->n_new;
+  p.hdr = header(ws);
+  return from_cuda(launch_cache8_write(p, (cudaStream_t)stream));
+}
+
+static int64_t cache8_chunks(int64_t max_n, int W) {
+  return dense_chunks(max_n) - WIN / KEYS_CHUNK + ceil_div(W, KEYS_CHUNK);
+}
+
+size_t csa2_cache8_attn_workspace_size(int B, int Q, int64_t max_n, int W) {
+  if (B < 0 || Q < 0 || max_n < 0 || W < 0 || (int64_t)B * Q > MAX_KEY_QUERIES) return 0;
+  return HDR + align256(keys_part_bytes((int64_t)B * Q, cache8_chunks(max_n, W)));
+}
+
+csa2_status csa2_cache8_attn(const csa2_cache8* cache, const csa2_cache8_attn_args* a, void* ws, size_t ws_bytes,
+                             void* stream) {
+  if (!a || a->max_n < 0 || a->W < 0) return CSA2_ERR_INVALID_ARG;
+  csa2_status st = check_cache8(cache, a->B);
+  if (st != CSA2_OK) return st;
+  KeysParams p{};
+  p.q = a->q;
+  p.q_pos = a->q_pos;
+  p.Q = a->Q;
+  p.W = a->W;
+  if (a->W > 0) {
+    p.rows = static_cast<const uint8_t*>(a->swa);
+    p.base_pos = a->swa_base_pos;
+    p.S = a->S;
+    p.rows_fp8 = a->swa_fp8;
+  }
+  p.main_kv = reinterpret_cast<const uint8_t*>(cache->codes);
+  p.scales8 = cache->scales;
+  p.cap = cache->cap;
+  p.n_entries = cache->n_entries;
+  p.m = cache->m;
+  p.scale = a->scale;
+  p.out = a->out;
+  p.lse = a->lse;
+  st = check_keys_call(p, a->B, a->Q, csa2_cache8_attn_workspace_size(a->B, a->Q, a->max_n, a->W), ws, ws_bytes);
+  if (st != CSA2_OK || a->B == 0 || a->Q == 0) return st;
+  p.hdr = header(ws);
+  return from_cuda(launch_keys_attention(p, a->B, cache8_chunks(a->max_n, a->W), scratch(ws), (cudaStream_t)stream));
 }
 
 // HISA keeps up to 2048 of its summary rows: past 4096 blocks a row goes to

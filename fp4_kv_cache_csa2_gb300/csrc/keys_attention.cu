@@ -69,7 +69,8 @@ constexpr int KA_HALF = 4 * KA_COL;                       // half of a K buffer:
 constexpr int KA_BUFS = 3;                                // K buffers: chunk c in c % 3
 constexpr int KA_OFF_STAGE = KA_BUFS * 2 * KA_HALF;
 constexpr int KA_OFF_OUT = 0;                             // outputs: [32 rows][128 dims] bf16 an output warp, over the K buffers
-constexpr int KA_OFF_SMALL = KA_OFF_STAGE + KA_KEYS * MAIN_BYTES;
+template <bool E8> constexpr int KA_ENTRY = E8 ? D : MAIN_BYTES;          // bytes of an entry as stored
+template <bool E8> constexpr int KA_OFF_SMALL = KA_OFF_STAGE + KA_KEYS * KA_ENTRY<E8>;
 constexpr int KA_TMEM_COLS = 512;
 constexpr int KA_O_COL = 0;                               // half h of the dims: lanes 16h .. of each quarter
 constexpr int KA_Q_COL = 256;
@@ -87,6 +88,11 @@ constexpr float KA_LN2 = 0.6931471805599453f;
 // 2^0 at the top 1910, with 2^10 1933, with 2^11 1971 (and 15 more each with the check of q's range).
 constexpr float KA_TAU = 8.0f * KA_LOG2E;
 constexpr float KA_TOP = 8.0f, KA_MOST = 15.9f;
+// 8-bit entries: codes times a block's scale s.  The tensor cores see the codes; s enters the scores, and the
+// weights that go to the second product are P s, so the reference follows the scores plus log2 s.  The
+// sum of the softmax is of P without s, which is why s counts as KA_FLOOR8 at least there: P stays below
+// 2^(KA_MOST + 60), its sum inside binary32.
+constexpr float KA_FLOOR8 = 0x1p-60f;
 constexpr int KA_SMS = 152;                               // GB300; CTAs a query is divided over at most
 constexpr int KA_PART_FLOATS = 2 * H + H * D;             // one partial state: references, sums, O [dims / 4][head][4]
 
@@ -105,8 +111,8 @@ struct KaSmall {
   uint32_t tmem_base;
   int err;
 };
-constexpr int KA_SMEM = KA_OFF_SMALL + (int)sizeof(KaSmall);
-static_assert(KA_SMEM <= 227 * 1024, "shared memory per CTA");
+template <bool E8> constexpr int KA_SMEM = KA_OFF_SMALL<E8> + (int)sizeof(KaSmall);
+static_assert(KA_SMEM<true> <= 227 * 1024, "shared memory per CTA");
 
 __device__ __noinline__ bool ka_timeout(int* err, WsHeader* hdr, int where) {
   if (atomicExch(err, 1) == 0) report(hdr, CSA2_ERR_TIMEOUT, where);
@@ -176,13 +182,15 @@ __device__ __forceinline__ int ka_keys(const KaRun& q, int c) {
   return left < (uint32_t)KA_KEYS ? (int)left : KA_KEYS;
 }
 
-template <bool F16>
+template <bool F16, bool E8>
 __global__ void __launch_bounds__(KA_THREADS, 1)
 keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_rows,
                  const __grid_constant__ CUtensorMap map_sinks) {
+  static_assert(F16 || !E8, "8-bit entries are widened to f16");
+  constexpr int ENTRY = KA_ENTRY<E8>;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* stage = smem + KA_OFF_STAGE;
-  KaSmall& sm = *reinterpret_cast<KaSmall*>(smem + KA_OFF_SMALL);
+  KaSmall& sm = *reinterpret_cast<KaSmall*>(smem + KA_OFF_SMALL<E8>);
 
   if (tc::smem_u32(smem) & 1023u) {                   // the swizzled tiles need the declared alignment
     if (threadIdx.x == 0) report(p.hdr, CSA2_ERR_CUDA, 1);
@@ -226,11 +234,12 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   if (sm.tmem_base != 0 && tid == 0) report(p.hdr, CSA2_ERR_CUDA, 2);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  const int64_t base = p.base_pos[b];
+  const int64_t base = E8 && p.W == 0 ? 0 : p.base_pos[b];
   const KaRun q = ka_run(p, bq, b, base, sp, split);
   const int n_ch = q.n;
   if (sp == 0 && tid == 0 && q.t >= 0) {              // what the caller did not supply
-    if (q.lo < base) report(p.hdr, CSA2_ERR_BOUNDS, q.lo);
+    if (E8 && p.W == 0) {                             // no window
+    } else if (q.lo < base) report(p.hdr, CSA2_ERR_BOUNDS, q.lo);
     else if ((uint64_t)q.t - (uint64_t)base >= (uint64_t)p.S) report(p.hdr, CSA2_ERR_BOUNDS, q.t);
     if (p.main_kv && p.n_entries[b] > p.cap) report(p.hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
   }
@@ -310,17 +319,17 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       int kb = 0, use = 0;
       // entries ahead of the staging area into L2: a copy from there takes a third of the
       // time of one from memory, and there is room for one chunk only
-      const uint8_t* kv = p.main_kv + ((int64_t)b * p.cap + q.e0) * MAIN_BYTES;   // entry 0 of chunk 0
+      const uint8_t* kv = p.main_kv + ((int64_t)b * p.cap + q.e0) * ENTRY;   // entry 0 of chunk 0
       auto ahead = [&](int c) {
-        if (c >= q.cr && c < n_ch) tc::prefetch_l2(kv + (int64_t)c * (KA_KEYS * MAIN_BYTES), ka_keys(q, c) * MAIN_BYTES);
+        if (c >= q.cr && c < n_ch) tc::prefetch_l2(kv + (int64_t)c * (KA_KEYS * ENTRY), ka_keys(q, c) * ENTRY);
       };
       if (p.main_kv)
         for (int c = 1; c < KA_AHEAD; c++) ahead(c);
       for (int c = 0; c < n_ch; c++) {
         if (c >= q.cr) {                              // entries, contiguous
-          const uint32_t bytes = (uint32_t)(ka_keys(q, c) * MAIN_BYTES);
+          const uint32_t bytes = (uint32_t)(ka_keys(q, c) * ENTRY);
           next_stage(bytes);
-          tc::bulk_load(stage, kv + (int64_t)c * (KA_KEYS * MAIN_BYTES), bytes, &sm.stage_full);
+          tc::bulk_load(stage, kv + (int64_t)c * (KA_KEYS * ENTRY), bytes, &sm.stage_full);
           ahead(c + KA_AHEAD);
           continue;
         }
@@ -410,12 +419,23 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         ok = ok && ka_wait(&sm.q_moved, 0, sm, p.hdr, 47);
       }
       uint4 cd[4] = {}, sc[2] = {};                   // entries: codes of the four quarters, scales of the two halves
+      uint4 c8[E8 ? 4 : 1][2] = {};                   // 8-bit entries: codes of the four quarters
       if (F16 && entries) {
         // all at once (263 us for 16 queries over 131,072 entries; a half at a time, which holds
         // the staging area longer, 310)
         ok = ok && ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46);
-        if (key < keys) {                             // keys behind the last: zeros
-          const uint4* e = reinterpret_cast<const uint4*>(stage + key * MAIN_BYTES);
+        if (E8 && key < keys) {
+          // (a row is 512 bytes: the two keys of a phase take their two pieces in turn)
+          const uint4* e = reinterpret_cast<const uint4*>(stage + key * ENTRY) + 2 * j;
+          const int turn = k8 & 1;
+#pragma unroll
+          for (int i = 0; i < (E8 ? 4 : 0); i++) {
+            const uint4 a = e[8 * i + turn], o = e[8 * i + (turn ^ 1)];
+            c8[i][0] = turn ? o : a;
+            c8[i][1] = turn ? a : o;
+          }
+        } else if (!E8 && key < keys) {               // keys behind the last: zeros
+          const uint4* e = reinterpret_cast<const uint4*>(stage + key * ENTRY);
 #pragma unroll
           for (int i = 0; i < 4; i++) cd[i] = e[4 * i + j];
           sc[0] = e[16];
@@ -428,7 +448,13 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         unsigned char* kt = smem + (2 * kb + h) * KA_HALF;
         if (F16 && (entries || p.rows_fp8)) {
           uint32_t o[2][16];
-          if (entries) {
+          if (E8 && entries) {
+#pragma unroll
+            for (int i = 0; i < (E8 ? 2 : 0); i++) {
+              i8x16_to_f16(c8[2 * h + i][0], o[i]);
+              i8x16_to_f16(c8[2 * h + i][1], o[i] + 8);
+            }
+          } else if (!E8 && entries) {
             // scale bytes 2j, 2j + 1 of each quarter
             dequant(cd[2 * h], (odd ? sc[h].y : sc[h].x) >> (16 * (j & 1)), o[0]);
             dequant(cd[2 * h + 1], (odd ? sc[h].w : sc[h].z) >> (16 * (j & 1)), o[1]);
@@ -533,7 +559,25 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       if (lane == 0) tc::bar_arrive(&sm.q_moved);
     }
     int ob = 0, ou = 0;                               // K buffer and use of the chunk before
+    // 8-bit entries: the scales of this lane's four blocks of keys of chunk c (rows: 1)
+    auto scales = [&](int c, float* s) {
+      const int n = c < n_ch && c >= q.cr ? ka_keys(q, c) - 32 * half : 0;
+      const float* at = p.scales8 + (int64_t)b * (p.cap / BLK) + (q.e0 + (int64_t)KA_KEYS * c) / BLK + 4 * half;
+#pragma unroll
+      for (int i = 0; i < 4; i++) s[i] = BLK * i < n ? __ldcg(at + i) : 1.f;
+    };
+    float s8_next[4] = {1.f, 1.f, 1.f, 1.f};
+    if (E8) scales(0, s8_next);
     for (int c = 0; c < n_ch; c++) {
+      float s8[4] = {1.f, 1.f, 1.f, 1.f}, by[4];      // scales, and what turns products into scores
+      if (E8) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          s8[i] = s8_next[i];
+          by[i] = fmaxf(fminf(sc2 * s8[i], FLT_MAX), -FLT_MAX);   // finite: a product may be 0
+        }
+        scales(c + 1, s8_next);
+      }
       const int n = ka_keys(q, c) - 32 * half;   // this lane takes keys 32 half ..: n of them are there
       const uint32_t s_addr = quarter + KA_S_COL + 64 * (c & 1);
       ok = ok && ka_wait(&sm.s_full[c & 1], c >> 1, sm, p.hdr, 49);
@@ -551,7 +595,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         for (int x = 0; x < 32; x++) {
           const float got = __uint_as_float(__shfl_xor_sync(0xFFFFFFFFu, half ? s0[x] : s1[x], 16));
           // (not to be fused with the reference's subtraction: the largest score minus itself is 0)
-          v[x] = __fmul_rn(__uint_as_float(half ? s1[x] : s0[x]) + got, sc2);
+          v[x] = __fmul_rn(__uint_as_float(half ? s1[x] : s0[x]) + got, E8 ? by[x / BLK] : sc2);
         }
       }
       const bool whole = __all_sync(0xFFFFFFFFu, n >= 32);
@@ -561,7 +605,11 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       }
       float c4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int x = 0; x < 32; x++) c4[x & 3] = fmaxf(c4[x & 3], v[x]);
+      for (int x = 0; x < 32; x++) c4[E8 ? x / BLK : x & 3] = fmaxf(c4[E8 ? x / BLK : x & 3], v[x]);
+      if (E8) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) c4[i] += log2f(fmaxf(s8[i], KA_FLOOR8));
+      }
       float cm = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
       cm = fmaxf(cm, __shfl_xor_sync(0xFFFFFFFFu, cm, 16));
       float alpha = 1.f;
@@ -594,7 +642,9 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       for (int x = 0; x < 16; x++) {
         float e0 = ex2_ftz(v[2 * x] - ref), e1 = ex2_ftz(v[2 * x + 1] - ref);
         l4[x & 3] += e0 + e1;
-        pk[x] = F16 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+        pk[x] = E8    ? pack_f16x2(e0 * s8[2 * x / BLK], e1 * s8[2 * x / BLK])
+                : F16 ? pack_f16x2(e0, e1)
+                      : pack_bf16x2(e0, e1);
         if (!F16) rest[x] = bf16x2_rest(e0, e1, pk[x]);
       }
       l_sum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
@@ -826,25 +876,25 @@ size_t keys_part_bytes(int64_t BQ, int64_t chunks) {
   return s > 1 ? (size_t)(BQ * s) * KA_PART_FLOATS * sizeof(float) : 0;
 }
 
-template <bool F16>
+template <bool F16, bool E8>
 static cudaError_t keys_launch(const KeysParams& p, int64_t BQ, const CUtensorMap& mq, const CUtensorMap& mr,
                                const CUtensorMap& ms, cudaStream_t stream) {
   static PerDeviceOnce attrs;
   cudaError_t e = attrs.ensure([](int) {
-    return cudaFuncSetAttribute(keys_attn_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, KA_SMEM);
+    return cudaFuncSetAttribute(keys_attn_kernel<F16, E8>, cudaFuncAttributeMaxDynamicSharedMemorySize, KA_SMEM<E8>);
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(BQ * p.split));
   cfg.blockDim = dim3(KA_THREADS);
-  cfg.dynamicSmemBytes = KA_SMEM;
+  cfg.dynamicSmemBytes = KA_SMEM<E8>;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // set-up overlaps the previous kernel
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, keys_attn_kernel<F16>, p, mq, mr, ms);
+  e = cudaLaunchKernelEx(&cfg, keys_attn_kernel<F16, E8>, p, mq, mr, ms);
   if (e != cudaSuccess || p.split == 1) return e;
   cudaLaunchConfig_t cc = {};
   // Few queries: CTAs of many threads, one to an SM.  Else one slice; up to four states then
@@ -897,7 +947,9 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
   if (nr == 0) mr = mq;
   if (nk > 0 && !rows(&ms, p.sinks, nk)) return cudaErrorInvalidValue;
   if (nk == 0) ms = mr;
-  return p.main_kv || p.rows_fp8 ? keys_launch<true>(p, BQ, mq, mr, ms, stream) : keys_launch<false>(p, BQ, mq, mr, ms, stream);
+  if (p.scales8) return keys_launch<true, true>(p, BQ, mq, mr, ms, stream);
+  return p.main_kv || p.rows_fp8 ? keys_launch<true, false>(p, BQ, mq, mr, ms, stream)
+                                 : keys_launch<false, false>(p, BQ, mq, mr, ms, stream);
 }
 
 }  // namespace csa2

@@ -119,7 +119,8 @@ struct KeysParams {           // attention over every visible key
   int n_sink;
   int rows_fp8;
   int64_t W;                  // window
-  const uint8_t* main_kv;     // [B][cap][288], or null: no cache entries
+  const uint8_t* main_kv;     // [B][cap][288], with scales8 [B][cap][512]; or null: no cache entries
+  const float* scales8;       // 8-bit entries: [B][cap / 8]; null: 4-bit
   int64_t cap;
   const int32_t* n_entries;   // [B]
   int m;
@@ -128,6 +129,19 @@ struct KeysParams {           // attention over every visible key
   float* lse;                 // [BQ][64] or null
   int split;                  // CTAs per query (set by the launcher)
   float* part;                // split > 1: partial states
+  WsHeader* hdr;
+};
+
+struct C8WriteParams {        // entries of the 8-bit cache
+  uint8_t* codes;             // [B][cap][512]
+  float* scales;              // [B][cap / 8]
+  int64_t cap;
+  const int32_t* n_entries;
+  const uint16_t* x;          // token i of sequence b at (b * T + i) * x_stride
+  int64_t x_stride;
+  int B, T;
+  const int64_t* start;       // [B]
+  const int32_t* n_new;       // [B] or null
   WsHeader* hdr;
 };
 
@@ -162,6 +176,7 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
 cudaError_t launch_window_ring(const KeysParams& p, int B, cudaStream_t stream);
 bool window_ring_fits(int64_t W, int n_sink);
 size_t keys_part_bytes(int64_t BQ, int64_t chunks);
+cudaError_t launch_cache8_write(const C8WriteParams& p, cudaStream_t stream);
 cudaError_t launch_qk_norm_rope(const QkParams& p, cudaStream_t stream);
 
 }  // namespace csa2

@@ -508,6 +508,83 @@ csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_dense_args *args
                             void *stream);
 
 /*
+ * The 8-bit cache: the same latents as csa2_cache in 512.5 bytes an entry, for
+ * contexts whose attention the 4-bit entries disturb too much.
+ *   codes        [B][cap][512]: int8.
+ *   scales       [B][cap / 8]: one float for entries 8r .. 8r + 7 (of the one
+ *                latent that all heads share); entry j is codes[j] * scales[j / 8].
+ *   cap          entries per sequence, a multiple of 8.
+ *   n_entries    device [B]: entries valid per sequence (maintained by the caller).
+ *   m            compression ratio, 1 or 2: a query at position t sees the entries
+ *                j < min(n_entries[b], floor((t+1)/m)).
+ * codes 16-byte, scales and n_entries 4-byte aligned.  B * cap < 2^31 (more:
+ * CSA2_ERR_UNSUPPORTED).
+ */
+typedef struct {
+    int8_t *codes;
+    float *scales;
+    int64_t cap;
+    const int32_t *n_entries;
+    int32_t m;
+} csa2_cache8;
+
+/*
+ * Writes finished latents (normalised and rotated, as csa2_qk_norm_rope leaves its
+ * bf16 rows) into the 8-bit cache: entries entry_start[b] + i, i < n_new[b].
+ *   A block's scale is s = max(a / 127, 2^-60), a the largest magnitude written
+ *   into it, and codes are x / s, exactly rounded to nearest even.  A block that
+ *   keeps entries (those before entry_start[b], which count as written, and those
+ *   behind the call's that lie below n_entries[b]) keeps its scale too if that is
+ *   larger; otherwise the codes it keeps become code * old / new, rounded the same
+ *   way.  Infinities count as the largest finite bf16, NaN as 0.
+ * Entries outside [0, cap) are skipped and raise CSA2_ERR_BOUNDS, and so does an
+ * n_new[b] outside [0, T] (the nearest inside is taken).  Nothing else of the
+ * cache is written, n_entries neither.
+ * B * T <= 2^26.  x 16-byte, entry_start 8-byte, n_new 4-byte aligned; x_stride
+ * at least 512 and a multiple of 8.  The cache must not overlap the inputs (or
+ * n_entries).  Needs only the workspace header.
+ */
+typedef struct {
+    int B, T;                   /* sequences, most tokens of one                */
+    const uint16_t *x;          /* bf16, token i of sequence b at x + (b * T + i) * x_stride: [512] */
+    int64_t x_stride;           /* elements                                     */
+    const int64_t *entry_start; /* [B]                                          */
+    const int32_t *n_new;       /* [B], NULL: T                                 */
+} csa2_cache8_write_args;
+
+csa2_status csa2_cache8_write(const csa2_cache8 *cache, const csa2_cache8_write_args *args, void *ws,
+                              size_t ws_bytes, void *stream);
+
+/*
+ * Attention over every visible entry of the 8-bit cache and the W window rows
+ * max(0, t-W+1) .. t (W = 0: the entries alone): csa2_dense_attn on this cache,
+ * with its padding, outputs, reports, limits and operands (codes are exact in f16;
+ * the scales enter the scores and the weights in binary32, before the weights are
+ * rounded to 11 bits).  Scales of 2^-60 and more keep that precision (the write
+ * makes no others).  n_entries[b] > cap raises CSA2_ERR_BOUNDS (cap entries are
+ * attended).  Workspace: csa2_cache8_attn_workspace_size with the call's B, Q,
+ * max_n and W.
+ */
+typedef struct {
+    int B, Q;                   /* sequences, queries per sequence              */
+    int S;                      /* window rows supplied per sequence            */
+    int W;                      /* window, 0: none (swa, swa_base_pos unused)   */
+    float scale;                /* softmax scale                                */
+    int64_t max_n;              /* >= 0: only sizes the split of a query        */
+    const int64_t *q_pos;       /* [B][Q] raw positions                         */
+    const uint16_t *q;          /* bf16 [B][Q][64][512], rotated                */
+    const void *swa;            /* [B][S][512]                                  */
+    const int64_t *swa_base_pos;/* [B]                                          */
+    uint16_t *out;              /* bf16 [B][Q][64][512]                         */
+    float *lse;                 /* [B][Q][64] or NULL                           */
+    int32_t swa_fp8;            /* 0: swa is bf16; 1: E4M3                      */
+} csa2_cache8_attn_args;
+
+size_t csa2_cache8_attn_workspace_size(int B, int Q, int64_t max_n, int W);
+csa2_status csa2_cache8_attn(const csa2_cache8 *cache, const csa2_cache8_attn_args *args, void *ws,
+                             size_t ws_bytes, void *stream);
+
+/*
  * Test hook for the device-side timeout path; off unless a caller turns it on,
  * and never needed in production.  The pages have no counterpart.
  * While enabled (enable = 1) on the calling host thread, every index-scan
