@@ -327,9 +327,15 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         for (int c = 1; c < KA_AHEAD; c++) ahead(c);
       for (int c = 0; c < n_ch; c++) {
         if (c >= q.cr) {                              // entries, contiguous
-          const uint32_t bytes = (uint32_t)(ka_keys(q, c) * ENTRY);
+          const uint32_t bytes = (uint32_t)((E8 ? KA_KEYS : ka_keys(q, c)) * ENTRY);
           next_stage(bytes);
-          tc::bulk_load(stage, kv + (int64_t)c * (KA_KEYS * ENTRY), bytes, &sm.stage_full);
+          if (E8) {                                   // four column chunks of 128 dims, SW128
+            for (int i = 0; i < D / 128; i++)
+              tc::tma_load_2d(stage + i * (KA_KEYS * 128), &map_sinks, i * 128,
+                              (int32_t)((int64_t)b * p.cap + q.e0 + KA_KEYS * c), &sm.stage_full);
+          } else {
+            tc::bulk_load(stage, kv + (int64_t)c * (KA_KEYS * ENTRY), bytes, &sm.stage_full);
+          }
           ahead(c + KA_AHEAD);
           continue;
         }
@@ -419,22 +425,23 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         ok = ok && ka_wait(&sm.q_moved, 0, sm, p.hdr, 47);
       }
       uint4 cd[4] = {}, sc[2] = {};                   // entries: codes of the four quarters, scales of the two halves
-      uint4 c8[E8 ? 4 : 1][2] = {};                   // 8-bit entries: codes of the four quarters
+      // 8-bit entries: a lane takes 64 dims of each half of one key, so that eight lanes of a phase have
+      // eight rows and both swizzles spread them over the banks.  (Keys behind the last: whatever lies there;
+      // codes are finite and their weights 0.)
+      uint4 c8[E8 ? 8 : 1] = {};
+      const int k8l = 32 * ((ft >> 5) & 1) + lane, part8 = ft >> 6;
       if (F16 && entries) {
         // all at once (263 us for 16 queries over 131,072 entries; a half at a time, which holds
         // the staging area longer, 310)
         ok = ok && ka_wait(&sm.stage_full, staged++, sm, p.hdr, 46);
-        if (E8 && key < keys) {
-          // (a row is 512 bytes: the two keys of a phase take their two pieces in turn)
-          const uint4* e = reinterpret_cast<const uint4*>(stage + key * ENTRY) + 2 * j;
-          const int turn = k8 & 1;
+        if (E8) {
+          // dims 64 part8 .. of half h: units 4 (part8 % 2) .. of the 128-dim column chunk 2 h + part8 / 2
+          const unsigned char* e = stage + (part8 >> 1) * (KA_KEYS * 128);
 #pragma unroll
-          for (int i = 0; i < (E8 ? 4 : 0); i++) {
-            const uint4 a = e[8 * i + turn], o = e[8 * i + (turn ^ 1)];
-            c8[i][0] = turn ? o : a;
-            c8[i][1] = turn ? a : o;
-          }
-        } else if (!E8 && key < keys) {               // keys behind the last: zeros
+          for (int i = 0; i < (E8 ? 8 : 0); i++)
+            c8[i] = *reinterpret_cast<const uint4*>(e + (i >> 2) * (2 * KA_KEYS * 128) +
+                                                    sw128((uint32_t)k8l, 16u * (uint32_t)(4 * (part8 & 1) + (i & 3))));
+        } else if (key < keys) {                      // keys behind the last: zeros
           const uint4* e = reinterpret_cast<const uint4*>(stage + key * ENTRY);
 #pragma unroll
           for (int i = 0; i < 4; i++) cd[i] = e[4 * i + j];
@@ -446,15 +453,18 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         unsigned char* kt = smem + (2 * kb + h) * KA_HALF;
-        if (F16 && (entries || p.rows_fp8)) {
-          uint32_t o[2][16];
-          if (E8 && entries) {
+        if (E8 && entries) {
+          unsigned char* dst = kt + part8 * KA_COL;
 #pragma unroll
-            for (int i = 0; i < (E8 ? 2 : 0); i++) {
-              i8x16_to_f16(c8[2 * h + i][0], o[i]);
-              i8x16_to_f16(c8[2 * h + i][1], o[i] + 8);
-            }
-          } else if (!E8 && entries) {
+          for (int i = 0; i < (E8 ? 4 : 0); i++) {
+            uint32_t o[8];
+            i8x16_to_f16(c8[4 * h + i], o);
+            *reinterpret_cast<uint4*>(dst + sw128((uint32_t)k8l, 32u * i)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + sw128((uint32_t)k8l, 32u * i + 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        } else if (F16 && (entries || p.rows_fp8)) {
+          uint32_t o[2][16];
+          if (!E8 && entries) {
             // scale bytes 2j, 2j + 1 of each quarter
             dequant(cd[2 * h], (odd ? sc[h].y : sc[h].x) >> (16 * (j & 1)), o[0]);
             dequant(cd[2 * h + 1], (odd ? sc[h].w : sc[h].z) >> (16 * (j & 1)), o[1]);
@@ -947,7 +957,10 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
   if (nr == 0) mr = mq;
   if (nk > 0 && !rows(&ms, p.sinks, nk)) return cudaErrorInvalidValue;
   if (nk == 0) ms = mr;
-  if (p.scales8) return keys_launch<true, true>(p, BQ, mq, mr, ms, stream);
+  if (p.scales8) {                                    // no sinks: their map is the codes'
+    if (p.cap > 0 && !encode_u8_rows512_sw128(&ms, p.main_kv, (uint64_t)B * p.cap, KA_KEYS)) return cudaErrorInvalidValue;
+    return keys_launch<true, true>(p, BQ, mq, mr, ms, stream);
+  }
   return p.main_kv || p.rows_fp8 ? keys_launch<true, false>(p, BQ, mq, mr, ms, stream)
                                  : keys_launch<false, false>(p, BQ, mq, mr, ms, stream);
 }
