@@ -92,6 +92,18 @@ class Cache8AttnArgs(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("swa_fp8", ctypes.c_int32)]
 
 
+class WeightsArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Q", ctypes.c_int), ("scale", ctypes.c_float), ("decay", ctypes.c_float),
+                ("max_n", ctypes.c_int64), ("q_pos", ctypes.c_void_p), ("q", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("prev", ctypes.c_void_p), ("weights", ctypes.c_void_p)]
+
+
+class EvictArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("unit", ctypes.c_int32), ("budget", ctypes.c_int64), ("n_first", ctypes.c_int64),
+                ("n_recent", ctypes.c_int64), ("weights", ctypes.c_void_p), ("to_weights", ctypes.c_void_p),
+                ("kept", ctypes.c_void_p), ("n_out", ctypes.c_void_p)]
+
+
 _P, _I, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _SIGNATURES = {
     "csa2_layout_version": (ctypes.c_int, []),
@@ -127,6 +139,12 @@ _SIGNATURES = {
     "csa2_cache8_write": (_I, [_P, _P, _P, _SZ, _P]),
     "csa2_cache8_attn_workspace_size": (_SZ, [_I, _I, _I64, _I]),
     "csa2_cache8_attn": (_I, [_P, _P, _P, _SZ, _P]),
+    "csa2_attn_weights_workspace_size": (_SZ, [_I, _I, _I64]),
+    "csa2_attn_weights": (_I, [_P, _P, _P, _SZ, _P]),
+    "csa2_cache8_attn_weights": (_I, [_P, _P, _P, _SZ, _P]),
+    "csa2_evict_workspace_size": (_SZ, [_I, _I64, _I]),
+    "csa2_evict": (_I, [_P, _P, _P, _P, _SZ, _P]),
+    "csa2_cache8_evict": (_I, [_P, _P, _P, _P, _SZ, _P]),
     "csa2_test_withhold_arrival": (_I, [_I]),
 }
 
@@ -409,6 +427,7 @@ def _packer(cls):
 
 _pack_qk, _pack_window, _pack_dense = _packer(QkArgs), _packer(WindowArgs), _packer(DenseArgs)
 _pack_cache8, _pack_write8, _pack_attn8 = _packer(Cache8Struct), _packer(Cache8WriteArgs), _packer(Cache8AttnArgs)
+_pack_cache, _pack_weights, _pack_evict = _packer(CacheStruct), _packer(WeightsArgs), _packer(EvictArgs)
 
 
 def _refuse(name: str, t, shape, what, index):
@@ -606,3 +625,68 @@ def cache8_attn(cache: Cache8, q, q_pos, scale: float, out, ws: Workspace, *, ma
                     base, _at("out", out, shape, bf16, dev),
                     0 if lse is None else _at("lse", lse, (B, Q, N_HEADS), f32, dev), fp8)
     _call("csa2_cache8_attn", dev, stream, c, a, buf.data_ptr(), ws.nbytes)
+
+
+def _cache(cache: Cache, dev, index: bool):
+    """The cache's tensors, checked, as the bytes of a csa2_cache; index keys only when asked for and there."""
+    B, cap = cache.B, cache.cap
+    if cap % BLOCK:
+        raise ValueError(f"cache.cap: {cap}; expected a multiple of {BLOCK}")
+    u8, i32 = _cache_types()
+    codes = scales = 0
+    if index and cache.idx_codes is not None and cache.idx_scales is not None:
+        codes = _at("cache.idx_codes", cache.idx_codes, (B, cap, INDEX_CODE_BYTES), u8, dev)
+        scales = _at("cache.idx_scales", cache.idx_scales, (B, cap, INDEX_SCALE_BYTES), u8, dev)
+    return _pack_cache(_at("cache.main_kv", cache.main_kv, (B, cap, MAIN_ENTRY_BYTES), u8, dev), codes, scales, cap,
+                       _at("cache.n_entries", cache.n_entries, (B,), i32, dev), cache.m)
+
+
+def attn_weights_workspace_size(B: int, Q: int, max_n: int) -> int:
+    return load().csa2_attn_weights_workspace_size(B, Q, max_n)
+
+
+def attn_weights(cache: Cache | Cache8, q, q_pos, lse, scale: float, weights, ws: Workspace, *, max_n: int, prev=None,
+                 decay: float = 1.0, stream=None):
+    """weights[b][j] (float32 [B][cap]) = decay * prev[b][j] + the attention weights that the queries
+    [B][Q][64][512] give entry j of the 4-bit or 8-bit cache, lse [B][Q][64] from their attention.
+    prev None: nothing gathered so far; it may be weights itself.  max_n: no sequence has more entries."""
+    buf, (B, Q) = ws.buf, _rank("q_pos", q_pos, ("B", "Q"))
+    dev = buf.get_device()
+    if B != cache.B:
+        raise ValueError(f"q_pos: {B} sequences, the cache has {cache.B}")
+    bf16, _, i64, f32 = _types()
+    eight = isinstance(cache, Cache8)
+    c = _cache8(cache, dev) if eight else _cache(cache, dev, False)
+    shape = (B, cache.cap)
+    a = _pack_weights(B, Q, scale, decay, max_n, _at("q_pos", q_pos, (B, Q), i64, dev),
+                      _at("q", q, (B, Q, N_HEADS, D_LATENT), bf16, dev), _at("lse", lse, (B, Q, N_HEADS), f32, dev),
+                      0 if prev is None else _at("prev", prev, shape, f32, dev), _at("weights", weights, shape, f32, dev))
+    _call("csa2_cache8_attn_weights" if eight else "csa2_attn_weights", dev, stream, c, a, buf.data_ptr(), ws.nbytes)
+
+
+def evict_workspace_size(cache: Cache | Cache8, budget: int, unit: int) -> int:
+    return load().csa2_evict_workspace_size(cache.B, budget, unit)
+
+
+def evict(cache: Cache | Cache8, weights, kept, n_out, ws: Workspace, *, budget: int, unit: int = 1, first: int = 0,
+          recent: int = 0, to: Cache | Cache8 | None = None, to_weights=None, stream=None):
+    """Of every sequence the `budget` entries with the largest weights (float32 [B][cap]) stay, in units of 1 or 8
+    (8-bit cache: 8), with the first `first` and the last `recent` entries among them; they move to the
+    front of the cache, or to the front of `to`.  kept: int32 [B][budget / unit], the units that stay, -1 behind
+    them; n_out: int32 [B] entries that stay (it may be cache.n_entries).  to_weights: their weights, zeros behind
+    them; it may be `weights` when in place."""
+    dev = ws.buf.get_device()
+    _, i32 = _cache_types()
+    f32 = _types()[3]
+    eight = isinstance(cache, Cache8)
+    if to is not None and (type(to) is not type(cache) or to.B != cache.B):
+        raise ValueError(f"to: {type(to).__name__} of {to.B} sequences; expected {type(cache).__name__} of {cache.B}")
+    if unit not in (1, 8) or budget % unit:
+        raise ValueError(f"budget: {budget} in units of {unit}; expected a multiple of 1 or 8")
+    c = _cache8(cache, dev) if eight else _cache(cache, dev, True)
+    d = c if to is None else _cache8(to, dev) if eight else _cache(to, dev, True)
+    a = _pack_evict(cache.B, unit, budget, first, recent, _at("weights", weights, (cache.B, cache.cap), f32, dev),
+                    0 if to_weights is None else
+                    _at("to_weights", to_weights, (cache.B, (cache if to is None else to).cap), f32, dev),
+                    _at("kept", kept, (cache.B, budget // unit), i32, dev), _at("n_out", n_out, (cache.B,), i32, dev))
+    _call("csa2_cache8_evict" if eight else "csa2_evict", dev, stream, c, d, a, ws.buf.data_ptr(), ws.nbytes)

@@ -1,0 +1,476 @@
+// The attention weight that every cache entry gathers from a call's queries:
+//
+//   w_j = decay prev_j + sum over queries and heads that see j of exp(scale q_h . k_j - lse_h)
+//
+// on the 5th-generation tensor cores: S^T = K Q^T with 128 entries as the rows of an
+// M = 128 tile, so that a thread has all heads of one entry in its TMEM lane and the sum
+// over heads and queries stays in its registers: no exchange between lanes, no
+// atomics, the same result every time.
+//
+// A small kernel first writes the queries as f16 (a head that reaches 2^16 scaled into f16's
+// range by a power of two) and for each head its factor and its lse in powers of two.
+// The entries are exact in f16 (FP4 values; 8-bit codes, whose scale is the thread's
+// own factor), as in keys_attention.cu.  Sums: 64 weights in binary32, then compensated over a
+// CTA's queries.
+//
+// A CTA takes a run of tiles of one sequence and a run of query groups (one query, N = 64,
+// when there is only one; else two, N = 128).  The tile's entries lie in TMEM as the A operand
+// (256 columns of f16 pairs): with A in shared memory a product of N = 64 would take 48
+// cycles instead of 32, and the widened tile 128 KB.  Two S accumulators; the queries' dims come
+// through a ring of stages, or stay there when the CTA has one group.
+// Warps 0..7: exponentials and sums (warps 4..7: the second query, or the second half of the heads);
+// 8..15: entries to TMEM, a half of the dims each four; 16: MMAs; 17: copies of entries; 18: copies of
+// queries.  All waits are bounded; a timeout reports CSA2_ERR_TIMEOUT.
+#include <cfloat>
+
+#include "attn_common.cuh"
+#include "params.cuh"
+
+namespace csa2 {
+
+constexpr int AW_KEYS = 128;                              // entries of a tile
+constexpr int AW_SUM_WARPS = 8, AW_FILL_WARPS = 8;
+constexpr int AW_MMA_WARP = AW_SUM_WARPS + AW_FILL_WARPS, AW_KEY_WARP = AW_MMA_WARP + 1, AW_Q_WARP = AW_KEY_WARP + 1;
+constexpr int AW_THREADS = 32 * (AW_Q_WARP + 1);
+constexpr int AW_STAGES = 8;                              // of 64 dims of a group
+constexpr int AW_GROUPS = 512;                            // query groups of a CTA at most
+constexpr float AW_LOG2E = 1.4426950408889634f;
+constexpr int AW_SMS = 152;
+
+// NQ: queries of a group.  A buffers hold half of the dims of a tile.
+template <bool E8, int NQ>
+struct Aw {
+  static constexpr int N = 64 * NQ;
+  static constexpr int ENTRY = E8 ? D : MAIN_BYTES;
+  static constexpr int TILE = AW_KEYS * ENTRY;            // bytes of a tile as stored
+  static constexpr int TILES = NQ == 1 ? (E8 ? 2 : 4) : (E8 ? 1 : 2);   // staged tiles
+  static constexpr int A_BUFS = NQ == 1 ? 3 : 2;          // of 128 columns
+  static constexpr int S_COL = 128 * A_BUFS;
+  static constexpr int STAGE = N * 128;                   // [N heads][64 dims] f16, SW128
+  static constexpr int OFF_TILE = AW_STAGES * STAGE;
+  static constexpr int OFF_SMALL = OFF_TILE + TILES * TILE;
+  struct Small {
+    float2 col[2][N];                 // a head's factor, minus its lse, in powers of two
+    float joined[2][AW_KEYS];         // the second half's sums
+    int vis[AW_GROUPS * NQ];          // entries each query sees
+    uint64_t tile_full[TILES], tile_free[TILES];    // TMA; a fill warp each
+    uint64_t a_full[A_BUFS], a_free[A_BUFS];        // four fill warps; MMAs
+    uint64_t q_full[AW_STAGES], q_free[AW_STAGES];  // TMA; MMAs
+    uint64_t s_full[2], s_free[2], col_full[2];     // MMAs; a sum warp each; TMA
+    uint32_t tmem_base;
+    int most, err;
+  };
+  static constexpr int SMEM = OFF_SMALL + (int)sizeof(Small);
+  static_assert(SMEM <= 227 * 1024 && S_COL + 2 * N <= 512 && TILE % 1024 == 0, "");
+};
+
+__device__ __noinline__ bool aw_timeout(int* err, WsHeader* hdr, int where) {
+  if (atomicExch(err, 1) == 0) report(hdr, CSA2_ERR_TIMEOUT, where);
+  return false;
+}
+
+// entries of sequence b that the call deals with
+__device__ __forceinline__ int aw_entries(const AwParams& p, int b) {
+  return (int)max((int64_t)0, min((int64_t)p.n_entries[b], min(p.cap, p.max_n)));
+}
+
+// A warp a head: q as f16, the head's factor and its lse in powers of two.
+__global__ void __launch_bounds__(256) attn_weights_query_kernel(AwParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), bq = row / H;
+  const uint4* in = reinterpret_cast<const uint4*>(p.q + row * D);
+  uint4* out = reinterpret_cast<uint4*>(p.q16 + row * D);
+  const float lse = p.lse[row];
+  if (p.q_pos[bq] < 0 || lse == -INFINITY) {          // sees nothing: weights of 0, whatever q holds
+    out[lane] = out[32 + lane] = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0) p.col[row] = make_float2(0.f, -INFINITY);
+    return;
+  }
+  const uint4 v[2] = {__ldcs(in + lane), __ldcs(in + 32 + lane)};
+  const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+  uint32_t most = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; i++) most = __vmaxu2(most, w[i] & 0x7FFF7FFFu);
+  most = __reduce_max_sync(0xFFFFFFFFu, max(most & 0xFFFFu, most >> 16));
+  // |q| of 2^16 or more (bf16 bits 143 << 7): the largest goes to [2^15, 2^16)
+  const int e = max(min((int)(most >> 7), 254) - 142, 0);
+  const float down = __int_as_float((127 - e) << 23);
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    o[i] = pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
+  out[lane] = make_uint4(o[0], o[1], o[2], o[3]);
+  out[32 + lane] = make_uint4(o[4], o[5], o[6], o[7]);
+  if (lane == 0) {
+    const float by = p.scale * AW_LOG2E * __int_as_float((127 + e) << 23);
+    p.col[row] = make_float2(fmaxf(fminf(by, FLT_MAX), -FLT_MAX), -lse * AW_LOG2E);   // finite: a product may be 0
+  }
+}
+
+template <bool E8, int NQ>
+__global__ void __launch_bounds__(AW_THREADS, 1)
+attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_codes) {
+  using C = Aw<E8, NQ>;
+  using Small = typename C::Small;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Small& sm = *reinterpret_cast<Small*>(smem + C::OFF_SMALL);
+  WsHeader* hdr = p.hdr;
+  if (tc::smem_u32(smem) & 1023u) {                   // the swizzled tiles need the declared alignment
+    if (threadIdx.x == 0) report(hdr, CSA2_ERR_CUDA, 3);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  // block = (query split, sequence, run of tiles)
+  const int run = (int)(blockIdx.x % (uint32_t)p.runs), sb = (int)(blockIdx.x / (uint32_t)p.runs);
+  const int b = sb % p.B, qs = sb / p.B;
+
+  if (warp == AW_MMA_WARP) tc::tmem_alloc(&sm.tmem_base, 512);
+  if (tid == 0) {
+    for (int i = 0; i < C::TILES; i++) {
+      tc::bar_init(&sm.tile_full[i], 1);
+      tc::bar_init(&sm.tile_free[i], AW_FILL_WARPS);
+    }
+    for (int i = 0; i < C::A_BUFS; i++) {
+      tc::bar_init(&sm.a_full[i], AW_FILL_WARPS / 2);
+      tc::bar_init(&sm.a_free[i], 1);
+    }
+    for (int i = 0; i < AW_STAGES; i++) {
+      tc::bar_init(&sm.q_full[i], 1);
+      tc::bar_init(&sm.q_free[i], 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      tc::bar_init(&sm.s_full[i], 1);
+      tc::bar_init(&sm.s_free[i], AW_SUM_WARPS);
+      tc::bar_init(&sm.col_full[i], 1);
+    }
+    sm.most = 0;
+    sm.err = 0;
+    tc::bar_init_fence();
+    tc::prefetch_tensormap(&map_q);
+    if (E8) tc::prefetch_tensormap(&map_codes);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (sm.tmem_base != 0 && tid == 0) report(hdr, CSA2_ERR_CUDA, 4);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  const int n = aw_entries(p, b);
+  if (run == 0 && qs == 0 && tid == 0 && p.n_entries[b] > min(p.cap, p.max_n))
+    report(hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
+  const int tiles = (n + AW_KEYS - 1) / AW_KEYS;
+  const int t_lo = (int)((int64_t)tiles * run / p.runs), t_n = (int)((int64_t)tiles * (run + 1) / p.runs) - t_lo;
+  const int groups = (p.Q + NQ - 1) / NQ;
+  const int g_lo = (int)((int64_t)groups * qs / p.splits), ng = (int)((int64_t)groups * (qs + 1) / p.splits) - g_lo;
+  // what the run's queries see (AW_GROUPS groups at most); those behind the last query: nothing
+  int most = 0;
+  for (int i = tid; i < ng * NQ; i += AW_THREADS) {
+    const int qi = g_lo * NQ + i;
+    int v = 0;
+    if (qi < p.Q) {
+      const int64_t t = p.q_pos[(int64_t)b * p.Q + qi];
+      if (t >= 0) v = (int)visible_entries(min(t, INT64_MAX - 1), p.m, n);
+    }
+    sm.vis[i] = v;
+    most = max(most, v);
+  }
+  if (most > 0) atomicMax(&sm.most, most);
+  __syncthreads();
+  // the tiles that some query sees come first
+  const int live = min(max((sm.most + AW_KEYS - 1) / AW_KEYS - t_lo, 0), t_n);
+  const bool resident = ng == 1;                      // the one group's dims stay in their stages
+  auto next_group = [&](int g, int tile) {            // the first group from g on that sees the tile
+    while (g < ng && max(sm.vis[NQ * g], sm.vis[NQ * g + NQ - 1]) <= tile * AW_KEYS) g++;
+    return g;
+  };
+  bool ok = true;                                     // a thread that has given up once waits no more
+  auto wait = [&](uint64_t* bar, uint32_t use, int where) {
+    if (ok) ok = tc::bar_wait(bar, use & 1u) || aw_timeout(&sm.err, hdr, where);
+  };
+
+  if (warp == AW_MMA_WARP) {
+    // ================= MMAs (the whole warp runs the loop, one lane issues)
+    constexpr uint32_t idesc = tc::idesc_f16(AW_KEYS, C::N, 0, 0);
+    const uint64_t q_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
+    const uint32_t leader = tc::elect_one();
+    uint32_t u = 0, st = 0, st_use = 0;               // group of the CTA, query stage and its use
+    for (int t = 0; t < live; t++) {
+      int g = next_group(0, t_lo + t);
+      bool first = true;
+      while (g < ng) {
+        const int after = next_group(g + 1, t_lo + t);
+        if (u >= 2) wait(&sm.s_free[u & 1], (u >> 1) - 1, 60);
+        for (int h = 0; h < 2; h++) {
+          const uint32_t k = 2 * t + h, ab = k % C::A_BUFS;
+          if (first) wait(&sm.a_full[ab], k / C::A_BUFS, 61);
+#pragma unroll 1
+          for (int i = 0; i < 4; i++) {
+            if (!resident || u == 0) wait(&sm.q_full[st], st_use, 62);
+            tc::fence_after_sync();
+            const uint64_t qa = q_d + (uint32_t)(st * C::STAGE >> 4);
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+              tc::mma_f16_ts_warp(leader, C::S_COL + C::N * (u & 1), 128 * ab + 32 * i + 8 * x, qa + 2 * x, idesc,
+                                  (h || i || x) ? 1u : 0u);
+            if (!resident) tc::commit_warp(leader, &sm.q_free[st]);
+            if (++st == AW_STAGES) st = 0, st_use++;
+          }
+          if (after >= ng) tc::commit_warp(leader, &sm.a_free[ab]);
+        }
+        tc::commit_warp(leader, &sm.s_full[u & 1]);
+        u++;
+        g = after;
+        first = false;
+      }
+    }
+  } else if (warp == AW_KEY_WARP) {
+    // ================= copies of entries
+    if (lane == 0) {
+      for (int t = 0; t < live; t++) {
+        const uint32_t ts = t % C::TILES, use = t / C::TILES;
+        const int64_t first = (int64_t)(t_lo + t) * AW_KEYS;
+        unsigned char* dst = smem + C::OFF_TILE + ts * C::TILE;
+        if (use > 0) wait(&sm.tile_free[ts], use - 1, 63);
+        if (E8) {                                     // four column chunks of 128 dims, SW128
+          tc::bar_arrive_expect_tx(&sm.tile_full[ts], C::TILE);
+          for (int i = 0; i < D / 128; i++)
+            tc::tma_load_2d(dst + i * (AW_KEYS * 128), &map_codes, i * 128, (int32_t)(b * p.cap + first), &sm.tile_full[ts]);
+        } else {
+          const uint32_t bytes = (uint32_t)min((int64_t)AW_KEYS, p.cap - first) * MAIN_BYTES;
+          tc::bar_arrive_expect_tx(&sm.tile_full[ts], bytes);
+          tc::bulk_load(dst, p.kv + (b * p.cap + first) * MAIN_BYTES, bytes, &sm.tile_full[ts]);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == AW_Q_WARP) {
+    // ================= copies of queries
+    if (lane == 0) {
+      uint32_t u = 0, st = 0, st_use = 0;
+      for (int t = 0; t < (resident ? min(live, 1) : live); t++) {
+        for (int g = next_group(0, t_lo + t); g < ng; g = next_group(g + 1, t_lo + t)) {
+          const int64_t row = ((int64_t)b * p.Q + (int64_t)(g_lo + g) * NQ) * H;
+          if (u >= 2) wait(&sm.s_free[u & 1], (u >> 1) - 1, 64);
+          tc::bar_arrive_expect_tx(&sm.col_full[u & 1], C::N * (uint32_t)sizeof(float2));
+          tc::bulk_load(sm.col[u & 1], p.col + row, C::N * (uint32_t)sizeof(float2), &sm.col_full[u & 1]);
+          for (int i = 0; i < AW_STAGES; i++) {
+            if (st_use > 0) wait(&sm.q_free[st], st_use - 1, 65);
+            tc::bar_arrive_expect_tx(&sm.q_full[st], C::STAGE);
+            tc::tma_load_2d(smem + st * C::STAGE, &map_q, i * 64, (int32_t)row, &sm.q_full[st]);
+            if (++st == AW_STAGES) st = 0, st_use++;
+          }
+          u++;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= AW_SUM_WARPS) {
+    // ================= entries to TMEM: lane = entry, four warps a half of the dims
+    const int h = (warp - AW_SUM_WARPS) >> 2, row = 32 * (warp & 3) + lane;
+    const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
+    for (int t = 0; t < live; t++) {
+      const uint32_t k = 2 * t + h, ab = k % C::A_BUFS, use = k / C::A_BUFS, ts = t % C::TILES;
+      const unsigned char* tile = smem + C::OFF_TILE + ts * C::TILE;
+      wait(&sm.tile_full[ts], t / C::TILES, 66);
+      if (use > 0) wait(&sm.a_free[ab], use - 1, 67);
+      tc::fence_after_sync();
+      uint4 sc = make_uint4(0u, 0u, 0u, 0u);
+      if (!E8) sc = *reinterpret_cast<const uint4*>(tile + row * MAIN_BYTES + 256 + 16 * h);
+      const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+      for (int i = 0; i < 4; i++) {                   // 64 dims: 32 columns
+        uint32_t o[32];
+        if (E8) {
+#pragma unroll
+          for (int x = 0; x < 4; x++)
+            i8x16_to_f16(*reinterpret_cast<const uint4*>(tile + (2 * h + (i >> 1)) * (AW_KEYS * 128) +
+                                                         sw128((uint32_t)row, 16u * (4 * (i & 1) + x))),
+                         o + 8 * x);
+        } else {
+          // rows are 18 units of 16 bytes: of the eight lanes of a phase four take their two units in the
+          // other order, so that they lie in eight bank groups
+          const uint4* src = reinterpret_cast<const uint4*>(tile + row * MAIN_BYTES + 128 * h + 32 * i);
+          const int turn = lane >> 2 & 1;
+          const uint4 a = src[turn], c = src[turn ^ 1];
+          const uint32_t w[8] = {turn ? c.x : a.x, turn ? c.y : a.y, turn ? c.z : a.z, turn ? c.w : a.w,
+                                 turn ? a.x : c.x, turn ? a.y : c.y, turn ? a.z : c.z, turn ? a.w : c.w};
+#pragma unroll
+          for (int x = 0; x < 8; x++) {
+            e2m1x8_to_f16(w[x], o + 4 * x);
+            const uint32_t s2 = e4m3x2_to_f16x2(prmt(scw[i], 0u, 0x1111u * (x >> 1)));
+#pragma unroll
+            for (int y = 0; y < 4; y++) o[4 * x + y] = hmul2(o[4 * x + y], s2);
+          }
+        }
+        tmem_st32(quarter + 128 * ab + 32 * i, o);
+      }
+      tc::fence_proxy_async_smem();                   // reads done before a copy writes there again
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        tc::bar_arrive(&sm.tile_free[ts]);
+        tc::bar_arrive(&sm.a_full[ab]);
+      }
+    }
+  } else {
+    // ================= weights: lane = entry, warps 4..7 the second half of the columns
+    const int half = warp >> 2, row = 32 * (warp & 3) + lane;
+    constexpr int COLS = C::N / 2;
+    const uint32_t addr = ((uint32_t)(32 * (warp & 3)) << 16) + C::S_COL + COLS * half;
+    uint32_t u = 0;
+    for (int t = 0; t < t_n; t++) {
+      const int tile = t_lo + t, j = tile * AW_KEYS + row;
+      float acc = 0.f, lost = 0.f;                    // compensated over the queries
+      if (t < live) {
+        float s8 = 1.f;
+        if (E8) s8 = j < n ? __ldcg(p.scales8 + (int64_t)b * (p.cap / BLK) + j / BLK) : 0.f;
+        for (int g = next_group(0, tile); g < ng; g = next_group(g + 1, tile)) {
+          const uint32_t i = u & 1;
+          const float4* col = reinterpret_cast<const float4*>(sm.col[resident ? 0 : i] + COLS * half);
+          if (resident) {
+            if (u == 0) wait(&sm.col_full[0], 0, 68);
+          } else {
+            wait(&sm.col_full[i], u >> 1, 68);
+          }
+          wait(&sm.s_full[i], u >> 1, 69);
+          tc::fence_after_sync();
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < COLS; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(addr + C::N * i + c, r);
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              const float4 f = col[(c + x) / 2];
+              const float v0 = __uint_as_float(r[x]), v1 = __uint_as_float(r[x + 1]);
+              s4[x & 2] += ex2_ftz(fmaf(E8 ? v0 * s8 : v0, f.x, f.y));
+              s4[(x & 2) + 1] += ex2_ftz(fmaf(E8 ? v1 * s8 : v1, f.z, f.w));
+            }
+          }
+          tc::fence_before_sync();
+          tc::fence_proxy_async_smem();               // reads of the factors done before a copy writes there again
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&sm.s_free[i]);
+          if (j < sm.vis[NQ == 1 ? g : 2 * g + half]) {
+            const float y = (s4[0] + s4[1]) + (s4[2] + s4[3]) - lost, z = acc + y;
+            lost = (z - acc) - y;
+            acc = z;
+          }
+          u++;
+        }
+      }
+      if (half == 1) sm.joined[t & 1][row] = acc;
+      named_sync(1, 32 * AW_SUM_WARPS);
+      if (half == 0 && j < n) {
+        acc += sm.joined[t & 1][row];
+        if (p.splits > 1) {
+          p.part[((int64_t)qs * p.B + b) * p.pitch + j] = acc;
+        } else {
+          const int64_t at = (int64_t)b * p.cap + j;
+          p.out[at] = p.prev ? fmaf(p.decay, p.prev[at], acc) : acc;
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  // after a timeout copies may be in flight that nobody waited for: time for them to land
+  if (*(volatile int*)&sm.err != 0)
+    for (int i = 0; i < 1000; i++) __nanosleep(1000);
+  if (warp == AW_MMA_WARP) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(0u, 512);
+  }
+}
+
+// The query splits' sums of an entry, in order, and what it had.
+__global__ void __launch_bounds__(256) attn_weights_join_kernel(AwParams p, int blocks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = (int)(blockIdx.x / (uint32_t)blocks), n = aw_entries(p, b);
+  const int64_t j = (int64_t)(blockIdx.x % (uint32_t)blocks) * 256 + threadIdx.x;
+  if (p.Q == 0 && j == 0 && p.n_entries[b] > min(p.cap, p.max_n)) report(p.hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
+  if (j >= n) return;
+  float acc = 0.f;
+  for (int s = 0; s < p.splits; s++) acc += __ldcg(p.part + ((int64_t)s * p.B + b) * p.pitch + j);
+  const int64_t at = (int64_t)b * p.cap + j;
+  p.out[at] = p.prev ? fmaf(p.decay, p.prev[at], acc) : acc;
+}
+
+// ------------------------------------------------------------------ host side
+// Runs of tiles of a sequence and splits of its queries: the least time on 152 SMs with one CTA each.  In
+// tenths of a us: a CTA costs 50, a tile 8 with one query, else 10 and 11 a group; the join of splits 30.
+AwPlan attn_weights_plan(int B, int Q, int64_t max_n) {
+  AwPlan best{1, 1};
+  const int64_t tiles = ceil_div(max_n, AW_KEYS), groups = Q == 1 ? 1 : ceil_div(Q, 2);
+  if (B <= 0 || Q <= 0 || tiles == 0) return best;
+  int64_t best_cost = INT64_MAX;
+  const int64_t least = ceil_div(groups, AW_GROUPS);
+  for (int64_t s = least; s <= groups && s < least + 32; s++) {
+    for (int waves = 1; waves <= 4; waves++) {
+      int64_t runs = (int64_t)AW_SMS * waves / (B * s);
+      runs = runs < 1 ? 1 : runs > tiles ? tiles : runs;
+      const int64_t per = ceil_div(tiles, runs) * (Q == 1 ? 8 : 10 + 11 * ceil_div(groups, s));
+      const int64_t cost = ceil_div(B * s * runs, AW_SMS) * (50 + per) + (s > 1 ? 30 : 0);
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {(int)runs, (int)s};
+      }
+    }
+  }
+  return best;
+}
+
+int64_t attn_weights_pitch(int64_t max_n) { return ceil_div(max_n, AW_KEYS) * AW_KEYS; }
+
+template <bool E8, int NQ>
+static cudaError_t aw_launch(const AwParams& p, const CUtensorMap& mq, const CUtensorMap& mc, cudaLaunchConfig_t cfg) {
+  using C = Aw<E8, NQ>;
+  static PerDeviceOnce attrs;
+  cudaError_t e = attrs.ensure([](int) {
+    return cudaFuncSetAttribute(attn_weights_kernel<E8, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.runs * p.splits));
+  cfg.blockDim = dim3(AW_THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  return cudaLaunchKernelEx(&cfg, attn_weights_kernel<E8, NQ>, p, mq, mc);
+}
+
+cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream) {
+  if (p.B == 0 || p.max_n == 0) return cudaSuccess;
+  const AwPlan plan = attn_weights_plan(p.B, p.Q, p.max_n);
+  p.runs = plan.runs;
+  p.splits = p.Q ? plan.splits : 0;
+  p.pitch = attn_weights_pitch(p.max_n);
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaSuccess;
+  if (p.Q > 0) {
+    const int64_t rows = (int64_t)p.B * p.Q * H;
+    CUtensorMap mq, mc;
+    if (!encode_bf16_rows512(&mq, p.q16, (uint64_t)rows, p.Q == 1 ? 64 : 128)) return cudaErrorInvalidValue;
+    if (!p.scales8) mc = mq;
+    else if (!encode_u8_rows512_sw128(&mc, p.kv, (uint64_t)p.B * p.cap, AW_KEYS)) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3((unsigned)(rows / 8));
+    cfg.blockDim = dim3(256);
+    e = cudaLaunchKernelEx(&cfg, attn_weights_query_kernel, p);
+    if (e != cudaSuccess) return e;
+    if (p.scales8) e = p.Q == 1 ? aw_launch<true, 1>(p, mq, mc, cfg) : aw_launch<true, 2>(p, mq, mc, cfg);
+    else e = p.Q == 1 ? aw_launch<false, 1>(p, mq, mc, cfg) : aw_launch<false, 2>(p, mq, mc, cfg);
+    if (e != cudaSuccess || p.splits == 1) return e;
+  }
+  const int blocks = (int)ceil_div(p.max_n, 256);
+  cfg.gridDim = dim3((unsigned)p.B * (unsigned)blocks);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, attn_weights_join_kernel, p, blocks);
+}
+
+}  // namespace csa2

@@ -577,6 +577,206 @@ csa2_status csa2_cache8_attn(const csa2_cache8* cache, const csa2_cache8_attn_ar
   return from_cuda(launch_keys_attention(p, a->B, cache8_chunks(a->max_n, a->W), scratch(ws), (cudaStream_t)stream));
 }
 
+// ---------------------------------------------------------------- gathered weights
+static int64_t weights_n(int64_t max_n) { return max_n < INT32_MAX ? max_n : INT32_MAX; }   // n_entries is 32 bits
+
+size_t csa2_attn_weights_workspace_size(int B, int Q, int64_t max_n) {
+  if (B < 0 || Q < 0 || max_n < 0 || (int64_t)B * Q > MAX_KEY_QUERIES) return 0;
+  const int64_t n = weights_n(max_n), BQ = (int64_t)B * Q;
+  const AwPlan plan = attn_weights_plan(B, Q, n);
+  return HDR + align256((size_t)BQ * H * D * 2) + align256((size_t)(BQ + 1) * H * sizeof(float2)) +
+         (plan.splits > 1 ? align256((size_t)plan.splits * B * attn_weights_pitch(n) * sizeof(float)) : 0);
+}
+
+// p: the cache's part, filled in; entry: bytes of one of its entries
+static csa2_status do_attn_weights(AwParams p, int64_t entry, const csa2_weights_args* a, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  if (a->Q < 0 || a->max_n < 0 || !std::isfinite(a->scale) || !std::isfinite(a->decay)) return CSA2_ERR_INVALID_ARG;
+  const int64_t BQ = (int64_t)a->B * a->Q, out_n = a->B * p.cap * 4;
+  if (BQ > MAX_KEY_QUERIES || a->B > MAX_KEY_QUERIES) return CSA2_ERR_UNSUPPORTED;
+  const size_t need = csa2_attn_weights_workspace_size(a->B, a->Q, a->max_n);
+  csa2_status st = check_ws(ws, ws_bytes, need);
+  if (st != CSA2_OK || a->B == 0) return st;
+  if (!a->weights || !aligned4(a->weights) || !aligned4(a->prev) || !aligned4(p.n_entries)) return CSA2_ERR_INVALID_ARG;
+  if (BQ > 0 && (!a->q || !aligned16(a->q) || !a->q_pos || !aligned8(a->q_pos) || !a->lse || !aligned4(a->lse)))
+    return CSA2_ERR_INVALID_ARG;
+  const struct { const void* a; int64_t n; } in[] = {
+      {a->q, BQ * H * D * 2}, {a->q_pos, BQ * 8}, {a->lse, BQ * H * 4}, {ws, (int64_t)need}, {p.kv, a->B * p.cap * entry},
+      {p.scales8, p.scales8 ? a->B * (p.cap / BLK) * 4 : 0}, {p.n_entries, (int64_t)a->B * 4},
+      {a->prev, a->prev && a->prev != a->weights ? out_n : 0}};
+  for (const auto& x : in)
+    if (overlap(x.a, x.n, a->weights, out_n)) return CSA2_ERR_INVALID_ARG;
+  p.q = a->q;
+  p.q_pos = a->q_pos;
+  p.lse = a->lse;
+  p.scale = a->scale;
+  p.decay = a->decay;
+  p.prev = a->prev;
+  p.out = a->weights;
+  p.B = a->B;
+  p.Q = a->Q;
+  p.max_n = weights_n(a->max_n);
+  p.hdr = header(ws);
+  unsigned char* cur = scratch(ws);
+  p.q16 = reinterpret_cast<uint16_t*>(cur);
+  cur += align256((size_t)BQ * H * D * 2);
+  p.col = reinterpret_cast<float2*>(cur);
+  cur += align256((size_t)(BQ + 1) * H * sizeof(float2));
+  p.part = reinterpret_cast<float*>(cur);
+  return from_cuda(launch_attn_weights(p, (cudaStream_t)stream));
+}
+
+csa2_status csa2_attn_weights(const csa2_cache* cache, const csa2_weights_args* a, void* ws, size_t ws_bytes,
+                              void* stream) {
+  if (!a || a->B < 0) return CSA2_ERR_INVALID_ARG;
+  const csa2_status st = check_cache_entries(cache);
+  if (st != CSA2_OK) return st;
+  AwParams p{};
+  p.kv = cache->main_kv;
+  p.cap = cache->cap;
+  p.n_entries = cache->n_entries;
+  p.m = cache->m;
+  return do_attn_weights(p, MAIN_BYTES, a, ws, ws_bytes, stream);
+}
+
+csa2_status csa2_cache8_attn_weights(const csa2_cache8* cache, const csa2_weights_args* a, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  if (!a) return CSA2_ERR_INVALID_ARG;
+  const csa2_status st = check_cache8(cache, a->B);
+  if (st != CSA2_OK) return st;
+  AwParams p{};
+  p.kv = reinterpret_cast<const uint8_t*>(cache->codes);
+  p.scales8 = cache->scales;
+  p.cap = cache->cap;
+  p.n_entries = cache->n_entries;
+  p.m = cache->m;
+  return do_attn_weights(p, D, a, ws, ws_bytes, stream);
+}
+
+// ---------------------------------------------------------------- eviction
+size_t csa2_evict_workspace_size(int B, int64_t budget, int unit) {
+  if (B < 0 || budget < 1 || budget > INT32_MAX || (unit != 1 && unit != 8) || budget % unit != 0) return 0;
+  // the chunks of an 8-bit cache are the smaller ones
+  const int64_t chunks = evict_chunks(unit == 8 ? 8 : 4, unit, budget / unit);
+  return HDR + align256(sizeof(uint32_t)) + 2 * align256((size_t)B * 4) + align256((size_t)B * chunks * 4);
+}
+
+// p: the caches' part, filled in.  An array of either cache: its bytes for one entry times 8.
+struct EvArray {
+  const void* from;
+  void* to;
+  int64_t bytes8;
+};
+
+static csa2_status do_evict(EvParams p, const EvArray* arrays, int n_arrays, int bits, const csa2_evict_args* a, void* ws,
+                            size_t ws_bytes, void* stream) {
+  const int64_t unit = a->unit, lim = INT32_MAX;
+  if (a->B < 0 || a->budget < 1 || a->budget % unit != 0 || a->n_first < 0 || a->n_recent < 0) return CSA2_ERR_INVALID_ARG;
+  if (p.cap > lim || p.to_cap > lim || a->budget > lim) return CSA2_ERR_UNSUPPORTED;
+  if (a->n_first > a->budget || a->n_recent > a->budget || a->budget > p.to_cap) return CSA2_ERR_INVALID_ARG;
+  const int64_t first = ceil_div(a->n_first, unit), recent = ceil_div(a->n_recent, unit) + (unit > 1 ? 1 : 0);
+  if (first + recent > a->budget / unit) return CSA2_ERR_INVALID_ARG;
+  // a chunk of the moves is 160 entries or more: every grid stays below 2^31 CTAs
+  if (a->B > (1 << 20) || a->B * (a->budget / 128 + p.to_cap / 8192 + 2) >= lim) return CSA2_ERR_UNSUPPORTED;
+  const size_t need = csa2_evict_workspace_size(a->B, a->budget, a->unit);
+  csa2_status st = check_ws(ws, ws_bytes, need);
+  if (st != CSA2_OK || a->B == 0) return st;
+  if (!a->weights || !aligned16(a->weights) || !aligned4(a->to_weights) || !a->kept || !aligned4(a->kept) || !a->n_out ||
+      !aligned4(a->n_out) || !aligned4(p.n_entries))
+    return CSA2_ERR_INVALID_ARG;
+  // in place: every array the same
+  int same = 0;
+  for (int i = 0; i < n_arrays; i++) same += arrays[i].from == arrays[i].to;
+  if (same != 0 && (same != n_arrays || p.cap != p.to_cap)) return CSA2_ERR_INVALID_ARG;
+  p.in_place = same != 0;
+  // what the call writes and what it reads; [from, from + n) are pairs that may be one
+  struct Range { const void* a; int64_t n; } out[8], in[12];
+  int n_out = 0, n_in = 0;
+  for (int i = 0; i < n_arrays; i++) {
+    out[n_out++] = {arrays[i].to, a->B * (p.to_cap / 8) * arrays[i].bytes8};
+    if (!p.in_place) in[n_in++] = {arrays[i].from, a->B * (p.cap / 8) * arrays[i].bytes8};
+  }
+  if (a->to_weights) out[n_out++] = {a->to_weights, a->B * p.to_cap * 4};
+  out[n_out++] = {a->kept, a->B * (a->budget / unit) * 4};
+  out[n_out++] = {a->n_out, (int64_t)a->B * 4};
+  if (!(p.in_place && a->to_weights == a->weights)) in[n_in++] = {a->weights, a->B * p.cap * 4};
+  if (a->n_out != p.n_entries) in[n_in++] = {p.n_entries, (int64_t)a->B * 4};
+  in[n_in++] = {ws, (int64_t)need};
+  for (int i = 0; i < n_out; i++) {
+    for (int k = 0; k < n_in; k++)
+      if (overlap(out[i].a, out[i].n, in[k].a, in[k].n)) return CSA2_ERR_INVALID_ARG;
+    for (int k = 0; k < i; k++)
+      if (overlap(out[i].a, out[i].n, out[k].a, out[k].n)) return CSA2_ERR_INVALID_ARG;
+  }
+  p.B = a->B;
+  p.units = a->budget / unit;
+  p.first = first;
+  p.recent = a->n_recent;
+  p.weights = a->weights;
+  p.to_weights = a->to_weights;
+  p.kept = a->kept;
+  p.n_out = a->n_out;
+  p.hdr = header(ws);
+  unsigned char* cur = scratch(ws);
+  p.ticket = reinterpret_cast<uint32_t*>(cur);
+  cur += align256(sizeof(uint32_t));
+  p.marks = reinterpret_cast<int32_t*>(cur);
+  cur += align256((size_t)a->B * 4);
+  p.n_new = reinterpret_cast<int32_t*>(cur);
+  cur += align256((size_t)a->B * 4);
+  p.flags = reinterpret_cast<int32_t*>(cur);
+  return from_cuda(launch_evict(p, bits, a->unit, (cudaStream_t)stream));
+}
+
+csa2_status csa2_evict(const csa2_cache* cache, const csa2_cache* to, const csa2_evict_args* a, void* ws, size_t ws_bytes,
+                       void* stream) {
+  if (!a || (a->unit != 1 && a->unit != 8)) return CSA2_ERR_INVALID_ARG;
+  if (!to) to = cache;
+  csa2_status st = check_cache_entries(cache);
+  if (st != CSA2_OK) return st;
+  if (!to->main_kv || !aligned16(to->main_kv) || to->cap < 0 || to->cap % BLK != 0) return CSA2_ERR_INVALID_ARG;
+  const bool index = cache->idx_codes && cache->idx_scales && to->idx_codes && to->idx_scales;
+  if (index && (!aligned16(cache->idx_codes) || !aligned16(cache->idx_scales) || !aligned16(to->idx_codes) ||
+                !aligned16(to->idx_scales)))
+    return CSA2_ERR_INVALID_ARG;
+  EvParams p{};
+  p.rows = cache->main_kv;
+  p.to_rows = to->main_kv;
+  if (index) {
+    p.idx_codes = cache->idx_codes;
+    p.idx_scales = cache->idx_scales;
+    p.to_idx_codes = to->idx_codes;
+    p.to_idx_scales = to->idx_scales;
+  }
+  p.cap = cache->cap;
+  p.to_cap = to->cap;
+  p.n_entries = cache->n_entries;
+  const EvArray arrays[] = {{p.rows, p.to_rows, 8 * MAIN_BYTES}, {p.idx_codes, p.to_idx_codes, 8 * IDX_CODE_BYTES},
+                            {p.idx_scales, p.to_idx_scales, 8 * IDX_SCALE_BYTES}};
+  return do_evict(p, arrays, index ? 3 : 1, 4, a, ws, ws_bytes, stream);
+}
+
+csa2_status csa2_cache8_evict(const csa2_cache8* cache, const csa2_cache8* to, const csa2_evict_args* a, void* ws,
+                              size_t ws_bytes, void* stream) {
+  if (!a) return CSA2_ERR_INVALID_ARG;
+  if (a->unit != 8) return a->unit == 1 ? CSA2_ERR_UNSUPPORTED : CSA2_ERR_INVALID_ARG;
+  if (!to) to = cache;
+  csa2_status st = check_cache8(cache, a->B);
+  if (st != CSA2_OK) return st;
+  if (!to->codes || !to->scales || !aligned16(to->codes) || !aligned4(to->scales) || to->cap < 0 || to->cap % BLK != 0)
+    return CSA2_ERR_INVALID_ARG;
+  EvParams p{};
+  p.rows = reinterpret_cast<const uint8_t*>(cache->codes);
+  p.scales = cache->scales;
+  p.to_rows = reinterpret_cast<uint8_t*>(to->codes);
+  p.to_scales = to->scales;
+  p.cap = cache->cap;
+  p.to_cap = to->cap;
+  p.n_entries = cache->n_entries;
+  const EvArray arrays[] = {{p.rows, p.to_rows, 8 * D}, {p.scales, p.to_scales, 4}};
+  return do_evict(p, arrays, 2, 8, a, ws, ws_bytes, stream);
+}
+
 // HISA keeps up to 2048 of its summary rows: past 4096 blocks a row goes to
 // the multi-CTA selection (a single CTA spends most of its time on the
 // output once M is a large part of the row)

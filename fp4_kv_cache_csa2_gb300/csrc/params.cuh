@@ -145,6 +145,52 @@ struct C8WriteParams {        // entries of the 8-bit cache
   WsHeader* hdr;
 };
 
+struct AwParams {             // attention weight that entries gather
+  const uint8_t* kv;          // [B][cap][288], with scales8 [B][cap][512]
+  const float* scales8;       // 8-bit entries: [B][cap / 8]; null: 4-bit
+  int64_t cap;
+  const int32_t* n_entries;   // [B]
+  int m;
+  const uint16_t* q;          // [BQ][64][512] bf16
+  const int64_t* q_pos;       // [BQ]
+  const float* lse;           // [BQ][64]
+  float scale, decay;
+  const float* prev;          // [B][cap] or null
+  float* out;                 // [B][cap]
+  int B, Q;
+  int64_t max_n;
+  uint16_t* q16;              // scratch: [BQ][64][512] f16
+  float2* col;                // scratch: [BQ + 1][64]
+  float* part;                // splits > 1: [splits][B][pitch]
+  int64_t pitch;              // set by the launcher, as the next two
+  int runs, splits;
+  WsHeader* hdr;
+};
+
+struct EvParams {             // eviction; `to_`: where entries go
+  const uint8_t *rows, *idx_codes, *idx_scales;   // idx_*: null when not moved
+  const float* scales;        // 8-bit entries
+  uint8_t *to_rows, *to_idx_codes, *to_idx_scales;
+  float* to_scales;
+  int64_t cap, to_cap;
+  const int32_t* n_entries;   // [B]
+  int B;
+  int64_t units;              // units that stay at most
+  int64_t first;              // first units that stay
+  int64_t recent;             // last entries that stay
+  const float* weights;       // [B][cap]
+  float* to_weights;          // [B][to_cap] or null
+  int32_t* kept;              // [B][units]
+  int32_t* n_out;             // [B]
+  int in_place;
+  uint32_t* ticket;           // scratch: the next chunk
+  int32_t* marks;             // scratch: [B] chunks that are known to have been read
+  int32_t* n_new;             // scratch: [B] entries that stay
+  int32_t* flags;             // scratch: [B][chunks] chunks that have been read
+  int64_t chunks;             // set by the launcher
+  WsHeader* hdr;
+};
+
 cudaError_t launch_cache_write(const CwParams& p, cudaStream_t stream, int num_sms);
 cudaError_t launch_swa_fp8(const uint16_t* x, int64_t n_rows, uint8_t* out, cudaStream_t stream);
 cudaError_t launch_index_score(IsParams p, cudaStream_t stream);
@@ -176,6 +222,12 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
 cudaError_t launch_window_ring(const KeysParams& p, int B, cudaStream_t stream);
 bool window_ring_fits(int64_t W, int n_sink);
 size_t keys_part_bytes(int64_t BQ, int64_t chunks);
+struct AwPlan { int runs, splits; };    // of a sequence's tiles, of its queries
+AwPlan attn_weights_plan(int B, int Q, int64_t max_n);
+int64_t attn_weights_pitch(int64_t max_n);
+cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream);
+int64_t evict_chunks(int bits, int unit, int64_t units);
+cudaError_t launch_evict(EvParams p, int bits, int unit, cudaStream_t stream);
 cudaError_t launch_cache8_write(const C8WriteParams& p, cudaStream_t stream);
 cudaError_t launch_qk_norm_rope(const QkParams& p, cudaStream_t stream);
 

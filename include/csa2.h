@@ -585,6 +585,97 @@ csa2_status csa2_cache8_attn(const csa2_cache8 *cache, const csa2_cache8_attn_ar
                              size_t ws_bytes, void *stream);
 
 /*
+ * The attention weight that cache entries gather: for every entry j of a sequence,
+ *   weights[b][j] = decay * prev[b][j] + sum exp(scale * q_h . k_j - lse_h)
+ * over the call's queries that see j (j < floor((t+1)/m), as in the attention over
+ * the same cache) and their 64 heads, natural exponentials.  lse is what the
+ * attention of these queries wrote (csa2_dense_attn, csa2_cache8_attn: then the
+ * weights are the softmax's own; or that of another attention over more or fewer
+ * keys).  A query with t < 0, or a head with lse = -inf, adds nothing, whatever its
+ * q holds.  What a query does not see may hold anything.
+ *   prev         [B][cap], NULL: zeros (decay is then unused).  prev may be
+ *                weights itself.
+ *   weights      out [B][cap]: entries j < min(n_entries[b], max_n) are written,
+ *                the others left as they were.
+ *   max_n        no sequence has more entries; n_entries[b] above it or above cap
+ *                raises CSA2_ERR_BOUNDS (the entries from there on are left out).
+ * Q = 0 scales what was gathered.  B * Q <= 2^24; 4-bit and 8-bit cache
+ * (csa2_cache8_attn_weights).  q and the cache 16-byte, q_pos 8-byte, the others
+ * 4-byte aligned; weights must not overlap an input other than prev.
+ * Precision: f16 operands as in csa2_dense_attn (entries exact, q rounded to f16,
+ * of any size), binary32 products and sums, compensated over queries; the same
+ * inputs give the same bits.  Workspace: csa2_attn_weights_workspace_size with the
+ * call's B, Q and max_n (64 KB a query).
+ */
+typedef struct {
+    int B, Q;                   /* sequences, queries per sequence              */
+    float scale;                /* softmax scale                                */
+    float decay;                /* finite                                       */
+    int64_t max_n;              /* >= 0                                         */
+    const int64_t *q_pos;       /* [B][Q] raw positions                         */
+    const uint16_t *q;          /* bf16 [B][Q][64][512], rotated                */
+    const float *lse;           /* [B][Q][64]                                   */
+    const float *prev;          /* [B][cap] or NULL                             */
+    float *weights;             /* [B][cap]                                     */
+} csa2_weights_args;
+
+size_t csa2_attn_weights_workspace_size(int B, int Q, int64_t max_n);
+csa2_status csa2_attn_weights(const csa2_cache *cache, const csa2_weights_args *args, void *ws, size_t ws_bytes,
+                              void *stream);
+csa2_status csa2_cache8_attn_weights(const csa2_cache8 *cache, const csa2_weights_args *args, void *ws,
+                                     size_t ws_bytes, void *stream);
+
+/*
+ * Eviction: of every sequence with more than `budget` entries those leave that
+ * gathered the least weight, and the others move to the front, in their order.
+ *   unit         entries that stay or leave together: 1, or 8 (a block; the only
+ *                one for an 8-bit cache, whose scale is a block's).  A unit is
+ *                worth the largest weight of its entries (NaN below every number).
+ *   budget       entries that stay at most; a positive multiple of unit.
+ *   n_first, n_recent  the units with any of the first n_first or of the last
+ *                n_recent entries stay in any case.  Both, rounded up to units, and
+ *                with unit = 8 one more must fit into the budget.
+ *   Of the other units those worth most stay until the budget is full, of equals
+ *   the lower ones.
+ *   kept         out [B][budget / unit]: numbers of the units that stay,
+ *                ascending, -1 behind them.
+ *   n_out        out [B]: entries that stay (a sequence that ends inside a
+ *                block may keep fewer than budget).  May be n_entries.
+ *   `to`         where the entries go: another cache of its own memory (cap at
+ *                least budget; m and n_entries of it are not read), or NULL or the
+ *                same arrays: in place.  Index keys move along when both caches have them.
+ *                Rows behind the last entry are left as they were.
+ *   to_weights   out [B][cap of `to`]: weights of the entries that stay, zeros behind
+ *                them.  NULL: left out.  May be weights when in place.
+ * An evicted cache numbers its entries anew: entry j was entry kept[j] (of units:
+ * 8 kept[j / 8] + j % 8).  A caller that goes on with it takes m * (entries that
+ * left) off the positions it passes to the calls that read the cache (q_pos and, of a window,
+ * its base), and rotates new entries with the positions they really have.  Block
+ * summaries have to be made again.
+ * n_entries[b] > cap raises CSA2_ERR_BOUNDS (cap entries are taken).  cap < 2^31,
+ * budget < 2^31, else CSA2_ERR_UNSUPPORTED.  weights 16-byte, kept, n_out and
+ * to_weights 4-byte aligned, the caches as everywhere.  Outputs must not overlap
+ * inputs or each other but where it says so.  Workspace:
+ * csa2_evict_workspace_size.
+ */
+typedef struct {
+    int B;                      /* sequences                                    */
+    int32_t unit;               /* 1 or 8                                       */
+    int64_t budget;
+    int64_t n_first, n_recent;  /* >= 0                                         */
+    const float *weights;       /* [B][cap]                                     */
+    float *to_weights;          /* [B][cap of `to`] or NULL                     */
+    int32_t *kept;              /* [B][budget / unit]                           */
+    int32_t *n_out;             /* [B]                                          */
+} csa2_evict_args;
+
+size_t csa2_evict_workspace_size(int B, int64_t budget, int unit);
+csa2_status csa2_evict(const csa2_cache *cache, const csa2_cache *to, const csa2_evict_args *args, void *ws,
+                       size_t ws_bytes, void *stream);
+csa2_status csa2_cache8_evict(const csa2_cache8 *cache, const csa2_cache8 *to, const csa2_evict_args *args, void *ws,
+                              size_t ws_bytes, void *stream);
+
+/*
  * Test hook for the device-side timeout path; off unless a caller turns it on,
  * and never needed in production.  The pages have no counterpart.
  * While enabled (enable = 1) on the calling host thread, every index-scan
