@@ -1,12 +1,13 @@
 // Eviction: the units (1 or 8 entries) of a cache that gathered the least weight leave, the
 // others move to the front in their order.
 //
-// evict_select_kernel: a cluster of EV_CLUSTER CTAs a sequence.  Units become 32-bit
+// evict_select_kernel: a CTA or a cluster of them a sequence.  Units become 32-bit
 // keys in the order of their weights (the largest of a unit's entries; forced units above
-// all); three radix passes (11, 11, 10 bits) with histograms in shared memory, joined over
-// the cluster, find the key of the last unit that stays and how many of its equals do; a last walk
+// all); three radix passes (11, 11, 10 bits) with histograms in shared memory find the
+// key of the last unit that stays and how many of its equals do; a last walk
 // writes the numbers of the units that stay, ascending.  A CTA keeps its slice of the keys in
-// shared memory when it fits.
+// shared memory when it fits.  Of the other CTAs' histograms a CTA reads 32 sums and then the 64 bins
+// under one of them: all 2048 bins of eight CTAs took 4.5 us a pass.
 //
 // evict_move_kernel: a CTA moves a chunk of units: their bytes into shared memory, then to
 // where they go, one contiguous piece an array.  In place a chunk may be written only when the
@@ -25,19 +26,22 @@
 
 namespace csa2 {
 
-constexpr int EV_CLUSTER = 8, EV_THREADS = 1024, EV_BINS = 2048;
+constexpr int EV_THREADS = 1024, EV_BINS = 2048;
+constexpr int EV_COARSE = 32, EV_FINE = EV_BINS / EV_COARSE;   // a pass finds its bin in two steps
 constexpr int EV_KEYS = 48 * 1024;                        // of a slice that are kept in shared memory at most
 constexpr uint32_t EV_FORCED = 0xFFFFFFFFu;
 constexpr int EV_MOVE_THREADS = 256, EV_MOVE_BYTES = 96 * 1024;
 constexpr int EV_ZEROS = 16384;                           // weights behind the last that a CTA clears
 
+template <int CLUSTER>
 struct EvSelect {
-  int hist[EV_BINS];
-  int warp_sum[EV_THREADS / 32];
-  int warp_eq[EV_THREADS / 32];
-  int bin, above;                     // the pass's bin, keys of the sequence above it
+  int hist[2][EV_BINS];               // of a pass, in turn
+  int coarse[2][EV_COARSE];           // its sums over EV_FINE bins
+  int all_coarse[CLUSTER][EV_COARSE]; // of every CTA
+  int all_fine[CLUSTER][EV_FINE];     // the bins of the chosen coarse one, of every CTA
+  int warp_gt[EV_THREADS / 32], warp_eq[EV_THREADS / 32];
   int gt, eq;                         // of this CTA: keys above the last key, equal to it
-  uint32_t keys[1];                   // the slice, when it fits
+  alignas(16) uint32_t keys[4];       // the slice, when it fits
 };
 
 __device__ __forceinline__ uint32_t ev_cluster_rank() {
@@ -46,12 +50,20 @@ __device__ __forceinline__ uint32_t ev_cluster_rank() {
   return r;
 }
 
-__device__ __forceinline__ void ev_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// Every thread of the cluster (of the CTA, when it is alone).
+template <int CLUSTER>
+__device__ __forceinline__ void ev_sync() {
+  if (CLUSTER == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
 }
 
 // the int at `p`'s place in the shared memory of the cluster's CTA `rank`
+template <int CLUSTER>
 __device__ __forceinline__ int ev_remote(const int* p, uint32_t rank) {
+  if (CLUSTER == 1) return *p;
   uint32_t a;
   int v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
@@ -59,34 +71,71 @@ __device__ __forceinline__ int ev_remote(const int* p, uint32_t rank) {
   return v;
 }
 
+// Sum of x over the lanes before this one.
+__device__ __forceinline__ int ev_before(int x, int lane) {
+  int s = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, s, d);
+    if (lane >= d) s += y;
+  }
+  return s - x;
+}
+
 __device__ __forceinline__ uint32_t ev_key(float w) {
   if (w != w) return 0u;                              // NaN: below every number
   return float_key(w == 0.f ? 0.f : w);               // -0 is 0
 }
 
-// Key of unit u of a sequence with n entries.
+// Keys of a sequence's units: the order of their weights, those that stay in any case above all.
 template <int UNIT>
-__device__ __forceinline__ uint32_t ev_unit_key(const EvParams& p, const float* w, int64_t u, int64_t n) {
-  if (u < p.first || u >= (p.recent > 0 ? max(n - p.recent, (int64_t)0) / UNIT : INT64_MAX)) return EV_FORCED;
-  if (UNIT == 1) return ev_key(__ldcg(w + u));
-  uint32_t k = 0u;
-  if (u * UNIT + UNIT <= n) {
-    const float4 a = __ldcg(reinterpret_cast<const float4*>(w + u * UNIT)), c = __ldcg(reinterpret_cast<const float4*>(w + u * UNIT) + 1);
-    k = max(max(max(ev_key(a.x), ev_key(a.y)), max(ev_key(a.z), ev_key(a.w))),
-            max(max(ev_key(c.x), ev_key(c.y)), max(ev_key(c.z), ev_key(c.w))));
-  } else {
-    for (int64_t j = u * UNIT; j < n; j++) k = max(k, ev_key(__ldcg(w + j)));
-  }
-  return k;
-}
+struct EvUnits {
+  const float* w;                     // the sequence's weights
+  int64_t n, first, recent;           // entries; units before `first` and from `recent` on are forced
 
-template <int UNIT>
+  __device__ __forceinline__ uint32_t one(int64_t u) const {
+    if (u < first || u >= recent) return EV_FORCED;
+    uint32_t k = 0u;
+    for (int64_t j = u * UNIT; j < min(u * UNIT + UNIT, n); j++) k = max(k, ev_key(__ldcg(w + j)));
+    return k;
+  }
+  // units u .. u + 3 (u a multiple of 4; behind the last: anything)
+  __device__ __forceinline__ uint4 four(int64_t u) const {
+    uint32_t k[4];
+    if ((u + 4) * UNIT <= n) {
+      float4 v[UNIT];
+#pragma unroll
+      for (int i = 0; i < UNIT; i++) v[i] = __ldcg(reinterpret_cast<const float4*>(w + u * UNIT) + i);
+      if (UNIT == 1) {
+        k[0] = ev_key(v[0].x), k[1] = ev_key(v[0].y), k[2] = ev_key(v[0].z), k[3] = ev_key(v[0].w);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          k[x] = 0u;
+#pragma unroll
+          for (int i = x * UNIT / 4; i < (x + 1) * UNIT / 4; i++)
+            k[x] = max(k[x], max(max(ev_key(v[i].x), ev_key(v[i].y)), max(ev_key(v[i].z), ev_key(v[i].w))));
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; x++)
+        if (u + x < first || u + x >= recent) k[x] = EV_FORCED;
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; x++) k[x] = one(u + x);
+    }
+    return make_uint4(k[0], k[1], k[2], k[3]);
+  }
+};
+
+template <int UNIT, int CLUSTER>
 __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvParams p, int slots) {
   extern __shared__ __align__(16) unsigned char smem[];
-  EvSelect& sm = *reinterpret_cast<EvSelect*>(smem);
+  EvSelect<CLUSTER>& sm = *reinterpret_cast<EvSelect<CLUSTER>*>(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = ev_cluster_rank();
-  const int b = (int)(blockIdx.x / EV_CLUSTER);
+  const uint32_t rank = CLUSTER == 1 ? 0u : ev_cluster_rank();
+  const int b = (int)(blockIdx.x / CLUSTER);
+  for (int i = tid; i < 2 * EV_BINS; i += EV_THREADS) sm.hist[0][i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t given = p.n_entries[b];
   const int64_t n = max((int64_t)0, min((int64_t)given, p.cap));
@@ -95,154 +144,157 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvParams p,
   const int count = (int)min(units, K);
   int32_t* kept = p.kept + (int64_t)b * K;
   // flags of the moves, and behind the last kept unit: -1
-  for (int64_t i = rank * EV_THREADS + tid; i < p.chunks; i += EV_CLUSTER * EV_THREADS) p.flags[(int64_t)b * p.chunks + i] = 0;
-  for (int64_t i = count + rank * EV_THREADS + tid; i < K; i += EV_CLUSTER * EV_THREADS) kept[i] = -1;
+  for (int64_t i = rank * EV_THREADS + tid; i < p.chunks; i += CLUSTER * EV_THREADS) p.flags[(int64_t)b * p.chunks + i] = 0;
+  for (int64_t i = count + rank * EV_THREADS + tid; i < K; i += CLUSTER * EV_THREADS) kept[i] = -1;
   if (rank == 0 && tid == 0) p.marks[b] = 0;
   if (b == 0 && rank == 0 && tid == 0) *p.ticket = 0u;
   if (units <= K) {                                   // all stay
-    for (int64_t i = rank * EV_THREADS + tid; i < units; i += EV_CLUSTER * EV_THREADS) kept[i] = (int32_t)i;
-    ev_cluster_sync();                                // every CTA has read n_entries
+    for (int64_t i = rank * EV_THREADS + tid; i < units; i += CLUSTER * EV_THREADS) kept[i] = (int32_t)i;
+    ev_sync<CLUSTER>();                               // every CTA has read n_entries
     if (rank == 0 && tid == 0) {
       p.n_new[b] = (int32_t)n;
       p.n_out[b] = (int32_t)n;
     }
     return;
   }
-  const float* w = p.weights + (int64_t)b * p.cap;
-  const int64_t per = (units + EV_CLUSTER - 1) / EV_CLUSTER, u0 = min(per * rank, units);
-  const int mine = (int)(min(u0 + per, units) - u0);
-  const bool cached = mine <= slots;
-  auto key = [&](int i) { return cached ? sm.keys[i] : ev_unit_key<UNIT>(p, w, u0 + i, n); };
-  if (cached)
-    for (int i = tid; i < mine; i += EV_THREADS) sm.keys[i] = ev_unit_key<UNIT>(p, w, u0 + i, n);
-  int64_t left = K;                                   // units still to be found at or below the prefix's bins
+  const EvUnits<UNIT> all{p.weights + (int64_t)b * p.cap, n, p.first,
+                          p.recent > 0 ? max(n - p.recent, (int64_t)0) / UNIT : INT64_MAX};
+  const int64_t per = ((units + CLUSTER - 1) / CLUSTER + 3) / 4 * 4, u0 = min(per * rank, units);
+  const int mine = (int)(min(u0 + per, units) - u0), quads = (mine + 3) / 4;
+  const bool cached = 4 * quads <= slots;
+  uint4* keys = reinterpret_cast<uint4*>(sm.keys);
+  if (cached) {
+#pragma unroll 4
+    for (int i = tid; i < quads; i += EV_THREADS) keys[i] = all.four(u0 + 4 * i);
+  }
+  auto four = [&](int i) { return cached ? keys[i] : all.four(u0 + 4 * (int64_t)i); };
+  int left = (int)K;                                  // keys still to be found among those with the prefix
   uint32_t prefix = 0u;
-  int gt = 0;                                         // keys of this CTA above the prefix so far
+  int gt = 0;                                         // keys of this CTA above the prefix
+  int eq = 0;                                         // keys of this CTA with it
   for (int pass = 0; pass < 3; pass++) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    for (int i = tid; i < EV_BINS; i += EV_THREADS) sm.hist[i] = 0;
+    // (the first pass's buffer again in the third: between them lies a barrier that its readers have come to)
+    int* hist = sm.hist[pass & 1];
+    if (pass == 2)
+      for (int i = tid; i < EV_BINS; i += EV_THREADS) hist[i] = 0;
     __syncthreads();
-    for (int i = tid; i < mine; i += EV_THREADS) {
-      const uint32_t k = key(i);
-      if (pass == 0 || (k ^ prefix) >> (shift + bits) == 0u) atomicAdd(&sm.hist[k >> shift & ((1u << bits) - 1u)], 1);
-    }
-    __syncthreads();
-    ev_cluster_sync();
-    // thread t has bins 2 t', 2 t' + 1 from the top, t' = EV_THREADS - 1 - t
-    const int lo = 2 * (EV_THREADS - 1 - tid);
-    int own[2] = {sm.hist[lo], sm.hist[lo + 1]}, all[2] = {0, 0};
+#pragma unroll 2
+    for (int i = tid; i < quads; i += EV_THREADS) {
+      const uint4 v = four(i);
+      const uint32_t k[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (uint32_t r = 0; r < EV_CLUSTER; r++) {
-      all[0] += ev_remote(&sm.hist[lo], r);
-      all[1] += ev_remote(&sm.hist[lo + 1], r);
+      for (int x = 0; x < 4; x++)
+        if (4 * i + x < mine && (pass == 0 || (k[x] ^ prefix) >> (shift + bits) == 0u))
+          atomicAdd(&hist[k[x] >> shift & ((1u << bits) - 1u)], 1);
     }
-    // sums over the threads before this one (the bins above)
-    int sum = all[0] + all[1], own_sum = own[0] + own[1];
+    __syncthreads();
+    {                                                 // warp = coarse bin
+      const int s = __reduce_add_sync(0xFFFFFFFFu, hist[EV_FINE * warp + lane] + hist[EV_FINE * warp + 32 + lane]);
+      if (lane == 0) sm.coarse[pass & 1][warp] = s;
+    }
+    ev_sync<CLUSTER>();
+    if (warp < CLUSTER) sm.all_coarse[warp][lane] = ev_remote<CLUSTER>(&sm.coarse[pass & 1][lane], warp);
+    __syncthreads();
+    // Lane l has bin EV_COARSE - 1 - l; in every warp the same.
+    int sum = 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d), y = __shfl_up_sync(0xFFFFFFFFu, own_sum, d);
-      if (lane >= d) sum += x, own_sum += y;
-    }
-    if (lane == 31) sm.warp_sum[warp] = sum, sm.warp_eq[warp] = own_sum;
+    for (int r = 0; r < CLUSTER; r++) sum += sm.all_coarse[r][EV_COARSE - 1 - lane];
+    int own = sm.all_coarse[rank][EV_COARSE - 1 - lane];
+    int above = ev_before(sum, lane), own_above = ev_before(own, lane);
+    int at = __ffs(__ballot_sync(0xFFFFFFFFu, above < left && left <= above + sum)) - 1;
+    const int coarse = EV_COARSE - 1 - at;
+    left -= __shfl_sync(0xFFFFFFFFu, above, at);
+    gt += __shfl_sync(0xFFFFFFFFu, own_above, at);
+    if (warp < 2 * CLUSTER)
+      sm.all_fine[warp >> 1][32 * (warp & 1) + lane] =
+          ev_remote<CLUSTER>(&hist[EV_FINE * coarse + 32 * (warp & 1) + lane], warp >> 1);
     __syncthreads();
-    if (warp == 0) {
-      int x = sm.warp_sum[lane], y = sm.warp_eq[lane];
+    // lane l has bins EV_FINE - 1 - 2 l and the one below
+    int2 f = make_int2(0, 0);
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int a = __shfl_up_sync(0xFFFFFFFFu, x, d), c = __shfl_up_sync(0xFFFFFFFFu, y, d);
-        if (lane >= d) x += a, y += c;
-      }
-      sm.warp_sum[lane] = x, sm.warp_eq[lane] = y;
+    for (int r = 0; r < CLUSTER; r++) {
+      f.x += sm.all_fine[r][EV_FINE - 1 - 2 * lane];
+      f.y += sm.all_fine[r][EV_FINE - 2 - 2 * lane];
     }
-    __syncthreads();
-    const int before = (warp ? sm.warp_sum[warp - 1] : 0) + sum - all[0] - all[1];
-    const int own_before = (warp ? sm.warp_eq[warp - 1] : 0) + own_sum - own[0] - own[1];
-    // the bin in which the `left`-th key from the top lies
-    if (before < left && left <= (int64_t)before + all[1]) {
-      sm.bin = lo + 1;
-      sm.above = before;
-      sm.gt = own_before;
-      sm.eq = own[1];
-    } else if (before + all[1] < left && left <= (int64_t)before + all[1] + all[0]) {
-      sm.bin = lo;
-      sm.above = before + all[1];
-      sm.gt = own_before + own[1];
-      sm.eq = own[0];
-    }
-    __syncthreads();
-    prefix |= (uint32_t)sm.bin << shift;
-    left -= sm.above;
-    gt += sm.gt;
-    ev_cluster_sync();                                // all have read this pass's histogram
+    const int ox = sm.all_fine[rank][EV_FINE - 1 - 2 * lane], oy = sm.all_fine[rank][EV_FINE - 2 - 2 * lane];
+    above = ev_before(f.x + f.y, lane);
+    own_above = ev_before(ox + oy, lane);
+    at = __ffs(__ballot_sync(0xFFFFFFFFu, above < left && left <= above + f.x + f.y)) - 1;
+    const bool second = left > above + f.x;           // (of lane `at`)
+    const int bin = EV_FINE * coarse + EV_FINE - 1 - 2 * lane - (second ? 1 : 0);
+    prefix |= (uint32_t)__shfl_sync(0xFFFFFFFFu, bin, at) << shift;
+    eq = __shfl_sync(0xFFFFFFFFu, second ? oy : ox, at);
+    gt += __shfl_sync(0xFFFFFFFFu, own_above + (second ? ox : 0), at);
+    left -= __shfl_sync(0xFFFFFFFFu, above + (second ? f.x : 0), at);
   }
   const uint32_t last = prefix;                       // key of the last unit that stays; `left` of its equals do
-  if (tid == 0) sm.gt = gt;
-  ev_cluster_sync();
+  if (tid == 0) {
+    sm.gt = gt;
+    sm.eq = eq;
+  }
+  ev_sync<CLUSTER>();
+  int gt_base, eq_base, eq_all;                       // of the CTAs before this one; of all
+  {
+    const int g = lane < CLUSTER ? ev_remote<CLUSTER>(&sm.gt, lane) : 0, e = lane < CLUSTER ? ev_remote<CLUSTER>(&sm.eq, lane) : 0;
+    gt_base = __reduce_add_sync(0xFFFFFFFFu, lane < (int)rank ? g : 0);
+    eq_base = __reduce_add_sync(0xFFFFFFFFu, lane < (int)rank ? e : 0);
+    eq_all = __reduce_add_sync(0xFFFFFFFFu, e);
+  }
+  // (no CTA leaves while another reads its shared memory: waited for at the end)
+  if (CLUSTER > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if (rank == 0 && tid == 0) {
-    // the last unit may be a part, which is not kept when another of its key comes first
+    // the last unit may be a part, which is not kept when others of its key come first
     const int64_t tail = n - (units - 1) * UNIT;
     bool tail_stays = true;
     if (UNIT > 1 && tail < UNIT) {
-      const uint32_t k = ev_unit_key<UNIT>(p, w, units - 1, n);
-      int equal = 0;
-      for (uint32_t r = 0; r < EV_CLUSTER; r++) equal += ev_remote(&sm.eq, r);
-      tail_stays = k > last || (k == last && left == equal);
+      const uint32_t k = all.one(units - 1);
+      tail_stays = k > last || (k == last && left == eq_all);
     }
     const int32_t out = (int32_t)(K * UNIT - (tail_stays ? UNIT - tail : 0));
     p.n_new[b] = out;
     p.n_out[b] = out;
   }
-  int64_t gt_base = 0, eq_base = 0;                   // of the CTAs before this one
-  for (uint32_t r = 0; r < rank; r++) {
-    gt_base += ev_remote(&sm.gt, r);
-    eq_base += ev_remote(&sm.eq, r);
-  }
-  ev_cluster_sync();                                  // (no CTA leaves while another reads its shared memory)
-  constexpr int EACH = 8;                             // units of a thread in a row
-  for (int i0 = 0; i0 < mine; i0 += EACH * EV_THREADS) {
-    uint32_t k[EACH];
+  for (int i0 = 0; i0 < quads; i0 += 2 * EV_THREADS) {   // a thread takes two fours in a row
+    uint32_t k[8];
     int g = 0, e = 0;
+    const int q0 = i0 + 2 * tid;
 #pragma unroll
-    for (int x = 0; x < EACH; x++) {
-      const int i = i0 + EACH * tid + x;
-      k[x] = i < mine ? key(i) : 0u;
-      if (i < mine) {
-        g += k[x] > last;
-        e += k[x] == last;
-      }
+    for (int y = 0; y < 2; y++) {
+      const uint4 v = q0 + y < quads ? four(q0 + y) : make_uint4(0u, 0u, 0u, 0u);
+      k[4 * y] = v.x, k[4 * y + 1] = v.y, k[4 * y + 2] = v.z, k[4 * y + 3] = v.w;
     }
-    int gs = g, es = e;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(0xFFFFFFFFu, gs, d), y = __shfl_up_sync(0xFFFFFFFFu, es, d);
-      if (lane >= d) gs += x, es += y;
+    for (int x = 0; x < 8; x++) {
+      const bool there = 4 * q0 + x < mine;
+      g += there && k[x] > last;
+      e += there && k[x] == last;
     }
+    int gp = ev_before(g, lane), ep = ev_before(e, lane);
     __syncthreads();                                  // the sums of the turn before are read
-    if (lane == 31) sm.warp_sum[warp] = gs, sm.warp_eq[warp] = es;
-    __syncthreads();
-    int64_t gp = gt_base + gs - g, ep = eq_base + es - e;
-    int gt_all = 0, eq_all = 0;
-    for (int x = 0; x < EV_THREADS / 32; x++) {
-      const int a = sm.warp_sum[x], c = sm.warp_eq[x];
-      if (x < warp) gp += a, ep += c;
-      gt_all += a;
-      eq_all += c;
+    if (lane == 31) {
+      sm.warp_gt[warp] = gp + g;
+      sm.warp_eq[warp] = ep + e;
     }
-    gt_base += gt_all;
-    eq_base += eq_all;
+    __syncthreads();
+    const int wg = sm.warp_gt[lane], we = sm.warp_eq[lane];
+    gp += gt_base + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wg : 0);
+    ep += eq_base + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? we : 0);
+    gt_base += __reduce_add_sync(0xFFFFFFFFu, wg);
+    eq_base += __reduce_add_sync(0xFFFFFFFFu, we);
 #pragma unroll
-    for (int x = 0; x < EACH; x++) {
-      const int i = i0 + EACH * tid + x;
-      if (i >= mine) break;
+    for (int x = 0; x < 8; x++) {
+      if (4 * q0 + x >= mine) break;
       if (k[x] > last) {
-        kept[gp + min(ep, left)] = (int32_t)(u0 + i);
+        kept[gp + min(ep, left)] = (int32_t)(u0 + 4 * q0 + x);
         gp++;
       } else if (k[x] == last) {
-        if (ep < left) kept[gp + ep] = (int32_t)(u0 + i);
+        if (ep < left) kept[gp + ep] = (int32_t)(u0 + 4 * q0 + x);
         ep++;
       }
     }
   }
+  if (CLUSTER > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void ev_copy16(void* dst, const void* src) {
@@ -375,27 +427,40 @@ int64_t evict_chunks(int bits, int unit, int64_t units) {
   return ceil_div(units, c);
 }
 
-template <int UNIT>
+template <int UNIT, int CLUSTER>
 static cudaError_t ev_select(const EvParams& p, cudaLaunchConfig_t cfg) {
+  using S = EvSelect<CLUSTER>;
   static PerDeviceOnce attrs;
-  constexpr int most = (int)sizeof(EvSelect) + EV_KEYS * 4;
+  constexpr int most = (int)sizeof(S) + EV_KEYS * 4;
+  static_assert(most <= 227 * 1024, "shared memory per CTA");
   cudaError_t e = attrs.ensure([](int) {
-    return cudaFuncSetAttribute(evict_select_kernel<UNIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    cudaError_t r = cudaFuncSetAttribute(evict_select_kernel<UNIT, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r == cudaSuccess && CLUSTER > 8)
+      r = cudaFuncSetAttribute(evict_select_kernel<UNIT, CLUSTER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return r;
   });
   if (e != cudaSuccess) return e;
-  const int64_t slice = ceil_div(ceil_div(p.cap, UNIT), EV_CLUSTER);
-  const int slots = (int)(slice < EV_KEYS ? slice : EV_KEYS);
-  cfg.gridDim = dim3((unsigned)p.B * EV_CLUSTER);
+  const int64_t slice = ceil_div(ceil_div(ceil_div(p.cap, UNIT), CLUSTER), 4) * 4;
+  const int slots = slice <= EV_KEYS ? (int)slice : 0;
+  cfg.gridDim = dim3((unsigned)p.B * CLUSTER);
   cfg.blockDim = dim3(EV_THREADS);
-  cfg.dynamicSmemBytes = sizeof(EvSelect) + (size_t)slots * 4;
+  cfg.dynamicSmemBytes = sizeof(S) + (size_t)slots * 4;
   cudaLaunchAttribute attr[2];
   attr[0] = cfg.attrs[0];
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = EV_CLUSTER;
+  attr[1].val.clusterDim.x = CLUSTER;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<UNIT>, p, slots);
+  cfg.numAttrs = CLUSTER > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<UNIT, CLUSTER>, p, slots);
+}
+
+// CTAs of a sequence's selection.
+template <int UNIT>
+static cudaError_t ev_select_any(const EvParams& p, const cudaLaunchConfig_t& cfg) {
+  const int64_t units = ceil_div(p.cap, UNIT);
+  if (units <= 8192) return ev_select<UNIT, 1>(p, cfg);
+  return units <= 65536 || p.B > 8 ? ev_select<UNIT, 8>(p, cfg) : ev_select<UNIT, 16>(p, cfg);
 }
 
 template <int BITS, int UNIT>
@@ -423,7 +488,7 @@ cudaError_t launch_evict(EvParams p, int bits, int unit, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = unit == 1 ? ev_select<1>(p, cfg) : ev_select<8>(p, cfg);
+  cudaError_t e = unit == 1 ? ev_select_any<1>(p, cfg) : ev_select_any<8>(p, cfg);
   if (e != cudaSuccess) return e;
   return bits == 8 ? ev_move<8, 8>(p, cfg) : unit == 1 ? ev_move<4, 1>(p, cfg) : ev_move<4, 8>(p, cfg);
 }

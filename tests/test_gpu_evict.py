@@ -122,6 +122,15 @@ def test_evict_slices_beyond_shared_memory():
     run_and_check(4, 1, 1, cap, [n], 3_000, 0, 0, make_weights(2, 1, cap, "spread"), False, index=False)
 
 
+@pytest.mark.parametrize("B", [1, 9])
+def test_evict_slices_of_every_cluster_beyond_shared_memory(B):
+    """One sequence: 16 CTAs; nine: 8 CTAs each.  The keys of a slice are read anew in every pass."""
+    n = 16 * 49_152 + 1_234 if B == 1 else 8 * 49_152 + 1_234
+    cap = -(-n // 8) * 8
+    w = make_weights(3, B, cap, "ties" if B == 1 else "spread")
+    run_and_check(4, 1, B, cap, [n - 1000 * b for b in range(B)], 150_000, 4, 100, w, B == 1, index=False)
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict_without_weights_or_index_keys(in_place):
     w = make_weights(3, 2, 304, "spread")
