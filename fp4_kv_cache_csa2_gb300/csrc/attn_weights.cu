@@ -69,6 +69,9 @@ __device__ __noinline__ bool aw_timeout(int* err, WsHeader* hdr, int where) {
   return false;
 }
 
+// x, the same in every lane, in a uniform register.
+__device__ __forceinline__ uint32_t aw_uniform(uint32_t x) { return __reduce_or_sync(0xFFFFFFFFu, x); }
+
 // entries of sequence b that the call deals with
 __device__ __forceinline__ int aw_entries(const AwParams& p, int b) {
   return (int)max((int64_t)0, min((int64_t)p.n_entries[b], min(p.cap, p.max_n)));
@@ -194,29 +197,39 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     constexpr uint32_t idesc = tc::idesc_f16(AW_KEYS, C::N, 0, 0);
     const uint64_t q_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
     const uint32_t leader = tc::elect_one();
-    uint32_t u = 0, st = 0, st_use = 0;               // group of the CTA, query stage and its use
-    for (int t = 0; t < live; t++) {
-      int g = next_group(0, t_lo + t);
+    // An MMA takes its addresses from uniform registers: what the loops follow from goes through a
+    // reduction over the warp, whose result is uniform (else an MMA takes 82 cycles to issue).
+    const int n_live = (int)aw_uniform((uint32_t)live), n_g = (int)aw_uniform((uint32_t)ng);
+    uint32_t u = 0, st = 0, st_use = 0, ab = 0, ab_use = 0;   // group of the CTA; query stage, A buffer and their uses
+    for (int t = 0; t < n_live; t++) {
+      int g = (int)aw_uniform((uint32_t)next_group(0, t_lo + t));
       bool first = true;
-      while (g < ng) {
-        const int after = next_group(g + 1, t_lo + t);
+      const uint32_t ab0 = ab;
+      while (g < n_g) {
+        const int after = (int)aw_uniform((uint32_t)next_group(g + 1, t_lo + t));
         if (u >= 2) wait(&sm.s_free[u & 1], (u >> 1) - 1, 60);
+        const uint32_t s = C::S_COL + C::N * (u & 1);
+        uint32_t k = ab0;
+#pragma unroll 1
         for (int h = 0; h < 2; h++) {
-          const uint32_t k = 2 * t + h, ab = k % C::A_BUFS;
-          if (first) wait(&sm.a_full[ab], k / C::A_BUFS, 61);
+          if (first) {
+            wait(&sm.a_full[ab], ab_use, 61);
+            if (++ab == C::A_BUFS) ab = 0, ab_use++;
+          }
 #pragma unroll 1
           for (int i = 0; i < 4; i++) {
-            if (!resident || u == 0) wait(&sm.q_full[st], st_use, 62);
+            if (n_g > 1 || u == 0) wait(&sm.q_full[st], st_use, 62);
             tc::fence_after_sync();
             const uint64_t qa = q_d + (uint32_t)(st * C::STAGE >> 4);
+            const uint32_t a = 128 * k + 32 * i;
 #pragma unroll
             for (int x = 0; x < 4; x++)
-              tc::mma_f16_ts_warp(leader, C::S_COL + C::N * (u & 1), 128 * ab + 32 * i + 8 * x, qa + 2 * x, idesc,
-                                  (h || i || x) ? 1u : 0u);
-            if (!resident) tc::commit_warp(leader, &sm.q_free[st]);
+              tc::mma_f16_ts_warp(leader, s, a + 8 * x, qa + 2 * x, idesc, (h || i || x) ? 1u : 0u);
+            if (n_g > 1) tc::commit_warp(leader, &sm.q_free[st]);
             if (++st == AW_STAGES) st = 0, st_use++;
           }
-          if (after >= ng) tc::commit_warp(leader, &sm.a_free[ab]);
+          if (after >= n_g) tc::commit_warp(leader, &sm.a_free[k]);
+          if (++k == C::A_BUFS) k = 0;
         }
         tc::commit_warp(leader, &sm.s_full[u & 1]);
         u++;
