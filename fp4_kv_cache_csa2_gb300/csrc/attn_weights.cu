@@ -13,11 +13,14 @@
 // own factor), as in keys_attention.cu.  Sums: 64 weights in binary32, then compensated over a
 // CTA's queries.
 //
-// A CTA takes a run of tiles of one sequence and a run of query groups (one query, N = 64,
-// when there is only one; else two, N = 128).  The tile's entries lie in TMEM as the A operand
+// A CTA takes a run of tiles of one sequence.  The tile's entries lie in TMEM as the A operand
 // (256 columns of f16 pairs): with A in shared memory a product of N = 64 would take 48
-// cycles instead of 32, and the widened tile 128 KB.  Two S accumulators; the queries' dims come
-// through a ring of stages, or stay there when the CTA has one group.
+// cycles instead of 32, and the widened tile 128 KB.  Two S accumulators.
+// One query (N = 64): its dims stay in shared memory.  More: two CTAs make a pair
+// (cta_group::2) that takes 256 entries, a half each, and a run of groups of two queries (N = 128);
+// each CTA loads one query of a group through a ring of stages, and the pair's products read
+// both.  With single CTAs of two queries every SM took 128 KB of queries from L2 for
+// 2048 cycles of products and waited for them: 4180 cycles a group.
 // Warps 0..7: exponentials and sums (warps 4..7: the second query, or the second half of the heads);
 // 8..15: entries to TMEM, a half of the dims each four; 16: MMAs; 17: copies of entries; 18: copies of
 // queries.  All waits are bounded; a timeout reports CSA2_ERR_TIMEOUT.
@@ -32,31 +35,34 @@ constexpr int AW_KEYS = 128;                              // entries of a tile
 constexpr int AW_SUM_WARPS = 8, AW_FILL_WARPS = 8;
 constexpr int AW_MMA_WARP = AW_SUM_WARPS + AW_FILL_WARPS, AW_KEY_WARP = AW_MMA_WARP + 1, AW_Q_WARP = AW_KEY_WARP + 1;
 constexpr int AW_THREADS = 32 * (AW_Q_WARP + 1);
-constexpr int AW_STAGES = 8;                              // of 64 dims of a group
+constexpr int AW_PIECES = 8;                              // of 64 dims of a query
+constexpr int AW_STAGE = 64 * 128;                        // [64 heads][64 dims] f16, SW128
 constexpr int AW_GROUPS = 512;                            // query groups of a CTA at most
 constexpr float AW_LOG2E = 1.4426950408889634f;
 constexpr int AW_SMS = 152;
 
-// NQ: queries of a group.  A buffers hold half of the dims of a tile.
-template <bool E8, int NQ>
+// PAIR: two CTAs, two queries a group; else one of each.  A buffers hold half of the dims of a tile.
+template <bool E8, bool PAIR>
 struct Aw {
-  static constexpr int N = 64 * NQ;
+  static constexpr int NQ = PAIR ? 2 : 1, N = 64 * NQ;
+  static constexpr int STEP = NQ * AW_KEYS;               // entries of a step
   static constexpr int ENTRY = E8 ? D : MAIN_BYTES;
   static constexpr int TILE = AW_KEYS * ENTRY;            // bytes of a tile as stored
-  static constexpr int TILES = NQ == 1 ? (E8 ? 2 : 4) : (E8 ? 1 : 2);   // staged tiles
-  static constexpr int A_BUFS = NQ == 1 ? 3 : 2;          // of 128 columns
+  static constexpr int TILES = PAIR ? 1 : E8 ? 2 : 4;     // staged tiles
+  static constexpr int A_BUFS = PAIR ? 2 : 3;             // of 128 columns
   static constexpr int S_COL = 128 * A_BUFS;
-  static constexpr int STAGE = N * 128;                   // [N heads][64 dims] f16, SW128
-  static constexpr int OFF_TILE = AW_STAGES * STAGE;
+  static constexpr int RING = PAIR ? 2 : 1;               // groups of query stages
+  static constexpr int OFF_TILE = RING * AW_PIECES * AW_STAGE;
   static constexpr int OFF_SMALL = OFF_TILE + TILES * TILE;
   struct Small {
     float2 col[2][N];                 // a head's factor, minus its lse, in powers of two
     float joined[2][AW_KEYS];         // the second half's sums
     int vis[AW_GROUPS * NQ];          // entries each query sees
     uint64_t tile_full[TILES], tile_free[TILES];    // TMA; a fill warp each
-    uint64_t a_full[A_BUFS], a_free[A_BUFS];        // four fill warps; MMAs
-    uint64_t q_full[AW_STAGES], q_free[AW_STAGES];  // TMA; MMAs
-    uint64_t s_full[2], s_free[2], col_full[2];     // MMAs; a sum warp each; TMA
+    // Of a pair CTA 0's a_full, q_full and s_free count, for both; what MMAs complete is told to both.
+    uint64_t a_full[A_BUFS], a_free[A_BUFS];        // four fill warps of a CTA; MMAs
+    uint64_t q_full[RING][AW_PIECES], q_free[RING][AW_PIECES];      // TMA; MMAs
+    uint64_t s_full[2], s_free[2], col_full[2], col_free[2];        // MMAs; sum warps; TMA; sum warps
     uint32_t tmem_base;
     int most, err;
   };
@@ -111,41 +117,49 @@ __global__ void __launch_bounds__(256) attn_weights_query_kernel(AwParams p) {
   }
 }
 
-template <bool E8, int NQ>
+template <bool E8, bool PAIR>
 __global__ void __launch_bounds__(AW_THREADS, 1)
 attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_codes) {
-  using C = Aw<E8, NQ>;
+  using C = Aw<E8, PAIR>;
   using Small = typename C::Small;
+  constexpr int NQ = C::NQ;
   extern __shared__ __align__(1024) unsigned char smem[];
   Small& sm = *reinterpret_cast<Small*>(smem + C::OFF_SMALL);
   WsHeader* hdr = p.hdr;
-  if (tc::smem_u32(smem) & 1023u) {                   // the swizzled tiles need the declared alignment
+  if (tc::smem_u32(smem) & 1023u) {                   // the swizzled tiles need the declared alignment (the same in both CTAs)
     if (threadIdx.x == 0) report(hdr, CSA2_ERR_CUDA, 3);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-  // block = (query split, sequence, run of tiles)
-  const int run = (int)(blockIdx.x % (uint32_t)p.runs), sb = (int)(blockIdx.x / (uint32_t)p.runs);
+  const int rank = PAIR ? (int)tc::cluster_rank() : 0;
+  // block = (query split, sequence, run of steps, CTA of the pair)
+  const uint32_t item = blockIdx.x / (uint32_t)NQ;
+  const int run = (int)(item % (uint32_t)p.runs), sb = (int)(item / (uint32_t)p.runs);
   const int b = sb % p.B, qs = sb / p.B;
 
-  if (warp == AW_MMA_WARP) tc::tmem_alloc(&sm.tmem_base, 512);
+  if (warp == AW_MMA_WARP) {
+    if (PAIR) tc::tmem_alloc_pair(&sm.tmem_base, 512);
+    else tc::tmem_alloc(&sm.tmem_base, 512);
+  }
   if (tid == 0) {
     for (int i = 0; i < C::TILES; i++) {
       tc::bar_init(&sm.tile_full[i], 1);
       tc::bar_init(&sm.tile_free[i], AW_FILL_WARPS);
     }
     for (int i = 0; i < C::A_BUFS; i++) {
-      tc::bar_init(&sm.a_full[i], AW_FILL_WARPS / 2);
+      tc::bar_init(&sm.a_full[i], NQ * AW_FILL_WARPS / 2);
       tc::bar_init(&sm.a_free[i], 1);
     }
-    for (int i = 0; i < AW_STAGES; i++) {
-      tc::bar_init(&sm.q_full[i], 1);
-      tc::bar_init(&sm.q_free[i], 1);
-    }
+    for (int i = 0; i < C::RING; i++)
+      for (int k = 0; k < AW_PIECES; k++) {
+        tc::bar_init(&sm.q_full[i][k], 1);
+        tc::bar_init(&sm.q_free[i][k], 1);
+      }
     for (int i = 0; i < 2; i++) {
       tc::bar_init(&sm.s_full[i], 1);
-      tc::bar_init(&sm.s_free[i], AW_SUM_WARPS);
+      tc::bar_init(&sm.s_free[i], NQ * AW_SUM_WARPS);
       tc::bar_init(&sm.col_full[i], 1);
+      tc::bar_init(&sm.col_free[i], AW_SUM_WARPS);
     }
     sm.most = 0;
     sm.err = 0;
@@ -154,16 +168,17 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     if (E8) tc::prefetch_tensormap(&map_codes);
   }
   tc::fence_before_sync();
-  __syncthreads();
+  if (PAIR) tc::cluster_sync();
+  else __syncthreads();
   tc::fence_after_sync();
   if (sm.tmem_base != 0 && tid == 0) report(hdr, CSA2_ERR_CUDA, 4);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const int n = aw_entries(p, b);
-  if (run == 0 && qs == 0 && tid == 0 && p.n_entries[b] > min(p.cap, p.max_n))
+  if (item == (uint32_t)(b * p.runs) && rank == 0 && tid == 0 && p.n_entries[b] > min(p.cap, p.max_n))
     report(hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
-  const int tiles = (n + AW_KEYS - 1) / AW_KEYS;
-  const int t_lo = (int)((int64_t)tiles * run / p.runs), t_n = (int)((int64_t)tiles * (run + 1) / p.runs) - t_lo;
+  const int steps = (n + C::STEP - 1) / C::STEP;
+  const int t_lo = (int)((int64_t)steps * run / p.runs), t_n = (int)((int64_t)steps * (run + 1) / p.runs) - t_lo;
   const int groups = (p.Q + NQ - 1) / NQ;
   const int g_lo = (int)((int64_t)groups * qs / p.splits), ng = (int)((int64_t)groups * (qs + 1) / p.splits) - g_lo;
   // what the run's queries see (AW_GROUPS groups at most); those behind the last query: nothing
@@ -180,27 +195,35 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
   }
   if (most > 0) atomicMax(&sm.most, most);
   __syncthreads();
-  // the tiles that some query sees come first
-  const int live = min(max((sm.most + AW_KEYS - 1) / AW_KEYS - t_lo, 0), t_n);
+  // the steps that some query sees come first
+  const int live = min(max((sm.most + C::STEP - 1) / C::STEP - t_lo, 0), t_n);
   const bool resident = ng == 1;                      // the one group's dims stay in their stages
-  auto next_group = [&](int g, int tile) {            // the first group from g on that sees the tile
-    while (g < ng && max(sm.vis[NQ * g], sm.vis[NQ * g + NQ - 1]) <= tile * AW_KEYS) g++;
+  auto next_group = [&](int g, int step) {            // the first group from g on that sees the step
+    while (g < ng && max(sm.vis[NQ * g], sm.vis[NQ * g + NQ - 1]) <= step * C::STEP) g++;
     return g;
   };
   bool ok = true;                                     // a thread that has given up once waits no more
   auto wait = [&](uint64_t* bar, uint32_t use, int where) {
     if (ok) ok = tc::bar_wait(bar, use & 1u) || aw_timeout(&sm.err, hdr, where);
   };
+  auto arrive_first = [&](uint64_t* bar) {            // on CTA 0's barrier
+    if (PAIR && rank != 0) tc::bar_arrive_first(bar);
+    else tc::bar_arrive(bar);
+  };
 
   if (warp == AW_MMA_WARP) {
-    // ================= MMAs (the whole warp runs the loop, one lane issues)
-    constexpr uint32_t idesc = tc::idesc_f16(AW_KEYS, C::N, 0, 0);
-    const uint64_t q_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
-    const uint32_t leader = tc::elect_one();
+    // ================= MMAs (the whole warp runs the loop, one lane issues; of a pair, in CTA 0)
     // An MMA takes its addresses from uniform registers: what the loops follow from goes through a
     // reduction over the warp, whose result is uniform (else an MMA takes 82 cycles to issue).
-    const int n_live = (int)aw_uniform((uint32_t)live), n_g = (int)aw_uniform((uint32_t)ng);
-    uint32_t u = 0, st = 0, st_use = 0, ab = 0, ab_use = 0;   // group of the CTA; query stage, A buffer and their uses
+    constexpr uint32_t idesc = tc::idesc_f16(NQ * AW_KEYS, C::N, 0, 0);
+    const uint64_t q_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
+    const uint32_t leader = tc::elect_one();
+    const int n_live = rank == 0 ? (int)aw_uniform((uint32_t)live) : 0, n_g = (int)aw_uniform((uint32_t)ng);
+    auto commit = [&](uint64_t* bar) {
+      if (PAIR) tc::commit_pair(leader, bar);
+      else tc::commit_warp(leader, bar);
+    };
+    uint32_t u = 0, ab = 0, ab_use = 0;               // group of the CTA; A buffer and its use
     for (int t = 0; t < n_live; t++) {
       int g = (int)aw_uniform((uint32_t)next_group(0, t_lo + t));
       bool first = true;
@@ -208,7 +231,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
       while (g < n_g) {
         const int after = (int)aw_uniform((uint32_t)next_group(g + 1, t_lo + t));
         if (u >= 2) wait(&sm.s_free[u & 1], (u >> 1) - 1, 60);
-        const uint32_t s = C::S_COL + C::N * (u & 1);
+        const uint32_t s = C::S_COL + C::N * (u & 1), ring = u % C::RING;
         uint32_t k = ab0;
 #pragma unroll 1
         for (int h = 0; h < 2; h++) {
@@ -216,22 +239,27 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
             wait(&sm.a_full[ab], ab_use, 61);
             if (++ab == C::A_BUFS) ab = 0, ab_use++;
           }
-#pragma unroll 1
-          for (int i = 0; i < 4; i++) {
-            if (n_g > 1 || u == 0) wait(&sm.q_full[st], st_use, 62);
-            tc::fence_after_sync();
-            const uint64_t qa = q_d + (uint32_t)(st * C::STAGE >> 4);
-            const uint32_t a = 128 * k + 32 * i;
+          const uint64_t qa = q_d + (uint32_t)((ring * AW_PIECES + 4 * h) * AW_STAGE >> 4);
+          const uint32_t a = 128 * k;
 #pragma unroll
-            for (int x = 0; x < 4; x++)
-              tc::mma_f16_ts_warp(leader, s, a + 8 * x, qa + 2 * x, idesc, (h || i || x) ? 1u : 0u);
-            if (n_g > 1) tc::commit_warp(leader, &sm.q_free[st]);
-            if (++st == AW_STAGES) st = 0, st_use++;
+          for (int i = 0; i < 4; i++) {
+            if (n_g > 1 || u == 0) wait(&sm.q_full[ring][4 * h + i], u / C::RING, 62);
+            if (i == 0 || n_g > 1 || u == 0) tc::fence_after_sync();
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+              if (PAIR)
+                tc::mma_f16_ts_pair(leader, s, a + 32 * i + 8 * x, qa + (uint32_t)((i * AW_STAGE + 32 * x) >> 4), idesc,
+                                    (h || i || x) ? 1u : 0u);
+              else
+                tc::mma_f16_ts_warp(leader, s, a + 32 * i + 8 * x, qa + (uint32_t)((i * AW_STAGE + 32 * x) >> 4), idesc,
+                                    (h || i || x) ? 1u : 0u);
+            }
+            if (n_g > 1) commit(&sm.q_free[ring][4 * h + i]);
           }
-          if (after >= n_g) tc::commit_warp(leader, &sm.a_free[k]);
+          if (after >= n_g) commit(&sm.a_free[k]);
           if (++k == C::A_BUFS) k = 0;
         }
-        tc::commit_warp(leader, &sm.s_full[u & 1]);
+        commit(&sm.s_full[u & 1]);
         u++;
         g = after;
         first = false;
@@ -242,36 +270,39 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     if (lane == 0) {
       for (int t = 0; t < live; t++) {
         const uint32_t ts = t % C::TILES, use = t / C::TILES;
-        const int64_t first = (int64_t)(t_lo + t) * AW_KEYS;
+        const int64_t first = (int64_t)(t_lo + t) * C::STEP + AW_KEYS * rank;
         unsigned char* dst = smem + C::OFF_TILE + ts * C::TILE;
         if (use > 0) wait(&sm.tile_free[ts], use - 1, 63);
         if (E8) {                                     // four column chunks of 128 dims, SW128
           tc::bar_arrive_expect_tx(&sm.tile_full[ts], C::TILE);
           for (int i = 0; i < D / 128; i++)
             tc::tma_load_2d(dst + i * (AW_KEYS * 128), &map_codes, i * 128, (int32_t)(b * p.cap + first), &sm.tile_full[ts]);
-        } else {
-          const uint32_t bytes = (uint32_t)min((int64_t)AW_KEYS, p.cap - first) * MAIN_BYTES;
+        } else {                                      // (none: the pair's second half may lie behind the cache)
+          const uint32_t bytes = (uint32_t)max(min((int64_t)AW_KEYS, p.cap - first), (int64_t)0) * MAIN_BYTES;
           tc::bar_arrive_expect_tx(&sm.tile_full[ts], bytes);
-          tc::bulk_load(dst, p.kv + (b * p.cap + first) * MAIN_BYTES, bytes, &sm.tile_full[ts]);
+          if (bytes > 0) tc::bulk_load(dst, p.kv + (b * p.cap + first) * MAIN_BYTES, bytes, &sm.tile_full[ts]);
         }
       }
     }
     __syncwarp();
   } else if (warp == AW_Q_WARP) {
-    // ================= copies of queries
+    // ================= copies of queries: of a pair each CTA takes one query of a group
     if (lane == 0) {
-      uint32_t u = 0, st = 0, st_use = 0;
+      uint32_t u = 0;
       for (int t = 0; t < (resident ? min(live, 1) : live); t++) {
         for (int g = next_group(0, t_lo + t); g < ng; g = next_group(g + 1, t_lo + t)) {
           const int64_t row = ((int64_t)b * p.Q + (int64_t)(g_lo + g) * NQ) * H;
-          if (u >= 2) wait(&sm.s_free[u & 1], (u >> 1) - 1, 64);
+          const uint32_t ring = u % C::RING;
+          if (u >= 2) wait(&sm.col_free[u & 1], (u >> 1) - 1, 64);
           tc::bar_arrive_expect_tx(&sm.col_full[u & 1], C::N * (uint32_t)sizeof(float2));
           tc::bulk_load(sm.col[u & 1], p.col + row, C::N * (uint32_t)sizeof(float2), &sm.col_full[u & 1]);
-          for (int i = 0; i < AW_STAGES; i++) {
-            if (st_use > 0) wait(&sm.q_free[st], st_use - 1, 65);
-            tc::bar_arrive_expect_tx(&sm.q_full[st], C::STAGE);
-            tc::tma_load_2d(smem + st * C::STAGE, &map_q, i * 64, (int32_t)row, &sm.q_full[st]);
-            if (++st == AW_STAGES) st = 0, st_use++;
+          for (int i = 0; i < AW_PIECES; i++) {
+            unsigned char* dst = smem + (ring * AW_PIECES + i) * AW_STAGE;
+            uint64_t* bar = &sm.q_full[ring][i];
+            if (u >= C::RING) wait(&sm.q_free[ring][i], u / C::RING - 1, 65);
+            if (rank == 0) tc::bar_arrive_expect_tx(bar, NQ * AW_STAGE);
+            if (PAIR) tc::tma_load_2d_pair(dst, &map_q, i * 64, (int32_t)row + H * rank, bar);
+            else tc::tma_load_2d(dst, &map_q, i * 64, (int32_t)row, bar);
           }
           u++;
         }
@@ -324,7 +355,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
       __syncwarp();
       if (lane == 0) {
         tc::bar_arrive(&sm.tile_free[ts]);
-        tc::bar_arrive(&sm.a_full[ab]);
+        arrive_first(&sm.a_full[ab]);
       }
     }
   } else {
@@ -334,12 +365,12 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     const uint32_t addr = ((uint32_t)(32 * (warp & 3)) << 16) + C::S_COL + COLS * half;
     uint32_t u = 0;
     for (int t = 0; t < t_n; t++) {
-      const int tile = t_lo + t, j = tile * AW_KEYS + row;
+      const int j = (t_lo + t) * C::STEP + AW_KEYS * rank + row;
       float acc = 0.f, lost = 0.f;                    // compensated over the queries
       if (t < live) {
         float s8 = 1.f;
         if (E8) s8 = j < n ? __ldcg(p.scales8 + (int64_t)b * (p.cap / BLK) + j / BLK) : 0.f;
-        for (int g = next_group(0, tile); g < ng; g = next_group(g + 1, tile)) {
+        for (int g = next_group(0, t_lo + t); g < ng; g = next_group(g + 1, t_lo + t)) {
           const uint32_t i = u & 1;
           const float4* col = reinterpret_cast<const float4*>(sm.col[resident ? 0 : i] + COLS * half);
           if (resident) {
@@ -365,7 +396,10 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
           tc::fence_before_sync();
           tc::fence_proxy_async_smem();               // reads of the factors done before a copy writes there again
           __syncwarp();
-          if (lane == 0) tc::bar_arrive(&sm.s_free[i]);
+          if (lane == 0) {
+            arrive_first(&sm.s_free[i]);
+            tc::bar_arrive(&sm.col_free[i]);
+          }
           if (j < sm.vis[NQ == 1 ? g : 2 * g + half]) {
             const float y = (s4[0] + s4[1]) + (s4[2] + s4[3]) - lost, z = acc + y;
             lost = (z - acc) - y;
@@ -392,9 +426,12 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
   // after a timeout copies may be in flight that nobody waited for: time for them to land
   if (*(volatile int*)&sm.err != 0)
     for (int i = 0; i < 1000; i++) __nanosleep(1000);
+  // (nothing of the other CTA's is on its way here once both are done)
+  if (PAIR) tc::cluster_sync();
   if (warp == AW_MMA_WARP) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(0u, 512);
+    if (PAIR) tc::tmem_dealloc_pair(0u, 512);
+    else tc::tmem_dealloc(0u, 512);
   }
 }
 
@@ -412,20 +449,21 @@ __global__ void __launch_bounds__(256) attn_weights_join_kernel(AwParams p, int 
 }
 
 // ------------------------------------------------------------------ host side
-// Runs of tiles of a sequence and splits of its queries: the least time on 152 SMs with one CTA each.  In
-// tenths of a us: a CTA costs 50, a tile 8 with one query, else 10 and 11 a group; the join of splits 30.
+// Runs of steps of a sequence and splits of its queries: the least time on 152 SMs with one CTA each.  In
+// tenths of a us: a CTA costs 50, a step 8 with one query, else 10 and 11 a group; the join of splits 30.
 AwPlan attn_weights_plan(int B, int Q, int64_t max_n) {
   AwPlan best{1, 1};
-  const int64_t tiles = ceil_div(max_n, AW_KEYS), groups = Q == 1 ? 1 : ceil_div(Q, 2);
-  if (B <= 0 || Q <= 0 || tiles == 0) return best;
+  const int ctas = Q == 1 ? AW_SMS : AW_SMS / 2;      // or pairs
+  const int64_t steps = ceil_div(max_n, Q == 1 ? AW_KEYS : 2 * AW_KEYS), groups = Q == 1 ? 1 : ceil_div(Q, 2);
+  if (B <= 0 || Q <= 0 || steps == 0) return best;
   int64_t best_cost = INT64_MAX;
   const int64_t least = ceil_div(groups, AW_GROUPS);
   for (int64_t s = least; s <= groups && s < least + 32; s++) {
     for (int waves = 1; waves <= 4; waves++) {
-      int64_t runs = (int64_t)AW_SMS * waves / (B * s);
-      runs = runs < 1 ? 1 : runs > tiles ? tiles : runs;
-      const int64_t per = ceil_div(tiles, runs) * (Q == 1 ? 8 : 10 + 11 * ceil_div(groups, s));
-      const int64_t cost = ceil_div(B * s * runs, AW_SMS) * (50 + per) + (s > 1 ? 30 : 0);
+      int64_t runs = (int64_t)ctas * waves / (B * s);
+      runs = runs < 1 ? 1 : runs > steps ? steps : runs;
+      const int64_t per = ceil_div(steps, runs) * (Q == 1 ? 8 : 10 + 11 * ceil_div(groups, s));
+      const int64_t cost = ceil_div(B * s * runs, ctas) * (50 + per) + (s > 1 ? 30 : 0);
       if (cost < best_cost) {
         best_cost = cost;
         best = {(int)runs, (int)s};
@@ -435,20 +473,27 @@ AwPlan attn_weights_plan(int B, int Q, int64_t max_n) {
   return best;
 }
 
-int64_t attn_weights_pitch(int64_t max_n) { return ceil_div(max_n, AW_KEYS) * AW_KEYS; }
+int64_t attn_weights_pitch(int64_t max_n) { return ceil_div(max_n, AW_KEYS) * AW_KEYS; }   // floats of a sequence's partial sums
 
-template <bool E8, int NQ>
+template <bool E8, bool PAIR>
 static cudaError_t aw_launch(const AwParams& p, const CUtensorMap& mq, const CUtensorMap& mc, cudaLaunchConfig_t cfg) {
-  using C = Aw<E8, NQ>;
+  using C = Aw<E8, PAIR>;
   static PerDeviceOnce attrs;
   cudaError_t e = attrs.ensure([](int) {
-    return cudaFuncSetAttribute(attn_weights_kernel<E8, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    return cudaFuncSetAttribute(attn_weights_kernel<E8, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.runs * p.splits));
+  cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.runs * p.splits * C::NQ));
   cfg.blockDim = dim3(AW_THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
-  return cudaLaunchKernelEx(&cfg, attn_weights_kernel<E8, NQ>, p, mq, mc);
+  cudaLaunchAttribute attr[2];
+  attr[0] = cfg.attrs[0];
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C::NQ;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, attn_weights_kernel<E8, PAIR>, p, mq, mc);
 }
 
 cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream) {
@@ -468,15 +513,15 @@ cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream) {
   if (p.Q > 0) {
     const int64_t rows = (int64_t)p.B * p.Q * H;
     CUtensorMap mq, mc;
-    if (!encode_bf16_rows512(&mq, p.q16, (uint64_t)rows, p.Q == 1 ? 64 : 128)) return cudaErrorInvalidValue;
+    if (!encode_bf16_rows512(&mq, p.q16, (uint64_t)rows, H)) return cudaErrorInvalidValue;
     if (!p.scales8) mc = mq;
     else if (!encode_u8_rows512_sw128(&mc, p.kv, (uint64_t)p.B * p.cap, AW_KEYS)) return cudaErrorInvalidValue;
     cfg.gridDim = dim3((unsigned)(rows / 8));
     cfg.blockDim = dim3(256);
     e = cudaLaunchKernelEx(&cfg, attn_weights_query_kernel, p);
     if (e != cudaSuccess) return e;
-    if (p.scales8) e = p.Q == 1 ? aw_launch<true, 1>(p, mq, mc, cfg) : aw_launch<true, 2>(p, mq, mc, cfg);
-    else e = p.Q == 1 ? aw_launch<false, 1>(p, mq, mc, cfg) : aw_launch<false, 2>(p, mq, mc, cfg);
+    if (p.scales8) e = p.Q == 1 ? aw_launch<true, false>(p, mq, mc, cfg) : aw_launch<true, true>(p, mq, mc, cfg);
+    else e = p.Q == 1 ? aw_launch<false, false>(p, mq, mc, cfg) : aw_launch<false, true>(p, mq, mc, cfg);
     if (e != cudaSuccess || p.splits == 1) return e;
   }
   const int blocks = (int)ceil_div(p.max_n, 256);
