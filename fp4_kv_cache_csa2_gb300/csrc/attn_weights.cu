@@ -61,7 +61,7 @@ struct Aw {
     uint64_t tile_full[TILES], tile_free[TILES];    // TMA; a fill warp each
     // Of a pair CTA 0's a_full, q_full and s_free count, for both; what MMAs complete is told to both.
     uint64_t a_full[A_BUFS], a_free[A_BUFS];        // four fill warps of a CTA; MMAs
-    uint64_t q_full[RING][AW_PIECES], q_free[RING][AW_PIECES];      // TMA; MMAs
+    uint64_t q_full[RING][2], q_free[RING][2];      // half of a group's dims: TMA; MMAs
     uint64_t s_full[2], s_free[2], col_full[2], col_free[2];        // MMAs; sum warps; TMA; sum warps
     uint32_t tmem_base;
     int most, err;
@@ -151,7 +151,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
       tc::bar_init(&sm.a_free[i], 1);
     }
     for (int i = 0; i < C::RING; i++)
-      for (int k = 0; k < AW_PIECES; k++) {
+      for (int k = 0; k < 2; k++) {
         tc::bar_init(&sm.q_full[i][k], 1);
         tc::bar_init(&sm.q_free[i][k], 1);
       }
@@ -219,6 +219,9 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     const uint64_t q_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
     const uint32_t leader = tc::elect_one();
     const int n_live = rank == 0 ? (int)aw_uniform((uint32_t)live) : 0, n_g = (int)aw_uniform((uint32_t)ng);
+    auto wait_mma = [&](uint64_t* bar, uint32_t use, int where) {
+      if (ok) ok = tc::bar_wait_relaxed(bar, use & 1u) || aw_timeout(&sm.err, hdr, where);
+    };
     auto commit = [&](uint64_t* bar) {
       if (PAIR) tc::commit_pair(leader, bar);
       else tc::commit_warp(leader, bar);
@@ -230,21 +233,21 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
       const uint32_t ab0 = ab;
       while (g < n_g) {
         const int after = (int)aw_uniform((uint32_t)next_group(g + 1, t_lo + t));
-        if (u >= 2) wait(&sm.s_free[u & 1], (u >> 1) - 1, 60);
+        if (u >= 2) wait_mma(&sm.s_free[u & 1], (u >> 1) - 1, 60);
         const uint32_t s = C::S_COL + C::N * (u & 1), ring = u % C::RING;
         uint32_t k = ab0;
 #pragma unroll 1
         for (int h = 0; h < 2; h++) {
           if (first) {
-            wait(&sm.a_full[ab], ab_use, 61);
+            wait_mma(&sm.a_full[ab], ab_use, 61);
             if (++ab == C::A_BUFS) ab = 0, ab_use++;
           }
+          if (n_g > 1 || u == 0) wait_mma(&sm.q_full[ring][h], u / C::RING, 62);
+          tc::fence_after_sync();
           const uint64_t qa = q_d + (uint32_t)((ring * AW_PIECES + 4 * h) * AW_STAGE >> 4);
           const uint32_t a = 128 * k;
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            if (n_g > 1 || u == 0) wait(&sm.q_full[ring][4 * h + i], u / C::RING, 62);
-            if (i == 0 || n_g > 1 || u == 0) tc::fence_after_sync();
+          for (int i = 0; i < 4; i++)
 #pragma unroll
             for (int x = 0; x < 4; x++) {
               if (PAIR)
@@ -254,8 +257,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
                 tc::mma_f16_ts_warp(leader, s, a + 32 * i + 8 * x, qa + (uint32_t)((i * AW_STAGE + 32 * x) >> 4), idesc,
                                     (h || i || x) ? 1u : 0u);
             }
-            if (n_g > 1) commit(&sm.q_free[ring][4 * h + i]);
-          }
+          if (n_g > 1) commit(&sm.q_free[ring][h]);
           if (after >= n_g) commit(&sm.a_free[k]);
           if (++k == C::A_BUFS) k = 0;
         }
@@ -298,9 +300,11 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
           tc::bulk_load(sm.col[u & 1], p.col + row, C::N * (uint32_t)sizeof(float2), &sm.col_full[u & 1]);
           for (int i = 0; i < AW_PIECES; i++) {
             unsigned char* dst = smem + (ring * AW_PIECES + i) * AW_STAGE;
-            uint64_t* bar = &sm.q_full[ring][i];
-            if (u >= C::RING) wait(&sm.q_free[ring][i], u / C::RING - 1, 65);
-            if (rank == 0) tc::bar_arrive_expect_tx(bar, NQ * AW_STAGE);
+            uint64_t* bar = &sm.q_full[ring][i >> 2];
+            if ((i & 3) == 0) {
+              if (u >= C::RING) wait(&sm.q_free[ring][i >> 2], u / C::RING - 1, 65);
+              if (rank == 0) tc::bar_arrive_expect_tx(bar, NQ * 4 * AW_STAGE);
+            }
             if (PAIR) tc::tma_load_2d_pair(dst, &map_q, i * 64, (int32_t)row + H * rank, bar);
             else tc::tma_load_2d(dst, &map_q, i * 64, (int32_t)row, bar);
           }
@@ -367,6 +371,8 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     for (int t = 0; t < t_n; t++) {
       const int j = (t_lo + t) * C::STEP + AW_KEYS * rank + row;
       float acc = 0.f, lost = 0.f;                    // compensated over the queries
+      float had = 0.f;                                // loaded ahead of the products it waits for
+      if (half == 0 && p.splits == 1 && p.prev && j < n) had = __ldcg(p.prev + (int64_t)b * p.cap + j);
       if (t < live) {
         float s8 = 1.f;
         if (E8) s8 = j < n ? __ldcg(p.scales8 + (int64_t)b * (p.cap / BLK) + j / BLK) : 0.f;
@@ -415,8 +421,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
         if (p.splits > 1) {
           p.part[((int64_t)qs * p.B + b) * p.pitch + j] = acc;
         } else {
-          const int64_t at = (int64_t)b * p.cap + j;
-          p.out[at] = p.prev ? fmaf(p.decay, p.prev[at], acc) : acc;
+          p.out[(int64_t)b * p.cap + j] = p.prev ? fmaf(p.decay, had, acc) : acc;
         }
       }
     }
