@@ -52,17 +52,19 @@ struct Aw {
   static constexpr int A_BUFS = PAIR ? 2 : 3;             // of 128 columns
   static constexpr int S_COL = 128 * A_BUFS;
   static constexpr int RING = PAIR ? 2 : 1;               // groups of query stages
+  static constexpr int COLS = PAIR ? 4 : 1;               // groups' factors
   static constexpr int OFF_TILE = RING * AW_PIECES * AW_STAGE;
   static constexpr int OFF_SMALL = OFF_TILE + TILES * TILE;
   struct Small {
-    float2 col[2][N];                 // a head's factor, minus its lse, in powers of two
+    float2 col[COLS][N];              // of groups in turn: a head's factor, minus its lse, in powers of two
     float joined[2][AW_KEYS];         // the second half's sums
     int vis[AW_GROUPS * NQ];          // entries each query sees
     uint64_t tile_full[TILES], tile_free[TILES];    // TMA; a fill warp each
     // Of a pair CTA 0's a_full, q_full and s_free count, for both; what MMAs complete is told to both.
     uint64_t a_full[A_BUFS], a_free[A_BUFS];        // four fill warps of a CTA; MMAs
     uint64_t q_full[RING][2], q_free[RING][2];      // half of a group's dims: TMA; MMAs
-    uint64_t s_full[2], s_free[2], col_full[2], col_free[2];        // MMAs; sum warps; TMA; sum warps
+    uint64_t s_full[2], s_free[2];                  // MMAs; sum warps
+    uint64_t col_full[COLS], col_free[COLS];        // TMA; sum warps
     uint32_t tmem_base;
     int most, err;
   };
@@ -158,6 +160,8 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     for (int i = 0; i < 2; i++) {
       tc::bar_init(&sm.s_full[i], 1);
       tc::bar_init(&sm.s_free[i], NQ * AW_SUM_WARPS);
+    }
+    for (int i = 0; i < C::COLS; i++) {
       tc::bar_init(&sm.col_full[i], 1);
       tc::bar_init(&sm.col_free[i], AW_SUM_WARPS);
     }
@@ -228,11 +232,11 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     };
     uint32_t u = 0, ab = 0, ab_use = 0;               // group of the CTA; A buffer and its use
     for (int t = 0; t < n_live; t++) {
-      int g = (int)aw_uniform((uint32_t)next_group(0, t_lo + t));
+      int g = n_g == 1 ? 0 : (int)aw_uniform((uint32_t)next_group(0, t_lo + t));
       bool first = true;
       const uint32_t ab0 = ab;
       while (g < n_g) {
-        const int after = (int)aw_uniform((uint32_t)next_group(g + 1, t_lo + t));
+        const int after = n_g == 1 ? 1 : (int)aw_uniform((uint32_t)next_group(g + 1, t_lo + t));
         if (u >= 2) wait_mma(&sm.s_free[u & 1], (u >> 1) - 1, 60);
         const uint32_t s = C::S_COL + C::N * (u & 1), ring = u % C::RING;
         uint32_t k = ab0;
@@ -295,19 +299,18 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
         for (int g = next_group(0, t_lo + t); g < ng; g = next_group(g + 1, t_lo + t)) {
           const int64_t row = ((int64_t)b * p.Q + (int64_t)(g_lo + g) * NQ) * H;
           const uint32_t ring = u % C::RING;
-          if (u >= 2) wait(&sm.col_free[u & 1], (u >> 1) - 1, 64);
-          tc::bar_arrive_expect_tx(&sm.col_full[u & 1], C::N * (uint32_t)sizeof(float2));
-          tc::bulk_load(sm.col[u & 1], p.col + row, C::N * (uint32_t)sizeof(float2), &sm.col_full[u & 1]);
-          for (int i = 0; i < AW_PIECES; i++) {
-            unsigned char* dst = smem + (ring * AW_PIECES + i) * AW_STAGE;
-            uint64_t* bar = &sm.q_full[ring][i >> 2];
-            if ((i & 3) == 0) {
-              if (u >= C::RING) wait(&sm.q_free[ring][i >> 2], u / C::RING - 1, 65);
-              if (rank == 0) tc::bar_arrive_expect_tx(bar, NQ * 4 * AW_STAGE);
-            }
-            if (PAIR) tc::tma_load_2d_pair(dst, &map_q, i * 64, (int32_t)row + H * rank, bar);
-            else tc::tma_load_2d(dst, &map_q, i * 64, (int32_t)row, bar);
+          for (int h = 0; h < 2; h++) {
+            unsigned char* dst = smem + (ring * AW_PIECES + 4 * h) * AW_STAGE;
+            uint64_t* bar = &sm.q_full[ring][h];
+            if (u >= C::RING) wait(&sm.q_free[ring][h], u / C::RING - 1, 65);
+            if (rank == 0) tc::bar_arrive_expect_tx(bar, NQ * 4 * AW_STAGE);
+            if (PAIR) tc::tma_load_3d_pair(dst, &map_q, 0, (int32_t)row + H * rank, 4 * h, bar);
+            else tc::tma_load_3d(dst, &map_q, 0, (int32_t)row, 4 * h, bar);
           }
+          const uint32_t ci = u % C::COLS;
+          if (u >= C::COLS) wait(&sm.col_free[ci], u / C::COLS - 1, 64);
+          tc::bar_arrive_expect_tx(&sm.col_full[ci], C::N * (uint32_t)sizeof(float2));
+          tc::bulk_load(sm.col[ci], p.col + row, C::N * (uint32_t)sizeof(float2), &sm.col_full[ci]);
           u++;
         }
       }
@@ -378,12 +381,9 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
         if (E8) s8 = j < n ? __ldcg(p.scales8 + (int64_t)b * (p.cap / BLK) + j / BLK) : 0.f;
         for (int g = next_group(0, t_lo + t); g < ng; g = next_group(g + 1, t_lo + t)) {
           const uint32_t i = u & 1;
-          const float4* col = reinterpret_cast<const float4*>(sm.col[resident ? 0 : i] + COLS * half);
-          if (resident) {
-            if (u == 0) wait(&sm.col_full[0], 0, 68);
-          } else {
-            wait(&sm.col_full[i], u >> 1, 68);
-          }
+          const uint32_t ci = resident ? 0 : u % C::COLS;
+          const float4* col = reinterpret_cast<const float4*>(sm.col[ci] + COLS * half);
+          if (!resident || u == 0) wait(&sm.col_full[ci], u / C::COLS, 68);
           wait(&sm.s_full[i], u >> 1, 69);
           tc::fence_after_sync();
           float s4[4] = {0.f, 0.f, 0.f, 0.f};
@@ -404,7 +404,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
           __syncwarp();
           if (lane == 0) {
             arrive_first(&sm.s_free[i]);
-            tc::bar_arrive(&sm.col_free[i]);
+            tc::bar_arrive(&sm.col_free[ci]);
           }
           if (j < sm.vis[NQ == 1 ? g : 2 * g + half]) {
             const float y = (s4[0] + s4[1]) + (s4[2] + s4[3]) - lost, z = acc + y;
@@ -480,6 +480,20 @@ AwPlan attn_weights_plan(int B, int Q, int64_t max_n) {
 
 int64_t attn_weights_pitch(int64_t max_n) { return ceil_div(max_n, AW_KEYS) * AW_KEYS; }   // floats of a sequence's partial sums
 
+// f16 matrix [rows][512] with SW128 boxes of 64 rows x 4 column chunks of 64: half of a query's dims in one
+// copy (one copy a chunk: a thread issues them at 200 cycles each).
+static bool encode_f16_halves(CUtensorMap* map, const void* base, uint64_t rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {64, rows, D / 64};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
+  cuuint32_t box[3] = {64, H, 4};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool E8, bool PAIR>
 static cudaError_t aw_launch(const AwParams& p, const CUtensorMap& mq, const CUtensorMap& mc, cudaLaunchConfig_t cfg) {
   using C = Aw<E8, PAIR>;
@@ -518,7 +532,7 @@ cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream) {
   if (p.Q > 0) {
     const int64_t rows = (int64_t)p.B * p.Q * H;
     CUtensorMap mq, mc;
-    if (!encode_bf16_rows512(&mq, p.q16, (uint64_t)rows, H)) return cudaErrorInvalidValue;
+    if (!encode_f16_halves(&mq, p.q16, (uint64_t)rows)) return cudaErrorInvalidValue;
     if (!p.scales8) mc = mq;
     else if (!encode_u8_rows512_sw128(&mc, p.kv, (uint64_t)p.B * p.cap, AW_KEYS)) return cudaErrorInvalidValue;
     cfg.gridDim = dim3((unsigned)(rows / 8));
