@@ -70,6 +70,16 @@ __device__ __forceinline__ void i8x16_to_f16(const uint4& c, uint32_t* o) {
   }
 }
 
+// The same -> eight bf16x2 words, exactly: b is 128 + (b & 127) less 128, or less 256 when b is negative.
+__device__ __forceinline__ void i8x16_to_bf16(const uint4& c, uint32_t* o) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const uint32_t u = prmt(w[i >> 1], 0x43434343u, i & 1 ? 0x4342u : 0x4140u);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(u & 0xFF7FFF7Fu), "r"(u & 0xFF80FF80u));
+  }
+}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));

@@ -7,23 +7,24 @@
 // over heads and queries stays in its registers: no exchange between lanes, no
 // atomics, the same result every time.
 //
-// A small kernel first writes the queries as f16 (a head that reaches 2^16 scaled into f16's
-// range by a power of two) and for each head its factor and its lse in powers of two.
-// The entries are exact in f16 (FP4 values; 8-bit codes, whose scale is the thread's
-// own factor), as in keys_attention.cu.  Sums: 64 weights in binary32, then compensated over a
-// CTA's queries.
+// Sums: 64 weights in binary32, then compensated over a CTA's queries.
 //
 // A CTA takes a run of tiles of one sequence.  The tile's entries lie in TMEM as the A operand
-// (256 columns of f16 pairs): with A in shared memory a product of N = 64 would take 48
+// (256 columns of 16-bit pairs): with A in shared memory a product of N = 64 would take 48
 // cycles instead of 32, and the widened tile 128 KB.  Two S accumulators.
-// One query (N = 64): its dims stay in shared memory.  More: two CTAs make a pair
-// (cta_group::2) that takes 256 entries, a half each, and a run of groups of two queries (N = 128);
-// each CTA loads one query of a group through a ring of stages, and the pair's products read
-// both.  With single CTAs of two queries every SM took 128 KB of queries from L2 for
-// 2048 cycles of products and waited for them: 4180 cycles a group.
+// One query (N = 64): a CTA rounds it to f16 (a head that reaches 2^16 scaled into f16's range
+// by a power of two) and keeps it in shared memory; the entries are exact in f16, the cheapest to
+// widen to.  More: two CTAs make a pair (cta_group::2) that takes 256 entries, a half each, and a run
+// of groups of two queries (N = 128); each CTA loads one query of a group through a ring of stages,
+// and the pair's products read both.  Operands are bf16, in which q is as it came and entries are exact
+// too (at most 8 significant bits).  With single CTAs of two queries every SM took 128 KB of queries
+// from L2 for 2048 cycles of products and waited for them: 4180 cycles a group.
+// An 8-bit entry's scale is a factor of the thread that has it.
+//
 // Warps 0..7: exponentials and sums (warps 4..7: the second query, or the second half of the heads);
-// 8..15: entries to TMEM, a half of the dims each four; 16: MMAs; 17: copies of entries; 18: copies of
-// queries.  All waits are bounded; a timeout reports CSA2_ERR_TIMEOUT.
+// 8..15: entries to TMEM, a half of the dims each four; 16: MMAs; 17: every second tile's MMAs (one
+// query: a warp issues one in about 40 cycles), or the lse of a group's heads; 18: copies of entries;
+// 19: copies of queries.  All waits are bounded; a timeout reports CSA2_ERR_TIMEOUT.
 #include <cfloat>
 
 #include "attn_common.cuh"
@@ -33,7 +34,8 @@ namespace csa2 {
 
 constexpr int AW_KEYS = 128;                              // entries of a tile
 constexpr int AW_SUM_WARPS = 8, AW_FILL_WARPS = 8;
-constexpr int AW_MMA_WARP = AW_SUM_WARPS + AW_FILL_WARPS, AW_KEY_WARP = AW_MMA_WARP + 1, AW_Q_WARP = AW_KEY_WARP + 1;
+constexpr int AW_MMA_WARP = AW_SUM_WARPS + AW_FILL_WARPS, AW_MMA2_WARP = AW_MMA_WARP + 1;
+constexpr int AW_KEY_WARP = AW_MMA2_WARP + 1, AW_Q_WARP = AW_KEY_WARP + 1;
 constexpr int AW_THREADS = 32 * (AW_Q_WARP + 1);
 constexpr int AW_PIECES = 8;                              // of 64 dims of a query
 constexpr int AW_STAGE = 64 * 128;                        // [64 heads][64 dims] f16, SW128
@@ -56,15 +58,17 @@ struct Aw {
   static constexpr int OFF_TILE = RING * AW_PIECES * AW_STAGE;
   static constexpr int OFF_SMALL = OFF_TILE + TILES * TILE;
   struct Small {
-    float2 col[COLS][N];              // of groups in turn: a head's factor, minus its lse, in powers of two
+    // A head's factor and minus its lse in powers of two; of a pair, groups in turn, minus the lse and what the
+    // exponent is cut to (infinity, or minus infinity for a head that saw nothing)
+    float2 col[COLS][N];
     float joined[2][AW_KEYS];         // the second half's sums
     int vis[AW_GROUPS * NQ];          // entries each query sees
     uint64_t tile_full[TILES], tile_free[TILES];    // TMA; a fill warp each
     // Of a pair CTA 0's a_full, q_full and s_free count, for both; what MMAs complete is told to both.
     uint64_t a_full[A_BUFS], a_free[A_BUFS];        // four fill warps of a CTA; MMAs
-    uint64_t q_full[RING][2], q_free[RING][2];      // half of a group's dims: TMA; MMAs
+    uint64_t q_full[RING][2], q_free[RING][2];      // half of a group's dims: TMA (one query: the sum warps); MMAs
     uint64_t s_full[2], s_free[2];                  // MMAs; sum warps
-    uint64_t col_full[COLS], col_free[COLS];        // TMA; sum warps
+    uint64_t col_full[COLS], col_free[COLS];        // warp 17; sum warps
     uint32_t tmem_base;
     int most, err;
   };
@@ -85,20 +89,14 @@ __device__ __forceinline__ int aw_entries(const AwParams& p, int b) {
   return (int)max((int64_t)0, min((int64_t)p.n_entries[b], min(p.cap, p.max_n)));
 }
 
-// A warp a head: q as f16, the head's factor and its lse in powers of two.
-__global__ void __launch_bounds__(256) attn_weights_query_kernel(AwParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), bq = row / H;
-  const uint4* in = reinterpret_cast<const uint4*>(p.q + row * D);
-  uint4* out = reinterpret_cast<uint4*>(p.q16 + row * D);
-  const float lse = p.lse[row];
-  if (p.q_pos[bq] < 0 || lse == -INFINITY) {          // sees nothing: weights of 0, whatever q holds
-    out[lane] = out[32 + lane] = make_uint4(0u, 0u, 0u, 0u);
-    if (lane == 0) p.col[row] = make_float2(0.f, -INFINITY);
-    return;
+// One head by a warp: q as f16 into its row of the stages, its factor and its lse in powers of two.
+__device__ __forceinline__ float2 aw_head(const uint16_t* q, float lse, float scale, bool live, unsigned char* stages, int row, int lane) {
+  uint4 v[2] = {};
+  live = live && lse > -INFINITY;                     // else weights of 0, whatever q holds
+  if (live) {
+    v[0] = __ldcg(reinterpret_cast<const uint4*>(q) + lane);
+    v[1] = __ldcg(reinterpret_cast<const uint4*>(q) + 32 + lane);
   }
-  const uint4 v[2] = {__ldcs(in + lane), __ldcs(in + 32 + lane)};
   const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
   uint32_t most = 0u;
 #pragma unroll
@@ -111,12 +109,19 @@ __global__ void __launch_bounds__(256) attn_weights_query_kernel(AwParams p) {
 #pragma unroll
   for (int i = 0; i < 8; i++)
     o[i] = pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
-  out[lane] = make_uint4(o[0], o[1], o[2], o[3]);
-  out[32 + lane] = make_uint4(o[4], o[5], o[6], o[7]);
-  if (lane == 0) {
-    const float by = p.scale * AW_LOG2E * __int_as_float((127 + e) << 23);
-    p.col[row] = make_float2(fmaxf(fminf(by, FLT_MAX), -FLT_MAX), -lse * AW_LOG2E);   // finite: a product may be 0
-  }
+  // dims 8 lane .. and 256 + 8 lane ..
+  unsigned char* dst = stages + (lane >> 3) * AW_STAGE + sw128((uint32_t)row, 16u * (lane & 7));
+  *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(dst + 4 * AW_STAGE) = make_uint4(o[4], o[5], o[6], o[7]);
+  if (!live) return make_float2(0.f, -INFINITY);
+  const float by = scale * AW_LOG2E * __int_as_float((127 + e) << 23);
+  return make_float2(fmaxf(fminf(by, FLT_MAX), -FLT_MAX), -lse * AW_LOG2E);   // finite: a product may be 0
+}
+
+// two f16 -> two bf16, exact for an entry's values
+__device__ __forceinline__ uint32_t aw_f16x2_to_bf16x2(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_bf16x2(f.x, f.y);
 }
 
 template <bool E8, bool PAIR>
@@ -154,7 +159,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     }
     for (int i = 0; i < C::RING; i++)
       for (int k = 0; k < 2; k++) {
-        tc::bar_init(&sm.q_full[i][k], 1);
+        tc::bar_init(&sm.q_full[i][k], PAIR ? 1 : AW_SUM_WARPS);
         tc::bar_init(&sm.q_free[i][k], 1);
       }
     for (int i = 0; i < 2; i++) {
@@ -215,11 +220,11 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     else tc::bar_arrive(bar);
   };
 
-  if (warp == AW_MMA_WARP) {
+  if (warp == AW_MMA_WARP || (!PAIR && warp == AW_MMA2_WARP)) {
     // ================= MMAs (the whole warp runs the loop, one lane issues; of a pair, in CTA 0)
     // An MMA takes its addresses from uniform registers: what the loops follow from goes through a
     // reduction over the warp, whose result is uniform (else an MMA takes 82 cycles to issue).
-    constexpr uint32_t idesc = tc::idesc_f16(NQ * AW_KEYS, C::N, 0, 0);
+    constexpr uint32_t idesc = PAIR ? tc::idesc_bf16(NQ * AW_KEYS, C::N, 0, 0) : tc::idesc_f16(NQ * AW_KEYS, C::N, 0, 0);
     const uint64_t q_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
     const uint32_t leader = tc::elect_one();
     const int n_live = rank == 0 ? (int)aw_uniform((uint32_t)live) : 0, n_g = (int)aw_uniform((uint32_t)ng);
@@ -230,45 +235,82 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
       if (PAIR) tc::commit_pair(leader, bar);
       else tc::commit_warp(leader, bar);
     };
-    uint32_t u = 0, ab = 0, ab_use = 0;               // group of the CTA; A buffer and its use
-    for (int t = 0; t < n_live; t++) {
-      int g = n_g == 1 ? 0 : (int)aw_uniform((uint32_t)next_group(0, t_lo + t));
-      bool first = true;
-      const uint32_t ab0 = ab;
-      while (g < n_g) {
-        const int after = n_g == 1 ? 1 : (int)aw_uniform((uint32_t)next_group(g + 1, t_lo + t));
-        if (u >= 2) wait_mma(&sm.s_free[u & 1], (u >> 1) - 1, 60);
-        const uint32_t s = C::S_COL + C::N * (u & 1), ring = u % C::RING;
-        uint32_t k = ab0;
+    // S number i += the half h of the dims, A buffer k times the queries of ring place `ring`
+    auto products = [&](uint32_t i, int h, uint32_t k, uint32_t ring) {
+      tc::fence_after_sync();
+      const uint64_t qa = q_d + (uint32_t)((ring * AW_PIECES + 4 * h) * AW_STAGE >> 4);
+      const uint32_t s = C::S_COL + C::N * i, a = 128 * k;
+#pragma unroll
+      for (int x = 0; x < 16; x++) {
+        const uint64_t qx = qa + (uint32_t)(((x >> 2) * AW_STAGE + 32 * (x & 3)) >> 4);
+        if (PAIR) tc::mma_f16_ts_pair(leader, s, a + 8 * x, qx, idesc, (h || x) ? 1u : 0u);
+        else tc::mma_f16_ts_warp(leader, s, a + 8 * x, qx, idesc, (h || x) ? 1u : 0u);
+      }
+    };
+    if (!PAIR) {
+      // tiles in turn with the other warp
+      const uint32_t mine = warp == AW_MMA2_WARP ? 1u : 0u;
+      if (n_live > (int)mine)
+        for (int h = 0; h < 2; h++) wait_mma(&sm.q_full[0][h], 0, 62);
+      uint32_t ab = 2 * mine, ab_use = 0;             // A buffer and its use: 2 t % 3, 2 t / 3
+      for (uint32_t t = mine; t < (uint32_t)n_live; t += 2) {
+        if (t >= 2) wait_mma(&sm.s_free[mine], (t >> 1) - 1, 60);
 #pragma unroll 1
         for (int h = 0; h < 2; h++) {
-          if (first) {
-            wait_mma(&sm.a_full[ab], ab_use, 61);
-            if (++ab == C::A_BUFS) ab = 0, ab_use++;
-          }
-          if (n_g > 1 || u == 0) wait_mma(&sm.q_full[ring][h], u / C::RING, 62);
-          tc::fence_after_sync();
-          const uint64_t qa = q_d + (uint32_t)((ring * AW_PIECES + 4 * h) * AW_STAGE >> 4);
-          const uint32_t a = 128 * k;
-#pragma unroll
-          for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int x = 0; x < 4; x++) {
-              if (PAIR)
-                tc::mma_f16_ts_pair(leader, s, a + 32 * i + 8 * x, qa + (uint32_t)((i * AW_STAGE + 32 * x) >> 4), idesc,
-                                    (h || i || x) ? 1u : 0u);
-              else
-                tc::mma_f16_ts_warp(leader, s, a + 32 * i + 8 * x, qa + (uint32_t)((i * AW_STAGE + 32 * x) >> 4), idesc,
-                                    (h || i || x) ? 1u : 0u);
-            }
-          if (n_g > 1) commit(&sm.q_free[ring][h]);
-          if (after >= n_g) commit(&sm.a_free[k]);
-          if (++k == C::A_BUFS) k = 0;
+          wait_mma(&sm.a_full[ab], ab_use, 61);
+          products(mine, h, ab, 0);
+          commit(&sm.a_free[ab]);
+          if (++ab == C::A_BUFS) ab = 0, ab_use++;
         }
-        commit(&sm.s_full[u & 1]);
+        commit(&sm.s_full[mine]);
+        ab += 2;                                      // the other warp's two
+        if (ab >= C::A_BUFS) ab -= C::A_BUFS, ab_use++;
+      }
+    } else {
+      uint32_t u = 0;                                 // group of the CTA
+      for (int t = 0; t < n_live; t++) {              // A buffer = half of the dims
+        int g = (int)aw_uniform((uint32_t)next_group(0, t_lo + t));
+        bool first = true;
+        while (g < n_g) {
+          const int after = (int)aw_uniform((uint32_t)next_group(g + 1, t_lo + t));
+          if (u >= 2) wait_mma(&sm.s_free[u & 1], (u >> 1) - 1, 60);
+          const uint32_t ring = u % C::RING;
+#pragma unroll 1
+          for (int h = 0; h < 2; h++) {
+            if (first) wait_mma(&sm.a_full[h], t, 61);
+            if (n_g > 1 || u == 0) wait_mma(&sm.q_full[ring][h], u / C::RING, 62);
+            products(u & 1, h, h, ring);
+            if (n_g > 1) commit(&sm.q_free[ring][h]);
+            if (after >= n_g) commit(&sm.a_free[h]);
+          }
+          commit(&sm.s_full[u & 1]);
+          u++;
+          g = after;
+          first = false;
+        }
+      }
+    }
+  } else if (PAIR && warp == AW_MMA2_WARP) {
+    // ================= the lse of a group's heads
+    uint32_t u = 0;
+    for (int t = 0; t < (resident ? min(live, 1) : live); t++) {
+      for (int g = next_group(0, t_lo + t); g < ng; g = next_group(g + 1, t_lo + t)) {
+        float l[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {                 // (sequences are a query's 64 heads apart: none behind the last query)
+          const int64_t q = (int64_t)(g_lo + g) * NQ + (i >> 1);
+          l[i] = q < p.Q ? __ldcg(p.lse + ((int64_t)b * p.Q + q) * H + 32 * (i & 1) + lane) : -INFINITY;
+        }
+        const uint32_t ci = u % C::COLS;
+        if (u >= C::COLS) wait(&sm.col_free[ci], u / C::COLS - 1, 64);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          sm.col[ci][32 * i + lane] = l[i] > -INFINITY ? make_float2(-l[i] * AW_LOG2E, INFINITY)
+                                      : l[i] == -INFINITY ? make_float2(0.f, -INFINITY)
+                                                          : make_float2(l[i], INFINITY);   // NaN
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sm.col_full[ci]);
         u++;
-        g = after;
-        first = false;
       }
     }
   } else if (warp == AW_KEY_WARP) {
@@ -292,8 +334,8 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     }
     __syncwarp();
   } else if (warp == AW_Q_WARP) {
-    // ================= copies of queries: of a pair each CTA takes one query of a group
-    if (lane == 0) {
+    // ================= copies of queries: each CTA of a pair takes one query of a group
+    if (PAIR && lane == 0) {
       uint32_t u = 0;
       for (int t = 0; t < (resident ? min(live, 1) : live); t++) {
         for (int g = next_group(0, t_lo + t); g < ng; g = next_group(g + 1, t_lo + t)) {
@@ -304,13 +346,8 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
             uint64_t* bar = &sm.q_full[ring][h];
             if (u >= C::RING) wait(&sm.q_free[ring][h], u / C::RING - 1, 65);
             if (rank == 0) tc::bar_arrive_expect_tx(bar, NQ * 4 * AW_STAGE);
-            if (PAIR) tc::tma_load_3d_pair(dst, &map_q, 0, (int32_t)row + H * rank, 4 * h, bar);
-            else tc::tma_load_3d(dst, &map_q, 0, (int32_t)row, 4 * h, bar);
+            tc::tma_load_3d_pair(dst, &map_q, 0, (int32_t)row + H * rank, 4 * h, bar);
           }
-          const uint32_t ci = u % C::COLS;
-          if (u >= C::COLS) wait(&sm.col_free[ci], u / C::COLS - 1, 64);
-          tc::bar_arrive_expect_tx(&sm.col_full[ci], C::N * (uint32_t)sizeof(float2));
-          tc::bulk_load(sm.col[ci], p.col + row, C::N * (uint32_t)sizeof(float2), &sm.col_full[ci]);
           u++;
         }
       }
@@ -334,10 +371,12 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
         uint32_t o[32];
         if (E8) {
 #pragma unroll
-          for (int x = 0; x < 4; x++)
-            i8x16_to_f16(*reinterpret_cast<const uint4*>(tile + (2 * h + (i >> 1)) * (AW_KEYS * 128) +
-                                                         sw128((uint32_t)row, 16u * (4 * (i & 1) + x))),
-                         o + 8 * x);
+          for (int x = 0; x < 4; x++) {
+            const uint4 c = *reinterpret_cast<const uint4*>(tile + (2 * h + (i >> 1)) * (AW_KEYS * 128) +
+                                                            sw128((uint32_t)row, 16u * (4 * (i & 1) + x)));
+            if (PAIR) i8x16_to_bf16(c, o + 8 * x);
+            else i8x16_to_f16(c, o + 8 * x);
+          }
         } else {
           // rows are 18 units of 16 bytes: of the eight lanes of a phase four take their two units in the
           // other order, so that they lie in eight bank groups
@@ -351,7 +390,10 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
             e2m1x8_to_f16(w[x], o + 4 * x);
             const uint32_t s2 = e4m3x2_to_f16x2(prmt(scw[i], 0u, 0x1111u * (x >> 1)));
 #pragma unroll
-            for (int y = 0; y < 4; y++) o[4 * x + y] = hmul2(o[4 * x + y], s2);
+            for (int y = 0; y < 4; y++) {
+              o[4 * x + y] = hmul2(o[4 * x + y], s2);
+              if (PAIR) o[4 * x + y] = aw_f16x2_to_bf16x2(o[4 * x + y]);
+            }
           }
         }
         tmem_st32(quarter + 128 * ab + 32 * i, o);
@@ -370,6 +412,20 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     const int half = warp >> 2, row = 32 * (warp & 3) + lane;
     constexpr int COLS = C::N / 2;
     const uint32_t addr = ((uint32_t)(32 * (warp & 3)) << 16) + C::S_COL + COLS * half;
+    if (!PAIR && live > 0) {                          // the query: eight heads a warp
+      for (int i = 0; i < H / AW_SUM_WARPS; i++) {
+        const int head = (H / AW_SUM_WARPS) * warp + i;
+        const float2 c = aw_head(p.q + ((int64_t)b * H + head) * D, __ldcg(p.lse + (int64_t)b * H + head), p.scale, sm.vis[0] > 0,
+                                 smem, head, lane);
+        if (lane == 0) sm.col[0][head] = c;
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0)
+        for (int h = 0; h < 2; h++) tc::bar_arrive(&sm.q_full[0][h]);
+      named_sync(1, 32 * AW_SUM_WARPS);               // the factors
+    }
+    const float by0 = p.scale * AW_LOG2E;
     uint32_t u = 0;
     for (int t = 0; t < t_n; t++) {
       const int j = (t_lo + t) * C::STEP + AW_KEYS * rank + row;
@@ -379,11 +435,12 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
       if (t < live) {
         float s8 = 1.f;
         if (E8) s8 = j < n ? __ldcg(p.scales8 + (int64_t)b * (p.cap / BLK) + j / BLK) : 0.f;
+        const float by = by0 * s8;                    // (of a pair: one query's heads have their own)
         for (int g = next_group(0, t_lo + t); g < ng; g = next_group(g + 1, t_lo + t)) {
           const uint32_t i = u & 1;
           const uint32_t ci = resident ? 0 : u % C::COLS;
           const float4* col = reinterpret_cast<const float4*>(sm.col[ci] + COLS * half);
-          if (!resident || u == 0) wait(&sm.col_full[ci], u / C::COLS, 68);
+          if (PAIR && (!resident || u == 0)) wait(&sm.col_full[ci], u / C::COLS, 68);
           wait(&sm.s_full[i], u >> 1, 69);
           tc::fence_after_sync();
           float s4[4] = {0.f, 0.f, 0.f, 0.f};
@@ -395,8 +452,13 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
             for (int x = 0; x < 32; x += 2) {
               const float4 f = col[(c + x) / 2];
               const float v0 = __uint_as_float(r[x]), v1 = __uint_as_float(r[x + 1]);
-              s4[x & 2] += ex2_ftz(fmaf(E8 ? v0 * s8 : v0, f.x, f.y));
-              s4[(x & 2) + 1] += ex2_ftz(fmaf(E8 ? v1 * s8 : v1, f.z, f.w));
+              if (PAIR) {
+                s4[x & 2] += ex2_ftz(fminf(fmaf(v0, by, f.x), f.y));
+                s4[(x & 2) + 1] += ex2_ftz(fminf(fmaf(v1, by, f.z), f.w));
+              } else {
+                s4[x & 2] += ex2_ftz(fmaf(E8 ? v0 * s8 : v0, f.x, f.y));
+                s4[(x & 2) + 1] += ex2_ftz(fmaf(E8 ? v1 * s8 : v1, f.z, f.w));
+              }
             }
           }
           tc::fence_before_sync();
@@ -480,16 +542,16 @@ AwPlan attn_weights_plan(int B, int Q, int64_t max_n) {
 
 int64_t attn_weights_pitch(int64_t max_n) { return ceil_div(max_n, AW_KEYS) * AW_KEYS; }   // floats of a sequence's partial sums
 
-// f16 matrix [rows][512] with SW128 boxes of 64 rows x 4 column chunks of 64: half of a query's dims in one
+// bf16 matrix [rows][512] with SW128 boxes of 64 rows x 4 column chunks of 64: half of a query's dims in one
 // copy (one copy a chunk: a thread issues them at 200 cycles each).
-static bool encode_f16_halves(CUtensorMap* map, const void* base, uint64_t rows) {
+static bool encode_query_halves(CUtensorMap* map, const void* base, uint64_t rows) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[3] = {64, rows, D / 64};
   cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
   cuuint32_t box[3] = {64, H, 4};
   cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -530,15 +592,10 @@ cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaSuccess;
   if (p.Q > 0) {
-    const int64_t rows = (int64_t)p.B * p.Q * H;
     CUtensorMap mq, mc;
-    if (!encode_f16_halves(&mq, p.q16, (uint64_t)rows)) return cudaErrorInvalidValue;
+    if (!encode_query_halves(&mq, p.q, (uint64_t)p.B * p.Q * H)) return cudaErrorInvalidValue;
     if (!p.scales8) mc = mq;
     else if (!encode_u8_rows512_sw128(&mc, p.kv, (uint64_t)p.B * p.cap, AW_KEYS)) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3((unsigned)(rows / 8));
-    cfg.blockDim = dim3(256);
-    e = cudaLaunchKernelEx(&cfg, attn_weights_query_kernel, p);
-    if (e != cudaSuccess) return e;
     if (p.scales8) e = p.Q == 1 ? aw_launch<true, false>(p, mq, mc, cfg) : aw_launch<true, true>(p, mq, mc, cfg);
     else e = p.Q == 1 ? aw_launch<false, false>(p, mq, mc, cfg) : aw_launch<false, true>(p, mq, mc, cfg);
     if (e != cudaSuccess || p.splits == 1) return e;

@@ -582,10 +582,9 @@ static int64_t weights_n(int64_t max_n) { return max_n < INT32_MAX ? max_n : INT
 
 size_t csa2_attn_weights_workspace_size(int B, int Q, int64_t max_n) {
   if (B < 0 || Q < 0 || max_n < 0 || (int64_t)B * Q > MAX_KEY_QUERIES) return 0;
-  const int64_t n = weights_n(max_n), BQ = (int64_t)B * Q;
+  const int64_t n = weights_n(max_n);
   const AwPlan plan = attn_weights_plan(B, Q, n);
-  return HDR + align256((size_t)BQ * H * D * 2) + align256((size_t)(BQ + 1) * H * sizeof(float2)) +
-         (plan.splits > 1 ? align256((size_t)plan.splits * B * attn_weights_pitch(n) * sizeof(float)) : 0);
+  return HDR + (plan.splits > 1 ? align256((size_t)plan.splits * B * attn_weights_pitch(n) * sizeof(float)) : 0);
 }
 
 // p: the cache's part, filled in; entry: bytes of one of its entries
@@ -617,12 +616,7 @@ static csa2_status do_attn_weights(AwParams p, int64_t entry, const csa2_weights
   p.Q = a->Q;
   p.max_n = weights_n(a->max_n);
   p.hdr = header(ws);
-  unsigned char* cur = scratch(ws);
-  p.q16 = reinterpret_cast<uint16_t*>(cur);
-  cur += align256((size_t)BQ * H * D * 2);
-  p.col = reinterpret_cast<float2*>(cur);
-  cur += align256((size_t)(BQ + 1) * H * sizeof(float2));
-  p.part = reinterpret_cast<float*>(cur);
+  p.part = reinterpret_cast<float*>(scratch(ws));
   return from_cuda(launch_attn_weights(p, (cudaStream_t)stream));
 }
 

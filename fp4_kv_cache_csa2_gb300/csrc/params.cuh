@@ -159,8 +159,6 @@ struct AwParams {             // attention weight that entries gather
   float* out;                 // [B][cap]
   int B, Q;
   int64_t max_n;
-  uint16_t* q16;              // scratch: [BQ][64][512] f16
-  float2* col;                // scratch: [BQ + 1][64]
   float* part;                // splits > 1: [splits][B][pitch]
   int64_t pitch;              // set by the launcher, as the next two
   int runs, splits;

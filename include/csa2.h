@@ -602,10 +602,11 @@ csa2_status csa2_cache8_attn(const csa2_cache8 *cache, const csa2_cache8_attn_ar
  * Q = 0 scales what was gathered.  B * Q <= 2^24; 4-bit and 8-bit cache
  * (csa2_cache8_attn_weights).  q and the cache 16-byte, q_pos 8-byte, the others
  * 4-byte aligned; weights must not overlap an input other than prev.
- * Precision: f16 operands as in csa2_dense_attn (entries exact, q rounded to f16,
- * of any size), binary32 products and sums, compensated over queries; the same
- * inputs give the same bits.  Workspace: csa2_attn_weights_workspace_size with the
- * call's B, Q and max_n (64 KB a query).
+ * Precision: entries are exact operands; one query (Q = 1) is rounded to f16 as in
+ * csa2_dense_attn (of any size), several are taken as they are in bf16.
+ * Binary32 products and sums, compensated over queries; the same inputs
+ * give the same bits.  Workspace: csa2_attn_weights_workspace_size with the
+ * call's B, Q and max_n (partial sums when the queries are divided over CTAs).
  */
 typedef struct {
     int B, Q;                   /* sequences, queries per sequence              */
