@@ -26,20 +26,20 @@
 
 namespace csa2 {
 
-constexpr int EV_THREADS = 1024, EV_BINS = 2048;
+constexpr int EV_BINS = 2048;
 constexpr int EV_COARSE = 32, EV_FINE = EV_BINS / EV_COARSE;   // a pass finds its bin in two steps
 constexpr int EV_KEYS = 48 * 1024;                        // of a slice that are kept in shared memory at most
 constexpr uint32_t EV_FORCED = 0xFFFFFFFFu;
 constexpr int EV_MOVE_THREADS = 256, EV_MOVE_BYTES = 96 * 1024;
 constexpr int EV_ZEROS = 16384;                           // weights behind the last that a CTA clears
 
-template <int CLUSTER>
+template <int CLUSTER, int THREADS>
 struct EvSelect {
   int hist[2][EV_BINS];               // of a pass, in turn
   int coarse[2][EV_COARSE];           // its sums over EV_FINE bins
   int all_coarse[CLUSTER][EV_COARSE]; // of every CTA
   int all_fine[CLUSTER][EV_FINE];     // the bins of the chosen coarse one, of every CTA
-  int warp_gt[EV_THREADS / 32], warp_eq[EV_THREADS / 32];
+  int warp_gt[THREADS / 32], warp_eq[THREADS / 32];
   int gt, eq;                         // of this CTA: keys above the last key, equal to it
   alignas(16) uint32_t keys[4];       // the slice, when it fits
 };
@@ -128,10 +128,12 @@ struct EvUnits {
   }
 };
 
-template <int UNIT, int CLUSTER>
-__global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvParams p, int slots) {
+template <int UNIT, int CLUSTER, int EV_THREADS>
+__global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) evict_select_kernel(EvParams p, int slots) {
   extern __shared__ __align__(16) unsigned char smem[];
-  EvSelect<CLUSTER>& sm = *reinterpret_cast<EvSelect<CLUSTER>*>(smem);
+  using S = EvSelect<CLUSTER, EV_THREADS>;
+  constexpr int EV_WARPS = EV_THREADS / 32;
+  S& sm = *reinterpret_cast<S*>(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = CLUSTER == 1 ? 0u : ev_cluster_rank();
   const int b = (int)(blockIdx.x / CLUSTER);
@@ -163,9 +165,26 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvParams p,
   const int mine = (int)(min(u0 + per, units) - u0), quads = (mine + 3) / 4;
   const bool cached = 4 * quads <= slots;
   uint4* keys = reinterpret_cast<uint4*>(sm.keys);
-  if (cached) {
+  if (cached && UNIT == 1) {
 #pragma unroll 4
     for (int i = tid; i < quads; i += EV_THREADS) keys[i] = all.four(u0 + 4 * i);
+  } else if (cached) {
+    // a lane takes half a unit (a lane a unit would touch a line each), neighbours join theirs
+    const int halves = (2 * mine + 31) / 32 * 32;
+#pragma unroll 4
+    for (int i = tid; i < halves; i += EV_THREADS) {
+      const int64_t j = (u0 * 2 + i) * 4;             // first weight
+      uint32_t k = 0u;
+      if (j + 4 <= n) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(all.w + j));
+        k = max(max(ev_key(v.x), ev_key(v.y)), max(ev_key(v.z), ev_key(v.w)));
+      } else {
+        for (int64_t y = j; y < n; y++) k = max(k, ev_key(__ldcg(all.w + y)));
+      }
+      k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 1));
+      const int64_t u = u0 + i / 2;
+      if ((i & 1) == 0 && i / 2 < 4 * quads) sm.keys[i / 2] = u < all.first || u >= all.recent ? EV_FORCED : k;
+    }
   }
   auto four = [&](int i) { return cached ? keys[i] : all.four(u0 + 4 * (int64_t)i); };
   int left = (int)K;                                  // keys still to be found among those with the prefix
@@ -189,9 +208,9 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvParams p,
           atomicAdd(&hist[k[x] >> shift & ((1u << bits) - 1u)], 1);
     }
     __syncthreads();
-    {                                                 // warp = coarse bin
-      const int s = __reduce_add_sync(0xFFFFFFFFu, hist[EV_FINE * warp + lane] + hist[EV_FINE * warp + 32 + lane]);
-      if (lane == 0) sm.coarse[pass & 1][warp] = s;
+    for (int c = warp; c < EV_COARSE; c += EV_WARPS) {
+      const int s = __reduce_add_sync(0xFFFFFFFFu, hist[EV_FINE * c + lane] + hist[EV_FINE * c + 32 + lane]);
+      if (lane == 0) sm.coarse[pass & 1][c] = s;
     }
     ev_sync<CLUSTER>();
     if (warp < CLUSTER) sm.all_coarse[warp][lane] = ev_remote<CLUSTER>(&sm.coarse[pass & 1][lane], warp);
@@ -206,9 +225,8 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvParams p,
     const int coarse = EV_COARSE - 1 - at;
     left -= __shfl_sync(0xFFFFFFFFu, above, at);
     gt += __shfl_sync(0xFFFFFFFFu, own_above, at);
-    if (warp < 2 * CLUSTER)
-      sm.all_fine[warp >> 1][32 * (warp & 1) + lane] =
-          ev_remote<CLUSTER>(&hist[EV_FINE * coarse + 32 * (warp & 1) + lane], warp >> 1);
+    for (int c = warp; c < 2 * CLUSTER; c += EV_WARPS)
+      sm.all_fine[c >> 1][32 * (c & 1) + lane] = ev_remote<CLUSTER>(&hist[EV_FINE * coarse + 32 * (c & 1) + lane], c >> 1);
     __syncthreads();
     // lane l has bins EV_FINE - 1 - 2 l and the one below
     int2 f = make_int2(0, 0);
@@ -255,44 +273,52 @@ __global__ void __launch_bounds__(EV_THREADS, 1) evict_select_kernel(EvParams p,
     p.n_new[b] = out;
     p.n_out[b] = out;
   }
-  for (int i0 = 0; i0 < quads; i0 += 2 * EV_THREADS) {   // a thread takes two fours in a row
-    uint32_t k[8];
-    int g = 0, e = 0;
-    const int q0 = i0 + 2 * tid;
+  // A warp takes a run of fours: it counts them, and when it knows what lies before them writes where they go.
+  const int run = ((quads + EV_WARPS - 1) / EV_WARPS + 31) / 32 * 32, q0 = run * warp, q1 = min(q0 + run, quads);
+  int g = 0, e = 0;
+#pragma unroll 2
+  for (int q = q0 + lane; q < q1; q += 32) {
+    const uint4 v = four(q);
+    const uint32_t k[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int y = 0; y < 2; y++) {
-      const uint4 v = q0 + y < quads ? four(q0 + y) : make_uint4(0u, 0u, 0u, 0u);
-      k[4 * y] = v.x, k[4 * y + 1] = v.y, k[4 * y + 2] = v.z, k[4 * y + 3] = v.w;
-    }
-#pragma unroll
-    for (int x = 0; x < 8; x++) {
-      const bool there = 4 * q0 + x < mine;
-      g += there && k[x] > last;
-      e += there && k[x] == last;
-    }
-    int gp = ev_before(g, lane), ep = ev_before(e, lane);
-    __syncthreads();                                  // the sums of the turn before are read
-    if (lane == 31) {
-      sm.warp_gt[warp] = gp + g;
-      sm.warp_eq[warp] = ep + e;
-    }
-    __syncthreads();
-    const int wg = sm.warp_gt[lane], we = sm.warp_eq[lane];
-    gp += gt_base + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wg : 0);
-    ep += eq_base + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? we : 0);
-    gt_base += __reduce_add_sync(0xFFFFFFFFu, wg);
-    eq_base += __reduce_add_sync(0xFFFFFFFFu, we);
-#pragma unroll
-    for (int x = 0; x < 8; x++) {
-      if (4 * q0 + x >= mine) break;
-      if (k[x] > last) {
-        kept[gp + min(ep, left)] = (int32_t)(u0 + 4 * q0 + x);
-        gp++;
-      } else if (k[x] == last) {
-        if (ep < left) kept[gp + ep] = (int32_t)(u0 + 4 * q0 + x);
-        ep++;
+    for (int x = 0; x < 4; x++)
+      if (4 * q + x < mine) {
+        g += k[x] > last;
+        e += k[x] == last;
       }
-    }
+  }
+  g = __reduce_add_sync(0xFFFFFFFFu, g);
+  e = __reduce_add_sync(0xFFFFFFFFu, e);
+  if (lane == 0) {
+    sm.warp_gt[warp] = g;
+    sm.warp_eq[warp] = e;
+  }
+  __syncthreads();
+  int gp = gt_base + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sm.warp_gt[lane] : 0);
+  int ep = eq_base + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sm.warp_eq[lane] : 0);
+  for (int qw = q0; qw < q1; qw += 32) {
+    const int q = qw + lane;
+    const uint4 v = q < q1 ? four(q) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+    uint32_t both = 0u;                               // keys above (low half) and equal (high half) in this lane's four
+#pragma unroll
+    for (int x = 0; x < 4; x++)
+      if (q < q1 && 4 * q + x < mine) both += (k[x] > last) + ((uint32_t)(k[x] == last) << 16);
+    const uint32_t sum = (uint32_t)ev_before((int)both, lane);
+    int gl = gp + (int)(sum & 0xFFFFu), el = ep + (int)(sum >> 16);
+#pragma unroll
+    for (int x = 0; x < 4; x++)
+      if (q < q1 && 4 * q + x < mine) {
+        if (k[x] > last) {
+          kept[gl + min(el, left)] = (int32_t)(u0 + 4 * q + x);
+          gl++;
+        } else if (k[x] == last) {
+          if (el < left) kept[gl + el] = (int32_t)(u0 + 4 * q + x);
+          el++;
+        }
+      }
+    gp = __shfl_sync(0xFFFFFFFFu, gl, 31);
+    ep = __shfl_sync(0xFFFFFFFFu, el, 31);
   }
   if (CLUSTER > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -427,23 +453,23 @@ int64_t evict_chunks(int bits, int unit, int64_t units) {
   return ceil_div(units, c);
 }
 
-template <int UNIT, int CLUSTER>
+template <int UNIT, int CLUSTER, int THREADS>
 static cudaError_t ev_select(const EvParams& p, cudaLaunchConfig_t cfg) {
-  using S = EvSelect<CLUSTER>;
+  using S = EvSelect<CLUSTER, THREADS>;
   static PerDeviceOnce attrs;
   constexpr int most = (int)sizeof(S) + EV_KEYS * 4;
   static_assert(most <= 227 * 1024, "shared memory per CTA");
-  cudaError_t e = attrs.ensure([](int) {
-    cudaError_t r = cudaFuncSetAttribute(evict_select_kernel<UNIT, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (r == cudaSuccess && CLUSTER > 8)
-      r = cudaFuncSetAttribute(evict_select_kernel<UNIT, CLUSTER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  auto* kernel = evict_select_kernel<UNIT, CLUSTER, THREADS>;
+  cudaError_t e = attrs.ensure([kernel](int) {
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r == cudaSuccess && CLUSTER > 8) r = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return r;
   });
   if (e != cudaSuccess) return e;
   const int64_t slice = ceil_div(ceil_div(ceil_div(p.cap, UNIT), CLUSTER), 4) * 4;
   const int slots = slice <= EV_KEYS ? (int)slice : 0;
   cfg.gridDim = dim3((unsigned)p.B * CLUSTER);
-  cfg.blockDim = dim3(EV_THREADS);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = sizeof(S) + (size_t)slots * 4;
   cudaLaunchAttribute attr[2];
   attr[0] = cfg.attrs[0];
@@ -452,15 +478,17 @@ static cudaError_t ev_select(const EvParams& p, cudaLaunchConfig_t cfg) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CLUSTER > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<UNIT, CLUSTER>, p, slots);
+  return cudaLaunchKernelEx(&cfg, kernel, p, slots);
 }
 
-// CTAs of a sequence's selection.
+// CTAs of a sequence's selection.  A cluster of 8 CTAs of 1024 threads fits 15 times (one to an SM), so that 16
+// sequences of 131,072 took two waves, 43 us; of 512 threads 32.  A few long ones: 16 CTAs, 32 us (512 threads: 40)
+// for 131,072 blocks.
 template <int UNIT>
 static cudaError_t ev_select_any(const EvParams& p, const cudaLaunchConfig_t& cfg) {
   const int64_t units = ceil_div(p.cap, UNIT);
-  if (units <= 8192) return ev_select<UNIT, 1>(p, cfg);
-  return units <= 65536 || p.B > 8 ? ev_select<UNIT, 8>(p, cfg) : ev_select<UNIT, 16>(p, cfg);
+  if (units <= 8192) return ev_select<UNIT, 1, 512>(p, cfg);
+  return units <= 65536 || p.B > 6 ? ev_select<UNIT, 8, 512>(p, cfg) : ev_select<UNIT, 16, 1024>(p, cfg);
 }
 
 template <int BITS, int UNIT>
