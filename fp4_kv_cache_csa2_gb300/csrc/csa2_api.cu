@@ -652,7 +652,7 @@ size_t csa2_evict_workspace_size(int B, int64_t budget, int unit) {
   if (B < 0 || budget < 1 || budget > INT32_MAX || (unit != 1 && unit != 8) || budget % unit != 0) return 0;
   // the chunks of an 8-bit cache are the smaller ones
   const int64_t chunks = evict_chunks(unit == 8 ? 8 : 4, unit, budget / unit);
-  return HDR + align256(sizeof(uint32_t)) + 2 * align256((size_t)B * 4) + align256((size_t)B * chunks * 4);
+  return HDR + align256(sizeof(uint32_t)) + align256((size_t)B * 4) + align256((size_t)B * chunks * 4);
 }
 
 // p: the caches' part, filled in.  An array of either cache: its bytes for one entry times 8.
@@ -670,8 +670,8 @@ static csa2_status do_evict(EvParams p, const EvArray* arrays, int n_arrays, int
   if (a->n_first > a->budget || a->n_recent > a->budget || a->budget > p.to_cap) return CSA2_ERR_INVALID_ARG;
   const int64_t first = ceil_div(a->n_first, unit), recent = ceil_div(a->n_recent, unit) + (unit > 1 ? 1 : 0);
   if (first + recent > a->budget / unit) return CSA2_ERR_INVALID_ARG;
-  // a chunk of the moves is 160 entries or more: every grid stays below 2^31 CTAs
-  if (a->B > (1 << 20) || a->B * (a->budget / 128 + p.to_cap / 8192 + 2) >= lim) return CSA2_ERR_UNSUPPORTED;
+  // a chunk of the moves is 40 entries or more: every grid stays below 2^31 CTAs
+  if (a->B > (1 << 20) || a->B * (a->budget / 40 + p.to_cap / 8192 + 2) >= lim) return CSA2_ERR_UNSUPPORTED;
   const size_t need = csa2_evict_workspace_size(a->B, a->budget, a->unit);
   csa2_status st = check_ws(ws, ws_bytes, need);
   if (st != CSA2_OK || a->B == 0) return st;
@@ -714,8 +714,6 @@ static csa2_status do_evict(EvParams p, const EvArray* arrays, int n_arrays, int
   unsigned char* cur = scratch(ws);
   p.ticket = reinterpret_cast<uint32_t*>(cur);
   cur += align256(sizeof(uint32_t));
-  p.marks = reinterpret_cast<int32_t*>(cur);
-  cur += align256((size_t)a->B * 4);
   p.n_new = reinterpret_cast<int32_t*>(cur);
   cur += align256((size_t)a->B * 4);
   p.flags = reinterpret_cast<int32_t*>(cur);

@@ -182,7 +182,6 @@ struct EvParams {             // eviction; `to_`: where entries go
   int32_t* n_out;             // [B]
   int in_place;
   uint32_t* ticket;           // scratch: the next chunk
-  int32_t* marks;             // scratch: [B] chunks that are known to have been read
   int32_t* n_new;             // scratch: [B] entries that stay
   int32_t* flags;             // scratch: [B][chunks] chunks that have been read
   int64_t chunks;             // set by the launcher
