@@ -588,9 +588,9 @@ def cache8_write(cache: Cache8, x, entry_start, ws: Workspace, *, n_new=None, st
     if B != cache.B:
         raise ValueError(f"x: {B} sequences, the cache has {cache.B}")
     bf16, _, i64, _ = _types()
-    stride = x.stride(1) if T > 1 else x.stride(0) if B > 1 else D_LATENT
+    stride = x.stride(1) if T > 1 else x.stride(0) if B > 1 and T else D_LATENT
     if (x.shape[2] != D_LATENT or x.dtype not in bf16 or x.get_device() != dev or x.stride(2) != 1
-            or (B > 1 and x.stride(0) != T * stride)):
+            or (B > 1 and T > 0 and x.stride(0) != T * stride)):
         _refuse("x", x, (B, T, D_LATENT), f"{bf16}, one stride between tokens", dev)
     c = _cache8(cache, dev)
     a = _pack_write8(B, T, x.data_ptr(), stride, _at("entry_start", entry_start, (B,), i64, dev),

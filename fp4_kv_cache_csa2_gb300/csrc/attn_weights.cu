@@ -92,7 +92,7 @@ __device__ __forceinline__ int aw_entries(const AwParams& p, int b) {
 // One head by a warp: q as f16 into its row of the stages, its factor and its lse in powers of two.
 __device__ __forceinline__ float2 aw_head(const uint16_t* q, float lse, float scale, bool live, unsigned char* stages, int row, int lane) {
   uint4 v[2] = {};
-  live = live && lse > -INFINITY;                     // else weights of 0, whatever q holds
+  live = live && lse != -INFINITY;                    // else weights of 0, whatever q holds
   if (live) {
     v[0] = __ldcg(reinterpret_cast<const uint4*>(q) + lane);
     v[1] = __ldcg(reinterpret_cast<const uint4*>(q) + 32 + lane);
@@ -173,7 +173,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     sm.most = 0;
     sm.err = 0;
     tc::bar_init_fence();
-    tc::prefetch_tensormap(&map_q);
+    if (PAIR) tc::prefetch_tensormap(&map_q);
     if (E8) tc::prefetch_tensormap(&map_codes);
   }
   tc::fence_before_sync();
@@ -578,7 +578,7 @@ static cudaError_t aw_launch(const AwParams& p, const CUtensorMap& mq, const CUt
 }
 
 cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream) {
-  if (p.B == 0 || p.max_n == 0) return cudaSuccess;
+  if (p.B == 0 || p.max_n == 0 || p.cap == 0) return cudaSuccess;
   const AwPlan plan = attn_weights_plan(p.B, p.Q, p.max_n);
   p.runs = plan.runs;
   p.splits = p.Q ? plan.splits : 0;
@@ -592,15 +592,14 @@ cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaSuccess;
   if (p.Q > 0) {
-    CUtensorMap mq, mc;
-    if (!encode_query_halves(&mq, p.q, (uint64_t)p.B * p.Q * H)) return cudaErrorInvalidValue;
-    if (!p.scales8) mc = mq;
-    else if (!encode_u8_rows512_sw128(&mc, p.kv, (uint64_t)p.B * p.cap, AW_KEYS)) return cudaErrorInvalidValue;
+    CUtensorMap mq = {}, mc = {};                     // (of what the kernel does not copy: unused)
+    if (p.Q > 1 && !encode_query_halves(&mq, p.q, (uint64_t)p.B * p.Q * H)) return cudaErrorInvalidValue;
+    if (p.scales8 && !encode_u8_rows512_sw128(&mc, p.kv, (uint64_t)p.B * p.cap, AW_KEYS)) return cudaErrorInvalidValue;
     if (p.scales8) e = p.Q == 1 ? aw_launch<true, false>(p, mq, mc, cfg) : aw_launch<true, true>(p, mq, mc, cfg);
     else e = p.Q == 1 ? aw_launch<false, false>(p, mq, mc, cfg) : aw_launch<false, true>(p, mq, mc, cfg);
     if (e != cudaSuccess || p.splits == 1) return e;
   }
-  const int blocks = (int)ceil_div(p.max_n, 256);
+  const int blocks = (int)ceil_div(min(p.max_n, p.cap), 256);
   cfg.gridDim = dim3((unsigned)p.B * (unsigned)blocks);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;

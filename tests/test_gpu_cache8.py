@@ -75,6 +75,15 @@ def test_write_reports_what_lies_outside(start, n_new, n):
     write_and_check(codes, scales, np.asarray(n, np.int32), latents(g, 1, 6), start, n_new, status=6)
 
 
+def test_write_nothing_and_padded_rows():
+    """No tokens; and of a padded batch only the first n_new, whatever the others hold."""
+    codes, scales = old_cache(6, 2, 16)
+    write_and_check(codes, scales, np.zeros(2, np.int32), torch.zeros(2, 0, D, dtype=torch.bfloat16), [0, 3], None)
+    x = latents(torch.Generator().manual_seed(6), 2, 9)
+    x[0, 4:], x[1, 1:] = float("nan"), float("inf")
+    write_and_check(codes, scales, np.zeros(2, np.int32), x, [0, 3], [4, 1])
+
+
 def test_write_ties_go_to_even():
     x = torch.zeros(1, 8, D)
     x[0, :, :127] = torch.arange(127)[None] - 62.5                 # -62.5 .. 63.5, ties of scale 1

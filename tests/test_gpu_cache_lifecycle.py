@@ -151,3 +151,50 @@ def test_4_bit_cache_cut_and_written_on():
         check_attention(out[b, 0], lse[b, 0], q[b, 0], keys)
         assert sel[b, 0, :n].tolist() == list(range(n)) and sel[b, 0, n].item() == -1
         check_attention(chosen[b, 0], lse[b, 0], q[b, 0], keys)
+
+
+def test_two_streams_at_once():
+    """The same chain of calls on two streams, each with its caches and its workspace, eight times over."""
+    B, cap, budget = 4, 20_000, 6_000
+
+    def chain(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        cache, to = csa2.Cache8(B, cap, 1), csa2.Cache8(B, budget, 1)
+        x = torch.randn(B, cap, D, generator=g, device="cuda").bfloat16()
+        q = torch.randn(B, 2, H, D, generator=g, device="cuda").bfloat16()
+        pos = torch.tensor([[cap - 2, cap - 1]] * B, device="cuda")
+        out, lse = torch.zeros(B, 2, H, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(B, 2, H, device="cuda")
+        w, to_w = torch.zeros(B, cap, device="cuda"), torch.zeros(B, budget, device="cuda")
+        kept, n = torch.zeros(B, budget // 8, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+        ws = csa2.Workspace(max(csa2.cache8_attn_workspace_size(B, 2, cap), csa2.attn_weights_workspace_size(B, 2, (1 << 31) - 1),
+                                csa2.evict_workspace_size(cache, budget, 8)))
+        zero = torch.zeros(B, dtype=torch.int64, device="cuda")
+        cache.n_entries.fill_(cap)
+
+        def run(stream=None):
+            csa2.cache8_write(cache, x, zero, ws, stream=stream)
+            csa2.cache8_attn(cache, q, pos, SCALE, out, ws, max_n=cap, stream=stream)
+            csa2.cache8_attn(cache, q, pos, SCALE, out, ws, max_n=cap, lse=lse, stream=stream)
+            csa2.attn_weights(cache, q, pos, lse, SCALE, w, ws, max_n=(1 << 31) - 1, stream=stream)
+            csa2.evict(cache, w, kept, n, ws, budget=budget, unit=8, to=to, to_weights=to_w, stream=stream)
+        return run, (cache.codes, cache.scales, out, lse, w, to_w, kept, n, to.codes, to.scales), ws
+
+    chains = [chain(1), chain(2)]
+    want = []
+    for run, outputs, _ in chains:
+        run()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outputs])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(8):
+        for run, outputs, _ in chains:
+            for t in outputs[2:]:
+                t.zero_()
+        torch.cuda.synchronize()
+        for (run, _, _), s in zip(chains, streams):
+            run(s)
+        torch.cuda.synchronize()
+        for (_, outputs, ws), had in zip(chains, want):
+            assert ws.sync_status()[0] == 0
+            for t, u in zip(outputs, had):
+                assert torch.equal(t, u)
