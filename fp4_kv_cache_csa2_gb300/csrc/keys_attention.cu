@@ -1,6 +1,6 @@
 // Attention of 64 query heads over every visible key of the shared 512-d latent
 // (K = V), on the 5th-generation tensor cores: the window rows, a few first
-// rows that stay visible (sinks), and the entries of the 4-bit cache.
+// rows that stay visible (sinks), and the entries of the 4-bit or of the 8-bit cache.
 //
 //   o_h = sum_i softmax_i(scale q_h . v_i) v_i,   lse_h = log sum_i exp(scale q_h . v_i)
 //
@@ -35,8 +35,8 @@
 // before any rounding, in binary32.
 //
 // Shared memory: three K buffers of [64 keys][512 dims] (two halves of 32 KB, four SW128
-// column chunks each; the third takes Q on its way to TMEM first) and a staging area of
-// 18 KB for the next chunk's entries as stored.  Roles:
+// column chunks each; the third takes Q on its way to TMEM first) and a staging area
+// for the next chunk's entries as stored (18 KB; of 8-bit codes 32).  Roles:
 // warps 0..3 move Q, then softmax; warps 4..11 fill the K buffers (from the staged bytes
 // through registers; bf16 rows are rounded in place if need be); warps 0..7 write the
 // output; warp 12 issues the MMAs, S of chunk c + 1 before O of chunk c, so that the
@@ -49,6 +49,10 @@
 // entries 1.93 ms, 1.02 PFLOP/s, their pipe active in 86 % of the cycles; 16 queries over 131,072 entries
 // 262 us, 0.99 PFLOP/s; 602 queries of 1000 E4M3 rows 114 us.  A CTA costs about 7 us beside its chunks: 16
 // queries of 132 bf16 rows take 9.0 us.
+// With 8-bit entries the shared memory binds too: 2048 cycles a chunk (products 1024, staged bytes in and
+// out 512, widened codes 512) beside 2074 of MMAs.  2048 queries over 8192 entries 2.06 ms, 16 over 131,072
+// 287 us.  (Codes to registers without staging, four lanes a key, the same; staged rows without a swizzle,
+// two keys a phase with their pieces in turn, 2.65 ms.)
 #include <cfloat>
 
 #include "attn_common.cuh"
