@@ -102,6 +102,14 @@ __device__ __forceinline__ void named_sync(uint32_t id, uint32_t n) {
   asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(n) : "memory");
 }
 
+// Whether x holds in any of the n threads of named barrier `id`.
+__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t n, bool x) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, %2, %3, a;\n"
+               " selp.u32 %0, 1, 0, b;\n}\n" : "=r"(r) : "r"((uint32_t)x), "r"(id), "r"(n) : "memory");
+  return r != 0;
+}
+
 // 32 consecutive TMEM columns of this thread's lane -> r (waited)
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
   tc::tmem_ld_x32_nowait(taddr, r);

@@ -544,7 +544,7 @@ static int64_t cache8_chunks(int64_t max_n, int W) {
 
 size_t csa2_cache8_attn_workspace_size(int B, int Q, int64_t max_n, int W) {
   if (B < 0 || Q < 0 || max_n < 0 || W < 0 || (int64_t)B * Q > MAX_KEY_QUERIES) return 0;
-  return HDR + align256(keys_part_bytes((int64_t)B * Q, cache8_chunks(max_n, W)));
+  return HDR + align256(cache8_part_bytes(B, Q, cache8_chunks(max_n, W)));
 }
 
 csa2_status csa2_cache8_attn(const csa2_cache8* cache, const csa2_cache8_attn_args* a, void* ws, size_t ws_bytes,

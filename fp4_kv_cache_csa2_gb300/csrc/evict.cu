@@ -131,7 +131,7 @@ struct EvUnits {
 
 template <int UNIT, int CLUSTER, int EV_THREADS>
 __global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) evict_select_kernel(EvParams p, int slots) {
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   using S = EvSelect<CLUSTER, EV_THREADS>;
   constexpr int EV_WARPS = EV_THREADS / 32;
   S& sm = *reinterpret_cast<S*>(smem);

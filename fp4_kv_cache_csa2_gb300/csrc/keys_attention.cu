@@ -56,6 +56,7 @@
 #include <cfloat>
 
 #include "attn_common.cuh"
+#include "keys_common.cuh"
 #include "params.cuh"
 
 namespace csa2 {
@@ -81,24 +82,6 @@ constexpr int KA_Q_COL = 256;
 constexpr int KA_S_COL = 384;                             // S, then P, of chunk c at 64 (c % 2)
 constexpr uint32_t KA_HALF_LANES = 16u << 16;
 constexpr int KA_AHEAD = 5;                               // chunks of entries that are on their way to L2
-constexpr float KA_LOG2E = 1.4426950408889634f;
-constexpr float KA_LN2 = 0.6931471805599453f;
-// The reference of a head moves when a score (in powers of two) lies KA_TAU (bf16, where P has
-// binary32's range) or KA_MOST (F16) above it.  F16: P of the largest score is 2^KA_TOP when the reference is set, and at
-// most 2^KA_MOST, f16's range less a little, before it moves.  Weights down to 2^-22 of the largest
-// keep f16's 11 bits, and what lies below loses 2^-33 of it at most: with a reference at the largest
-// score itself one key 17.3 above 131,072 others alike lost all of their 0.4 %.  The room between
-// the two (5.5 in logits) keeps rescalings rare: 2048 queries over 8192 entries took 1911 us, with
-// 2^0 at the top 1910, with 2^10 1933, with 2^11 1971 (and 15 more each with the check of q's range).
-constexpr float KA_TAU = 8.0f * KA_LOG2E;
-constexpr float KA_TOP = 8.0f, KA_MOST = 15.9f;
-// 8-bit entries: codes times a block's scale s.  The tensor cores see the codes; s enters the scores, and the
-// weights that go to the second product are P s, so the reference follows the scores plus log2 s.  The
-// sum of the softmax is of P without s, which is why s counts as KA_FLOOR8 at least there: P stays below
-// 2^(KA_MOST + 60), its sum inside binary32.
-constexpr float KA_FLOOR8 = 0x1p-60f;
-constexpr int KA_SMS = 152;                               // GB300; CTAs a query is divided over at most
-constexpr int KA_PART_FLOATS = 2 * H + H * D;             // one partial state: references, sums, O [dims / 4][head][4]
 
 // A wait for a phase by its parity needs that the barrier cannot have passed the phase
 // after it: whatever completes that one must itself wait for the waiter.  Where two
@@ -885,6 +868,32 @@ int keys_split(int64_t BQ, int64_t chunks) {
   return best;
 }
 
+// The same for the pairs of CTAs of a call with several queries of an 8-bit cache: a chunk takes 0.75 us, and a
+// pair PAIR_FIXED chunks beside its own; in 48ths of a chunk's time.
+constexpr int PAIR_FIXED = 10;
+static int pair_split(int64_t pairs, int64_t chunks) {
+  const int64_t slots = KA_SMS / 2;
+  int best = 1;
+  int64_t best_cost = 48 * ceil_div(pairs, slots) * (PAIR_FIXED + chunks);
+  for (int s = 2; s <= slots && s <= chunks && pairs * s <= KA_WAVES * slots; s++) {
+    const int64_t cost = 48 * ceil_div(pairs * s, slots) * (PAIR_FIXED + ceil_div(chunks, s)) + 192 + 5 * s + 4 * pairs * s;
+    if (cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+static int cache8_split(int B, int Q, int64_t chunks) {
+  return Q > 1 ? pair_split((int64_t)B * ((Q + 1) / 2), chunks) : keys_split((int64_t)B * Q, chunks);
+}
+
+size_t cache8_part_bytes(int B, int Q, int64_t chunks) {
+  const int s = cache8_split(B, Q, chunks);
+  return s > 1 ? (size_t)((int64_t)B * Q * s) * KA_PART_FLOATS * sizeof(float) : 0;
+}
+
 size_t keys_part_bytes(int64_t BQ, int64_t chunks) {
   const int s = keys_split(BQ, chunks);
   return s > 1 ? (size_t)(BQ * s) * KA_PART_FLOATS * sizeof(float) : 0;
@@ -909,7 +918,13 @@ static cudaError_t keys_launch(const KeysParams& p, int64_t BQ, const CUtensorMa
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, keys_attn_kernel<F16, E8>, p, mq, mr, ms);
-  if (e != cudaSuccess || p.split == 1) return e;
+  return e != cudaSuccess || p.split == 1 ? e : launch_keys_join(p, BQ, stream);
+}
+
+cudaError_t launch_keys_join(const KeysParams& p, int64_t BQ, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cc = {};
   // Few queries: CTAs of many threads, one to an SM.  Else one slice; up to four states then
   // want the registers of half as many CTAs (4 states of 111 queries 132 us in all, 136 otherwise).
@@ -947,7 +962,7 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
   const int64_t BQ = (int64_t)B * p.Q;
   if (BQ == 0) return cudaSuccess;
   if (keys_in_ring(p, B, BQ)) return launch_window_ring(p, B, stream);
-  p.split = keys_split(BQ, chunks);
+  p.split = p.scales8 ? cache8_split(B, p.Q, chunks) : keys_split(BQ, chunks);
   p.part = reinterpret_cast<float*>(part);
   CUtensorMap mq, mr, ms;
   if (!encode_bf16_rows512(&mq, p.q, (uint64_t)BQ * H, H)) return cudaErrorInvalidValue;
@@ -963,7 +978,9 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
   if (nk == 0) ms = mr;
   if (p.scales8) {                                    // no sinks: their map is the codes'
     if (p.cap > 0 && !encode_u8_rows512_sw128(&ms, p.main_kv, (uint64_t)B * p.cap, KA_KEYS)) return cudaErrorInvalidValue;
-    return keys_launch<true, true>(p, BQ, mq, mr, ms, stream);
+    if (p.Q == 1) return keys_launch<true, true>(p, BQ, mq, mr, ms, stream);
+    const cudaError_t e = launch_pair_attention(p, B, mq, mr, ms, stream);
+    return e != cudaSuccess || p.split == 1 ? e : launch_keys_join(p, BQ, stream);
   }
   return p.main_kv || p.rows_fp8 ? keys_launch<true, false>(p, BQ, mq, mr, ms, stream)
                                  : keys_launch<false, false>(p, BQ, mq, mr, ms, stream);

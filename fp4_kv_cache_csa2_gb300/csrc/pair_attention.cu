@@ -1,0 +1,690 @@
+// Attention over the 8-bit cache and a window for calls of several queries a sequence: two
+// queries by a pair of CTAs, the 64 heads of each at the full rate of the tensor cores.
+//
+//   o_h = sum_i softmax_i(scale q_h . v_i) v_i,   lse_h = log sum_i exp(scale q_h . v_i)
+//
+// as in keys_attention.cu, whose chunks of 64 keys, softmax state, partial states and outputs these
+// are.  There a product of 64 rows runs at half the rate, and each query's CTA widens every key for
+// itself.  Here a product spans two CTAs (cta_group::2, M = 128: 64 rows in each).  Of such
+// a product TMEM lanes 0 .. 63 of a CTA take the columns of B that lie in CTA 0's shared memory, lanes
+// 64 .. 127 those in CTA 1's, each times the A of the lane itself: two products of 64 rows.  So CTA r
+// keeps half r of the dims of every key, and
+//   * S = Q K^T   A = the query's dims 0 .. 255 (lanes 0 ..), 256 .. 511 (lanes 64 ..), B = the
+//     keys' dims of either CTA: 16 MMAs of N = 128; a head's score is the sum of its two lanes
+//   * O += P V    A = P in both lanes of a head, B = 2 x 128 dims of either CTA: 8 MMAs of N = 256;
+//     lanes 0 .. 63 hold O's dims 0 .. 255, the others 256 .. 511
+// 1,079 cycles of MMAs a chunk for two queries on two SMs, against 2,074 for one on one; each CTA stages and
+// widens half of a chunk (512 cycles of shared memory instead of 1024), and the products read half (512).
+// The lanes of a head sit in two warps, which pass each other 32 partial scores and 32 weights through
+// shared memory (384 cycles).
+//
+// Both queries share the keys, each with its own limits: what one of them does not see has weight 0
+// for it.  So no key may hold an infinity or a NaN: codes cannot, and of window rows
+// such values are written as 0 and every output of the queries that see the row becomes NaN.
+//
+// Roles of each CTA's warps as there: 0..3 move Q, then softmax (lane of TMEM = lane of the
+// warp); 4..11 fill; 0..7 write the output; 12 issues the MMAs (in CTA 0); 13 the copies.
+#include <cfloat>
+
+#include "attn_common.cuh"
+#include "keys_common.cuh"
+#include "params.cuh"
+
+namespace csa2 {
+
+constexpr int PA_SOFT_WARPS = 4, PA_FILL_WARPS = 8, PA_OUT_WARPS = 8;
+constexpr int PA_FILL = 32 * PA_FILL_WARPS;
+constexpr int PA_MMA_WARP = PA_SOFT_WARPS + PA_FILL_WARPS, PA_COPY_WARP = PA_MMA_WARP + 1;
+constexpr int PA_THREADS = 32 * (PA_COPY_WARP + 1);
+constexpr int PA_KEYS = KEYS_CHUNK;
+constexpr int PA_COL = 64 * 128;                          // [64 rows][64 dims] 16-bit, SW128
+constexpr int PA_BUF = 4 * PA_COL;                        // a chunk's 256 dims
+constexpr int PA_BUFS = 4;                                // the last two take Q first
+constexpr int PA_STAGE = 2 * PA_COL;                      // a chunk's 256 codes a key, SW128
+constexpr int PA_STAGES = 2;
+constexpr int PA_OFF_STAGE = PA_BUFS * PA_BUF;
+constexpr int PA_OFF_S = PA_OFF_STAGE + PA_STAGES * PA_STAGE;   // partial scores for the other lane: [8][128 lanes] float4
+constexpr int PA_OFF_P = PA_OFF_S + 8 * 128 * 16;         // weights for the other lane: [4][128 lanes] uint4
+constexpr int PA_OFF_SMALL = PA_OFF_P + 4 * 128 * 16;
+constexpr int PA_O_COL = 0, PA_Q_COL = 256, PA_S_COL = 384;
+constexpr int PA_AHEAD = 6;                               // chunks of codes that are on their way to L2
+
+struct PaSmall {
+  uint64_t q_full, q_moved;           // TMA: Q; Q is in TMEM (both CTAs' softmax warps; CTA 0's counts)
+  uint64_t stage_full[PA_STAGES], stage_free[PA_STAGES];   // TMA; a fill warp each
+  uint64_t row_full[PA_BUFS];         // TMA: rows in K buffer i
+  uint64_t full[PA_BUFS];             // K buffer i is filled (both CTAs' fill warps; CTA 0's counts)
+  uint64_t free_[PA_BUFS];            // O of the chunk in K buffer i is done (told to both)
+  uint64_t s_full[2], p_ready[2];     // S of every second chunk is done (told to both); its P is written (CTA 0's counts)
+  uint64_t q_here;                    // this CTA's softmax warps have read Q
+  float sum[2][H], top[2][H];         // of the softmax, a half of the keys each; maxima on their way to the other lane
+  uint32_t tmem_base;
+  int err, poison;                    // a row that is not finite lies before this CTA's query
+};
+constexpr int PA_SMEM = PA_OFF_SMALL + (int)sizeof(PaSmall);
+static_assert(PA_SMEM <= 227 * 1024, "shared memory per CTA");
+
+__device__ __noinline__ bool pa_timeout(int* err, WsHeader* hdr, int where) {
+  if (atomicExch(err, 1) == 0) report(hdr, CSA2_ERR_TIMEOUT, where);
+  return false;
+}
+
+// What one query sees: window rows row_lo .. row_hi - 1 of the buffer, entries 0 .. entries - 1.
+struct PaQuery {
+  int64_t t, lo;                      // position (-1: none), first window position
+  int64_t row_lo, row_hi, entries;
+};
+
+__device__ __forceinline__ PaQuery pa_query(const KeysParams& p, int b, int64_t base, int i) {
+  PaQuery q{-1, 0, 0, 0, 0};
+  if (i >= p.Q) return q;
+  q.t = p.q_pos[(int64_t)b * p.Q + i];
+  if (q.t < 0) return q;
+  q.lo = q.t >= p.W ? q.t - p.W + 1 : 0;
+  if (p.W > 0 && q.t >= base) {       // (unsigned differences: any two positions have one)
+    const uint64_t s = (uint64_t)p.S, r0 = q.lo > base ? (uint64_t)q.lo - (uint64_t)base : 0;
+    const uint64_t end = (uint64_t)q.t - (uint64_t)base, r1 = end < s ? end + 1 : s;
+    if (r0 < r1) {
+      q.row_lo = (int64_t)r0;
+      q.row_hi = (int64_t)r1;
+    }
+  }
+  q.entries = visible_entries(min(q.t, INT64_MAX - 1), p.m, p.n_entries[b]);
+  q.entries = max(min(q.entries, p.cap), (int64_t)0);
+  return q;
+}
+
+// The pair's keys: rows a0 .. (chunks before ca), rows b0 .. (before cb), entries; a CTA's run of their
+// chunks is [c0, c0 + n).
+struct PaRun {
+  int64_t a0, an, b0, bn, en;         // first row and number of rows of either part; entries
+  int64_t ca, cb;
+  int64_t c0;
+  int n;
+  __device__ __forceinline__ bool rows(int c) const { return c0 + c < cb; }
+  // row or entry of the chunk's first key, keys of the chunk
+  __device__ __forceinline__ int64_t first(int c) const {
+    const int64_t k = c0 + c;
+    return k < ca ? a0 + PA_KEYS * k : k < cb ? b0 + PA_KEYS * (k - ca) : PA_KEYS * (k - cb);
+  }
+  __device__ __forceinline__ int keys(int c) const {
+    const int64_t k = c0 + c, left = k < ca ? an - PA_KEYS * k : k < cb ? bn - PA_KEYS * (k - ca) : en - PA_KEYS * (k - cb);
+    return left < PA_KEYS ? (int)left : PA_KEYS;
+  }
+};
+
+__device__ __forceinline__ PaRun pa_run(const PaQuery* q, int sp, int split) {
+  PaRun r{};
+  const int64_t n0 = q[0].row_hi - q[0].row_lo, n1 = q[1].row_hi - q[1].row_lo;
+  r.a0 = q[0].row_lo;
+  r.an = n0;
+  r.b0 = q[1].row_lo;
+  r.bn = n1;
+  if (n0 > 0 && n1 > 0) {
+    const int64_t lo = min(q[0].row_lo, q[1].row_lo), hi = max(q[0].row_hi, q[1].row_hi);
+    if (hi - lo <= n0 + n1) {         // windows that overlap or meet: one part.  (Else rows of one are none of the other's)
+      r.a0 = lo;
+      r.an = hi - lo;
+      r.bn = 0;
+    }
+  }
+  r.en = max(q[0].entries, q[1].entries);
+  r.ca = ceil_div(r.an, PA_KEYS);
+  r.cb = r.ca + ceil_div(r.bn, PA_KEYS);
+  const int64_t nc = r.cb + ceil_div(r.en, PA_KEYS), each = nc / split, more = nc % split;
+  r.c0 = sp * each + min((int64_t)sp, more);
+  r.n = (int)(each + (sp < more ? 1 : 0));
+  return r;
+}
+
+__global__ void __launch_bounds__(PA_THREADS, 1)
+pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_rows,
+                 const __grid_constant__ CUtensorMap map_codes) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  PaSmall& sm = *reinterpret_cast<PaSmall*>(smem + PA_OFF_SMALL);
+  if (tc::smem_u32(smem) & 1023u) {                   // the swizzled tiles need the declared alignment (the same in both CTAs)
+    if (threadIdx.x == 0) report(p.hdr, CSA2_ERR_CUDA, 5);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const int rank = (int)tc::cluster_rank(), split = p.split;
+  const uint32_t item = blockIdx.x / 2u, pairs = (uint32_t)(p.Q + 1) / 2u;
+  const int sp = (int)(item % (uint32_t)split);
+  const uint32_t pair = item / (uint32_t)split;
+  const int b = (int)(pair / pairs), qi = 2 * (int)(pair % pairs);
+  const bool there = qi + rank < p.Q;                 // the last pair of a sequence may have one query
+  const int64_t bq = (int64_t)b * p.Q + qi + rank;
+  float* part = p.part + (bq * split + sp) * KA_PART_FLOATS;   // with split > 1
+
+  if (warp == PA_MMA_WARP) tc::tmem_alloc_pair(&sm.tmem_base, 512);
+  if (tid == 0) {
+    tc::bar_init(&sm.q_full, 1);
+    tc::bar_init(&sm.q_moved, 2 * PA_SOFT_WARPS);
+    tc::bar_init(&sm.q_here, PA_SOFT_WARPS);
+    for (int i = 0; i < PA_STAGES; i++) {
+      tc::bar_init(&sm.stage_full[i], 1);
+      tc::bar_init(&sm.stage_free[i], PA_FILL_WARPS);
+    }
+    for (int i = 0; i < PA_BUFS; i++) {
+      tc::bar_init(&sm.row_full[i], 1);
+      tc::bar_init(&sm.full[i], 2 * PA_FILL_WARPS);
+      tc::bar_init(&sm.free_[i], 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      tc::bar_init(&sm.s_full[i], 1);
+      tc::bar_init(&sm.p_ready[i], 2 * PA_SOFT_WARPS);
+    }
+    sm.err = 0;
+    sm.poison = 0;
+    tc::bar_init_fence();
+    tc::prefetch_tensormap(&map_q);
+    tc::prefetch_tensormap(&map_rows);
+    tc::prefetch_tensormap(&map_codes);
+  }
+  tc::fence_before_sync();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  if (sm.tmem_base != 0 && tid == 0) report(p.hdr, CSA2_ERR_CUDA, 6);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  const int64_t base = p.W > 0 ? p.base_pos[b] : 0;
+  const PaQuery qs[2] = {pa_query(p, b, base, qi), pa_query(p, b, base, qi + 1)};
+  const PaRun run = pa_run(qs, sp, split);
+  const int n_ch = run.n;
+  const PaQuery mine = rank ? qs[1] : qs[0];
+  if (sp == 0 && tid == 0 && mine.t >= 0) {           // what the caller did not supply
+    if (p.W > 0) {
+      if (mine.lo < base) report(p.hdr, CSA2_ERR_BOUNDS, mine.lo);
+      else if ((uint64_t)mine.t - (uint64_t)base >= (uint64_t)p.S) report(p.hdr, CSA2_ERR_BOUNDS, mine.t);
+    }
+    if (p.n_entries[b] > p.cap) report(p.hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
+  }
+  bool ok = true;                                     // a thread that has given up once waits no more
+  auto wait = [&](uint64_t* bar, uint32_t use, int where) {
+    if (ok) ok = tc::bar_wait(bar, use & 1u) || pa_timeout(&sm.err, p.hdr, where);
+  };
+  auto arrive_first = [&](uint64_t* bar) {            // on CTA 0's barrier
+    if (rank) tc::bar_arrive_first(bar);
+    else tc::bar_arrive(bar);
+  };
+
+  if (warp == PA_MMA_WARP) {
+    // ================= MMAs, in CTA 0 (the whole warp runs the loop, one lane issues)
+    constexpr uint32_t idesc_s = tc::idesc_f16(128, 128, 0, 0), idesc_o = tc::idesc_f16(128, 256, 0, 1);
+    const uint64_t k_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
+    const uint64_t v_d = tc::smem_desc(tc::smem_u32(smem), PA_COL, 1024, tc::SW_128B);
+    const uint32_t leader = tc::elect_one();
+    const int n = rank == 0 ? (int)__reduce_or_sync(0xFFFFFFFFu, (uint32_t)n_ch) : 0;
+    auto wait_mma = [&](uint64_t* bar, uint32_t use, int where) {
+      if (ok) ok = tc::bar_wait_relaxed(bar, use & 1u) || pa_timeout(&sm.err, p.hdr, where);
+      tc::fence_after_sync();
+    };
+    if (n > 0) wait_mma(&sm.q_moved, 0, 80);
+    auto scores = [&](uint32_t c) {
+      const uint32_t buf = c % PA_BUFS;
+      wait_mma(&sm.full[buf], c / PA_BUFS, 81);
+      const uint64_t ka = k_d + buf * (PA_BUF >> 4);
+      const uint32_t s = PA_S_COL + 64 * (c & 1);
+#pragma unroll
+      for (int i = 0; i < 16; i++)
+        tc::mma_f16_ts_pair(leader, s, PA_Q_COL + 8 * i, ka + ((uint32_t)((i >> 2) * PA_COL + (i & 3) * 32) >> 4), idesc_s,
+                            i ? 1u : 0u);
+      tc::commit_pair(leader, &sm.s_full[c & 1]);
+    };
+    if (n > 0) scores(0);
+    for (uint32_t c = 0; c < (uint32_t)n; c++) {
+      if (c + 1 < (uint32_t)n) scores(c + 1);
+      wait_mma(&sm.p_ready[c & 1], c >> 1, 82);
+      const uint32_t buf = c % PA_BUFS, s = PA_S_COL + 64 * (c & 1);
+#pragma unroll
+      for (int g = 0; g < 2; g++) {
+        const uint64_t va = v_d + ((buf * PA_BUF + g * 2 * PA_COL) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < PA_KEYS / 16; ks++)
+          tc::mma_f16_ts_pair(leader, PA_O_COL + 128 * g, s + 8 * ks, va + (uint32_t)(ks * (2048 >> 4)), idesc_o,
+                              (c || ks) ? 1u : 0u);
+      }
+      tc::commit_pair(leader, &sm.free_[buf]);
+    }
+  } else if (warp == PA_COPY_WARP) {
+    // ================= copies: this CTA's half of the dims
+    if (lane == 0 && n_ch > 0) {
+      if (there) {                                    // Q into the last two K buffers
+        tc::bar_arrive_expect_tx(&sm.q_full, 8u * PA_COL);
+        for (int i = 0; i < 8; i++)
+          tc::tma_load_2d(smem + (PA_BUFS - 2) * PA_BUF + i * PA_COL, &map_q, i * 64, (int32_t)(bq * H), &sm.q_full);
+      }
+      const uint8_t* kv = p.main_kv + (int64_t)b * p.cap * D;
+      auto ahead = [&](int c) {                       // (each CTA sends for half of the keys, whole)
+        if (c >= n_ch || run.rows(c)) return;
+        const int keys = run.keys(c), k0 = rank ? keys / 2 : 0, k1 = rank ? keys : keys / 2;
+        if (k1 > k0) tc::prefetch_l2(kv + (run.first(c) + k0) * D, (uint32_t)((k1 - k0) * D));
+      };
+      for (int c = 1; c < PA_AHEAD; c++) ahead(c);
+      uint32_t staged = 0;
+      for (int c = 0; c < n_ch; c++) {
+        const int64_t first = run.first(c);
+        ahead(c + PA_AHEAD);
+        if (!run.rows(c)) {
+          const uint32_t s = staged % PA_STAGES;
+          if (staged >= PA_STAGES) wait(&sm.stage_free[s], staged / PA_STAGES - 1, 83);
+          staged++;
+          unsigned char* dst = smem + PA_OFF_STAGE + s * PA_STAGE;
+          tc::bar_arrive_expect_tx(&sm.stage_full[s], PA_STAGE);
+          for (int i = 0; i < 2; i++)
+            tc::tma_load_2d(dst + i * PA_COL, &map_codes, 256 * rank + 128 * i, (int32_t)(b * p.cap + first), &sm.stage_full[s]);
+          continue;
+        }
+        const uint32_t buf = c % PA_BUFS, use = c / PA_BUFS;
+        if (use > 0) wait(&sm.free_[buf], use - 1, 84);
+        else if (buf >= PA_BUFS - 2 && there) wait(&sm.q_here, 0, 84);
+        unsigned char* kt = smem + buf * PA_BUF + (p.rows_fp8 ? PA_COL / 2 : 0);
+        tc::bar_arrive_expect_tx(&sm.row_full[buf], p.rows_fp8 ? PA_BUF / 2 : PA_BUF);
+        for (int i = 0; i < 4; i++)
+          tc::tma_load_2d(kt + i * PA_COL, &map_rows, 256 * rank + 64 * i, (int32_t)((int64_t)b * p.S + first), &sm.row_full[buf]);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= PA_SOFT_WARPS) {
+    // ================= K buffers
+    const int ft = tid - 32 * PA_SOFT_WARPS;
+    // codes: lane = key, 64 dims a thread, so that both swizzles spread eight lanes over the banks
+    const int key8 = 32 * (ft >> 5 & 1) + lane, part8 = ft >> 6;
+    // rows in E4M3: thread = (key, part j: 32 of each 128 dims), as in keys_attention.cu
+    const int k8 = (ft >> 2) & 7, j = ft & 3, key = ((ft >> 2) & ~7) + ((k8 & 4) | (k8 & 1) << 1 | (k8 >> 1 & 1));
+    const bool odd = (j & 2) != 0;
+    uint32_t staged = 0;
+    for (int c = 0; c < n_ch; c++) {
+      const uint32_t buf = c % PA_BUFS, use = c / PA_BUFS;
+      unsigned char* kt = smem + buf * PA_BUF;
+      if (use > 0) wait(&sm.free_[buf], use - 1, 85);
+      else if (buf >= PA_BUFS - 2 && there) wait(&sm.q_here, 0, 85);
+      tc::fence_after_sync();
+      if (!run.rows(c)) {
+        // (keys behind the last: whatever lies there, finite, with weights of 0)
+        const uint32_t s = staged % PA_STAGES;
+        wait(&sm.stage_full[s], staged / PA_STAGES, 86);
+        staged++;
+        const unsigned char* e = smem + PA_OFF_STAGE + s * PA_STAGE + (part8 >> 1) * PA_COL;
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          v[i] = *reinterpret_cast<const uint4*>(e + sw128((uint32_t)key8, 16u * (uint32_t)(4 * (part8 & 1) + i)));
+        tc::fence_proxy_async_smem();                 // reads done before a copy writes there again
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sm.stage_free[s]);
+        unsigned char* dst = kt + part8 * PA_COL;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          uint32_t o[8];
+          i8x16_to_f16(v[i], o);
+          *reinterpret_cast<uint4*>(dst + sw128((uint32_t)key8, 32u * i)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(dst + sw128((uint32_t)key8, 32u * i + 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      } else {
+        const int64_t first = run.first(c);
+        const int keys = run.keys(c);
+        wait(&sm.row_full[buf], use, 87);             // (rows come first: copy `use` of the buffer too)
+        // a value that is not finite: 0, and the queries that see its row are told
+        auto finite = [&](uint32_t w, int row) -> uint32_t {
+          const uint32_t bad = ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u;   // exponent of all ones
+          if (bad == 0u) return w;
+          for (int q = 0; q < 2; q++)
+            if (first + row >= qs[q].row_lo && first + row < qs[q].row_hi) {
+              if (q == rank) *(volatile int*)&sm.poison = 1;
+              else tc::store_other(&sm.poison, 1, q);
+            }
+          return (bad & 0x8000u ? 0u : w & 0xFFFFu) | (bad & 0x80000000u ? 0u : w & 0xFFFF0000u);
+        };
+        if (p.rows_fp8) {
+          uint32_t o[2][16];
+#pragma unroll
+          for (int y = 0; y < 2; y++) {
+            const uint4* src = reinterpret_cast<const uint4*>(kt + 2 * y * PA_COL + (j >> 1) * PA_COL + PA_COL / 2 + key * 64 + 32 * (j & 1));
+            uint4 a = make_uint4(0u, 0u, 0u, 0u), e = a;
+            if (key < keys) {
+              a = src[odd ? 1 : 0];
+              e = src[odd ? 0 : 1];
+            }
+            const uint32_t v[8] = {odd ? e.x : a.x, odd ? e.y : a.y, odd ? e.z : a.z, odd ? e.w : a.w,
+                                   odd ? a.x : e.x, odd ? a.y : e.y, odd ? a.z : e.z, odd ? a.w : e.w};
+#pragma unroll
+            for (int x = 0; x < 8; x++) {
+              o[y][2 * x] = finite(e4m3x2_to_f16x2(v[x]), key);
+              o[y][2 * x + 1] = finite(e4m3x2_to_f16x2(v[x] >> 16), key);
+            }
+          }
+          named_sync(1, PA_FILL);                     // all are read before any is written
+#pragma unroll
+          for (int y = 0; y < 2; y++) {
+            unsigned char* dst = kt + 2 * y * PA_COL + (j >> 1) * PA_COL + key * 128;
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+              const uint4 v = make_uint4(odd ? o[y][4 * (g ^ 1)] : o[y][4 * g], odd ? o[y][4 * (g ^ 1) + 1] : o[y][4 * g + 1],
+                                         odd ? o[y][4 * (g ^ 1) + 2] : o[y][4 * g + 2], odd ? o[y][4 * (g ^ 1) + 3] : o[y][4 * g + 3]);
+              const uint32_t unit = (uint32_t)(4 * (j & 1) + (odd ? g ^ 1 : g));
+              *reinterpret_cast<uint4*>(dst + ((unit ^ (uint32_t)(key & 7)) << 4)) = v;
+            }
+          }
+        } else {
+          uint4* u = reinterpret_cast<uint4*>(kt) + ft;
+          uint4 x[PA_BUF / 16 / PA_FILL] = {};
+#pragma unroll
+          for (int i = 0; i < PA_BUF / 16 / PA_FILL; i++) {
+            const int row = ((ft + i * PA_FILL) >> 3) & (PA_KEYS - 1);
+            if (row < keys) x[i] = u[i * PA_FILL];
+          }
+#pragma unroll
+          for (int i = 0; i < PA_BUF / 16 / PA_FILL; i++) {
+            const int row = ((ft + i * PA_FILL) >> 3) & (PA_KEYS - 1);
+            u[i * PA_FILL] = make_uint4(finite(bf16x2_to_f16x2(x[i].x), row), finite(bf16x2_to_f16x2(x[i].y), row),
+                                        finite(bf16x2_to_f16x2(x[i].z), row), finite(bf16x2_to_f16x2(x[i].w), row));
+          }
+        }
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_first(&sm.full[buf]);
+    }
+  } else {
+    // ================= softmax: lane of TMEM l = 32 warp + lane: head l % 64, half l / 64 (of Q's dims, of the keys)
+    const uint32_t quarter = (uint32_t)(warp * 32) << 16;
+    const int half = warp >> 1, head = 32 * (warp & 1) + lane, me = 32 * warp + lane, other = me ^ 64;
+    const int pair_bar = 3 + (warp & 1);              // named barrier of the two warps of a head's lanes
+    float4* xs = reinterpret_cast<float4*>(smem + PA_OFF_S);
+    uint4* xp = reinterpret_cast<uint4*>(smem + PA_OFF_P);
+    float sc2 = p.scale * KA_LOG2E;                 // products to scores in powers of two
+    float m_used = -INFINITY, l_sum = 0.f;
+    if (n_ch > 0) {                                   // Q: this lane's 256 dims of its head to TMEM
+      if (there) wait(&sm.q_full, 0, 88);
+      const unsigned char* qh = smem + (PA_BUFS - 2 + half) * PA_BUF;
+      __half2 most = __half2half2(__ushort_as_half(0));
+#pragma unroll 1
+      for (int g = 0; g < 4; g++) {
+        uint32_t w[32] = {};
+        if (there) {
+#pragma unroll
+          for (int u = 0; u < 8; u++) {
+            const uint4 x = *reinterpret_cast<const uint4*>(qh + g * PA_COL + sw128((uint32_t)head, 16u * u));
+            w[4 * u] = x.x;
+            w[4 * u + 1] = x.y;
+            w[4 * u + 2] = x.z;
+            w[4 * u + 3] = x.w;
+          }
+#pragma unroll
+          for (int x = 0; x < 32; x++) {
+            w[x] = bf16x2_to_f16x2(w[x]);
+            most = __hmax2(most, __habs2(*reinterpret_cast<const __half2*>(&w[x])));
+          }
+        }
+        tmem_st32(quarter + PA_Q_COL + 32 * g, w);
+      }
+      const bool big = __hisinf(__hmax(__low2half(most), __high2half(most))) != 0;
+      if (bar_any(pair_bar, 64, big)) {
+        // heads with a |q| of 2^16 or more, out of f16's range: once more, times a power of two that puts the
+        // largest into [2^15, 2^16), and their scale times its inverse.  (An infinity stays one.)
+        uint32_t size = 0u;                           // largest |q|, bf16 bits
+        if (there) {
+#pragma unroll 1
+          for (uint32_t x = 0; x < 128; x++) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(qh + (x >> 5) * PA_COL + sw128((uint32_t)head, 4u * (x & 31u)));
+            size = max(size, max(w & 0x7FFFu, w >> 16 & 0x7FFFu));
+          }
+        }
+        sm.top[half][head] = __uint_as_float(size);
+        named_sync(pair_bar, 64);
+        size = max(size, __float_as_uint(sm.top[half ^ 1][head]));
+        named_sync(pair_bar, 64);                     // (the maxima of a chunk go there next)
+        const int e = max(min((int)(size >> 7), 254) - 142, 0);
+        const float down = __int_as_float((127 - e) << 23);
+        sc2 = fmaxf(fminf(sc2 * __int_as_float((127 + e) << 23), FLT_MAX), -FLT_MAX);
+        tc::tmem_wait_st();
+#pragma unroll 1
+        for (int g = 0; g < 4; g++) {
+          uint32_t w[32] = {};
+          if (there) {
+#pragma unroll
+            for (int x = 0; x < 32; x++) {
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(qh + g * PA_COL + sw128((uint32_t)head, 4u * x));
+              w[x] = pack_f16x2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down);
+            }
+          }
+          tmem_st32(quarter + PA_Q_COL + 32 * g, w);
+        }
+      }
+      tc::tmem_wait_st();
+      tc::fence_proxy_async_smem();                   // the buffers go to copies and stores of others
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        tc::bar_arrive(&sm.q_here);
+        arrive_first(&sm.q_moved);
+      }
+    }
+    // the scales of this lane's four blocks of keys of chunk c (rows, and what the query does not see: 1)
+    auto scales = [&](int c, float* s) {
+      const bool entries = c < n_ch && !run.rows(c);
+      const int64_t k0 = entries ? run.first(c) + 32 * half : 0;
+      const float* at = p.scales8 + (int64_t)b * (p.cap / BLK) + k0 / BLK;
+#pragma unroll
+      for (int i = 0; i < 4; i++) s[i] = entries && k0 + BLK * i < mine.entries ? __ldcg(at + i) : 1.f;
+    };
+    float s8_next[4];
+    scales(0, s8_next);
+    for (int c = 0; c < n_ch; c++) {
+      float s8[4], by[4];                             // scales, and what turns products into scores
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        s8[i] = s8_next[i];
+        by[i] = fmaxf(fminf(sc2 * s8[i], FLT_MAX), -FLT_MAX);   // finite: a product may be 0
+      }
+      // keys of this lane that the query sees: x_lo .. x_hi - 1 of 32
+      const bool rows = run.rows(c);
+      const int64_t k0 = run.first(c) + 32 * half;
+      const int x_lo = rows ? (int)max(min(mine.row_lo - k0, (int64_t)32), (int64_t)0) : 0;
+      // (a part's chunk may end before rows that the query sees in the other part)
+      const int x_hi = (int)max(min((rows ? mine.row_hi : mine.entries) - k0, (int64_t)min(run.keys(c) - 32 * half, 32)), (int64_t)0);
+      const uint32_t s_addr = quarter + PA_S_COL + 64 * (c & 1);
+      wait(&sm.s_full[c & 1], c >> 1, 89);
+      tc::fence_after_sync();
+      scales(c + 1, s8_next);
+      float v[32];
+      {
+        // every lane holds its half of the dims' part of 64 keys: 32 of them go to the other lane
+        uint32_t s0[32], s1[32];
+        tc::tmem_ld_x32_nowait(s_addr, s0);
+        tc::tmem_ld_x32_nowait(s_addr + 32, s1);
+        tc::tmem_wait_ld_regs(s0);
+        tc::tmem_wait_ld_regs(s1);
+#pragma unroll
+        for (int x = 0; x < 8; x++) {
+          float4 f;
+          f.x = __uint_as_float(half ? s0[4 * x] : s1[4 * x]);
+          f.y = __uint_as_float(half ? s0[4 * x + 1] : s1[4 * x + 1]);
+          f.z = __uint_as_float(half ? s0[4 * x + 2] : s1[4 * x + 2]);
+          f.w = __uint_as_float(half ? s0[4 * x + 3] : s1[4 * x + 3]);
+          xs[x * 128 + me] = f;
+        }
+        named_sync(pair_bar, 64);
+#pragma unroll
+        for (int x = 0; x < 8; x++) {
+          const float4 f = xs[x * 128 + other];
+          const float got[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int y = 0; y < 4; y++)                 // (not to be fused with the reference's subtraction)
+            v[4 * x + y] = __fmul_rn(__uint_as_float(half ? s1[4 * x + y] : s0[4 * x + y]) + got[y], by[(4 * x + y) / BLK]);
+        }
+      }
+      if (!__all_sync(0xFFFFFFFFu, x_lo == 0 && x_hi == 32)) {
+#pragma unroll
+        for (int x = 0; x < 32; x++) v[x] = x >= x_lo && x < x_hi ? v[x] : -INFINITY;
+      }
+      float cm = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        float m4 = v[8 * i];
+#pragma unroll
+        for (int x = 1; x < 8; x++) m4 = fmaxf(m4, v[8 * i + x]);
+        cm = fmaxf(cm, m4 + log2f(fmaxf(s8[i], KA_FLOOR8)));
+      }
+      float alpha = 1.f;
+      // the reference moves when a score of the head lies far above it, or when it has none (rare, but for the
+      // first chunk): then both lanes of every head of the two warps look at both maxima
+      if (bar_any(pair_bar, 64, cm > -INFINITY && !(cm - m_used <= KA_MOST))) {
+        sm.top[half][head] = cm;
+        named_sync(pair_bar, 64);
+        cm = fmaxf(cm, sm.top[half ^ 1][head]);
+        const float to = fabsf(cm) < 0x1p26f ? cm - KA_TOP : cm;
+        if (m_used == -INFINITY) {
+          m_used = to;                                // O holds nothing yet, or only zeros
+        } else if (cm - m_used > KA_MOST) {
+          alpha = ex2_ftz(m_used - to);
+          m_used = to;
+          l_sum *= alpha;
+        }
+        if (__any_sync(0xFFFFFFFFu, alpha != 1.f) && c > 0) {   // after the chunk before is in O
+          wait(&sm.free_[(c - 1) % PA_BUFS], (c - 1) / PA_BUFS, 90);
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int g = 0; g < D / 2; g += 32) {
+            uint32_t o[32];
+            tmem_ld32(quarter + PA_O_COL + g, o);
+#pragma unroll
+            for (int x = 0; x < 32; x++) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+            tmem_st32(quarter + PA_O_COL + g, o);
+          }
+        }
+      }
+      const float ref = m_used == -INFINITY ? 0.f : m_used;
+      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t pk[16];
+#pragma unroll
+      for (int x = 0; x < 16; x++) {
+        const float e0 = ex2_ftz(v[2 * x] - ref), e1 = ex2_ftz(v[2 * x + 1] - ref);
+        l4[x & 3] += e0 + e1;
+        pk[x] = pack_f16x2(e0 * s8[2 * x / BLK], e1 * s8[2 * x / BLK]);
+      }
+      l_sum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+#pragma unroll
+      for (int x = 0; x < 4; x++) xp[x * 128 + me] = make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+      named_sync(pair_bar, 64);
+      {
+        uint32_t pw[32];                              // P of all 64 keys, over S
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          const uint4 g = xp[x * 128 + other];
+          const uint32_t got[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+          for (int y = 0; y < 4; y++) {
+            pw[4 * x + y] = half ? got[y] : pk[4 * x + y];
+            pw[16 + 4 * x + y] = half ? pk[4 * x + y] : got[y];
+          }
+        }
+        tmem_st32(s_addr, pw);
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_first(&sm.p_ready[c & 1]);
+    }
+    sm.sum[half][head] = l_sum;
+    sm.top[half][head] = m_used;                      // (both lanes of a head have the same)
+  }
+
+  if (warp < PA_OUT_WARPS) {
+    // ================= output: 128 of a lane's 256 dims a warp
+    if (n_ch > 0) {
+      const int last = n_ch - 1;
+      if (*(volatile int*)&sm.err == 0) wait(&sm.free_[last % PA_BUFS], last / PA_BUFS, 91);
+      tc::fence_after_sync();
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    named_sync(2, 32 * PA_OUT_WARPS);                 // the sums
+    const int qt = warp & 3, half = qt >> 1, head0 = 32 * (qt & 1), head = head0 + lane, g0 = 128 * (warp >> 2);
+    const uint32_t o_addr = ((uint32_t)(qt * 32) << 16) + PA_O_COL + g0;
+    float l = sm.sum[0][head] + sm.sum[1][head];
+    if (*(volatile int*)&sm.poison != 0) l = __int_as_float(0x7FC00000);
+    if (there && half == 0 && g0 == 0) {
+      const float m = sm.top[0][head];
+      if (split > 1) {
+        part[head] = m;
+        part[H + head] = l;
+      } else if (p.lse) {                             // l = 0: no visible key
+        p.lse[bq * H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * KA_LN2;
+      }
+    }
+    if (!there) {
+    } else if (split == 1) {
+      const float inv = 1.0f / l;
+      const bool none = l == 0.f;                     // no visible key: zeros
+      unsigned char* mine8 = smem + warp * 8192;      // over the K buffers, whose last reader is done
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        if (n_ch > 0) tmem_ld32(o_addr + c, o);
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          float f[8];
+#pragma unroll
+          for (int y = 0; y < 8; y++) f[y] = none ? 0.f : __uint_as_float(o[8 * x + y]) * inv;
+          *reinterpret_cast<uint4*>(mine8 + lane * 256 + ((((c >> 3) + x) ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+        }
+      }
+      __syncwarp();
+      uint4* out = reinterpret_cast<uint4*>(p.out + (bq * H + head0) * D) + (D / 16) * half + g0 / 8;
+#pragma unroll 4
+      for (int x = 0; x < 16; x++) {                  // two rows of 256 bytes an instruction
+        const int row = 2 * x + (lane >> 4), u = lane & 15;
+        out[row * (D / 8) + u] = *reinterpret_cast<const uint4*>(mine8 + row * 256 + ((u ^ (row & 7)) << 4));
+      }
+    } else if (n_ch > 0) {
+      // a partial state: O as [dims / 4][head][4]
+      float4* out = reinterpret_cast<float4*>(part + 2 * H) + ((D / 8) * half + g0 / 4) * H + head;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_addr + c, o);
+#pragma unroll
+        for (int x = 0; x < 8; x++)
+          out[(c / 4 + x) * H] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                             __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  // after a timeout copies may be in flight that nobody waited for: time for them to land
+  if (*(volatile int*)&sm.err != 0)
+    for (int i = 0; i < 1000; i++) __nanosleep(1000);
+  tc::cluster_sync();                                 // (nothing of the other CTA's is on its way here once both are done)
+  if (warp == PA_MMA_WARP) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc_pair(0u, 512);
+  }
+}
+
+cudaError_t launch_pair_attention(const KeysParams& p, int B, const CUtensorMap& mq, const CUtensorMap& mr, const CUtensorMap& mc,
+                                  cudaStream_t stream) {
+  static PerDeviceOnce attrs;
+  cudaError_t e = attrs.ensure([](int) {
+    return cudaFuncSetAttribute(pair_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)B * ((p.Q + 1) / 2) * p.split * 2));
+  cfg.blockDim = dim3(PA_THREADS);
+  cfg.dynamicSmemBytes = PA_SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, pair_attn_kernel, p, mq, mr, mc);
+}
+
+}  // namespace csa2

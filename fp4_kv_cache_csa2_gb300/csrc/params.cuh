@@ -1,6 +1,8 @@
 // Launch parameters and launcher declarations shared by the CSA2 translation units.
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace csa2 {
@@ -219,6 +221,10 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
 cudaError_t launch_window_ring(const KeysParams& p, int B, cudaStream_t stream);
 bool window_ring_fits(int64_t W, int n_sink);
 size_t keys_part_bytes(int64_t BQ, int64_t chunks);
+size_t cache8_part_bytes(int B, int Q, int64_t chunks);   // of a call with scales8
+// Several queries of an 8-bit cache (p.split and p.part set; the maps of q, the rows and the codes)
+cudaError_t launch_pair_attention(const KeysParams& p, int B, const CUtensorMap& mq, const CUtensorMap& mr,
+                                  const CUtensorMap& mc, cudaStream_t stream);
 struct AwPlan { int runs, splits; };    // of a sequence's tiles, of its queries
 AwPlan attn_weights_plan(int B, int Q, int64_t max_n);
 int64_t attn_weights_pitch(int64_t max_n);

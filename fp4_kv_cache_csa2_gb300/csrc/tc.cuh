@@ -195,6 +195,12 @@ __device__ __forceinline__ void bar_arrive_first(uint64_t* bar) {
                " mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n}\n" :: "r"(smem_u32(bar)) : "memory");
 }
 
+// *p = x in the shared memory of the cluster's CTA `rank`, before anything this thread does next.
+__device__ __forceinline__ void store_other(int* p, int x, int rank) {
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %2;\n st.relaxed.cluster.shared::cluster.s32 [a], %1;\n"
+               " fence.acq_rel.cluster;\n}\n" :: "r"(smem_u32(p)), "r"(x), "r"(rank) : "memory");
+}
+
 // A load into this CTA's shared memory that completes on the barrier at `bar`'s place in CTA 0 of the
 // pair (bit 24 of a shared::cluster address tells the two apart).
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,

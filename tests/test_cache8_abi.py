@@ -116,7 +116,7 @@ def test_attention_workspace(lib):
     assert lib.csa2_cache8_attn(c, ctypes.byref(attn_args(max_n=5000)), WS, need - 1, None) == 3
     assert lib.csa2_cache8_attn(c, ctypes.byref(attn_args(B=0, q=None, out=None)), WS, 256, None) == 0
     assert csa2.cache8_attn_workspace_size(1, 1, 8, -1) == 0 and csa2.cache8_attn_workspace_size(1, 1, -8, 0) == 0
-    assert csa2.cache8_attn_workspace_size(2, 3, 5000, 128) == csa2.dense_attn_workspace_size(2, 3, 5000)
+    assert csa2.cache8_attn_workspace_size(6, 1, 5000, 128) == csa2.dense_attn_workspace_size(6, 1, 5000)
     assert csa2.cache8_attn_workspace_size(2, 3, (1 << 63) - 1, 0) <= 256 + 4 * 152 * (2 * 64 + 64 * 512) * 4
 
 

@@ -224,6 +224,40 @@ def test_attention_what_is_not_seen_may_hold_anything():
     attend_and_check(codes, scales, n, 1, q, rows, base, pos, 9)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attention_rows_that_only_the_newer_query_sees(bad, fp8):
+    """A window row that is not finite: the queries that see it become NaN, their neighbours stay as they are."""
+    if fp8 and bad == float("inf"):
+        pytest.skip("E4M3 has no infinity")
+    pos = np.array([[80, 81, 82, 83, 84]])
+    codes, scales, q, rows, base = attn_case(14, 1, 5, 96, [90], 1, 16, fp8, pos)
+    clean, _ = attend_and_check(codes, scales, [90], 1, q, rows, base, pos, 16)
+    rows = rows.clone()
+    rows[0, 83 - int(base[0]), 300] = 0x7F if fp8 else bad
+    out = torch.zeros(1, 5, H, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(1, 5, H, device="cuda")
+    ws = csa2.Workspace(csa2.cache8_attn_workspace_size(1, 5, 96, 16))
+    csa2.cache8_attn(cache_of(codes, scales, [90]), q.cuda(), dev(pos), SCALE, out, ws, max_n=96, W=16, swa=rows.cuda(),
+                     swa_base_pos=dev(base), lse=lse)
+    assert ws.sync_status()[0] == 0
+    assert torch.equal(out[0, :3], clean[0, :3]) and torch.all(torch.isnan(out[0, 3:])) and torch.all(torch.isnan(lse[0, 3:]))
+
+
+@pytest.mark.parametrize("W,fp8", [(0, False), (40, False), (200, True)])
+def test_attention_neighbours_far_apart(W, fp8):
+    """Two queries of a pair whose windows lie apart, meet or overlap, one of them padding, and queries in no order."""
+    pos = np.array([[600, 10, 300, 341, 5, -1, 44, 45, -7]])
+    n = [512]
+    codes, scales, q, rows, base = attn_case(15, 1, 9, 512, n, 1, W, fp8, pos)
+    if W:
+        base = np.zeros(1, np.int64)
+        g = torch.Generator().manual_seed(16)
+        rows = latents(g, 1, 601)
+        rows = rows.to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else rows
+    attend_and_check(codes, scales, n, 1, q, rows, base, pos, W)
+
+
 def test_attention_reports():
     pos = np.array([[63]])
     codes, scales, q, _, _ = attn_case(8, 1, 1, 64, [70], 1, 0, False, pos)
