@@ -15,15 +15,16 @@
 //     lanes 0 .. 63 hold O's dims 0 .. 255, the others 256 .. 511
 // 1,079 cycles of MMAs a chunk for two queries on two SMs, against 2,074 for one on one; each CTA stages and
 // widens half of a chunk (512 cycles of shared memory instead of 1024), and the products read half (512).
-// The lanes of a head sit in two warps, which pass each other 32 partial scores and 32 weights through
+// The lanes of a head sit in different warps, which pass each other partial scores and weights through
 // shared memory (384 cycles).
 //
 // Both queries share the keys, each with its own limits: what one of them does not see has weight 0
 // for it.  So no key may hold an infinity or a NaN: codes cannot, and of window rows
 // such values are written as 0 and every output of the queries that see the row becomes NaN.
 //
-// Roles of each CTA's warps as there: 0..3 move Q, then softmax (lane of TMEM = lane of the
-// warp); 4..11 fill; 0..7 write the output; 12 issues the MMAs (in CTA 0); 13 the copies.
+// Roles of each CTA's warps: 0..7 move Q, then softmax (two a quarter of the lanes, a half of a lane's
+// keys each: four alone take 2,200 cycles a chunk), then write the output; 8..15 fill; 16 issues the MMAs (in
+// CTA 0); 17 the copies.
 #include <cfloat>
 
 #include "attn_common.cuh"
@@ -32,7 +33,7 @@
 
 namespace csa2 {
 
-constexpr int PA_SOFT_WARPS = 4, PA_FILL_WARPS = 8, PA_OUT_WARPS = 8;
+constexpr int PA_SOFT_WARPS = 8, PA_FILL_WARPS = 8;
 constexpr int PA_FILL = 32 * PA_FILL_WARPS;
 constexpr int PA_MMA_WARP = PA_SOFT_WARPS + PA_FILL_WARPS, PA_COPY_WARP = PA_MMA_WARP + 1;
 constexpr int PA_THREADS = 32 * (PA_COPY_WARP + 1);
@@ -43,9 +44,9 @@ constexpr int PA_BUFS = 4;                                // the last two take Q
 constexpr int PA_STAGE = 2 * PA_COL;                      // a chunk's 256 codes a key, SW128
 constexpr int PA_STAGES = 2;
 constexpr int PA_OFF_STAGE = PA_BUFS * PA_BUF;
-constexpr int PA_OFF_S = PA_OFF_STAGE + PA_STAGES * PA_STAGE;   // partial scores for the other lane: [8][128 lanes] float4
-constexpr int PA_OFF_P = PA_OFF_S + 8 * 128 * 16;         // weights for the other lane: [4][128 lanes] uint4
-constexpr int PA_OFF_SMALL = PA_OFF_P + 4 * 128 * 16;
+constexpr int PA_OFF_S = PA_OFF_STAGE + PA_STAGES * PA_STAGE;   // partial scores for the other lane: [4][256 threads] float4
+constexpr int PA_OFF_P = PA_OFF_S + 4 * 256 * 16;         // weights for the other lane: [2][256 threads] uint4
+constexpr int PA_OFF_SMALL = PA_OFF_P + 2 * 256 * 16;
 constexpr int PA_O_COL = 0, PA_Q_COL = 256, PA_S_COL = 384;
 constexpr int PA_AHEAD = 6;                               // chunks of codes that are on their way to L2
 
@@ -57,7 +58,8 @@ struct PaSmall {
   uint64_t free_[PA_BUFS];            // O of the chunk in K buffer i is done (told to both)
   uint64_t s_full[2], p_ready[2];     // S of every second chunk is done (told to both); its P is written (CTA 0's counts)
   uint64_t q_here;                    // this CTA's softmax warps have read Q
-  float sum[2][H], top[2][H];         // of the softmax, a half of the keys each; maxima on their way to the other lane
+  float sum[4][H], top[4][H];         // of the softmax, a quarter of the keys each; maxima on their way to the others
+  float ref[H];                       // the heads' references
   uint32_t tmem_base;
   int err, poison;                    // a row that is not finite lies before this CTA's query
 };
@@ -69,10 +71,10 @@ __device__ __noinline__ bool pa_timeout(int* err, WsHeader* hdr, int where) {
   return false;
 }
 
-// What one query sees: window rows row_lo .. row_hi - 1 of the buffer, entries 0 .. entries - 1.
+// What one query sees: window rows row_lo .. row_hi - 1 of the buffer, entries 0 .. entries - 1 (each below 2^31).
 struct PaQuery {
   int64_t t, lo;                      // position (-1: none), first window position
-  int64_t row_lo, row_hi, entries;
+  int row_lo, row_hi, entries;
 };
 
 __device__ __forceinline__ PaQuery pa_query(const KeysParams& p, int b, int64_t base, int i) {
@@ -85,55 +87,53 @@ __device__ __forceinline__ PaQuery pa_query(const KeysParams& p, int b, int64_t 
     const uint64_t s = (uint64_t)p.S, r0 = q.lo > base ? (uint64_t)q.lo - (uint64_t)base : 0;
     const uint64_t end = (uint64_t)q.t - (uint64_t)base, r1 = end < s ? end + 1 : s;
     if (r0 < r1) {
-      q.row_lo = (int64_t)r0;
-      q.row_hi = (int64_t)r1;
+      q.row_lo = (int)r0;
+      q.row_hi = (int)r1;
     }
   }
-  q.entries = visible_entries(min(q.t, INT64_MAX - 1), p.m, p.n_entries[b]);
-  q.entries = max(min(q.entries, p.cap), (int64_t)0);
+  const int64_t n = visible_entries(min(q.t, INT64_MAX - 1), p.m, p.n_entries[b]);
+  q.entries = (int)max(min(n, p.cap), (int64_t)0);
   return q;
 }
 
 // The pair's keys: rows a0 .. (chunks before ca), rows b0 .. (before cb), entries; a CTA's run of their
 // chunks is [c0, c0 + n).
 struct PaRun {
-  int64_t a0, an, b0, bn, en;         // first row and number of rows of either part; entries
-  int64_t ca, cb;
-  int64_t c0;
-  int n;
+  int a0, an, b0, bn, en;             // first row and number of rows of either part; entries
+  int ca, cb, c0, n;
   __device__ __forceinline__ bool rows(int c) const { return c0 + c < cb; }
   // row or entry of the chunk's first key, keys of the chunk
-  __device__ __forceinline__ int64_t first(int c) const {
-    const int64_t k = c0 + c;
-    return k < ca ? a0 + PA_KEYS * k : k < cb ? b0 + PA_KEYS * (k - ca) : PA_KEYS * (k - cb);
+  __device__ __forceinline__ int first(int c) const {
+    const int k = c0 + c;
+    return k >= cb ? PA_KEYS * (k - cb) : k < ca ? a0 + PA_KEYS * k : b0 + PA_KEYS * (k - ca);
   }
   __device__ __forceinline__ int keys(int c) const {
-    const int64_t k = c0 + c, left = k < ca ? an - PA_KEYS * k : k < cb ? bn - PA_KEYS * (k - ca) : en - PA_KEYS * (k - cb);
-    return left < PA_KEYS ? (int)left : PA_KEYS;
+    const int k = c0 + c;
+    return min(k >= cb ? en - PA_KEYS * (k - cb) : k < ca ? an - PA_KEYS * k : bn - PA_KEYS * (k - ca), PA_KEYS);
   }
 };
 
 __device__ __forceinline__ PaRun pa_run(const PaQuery* q, int sp, int split) {
   PaRun r{};
-  const int64_t n0 = q[0].row_hi - q[0].row_lo, n1 = q[1].row_hi - q[1].row_lo;
+  const int n0 = q[0].row_hi - q[0].row_lo, n1 = q[1].row_hi - q[1].row_lo;
   r.a0 = q[0].row_lo;
   r.an = n0;
   r.b0 = q[1].row_lo;
   r.bn = n1;
   if (n0 > 0 && n1 > 0) {
-    const int64_t lo = min(q[0].row_lo, q[1].row_lo), hi = max(q[0].row_hi, q[1].row_hi);
-    if (hi - lo <= n0 + n1) {         // windows that overlap or meet: one part.  (Else rows of one are none of the other's)
+    const int lo = min(q[0].row_lo, q[1].row_lo), hi = max(q[0].row_hi, q[1].row_hi);
+    if ((int64_t)hi - lo <= (int64_t)n0 + n1) {   // windows that overlap or meet: one part.  (Else rows of one are none of the other's)
       r.a0 = lo;
       r.an = hi - lo;
       r.bn = 0;
     }
   }
   r.en = max(q[0].entries, q[1].entries);
-  r.ca = ceil_div(r.an, PA_KEYS);
-  r.cb = r.ca + ceil_div(r.bn, PA_KEYS);
-  const int64_t nc = r.cb + ceil_div(r.en, PA_KEYS), each = nc / split, more = nc % split;
-  r.c0 = sp * each + min((int64_t)sp, more);
-  r.n = (int)(each + (sp < more ? 1 : 0));
+  r.ca = (int)ceil_div(r.an, PA_KEYS);
+  r.cb = r.ca + (int)ceil_div(r.bn, PA_KEYS);
+  const uint32_t nc = (uint32_t)r.cb + (uint32_t)ceil_div(r.en, PA_KEYS), each = nc / (uint32_t)split, more = nc % (uint32_t)split;
+  r.c0 = sp * (int)each + min(sp, (int)more);
+  r.n = (int)each + (sp < (int)more ? 1 : 0);
   return r;
 }
 
@@ -258,12 +258,12 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       auto ahead = [&](int c) {                       // (each CTA sends for half of the keys, whole)
         if (c >= n_ch || run.rows(c)) return;
         const int keys = run.keys(c), k0 = rank ? keys / 2 : 0, k1 = rank ? keys : keys / 2;
-        if (k1 > k0) tc::prefetch_l2(kv + (run.first(c) + k0) * D, (uint32_t)((k1 - k0) * D));
+        if (k1 > k0) tc::prefetch_l2(kv + (int64_t)(run.first(c) + k0) * D, (uint32_t)((k1 - k0) * D));
       };
       for (int c = 1; c < PA_AHEAD; c++) ahead(c);
       uint32_t staged = 0;
       for (int c = 0; c < n_ch; c++) {
-        const int64_t first = run.first(c);
+        const int first = run.first(c);
         ahead(c + PA_AHEAD);
         if (!run.rows(c)) {
           const uint32_t s = staged % PA_STAGES;
@@ -322,8 +322,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           *reinterpret_cast<uint4*>(dst + sw128((uint32_t)key8, 32u * i + 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
       } else {
-        const int64_t first = run.first(c);
-        const int keys = run.keys(c);
+        const int first = run.first(c), keys = run.keys(c);
         wait(&sm.row_full[buf], use, 87);             // (rows come first: copy `use` of the buffer too)
         // a value that is not finite: 0, and the queries that see its row are told
         auto finite = [&](uint32_t w, int row) -> uint32_t {
@@ -387,20 +386,23 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       if (lane == 0) arrive_first(&sm.full[buf]);
     }
   } else {
-    // ================= softmax: lane of TMEM l = 32 warp + lane: head l % 64, half l / 64 (of Q's dims, of the keys)
-    const uint32_t quarter = (uint32_t)(warp * 32) << 16;
-    const int half = warp >> 1, head = 32 * (warp & 1) + lane, me = 32 * warp + lane, other = me ^ 64;
-    const int pair_bar = 3 + (warp & 1);              // named barrier of the two warps of a head's lanes
+    // ================= softmax: lane of TMEM l = 32 (warp % 4) + lane: head l % 64, half l / 64 (of Q's dims, of the
+    // keys); of its 32 keys and its columns of Q and O the warp takes the half `sub`
+    const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
+    const int half = warp >> 1 & 1, sub = warp >> 2, head = 32 * (warp & 1) + lane, other = tid ^ 64;
+    const int two = 3 + (warp & 1) + 2 * sub;         // named barrier of the two warps that have a head's lanes for the same keys
+    const int four = 7 + (warp & 1);                  // of the four that have a head
+    const int own = 2 * half + sub;                   // quarter of the keys
     float4* xs = reinterpret_cast<float4*>(smem + PA_OFF_S);
     uint4* xp = reinterpret_cast<uint4*>(smem + PA_OFF_P);
-    float sc2 = p.scale * KA_LOG2E;                 // products to scores in powers of two
+    float sc2 = p.scale * KA_LOG2E;                   // products to scores in powers of two
     float m_used = -INFINITY, l_sum = 0.f;
-    if (n_ch > 0) {                                   // Q: this lane's 256 dims of its head to TMEM
+    if (n_ch > 0) {                                   // Q: 128 dims of this lane's head to TMEM
       if (there) wait(&sm.q_full, 0, 88);
       const unsigned char* qh = smem + (PA_BUFS - 2 + half) * PA_BUF;
       __half2 most = __half2half2(__ushort_as_half(0));
 #pragma unroll 1
-      for (int g = 0; g < 4; g++) {
+      for (int g = 2 * sub; g < 2 * sub + 2; g++) {
         uint32_t w[32] = {};
         if (there) {
 #pragma unroll
@@ -420,27 +422,28 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         tmem_st32(quarter + PA_Q_COL + 32 * g, w);
       }
       const bool big = __hisinf(__hmax(__low2half(most), __high2half(most))) != 0;
-      if (bar_any(pair_bar, 64, big)) {
+      if (bar_any(four, 128, big)) {
         // heads with a |q| of 2^16 or more, out of f16's range: once more, times a power of two that puts the
         // largest into [2^15, 2^16), and their scale times its inverse.  (An infinity stays one.)
         uint32_t size = 0u;                           // largest |q|, bf16 bits
         if (there) {
 #pragma unroll 1
-          for (uint32_t x = 0; x < 128; x++) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(qh + (x >> 5) * PA_COL + sw128((uint32_t)head, 4u * (x & 31u)));
+          for (uint32_t x = 0; x < 64; x++) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(qh + (2 * sub + (x >> 5)) * PA_COL + sw128((uint32_t)head, 4u * (x & 31u)));
             size = max(size, max(w & 0x7FFFu, w >> 16 & 0x7FFFu));
           }
         }
-        sm.top[half][head] = __uint_as_float(size);
-        named_sync(pair_bar, 64);
-        size = max(size, __float_as_uint(sm.top[half ^ 1][head]));
-        named_sync(pair_bar, 64);                     // (the maxima of a chunk go there next)
+        sm.top[own][head] = __uint_as_float(size);
+        named_sync(four, 128);
+#pragma unroll
+        for (int i = 0; i < 4; i++) size = max(size, __float_as_uint(sm.top[i][head]));
+        named_sync(four, 128);                        // (the maxima of a chunk go there next)
         const int e = max(min((int)(size >> 7), 254) - 142, 0);
         const float down = __int_as_float((127 - e) << 23);
         sc2 = fmaxf(fminf(sc2 * __int_as_float((127 + e) << 23), FLT_MAX), -FLT_MAX);
         tc::tmem_wait_st();
 #pragma unroll 1
-        for (int g = 0; g < 4; g++) {
+        for (int g = 2 * sub; g < 2 * sub + 2; g++) {
           uint32_t w[32] = {};
           if (there) {
 #pragma unroll
@@ -461,80 +464,76 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         arrive_first(&sm.q_moved);
       }
     }
-    // the scales of this lane's four blocks of keys of chunk c (rows, and what the query does not see: 1)
+    // the scales of this lane's two blocks of keys of chunk c (rows, and what the query does not see: 1)
+    const float* scale_row = p.scales8 + (int64_t)b * (p.cap / BLK);
+    const int k_own = 32 * half + 16 * sub;
     auto scales = [&](int c, float* s) {
-      const bool entries = c < n_ch && !run.rows(c);
-      const int64_t k0 = entries ? run.first(c) + 32 * half : 0;
-      const float* at = p.scales8 + (int64_t)b * (p.cap / BLK) + k0 / BLK;
+      const int k0 = c < n_ch && !run.rows(c) ? run.first(c) + k_own : INT32_MAX - 16;
 #pragma unroll
-      for (int i = 0; i < 4; i++) s[i] = entries && k0 + BLK * i < mine.entries ? __ldcg(at + i) : 1.f;
+      for (int i = 0; i < 2; i++) s[i] = k0 + BLK * i < mine.entries ? __ldcg(scale_row + k0 / BLK + i) : 1.f;
     };
-    float s8_next[4];
+    float s8_next[2];
     scales(0, s8_next);
     for (int c = 0; c < n_ch; c++) {
-      float s8[4], by[4];                             // scales, and what turns products into scores
+      float s8[2], by[2], up[2];                      // scales, what turns products into scores, log2 of the scales
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
+      for (int i = 0; i < 2; i++) {
         s8[i] = s8_next[i];
         by[i] = fmaxf(fminf(sc2 * s8[i], FLT_MAX), -FLT_MAX);   // finite: a product may be 0
+        up[i] = __log2f(fmaxf(s8[i], KA_FLOOR8));     // (of the reference alone: any value near it would do)
       }
-      // keys of this lane that the query sees: x_lo .. x_hi - 1 of 32
+      // keys of this lane that the query sees: x_lo .. x_hi - 1 of 16.  (A part's chunk may end before rows that
+      // the query sees in the other part)
       const bool rows = run.rows(c);
-      const int64_t k0 = run.first(c) + 32 * half;
-      const int x_lo = rows ? (int)max(min(mine.row_lo - k0, (int64_t)32), (int64_t)0) : 0;
-      // (a part's chunk may end before rows that the query sees in the other part)
-      const int x_hi = (int)max(min((rows ? mine.row_hi : mine.entries) - k0, (int64_t)min(run.keys(c) - 32 * half, 32)), (int64_t)0);
+      const int k0 = run.first(c) + k_own;
+      const int x_lo = rows ? mine.row_lo - k0 : 0;
+      const int x_hi = min((rows ? mine.row_hi : mine.entries) - k0, run.keys(c) - k_own);
       const uint32_t s_addr = quarter + PA_S_COL + 64 * (c & 1);
       wait(&sm.s_full[c & 1], c >> 1, 89);
       tc::fence_after_sync();
       scales(c + 1, s8_next);
-      float v[32];
+      float v[16];
       {
-        // every lane holds its half of the dims' part of 64 keys: 32 of them go to the other lane
-        uint32_t s0[32], s1[32];
-        tc::tmem_ld_x32_nowait(s_addr, s0);
-        tc::tmem_ld_x32_nowait(s_addr + 32, s1);
-        tc::tmem_wait_ld_regs(s0);
-        tc::tmem_wait_ld_regs(s1);
+        // every lane has its half of the dims' part of each score: those of 16 keys go to the other lane
+        uint32_t s0[16], s1[16];
+        tmem_ld_x16_nowait(s_addr + 32 * (half ^ 1) + 16 * sub, s0);
+        tmem_ld_x16_nowait(s_addr + k_own, s1);
+        tmem_wait_ld16(s0, s1);
 #pragma unroll
-        for (int x = 0; x < 8; x++) {
-          float4 f;
-          f.x = __uint_as_float(half ? s0[4 * x] : s1[4 * x]);
-          f.y = __uint_as_float(half ? s0[4 * x + 1] : s1[4 * x + 1]);
-          f.z = __uint_as_float(half ? s0[4 * x + 2] : s1[4 * x + 2]);
-          f.w = __uint_as_float(half ? s0[4 * x + 3] : s1[4 * x + 3]);
-          xs[x * 128 + me] = f;
-        }
-        named_sync(pair_bar, 64);
+        for (int x = 0; x < 4; x++)
+          xs[x * 256 + tid] = make_float4(__uint_as_float(s0[4 * x]), __uint_as_float(s0[4 * x + 1]),
+                                          __uint_as_float(s0[4 * x + 2]), __uint_as_float(s0[4 * x + 3]));
+        named_sync(two, 64);
 #pragma unroll
-        for (int x = 0; x < 8; x++) {
-          const float4 f = xs[x * 128 + other];
+        for (int x = 0; x < 4; x++) {
+          const float4 f = xs[x * 256 + other];
           const float got[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
           for (int y = 0; y < 4; y++)                 // (not to be fused with the reference's subtraction)
-            v[4 * x + y] = __fmul_rn(__uint_as_float(half ? s1[4 * x + y] : s0[4 * x + y]) + got[y], by[(4 * x + y) / BLK]);
+            v[4 * x + y] = __fmul_rn(__uint_as_float(s1[4 * x + y]) + got[y], by[(4 * x + y) / BLK]);
         }
       }
-      if (!__all_sync(0xFFFFFFFFu, x_lo == 0 && x_hi == 32)) {
+      if (!__all_sync(0xFFFFFFFFu, x_lo <= 0 && x_hi >= 16)) {
 #pragma unroll
-        for (int x = 0; x < 32; x++) v[x] = x >= x_lo && x < x_hi ? v[x] : -INFINITY;
+        for (int x = 0; x < 16; x++) v[x] = x >= x_lo && x < x_hi ? v[x] : -INFINITY;
       }
       float cm = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        float m4 = v[8 * i];
+      for (int i = 0; i < 2; i++) {
+        float m8 = v[8 * i];
 #pragma unroll
-        for (int x = 1; x < 8; x++) m4 = fmaxf(m4, v[8 * i + x]);
-        cm = fmaxf(cm, m4 + log2f(fmaxf(s8[i], KA_FLOOR8)));
+        for (int x = 1; x < 8; x++) m8 = fmaxf(m8, v[8 * i + x]);
+        cm = fmaxf(cm, m8 + up[i]);
       }
-      float alpha = 1.f;
       // the reference moves when a score of the head lies far above it, or when it has none (rare, but for the
-      // first chunk): then both lanes of every head of the two warps look at both maxima
-      if (bar_any(pair_bar, 64, cm > -INFINITY && !(cm - m_used <= KA_MOST))) {
-        sm.top[half][head] = cm;
-        named_sync(pair_bar, 64);
-        cm = fmaxf(cm, sm.top[half ^ 1][head]);
+      // first chunk): then the four lanes of every head of these warps look at all maxima
+      if (bar_any(four, 128, cm > -INFINITY && !(cm - m_used <= KA_MOST))) {
+        sm.top[own][head] = cm;
+        named_sync(four, 128);
+#pragma unroll
+        for (int i = 0; i < 4; i++) cm = fmaxf(cm, sm.top[i][head]);
         const float to = fabsf(cm) < 0x1p26f ? cm - KA_TOP : cm;
+        float alpha = 1.f;
         if (m_used == -INFINITY) {
           m_used = to;                                // O holds nothing yet, or only zeros
         } else if (cm - m_used > KA_MOST) {
@@ -546,7 +545,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           wait(&sm.free_[(c - 1) % PA_BUFS], (c - 1) / PA_BUFS, 90);
           tc::fence_after_sync();
 #pragma unroll 1
-          for (int g = 0; g < D / 2; g += 32) {
+          for (int g = 128 * sub; g < 128 * sub + 128; g += 32) {
             uint32_t o[32];
             tmem_ld32(quarter + PA_O_COL + g, o);
 #pragma unroll
@@ -557,41 +556,33 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       }
       const float ref = m_used == -INFINITY ? 0.f : m_used;
       float l4[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t pk[16];
+      uint32_t pk[8];
 #pragma unroll
-      for (int x = 0; x < 16; x++) {
+      for (int x = 0; x < 8; x++) {
         const float e0 = ex2_ftz(v[2 * x] - ref), e1 = ex2_ftz(v[2 * x + 1] - ref);
         l4[x & 3] += e0 + e1;
         pk[x] = pack_f16x2(e0 * s8[2 * x / BLK], e1 * s8[2 * x / BLK]);
       }
       l_sum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-#pragma unroll
-      for (int x = 0; x < 4; x++) xp[x * 128 + me] = make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
-      named_sync(pair_bar, 64);
+      xp[tid] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      xp[256 + tid] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+      // P of the 16 keys in this lane and in the other, over S: columns of the keys' pairs.  (A column of S is
+      // read by one of the two warps of a quarter and written by either: all four have read theirs)
+      tmem_st8(s_addr + 8 * own, pk);
+      named_sync(two, 64);
       {
-        uint32_t pw[32];                              // P of all 64 keys, over S
-#pragma unroll
-        for (int x = 0; x < 4; x++) {
-          const uint4 g = xp[x * 128 + other];
-          const uint32_t got[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-          for (int y = 0; y < 4; y++) {
-            pw[4 * x + y] = half ? got[y] : pk[4 * x + y];
-            pw[16 + 4 * x + y] = half ? pk[4 * x + y] : got[y];
-          }
-        }
-        tmem_st32(s_addr, pw);
+        const uint4 a = xp[other], d = xp[256 + other];
+        const uint32_t got[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+        tmem_st8(s_addr + 8 * (own ^ 2), got);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) arrive_first(&sm.p_ready[c & 1]);
     }
-    sm.sum[half][head] = l_sum;
-    sm.top[half][head] = m_used;                      // (both lanes of a head have the same)
-  }
+    sm.sum[own][head] = l_sum;
+    if (own == 0) sm.ref[head] = m_used;              // (all lanes of a head have the same)
 
-  if (warp < PA_OUT_WARPS) {
     // ================= output: 128 of a lane's 256 dims a warp
     if (n_ch > 0) {
       const int last = n_ch - 1;
@@ -599,13 +590,13 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       tc::fence_after_sync();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    named_sync(2, 32 * PA_OUT_WARPS);                 // the sums
-    const int qt = warp & 3, half = qt >> 1, head0 = 32 * (qt & 1), head = head0 + lane, g0 = 128 * (warp >> 2);
-    const uint32_t o_addr = ((uint32_t)(qt * 32) << 16) + PA_O_COL + g0;
-    float l = sm.sum[0][head] + sm.sum[1][head];
+    named_sync(2, 32 * PA_SOFT_WARPS);                // the sums
+    const int head0 = 32 * (warp & 1), g0 = 128 * sub;
+    const uint32_t o_addr = quarter + PA_O_COL + g0;
+    float l = (sm.sum[0][head] + sm.sum[1][head]) + (sm.sum[2][head] + sm.sum[3][head]);
     if (*(volatile int*)&sm.poison != 0) l = __int_as_float(0x7FC00000);
-    if (there && half == 0 && g0 == 0) {
-      const float m = sm.top[0][head];
+    if (there && own == 0) {
+      const float m = sm.ref[head];
       if (split > 1) {
         part[head] = m;
         part[H + head] = l;
@@ -617,7 +608,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     } else if (split == 1) {
       const float inv = 1.0f / l;
       const bool none = l == 0.f;                     // no visible key: zeros
-      unsigned char* mine8 = smem + warp * 8192;      // over the K buffers, whose last reader is done
+      unsigned char* rows8 = smem + warp * 8192;      // over the K buffers, whose last reader is done
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         uint32_t o[32];
@@ -627,7 +618,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           float f[8];
 #pragma unroll
           for (int y = 0; y < 8; y++) f[y] = none ? 0.f : __uint_as_float(o[8 * x + y]) * inv;
-          *reinterpret_cast<uint4*>(mine8 + lane * 256 + ((((c >> 3) + x) ^ (lane & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(rows8 + lane * 256 + ((((c >> 3) + x) ^ (lane & 7)) << 4)) =
               make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
         }
       }
@@ -636,7 +627,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
 #pragma unroll 4
       for (int x = 0; x < 16; x++) {                  // two rows of 256 bytes an instruction
         const int row = 2 * x + (lane >> 4), u = lane & 15;
-        out[row * (D / 8) + u] = *reinterpret_cast<const uint4*>(mine8 + row * 256 + ((u ^ (row & 7)) << 4));
+        out[row * (D / 8) + u] = *reinterpret_cast<const uint4*>(rows8 + row * 256 + ((u ^ (row & 7)) << 4));
       }
     } else if (n_ch > 0) {
       // a partial state: O as [dims / 4][head][4]
