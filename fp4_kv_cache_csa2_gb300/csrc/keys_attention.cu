@@ -605,7 +605,7 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       for (int x = 0; x < 32; x++) c4[E8 ? x / BLK : x & 3] = fmaxf(c4[E8 ? x / BLK : x & 3], v[x]);
       if (E8) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) c4[i] += log2f(fmaxf(s8[i], KA_FLOOR8));
+        for (int i = 0; i < 4; i++) c4[i] += __log2f(fmaxf(s8[i], KA_FLOOR8));   // (of the reference alone: any value near it would do)
       }
       float cm = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
       cm = fmaxf(cm, __shfl_xor_sync(0xFFFFFFFFu, cm, 16));
@@ -854,7 +854,7 @@ constexpr int KA_FIXED = 6, KA_WAVES = 4;
 // slice's CTA lie in shared memory for 608 / (KC_LATENT + 1) states.)
 constexpr int KC_LATENT = 4;
 
-int keys_split(int64_t BQ, int64_t chunks) {
+static int keys_split(int64_t BQ, int64_t chunks, int64_t* cost_out = nullptr) {
   if (BQ <= 0) return 1;
   int best = 1;
   int64_t best_cost = 48 * ceil_div(BQ, KA_SMS) * (KA_FIXED + chunks);   // in 48ths
@@ -865,32 +865,37 @@ int keys_split(int64_t BQ, int64_t chunks) {
       best_cost = cost;
     }
   }
+  if (cost_out) *cost_out = best_cost;
   return best;
 }
 
-// The same for the pairs of CTAs of a call with several queries of an 8-bit cache: a chunk takes 0.75 us, and a
-// pair PAIR_FIXED chunks beside its own; in 48ths of a chunk's time.
-constexpr int PAIR_FIXED = 10;
-static int pair_split(int64_t pairs, int64_t chunks) {
-  const int64_t slots = KA_SMS / 2;
-  int best = 1;
-  int64_t best_cost = 48 * ceil_div(pairs, slots) * (PAIR_FIXED + chunks);
-  for (int s = 2; s <= slots && s <= chunks && pairs * s <= KA_WAVES * slots; s++) {
-    const int64_t cost = 48 * ceil_div(pairs * s, slots) * (PAIR_FIXED + ceil_div(chunks, s)) + 192 + 5 * s + 4 * pairs * s;
-    if (cost < best_cost) {
-      best = s;
-      best_cost = cost;
+// A call over an 8-bit cache: pairs of CTAs with two queries each (pair_attention.cu), or a CTA a query as
+// here, whichever takes less time by the same count.  A pair's chunk takes 0.85 us (1.2 here), and it costs
+// PAIR_FIXED of them, 14 us, beside its own (7 here).  As chosen, us (pairs / single CTAs, each with its best split):
+// 3 x 37 queries of 10,007 entries 108 / 134, 1 x 100 of 4000 71 / 81, 1 x 2 of 8000 24.9 / 19.9, 16 x 2 of
+// 2000 27.5 / 22.6, 1 x 8 of 600 18.0 / 13.4.
+constexpr int PAIR_FIXED = 16;
+struct Cache8Plan { bool pairs; int split; };
+
+static Cache8Plan cache8_plan(int B, int Q, int64_t chunks) {
+  int64_t single = 0;
+  Cache8Plan plan{false, keys_split((int64_t)B * Q, chunks, &single)};
+  const int64_t pairs = (int64_t)B * ((Q + 1) / 2), slots = KA_SMS / 2;
+  if (Q < 2 || B < 1) return plan;
+  int64_t best = 120 * single;                        // 48ths of 1.2 us, in 10 ns
+  for (int s = 1; s <= slots && s <= chunks && (s == 1 || pairs * s <= KA_WAVES * slots); s++) {
+    const int64_t join = s > 1 ? 169 + 4 * s + 3 * pairs * s : 0;
+    const int64_t cost = 85 * (48 * ceil_div(pairs * s, slots) * (PAIR_FIXED + ceil_div(chunks, s)) + join);
+    if (cost < best) {
+      plan = {true, s};
+      best = cost;
     }
   }
-  return best;
-}
-
-static int cache8_split(int B, int Q, int64_t chunks) {
-  return Q > 1 ? pair_split((int64_t)B * ((Q + 1) / 2), chunks) : keys_split((int64_t)B * Q, chunks);
+  return plan;
 }
 
 size_t cache8_part_bytes(int B, int Q, int64_t chunks) {
-  const int s = cache8_split(B, Q, chunks);
+  const int s = cache8_plan(B, Q, chunks).split;
   return s > 1 ? (size_t)((int64_t)B * Q * s) * KA_PART_FLOATS * sizeof(float) : 0;
 }
 
@@ -962,7 +967,8 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
   const int64_t BQ = (int64_t)B * p.Q;
   if (BQ == 0) return cudaSuccess;
   if (keys_in_ring(p, B, BQ)) return launch_window_ring(p, B, stream);
-  p.split = p.scales8 ? cache8_split(B, p.Q, chunks) : keys_split(BQ, chunks);
+  const Cache8Plan plan = p.scales8 ? cache8_plan(B, p.Q, chunks) : Cache8Plan{false, keys_split(BQ, chunks)};
+  p.split = plan.split;
   p.part = reinterpret_cast<float*>(part);
   CUtensorMap mq, mr, ms;
   if (!encode_bf16_rows512(&mq, p.q, (uint64_t)BQ * H, H)) return cudaErrorInvalidValue;
@@ -978,7 +984,7 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
   if (nk == 0) ms = mr;
   if (p.scales8) {                                    // no sinks: their map is the codes'
     if (p.cap > 0 && !encode_u8_rows512_sw128(&ms, p.main_kv, (uint64_t)B * p.cap, KA_KEYS)) return cudaErrorInvalidValue;
-    if (p.Q == 1) return keys_launch<true, true>(p, BQ, mq, mr, ms, stream);
+    if (!plan.pairs) return keys_launch<true, true>(p, BQ, mq, mr, ms, stream);
     const cudaError_t e = launch_pair_attention(p, B, mq, mr, ms, stream);
     return e != cudaSuccess || p.split == 1 ? e : launch_keys_join(p, BQ, stream);
   }

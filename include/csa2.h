@@ -561,7 +561,8 @@ csa2_status csa2_cache8_write(const csa2_cache8 *cache, const csa2_cache8_write_
  * with its padding, outputs, reports, limits and operands (codes are exact in f16;
  * the scales enter the scores and the weights in binary32, before the weights are
  * rounded to 11 bits).  Scales of 2^-60 and more keep that precision (the write
- * makes no others).  n_entries[b] > cap raises CSA2_ERR_BOUNDS (cap entries are
+ * makes no others).  A window row that a query sees has to be finite in f16 (NaN makes the
+ * outputs of the queries that see it NaN).  n_entries[b] > cap raises CSA2_ERR_BOUNDS (cap entries are
  * attended).  Workspace: csa2_cache8_attn_workspace_size with the call's B, Q,
  * max_n and W.
  */

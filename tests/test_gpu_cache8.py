@@ -141,13 +141,14 @@ def attn_case(seed, B, Q, cap, n, m, W, fp8, pos, spread=0.0, q_size=1.5):
     return codes, scales, q, rows, base
 
 
-def attend_and_check(codes, scales, n, m, q, rows, base, pos, W, heads=None, status=0):
+def attend_and_check(codes, scales, n, m, q, rows, base, pos, W, status=0, max_n=None):
     B, Q = pos.shape
+    max_n = max_n or int(max(n))
     cache = cache_of(codes, scales, n, m)
     out = torch.full((B, Q, H, D), 3.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((B, Q, H), 3.0, device="cuda")
-    ws = csa2.Workspace(csa2.cache8_attn_workspace_size(B, Q, int(max(n)), W))
-    csa2.cache8_attn(cache, q.cuda(), dev(pos), SCALE, out, ws, max_n=int(max(n)), W=W,
+    ws = csa2.Workspace(csa2.cache8_attn_workspace_size(B, Q, max_n, W))
+    csa2.cache8_attn(cache, q.cuda(), dev(pos), SCALE, out, ws, max_n=max_n, W=W,
                      swa=None if rows is None else rows.cuda(), swa_base_pos=None if base is None else dev(base), lse=lse)
     assert ws.sync_status()[0] == status
     got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
@@ -224,32 +225,66 @@ def test_attention_what_is_not_seen_may_hold_anything():
     attend_and_check(codes, scales, n, 1, q, rows, base, pos, 9)
 
 
+# Calls that go to pairs of CTAs: enough queries of enough entries (152 of 1200 and more; divided over CTAs, 60 of
+# 3000)
+@pytest.mark.parametrize("B,Q,cap,n,m,W,fp8,last", [
+    (1, 152, 1304, [1300], 1, 0, False, [1299]), (2, 76, 1448, [1441, 1300], 2, 130, False, [2880, 2590]),
+    (4, 37, 1608, [1600, 1600, 1333, 20], 1, 99, True, [1599, 1000, 1332, 19]), (1, 60, 3000, [2999], 1, 128, False, [2998]),
+    (2, 31, 3000, [2999, 1777], 2, 64, True, [5997, 3554]), (1, 151, 1304, [70], 1, 200, False, [1500])])
+def test_attention_pairs(B, Q, cap, n, m, W, fp8, last):
+    pos = np.asarray(last)[:, None] - (Q - 1) + np.arange(Q)[None, :]              # some before position 0: padding
+    case = attn_case(cap + Q, B, Q, cap, n, m, W, fp8, pos)
+    n_call = [max(n)] * B                                                          # (max_n: the rule's input)
+    attend_and_check(*case[:2], n, m, *case[2:], pos, W, max_n=max(1300, *n_call))
+
+
+@pytest.mark.parametrize("spread,q_size", [(2.0, 0.5), (3.0, 0.02)])
+def test_attention_pairs_scales_of_every_size(spread, q_size):
+    pos = 1299 - np.arange(152)[None, :]
+    case = attn_case(21, 1, 152, 1304, [1300], 1, 64, False, pos, spread=spread, q_size=q_size)
+    attend_and_check(*case[:2], [1300], 1, *case[2:], pos, 64)
+
+
+def test_attention_pairs_queries_beyond_f16_and_blocks_of_zeros():
+    pos = np.repeat(np.array([[1299, 640, 7, 600]]), 38, 1)
+    codes, scales, q, _, _ = attn_case(22, 1, 152, 1304, [1300], 1, 0, False, pos)
+    codes[0, :640], scales[0, :80] = 0, 0.0                                        # never written: zeros
+    scales *= np.float32(2.0 ** -20)
+    q[0, ::3, 5] *= 2.0 ** 20
+    q[0, 1::4, 60] *= 2.0 ** 30
+    attend_and_check(codes, scales, [1300], 1, q, None, None, pos, 0)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_attention_rows_that_only_the_newer_query_sees(bad, fp8):
-    """A window row that is not finite: the queries that see it become NaN, their neighbours stay as they are."""
-    if fp8 and bad == float("inf"):
-        pytest.skip("E4M3 has no infinity")
-    pos = np.array([[80, 81, 82, 83, 84]])
-    codes, scales, q, rows, base = attn_case(14, 1, 5, 96, [90], 1, 16, fp8, pos)
-    clean, _ = attend_and_check(codes, scales, [90], 1, q, rows, base, pos, 16)
-    rows = rows.clone()
-    rows[0, 83 - int(base[0]), 300] = 0x7F if fp8 else bad
-    out = torch.zeros(1, 5, H, D, dtype=torch.bfloat16, device="cuda")
-    lse = torch.zeros(1, 5, H, device="cuda")
-    ws = csa2.Workspace(csa2.cache8_attn_workspace_size(1, 5, 96, 16))
-    csa2.cache8_attn(cache_of(codes, scales, [90]), q.cuda(), dev(pos), SCALE, out, ws, max_n=96, W=16, swa=rows.cuda(),
-                     swa_base_pos=dev(base), lse=lse)
+def test_attention_rows_that_only_the_newer_query_sees(fp8):
+    """A window row with a NaN: the queries that see it become NaN, their neighbours stay as they are."""
+    pos = 1100 + np.arange(152)[None, :]
+    codes, scales, q, rows, base = attn_case(14, 1, 152, 1304, [1300], 1, 16, fp8, pos)
+    cache, ws = cache_of(codes, scales, [1300]), csa2.Workspace(csa2.cache8_attn_workspace_size(1, 152, 1300, 16))
+    got = []
+    for bad in (False, True):
+        if bad:
+            rows = rows.clone()
+            rows[0, 1183 - int(base[0]), 300] = 0x7F if fp8 else float("nan")
+        out = torch.zeros(1, 152, H, D, dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros(1, 152, H, device="cuda")
+        csa2.cache8_attn(cache, q.cuda(), dev(pos), SCALE, out, ws, max_n=1300, W=16, swa=rows.cuda(), swa_base_pos=dev(base), lse=lse)
+        got.append((out, lse))
     assert ws.sync_status()[0] == 0
-    assert torch.equal(out[0, :3], clean[0, :3]) and torch.all(torch.isnan(out[0, 3:])) and torch.all(torch.isnan(lse[0, 3:]))
+    (out, lse), (bad_out, bad_lse) = got
+    assert torch.all(torch.isfinite(out.float()))
+    sees = slice(83, 99)                                                           # positions 1183 .. 1198
+    assert torch.all(torch.isnan(bad_out[0, sees])) and torch.all(torch.isnan(bad_lse[0, sees]))
+    keep = [i for i in range(152) if not 83 <= i < 99]
+    assert torch.equal(bad_out[0, keep], out[0, keep]) and torch.equal(bad_lse[0, keep], lse[0, keep])
 
 
 @pytest.mark.parametrize("W,fp8", [(0, False), (40, False), (200, True)])
 def test_attention_neighbours_far_apart(W, fp8):
     """Two queries of a pair whose windows lie apart, meet or overlap, one of them padding, and queries in no order."""
-    pos = np.array([[600, 10, 300, 341, 5, -1, 44, 45, -7]])
-    n = [512]
-    codes, scales, q, rows, base = attn_case(15, 1, 9, 512, n, 1, W, fp8, pos)
+    pos = np.tile(np.array([[600, 10, 300, 341, 5, -1, 44, 45, -7]]), (1, 17))[:, :151]
+    n = [1300]
+    codes, scales, q, rows, base = attn_case(15, 1, 151, 1304, n, 1, W, fp8, pos)
     if W:
         base = np.zeros(1, np.int64)
         g = torch.Generator().manual_seed(16)
