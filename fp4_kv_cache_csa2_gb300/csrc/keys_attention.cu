@@ -874,24 +874,30 @@ static int keys_split(int64_t BQ, int64_t chunks, int64_t* cost_out = nullptr) {
 // PAIR_FIXED of them, 14 us, beside its own (7 here).  As chosen, us (pairs / single CTAs, each with its best split):
 // 3 x 37 queries of 10,007 entries 108 / 134, 1 x 100 of 4000 71 / 81, 1 x 2 of 8000 24.9 / 19.9, 16 x 2 of
 // 2000 27.5 / 22.6, 1 x 8 of 600 18.0 / 13.4.
+// The lengths of the sequences are on the device, and `chunks` is the longest's.  So a split counts for pairs with the mean of
+// two times: of all alike, and of several that have 7/10 on average, whose items fill the gaps in each other's
+// waves.  (3 x 37 queries, split in 1 / 2: of 10,007, 7006 and 4005 entries 155 / 108, of 10,007 each 155 / 172.)
 constexpr int PAIR_FIXED = 16;
 struct Cache8Plan { bool pairs; int split; };
 
 static Cache8Plan cache8_plan(int B, int Q, int64_t chunks) {
   int64_t single = 0;
-  Cache8Plan plan{false, keys_split((int64_t)B * Q, chunks, &single)};
+  const Cache8Plan alone{false, keys_split((int64_t)B * Q, chunks, &single)};
   const int64_t pairs = (int64_t)B * ((Q + 1) / 2), slots = KA_SMS / 2;
-  if (Q < 2 || B < 1) return plan;
-  int64_t best = 120 * single;                        // 48ths of 1.2 us, in 10 ns
+  if (Q < 2 || B < 1) return alone;
+  int split = 1;
+  int64_t best = INT64_MAX, time = 0;
   for (int s = 1; s <= slots && s <= chunks && (s == 1 || pairs * s <= KA_WAVES * slots); s++) {
-    const int64_t join = s > 1 ? 169 + 4 * s + 3 * pairs * s : 0;
-    const int64_t cost = 85 * (48 * ceil_div(pairs * s, slots) * (PAIR_FIXED + ceil_div(chunks, s)) + join);
-    if (cost < best) {
-      plan = {true, s};
-      best = cost;
+    const int64_t join = s > 1 ? 169 + 4 * s + 3 * pairs * s : 0, longest = 48 * (PAIR_FIXED + ceil_div(chunks, s));
+    const int64_t alike = longest * ceil_div(pairs * s, slots) + join;
+    const int64_t uneven = B > 1 ? max(longest, 48 * pairs * s * (PAIR_FIXED + 7 * ceil_div(chunks, s) / 10) / slots) + join : alike;
+    if (alike + uneven < best) {
+      split = s;
+      best = alike + uneven;
+      time = alike;
     }
   }
-  return plan;
+  return time == 0 || 85 * time >= 120 * single ? alone : Cache8Plan{true, split};   // (48ths of 0.85 and 1.2 us)
 }
 
 size_t cache8_part_bytes(int B, int Q, int64_t chunks) {
