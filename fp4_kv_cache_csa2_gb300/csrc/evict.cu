@@ -18,6 +18,7 @@
 // us instead of 213 for 16 x 131,072 entries in place, 280 instead of 153 for 1M in 8 bits.)
 //
 // Bound by HBM: the bytes that stay, in and out.
+#include <climits>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -165,25 +166,41 @@ __global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) evict_select_ke
   const int mine = (int)(min(u0 + per, units) - u0), quads = (mine + 3) / 4;
   const bool cached = 4 * quads <= slots;
   uint4* keys = reinterpret_cast<uint4*>(sm.keys);
-  if (cached && UNIT == 1) {
-#pragma unroll 4
-    for (int i = tid; i < quads; i += EV_THREADS) keys[i] = all.four(u0 + 4 * i);
-  } else if (cached) {
-    // a lane takes half a unit (a lane a unit would touch a line each), neighbours join theirs
-    const int halves = (2 * mine + 31) / 32 * 32;
-#pragma unroll 4
-    for (int i = tid; i < halves; i += EV_THREADS) {
-      const int64_t j = (u0 * 2 + i) * 4;             // first weight
-      uint32_t k = 0u;
-      if (j + 4 <= n) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(all.w + j));
-        k = max(max(ev_key(v.x), ev_key(v.y)), max(ev_key(v.z), ev_key(v.w)));
-      } else {
-        for (int64_t y = j; y < n; y++) k = max(k, ev_key(__ldcg(all.w + y)));
+  if (cached) {
+    // Batches of loads, then their keys.  UNIT 8: a lane takes half a unit (a lane a unit would touch a line each),
+    // neighbours join theirs.
+    constexpr int BATCH = UNIT == 1 ? 4 : 8;
+    const float4* w4 = reinterpret_cast<const float4*>(all.w + u0 * UNIT);
+    const int fours = UNIT == 1 ? quads : (2 * mine + 31) / 32 * 32;
+    const int whole = (int)min(max(n - u0 * UNIT, (int64_t)0) / 4, (int64_t)fours);   // of them without a part behind the last entry
+    const int f_lo = (int)min(max(all.first - u0, (int64_t)0), (int64_t)INT_MAX), f_hi = (int)min(max(all.recent - u0, (int64_t)0), (int64_t)INT_MAX);
+    for (int i0 = tid; i0 < fours; i0 += BATCH * EV_THREADS) {
+      float4 v[BATCH];
+#pragma unroll
+      for (int y = 0; y < BATCH; y++)
+        if (i0 + y * EV_THREADS < whole) v[y] = __ldcg(w4 + i0 + y * EV_THREADS);
+#pragma unroll
+      for (int y = 0; y < BATCH; y++) {
+        const int i = i0 + y * EV_THREADS;
+        if (i >= fours) continue;                     // (of UNIT 8 whole warps)
+        uint32_t k[4] = {};
+        if (i < whole) {
+          k[0] = ev_key(v[y].x), k[1] = ev_key(v[y].y), k[2] = ev_key(v[y].z), k[3] = ev_key(v[y].w);
+        } else {
+          for (int x = 0; x < 4; x++)
+            if (u0 * UNIT + 4 * (int64_t)i + x < n) k[x] = ev_key(__ldcg(all.w + u0 * UNIT + 4 * (int64_t)i + x));
+        }
+        if (UNIT == 1) {
+          if (4 * i < f_lo || 4 * i + 3 >= f_hi)
+            for (int x = 0; x < 4; x++)
+              if (4 * i + x < f_lo || 4 * i + x >= f_hi) k[x] = EV_FORCED;
+          keys[i] = make_uint4(k[0], k[1], k[2], k[3]);
+        } else {
+          uint32_t most = max(max(k[0], k[1]), max(k[2], k[3]));
+          most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+          if ((i & 1) == 0 && i / 2 < 4 * quads) sm.keys[i / 2] = i / 2 < f_lo || i / 2 >= f_hi ? EV_FORCED : most;
+        }
       }
-      k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 1));
-      const int64_t u = u0 + i / 2;
-      if ((i & 1) == 0 && i / 2 < 4 * quads) sm.keys[i / 2] = u < all.first || u >= all.recent ? EV_FORCED : k;
     }
   }
   auto four = [&](int i) { return cached ? keys[i] : all.four(u0 + 4 * (int64_t)i); };
@@ -300,6 +317,23 @@ __global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) evict_select_ke
     const int q = qw + lane;
     const uint4 v = q < q1 ? four(q) : make_uint4(0u, 0u, 0u, 0u);
     const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+    uint32_t above[4], equal = 0u;
+#pragma unroll
+    for (int x = 0; x < 4; x++) {
+      const bool in = q < q1 && 4 * q + x < mine;
+      above[x] = __ballot_sync(0xFFFFFFFFu, in && k[x] > last);
+      equal |= in && k[x] == last;
+    }
+    if (!__any_sync(0xFFFFFFFFu, equal)) {            // nearly always
+      const uint32_t lower = (1u << lane) - 1u;
+      int32_t* to = kept + gp + min(ep, left);
+      int at = __popc(above[0] & lower) + __popc(above[1] & lower) + __popc(above[2] & lower) + __popc(above[3] & lower);
+#pragma unroll
+      for (int x = 0; x < 4; x++)
+        if (above[x] >> lane & 1u) to[at++] = (int32_t)(u0 + 4 * q + x);
+      gp += __popc(above[0]) + __popc(above[1]) + __popc(above[2]) + __popc(above[3]);
+      continue;
+    }
     uint32_t both = 0u;                               // keys above (low half) and equal (high half) in this lane's four
 #pragma unroll
     for (int x = 0; x < 4; x++)
