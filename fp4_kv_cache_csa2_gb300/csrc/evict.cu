@@ -15,7 +15,8 @@
 // which they are a search over the kept numbers tells, while the chunk's own copies are on their way.
 // Chunks are taken by ticket, in order: all a CTA waits for (with a limit) are flags of CTAs that
 // run already and wait for nothing before they set them.  (Waiting for every chunk before it: 225
-// us instead of 213 for 16 x 131,072 entries in place, 280 instead of 153 for 1M in 8 bits.)
+// us instead of 213 for 16 x 131,072 entries in place, 280 instead of 153 for 1M in 8 bits; with the selection
+// as it is now 187 and 131.)
 //
 // Bound by HBM: the bytes that stay, in and out.
 #include <climits>
@@ -532,8 +533,8 @@ static cudaError_t ev_select(const EvParams& p, cudaLaunchConfig_t cfg) {
 }
 
 // CTAs of a sequence's selection.  A cluster of 8 CTAs of 1024 threads fits 15 times (one to an SM), so that 16
-// sequences of 131,072 took two waves, 43 us; of 512 threads 32.  A few long ones: 16 CTAs, 32 us (512 threads: 40)
-// for 131,072 blocks.
+// sequences of 131,072 took two waves, 43 us; of 512 threads 32 (26 since loads go in batches and numbers by
+// ballots).  A few long ones: 16 CTAs, then 32 us, now 28 (512 threads: 40) for 131,072 blocks.
 template <int UNIT>
 static cudaError_t ev_select_any(const EvParams& p, const cudaLaunchConfig_t& cfg) {
   const int64_t units = ceil_div(p.cap, UNIT);

@@ -50,8 +50,8 @@
 // 262 us, 0.99 PFLOP/s; 602 queries of 1000 E4M3 rows 114 us.  A CTA costs about 7 us beside its chunks: 16
 // queries of 132 bf16 rows take 9.0 us.
 // With 8-bit entries the shared memory binds too: 2048 cycles a chunk (products 1024, staged bytes in and
-// out 512, widened codes 512) beside 2074 of MMAs.  2048 queries over 8192 entries 2.06 ms, 16 over 131,072
-// 287 us.  (Codes to registers without staging, four lanes a key, the same; staged rows without a swizzle,
+// out 512, widened codes 512) beside 2074 of MMAs.  16 queries over 131,072 entries 275 us; 2048 over 8192 would
+// take 2.06 ms, pairs of CTAs (pair_attention.cu) 1.56.  (Codes to registers without staging, four lanes a key, the same; staged rows without a swizzle,
 // two keys a phase with their pieces in turn, 2.65 ms.)
 #include <cfloat>
 
