@@ -58,8 +58,8 @@ struct Aw {
   static constexpr int OFF_TILE = RING * AW_PIECES * AW_STAGE;
   static constexpr int OFF_SMALL = OFF_TILE + TILES * TILE;
   struct Small {
-    // A head's factor and minus its lse in powers of two; of a pair, groups in turn, minus the lse and what the
-    // exponent is cut to (infinity, or minus infinity for a head that saw nothing)
+    // A head's factor and minus its lse in powers of two; of a pair, groups in turn, minus the lse and a mask of
+    // its weights' bits (none for a head that saw nothing: its q may be NaN)
     float2 col[COLS][N];
     float joined[2][AW_KEYS];         // the second half's sums
     int vis[AW_GROUPS * NQ];          // entries each query sees
@@ -83,6 +83,11 @@ __device__ __noinline__ bool aw_timeout(int* err, WsHeader* hdr, int where) {
 
 // x, the same in every lane, in a uniform register.
 __device__ __forceinline__ uint32_t aw_uniform(uint32_t x) { return __reduce_or_sync(0xFFFFFFFFu, x); }
+
+// x's bits that the mask has
+__device__ __forceinline__ float aw_masked(float x, float mask) {
+  return __uint_as_float(__float_as_uint(x) & __float_as_uint(mask));
+}
 
 // entries of sequence b that the call deals with
 __device__ __forceinline__ int aw_entries(const AwParams& p, int b) {
@@ -305,9 +310,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
         if (u >= C::COLS) wait(&sm.col_free[ci], u / C::COLS - 1, 64);
 #pragma unroll
         for (int i = 0; i < 4; i++)
-          sm.col[ci][32 * i + lane] = l[i] > -INFINITY ? make_float2(-l[i] * AW_LOG2E, INFINITY)
-                                      : l[i] == -INFINITY ? make_float2(0.f, -INFINITY)
-                                                          : make_float2(l[i], INFINITY);   // NaN
+          sm.col[ci][32 * i + lane] = make_float2(-l[i] * AW_LOG2E, __uint_as_float(l[i] == -INFINITY ? 0u : ~0u));
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&sm.col_full[ci]);
         u++;
@@ -453,8 +456,8 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
               const float4 f = col[(c + x) / 2];
               const float v0 = __uint_as_float(r[x]), v1 = __uint_as_float(r[x + 1]);
               if (PAIR) {
-                s4[x & 2] += ex2_ftz(fminf(fmaf(v0, by, f.x), f.y));
-                s4[(x & 2) + 1] += ex2_ftz(fminf(fmaf(v1, by, f.z), f.w));
+                s4[x & 2] += aw_masked(ex2_ftz(fmaf(v0, by, f.x)), f.y);
+                s4[(x & 2) + 1] += aw_masked(ex2_ftz(fmaf(v1, by, f.z)), f.w);
               } else {
                 s4[x & 2] += ex2_ftz(fmaf(E8 ? v0 * s8 : v0, f.x, f.y));
                 s4[(x & 2) + 1] += ex2_ftz(fmaf(E8 ? v1 * s8 : v1, f.z, f.w));
@@ -470,7 +473,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
           }
           if (j < sm.vis[NQ == 1 ? g : 2 * g + half]) {
             const float y = (s4[0] + s4[1]) + (s4[2] + s4[3]) - lost, z = acc + y;
-            lost = (z - acc) - y;
+            lost = fabsf(z) < INFINITY ? (z - acc) - y : 0.f;
             acc = z;
           }
           u++;

@@ -593,7 +593,7 @@ csa2_status csa2_cache8_attn(const csa2_cache8 *cache, const csa2_cache8_attn_ar
  * attention of these queries wrote (csa2_dense_attn, csa2_cache8_attn: then the
  * weights are the softmax's own; or that of another attention over more or fewer
  * keys).  A query with t < 0, or a head with lse = -inf, adds nothing, whatever its
- * q holds.  What a query does not see may hold anything.
+ * q holds; NaN in q or lse reaches the entries that its query sees.  What a query does not see may hold anything.
  *   prev         [B][cap], NULL: zeros (decay is then unused).  prev may be
  *                weights itself.
  *   weights      out [B][cap]: entries j < min(n_entries[b], max_n) are written,

@@ -158,6 +158,29 @@ def test_weights_queries_beyond_f16():
     check(cache, values, n, 1, q, pos, lse)
 
 
+@pytest.mark.parametrize("bits,Q", [(4, 1), (8, 1), (4, 3), (8, 3), (8, 6)])
+@pytest.mark.parametrize("what", ["lse", "q", "overflow"])
+def test_weights_that_are_no_finite_numbers(bits, Q, what):
+    """A head's NaN, or a weight beyond binary32, reaches every entry that its query sees and no other."""
+    n = [200]
+    cache, values = make_cache(12, bits, 1, 200, n, 1)
+    pos = np.full((1, Q), 199)
+    pos[0, 0] = 149
+    q = torch.randn(1, Q, H, D, generator=torch.Generator().manual_seed(12)).bfloat16()
+    lse = some_lse(q.double().numpy(), values, n, 1, pos)
+    clean = check(cache, values, n, 1, q, pos, lse)
+    if what == "q":
+        q[0, 0, 33, 100] = float("nan")
+    else:
+        lse[0, 0, 33] = np.nan if what == "lse" else -1000.0                       # scores lie within 100 of 0
+    w = torch.full((1, 200), 5.0, device="cuda")
+    ws = csa2.Workspace(csa2.attn_weights_workspace_size(1, Q, 200))
+    csa2.attn_weights(cache, q.cuda(), dev(pos), dev(lse), SCALE, w, ws, max_n=200)
+    assert ws.sync_status()[0] == 0
+    assert torch.all(w[0, :150] == float("inf") if what == "overflow" else torch.isnan(w[0, :150]))
+    assert torch.equal(w[0, 150:], clean[0, 150:])
+
+
 def test_weights_in_place_repeat_and_add_up():
     """prev = weights; the same inputs give the same bits; the sum of a head's weights is 1."""
     n, Q = [700], 9
