@@ -279,7 +279,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
         while (g < n_g) {
           const int after = (int)aw_uniform((uint32_t)next_group(g + 1, t_lo + t));
           if (u >= 2) wait_mma(&sm.s_free[u & 1], (u >> 1) - 1, 60);
-          const uint32_t ring = u % C::RING;
+          const uint32_t ring = n_g > 1 ? u % C::RING : 0;   // (one group stays where it is)
 #pragma unroll 1
           for (int h = 0; h < 2; h++) {
             if (first) wait_mma(&sm.a_full[h], t, 61);

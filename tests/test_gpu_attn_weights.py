@@ -158,6 +158,17 @@ def test_weights_queries_beyond_f16():
     check(cache, values, n, 1, q, pos, lse)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("B,Q,cap", [(40, 2, 1000), (76, 2, 600), (25, 4, 1300), (19, 5, 800), (38, 1, 1500)])
+def test_weights_several_steps_of_a_run(bits, B, Q, cap):
+    """Enough sequences that a CTA, or a pair, takes several steps of entries with the same one or few queries."""
+    n = [cap - 7 * b for b in range(B)]
+    cache, values = make_cache(13, bits, B, cap, n, 1)
+    pos = np.asarray(n)[:, None] - Q + np.arange(Q)[None, :]
+    q = torch.randn(B, Q, H, D, generator=torch.Generator().manual_seed(13)).bfloat16()
+    check(cache, values, n, 1, q, pos, some_lse(q.double().numpy(), values, n, 1, pos))
+
+
 @pytest.mark.parametrize("bits,Q", [(4, 1), (8, 1), (4, 3), (8, 3), (8, 6)])
 @pytest.mark.parametrize("what", ["lse", "q", "overflow"])
 def test_weights_that_are_no_finite_numbers(bits, Q, what):
