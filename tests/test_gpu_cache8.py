@@ -353,3 +353,38 @@ def test_attention_captured_and_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, out) and ws.sync_status()[0] == 0
+
+
+@pytest.mark.parametrize("Q,n,W", [(152, 1300, 32), (60, 3000, 0)])
+def test_attention_pairs_captured_and_beside_themselves(Q, n, W):
+    """Graphs of the same call on two workspaces, replayed at once; its queries divided over CTAs (60 of 3000) or not."""
+    pos = n - Q + np.arange(Q)[None, :]
+    codes, scales, q, rows, base = attn_case(17, 1, Q, -(-n // 8) * 8, [n], 1, W, False, pos)
+    out, lse = attend_and_check(codes, scales, [n], 1, q, rows, base, pos, W)
+    cache, qd, pd = cache_of(codes, scales, [n]), q.cuda(), dev(pos)
+    rd, bd = (rows.cuda(), dev(base)) if W else (None, None)
+    calls = []
+    for _ in range(2):
+        got, got_lse = torch.zeros_like(out), torch.zeros_like(lse)
+        ws = csa2.Workspace(csa2.cache8_attn_workspace_size(1, Q, n, W))
+        ws.buf[256:].fill_(0xFF)                                                   # NaN where no state is written
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            csa2.cache8_attn(cache, qd, pd, SCALE, got, ws, max_n=n, W=W, swa=rd, swa_base_pos=bd, lse=got_lse)
+        calls.append((graph, got, got_lse, ws, torch.cuda.Stream()))
+    for _ in range(3):
+        for graph, _, _, _, s in calls:
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, got, got_lse, ws, _ in calls:
+        assert torch.equal(got, out) and torch.equal(got_lse, lse) and ws.sync_status()[0] == 0
+
+
+def test_attention_pairs_more_entries_than_max_n():
+    """max_n sizes the split and nothing else."""
+    pos = 2990 - 60 + np.arange(60)[None, :]
+    case = attn_case(18, 1, 60, 2992, [2992], 1, 20, False, pos)
+    attend_and_check(*case[:2], [2992], 1, *case[2:], pos, 20, max_n=1)
+    attend_and_check(*case[:2], [2992], 1, *case[2:], pos, 20, max_n=1 << 40)
