@@ -209,4 +209,25 @@ inline bool encode_bf16_rows512(CUtensorMap* map, const void* base, uint64_t row
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Matrices [rows][512] as column chunks of 128 bytes: half of a row's dims in one SW128 copy, chunk after chunk
+// (one copy a chunk: a thread issues them at 200 cycles each).  Coordinates: 0, row, first chunk.
+inline bool encode_rows512_halves(CUtensorMap* map, CUtensorMapDataType type, int bytes, const void* base, uint64_t rows,
+                                  uint32_t box_rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const uint32_t chunk = 128 / bytes, chunks = D / chunk;
+  cuuint64_t dims[3] = {chunk, rows, chunks};
+  cuuint64_t strides[2] = {(cuuint64_t)(D * bytes), 128};
+  cuuint32_t box[3] = {chunk, box_rows, chunks / 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline bool encode_bf16_rows512_halves(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
+  return encode_rows512_halves(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, box_rows);
+}
+inline bool encode_u8_rows512_halves(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
+  return encode_rows512_halves(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, box_rows);
+}
+
 }  // namespace csa2

@@ -545,20 +545,6 @@ AwPlan attn_weights_plan(int B, int Q, int64_t max_n) {
 
 int64_t attn_weights_pitch(int64_t max_n) { return ceil_div(max_n, AW_KEYS) * AW_KEYS; }   // floats of a sequence's partial sums
 
-// bf16 matrix [rows][512] with SW128 boxes of 64 rows x 4 column chunks of 64: half of a query's dims in one
-// copy (one copy a chunk: a thread issues them at 200 cycles each).
-static bool encode_query_halves(CUtensorMap* map, const void* base, uint64_t rows) {
-  auto fn = tensor_map_encoder();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {64, rows, D / 64};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
-  cuuint32_t box[3] = {64, H, 4};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool E8, bool PAIR>
 static cudaError_t aw_launch(const AwParams& p, const CUtensorMap& mq, const CUtensorMap& mc, cudaLaunchConfig_t cfg) {
   using C = Aw<E8, PAIR>;
@@ -596,7 +582,7 @@ cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (p.Q > 0) {
     CUtensorMap mq = {}, mc = {};                     // (of what the kernel does not copy: unused)
-    if (p.Q > 1 && !encode_query_halves(&mq, p.q, (uint64_t)p.B * p.Q * H)) return cudaErrorInvalidValue;
+    if (p.Q > 1 && !encode_bf16_rows512_halves(&mq, p.q, (uint64_t)p.B * p.Q * H, H)) return cudaErrorInvalidValue;
     if (p.scales8 && !encode_u8_rows512_sw128(&mc, p.kv, (uint64_t)p.B * p.cap, AW_KEYS)) return cudaErrorInvalidValue;
     if (p.scales8) e = p.Q == 1 ? aw_launch<true, false>(p, mq, mc, cfg) : aw_launch<true, true>(p, mq, mc, cfg);
     else e = p.Q == 1 ? aw_launch<false, false>(p, mq, mc, cfg) : aw_launch<false, true>(p, mq, mc, cfg);

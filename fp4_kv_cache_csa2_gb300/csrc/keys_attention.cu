@@ -989,10 +989,12 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
   if (nk > 0 && !rows(&ms, p.sinks, nk)) return cudaErrorInvalidValue;
   if (nk == 0) ms = mr;
   if (p.scales8) {                                    // no sinks: their map is the codes'
+    if (plan.pairs) {
+      const cudaError_t e = launch_pair_attention(p, B, mr, stream);
+      return e != cudaSuccess || p.split == 1 ? e : launch_keys_join(p, BQ, stream);
+    }
     if (p.cap > 0 && !encode_u8_rows512_sw128(&ms, p.main_kv, (uint64_t)B * p.cap, KA_KEYS)) return cudaErrorInvalidValue;
-    if (!plan.pairs) return keys_launch<true, true>(p, BQ, mq, mr, ms, stream);
-    const cudaError_t e = launch_pair_attention(p, B, mq, mr, ms, stream);
-    return e != cudaSuccess || p.split == 1 ? e : launch_keys_join(p, BQ, stream);
+    return keys_launch<true, true>(p, BQ, mq, mr, ms, stream);
   }
   return p.main_kv || p.rows_fp8 ? keys_launch<true, false>(p, BQ, mq, mr, ms, stream)
                                  : keys_launch<false, false>(p, BQ, mq, mr, ms, stream);

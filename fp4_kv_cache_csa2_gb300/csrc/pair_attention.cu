@@ -78,15 +78,13 @@ __device__ __noinline__ bool pa_timeout(int* err, WsHeader* hdr, int where) {
 
 // What one query sees: window rows row_lo .. row_hi - 1 of the buffer, entries 0 .. entries - 1 (each below 2^31).
 struct PaQuery {
-  int64_t t, lo;                      // position (-1: none), first window position
+  int64_t t, lo;                      // position (below 0: none), first window position
   int row_lo, row_hi, entries;
 };
 
-__device__ __forceinline__ PaQuery pa_query(const KeysParams& p, int b, int64_t base, int i) {
-  PaQuery q{-1, 0, 0, 0, 0};
-  if (i >= p.Q) return q;
-  q.t = p.q_pos[(int64_t)b * p.Q + i];
-  if (q.t < 0) return q;
+__device__ __forceinline__ PaQuery pa_query(const KeysParams& p, int32_t n_entries, int64_t base, int64_t t) {
+  PaQuery q{t, 0, 0, 0, 0};
+  if (t < 0) return q;
   q.lo = q.t >= p.W ? q.t - p.W + 1 : 0;
   if (p.W > 0 && q.t >= base) {       // (unsigned differences: any two positions have one)
     const uint64_t s = (uint64_t)p.S, r0 = q.lo > base ? (uint64_t)q.lo - (uint64_t)base : 0;
@@ -96,8 +94,8 @@ __device__ __forceinline__ PaQuery pa_query(const KeysParams& p, int b, int64_t 
       q.row_hi = (int)r1;
     }
   }
-  const int64_t n = visible_entries(min(q.t, INT64_MAX - 1), p.m, p.n_entries[b]);
-  q.entries = (int)max(min(n, p.cap), (int64_t)0);
+  const int64_t seen = (min(t, INT64_MAX - 1) + 1) >> (p.m - 1);   // (m is 1 or 2)
+  q.entries = (int)max(min(seen, min((int64_t)n_entries, p.cap)), (int64_t)0);
   return q;
 }
 
@@ -158,12 +156,20 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   const uint32_t pair = item / (uint32_t)split;
   const int b = (int)(pair / pairs), qi = 2 * (int)(pair % pairs);
   const bool there = qi + rank < p.Q;                 // the last pair of a sequence may have one query
+  // (the loads that all else follows from are on their way while the pair sets itself up)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t base = p.W > 0 ? p.base_pos[b] : 0;
+  const int64_t t0 = p.q_pos[(int64_t)b * p.Q + qi], t1 = qi + 1 < p.Q ? p.q_pos[(int64_t)b * p.Q + qi + 1] : -1;
+  const int32_t n_entries = p.n_entries[b];
   const int64_t bq = (int64_t)b * p.Q + qi + rank;
   float* part = p.part + (bq * split + sp) * KA_PART_FLOATS;   // with split > 1
 
   if (warp == PA_MMA_WARP) tc::tmem_alloc_pair(&sm.tmem_base, 512);
-  if (tid == 0) {
+  if (tid == 32 * PA_COPY_WARP) {
     tc::bar_init(&sm.q_full, 1);
+    tc::bar_init_fence();
+  }
+  if (tid == 0) {
     tc::bar_init(&sm.q_moved, 2 * PA_SOFT_WARPS);
     tc::bar_init(&sm.q_here, PA_SOFT_WARPS);
     for (int i = 0; i < PA_STAGES; i++) {
@@ -187,14 +193,20 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     tc::prefetch_tensormap(&map_codes);
   }
   tc::fence_before_sync();
-  tc::cluster_sync();
+  __syncwarp();
+  tc::cluster_arrive();
+  if (tid == 32 * PA_COPY_WARP && there) {            // Q into the last two K buffers
+    tc::bar_arrive_expect_tx(&sm.q_full, 8u * PA_COL);
+    for (int h = 0; h < 2; h++)
+      tc::tma_load_3d(smem + (PA_BUFS - 2 + h) * PA_BUF, &map_q, 0, (int32_t)(bq * H), 4 * h, &sm.q_full);
+  }
+
+  const PaQuery qs[2] = {pa_query(p, n_entries, base, t0), pa_query(p, n_entries, base, t1)};
+  const PaRun run = pa_run(qs, sp, split);
+  __syncwarp();
+  tc::cluster_wait();
   tc::fence_after_sync();
   if (sm.tmem_base != 0 && tid == 0) report(p.hdr, CSA2_ERR_CUDA, 6);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  const int64_t base = p.W > 0 ? p.base_pos[b] : 0;
-  const PaQuery qs[2] = {pa_query(p, b, base, qi), pa_query(p, b, base, qi + 1)};
-  const PaRun run = pa_run(qs, sp, split);
   const int n_ch = run.n;
   const PaQuery mine = rank ? qs[1] : qs[0];
   if (sp == 0 && tid == 0 && mine.t >= 0) {           // what the caller did not supply
@@ -202,7 +214,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       if (mine.lo < base) report(p.hdr, CSA2_ERR_BOUNDS, mine.lo);
       else if ((uint64_t)mine.t - (uint64_t)base >= (uint64_t)p.S) report(p.hdr, CSA2_ERR_BOUNDS, mine.t);
     }
-    if (p.n_entries[b] > p.cap) report(p.hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
+    if (n_entries > p.cap) report(p.hdr, CSA2_ERR_BOUNDS, n_entries);
   }
   bool ok = true;                                     // a thread that has given up once waits no more
   auto wait = [&](uint64_t* bar, uint32_t use, int where) {
@@ -254,39 +266,39 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   } else if (warp == PA_COPY_WARP) {
     // ================= copies: this CTA's half of the dims
     if (lane == 0 && n_ch > 0) {
-      if (there) {                                    // Q into the last two K buffers
-        tc::bar_arrive_expect_tx(&sm.q_full, 8u * PA_COL);
-        for (int i = 0; i < 8; i++)
-          tc::tma_load_2d(smem + (PA_BUFS - 2) * PA_BUF + i * PA_COL, &map_q, i * 64, (int32_t)(bq * H), &sm.q_full);
-      }
       const uint8_t* kv = p.main_kv + (int64_t)b * p.cap * D;
       auto ahead = [&](int c) {                       // (each CTA sends for half of the keys, whole)
         if (c >= n_ch || run.rows(c)) return;
         const int keys = run.keys(c), k0 = rank ? keys / 2 : 0, k1 = rank ? keys : keys / 2;
         if (k1 > k0) tc::prefetch_l2(kv + (int64_t)(run.first(c) + k0) * D, (uint32_t)((k1 - k0) * D));
       };
-      for (int c = 1; c < PA_AHEAD; c++) ahead(c);
       uint32_t staged = 0;
       for (int c = 0; c < n_ch; c++) {
         const int first = run.first(c);
-        ahead(c + PA_AHEAD);
+        if (c == 1)                                   // (behind the first chunk's own copies)
+          for (int i = 2; i < 1 + PA_AHEAD; i++) ahead(i);
+        if (c > 0) ahead(c + PA_AHEAD);
         if (!run.rows(c)) {
           const uint32_t s = staged % PA_STAGES;
           if (staged >= PA_STAGES) wait(&sm.stage_free[s], staged / PA_STAGES - 1, 83);
           staged++;
           unsigned char* dst = smem + PA_OFF_STAGE + s * PA_STAGE;
           tc::bar_arrive_expect_tx(&sm.stage_full[s], PA_STAGE);
-          for (int i = 0; i < 2; i++)
-            tc::tma_load_2d(dst + i * PA_COL, &map_codes, 256 * rank + 128 * i, (int32_t)(b * p.cap + first), &sm.stage_full[s]);
+          tc::tma_load_3d(dst, &map_codes, 0, (int32_t)(b * p.cap + first), 2 * rank, &sm.stage_full[s]);
           continue;
         }
         const uint32_t buf = c % PA_BUFS, use = c / PA_BUFS;
         if (use > 0) wait(&sm.free_[buf], use - 1, 84);
         else if (buf >= PA_BUFS - 2 && there) wait(&sm.q_here, 0, 84);
-        unsigned char* kt = smem + buf * PA_BUF + (p.rows_fp8 ? PA_COL / 2 : 0);
+        unsigned char* kt = smem + buf * PA_BUF;
+        const int32_t row = (int32_t)((int64_t)b * p.S + first);
         tc::bar_arrive_expect_tx(&sm.row_full[buf], p.rows_fp8 ? PA_BUF / 2 : PA_BUF);
-        for (int i = 0; i < 4; i++)
-          tc::tma_load_2d(kt + i * PA_COL, &map_rows, 256 * rank + 64 * i, (int32_t)((int64_t)b * p.S + first), &sm.row_full[buf]);
+        if (p.rows_fp8) {                             // the second half of each column chunk
+          for (int i = 0; i < 4; i++)
+            tc::tma_load_2d(kt + PA_COL / 2 + i * PA_COL, &map_rows, 256 * rank + 64 * i, row, &sm.row_full[buf]);
+        } else {
+          tc::tma_load_3d(kt, &map_rows, 0, row, 4 * rank, &sm.row_full[buf]);
+        }
       }
     }
     __syncwarp();
@@ -329,16 +341,17 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       } else {
         const int first = run.first(c), keys = run.keys(c);
         wait(&sm.row_full[buf], use, 87);             // (rows come first: copy `use` of the buffer too)
-        // a value that is not finite: 0, and the queries that see its row are told
+        // values that are not finite: 0, and the queries that see their row are told
+        auto bad = [](uint32_t w) { return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u; };   // exponent of all ones
         auto finite = [&](uint32_t w, int row) -> uint32_t {
-          const uint32_t bad = ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u;   // exponent of all ones
-          if (bad == 0u) return w;
+          const uint32_t is = bad(w);
+          if (is == 0u) return w;
           for (int q = 0; q < 2; q++)
             if (first + row >= qs[q].row_lo && first + row < qs[q].row_hi) {
               if (q == rank) *(volatile int*)&sm.poison = 1;
               else tc::store_other(&sm.poison, 1, q);
             }
-          return (bad & 0x8000u ? 0u : w & 0xFFFFu) | (bad & 0x80000000u ? 0u : w & 0xFFFF0000u);
+          return (is & 0x8000u ? 0u : w & 0xFFFFu) | (is & 0x80000000u ? 0u : w & 0xFFFF0000u);
         };
         if (p.rows_fp8) {
           uint32_t o[2][16];
@@ -354,9 +367,16 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
                                    odd ? a.x : e.x, odd ? a.y : e.y, odd ? a.z : e.z, odd ? a.w : e.w};
 #pragma unroll
             for (int x = 0; x < 8; x++) {
-              o[y][2 * x] = finite(e4m3x2_to_f16x2(v[x]), key);
-              o[y][2 * x + 1] = finite(e4m3x2_to_f16x2(v[x] >> 16), key);
+              o[y][2 * x] = e4m3x2_to_f16x2(v[x]);
+              o[y][2 * x + 1] = e4m3x2_to_f16x2(v[x] >> 16);
             }
+          }
+          uint32_t any = 0u;
+#pragma unroll
+          for (int x = 0; x < 32; x++) any |= bad(o[x >> 4][x & 15]);
+          if (any != 0u) {
+#pragma unroll
+            for (int x = 0; x < 32; x++) o[x >> 4][x & 15] = finite(o[x >> 4][x & 15], key);
           }
           named_sync(1, PA_FILL);                     // all are read before any is written
 #pragma unroll
@@ -380,9 +400,12 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           }
 #pragma unroll
           for (int i = 0; i < PA_BUF / 16 / PA_FILL; i++) {
-            const int row = ((ft + i * PA_FILL) >> 3) & (PA_KEYS - 1);
-            u[i * PA_FILL] = make_uint4(finite(bf16x2_to_f16x2(x[i].x), row), finite(bf16x2_to_f16x2(x[i].y), row),
-                                        finite(bf16x2_to_f16x2(x[i].z), row), finite(bf16x2_to_f16x2(x[i].w), row));
+            uint4 o = make_uint4(bf16x2_to_f16x2(x[i].x), bf16x2_to_f16x2(x[i].y), bf16x2_to_f16x2(x[i].z), bf16x2_to_f16x2(x[i].w));
+            if ((bad(o.x) | bad(o.y) | bad(o.z) | bad(o.w)) != 0u) {
+              const int row = ((ft + i * PA_FILL) >> 3) & (PA_KEYS - 1);
+              o = make_uint4(finite(o.x, row), finite(o.y, row), finite(o.z, row), finite(o.w, row));
+            }
+            u[i * PA_FILL] = o;
           }
         }
       }
@@ -402,8 +425,8 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     uint4* xp = reinterpret_cast<uint4*>(smem + PA_OFF_P);
     float sc2 = p.scale * KA_LOG2E;                   // products to scores in powers of two
     float m_used = -INFINITY, l_sum = 0.f;
+    if (there) wait(&sm.q_full, 0, 88);               // (without keys too: no copy may land behind the CTA's end)
     if (n_ch > 0) {                                   // Q: 128 dims of this lane's head to TMEM
-      if (there) wait(&sm.q_full, 0, 88);
       const unsigned char* qh = smem + (PA_BUFS - 2 + half) * PA_BUF;
       __half2 most = __half2half2(__ushort_as_half(0));
 #pragma unroll 1
@@ -653,15 +676,24 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   // after a timeout copies may be in flight that nobody waited for: time for them to land
   if (*(volatile int*)&sm.err != 0)
     for (int i = 0; i < 1000; i++) __nanosleep(1000);
-  tc::cluster_sync();                                 // (nothing of the other CTA's is on its way here once both are done)
+  __syncwarp();
+  tc::cluster_arrive_relaxed();                       // (nothing of the other CTA's is on its way here once both are done)
+  tc::cluster_wait();
   if (warp == PA_MMA_WARP) {
     tc::fence_after_sync();
     tc::tmem_dealloc_pair(0u, 512);
   }
 }
 
-cudaError_t launch_pair_attention(const KeysParams& p, int B, const CUtensorMap& mq, const CUtensorMap& mr, const CUtensorMap& mc,
-                                  cudaStream_t stream) {
+// mr8: map of E4M3 rows (boxes of 64 bytes, widened where they lie)
+cudaError_t launch_pair_attention(const KeysParams& p, int B, const CUtensorMap& mr8, cudaStream_t stream) {
+  CUtensorMap mq, mr = mr8, mc;
+  const uint64_t rows = (uint64_t)((int64_t)B * p.S), entries = (uint64_t)(B * p.cap);
+  if (!encode_bf16_rows512_halves(&mq, p.q, (uint64_t)((int64_t)B * p.Q * H), H)) return cudaErrorInvalidValue;
+  if (!p.rows_fp8 && rows > 0 && !encode_bf16_rows512_halves(&mr, p.rows, rows, PA_KEYS)) return cudaErrorInvalidValue;
+  if (entries > 0 && !encode_u8_rows512_halves(&mc, reinterpret_cast<const uint8_t*>(p.main_kv), entries, PA_KEYS))
+    return cudaErrorInvalidValue;
+  if (entries == 0) mc = mq;                          // (never read)
   static PerDeviceOnce attrs;
   cudaError_t e = attrs.ensure([](int) {
     return cudaFuncSetAttribute(pair_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM);

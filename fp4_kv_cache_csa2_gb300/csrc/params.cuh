@@ -223,8 +223,7 @@ bool window_ring_fits(int64_t W, int n_sink);
 size_t keys_part_bytes(int64_t BQ, int64_t chunks);
 size_t cache8_part_bytes(int B, int Q, int64_t chunks);   // of a call with scales8
 // Several queries of an 8-bit cache (p.split and p.part set; the maps of q, the rows and the codes)
-cudaError_t launch_pair_attention(const KeysParams& p, int B, const CUtensorMap& mq, const CUtensorMap& mr,
-                                  const CUtensorMap& mc, cudaStream_t stream);
+cudaError_t launch_pair_attention(const KeysParams& p, int B, const CUtensorMap& mr8, cudaStream_t stream);
 struct AwPlan { int runs, splits; };    // of a sequence's tiles, of its queries
 AwPlan attn_weights_plan(int B, int Q, int64_t max_n);
 int64_t attn_weights_pitch(int64_t max_n);

@@ -188,6 +188,12 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// In two steps, for work between them; relaxed: without waiting for the thread's stores (1,500 cycles for outputs on
+// their way to L2).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Arrives on the barrier at `bar`'s place in the shared memory of the cluster's CTA 0.  Relaxed (a release to
 // the cluster takes 2400 cycles): for what is done with TMEM, whose loads and stores have been waited for.
 __device__ __forceinline__ void bar_arrive_first(uint64_t* bar) {
