@@ -50,7 +50,7 @@
 // 262 us, 0.99 PFLOP/s; 602 queries of 1000 E4M3 rows 114 us.  A CTA costs about 7 us beside its chunks: 16
 // queries of 132 bf16 rows take 9.0 us.
 // With 8-bit entries the shared memory binds too: 2048 cycles a chunk (products 1024, staged bytes in and
-// out 512, widened codes 512) beside 2074 of MMAs.  16 queries over 131,072 entries 275 us; 2048 over 8192 would
+// out 512, widened codes 512) beside 2074 of MMAs.  16 queries over 131,072 entries 270 us; 2048 over 8192 would
 // take 2.06 ms, pairs of CTAs (pair_attention.cu) 1.56.  (Codes to registers without staging, four lanes a key, the same; staged rows without a swizzle,
 // two keys a phase with their pieces in turn, 2.65 ms.)
 #include <cfloat>
@@ -121,9 +121,9 @@ struct KaRun {
   uint32_t wl, sl, el;                // keys of each kind from chunk 0 on (chunk c has them less 64 c)
 };
 
-__device__ __forceinline__ KaRun ka_run(const KeysParams& p, int64_t bq, int b, int64_t base, int sp, int split) {
+__device__ __forceinline__ KaRun ka_run(const KeysParams& p, int64_t t, int64_t base, int32_t n_entries, int sp, int split) {
   KaRun q;
-  q.t = p.q_pos[bq];
+  q.t = t;
   const bool live = q.t >= 0;
   q.lo = live && q.t >= p.W ? q.t - p.W + 1 : 0;
   // the window positions lo .. t that lie in rows 0 .. S - 1 (unsigned differences: any
@@ -140,7 +140,8 @@ __device__ __forceinline__ KaRun ka_run(const KeysParams& p, int64_t bq, int b, 
   }
   const int64_t sn = live ? (q.lo < p.n_sink ? q.lo : (int64_t)p.n_sink) : 0;
   if (live && p.main_kv) {
-    en = visible_entries(min(q.t, INT64_MAX - 1), p.m, p.n_entries[b]);   // t + 1 has to exist
+    // (m is 1 or 2, and t + 1 has to exist)
+    en = min((min(q.t, INT64_MAX - 1) + 1) >> (p.m - 1), (int64_t)n_entries);
     if (en > p.cap) en = p.cap;       // reported by the kernel
     if (en < 0) en = 0;
   }
@@ -221,14 +222,21 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   if (sm.tmem_base != 0 && tid == 0) report(p.hdr, CSA2_ERR_CUDA, 2);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  const int64_t base = E8 && p.W == 0 ? 0 : p.base_pos[b];
-  const KaRun q = ka_run(p, bq, b, base, sp, split);
+  // (one latency for all three, in which the copy of Q into the last K buffer begins)
+  const int64_t base = E8 && p.W == 0 ? 0 : p.base_pos[b], t = p.q_pos[bq];
+  const int32_t n_entries = p.main_kv ? p.n_entries[b] : 0;
+  if (tid == 32 * KA_COPY_WARP) {
+    tc::bar_arrive_expect_tx(&sm.q_full, 8u * KA_COL);
+    for (int h = 0; h < 2; h++)
+      tc::tma_load_3d(smem + ((KA_BUFS - 1) * 2 + h) * KA_HALF, &map_q, 0, (int32_t)(bq * H), 4 * h, &sm.q_full);
+  }
+  const KaRun q = ka_run(p, t, base, n_entries, sp, split);
   const int n_ch = q.n;
   if (sp == 0 && tid == 0 && q.t >= 0) {              // what the caller did not supply
     if (E8 && p.W == 0) {                             // no window
     } else if (q.lo < base) report(p.hdr, CSA2_ERR_BOUNDS, q.lo);
     else if ((uint64_t)q.t - (uint64_t)base >= (uint64_t)p.S) report(p.hdr, CSA2_ERR_BOUNDS, q.t);
-    if (p.main_kv && p.n_entries[b] > p.cap) report(p.hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
+    if (n_entries > p.cap && p.main_kv) report(p.hdr, CSA2_ERR_BOUNDS, n_entries);
   }
 
   // Chunk c (counted from c_lo) uses K buffer c % 3; it is that buffer's use c / 3.
@@ -294,9 +302,6 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     // ================= copies
     if (lane == 0 && n_ch > 0) {
       bool ok = true;
-      tc::bar_arrive_expect_tx(&sm.q_full, 8u * KA_COL);   // Q into the last K buffer
-      for (int i = 0; i < 8; i++)
-        tc::tma_load_2d(smem + (KA_BUFS - 1) * 2 * KA_HALF + i * KA_COL, &map_q, i * 64, (int32_t)(bq * H), &sm.q_full);
       uint32_t staged = 0;                            // uses of the staging area
       auto next_stage = [&](uint32_t bytes) {
         if (staged > 0) ok = ok && ka_wait(&sm.stage_free, staged - 1, sm, p.hdr, 43);
@@ -310,23 +315,23 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       auto ahead = [&](int c) {
         if (c >= q.cr && c < n_ch) tc::prefetch_l2(kv + (int64_t)c * (KA_KEYS * ENTRY), ka_keys(q, c) * ENTRY);
       };
-      if (p.main_kv)
-        for (int c = 1; c < KA_AHEAD; c++) ahead(c);
       for (int c = 0; c < n_ch; c++) {
+        if (p.main_kv && c == 1)                      // (behind the first chunk's own copies)
+          for (int i = 1; i < 1 + KA_AHEAD; i++) ahead(i);
         if (c >= q.cr) {                              // entries, contiguous
           const uint32_t bytes = (uint32_t)((E8 ? KA_KEYS : ka_keys(q, c)) * ENTRY);
           next_stage(bytes);
           if (E8) {                                   // four column chunks of 128 dims, SW128
-            for (int i = 0; i < D / 128; i++)
-              tc::tma_load_2d(stage + i * (KA_KEYS * 128), &map_sinks, i * 128,
-                              (int32_t)((int64_t)b * p.cap + q.e0 + KA_KEYS * c), &sm.stage_full);
+            for (int i = 0; i < D / 128; i += 2)
+              tc::tma_load_3d(stage + i * (KA_KEYS * 128), &map_sinks, 0,
+                              (int32_t)((int64_t)b * p.cap + q.e0 + KA_KEYS * c), i, &sm.stage_full);
           } else {
             tc::bulk_load(stage, kv + (int64_t)c * (KA_KEYS * ENTRY), bytes, &sm.stage_full);
           }
-          ahead(c + KA_AHEAD);
+          if (c > 0) ahead(c + KA_AHEAD);
           continue;
         }
-        if (p.main_kv) ahead(c + KA_AHEAD);
+        if (p.main_kv && c > 0) ahead(c + KA_AHEAD);
         const bool window = c < q.cw;
         const CUtensorMap* map = window ? &map_rows : &map_sinks;
         const int32_t y = (int32_t)(window ? (int64_t)b * p.S + q.r0 + KA_KEYS * c : (int64_t)b * p.n_sink + q.s0 + KA_KEYS * c);
@@ -495,8 +500,8 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     const int head = 16 * warp + (lane & 15), half = lane >> 4;
     float m_used = -INFINITY, l_sum = 0.f;            // the head's reference; its sum over this lane's keys
     bool ok = true;
+    ok = ok && ka_wait(&sm.q_full, 0, sm, p.hdr, 45);   // (without keys too: no copy may land behind the CTA's end)
     if (n_ch > 0) {                                   // Q: this lane's 256 dims of its head to TMEM
-      ok = ok && ka_wait(&sm.q_full, 0, sm, p.hdr, 45);
       const unsigned char* qh = smem + ((KA_BUFS - 1) * 2 + half) * KA_HALF;
       __half2 most = __half2half2(__ushort_as_half(0));   // F16: largest |q| of the lane's even and odd dims
 #pragma unroll 1
@@ -873,7 +878,7 @@ static int keys_split(int64_t BQ, int64_t chunks, int64_t* cost_out = nullptr) {
 // here, whichever takes less time by the same count.  A pair's chunk takes 0.85 us (1.2 here), and it costs
 // PAIR_FIXED of them, 14 us, beside its own (7 here).  As chosen, us (pairs / single CTAs, each with its best split):
 // 3 x 37 queries of 10,007 entries 108 / 134, 1 x 100 of 4000 71 / 81, 1 x 2 of 8000 24.9 / 19.9, 16 x 2 of
-// 2000 27.5 / 22.6, 1 x 8 of 600 18.0 / 13.4.
+// 2000 27.5 / 22.6, 1 x 8 of 600 18.0 / 13.4.  (Pairs as they were: since then they cost about 4 us less.)
 // The lengths of the sequences are on the device, and `chunks` is the longest's.  So a split counts for pairs with the mean of
 // two times: of all alike, and of several that have 7/10 on average, whose items fill the gaps in each other's
 // waves.  (3 x 37 queries, split in 1 / 2: of 10,007, 7006 and 4005 entries 155 / 108, of 10,007 each 155 / 172.)
@@ -977,7 +982,7 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
   p.split = plan.split;
   p.part = reinterpret_cast<float*>(part);
   CUtensorMap mq, mr, ms;
-  if (!encode_bf16_rows512(&mq, p.q, (uint64_t)BQ * H, H)) return cudaErrorInvalidValue;
+  if (!encode_bf16_rows512_halves(&mq, p.q, (uint64_t)BQ * H, H)) return cudaErrorInvalidValue;
   auto rows = [&](CUtensorMap* map, const void* base, int64_t n) {
     return p.rows_fp8 ? encode_u8_rows512(map, base, (uint64_t)n, KA_KEYS)
                       : encode_bf16_rows512(map, base, (uint64_t)n, KA_KEYS);
@@ -993,7 +998,7 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
       const cudaError_t e = launch_pair_attention(p, B, mr, stream);
       return e != cudaSuccess || p.split == 1 ? e : launch_keys_join(p, BQ, stream);
     }
-    if (p.cap > 0 && !encode_u8_rows512_sw128(&ms, p.main_kv, (uint64_t)B * p.cap, KA_KEYS)) return cudaErrorInvalidValue;
+    if (p.cap > 0 && !encode_u8_rows512_halves(&ms, p.main_kv, (uint64_t)B * p.cap, KA_KEYS)) return cudaErrorInvalidValue;
     return keys_launch<true, true>(p, BQ, mq, mr, ms, stream);
   }
   return p.main_kv || p.rows_fp8 ? keys_launch<true, false>(p, BQ, mq, mr, ms, stream)

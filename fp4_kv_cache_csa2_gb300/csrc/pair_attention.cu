@@ -18,10 +18,11 @@
 // The lanes of a head sit in different warps, which pass each other partial scores and weights through
 // shared memory (384 cycles).
 //
-// Bound by shared memory: 1,600 cycles a chunk, 1,565 of them in use (by counters: 925 of the load/store
-// unit, with waits and the above; 512 of products; 128 of copies).  2048 queries over 8192 entries 1.56 ms (a CTA a query 2.06),
-// 3 x 37 over 10,007, 7006 and 4005 entries 108 us (134).  A pair costs 14 us beside its chunks.  Without the
-// staging area, codes by 16-byte loads a chunk ahead: 1.65 ms.
+// Bound by shared memory: 1,900 cycles a chunk, 1,565 of them in use (by counters: 925 of the load/store
+// unit, with waits and the above; 512 of products; 128 of copies), and what waits behind them: the softmax takes
+// 1,600 from scores to weights.  2048 queries over 8192 entries 1.51 ms (a CTA a query 2.06),
+// 3 x 37 over 10,007, 7006 and 4005 entries 103 us (134).  A pair costs 8 us beside its chunks.  Without the
+// staging area, codes by 16-byte loads a chunk ahead: 0.09 ms more; two softmax groups, even and odd chunks: 0.37 more.
 //
 // Both queries share the keys, each with its own limits: what one of them does not see has weight 0
 // for it.  So no key may hold an infinity or a NaN: codes cannot, and of window rows
