@@ -876,13 +876,14 @@ static int keys_split(int64_t BQ, int64_t chunks, int64_t* cost_out = nullptr) {
 
 // A call over an 8-bit cache: pairs of CTAs with two queries each (pair_attention.cu), or a CTA a query as
 // here, whichever takes less time by the same count.  A pair's chunk takes 0.85 us (1.2 here), and it costs
-// PAIR_FIXED of them, 14 us, beside its own (7 here).  As chosen, us (pairs / single CTAs, each with its best split):
-// 3 x 37 queries of 10,007 entries 108 / 134, 1 x 100 of 4000 71 / 81, 1 x 2 of 8000 24.9 / 19.9, 16 x 2 of
-// 2000 27.5 / 22.6, 1 x 8 of 600 18.0 / 13.4.  (Pairs as they were: since then they cost about 4 us less.)
+// PAIR_FIXED of them, 9 us, beside its own (7 here).  Us (pairs / single CTAs, each with its best split):
+// 1 x 100 queries of 4000 entries 60 / 81, 1 x 4 of 131,072 64 / 80, 8 x 4 of 4000 28.6 / 32.6, 16 x 2 of 2000
+// 21.2 / 23.0, 1 x 16 of 4000 21.8 / 23.2, 1 x 2 of 8000 17.6 / 17.4, 1 x 8 of 600 14.5 / 12.9, 1 x 32 of 1000
+// 18.2 / 17.7.  (Of 15 sizes two are chosen wrongly: 4 x 3 of 30,000 65.5 / 63.3 and 2 x 8 of 2000 17.4 / 18.4.)
 // The lengths of the sequences are on the device, and `chunks` is the longest's.  So a split counts for pairs with the mean of
 // two times: of all alike, and of several that have 7/10 on average, whose items fill the gaps in each other's
-// waves.  (3 x 37 queries, split in 1 / 2: of 10,007, 7006 and 4005 entries 155 / 108, of 10,007 each 155 / 172.)
-constexpr int PAIR_FIXED = 16;
+// waves.  (3 x 37 queries, split in 1 / 2: of 10,007, 7006 and 4005 entries 155 / 103, of 10,007 each 150 / 168.)
+constexpr int PAIR_FIXED = 11;
 struct Cache8Plan { bool pairs; int split; };
 
 static Cache8Plan cache8_plan(int B, int Q, int64_t chunks) {
