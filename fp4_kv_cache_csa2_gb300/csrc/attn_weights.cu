@@ -202,7 +202,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     int v = 0;
     if (qi < p.Q) {
       const int64_t t = p.q_pos[(int64_t)b * p.Q + qi];
-      if (t >= 0) v = (int)visible_entries(min(t, INT64_MAX - 1), p.m, n);
+      if (t >= 0) v = (int)min((min(t, INT64_MAX - 1) + 1) >> (p.m - 1), (int64_t)n);   // (m is 1 or 2)
     }
     sm.vis[i] = v;
     most = max(most, v);
@@ -497,7 +497,11 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
   if (*(volatile int*)&sm.err != 0)
     for (int i = 0; i < 1000; i++) __nanosleep(1000);
   // (nothing of the other CTA's is on its way here once both are done)
-  if (PAIR) tc::cluster_sync();
+  if (PAIR) {
+    __syncwarp();
+    tc::cluster_arrive_relaxed();
+    tc::cluster_wait();
+  }
   if (warp == AW_MMA_WARP) {
     tc::fence_after_sync();
     if (PAIR) tc::tmem_dealloc_pair(0u, 512);
