@@ -20,8 +20,8 @@
 //
 // Bound by shared memory: 1,900 cycles a chunk, 1,565 of them in use (by counters: 925 of the load/store
 // unit, with waits and the above; 512 of products; 128 of copies), and what waits behind them: the softmax takes
-// 1,600 from scores to weights.  2048 queries over 8192 entries 1.51 ms (a CTA a query 2.06),
-// 3 x 37 over 10,007, 7006 and 4005 entries 103 us (134).  A pair costs 8 us beside its chunks.  Without the
+// 1,600 from scores to weights.  2048 queries over 8192 entries 1.53 ms (a CTA a query 2.06),
+// 3 x 37 over 10,007, 7006 and 4005 entries 105 us (134).  A pair costs 8 us beside its chunks.  Without the
 // staging area, codes by 16-byte loads a chunk ahead: 0.09 ms more; two softmax groups, even and odd chunks: 0.37 more.
 //
 // Both queries share the keys, each with its own limits: what one of them does not see has weight 0
@@ -241,6 +241,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     auto scores = [&](uint32_t c) {
       const uint32_t buf = c % PA_BUFS;
       wait_mma(&sm.full[buf], c / PA_BUFS, 81);
+      tc::acquire_shared();
       const uint64_t ka = k_d + buf * (PA_BUF >> 4);
       const uint32_t s = PA_S_COL + 64 * (c & 1);
 #pragma unroll
@@ -412,7 +413,10 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_first(&sm.full[buf]);
+      if (lane == 0) {                                // (for the warp, whose writes come before)
+        if (rank) tc::bar_arrive_first_release(&sm.full[buf]);
+        else tc::bar_arrive(&sm.full[buf]);
+      }
     }
   } else {
     // ================= softmax: lane of TMEM l = 32 (warp % 4) + lane: head l % 64, half l / 64 (of Q's dims, of the

@@ -1,0 +1,33 @@
+"""The 8-bit cache where its calls can go wrong between CTAs and at the ends of their ranges."""
+import numpy as np
+import pytest
+import torch
+
+import fp4_kv_cache_csa2_gb300 as csa2
+from tests.test_gpu_cache8 import SCALE, attend_and_check, attn_case, cache_of, dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("Q,n,W,fp8", [(152, 1300, 128, True), (60, 3000, 0, False), (300, 1300, 200, False)])
+def test_attention_pairs_read_what_the_other_cta_wrote(Q, n, W, fp8):
+    """Each CTA of a pair widens half of the dims of every key, and one of them issues the products of both: the
+    same bits from every call, alone and beside a call that keeps the GPU's memory busy."""
+    pos = n - Q + np.arange(Q)[None, :]
+    codes, scales, q, rows, base = attn_case(31, 1, Q, -(-n // 8) * 8, [n], 1, W, fp8, pos)
+    out, lse = attend_and_check(codes, scales, [n], 1, q, rows, base, pos, W)
+    cache, qd, pd = cache_of(codes, scales, [n]), q.cuda(), dev(pos)
+    rd, bd = (rows.cuda(), dev(base)) if W else (None, None)
+    ws = csa2.Workspace(csa2.cache8_attn_workspace_size(1, Q, n, W))
+    a = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    b, beside = torch.zeros_like(a), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(40):
+        got, got_lse = torch.zeros_like(out), torch.zeros_like(lse)
+        if i % 2:
+            with torch.cuda.stream(beside):
+                b.copy_(a)
+        csa2.cache8_attn(cache, qd, pd, SCALE, got, ws, max_n=n, W=W, swa=rd, swa_base_pos=bd, lse=got_lse)
+        assert torch.equal(got, out) and torch.equal(got_lse, lse), i
+    torch.cuda.synchronize()
+    assert ws.sync_status()[0] == 0
