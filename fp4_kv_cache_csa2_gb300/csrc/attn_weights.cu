@@ -294,6 +294,8 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
           first = false;
         }
       }
+      // CTA 1's last arrivals, before this CTA ends
+      for (uint32_t x = u < 2 ? 0 : u - 2; x < u; x++) wait_mma(&sm.s_free[x & 1], x >> 1, 60);
     }
   } else if (PAIR && warp == AW_MMA2_WARP) {
     // ================= the lse of a group's heads
@@ -354,6 +356,11 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
           u++;
         }
       }
+      // the last arrivals of CTA 0's products, before this CTA ends
+      if (!resident)
+        for (uint32_t x = u < C::RING ? 0 : u - C::RING; x < u; x++)
+          for (int h = 0; h < 2; h++) wait(&sm.q_free[x % C::RING][h], x / C::RING, 65);
+      for (int h = 0; h < 2 && live > 0; h++) wait(&sm.a_free[h], live - 1, 67);
     }
     __syncwarp();
   } else if (warp >= AW_SUM_WARPS) {
@@ -496,7 +503,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
   // after a timeout copies may be in flight that nobody waited for: time for them to land
   if (*(volatile int*)&sm.err != 0)
     for (int i = 0; i < 1000; i++) __nanosleep(1000);
-  // (nothing of the other CTA's is on its way here once both are done)
+  // (each CTA has waited for all that the other sends it)
   if (PAIR) {
     __syncwarp();
     tc::cluster_arrive_relaxed();

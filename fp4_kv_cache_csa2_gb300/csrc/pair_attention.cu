@@ -302,6 +302,8 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           tc::tma_load_3d(kt, &map_rows, 0, row, 4 * rank, &sm.row_full[buf]);
         }
       }
+      // the last arrivals of CTA 0's products, of which the fill warps have not waited for all, before this CTA ends
+      for (int i = 0; i < min(n_ch, PA_BUFS); i++) wait(&sm.free_[i], (n_ch - 1 - i) / PA_BUFS, 92);
     }
     __syncwarp();
   } else if (warp >= PA_SOFT_WARPS) {
@@ -682,7 +684,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
   if (*(volatile int*)&sm.err != 0)
     for (int i = 0; i < 1000; i++) __nanosleep(1000);
   __syncwarp();
-  tc::cluster_arrive_relaxed();                       // (nothing of the other CTA's is on its way here once both are done)
+  tc::cluster_arrive_relaxed();                       // (each CTA has waited for all that the other sends it)
   tc::cluster_wait();
   if (warp == PA_MMA_WARP) {
     tc::fence_after_sync();

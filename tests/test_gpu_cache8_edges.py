@@ -31,3 +31,29 @@ def test_attention_pairs_read_what_the_other_cta_wrote(Q, n, W, fp8):
         assert torch.equal(got, out) and torch.equal(got_lse, lse), i
     torch.cuda.synchronize()
     assert ws.sync_status()[0] == 0
+
+
+@pytest.mark.parametrize("B,Q,n", [(76, 2, 600), (5, 9, 100), (1, 152, 1300)])
+def test_pairs_one_behind_another(B, Q, n):
+    """A CTA of a pair ends when nothing is on its way to it: calls follow each other without a pause, on SMs whose
+    shared memory the next one takes at once."""
+    pos = n - Q + np.repeat(np.arange(Q)[None, :], B, 0)
+    codes, scales, q, _, _ = attn_case(32, 1, Q, -(-n // 8) * 8, [n], 1, 0, False, pos[:1])
+    cache = cache_of(codes.repeat(B, 0), scales.repeat(B, 0), [n] * B)
+    qd, pd = q.repeat(B, 1, 1, 1).cuda(), dev(pos)
+    ws = csa2.Workspace(max(csa2.cache8_attn_workspace_size(B, Q, n), csa2.attn_weights_workspace_size(B, Q, n)))
+    calls = []
+    for _ in range(30):
+        out, lse = torch.zeros_like(qd), torch.zeros(B, Q, 64, device="cuda")
+        w = torch.zeros(B, cache.cap, device="cuda")
+        csa2.cache8_attn(cache, qd, pd, SCALE, out, ws, max_n=n, lse=lse)
+        csa2.attn_weights(cache, qd, pd, lse, SCALE, w, ws, max_n=n)
+        csa2.attn_weights(cache, qd, pd, lse, SCALE, w, ws, max_n=n, prev=w)
+        calls.append((out, lse, w))
+    assert ws.sync_status()[0] == 0
+    for got in calls[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(got, calls[0]))
+    # all sequences are alike, and every query spreads its 64 heads' weights, twice (lse off by 2^-20 (1 + |lse|))
+    assert torch.equal(calls[0][0], calls[0][0][:1].expand_as(qd)) and torch.equal(calls[0][2], calls[0][2][:1].expand(B, -1))
+    total = calls[0][2].double().sum(1)
+    assert torch.all((total - 128 * Q).abs() <= 1e-4 * 128 * Q)
