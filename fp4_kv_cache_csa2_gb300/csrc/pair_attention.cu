@@ -226,6 +226,15 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     else tc::bar_arrive(bar);
   };
 
+  // With a window every thread comes to one more barrier of the cluster: behind it the softmax warps know whether a
+  // fill warp of either CTA has met a row that is not finite.
+  auto told = [&]() {
+    if (p.W == 0) return;
+    __syncwarp();
+    tc::cluster_arrive();
+    tc::cluster_wait();
+  };
+
   if (warp == PA_MMA_WARP) {
     // ================= MMAs, in CTA 0 (the whole warp runs the loop, one lane issues)
     constexpr uint32_t idesc_s = tc::idesc_f16(128, 128, 0, 0), idesc_o = tc::idesc_f16(128, 256, 0, 1);
@@ -265,6 +274,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       }
       tc::commit_pair(leader, &sm.free_[buf]);
     }
+    told();
   } else if (warp == PA_COPY_WARP) {
     // ================= copies: this CTA's half of the dims
     if (lane == 0 && n_ch > 0) {
@@ -306,6 +316,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       for (int i = 0; i < min(n_ch, PA_BUFS); i++) wait(&sm.free_[i], (n_ch - 1 - i) / PA_BUFS, 92);
     }
     __syncwarp();
+    told();
   } else if (warp >= PA_SOFT_WARPS) {
     // ================= K buffers
     const int ft = tid - 32 * PA_SOFT_WARPS;
@@ -420,6 +431,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         else tc::bar_arrive(&sm.full[buf]);
       }
     }
+    told();
   } else {
     // ================= softmax: lane of TMEM l = 32 (warp % 4) + lane: head l % 64, half l / 64 (of Q's dims, of the
     // keys); of its 32 keys and its columns of Q and O the warp takes the half `sub`
@@ -619,10 +631,18 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     if (own == 0) sm.ref[head] = m_used;              // (all lanes of a head have the same)
 
     // ================= output: 128 of a lane's 256 dims a warp
+    if (p.W > 0) {
+      __syncwarp();
+      tc::cluster_arrive_relaxed();                   // (what these warps have written is not the other CTA's)
+    }
     if (n_ch > 0) {
       const int last = n_ch - 1;
       if (*(volatile int*)&sm.err == 0) wait(&sm.free_[last % PA_BUFS], last / PA_BUFS, 91);
       tc::fence_after_sync();
+    }
+    if (p.W > 0) {
+      __syncwarp();
+      tc::cluster_wait();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     named_sync(2, 32 * PA_SOFT_WARPS);                // the sums

@@ -214,10 +214,11 @@ __device__ __forceinline__ void acquire_shared() {
   asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 
-// *p = x in the shared memory of the cluster's CTA `rank`, before anything this thread does next.
+// *p = x in the shared memory of the cluster's CTA `rank`: there behind a cluster_arrive of this thread and the other's
+// cluster_wait.
 __device__ __forceinline__ void store_other(int* p, int x, int rank) {
-  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %2;\n st.relaxed.cluster.shared::cluster.s32 [a], %1;\n"
-               " fence.acq_rel.cluster;\n}\n" :: "r"(smem_u32(p)), "r"(x), "r"(rank) : "memory");
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %2;\n st.relaxed.cluster.shared::cluster.s32 [a], %1;\n}\n"
+               :: "r"(smem_u32(p)), "r"(x), "r"(rank) : "memory");
 }
 
 // A load into this CTA's shared memory that completes on the barrier at `bar`'s place in CTA 0 of the

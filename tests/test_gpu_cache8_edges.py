@@ -57,3 +57,26 @@ def test_pairs_one_behind_another(B, Q, n):
     assert torch.equal(calls[0][0], calls[0][0][:1].expand_as(qd)) and torch.equal(calls[0][2], calls[0][2][:1].expand(B, -1))
     total = calls[0][2].double().sum(1)
     assert torch.all((total - 128 * Q).abs() <= 1e-4 * 128 * Q)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [0, 1300])
+def test_attention_pairs_tell_each_other_of_rows_that_are_not_finite(n, fp8):
+    """Either half of the dims (a CTA each), met by the last chunk or long before the end: exactly the queries that
+    see the row become NaN."""
+    Q, W = 152, 40
+    pos = 1200 + np.arange(Q)[None, :]
+    codes, scales, q, rows, base = attn_case(33, 1, Q, 1304, [n], 1, W, fp8, pos)
+    cache, qd, pd, bd = cache_of(codes, scales, [n]), q.cuda(), dev(pos), dev(base)
+    ws = csa2.Workspace(csa2.cache8_attn_workspace_size(1, Q, 1300, W))
+    for at in (1200, 1201, 1350, 1351):                # seen by both queries of its pair, by the second alone, by the last two, one
+        for dim in (3, 255, 256, 511):
+            bad = rows.clone()
+            bad[0, at - int(base[0]), dim] = 0x7F if fp8 else float("inf" if dim == 3 else "nan")
+            out, lse = torch.zeros_like(qd), torch.zeros(1, Q, 64, device="cuda")
+            csa2.cache8_attn(cache, qd, pd, SCALE, out, ws, max_n=1300, W=W, swa=bad.cuda(), swa_base_pos=bd, lse=lse)
+            sees = torch.from_numpy((pos[0] >= at) & (pos[0] < at + W)).cuda()
+            assert torch.equal(torch.isnan(out[0].float()).all(-1).all(-1), sees), (at, dim)
+            assert torch.equal(torch.isnan(out[0].float()).any(-1).any(-1), sees), (at, dim)
+            assert torch.equal(torch.isnan(lse[0]).all(-1), sees) and torch.equal(torch.isnan(lse[0]).any(-1), sees)
+    assert ws.sync_status()[0] == 0
