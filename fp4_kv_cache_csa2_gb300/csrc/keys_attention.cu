@@ -125,11 +125,12 @@ __device__ __forceinline__ KaRun ka_run(const KeysParams& p, int64_t t, int64_t 
   KaRun q;
   q.t = t;
   const bool live = q.t >= 0;
-  q.lo = live && q.t >= p.W ? q.t - p.W + 1 : 0;
+  // W = 0: no window, and no first position of one (t + 1 need not exist)
+  q.lo = live && p.W > 0 && q.t >= p.W ? q.t - p.W + 1 : 0;
   // the window positions lo .. t that lie in rows 0 .. S - 1 (unsigned differences: any
   // two positions have one), so that the work is bounded by what was supplied
   int64_t row = 0, wn = 0, en = 0;
-  if (live && q.t >= base) {
+  if (live && p.W > 0 && q.t >= base) {
     const uint64_t s = (uint64_t)p.S, r0 = q.lo > base ? (uint64_t)q.lo - (uint64_t)base : 0;
     const uint64_t end = (uint64_t)q.t - (uint64_t)base;     // row of position t
     const uint64_t r1 = end < s ? end + 1 : s;

@@ -86,7 +86,7 @@ struct PaQuery {
 __device__ __forceinline__ PaQuery pa_query(const KeysParams& p, int32_t n_entries, int64_t base, int64_t t) {
   PaQuery q{t, 0, 0, 0, 0};
   if (t < 0) return q;
-  q.lo = q.t >= p.W ? q.t - p.W + 1 : 0;
+  q.lo = p.W > 0 && q.t >= p.W ? q.t - p.W + 1 : 0;   // (W = 0: t + 1 need not exist)
   if (p.W > 0 && q.t >= base) {       // (unsigned differences: any two positions have one)
     const uint64_t s = (uint64_t)p.S, r0 = q.lo > base ? (uint64_t)q.lo - (uint64_t)base : 0;
     const uint64_t end = (uint64_t)q.t - (uint64_t)base, r1 = end < s ? end + 1 : s;

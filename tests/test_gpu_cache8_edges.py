@@ -80,3 +80,13 @@ def test_attention_pairs_tell_each_other_of_rows_that_are_not_finite(n, fp8):
             assert torch.equal(torch.isnan(out[0].float()).any(-1).any(-1), sees), (at, dim)
             assert torch.equal(torch.isnan(lse[0]).all(-1), sees) and torch.equal(torch.isnan(lse[0]).any(-1), sees)
     assert ws.sync_status()[0] == 0
+
+
+@pytest.mark.parametrize("m", [1, 2])
+@pytest.mark.parametrize("Q,n,max_n", [(1, 200, 200), (2, 200, 200), (1, 3000, 3000), (152, 1300, 1300), (60, 3000, 3000)])
+def test_attention_at_the_last_positions_without_a_window(Q, n, max_n, m):
+    """2^63 - 1 has no successor: a CTA a query or pairs, divided over CTAs or not."""
+    top = (1 << 63) - 1
+    pos = np.array([[top - i for i in range(Q)]], np.int64)
+    codes, scales, q, _, _ = attn_case(34, 1, Q, -(-n // 8) * 8, [n], m, 0, False, np.zeros((1, Q), np.int64))
+    attend_and_check(codes, scales, [n], m, q, None, None, pos, 0, max_n=max_n)
