@@ -516,12 +516,13 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
   }
 }
 
-// The query splits' sums of an entry, in order, and what it had.
+// The query splits' sums of an entry, in order, and what it had.  (No splits: the call launches nothing else, and
+// this kernel reports.)
 __global__ void __launch_bounds__(256) attn_weights_join_kernel(AwParams p, int blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = (int)(blockIdx.x / (uint32_t)blocks), n = aw_entries(p, b);
   const int64_t j = (int64_t)(blockIdx.x % (uint32_t)blocks) * 256 + threadIdx.x;
-  if (p.Q == 0 && j == 0 && p.n_entries[b] > min(p.cap, p.max_n)) report(p.hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
+  if (p.splits == 0 && j == 0 && p.n_entries[b] > min(p.cap, p.max_n)) report(p.hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
   if (j >= n) return;
   float acc = 0.f;
   for (int s = 0; s < p.splits; s++) acc += __ldcg(p.part + ((int64_t)s * p.B + b) * p.pitch + j);
@@ -578,10 +579,11 @@ static cudaError_t aw_launch(const AwParams& p, const CUtensorMap& mq, const CUt
 }
 
 cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream) {
-  if (p.B == 0 || p.max_n == 0 || p.cap == 0) return cudaSuccess;
+  if (p.B == 0) return cudaSuccess;
+  const int64_t most = min(p.max_n, p.cap);           // (0: a report is all that can come of it)
   const AwPlan plan = attn_weights_plan(p.B, p.Q, p.max_n);
   p.runs = plan.runs;
-  p.splits = p.Q ? plan.splits : 0;
+  p.splits = p.Q > 0 && most > 0 ? plan.splits : 0;
   p.pitch = attn_weights_pitch(p.max_n);
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
@@ -591,7 +593,7 @@ cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e = cudaSuccess;
-  if (p.Q > 0) {
+  if (p.splits > 0) {
     CUtensorMap mq = {}, mc = {};                     // (of what the kernel does not copy: unused)
     if (p.Q > 1 && !encode_bf16_rows512_halves(&mq, p.q, (uint64_t)p.B * p.Q * H, H)) return cudaErrorInvalidValue;
     if (p.scales8 && !encode_u8_rows512_sw128(&mc, p.kv, (uint64_t)p.B * p.cap, AW_KEYS)) return cudaErrorInvalidValue;
@@ -599,7 +601,7 @@ cudaError_t launch_attn_weights(AwParams p, cudaStream_t stream) {
     else e = p.Q == 1 ? aw_launch<false, false>(p, mq, mc, cfg) : aw_launch<false, true>(p, mq, mc, cfg);
     if (e != cudaSuccess || p.splits == 1) return e;
   }
-  const int blocks = (int)ceil_div(min(p.max_n, p.cap), 256);
+  const int blocks = (int)max(ceil_div(most, 256), (int64_t)1);
   cfg.gridDim = dim3((unsigned)p.B * (unsigned)blocks);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;

@@ -1,5 +1,7 @@
 """The attention weight that cache entries gather (csa2_attn_weights, 4-bit and 8-bit
 cache) against the 64-bit form."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -234,3 +236,30 @@ def test_weights_offsets_beyond_32_bits():
     assert np.all(np.abs(w[1, cap - 128:].double().cpu().numpy() - want) <= tol)
     flat = 64 * np.exp(-20.0)                                                      # entries of zeros
     assert torch.all((w[1, :cap - 128].double() - flat).abs() <= 1e-5 * flat)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("Q", [0, 1, 3])
+def test_weights_of_no_entries_report_too(bits, Q):
+    """max_n = 0, or a cache without room: nothing is written, and a sequence that has entries is reported."""
+    cache, values = make_cache(14, bits, 2, 64, [0, 0], 1)
+    q, pos, lse = torch.zeros(2, Q, H, D, dtype=torch.bfloat16), np.full((2, Q), 70), np.zeros((2, Q, H), np.float32)
+    for n, status in (([0, 5], 6), ([0, -2], 0)):
+        cache.n_entries.copy_(dev(np.asarray(n, np.int32)))
+        check(cache, values, [0, 0], 1, q, pos, lse, max_n=0, status=status)
+    w, ws = torch.full((2, 8), 5.0, device="cuda"), csa2.Workspace(csa2.attn_weights_workspace_size(2, Q, 64))
+    qd, ld = torch.zeros(2, 4, H, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 4, H, device="cuda")
+    pd = torch.zeros(2, 4, dtype=torch.int64, device="cuda")
+    a = csa2.WeightsArgs(B=2, Q=Q, scale=SCALE, decay=1.0, max_n=64, q_pos=pd.data_ptr(), q=qd.data_ptr(), lse=ld.data_ptr(),
+                         weights=w.data_ptr())
+    if bits == 8:
+        c = csa2.Cache8Struct(codes=cache.codes.data_ptr(), scales=cache.scales.data_ptr(), cap=0,
+                              n_entries=cache.n_entries.data_ptr(), m=1)
+    else:
+        c = csa2.CacheStruct(main_kv=cache.main_kv.data_ptr(), cap=0, n_entries=cache.n_entries.data_ptr(), m=1)
+    call = csa2.load().csa2_cache8_attn_weights if bits == 8 else csa2.load().csa2_attn_weights
+    for n, status in (([0, 1], 6), ([0, 0], 0)):
+        cache.n_entries.copy_(dev(np.asarray(n, np.int32)))
+        assert call(ctypes.byref(c), ctypes.byref(a), ws.buf.data_ptr(), ws.nbytes, torch.cuda.current_stream().cuda_stream) == 0
+        assert ws.sync_status()[0] == status
+    assert torch.all(w == 5.0)
