@@ -7,7 +7,8 @@
 // over heads and queries stays in its registers: no exchange between lanes, no
 // atomics, the same result every time.
 //
-// Sums: 64 weights in binary32, then compensated over a CTA's queries.
+// Sums: the 64 weights of a query in binary32, in eight runs; compensated over a CTA's queries, and again over the
+// CTAs that share them.
 //
 // A CTA takes a run of tiles of one sequence.  The tile's entries lie in TMEM as the A operand
 // (256 columns of 16-bit pairs): with A in shared memory a product of N = 64 would take 48
@@ -87,6 +88,13 @@ __device__ __forceinline__ uint32_t aw_uniform(uint32_t x) { return __reduce_or_
 // x's bits that the mask has
 __device__ __forceinline__ float aw_masked(float x, float mask) {
   return __uint_as_float(__float_as_uint(x) & __float_as_uint(mask));
+}
+
+// acc += x, with what its rounding loses kept for the next sum.
+__device__ __forceinline__ void aw_add(float& acc, float& lost, float x) {
+  const float y = x - lost, z = acc + y;
+  lost = fabsf(z) < INFINITY ? (z - acc) - y : 0.f;
+  acc = z;
 }
 
 // entries of sequence b that the call deals with
@@ -479,9 +487,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
             tc::bar_arrive(&sm.col_free[ci]);
           }
           if (j < sm.vis[NQ == 1 ? g : 2 * g + half]) {
-            const float y = (s4[0] + s4[1]) + (s4[2] + s4[3]) - lost, z = acc + y;
-            lost = fabsf(z) < INFINITY ? (z - acc) - y : 0.f;
-            acc = z;
+            aw_add(acc, lost, (s4[0] + s4[1]) + (s4[2] + s4[3]));
           }
           u++;
         }
@@ -524,8 +530,8 @@ __global__ void __launch_bounds__(256) attn_weights_join_kernel(AwParams p, int 
   const int64_t j = (int64_t)(blockIdx.x % (uint32_t)blocks) * 256 + threadIdx.x;
   if (p.splits == 0 && j == 0 && p.n_entries[b] > min(p.cap, p.max_n)) report(p.hdr, CSA2_ERR_BOUNDS, p.n_entries[b]);
   if (j >= n) return;
-  float acc = 0.f;
-  for (int s = 0; s < p.splits; s++) acc += __ldcg(p.part + ((int64_t)s * p.B + b) * p.pitch + j);
+  float acc = 0.f, lost = 0.f;                        // compensated: there may be 16,384 splits
+  for (int s = 0; s < p.splits; s++) aw_add(acc, lost, __ldcg(p.part + ((int64_t)s * p.B + b) * p.pitch + j));
   const int64_t at = (int64_t)b * p.cap + j;
   p.out[at] = p.prev ? fmaf(p.decay, p.prev[at], acc) : acc;
 }

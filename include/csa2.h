@@ -605,8 +605,8 @@ csa2_status csa2_cache8_attn(const csa2_cache8 *cache, const csa2_cache8_attn_ar
  * 4-byte aligned; weights must not overlap an input other than prev.
  * Precision: entries are exact operands; one query (Q = 1) is rounded to f16 as in
  * csa2_dense_attn (of any size), several are taken as they are in bf16.
- * Binary32 products and sums, compensated over queries; the same inputs
- * give the same bits.  Workspace: csa2_attn_weights_workspace_size with the
+ * Binary32 products and sums: plain over a query's 64 heads, compensated over queries (over those of a CTA, and
+ * over CTAs when they are divided).  The same inputs give the same bits.  Workspace: csa2_attn_weights_workspace_size with the
  * call's B, Q and max_n (partial sums when the queries are divided over CTAs).
  */
 typedef struct {

@@ -263,3 +263,32 @@ def test_weights_of_no_entries_report_too(bits, Q):
         assert call(ctypes.byref(c), ctypes.byref(a), ws.buf.data_ptr(), ws.nbytes, torch.cuda.current_stream().cuda_stream) == 0
         assert ws.sync_status()[0] == status
     assert torch.all(w == 5.0)
+
+
+@pytest.mark.parametrize("Q", [64, 35 * 1024])
+def test_weights_of_divided_queries_keep_what_is_small(Q):
+    """One query's weights are 2^24 times the others': each CTA's sum of those alone is less than half of the last place
+    of the total (35 * 1024 queries are 35 CTAs' at least).  Queries of zeros, so that a weight is exp(-lse)."""
+    n = 11
+    cache, _ = make_cache(15, 4, 1, 16, [n], 1)
+
+    def weigh(lse):
+        k = lse.shape[0]
+        w = torch.zeros(1, 16, device="cuda")
+        ws = csa2.Workspace(csa2.attn_weights_workspace_size(1, k, 16))
+        csa2.attn_weights(cache, torch.zeros(1, k, H, D, dtype=torch.bfloat16, device="cuda"),
+                          torch.full((1, k), n, device="cuda"), lse[None, :, None].expand(1, k, H).contiguous(), SCALE, w, ws, max_n=16)
+        assert ws.sync_status()[0] == 0
+        assert torch.all(w[0, :n] == w[0, 0])                                      # entries are alike
+        return w[0, 0].double().item()
+
+    per_cta = 2 if Q == 64 else 1024                                               # queries of a CTA's sum, or fewer
+    lse = torch.full((Q,), -np.log(50.0 / (H * per_cta)), dtype=torch.float32, device="cuda")
+    big = torch.tensor([-24 * np.log(2.0)] + [np.inf] * 3, dtype=torch.float32, device="cuda")
+    small, large = weigh(lse[:4]) / 4, weigh(big)                                  # (2^-23 of themselves: 64 equal weights sum exactly)
+    assert 2 ** 29.9 < large < 2 ** 30.1 and 40 < small * per_cta < 60
+    lse[0] = big[0]
+    # Roundings to binary32 of compensated sums: of a half's queries, of the two halves, over CTAs, of the result: 2^-24 each
+    # of the total; `small` by 2^-22 of itself
+    want = large + (Q - 1) * small
+    assert abs(weigh(lse) - want) <= 4 * 2.0 ** -24 * want + 2.0 ** -22 * (Q - 1) * small
