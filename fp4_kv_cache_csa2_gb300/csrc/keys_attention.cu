@@ -51,7 +51,7 @@
 // queries of 132 bf16 rows take 9.0 us.
 // With 8-bit entries the shared memory binds too: 2048 cycles a chunk (products 1024, staged bytes in and
 // out 512, widened codes 512) beside 2074 of MMAs.  16 queries over 131,072 entries 270 us; 2048 over 8192 would
-// take 2.06 ms, pairs of CTAs (pair_attention.cu) 1.56.  (Codes to registers without staging, four lanes a key, the same; staged rows without a swizzle,
+// take 2.06 ms, pairs of CTAs (pair_attention.cu) 1.53.  (Codes to registers without staging, four lanes a key, the same; staged rows without a swizzle,
 // two keys a phase with their pieces in turn, 2.65 ms.)
 #include <cfloat>
 
@@ -881,9 +881,11 @@ static int keys_split(int64_t BQ, int64_t chunks, int64_t* cost_out = nullptr) {
 // 1 x 100 queries of 4000 entries 60 / 81, 1 x 4 of 131,072 64 / 80, 8 x 4 of 4000 28.6 / 32.6, 16 x 2 of 2000
 // 21.2 / 23.0, 1 x 16 of 4000 21.8 / 23.2, 1 x 2 of 8000 17.6 / 17.4, 1 x 8 of 600 14.5 / 12.9, 1 x 32 of 1000
 // 18.2 / 17.7.  (Of 15 sizes two are chosen wrongly: 4 x 3 of 30,000 65.5 / 63.3 and 2 x 8 of 2000 17.4 / 18.4.)
-// The lengths of the sequences are on the device, and `chunks` is the longest's.  So a split counts for pairs with the mean of
-// two times: of all alike, and of several that have 7/10 on average, whose items fill the gaps in each other's
-// waves.  (3 x 37 queries, split in 1 / 2: of 10,007, 7006 and 4005 entries 155 / 103, of 10,007 each 150 / 168.)
+// The lengths of the sequences are on the device, and `chunks` is the longest's.  So a split counts for pairs with the
+// mean of two times: of B lengths alike, and of B lengths spread evenly below the longest (B / B, .. 1 / B of it: (B + 1) / 2B
+// on average), whose items fill the gaps in each other's waves.  Of 18 sizes (2 to 32 sequences, 4 to 128 queries, 2000 to
+// 30,000 entries) the split taken costs 1.04 times the best one's time when lengths are alike (1.19 at most: 7 x 16 of
+// 5300, 103 us for 86), 1.03 when they are spread (1.16); a split for lengths alike 1.00 and 1.18 (1.68).
 constexpr int PAIR_FIXED = 11;
 struct Cache8Plan { bool pairs; int split; };
 
@@ -897,10 +899,11 @@ static Cache8Plan cache8_plan(int B, int Q, int64_t chunks) {
   for (int s = 1; s <= slots && s <= chunks && (s == 1 || pairs * s <= KA_WAVES * slots); s++) {
     const int64_t join = s > 1 ? 169 + 4 * s + 3 * pairs * s : 0, longest = 48 * (PAIR_FIXED + ceil_div(chunks, s));
     const int64_t alike = longest * ceil_div(pairs * s, slots) + join;
-    const int64_t uneven = B > 1 ? max(longest, 48 * pairs * s * (PAIR_FIXED + 7 * ceil_div(chunks, s) / 10) / slots) + join : alike;
-    if (alike + uneven < best) {
+    const int64_t each = PAIR_FIXED + (B + 1) * ceil_div(chunks, s) / (2 * (int64_t)B);
+    const int64_t spread = B > 1 ? max(longest, 48 * pairs * s * each / slots) + join : alike;
+    if (alike + spread < best) {
       split = s;
-      best = alike + uneven;
+      best = alike + spread;
       time = alike;
     }
   }

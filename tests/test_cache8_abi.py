@@ -269,3 +269,13 @@ def test_a_workspace_on_the_host_is_refused():
     for call in ("write", "attn", "weights", "evict"):
         with pytest.raises(ValueError, match="ws: the workspace is not on a CUDA device"):
             calls(call)
+
+
+def test_the_split_of_pairs_follows_the_number_of_sequences(lib):
+    """Lengths are not known on the host: the longest's work is divided as for lengths spread evenly below it (several
+    sequences), or as it is (one)."""
+    part = 64 * (2 + 512) * 4                                # a partial state
+    for (B, Q, n, W), split in {(4, 37, 10000, 128): 2, (3, 37, 10007, 128): 2, (7, 16, 5300, 128): 2, (16, 8, 2000, 128): 1,
+                                (2, 128, 3000, 128): 1, (3, 8, 30000, 128): 6, (1, 148, 10000, 128): 1}.items():
+        want = 256 + (-(-B * Q * split * part // 256) * 256 if split > 1 else 0)
+        assert csa2.cache8_attn_workspace_size(B, Q, n, W) == want, (B, Q, n, W)
