@@ -146,6 +146,7 @@ _SIGNATURES = {
     "csa2_evict": (_I, [_P, _P, _P, _P, _SZ, _P]),
     "csa2_cache8_evict": (_I, [_P, _P, _P, _P, _SZ, _P]),
     "csa2_test_withhold_arrival": (_I, [_I]),
+    "csa2_test_cache8_attn_plan": (_I, [_I, _I, _I64, _I, ctypes.POINTER(ctypes.c_int)]),
 }
 
 _lib = None

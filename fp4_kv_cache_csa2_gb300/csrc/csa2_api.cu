@@ -547,6 +547,13 @@ size_t csa2_cache8_attn_workspace_size(int B, int Q, int64_t max_n, int W) {
   return HDR + align256(cache8_part_bytes(B, Q, cache8_chunks(max_n, W)));
 }
 
+int csa2_test_cache8_attn_plan(int B, int Q, int64_t max_n, int W, int* split) {
+  if (B < 0 || Q < 0 || max_n < 0 || W < 0 || (int64_t)B * Q > MAX_KEY_QUERIES || !split) return -1;
+  const Cache8Plan plan = cache8_plan(B, Q, cache8_chunks(max_n, W));
+  *split = plan.split;
+  return plan.pairs ? 1 : 0;
+}
+
 csa2_status csa2_cache8_attn(const csa2_cache8* cache, const csa2_cache8_attn_args* a, void* ws, size_t ws_bytes,
                              void* stream) {
   if (!a || a->max_n < 0 || a->W < 0) return CSA2_ERR_INVALID_ARG;

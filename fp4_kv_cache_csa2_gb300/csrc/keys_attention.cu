@@ -887,9 +887,8 @@ static int keys_split(int64_t BQ, int64_t chunks, int64_t* cost_out = nullptr) {
 // 30,000 entries) the split taken costs 1.04 times the best one's time when lengths are alike (1.19 at most: 7 x 16 of
 // 5300, 103 us for 86), 1.03 when they are spread (1.16); a split for lengths alike 1.00 and 1.18 (1.68).
 constexpr int PAIR_FIXED = 11;
-struct Cache8Plan { bool pairs; int split; };
 
-static Cache8Plan cache8_plan(int B, int Q, int64_t chunks) {
+Cache8Plan cache8_plan(int B, int Q, int64_t chunks) {
   int64_t single = 0;
   const Cache8Plan alone{false, keys_split((int64_t)B * Q, chunks, &single)};
   const int64_t pairs = (int64_t)B * ((Q + 1) / 2), slots = KA_SMS / 2;

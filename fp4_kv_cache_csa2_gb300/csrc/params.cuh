@@ -221,7 +221,9 @@ cudaError_t launch_keys_attention(KeysParams p, int B, int64_t chunks, void* par
 cudaError_t launch_window_ring(const KeysParams& p, int B, cudaStream_t stream);
 bool window_ring_fits(int64_t W, int n_sink);
 size_t keys_part_bytes(int64_t BQ, int64_t chunks);
-size_t cache8_part_bytes(int B, int Q, int64_t chunks);   // of a call with scales8
+struct Cache8Plan { bool pairs; int split; };             // of a call with scales8
+Cache8Plan cache8_plan(int B, int Q, int64_t chunks);
+size_t cache8_part_bytes(int B, int Q, int64_t chunks);
 // Several queries of an 8-bit cache (p.split and p.part set; the maps of q, the rows and the codes)
 cudaError_t launch_pair_attention(const KeysParams& p, int B, const CUtensorMap& mr8, cudaStream_t stream);
 struct AwPlan { int runs, splits; };    // of a sequence's tiles, of its queries

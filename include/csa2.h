@@ -691,6 +691,14 @@ csa2_status csa2_cache8_evict(const csa2_cache8 *cache, const csa2_cache8 *to, c
  */
 csa2_status csa2_test_withhold_arrival(int enable);
 
+/*
+ * Test hook, host only: which kernel a csa2_cache8_attn call of these sizes takes.
+ * Returns 1 for pairs of CTAs with two queries each, 0 for a CTA a query, and
+ * writes the number of CTAs (pairs) that the keys of one are divided over to
+ * `split` (host).  -1: sizes that the call refuses, or no `split`.
+ */
+int csa2_test_cache8_attn_plan(int B, int Q, int64_t max_n, int W, int *split);
+
 #ifdef __cplusplus
 }
 #endif

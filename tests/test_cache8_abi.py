@@ -279,3 +279,20 @@ def test_the_split_of_pairs_follows_the_number_of_sequences(lib):
                                 (2, 128, 3000, 128): 1, (3, 8, 30000, 128): 6, (1, 148, 10000, 128): 1}.items():
         want = 256 + (-(-B * Q * split * part // 256) * 256 if split > 1 else 0)
         assert csa2.cache8_attn_workspace_size(B, Q, n, W) == want, (B, Q, n, W)
+
+
+def test_which_kernel_the_attention_takes(lib):
+    """The sizes of the GPU tests of either kernel (tests/test_gpu_cache8.py, tests/test_gpu_cache8_edges.py)."""
+    def plan(B, Q, max_n, W):
+        split = ctypes.c_int(0)
+        return lib.csa2_test_cache8_attn_plan(B, Q, max_n, W, ctypes.byref(split)), split.value
+
+    for call in [(1, 152, 1300, 0), (2, 76, 1441, 130), (4, 37, 1600, 99), (1, 151, 1300, 200), (1, 152, 1300, 64), (1, 152, 1300, 16),
+                 (1, 152, 1300, 40), (1, 152, 1300, 128), (1, 300, 1300, 200), (1, 152, 500, 20), (2, 76, 400, 0)]:
+        assert plan(*call) == (1, 1), call                   # pairs, undivided
+    for call in [(1, 60, 2999, 128), (2, 31, 2999, 64), (1, 60, 3000, 0), (1, 60, 1300, 20), (1, 60, 2000, 20), (1, 60, 1 << 40, 20)]:
+        assert plan(*call)[0] == 1 and plan(*call)[1] > 1, call
+    for call in [(1, 1, 200, 0), (1, 1, 3000, 0), (16, 1, 131072, 128), (1, 2, 200, 0), (1, 4, 600, 0), (3, 2, 1000, 130), (1, 60, 1, 20)]:
+        assert plan(*call)[0] == 0, call
+    assert plan(1, 0, 64, 0)[0] == 0 and plan(-1, 1, 64, 0)[0] == plan(1, 1, -1, 0)[0] == plan(1, 1, 1, -1)[0] == -1
+    assert plan(1 << 13, 1 << 12, 64, 0)[0] == -1 and lib.csa2_test_cache8_attn_plan(1, 1, 64, 0, None) == -1

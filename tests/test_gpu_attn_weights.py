@@ -292,3 +292,37 @@ def test_weights_of_divided_queries_keep_what_is_small(Q):
     # of the total; `small` by 2^-22 of itself
     want = large + (Q - 1) * small
     assert abs(weigh(lse) - want) <= 4 * 2.0 ** -24 * want + 2.0 ** -22 * (Q - 1) * small
+
+
+@pytest.mark.parametrize("Q", [1, 2])
+@pytest.mark.parametrize("bits,scale,keys", [(4, SCALE * 2.0 ** -17, 1.0), (8, SCALE * 2.0 ** -17, 1.0), (8, SCALE, 2.0 ** -18)])
+def test_weights_of_large_queries_are_their_softmax(bits, scale, keys, Q):
+    """Heads of 2^17 to 2^30, brought back to ordinary scores by the softmax scale or by the entries, with their own lse:
+    weights of 1 / n and more, as far as scores let them."""
+    n = [200]
+    cache, values = make_cache(16, bits, 1, 200, n, 1)
+    if keys != 1.0:
+        cache.scales.mul_(keys)
+        values = values * keys
+    pos = np.array([[199, 150][:Q]])
+    q = torch.randn(1, Q, H, D, generator=torch.Generator().manual_seed(16))
+    q = (q * 2.0 ** 17 * torch.exp2(torch.arange(H) % 3)[:, None]).bfloat16()
+    q[0, 0, 7] *= 2.0 ** 11                                                        # scores of thousands: one entry has all
+    qd = q.double().numpy()
+    # a head goes to f16 by a power of two that puts its largest below 2^16: what then is at least 2^-14 is exact
+    top = np.exp2(np.floor(np.log2(np.abs(qd).max(-1, keepdims=True))) - 15)
+    assert np.all((np.abs(qd) >= 2.0 ** -14 * np.maximum(top, 1)) | (qd == 0))
+    lse, want, tol = np.zeros((1, Q, H), np.float32), np.zeros(200), np.zeros(200)
+    for i in range(Q):
+        k = values[0, :pos[0, i] + 1]
+        x = scale * (k @ qd[0, i].T)
+        lse[0, i] = x.max(0) + np.log(np.exp(x - x.max(0)).sum(0))
+        w, t = c8.gathered(qd[0, i], k, lse[0, i].astype(np.float64), scale)
+        want[:len(k)] += w
+        tol[:len(k)] += t
+    assert abs(want.sum() - Q * H) < 0.1 and np.median(tol[:151] / want[:151]) < 1e-2
+    out, ws = torch.zeros(1, 200, device="cuda"), csa2.Workspace(csa2.attn_weights_workspace_size(1, Q, 200))
+    csa2.attn_weights(cache, q.cuda(), dev(pos), dev(lse), scale, out, ws, max_n=200)
+    assert ws.sync_status()[0] == 0
+    err = np.abs(out[0].double().cpu().numpy() - want)
+    assert np.all(err <= tol), np.max(err / tol)

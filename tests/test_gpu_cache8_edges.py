@@ -90,3 +90,11 @@ def test_attention_at_the_last_positions_without_a_window(Q, n, max_n, m):
     pos = np.array([[top - i for i in range(Q)]], np.int64)
     codes, scales, q, _, _ = attn_case(34, 1, Q, -(-n // 8) * 8, [n], m, 0, False, np.zeros((1, Q), np.int64))
     attend_and_check(codes, scales, [n], m, q, None, None, pos, 0, max_n=max_n)
+
+
+@pytest.mark.parametrize("Q,n,W,max_n", [(60, 2992, 20, 1300), (60, 2992, 20, 2000), (152, 1300, 20, 500)])
+def test_attention_pairs_of_more_entries_than_their_split_was_made_for(Q, n, W, max_n):
+    """Calls that take pairs (test_cache8_abi.py has the plan) over more chunks than max_n lets them expect."""
+    pos = n - Q + np.arange(Q)[None, :]
+    case = attn_case(35, 1, Q, -(-n // 8) * 8, [n], 1, W, False, pos)
+    attend_and_check(*case[:2], [n], 1, *case[2:], pos, W, max_n=max_n)
