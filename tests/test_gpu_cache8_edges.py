@@ -98,3 +98,27 @@ def test_attention_pairs_of_more_entries_than_their_split_was_made_for(Q, n, W, 
     pos = n - Q + np.arange(Q)[None, :]
     case = attn_case(35, 1, Q, -(-n // 8) * 8, [n], 1, W, False, pos)
     attend_and_check(*case[:2], [n], 1, *case[2:], pos, W, max_n=max_n)
+
+
+@pytest.mark.parametrize("B,Q,n,W", [(300, 1, 90, 0), (40, 3, 100, 20), (1, 1, 600, 0), (2, 76, 1300, 9)])
+def test_attention_of_padded_batches(B, Q, n, W):
+    """Padded queries, whatever their q holds, give zeros; the others what they give in a batch without padding."""
+    pos = n - Q + np.repeat(np.arange(Q)[None, :], B, 0)
+    codes, scales, q, rows, base = attn_case(36, B, Q, -(-n // 8) * 8, [n] * B, 1, W, False, pos)
+    cache, bd = cache_of(codes, scales, [n] * B), dev(base) if W else None
+    pad = np.random.default_rng(36).random((B, Q)) < 0.5
+    pad[0, 0] = True
+    ws = csa2.Workspace(csa2.cache8_attn_workspace_size(B, Q, n, W))
+    got = []
+    for padded in (False, True):
+        qd, p = q.cuda(), pos.copy()
+        if padded:
+            qd[torch.from_numpy(pad).cuda()] = float("nan")
+            p[pad] = -1
+        out, lse = torch.full_like(qd, 3.0), torch.full((B, Q, 64), 3.0, device="cuda")
+        csa2.cache8_attn(cache, qd, dev(p), SCALE, out, ws, max_n=n, W=W, swa=rows.cuda() if W else None, swa_base_pos=bd, lse=lse)
+        got.append((out, lse))
+    assert ws.sync_status()[0] == 0
+    at = torch.from_numpy(pad).cuda()
+    assert torch.all(got[1][0][at] == 0) and torch.all(got[1][1][at] == -float("inf"))
+    assert torch.equal(got[1][0][~at], got[0][0][~at]) and torch.equal(got[1][1][~at], got[0][1][~at])
