@@ -560,11 +560,12 @@ csa2_status csa2_cache8_write(const csa2_cache8 *cache, const csa2_cache8_write_
  * max(0, t-W+1) .. t (W = 0: the entries alone): csa2_dense_attn on this cache,
  * with its padding, outputs, reports, limits and operands (codes are exact in f16;
  * the scales enter the scores and the weights in binary32, before the weights are
- * rounded to 11 bits).  Scales of 2^-60 and more keep that precision (the write
- * makes no others).  A window row that a query sees has to be finite in f16 (NaN makes the
- * outputs of the queries that see it NaN).  n_entries[b] > cap raises CSA2_ERR_BOUNDS (cap entries are
- * attended).  Workspace: csa2_cache8_attn_workspace_size with the call's B, Q,
- * max_n and W.
+ * rounded to 11 bits).  Scales from 2^-60 to 2^80, and 0, keep that precision (the
+ * write makes none below, and larger ones of latents beyond 2^86 alone).  A window
+ * row that a query sees has to be finite in f16: one that is not makes the outputs
+ * of the queries that see it NaN.  n_entries[b] > cap raises CSA2_ERR_BOUNDS (cap
+ * entries are attended).  Workspace: csa2_cache8_attn_workspace_size with the
+ * call's B, Q, max_n and W.
  */
 typedef struct {
     int B, Q;                   /* sequences, queries per sequence              */
@@ -592,22 +593,26 @@ csa2_status csa2_cache8_attn(const csa2_cache8 *cache, const csa2_cache8_attn_ar
  * the same cache) and their 64 heads, natural exponentials.  lse is what the
  * attention of these queries wrote (csa2_dense_attn, csa2_cache8_attn: then the
  * weights are the softmax's own; or that of another attention over more or fewer
- * keys).  A query with t < 0, or a head with lse = -inf, adds nothing, whatever its
- * q holds; NaN in q or lse reaches the entries that its query sees.  What a query does not see may hold anything.
+ * keys; the attention over selected entries, csa2_sparse_swa_attn, writes none).
+ * A query with t < 0, or a head with lse = -inf, adds nothing, whatever its q
+ * holds; NaN in q or lse reaches the entries that its query sees.  What a query
+ * does not see may hold anything.
  *   prev         [B][cap], NULL: zeros (decay is then unused).  prev may be
  *                weights itself.
  *   weights      out [B][cap]: entries j < min(n_entries[b], max_n) are written,
  *                the others left as they were.
  *   max_n        no sequence has more entries; n_entries[b] above it or above cap
  *                raises CSA2_ERR_BOUNDS (the entries from there on are left out).
- * Q = 0 scales what was gathered.  B * Q <= 2^24; 4-bit and 8-bit cache
+ * Q = 0 scales what was gathered.  B and B * Q <= 2^24; 4-bit and 8-bit cache
  * (csa2_cache8_attn_weights).  q and the cache 16-byte, q_pos 8-byte, the others
  * 4-byte aligned; weights must not overlap an input other than prev.
  * Precision: entries are exact operands; one query (Q = 1) is rounded to f16 as in
- * csa2_dense_attn (of any size), several are taken as they are in bf16.
- * Binary32 products and sums: plain over a query's 64 heads, compensated over queries (over those of a CTA, and
- * over CTAs when they are divided).  The same inputs give the same bits.  Workspace: csa2_attn_weights_workspace_size with the
- * call's B, Q and max_n (partial sums when the queries are divided over CTAs).
+ * csa2_dense_attn (of any size), several are taken as they are in bf16; of an
+ * 8-bit cache with the scales that csa2_cache8_attn is made for.  Binary32 products
+ * and sums: plain over a query's 64 heads, compensated over queries (over those of
+ * a CTA, and over CTAs when they are divided).  The same inputs give the same bits.
+ * Workspace: csa2_attn_weights_workspace_size with the call's B, Q and max_n
+ * (partial sums when the queries are divided over CTAs).
  */
 typedef struct {
     int B, Q;                   /* sequences, queries per sequence              */
@@ -651,11 +656,14 @@ csa2_status csa2_cache8_attn_weights(const csa2_cache8 *cache, const csa2_weight
  *                them.  NULL: left out.  May be weights when in place.
  * An evicted cache numbers its entries anew: entry j was entry kept[j] (of units:
  * 8 kept[j / 8] + j % 8).  A caller that goes on with it takes m * (entries that
- * left) off the positions it passes to the calls that read the cache (q_pos and, of a window,
- * its base), and rotates new entries with the positions they really have.  Block
+ * left) off the positions it passes to the calls that read the cache (q_pos and, of a
+ * window, its base), and rotates new entries with the positions they really have
+ * (csa2_compress_quantize rotates by the entry's number: a call a sequence, each
+ * with its table shifted, where sequences lost different numbers).  Block
  * summaries have to be made again.
  * n_entries[b] > cap raises CSA2_ERR_BOUNDS (cap entries are taken).  cap < 2^31,
- * budget < 2^31, else CSA2_ERR_UNSUPPORTED.  weights 16-byte, kept, n_out and
+ * budget < 2^31, B <= 2^20 and B * (budget / 40 + cap of `to` / 8192 + 2) < 2^31,
+ * else CSA2_ERR_UNSUPPORTED.  weights 16-byte, kept, n_out and
  * to_weights 4-byte aligned, the caches as everywhere.  Outputs must not overlap
  * inputs or each other but where it says so.  Workspace:
  * csa2_evict_workspace_size.

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import fp4_kv_cache_csa2_gb300 as csa2
+from tests import cache8_ref as c8
 from tests.test_gpu_cache8 import SCALE, attend_and_check, attn_case, cache_of, dev
 
 pytestmark = pytest.mark.gpu
@@ -122,3 +123,29 @@ def test_attention_of_padded_batches(B, Q, n, W):
     at = torch.from_numpy(pad).cuda()
     assert torch.all(got[1][0][at] == 0) and torch.all(got[1][1][at] == -float("inf"))
     assert torch.equal(got[1][0][~at], got[0][0][~at]) and torch.equal(got[1][1][~at], got[0][1][~at])
+
+
+@pytest.mark.parametrize("Q,n", [(1, 300), (152, 1300)])
+@pytest.mark.parametrize("power", [-52, 80])
+def test_scales_at_the_ends_of_their_range(power, Q, n):
+    """Scales from 2^-60 to 2^80, with softmax scales that bring the scores back: attention and weights."""
+    pos = n - Q + np.arange(Q)[None, :]
+    codes, scales, q, _, _ = attn_case(37, 1, Q, -(-n // 8) * 8, [n], 1, 0, False, pos, spread=1.0, q_size=0.7)
+    scales = np.minimum(np.maximum(scales * np.float32(2.0 ** power), np.float32(2.0 ** -60)), np.float32(2.0 ** 80))
+    scale = float(np.float32(SCALE * 2.0 ** -power))
+    cache, qd, pd = cache_of(codes, scales, [n]), q.cuda(), dev(pos)
+    out, lse, w = torch.zeros_like(qd), torch.zeros(1, Q, 64, device="cuda"), torch.zeros(1, cache.cap, device="cuda")
+    ws = csa2.Workspace(max(csa2.cache8_attn_workspace_size(1, Q, n), csa2.attn_weights_workspace_size(1, Q, n)))
+    csa2.cache8_attn(cache, qd, pd, scale, out, ws, max_n=n, lse=lse)
+    csa2.attn_weights(cache, qd, pd, lse, scale, w, ws, max_n=n)
+    assert ws.sync_status()[0] == 0
+    e, got, got_lse = c8.entries(codes[0], scales[0]), out[0].double().cpu().numpy(), lse[0].double().cpu().numpy()
+    want, tol = np.zeros(cache.cap), np.zeros(cache.cap)
+    for i in range(Q):
+        seen, qi = int(pos[0, i]) + 1, q[0, i].double().numpy()
+        o, l, b_o, b_l = c8.attend(qi, e[:seen], scale, scales[0].max())
+        assert np.all(np.abs(got[i] - o) <= b_o) and np.all(np.abs(got_lse[i] - l) <= b_l), i
+        more, t = c8.gathered(qi, e[:seen], got_lse[i], scale)
+        want[:seen] += more
+        tol[:seen] += t
+    assert np.all(np.abs(w[0].double().cpu().numpy() - want) <= tol)
