@@ -103,7 +103,8 @@ __device__ __forceinline__ int aw_entries(const AwParams& p, int b) {
 }
 
 // One head by a warp: q as f16 into its row of the stages, its factor and its lse in powers of two.
-__device__ __forceinline__ float2 aw_head(const uint16_t* q, float lse, float scale, bool live, unsigned char* stages, int row, int lane) {
+__device__ __forceinline__ float2 aw_head(const uint16_t* q, float lse, float scale, bool live, unsigned char* stages,
+                                          int row, int lane) {
   uint4 v[2] = {};
   live = live && lse != -INFINITY;                    // else weights of 0, whatever q holds
   if (live) {
@@ -139,14 +140,16 @@ __device__ __forceinline__ uint32_t aw_f16x2_to_bf16x2(uint32_t w) {
 
 template <bool E8, bool PAIR>
 __global__ void __launch_bounds__(AW_THREADS, 1)
-attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_codes) {
+attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q,
+                    const __grid_constant__ CUtensorMap map_codes) {
   using C = Aw<E8, PAIR>;
   using Small = typename C::Small;
   constexpr int NQ = C::NQ;
   extern __shared__ __align__(1024) unsigned char smem[];
   Small& sm = *reinterpret_cast<Small*>(smem + C::OFF_SMALL);
   WsHeader* hdr = p.hdr;
-  if (tc::smem_u32(smem) & 1023u) {                   // the swizzled tiles need the declared alignment (the same in both CTAs)
+  // the swizzled tiles need the declared alignment (the same in both CTAs)
+  if (tc::smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) report(hdr, CSA2_ERR_CUDA, 3);
     return;
   }
@@ -237,7 +240,8 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     // ================= MMAs (the whole warp runs the loop, one lane issues; of a pair, in CTA 0)
     // An MMA takes its addresses from uniform registers: what the loops follow from goes through a
     // reduction over the warp, whose result is uniform (else an MMA takes 82 cycles to issue).
-    constexpr uint32_t idesc = PAIR ? tc::idesc_bf16(NQ * AW_KEYS, C::N, 0, 0) : tc::idesc_f16(NQ * AW_KEYS, C::N, 0, 0);
+    constexpr uint32_t idesc =
+        PAIR ? tc::idesc_bf16(NQ * AW_KEYS, C::N, 0, 0) : tc::idesc_f16(NQ * AW_KEYS, C::N, 0, 0);
     const uint64_t q_d = tc::smem_desc(tc::smem_u32(smem), 16, 1024, tc::SW_128B);
     const uint32_t leader = tc::elect_one();
     const int n_live = rank == 0 ? (int)aw_uniform((uint32_t)live) : 0, n_g = (int)aw_uniform((uint32_t)ng);
@@ -312,7 +316,7 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
       for (int g = next_group(0, t_lo + t); g < ng; g = next_group(g + 1, t_lo + t)) {
         float l[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {                 // (sequences are a query's 64 heads apart: none behind the last query)
+        for (int i = 0; i < 4; i++) {                 // (none behind the sequence's last query)
           const int64_t q = (int64_t)(g_lo + g) * NQ + (i >> 1);
           l[i] = q < p.Q ? __ldcg(p.lse + ((int64_t)b * p.Q + q) * H + 32 * (i & 1) + lane) : -INFINITY;
         }
@@ -337,7 +341,8 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
         if (E8) {                                     // four column chunks of 128 dims, SW128
           tc::bar_arrive_expect_tx(&sm.tile_full[ts], C::TILE);
           for (int i = 0; i < D / 128; i++)
-            tc::tma_load_2d(dst + i * (AW_KEYS * 128), &map_codes, i * 128, (int32_t)(b * p.cap + first), &sm.tile_full[ts]);
+            tc::tma_load_2d(dst + i * (AW_KEYS * 128), &map_codes, i * 128, (int32_t)(b * p.cap + first),
+                            &sm.tile_full[ts]);
         } else {                                      // (none: the pair's second half may lie behind the cache)
           const uint32_t bytes = (uint32_t)max(min((int64_t)AW_KEYS, p.cap - first), (int64_t)0) * MAIN_BYTES;
           tc::bar_arrive_expect_tx(&sm.tile_full[ts], bytes);
@@ -433,8 +438,8 @@ attn_weights_kernel(AwParams p, const __grid_constant__ CUtensorMap map_q, const
     if (!PAIR && live > 0) {                          // the query: eight heads a warp
       for (int i = 0; i < H / AW_SUM_WARPS; i++) {
         const int head = (H / AW_SUM_WARPS) * warp + i;
-        const float2 c = aw_head(p.q + ((int64_t)b * H + head) * D, __ldcg(p.lse + (int64_t)b * H + head), p.scale, sm.vis[0] > 0,
-                                 smem, head, lane);
+        const float2 c = aw_head(p.q + ((int64_t)b * H + head) * D, __ldcg(p.lse + (int64_t)b * H + head), p.scale,
+                                 sm.vis[0] > 0, smem, head, lane);
         if (lane == 0) sm.col[0][head] = c;
       }
       tc::fence_proxy_async_smem();
@@ -561,7 +566,8 @@ AwPlan attn_weights_plan(int B, int Q, int64_t max_n) {
   return best;
 }
 
-int64_t attn_weights_pitch(int64_t max_n) { return ceil_div(max_n, AW_KEYS) * AW_KEYS; }   // floats of a sequence's partial sums
+// floats of a sequence's partial sums
+int64_t attn_weights_pitch(int64_t max_n) { return ceil_div(max_n, AW_KEYS) * AW_KEYS; }
 
 template <bool E8, bool PAIR>
 static cudaError_t aw_launch(const AwParams& p, const CUtensorMap& mq, const CUtensorMap& mc, cudaLaunchConfig_t cfg) {

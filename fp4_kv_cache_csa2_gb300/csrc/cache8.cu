@@ -13,7 +13,8 @@
 // low byte.
 //
 // Moves 1024 bytes in and 512 out an entry.  A warp an entry (a CTA a block) was bound by its instructions, 71 %
-// of the issue slots: 14.0 us for 4 x 8191 tokens, here 11.8 (8.1 without the look at ties).
+// of the issue slots: 13.9 us for 4 x 8191 tokens, here 10.6 (in a graph 10.3; 8.1 without the look at ties, which 28 %
+// of the warps' steps of 256 values take).  1,025 CTAs of which 760 fit at once.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(C8_THREADS, 5) cache8_write_kernel(C8WritePara
         c[i] = __float_as_uint(w);
       }
       if (far > C8_TIE) {
-        // (more often than by chance, one value in 1700: quotients of 8-bit numbers.)  The rest
+        // (a value in 275, more often than by chance: quotients of 8-bit numbers, all of one scale.)  The rest
         // x - n s is exact; beyond half of s, or at it with an odd code, the code moves towards it.
 #pragma unroll
         for (int i = 0; i < 8; i++) {

@@ -14,9 +14,9 @@
 // chunks before it have been read whose sources lie there (a unit never moves up, so they are before it);
 // which they are a search over the kept numbers tells, while the chunk's own copies are on their way.
 // Chunks are taken by ticket, in order: all a CTA waits for (with a limit) are flags of CTAs that
-// run already and wait for nothing before they set them.  (Waiting for every chunk before it: 225
-// us instead of 213 for 16 x 131,072 entries in place, 280 instead of 153 for 1M in 8 bits; with the selection
-// as it is now 187 and 131.)
+// run already and wait for nothing before they set them.  16 x 131,072 entries in place 173 us (151 into another
+// cache), 1M in 8 bits 121 (107).  (Waiting for every chunk before it, with an earlier selection in both: 225 us
+// instead of 213 and 280 instead of 153.)
 //
 // Bound by HBM: the bytes that stay, in and out.
 #include <climits>
@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) evict_select_ke
   const int count = (int)min(units, K);
   int32_t* kept = p.kept + (int64_t)b * K;
   // flags of the moves, and behind the last kept unit: -1
-  for (int64_t i = rank * EV_THREADS + tid; i < p.chunks; i += CLUSTER * EV_THREADS) p.flags[(int64_t)b * p.chunks + i] = 0;
+  for (int64_t i = rank * EV_THREADS + tid; i < p.chunks; i += CLUSTER * EV_THREADS)
+    p.flags[(int64_t)b * p.chunks + i] = 0;
   for (int64_t i = count + rank * EV_THREADS + tid; i < K; i += CLUSTER * EV_THREADS) kept[i] = -1;
   if (b == 0 && rank == 0 && tid == 0) *p.ticket = 0u;
   if (units <= K) {                                   // all stay
@@ -173,8 +174,10 @@ __global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) evict_select_ke
     constexpr int BATCH = UNIT == 1 ? 4 : 8;
     const float4* w4 = reinterpret_cast<const float4*>(all.w + u0 * UNIT);
     const int fours = UNIT == 1 ? quads : (2 * mine + 31) / 32 * 32;
-    const int whole = (int)min(max(n - u0 * UNIT, (int64_t)0) / 4, (int64_t)fours);   // of them without a part behind the last entry
-    const int f_lo = (int)min(max(all.first - u0, (int64_t)0), (int64_t)INT_MAX), f_hi = (int)min(max(all.recent - u0, (int64_t)0), (int64_t)INT_MAX);
+    // of them without a part behind the last entry
+    const int whole = (int)min(max(n - u0 * UNIT, (int64_t)0) / 4, (int64_t)fours);
+    const int f_lo = (int)min(max(all.first - u0, (int64_t)0), (int64_t)INT_MAX);
+    const int f_hi = (int)min(max(all.recent - u0, (int64_t)0), (int64_t)INT_MAX);
     for (int i0 = tid; i0 < fours; i0 += BATCH * EV_THREADS) {
       float4 v[BATCH];
 #pragma unroll
@@ -244,7 +247,8 @@ __global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) evict_select_ke
     left -= __shfl_sync(0xFFFFFFFFu, above, at);
     gt += __shfl_sync(0xFFFFFFFFu, own_above, at);
     for (int c = warp; c < 2 * CLUSTER; c += EV_WARPS)
-      sm.all_fine[c >> 1][32 * (c & 1) + lane] = ev_remote<CLUSTER>(&hist[EV_FINE * coarse + 32 * (c & 1) + lane], c >> 1);
+      sm.all_fine[c >> 1][32 * (c & 1) + lane] =
+          ev_remote<CLUSTER>(&hist[EV_FINE * coarse + 32 * (c & 1) + lane], c >> 1);
     __syncthreads();
     // lane l has bins EV_FINE - 1 - 2 l and the one below
     int2 f = make_int2(0, 0);
@@ -272,7 +276,8 @@ __global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) evict_select_ke
   ev_sync<CLUSTER>();
   int gt_base, eq_base, eq_all;                       // of the CTAs before this one; of all
   {
-    const int g = lane < CLUSTER ? ev_remote<CLUSTER>(&sm.gt, lane) : 0, e = lane < CLUSTER ? ev_remote<CLUSTER>(&sm.eq, lane) : 0;
+    const int g = lane < CLUSTER ? ev_remote<CLUSTER>(&sm.gt, lane) : 0;
+    const int e = lane < CLUSTER ? ev_remote<CLUSTER>(&sm.eq, lane) : 0;
     gt_base = __reduce_add_sync(0xFFFFFFFFu, lane < (int)rank ? g : 0);
     eq_base = __reduce_add_sync(0xFFFFFFFFu, lane < (int)rank ? e : 0);
     eq_all = __reduce_add_sync(0xFFFFFFFFu, e);
@@ -384,7 +389,8 @@ __global__ void __launch_bounds__(EV_MOVE_THREADS) evict_move_kernel(EvParams p)
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* rows = smem;                         // entries, index codes, then 4-byte words
   unsigned char* idx = rows + CE * C::ROW;
-  uint32_t* word = reinterpret_cast<uint32_t*>(idx + (BITS == 8 ? 0 : CE * IDX_CODE_BYTES));   // index scales, or a scale a unit
+  // index scales, or a scale a unit
+  uint32_t* word = reinterpret_cast<uint32_t*>(idx + (BITS == 8 ? 0 : CE * IDX_CODE_BYTES));
   float* weight = reinterpret_cast<float*>(word + (BITS == 8 ? CU : CE));
   __shared__ uint32_t ticket;
   __shared__ int from[CU];

@@ -50,9 +50,9 @@
 // 262 us, 0.99 PFLOP/s; 602 queries of 1000 E4M3 rows 114 us.  A CTA costs about 7 us beside its chunks: 16
 // queries of 132 bf16 rows take 9.0 us.
 // With 8-bit entries the shared memory binds too: 2048 cycles a chunk (products 1024, staged bytes in and
-// out 512, widened codes 512) beside 2074 of MMAs.  16 queries over 131,072 entries 270 us; 2048 over 8192 would
-// take 2.06 ms, pairs of CTAs (pair_attention.cu) 1.53.  (Codes to registers without staging, four lanes a key, the same; staged rows without a swizzle,
-// two keys a phase with their pieces in turn, 2.65 ms.)
+// out 512, widened codes 512) beside 2074 of MMAs.  16 queries over 131,072 entries 271 us; 2048 over 8192 would
+// take 2.06 ms, pairs of CTAs (pair_attention.cu) 1.53.  (Codes to registers without staging, four lanes a key,
+// the same; staged rows without a swizzle, two keys a phase with their pieces in turn, 2.65 ms.)
 #include <cfloat>
 
 #include "attn_common.cuh"
@@ -121,7 +121,8 @@ struct KaRun {
   uint32_t wl, sl, el;                // keys of each kind from chunk 0 on (chunk c has them less 64 c)
 };
 
-__device__ __forceinline__ KaRun ka_run(const KeysParams& p, int64_t t, int64_t base, int32_t n_entries, int sp, int split) {
+__device__ __forceinline__ KaRun ka_run(const KeysParams& p, int64_t t, int64_t base, int32_t n_entries, int sp,
+                                        int split) {
   KaRun q;
   q.t = t;
   const bool live = q.t >= 0;
@@ -613,7 +614,8 @@ keys_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
       for (int x = 0; x < 32; x++) c4[E8 ? x / BLK : x & 3] = fmaxf(c4[E8 ? x / BLK : x & 3], v[x]);
       if (E8) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) c4[i] += __log2f(fmaxf(s8[i], KA_FLOOR8));   // (of the reference alone: any value near it would do)
+        for (int i = 0; i < 4; i++)                   // (of the reference alone: any value near it would do)
+          c4[i] += __log2f(fmaxf(s8[i], KA_FLOOR8));
       }
       float cm = fmaxf(fmaxf(c4[0], c4[1]), fmaxf(c4[2], c4[3]));
       cm = fmaxf(cm, __shfl_xor_sync(0xFFFFFFFFu, cm, 16));
@@ -883,11 +885,12 @@ static int keys_split(int64_t BQ, int64_t chunks, int64_t* cost_out = nullptr) {
 // 1 x 100 queries of 4000 entries 60 / 81, 1 x 4 of 131,072 64 / 80, 8 x 4 of 4000 28.6 / 32.6, 16 x 2 of 2000
 // 21.2 / 23.0, 1 x 16 of 4000 21.8 / 23.2, 1 x 2 of 8000 17.6 / 17.4, 1 x 8 of 600 14.5 / 12.9, 1 x 32 of 1000
 // 18.2 / 17.7.  (Of 15 sizes two are chosen wrongly: 4 x 3 of 30,000 65.5 / 63.3 and 2 x 8 of 2000 17.4 / 18.4.)
-// The lengths of the sequences are on the device, and `chunks` is the longest's.  So a split counts for pairs with the
-// mean of two times: of B lengths alike, and of B lengths spread evenly below the longest (B / B, .. 1 / B of it: (B + 1) / 2B
-// on average), whose items fill the gaps in each other's waves.  Of 18 sizes (2 to 32 sequences, 4 to 128 queries, 2000 to
-// 30,000 entries) the split taken costs 1.04 times the best one's time when lengths are alike (1.19 at most: 7 x 16 of
-// 5300, 103 us for 86), 1.03 when they are spread (1.16); a split for lengths alike 1.00 and 1.18 (1.68).
+// The lengths of the sequences are on the device, and `chunks` is the longest's.  So a split counts for pairs with
+// the mean of two times: of B lengths alike, and of B lengths spread evenly below the longest (B / B, .. 1 / B of
+// it: (B + 1) / 2B on average), whose items fill the gaps in each other's waves.  Of 18 sizes (2 to 32 sequences, 4
+// to 128 queries, 2000 to 30,000 entries) the split taken costs 1.04 times the best one's time when lengths are
+// alike (1.19 at most: 7 x 16 of 5300, 103 us for 86), 1.03 when they are spread (1.16); a split for lengths alike
+// 1.00 and 1.18 (1.68).
 constexpr int PAIR_FIXED = 11;
 
 Cache8Plan cache8_plan(int B, int Q, int64_t chunks) {

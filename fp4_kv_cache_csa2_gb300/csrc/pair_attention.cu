@@ -50,7 +50,7 @@ constexpr int PA_BUFS = 4;                                // the last two take Q
 constexpr int PA_STAGE = 2 * PA_COL;                      // a chunk's 256 codes a key, SW128
 constexpr int PA_STAGES = 2;
 constexpr int PA_OFF_STAGE = PA_BUFS * PA_BUF;
-constexpr int PA_OFF_S = PA_OFF_STAGE + PA_STAGES * PA_STAGE;   // partial scores for the other lane: [4][256 threads] float4
+constexpr int PA_OFF_S = PA_OFF_STAGE + PA_STAGES * PA_STAGE;   // scores for the other lane: [4][256 threads] float4
 constexpr int PA_OFF_P = PA_OFF_S + 4 * 256 * 16;         // weights for the other lane: [2][256 threads] uint4
 constexpr int PA_OFF_SMALL = PA_OFF_P + 2 * 256 * 16;
 constexpr int PA_O_COL = 0, PA_Q_COL = 256, PA_S_COL = 384;
@@ -126,7 +126,8 @@ __device__ __forceinline__ PaRun pa_run(const PaQuery* q, int sp, int split) {
   r.bn = n1;
   if (n0 > 0 && n1 > 0) {
     const int lo = min(q[0].row_lo, q[1].row_lo), hi = max(q[0].row_hi, q[1].row_hi);
-    if ((int64_t)hi - lo <= (int64_t)n0 + n1) {   // windows that overlap or meet: one part.  (Else rows of one are none of the other's)
+    // windows that overlap or meet: one part.  (Else rows of one are none of the other's)
+    if ((int64_t)hi - lo <= (int64_t)n0 + n1) {
       r.a0 = lo;
       r.an = hi - lo;
       r.bn = 0;
@@ -135,7 +136,8 @@ __device__ __forceinline__ PaRun pa_run(const PaQuery* q, int sp, int split) {
   r.en = max(q[0].entries, q[1].entries);
   r.ca = (int)ceil_div(r.an, PA_KEYS);
   r.cb = r.ca + (int)ceil_div(r.bn, PA_KEYS);
-  const uint32_t nc = (uint32_t)r.cb + (uint32_t)ceil_div(r.en, PA_KEYS), each = nc / (uint32_t)split, more = nc % (uint32_t)split;
+  const uint32_t nc = (uint32_t)r.cb + (uint32_t)ceil_div(r.en, PA_KEYS);
+  const uint32_t each = nc / (uint32_t)split, more = nc % (uint32_t)split;
   r.c0 = sp * (int)each + min(sp, (int)more);
   r.n = (int)each + (sp < (int)more ? 1 : 0);
   return r;
@@ -146,7 +148,8 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
                  const __grid_constant__ CUtensorMap map_codes) {
   extern __shared__ __align__(1024) unsigned char smem[];
   PaSmall& sm = *reinterpret_cast<PaSmall*>(smem + PA_OFF_SMALL);
-  if (tc::smem_u32(smem) & 1023u) {                   // the swizzled tiles need the declared alignment (the same in both CTAs)
+  // the swizzled tiles need the declared alignment (the same in both CTAs)
+  if (tc::smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) report(p.hdr, CSA2_ERR_CUDA, 5);
     return;
   }
@@ -372,7 +375,8 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           uint32_t o[2][16];
 #pragma unroll
           for (int y = 0; y < 2; y++) {
-            const uint4* src = reinterpret_cast<const uint4*>(kt + 2 * y * PA_COL + (j >> 1) * PA_COL + PA_COL / 2 + key * 64 + 32 * (j & 1));
+            const uint4* src = reinterpret_cast<const uint4*>(kt + 2 * y * PA_COL + (j >> 1) * PA_COL + PA_COL / 2 +
+                                                              key * 64 + 32 * (j & 1));
             uint4 a = make_uint4(0u, 0u, 0u, 0u), e = a;
             if (key < keys) {
               a = src[odd ? 1 : 0];
@@ -399,8 +403,9 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
             unsigned char* dst = kt + 2 * y * PA_COL + (j >> 1) * PA_COL + key * 128;
 #pragma unroll
             for (int g = 0; g < 4; g++) {
-              const uint4 v = make_uint4(odd ? o[y][4 * (g ^ 1)] : o[y][4 * g], odd ? o[y][4 * (g ^ 1) + 1] : o[y][4 * g + 1],
-                                         odd ? o[y][4 * (g ^ 1) + 2] : o[y][4 * g + 2], odd ? o[y][4 * (g ^ 1) + 3] : o[y][4 * g + 3]);
+              const uint4 v = make_uint4(
+                  odd ? o[y][4 * (g ^ 1)] : o[y][4 * g], odd ? o[y][4 * (g ^ 1) + 1] : o[y][4 * g + 1],
+                  odd ? o[y][4 * (g ^ 1) + 2] : o[y][4 * g + 2], odd ? o[y][4 * (g ^ 1) + 3] : o[y][4 * g + 3]);
               const uint32_t unit = (uint32_t)(4 * (j & 1) + (odd ? g ^ 1 : g));
               *reinterpret_cast<uint4*>(dst + ((unit ^ (uint32_t)(key & 7)) << 4)) = v;
             }
@@ -415,7 +420,8 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
           }
 #pragma unroll
           for (int i = 0; i < PA_BUF / 16 / PA_FILL; i++) {
-            uint4 o = make_uint4(bf16x2_to_f16x2(x[i].x), bf16x2_to_f16x2(x[i].y), bf16x2_to_f16x2(x[i].z), bf16x2_to_f16x2(x[i].w));
+            uint4 o = make_uint4(bf16x2_to_f16x2(x[i].x), bf16x2_to_f16x2(x[i].y), bf16x2_to_f16x2(x[i].z),
+                                 bf16x2_to_f16x2(x[i].w));
             if ((bad(o.x) | bad(o.y) | bad(o.z) | bad(o.w)) != 0u) {
               const int row = ((ft + i * PA_FILL) >> 3) & (PA_KEYS - 1);
               o = make_uint4(finite(o.x, row), finite(o.y, row), finite(o.z, row), finite(o.w, row));
@@ -437,7 +443,7 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
     // keys); of its 32 keys and its columns of Q and O the warp takes the half `sub`
     const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
     const int half = warp >> 1 & 1, sub = warp >> 2, head = 32 * (warp & 1) + lane, other = tid ^ 64;
-    const int two = 3 + (warp & 1) + 2 * sub;         // named barrier of the two warps that have a head's lanes for the same keys
+    const int two = 3 + (warp & 1) + 2 * sub;         // named barrier of the two warps with a head's lanes for the same keys
     const int four = 7 + (warp & 1);                  // of the four that have a head
     const int own = 2 * half + sub;                   // quarter of the keys
     float4* xs = reinterpret_cast<float4*>(smem + PA_OFF_S);
@@ -476,7 +482,8 @@ pair_attn_kernel(KeysParams p, const __grid_constant__ CUtensorMap map_q, const 
         if (there) {
 #pragma unroll 1
           for (uint32_t x = 0; x < 64; x++) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(qh + (2 * sub + (x >> 5)) * PA_COL + sw128((uint32_t)head, 4u * (x & 31u)));
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(qh + (2 * sub + (x >> 5)) * PA_COL +
+                                                                  sw128((uint32_t)head, 4u * (x & 31u)));
             size = max(size, max(w & 0x7FFFu, w >> 16 & 0x7FFFu));
           }
         }
