@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(C8_THREADS, 5) cache8_write_kernel(C8WritePara
         c[i] = __float_as_uint(w);
       }
       if (far > C8_TIE) {
-        // (a value in 275, more often than by chance: quotients of 8-bit numbers, all of one scale.)  The rest
+        // (one value in 300, more often than by chance: quotients of 8-bit numbers, all of one scale.)  The rest
         // x - n s is exact; beyond half of s, or at it with an odd code, the code moves towards it.
 #pragma unroll
         for (int i = 0; i < 8; i++) {
