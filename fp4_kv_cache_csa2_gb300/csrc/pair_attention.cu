@@ -18,7 +18,7 @@
 // The lanes of a head sit in different warps, which pass each other partial scores and weights through
 // shared memory (384 cycles).
 //
-// Bound by shared memory: 1,900 cycles a chunk, 1,565 of them in use (by counters: 925 of the load/store
+// Bound by shared memory: 1,900 cycles a chunk, 1,557 of them in use (by counters: 917 of the load/store
 // unit, with waits and the above; 512 of products; 128 of copies), and what waits behind them: the softmax takes
 // 1,600 from scores to weights.  2048 queries over 8192 entries 1.53 ms (a CTA a query 2.06),
 // 3 x 37 over 10,007, 7006 and 4005 entries 105 us (134).  A pair costs 8 us beside its chunks.  Without the
